@@ -116,7 +116,7 @@ def lib():
                 raise RuntimeError(f"{LIB_PATH} is missing: run precision_states_gb300.build.build() "
                                    "(needs nvcc); there is no fallback path")
             L = _c.CDLL(LIB_PATH)
-            for name, (res, args) in _SIGS.items():
+            for name, (res, args) in [*_SIGS.items(), *_layer.SIGS.items()]:
                 fn = getattr(L, name)
                 fn.restype = res
                 fn.argtypes = args
@@ -327,3 +327,9 @@ class Plan:
                                  f"{want} bytes")
         arr = (_vp * max(len(host_grads), 1))(*[t.data_ptr() for t in host_grads])
         _check(lib().opt_grads_upload(self.handle, arr, _stream_ptr(stream)), "opt_grads_upload")
+
+
+# ------------------------------------------------- training-layer operators
+from . import layer as _layer  # noqa: E402
+from .layer import (e4m3_storage, opt_dropout, opt_matmul, opt_quantize, opt_rms_norm,  # noqa: E402,F401
+                    opt_rms_norm_backward, opt_rms_norm_backward_workspace, opt_scales_bytes)

@@ -2,7 +2,7 @@
 
 nvcc compiles every translation unit for sm_103a only, in parallel, and links
 them into one shared library with the CUDA runtime linked statically; the
-library's C ABI is declared in include/opt.h.  A stamp of the sources and
+library's C ABI is declared in include/opt.h and opt_layer.h.  A stamp of the sources and
 flags skips the build when nothing changed.
 """
 from __future__ import annotations
@@ -21,7 +21,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libpsopt.so")
 
 CU_SOURCES = ["api.cu", "norm.cu", "step_f32.cu", "step_lowp.cu", "step_small.cu", "codec.cu", "norm_noalloc.cu",
-              "lamb.cu"]
+              "lamb.cu", "layer.cu", "dropout.cu", "rms_norm.cu", "quantize.cu", "matmul.cu"]
 CPP_SOURCES = ["host.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-I", INCLUDE, "-Xcompiler", "-fPIC",
@@ -83,7 +83,7 @@ def source_stamp(files) -> str:
 
 def _stamp() -> str:
     h = hashlib.sha256()
-    files = sorted(os.listdir(CSRC)) + ["../../include/opt.h"]
+    files = sorted(os.listdir(CSRC)) + ["../../include/opt.h", "../../include/opt_layer.h"]
     for f in files:
         path = os.path.normpath(os.path.join(CSRC, f))
         if os.path.isfile(path):

@@ -1,0 +1,75 @@
+// dropout.cu -- y = residual + dropout(x) (opt_layer.h).
+//
+// Mathematics: Philox4x32-10 gives eight 16-bit draws per call, and the mask is
+// recomputed wherever it is needed, so a pass moves x, the residual and y and
+// nothing else.  At 10 rounds of two 32 x 32 -> 64 products per eight elements
+// the generator stays under the memory time of BF16 elements.
+#include "layer.cuh"
+
+namespace psopt {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int64_t kMaxGridX = (int64_t)1 << 30;
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void drop_chunk(const opt_dropout_args& a, const DropArgs& d, int64_t r, int64_t c,
+                                           int valid) {
+  float x[8], res[8];
+  load8<VEC>(static_cast<const T*>(a.d_x) + r * a.x_pitch + c, valid, x);
+  if (a.d_residual != nullptr)
+    load8<VEC>(static_cast<const T*>(a.d_residual) + r * a.residual_pitch + c, valid, res);
+  drop8<VEC>(x, (uint64_t)(r * a.cols + c), d);
+  if (a.d_residual != nullptr) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] += res[j];
+  }
+  store8<VEC>(static_cast<T*>(a.d_y) + r * a.y_pitch + c, valid, x);
+}
+
+// One chunk of eight elements per thread; chunk `c` of row `r` starts at 8 c.
+// A contiguous matrix comes as one row.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant__ opt_dropout_args a,
+                                                           const __grid_constant__ DropArgs d, int64_t first) {
+  const int64_t c = 8 * (first + (int64_t)blockIdx.x * kThreads + threadIdx.x);
+  if (c >= a.cols) return;
+  const int valid = (int)(a.cols - c < 8 ? a.cols - c : 8);
+  for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
+    if (VEC && valid == 8) drop_chunk<T, true>(a, d, r, c, 8);
+    else drop_chunk<T, false>(a, d, r, c, valid);
+  }
+}
+
+template <typename T>
+cudaError_t launch(opt_dropout_args a, const DropArgs& d, cudaStream_t s) {
+  const bool res = a.d_residual != nullptr;
+  if (a.rows > 1 && a.x_pitch == a.cols && a.y_pitch == a.cols && (!res || a.residual_pitch == a.cols)) {
+    a.cols *= a.rows;              // one long row: the same element numbers
+    a.rows = 1;
+  }
+  // VEC: every full chunk starts on 16 bytes and, in element numbers, on a
+  // multiple of 8 (so that it is one generator call)
+  constexpr int64_t es = sizeof(T);
+  const auto fits = [&](const void* p, int64_t pitch) {
+    return ((uintptr_t)p & 15u) == 0 && (a.rows == 1 || pitch * es % 16 == 0);
+  };
+  const bool vec = fits(a.d_x, a.x_pitch) && fits(a.d_y, a.y_pitch) && (!res || fits(a.d_residual, a.residual_pitch)) &&
+                   (a.rows == 1 || a.cols % 8 == 0);
+  const int64_t blocks = ((a.cols + 7) / 8 + kThreads - 1) / kThreads;
+  const unsigned gy = (unsigned)(a.rows < 65535 ? a.rows : 65535);
+  for (int64_t b = 0; b < blocks; b += kMaxGridX) {
+    const dim3 grid((unsigned)(blocks - b < kMaxGridX ? blocks - b : kMaxGridX), gy);
+    if (vec) dropout_kernel<T, true><<<grid, kThreads, 0, s>>>(a, d, b * kThreads);
+    else dropout_kernel<T, false><<<grid, kThreads, 0, s>>>(a, d, b * kThreads);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_dropout(const opt_dropout_args& a, const DropArgs& d, cudaStream_t s) {
+  return a.dtype == OPT_F32 ? launch<float>(a, d, s) : launch<Bf16>(a, d, s);
+}
+
+}  // namespace psopt

@@ -1,0 +1,279 @@
+"""Python binding of the training-layer operators (include/opt_layer.h):
+dropout, residual RMS norm and its gradients, conversion to E4M3 with a scale
+for each block of 128, and the product of two matrices held in that form.
+
+Argument marshalling and shape checks only; the functions carry the C names
+and write into tensors that the caller owns.  A matrix argument is a CUDA
+tensor on the current device whose last dimension is contiguous: a 2-d tensor
+of any row stride, or a contiguous tensor of any other shape, taken as rows of
+its last dimension.  Wrong shapes and dtypes raise ValueError; everything else
+is checked by the library (OptError).
+"""
+from __future__ import annotations
+
+import ctypes
+import struct
+
+_c = ctypes
+_vp, _i64, _u64, _i32, _u32, _f32, _f64 = (_c.c_void_p, _c.c_int64, _c.c_uint64, _c.c_int32, _c.c_uint32,
+                                           _c.c_float, _c.c_double)
+
+
+class opt_dropout_args(_c.Structure):
+    _fields_ = [("d_x", _vp), ("d_residual", _vp), ("d_y", _vp),
+                ("x_pitch", _i64), ("residual_pitch", _i64), ("y_pitch", _i64),
+                ("rows", _i64), ("cols", _i64), ("p", _f64), ("seed", _u64), ("step", _i64),
+                ("tensor_index", _u32), ("dtype", _i32)]
+
+
+class opt_rms_norm_args(_c.Structure):
+    _fields_ = [("d_x", _vp), ("d_residual", _vp), ("d_weight", _vp), ("d_h", _vp), ("d_y", _vp), ("d_rstd", _vp),
+                ("d_codes", _vp), ("d_scales", _vp),
+                ("x_pitch", _i64), ("residual_pitch", _i64), ("h_pitch", _i64), ("y_pitch", _i64),
+                ("codes_pitch", _i64), ("rows", _i64), ("cols", _i64), ("p", _f64), ("seed", _u64), ("step", _i64),
+                ("tensor_index", _u32), ("dtype", _i32), ("weight_dtype", _i32), ("eps", _f32)]
+
+
+class opt_rms_norm_backward_args(_c.Structure):
+    _fields_ = [("d_dy", _vp), ("d_h", _vp), ("d_weight", _vp), ("d_rstd", _vp), ("d_dh_in", _vp), ("d_dh", _vp),
+                ("d_dx", _vp), ("d_dweight", _vp), ("d_workspace", _vp),
+                ("dy_pitch", _i64), ("h_pitch", _i64), ("dh_in_pitch", _i64), ("dh_pitch", _i64), ("dx_pitch", _i64),
+                ("workspace_bytes", _i64), ("rows", _i64), ("cols", _i64), ("p", _f64), ("seed", _u64),
+                ("step", _i64), ("tensor_index", _u32), ("dtype", _i32), ("weight_dtype", _i32), ("reserved", _i32)]
+
+
+class opt_quantize_args(_c.Structure):
+    _fields_ = [("d_x", _vp), ("d_codes", _vp), ("d_scales", _vp), ("d_codes_t", _vp), ("d_scales_t", _vp),
+                ("x_pitch", _i64), ("codes_pitch", _i64), ("codes_t_pitch", _i64), ("rows", _i64), ("cols", _i64),
+                ("dtype", _i32), ("block_rows", _i32)]
+
+
+class opt_matmul_args(_c.Structure):
+    _fields_ = [("d_a", _vp), ("d_a_scales", _vp), ("d_b", _vp), ("d_b_scales", _vp), ("d_addend", _vp),
+                ("d_out", _vp), ("a_pitch", _i64), ("b_pitch", _i64), ("addend_pitch", _i64), ("out_pitch", _i64),
+                ("m", _i64), ("n", _i64), ("k", _i64), ("out_dtype", _i32), ("reserved", _i32)]
+
+
+# the C ABI: name -> (restype, argtypes); the argument structs go as packed bytes
+SIGS = {
+    "opt_scales_bytes": (_i64, [_i64, _i64]),
+    "opt_dropout": (_c.c_int, [_c.c_char_p, _vp]),
+    "opt_rms_norm": (_c.c_int, [_c.c_char_p, _vp]),
+    "opt_rms_norm_backward": (_c.c_int, [_c.c_char_p, _vp]),
+    "opt_rms_norm_backward_workspace": (_i64, [_i64, _i64]),
+    "opt_quantize": (_c.c_int, [_c.c_char_p, _vp]),
+    "opt_matmul": (_c.c_int, [_c.c_char_p, _vp]),
+}
+
+_CODE = {_vp: "Q", _i64: "q", _u64: "Q", _i32: "i", _u32: "I", _f32: "f", _f64: "d"}
+
+
+def packer(struct_type):
+    """struct.pack for a ctypes argument struct: one call instead of one
+    attribute store per field.  Every struct orders its fields so that it has no
+    padding."""
+    return struct.Struct("=" + "".join(_CODE[t] for _, t in struct_type._fields_)).pack
+
+
+_pack_dropout = packer(opt_dropout_args)
+_pack_rms_norm = packer(opt_rms_norm_args)
+_pack_rms_norm_backward = packer(opt_rms_norm_backward_args)
+_pack_quantize = packer(opt_quantize_args)
+_pack_matmul = packer(opt_matmul_args)
+
+from . import (OPT_BF16, OPT_EUNSUPPORTED, OPT_F32, OptError, _check, _stream_ptr, lib)  # noqa: E402
+
+_DT = {}          # torch dtype -> OPT_F32 / OPT_BF16, filled at the first use of torch
+_FLAT = None      # torch's 8-bit storage dtypes
+
+
+def _dtype(t, what):
+    global _FLAT
+    if not _DT:
+        import torch
+        _FLAT = (torch.uint8, torch.float8_e4m3fn, torch.float8_e8m0fnu)
+        _DT.update({torch.float32: OPT_F32, torch.bfloat16: OPT_BF16})
+    got = _DT.get(t.dtype)
+    if got is None:
+        raise OptError(OPT_EUNSUPPORTED, f"{what}: dtype {t.dtype}")
+    return got
+
+
+def _device(t, what):
+    """The tensor's device index, which must be the current one."""
+    import torch
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{what} must be a CUDA tensor on the current device")
+    return t.get_device()
+
+
+def _matrix(t, what):
+    """(rows, cols, pitch) of a matrix argument."""
+    shape = t.shape
+    if len(shape) == 2:
+        rows, cols = shape
+        pitch, step = t.stride()
+        if step != 1 and cols > 1 and rows > 0:
+            raise ValueError(f"{what}: the last dimension must be contiguous")
+        return rows, cols, pitch
+    if not t.is_contiguous() or len(shape) == 0:
+        raise ValueError(f"{what} must be 2-d with a contiguous last dimension, or contiguous")
+    cols = shape[-1]
+    rows = 1
+    for n in shape[:-1]:
+        rows *= n
+    return rows, cols, cols
+
+
+def _like(t, what, rows, cols, dtype, device):
+    """(pointer, pitch) of a matrix of the given shape and dtype; (0, 0) for None."""
+    if t is None:
+        return 0, 0
+    if t.dtype != dtype or t.get_device() != device:
+        raise ValueError(f"{what}: expected {dtype} on cuda:{device}")
+    r, c, pitch = _matrix(t, what)
+    if r != rows or c != cols:
+        raise ValueError(f"{what}: expected {rows} x {cols}, got {tuple(t.shape)}")
+    return t.data_ptr(), pitch
+
+
+def _vector(t, what, n, device, dtype=None):
+    if t is None:
+        return 0
+    if t.get_device() != device or t.numel() != n or not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{what}: expected {n} contiguous elements" + (f" of {dtype}" if dtype else "") +
+                         f" on cuda:{device}")
+    return t.data_ptr()
+
+
+def _held(codes, scales, what, rows, cols, device):
+    """(codes pointer, scales pointer, pitch) of an 8-bit operand; zeros for None."""
+    if codes is None and scales is None:
+        return 0, 0, 0
+    if codes is None or scales is None:
+        raise ValueError(f"{what}: codes and scales go together")
+    if codes.dtype not in _FLAT or scales.dtype not in _FLAT or codes.get_device() != device:
+        raise ValueError(f"{what}: expected 8-bit codes and scales on cuda:{device}")
+    r, c, pitch = _matrix(codes, what)
+    if r != rows or c != cols:
+        raise ValueError(f"{what}: expected codes of {rows} x {cols}, got {tuple(codes.shape)}")
+    return codes.data_ptr(), _vector(scales, what + " scales", scales_bytes(rows, cols), device), pitch
+
+
+def scales_bytes(rows: int, cols: int) -> int:
+    """Bytes of the scale tiles of a rows x cols operand (opt_scales_bytes)."""
+    return -(-rows // 128) * -(-cols // 512) * 512
+
+
+def e4m3_storage(rows: int, cols: int, device="cuda"):
+    """Zeroed storage of an 8-bit operand: (codes, scales), uint8.  The codes are
+    a rows x cols view of rows that are padded to 16 bytes."""
+    import torch
+    codes = torch.zeros(rows, -(-max(cols, 1) // 16) * 16, dtype=torch.uint8, device=device)[:, :cols]
+    return codes, torch.zeros(scales_bytes(rows, cols), dtype=torch.uint8, device=device)
+
+
+def opt_scales_bytes(rows: int, cols: int) -> int:
+    return _check(lib().opt_scales_bytes(rows, cols), "opt_scales_bytes")
+
+
+def opt_dropout(x, y, p: float, seed=0, tensor_index=0, step=0, residual=None, stream=None):
+    """y = residual + dropout(x); y may be x or residual.  The backward pass is
+    the same call on the gradient (same p, seed, tensor_index and step)."""
+    dt, dev = _dtype(x, "x"), _device(x, "x")
+    rows, cols, xp = _matrix(x, "x")
+    yq, yp = _like(y, "y", rows, cols, x.dtype, dev)
+    rq, rp = _like(residual, "residual", rows, cols, x.dtype, dev)
+    _check(lib().opt_dropout(_pack_dropout(x.data_ptr(), rq, yq, xp, rp, yp, rows, cols, p, seed, step,
+                                           tensor_index, dt), _stream_ptr(stream)), "opt_dropout")
+
+
+def opt_rms_norm(x, weight, eps=1e-5, y=None, rstd=None, residual=None, h=None, codes=None, scales=None, p=0.0,
+                 seed=0, tensor_index=0, step=0, stream=None):
+    """h = residual + dropout(x), rstd = 1 / sqrt(mean(h^2) + eps) and
+    y = h rstd weight, into whichever of h, rstd, y and codes with scales (y as
+    E4M3, a scale for each 1 x 128) are given."""
+    dt, dev = _dtype(x, "x"), _device(x, "x")
+    rows, cols, xp = _matrix(x, "x")
+    rq, rp = _like(residual, "residual", rows, cols, x.dtype, dev)
+    hq, hp = _like(h, "h", rows, cols, x.dtype, dev)
+    yq, yp = _like(y, "y", rows, cols, x.dtype, dev)
+    cq, sq, cp = _held(codes, scales, "codes", rows, cols, dev)
+    _check(lib().opt_rms_norm(
+        _pack_rms_norm(x.data_ptr(), rq, _vector(weight, "weight", cols, dev), hq, yq,
+                       _vector(rstd, "rstd", rows, dev, _torch_f32()), cq, sq, xp, rp, hp, yp, cp, rows, cols, p,
+                       seed, step, tensor_index, dt, _dtype(weight, "weight"), eps), _stream_ptr(stream)),
+        "opt_rms_norm")
+
+
+def _torch_f32():
+    import torch
+    return torch.float32
+
+
+def opt_rms_norm_backward(dy, h, weight, rstd, dh, dh_in=None, dx=None, dweight=None, p=0.0, seed=0, tensor_index=0,
+                          step=0, workspace=None, stream=None):
+    """Gradients of opt_rms_norm from dy and the stored h and rstd: dh (the
+    residual's, with dh_in added), dx = dropout(dh) (the branch's) and dweight
+    (fp32).  workspace: a uint8 tensor of opt_rms_norm_backward_workspace(rows,
+    cols) bytes for dweight; without one the call takes it from torch's
+    allocator."""
+    dt, dev = _dtype(h, "h"), _device(h, "h")
+    rows, cols, hp = _matrix(h, "h")
+    gq, gp = _like(dy, "dy", rows, cols, h.dtype, dev)
+    iq, ip = _like(dh_in, "dh_in", rows, cols, h.dtype, dev)
+    oq, op = _like(dh, "dh", rows, cols, h.dtype, dev)
+    xq, xp = _like(dx, "dx", rows, cols, h.dtype, dev)
+    f32 = _torch_f32()
+    sp = _stream_ptr(stream)
+    need = 0
+    if dweight is not None:
+        need = lib().opt_rms_norm_backward_workspace(rows, cols)
+        if workspace is None:
+            workspace = _workspace(need, dev, stream)
+        else:
+            need = workspace.numel() * workspace.element_size()
+    _check(lib().opt_rms_norm_backward(
+        _pack_rms_norm_backward(gq, h.data_ptr(), _vector(weight, "weight", cols, dev),
+                                _vector(rstd, "rstd", rows, dev, f32), iq, oq, xq,
+                                _vector(dweight, "dweight", cols, dev, f32),
+                                workspace.data_ptr() if need else 0, gp, hp, ip, op, xp, need, rows, cols, p, seed,
+                                step, tensor_index, dt, _dtype(weight, "weight"), 0), sp), "opt_rms_norm_backward")
+
+
+def _workspace(nbytes, device, stream):
+    """Scratch from torch's allocator that stays the call's until its stream has passed it."""
+    import torch
+    t = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+    if stream is not None:
+        t.record_stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream)
+    return t
+
+
+def opt_rms_norm_backward_workspace(rows: int, cols: int) -> int:
+    return _check(lib().opt_rms_norm_backward_workspace(rows, cols), "opt_rms_norm_backward_workspace")
+
+
+def opt_quantize(x, codes=None, scales=None, codes_t=None, scales_t=None, block_rows=1, stream=None):
+    """x to E4M3 codes with a scale for each block of block_rows (1 or 128) x 128:
+    as it is (codes, scales) and/or transposed (codes_t of cols x rows,
+    scales_t)."""
+    dt, dev = _dtype(x, "x"), _device(x, "x")
+    rows, cols, xp = _matrix(x, "x")
+    cq, sq, cp = _held(codes, scales, "codes", rows, cols, dev)
+    tq, uq, tp = _held(codes_t, scales_t, "codes_t", cols, rows, dev)
+    _check(lib().opt_quantize(_pack_quantize(x.data_ptr(), cq, sq, tq, uq, xp, cp, tp, rows, cols, dt, block_rows),
+                              _stream_ptr(stream)), "opt_quantize")
+
+
+def opt_matmul(a, a_scales, b, b_scales, out, addend=None, stream=None):
+    """out = a b^T (+ addend): a of m x k and b of n x k codes with their scales,
+    out and addend float32 or bfloat16 of m x n; addend may be out."""
+    dt, dev = _dtype(out, "out"), _device(out, "out")
+    m, n, op = _matrix(out, "out")
+    k = a.shape[-1]
+    aq, asq, ap = _held(a, a_scales, "a", m, k, dev)
+    bq, bsq, bp = _held(b, b_scales, "b", n, k, dev)
+    dq, dp = _like(addend, "addend", m, n, out.dtype, dev)
+    _check(lib().opt_matmul(_pack_matmul(aq, asq, bq, bsq, dq, out.data_ptr(), ap, bp, dp, op, m, n, k, dt, 0),
+                            _stream_ptr(stream)), "opt_matmul")
