@@ -189,6 +189,13 @@ typedef struct opt_matmul_args {
 } opt_matmul_args;
 int opt_matmul(const opt_matmul_args* a, void* stream);
 
+/* Error flags raised by the current device's layer kernels since the last call,
+ * then cleared; 0 means that every kernel ran to completion.  Copies to host and
+ * synchronises the stream.  OPT_FLAG_WAIT_TIMEOUT: a product gave up a wait on
+ * its own copies or tensor-core work (each is bounded at 2 s, so the kernel never
+ * hangs) and left part of its output unwritten: discard that output. */
+int opt_layer_status(int32_t* h_flags, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -178,4 +178,12 @@ int opt_matmul(const opt_matmul_args* a, void* stream) {
   return status_of(launch_matmul(*a, sms, static_cast<cudaStream_t>(stream)));
 }
 
+int opt_layer_status(int32_t* h_flags, void* stream) {
+  if (h_flags == nullptr) return OPT_EINVAL;
+  int flags = 0;
+  PS_TRY(status_of(layer_flags(&flags, static_cast<cudaStream_t>(stream))));
+  *h_flags = flags;
+  return OPT_OK;
+}
+
 }  // extern "C"

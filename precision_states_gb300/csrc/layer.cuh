@@ -9,6 +9,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "internal.h"
 #include "layer.h"
 
 namespace psopt {

@@ -1,68 +1,609 @@
 // matmul.cu -- out = a b^T (+ addend) of two E4M3 operands with a scale for each
 // block of 128 along the depth (opt_layer.h).
+//
+// Mathematics: out = sum over blocks of 2^(ea + eb) times the block's sum of code
+// products.  The scales are powers of two in the tensor core's own scale format,
+// so tcgen05.mma (kind mxf8f6f4, block scaled) applies them as it multiplies:
+// each 32-deep instruction takes one scale byte per row of either operand, and
+// the four instructions of a 128-deep block take the same one.  Sums stay in the
+// accumulator's fp32 over the whole depth.
+//
+// Roles.  The kernel computes x y^T tiles of 128 rows of x per CTA (the tensor
+// memory's lanes) by NT rows of y (its columns); either operand of the call can
+// be x (`swap`), so that few rows on either side become a narrow NT and not a
+// mostly empty 128.  Warp 0 fills a ring of stages (128 bytes of depth of both
+// tiles, 128-byte swizzle; every fourth stage the 512-byte scale tiles too) by
+// TMA; one thread of warp 1 copies scale tiles to tensor memory and issues the
+// products; warps 4-7 read finished accumulators and write out.  Two
+// accumulators alternate, so that a tile's output overlaps the next one's
+// products.  At NT 256 they share 24 columns (two of 256 and two sets of scales
+// do not fit into 512): the output reads those first, and the next tile's
+// products wait for that alone.
+//
+// CG 2: a pair of CTAs works on one tile of 256 x NT (cta_group::2): each holds
+// its 128 rows of x and half of y's rows, which halves y's traffic and shared
+// memory per product.
+//
+// Splits.  With few tiles, the depth is split over a cluster of CTAs; their
+// accumulators are summed through distributed shared memory in rank order.
+//
+// Every wait is bounded (kWaitNs of the global timer): one that runs out raises
+// OPT_FLAG_WAIT_TIMEOUT (opt_layer_status), and the CTA leaves after its copies
+// and products in flight have ended.
+#include <cuda.h>
+
 #include "layer.cuh"
 
 namespace psopt {
 namespace {
 
-constexpr int kTile = 64, kDepth = 32, kThreads = 256;
+constexpr int kThreads = 256;
+constexpr unsigned long long kWaitNs = 2000000000ull;
+constexpr int kScaleTile = 512;        // bytes: 128 rows x 4 blocks
+constexpr int kStageDepth = 128;
+constexpr int kRingBytes = 204 * 1024;
 
-// A 64 x 64 tile of the output per CTA, 4 x 4 outputs per thread; both
-// operands' values (code times scale) lie in shared memory in fp32.
-__device__ __forceinline__ void stage(float (*t)[kTile + 4], const uint8_t* codes, int64_t pitch, const uint8_t* scales,
-                                      int64_t row0, int64_t rows, int64_t k0, int64_t k, int64_t panel) {
-  for (int i = threadIdx.x; i < kTile * kDepth; i += kThreads) {
-    const int64_t r = row0 + i / kDepth, c = k0 + i % kDepth;
-    float v = 0.0f;
-    if (r < rows && c < k) {
-      const uint32_t b = scales[scale_place(r, c >> 7, panel)];
-      v = e4m3_dec(codes[r * pitch + c]) * (b > 0u ? u2f(b << 23) : u2f(1u << 22));
+__device__ int g_flags;
+
+struct MatmulArgs {
+  void* out;
+  const void* addend;
+  int64_t out_pitch, addend_pitch;
+  int nx, ny;                // rows of x and of y
+  int x_tiles, y_tiles;
+  int blocks;                // ceil(k / 128)
+  int panel;                 // scale tiles per 128 rows: ceil(blocks / 4)
+  int split;                 // CTAs per cluster along the depth (CG 1)
+  int swap;                  // x is the call's b: out[y][x]
+  int vec;                   // rows of out and addend allow 16-byte accesses
+};
+
+template <int CG, int NT>
+struct Layout {
+  static constexpr int kY = NT / CG;                                   // rows of y per CTA
+  static constexpr int kYScaleTiles = (NT + 127) / 128;
+  static constexpr int kXBytes = 128 * kStageDepth, kYBytes = kY * kStageDepth;
+  static constexpr int kScaleBytes = (1 + kYScaleTiles) * kScaleTile;
+  static constexpr int kStage = kXBytes + (kYBytes + 1023) / 1024 * 1024;
+  static constexpr int kFit = kRingBytes / (kStage + kScaleBytes);
+  static constexpr int kStages = kFit < 12 ? kFit : 12;
+  // tensor memory columns: two accumulators, two sets of scales (x: 4, y: 4 per 128 rows)
+  static constexpr bool kOverlap = NT == 256;
+  static constexpr int kScaleCols = 4 + 4 * kYScaleTiles;
+  static constexpr int kAcc1 = kOverlap ? 256 - 2 * kScaleCols : NT;
+  static constexpr int kScaleCol = kAcc1 + NT;
+  static constexpr int kNeed = kScaleCol + 2 * kScaleCols;
+  static constexpr int kCols = kNeed <= 64 ? 64 : kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
+  static constexpr int kBars = 2 * kStages + 5;      // full, empty, done[2], free[2], drain
+  // dynamic shared memory: ring | scales | barriers, tensor memory address, failure
+  static constexpr int kScaleAt = kStages * kStage;
+  static constexpr int kBarAt = kScaleAt + kStages * kScaleBytes;
+  static constexpr int kBytes = kBarAt + kBars * 8 + 16 + 1024;        // 1024: alignment of the ring
+  static_assert(kNeed <= 512, "tensor memory");
+  static_assert(kBytes <= 227 * 1024, "shared memory");
+  static_assert(NT * 128 * 4 <= kScaleAt || CG == 2 || NT > 128, "split sums fit into the ring");
+};
+
+// ------------------------------------------------------------------ barriers
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t map_to(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ unsigned long long now_ns() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
+  if (bar_try(bar, parity)) return true;
+  const unsigned long long t0 = now_ns();
+  while (!bar_try(bar, parity))
+    if (now_ns() - t0 > kWaitNs) return false;
+  return true;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// ------------------------------------------------------- copies and products
+template <int CG>
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  if (CG == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3}], [%4];"
+        ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+
+// Shared-memory matrix descriptors: rows of 128 bytes, 128-byte swizzle, groups
+// of 8 rows 1024 bytes apart; and scale tiles, not swizzled, 8 rows of 16 bytes
+// in 128 bytes.
+__device__ __forceinline__ uint64_t tile_desc(uint32_t addr) {
+  return (uint64_t)((addr & 0x3FFFF) >> 4) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
+  return (uint64_t)((addr & 0x3FFFF) >> 4) | ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
+}
+// Instruction descriptor: E4M3 by E4M3, both with the depth along their rows,
+// E8M0 scales, M = 128 CG, N = NT; the scale byte of both operands.
+template <int CG, int NT>
+__device__ __forceinline__ uint32_t instr_desc(uint32_t byte) {
+  return (byte << 4) | ((uint32_t)(NT >> 3) << 17) | (1u << 23) | ((uint32_t)CG << 27) | (byte << 29);
+}
+template <int CG>
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
+  if (CG == 1) asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+  else asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void product(uint32_t acc, uint64_t x, uint64_t y, uint32_t instr, uint32_t sx, uint32_t sy,
+                                        uint32_t add) {
+  if (CG == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+        ::"r"(acc), "l"(x), "l"(y), "r"(instr), "r"(sx), "r"(sy), "r"(add) : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+        ::"r"(acc), "l"(x), "l"(y), "r"(instr), "r"(sx), "r"(sy), "r"(add) : "memory");
+}
+// An arrival on `bar` (of both CTAs of a pair) when everything issued has ended.
+template <int CG>
+__device__ __forceinline__ void commit(uint32_t bar) {
+  if (CG == 1)
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+        ::"r"(bar), "h"((uint16_t)3) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// N consecutive accumulator columns of this warp's 32 lanes (N 16 or 32).
+template <int N>
+__device__ __forceinline__ void acc_load(uint32_t tmem, float (&v)[N]) {
+  uint32_t r[N];
+  if constexpr (N == 32) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
+        "%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(tmem));
+  } else {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(tmem));
+  }
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = u2f(r[i]);
+}
+
+// -------------------------------------------------------------------- output
+// N outputs of row `x` of the tile's operand, columns y0 .. y0 + N - 1.
+template <typename T>
+__device__ __forceinline__ void store_one(const MatmulArgs& a, int x, int y, float v) {
+  const int64_t row = a.swap ? y : x, col = a.swap ? x : y;
+  float t[8] = {v};
+  if (a.addend != nullptr) {
+    float c[8];
+    load8<false>(static_cast<const T*>(a.addend) + row * a.addend_pitch + col, 1, c);
+    t[0] += c[0];
+  }
+  store8<false>(static_cast<T*>(a.out) + row * a.out_pitch + col, 1, t);
+}
+template <typename T, int N>
+__device__ __forceinline__ void store_cols(const MatmulArgs& a, int x, int y0, const float (&v)[N]) {
+  if (x >= a.nx) return;
+  if (a.vec && !a.swap && y0 + N <= a.ny) {
+    T* out = static_cast<T*>(a.out) + (int64_t)x * a.out_pitch + y0;
+#pragma unroll
+    for (int i = 0; i < N; i += 8) {
+      float t[8];
+      if (a.addend != nullptr) {
+        load8<true>(static_cast<const T*>(a.addend) + (int64_t)x * a.addend_pitch + y0 + i, 8, t);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t[j] += v[i + j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t[j] = v[i + j];
+      }
+      store8<true>(out + i, 8, t);
     }
-    t[i % kDepth][i / kDepth] = v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (y0 + i < a.ny) store_one<T>(a, x, y0 + i, v[i]);
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) matmul_kernel(const __grid_constant__ opt_matmul_args a, int64_t col_tiles) {
-  __shared__ float sa[kDepth][kTile + 4], sb[kDepth][kTile + 4];
-  const int64_t m0 = kTile * (blockIdx.x / col_tiles), n0 = kTile * (blockIdx.x % col_tiles);
-  const int64_t panel = (a.k + 511) / 512;
-  const int tm = 4 * (threadIdx.x / 16), tn = 4 * (threadIdx.x % 16);
-  float acc[4][4] = {};
-  for (int64_t k0 = 0; k0 < a.k; k0 += kDepth) {
-    __syncthreads();
-    stage(sa, static_cast<const uint8_t*>(a.d_a), a.a_pitch, static_cast<const uint8_t*>(a.d_a_scales), m0, a.m, k0, a.k, panel);
-    stage(sb, static_cast<const uint8_t*>(a.d_b), a.b_pitch, static_cast<const uint8_t*>(a.d_b_scales), n0, a.n, k0, a.k, panel);
-    __syncthreads();
-    for (int k = 0; k < kDepth; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[k][tm + i], sb[k][tn + j], acc[i][j]);
+// Tile t of the grid: panels of kGroup x tiles go through all y tiles, so that
+// the tiles in flight share operands in L2.
+constexpr int kGroup = 8;
+__device__ __forceinline__ void tile_at(const MatmulArgs& a, int t, int& tx, int& ty) {
+  const int per = kGroup * a.y_tiles, g = t / per, in = t - g * per;
+  const int high = min(kGroup, a.x_tiles - g * kGroup);
+  ty = in / high;
+  tx = g * kGroup + in - ty * high;
+}
+
+template <typename T, int CG, int NT>
+__global__ void __launch_bounds__(kThreads, 1)
+matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_y,
+              const __grid_constant__ CUtensorMap map_sx, const __grid_constant__ CUtensorMap map_sy,
+              const __grid_constant__ MatmulArgs a) {
+  using L = Layout<CG, NT>;
+  constexpr int S = L::kStages;
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+  const uint32_t ring = smem_addr(smem), scales = ring + L::kScaleAt, bars = ring + L::kBarAt;
+  const uint32_t full = bars, empty = full + 8 * S, done = empty + 8 * S, free_ = done + 16, drain = free_ + 16;
+  volatile uint32_t* tmem_at = reinterpret_cast<volatile uint32_t*>(smem + L::kBarAt + 8 * L::kBars);
+  volatile uint32_t* failed = tmem_at + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool clustered = CG == 2 || a.split > 1;
+  const uint32_t rank = clustered ? cta_rank() : 0;
+
+  // this CTA's tiles and its part of the depth (in blocks, from a multiple of 4)
+  const int per = CG == 2 ? 2 : a.split;
+  const int tiles = a.x_tiles * a.y_tiles;
+  const int first = blockIdx.x / per, step = gridDim.x / per;
+  int kb0 = 0, kb1 = a.blocks;
+  if (CG == 1 && a.split > 1) {
+    kb0 = 4 * (int)((int64_t)a.panel * rank / a.split);
+    kb1 = min(a.blocks, 4 * (int)((int64_t)a.panel * (rank + 1) / a.split));
   }
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) {
+      bar_init(full + 8 * i, 1);
+      bar_init(empty + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(done + 8 * i, 1);
+      bar_init(free_ + 8 * i, 4 * CG);
+    }
+    bar_init(drain, 1);
+    *failed = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 2) {
+    if (CG == 1) {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                   ::"r"(smem_addr((const void*)tmem_at)), "r"(L::kCols) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                   ::"r"(smem_addr((const void*)tmem_at)), "r"(L::kCols) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
+  }
+  fence_before();
+  __syncthreads();
+  if (clustered) cluster_sync();
+  fence_after();
+  const uint32_t tmem = *tmem_at;
+
+  if (warp == 0 && lane == 0) {
+    // ------------------------------------------------------------- producer
+    // A pair's copies all count on the leader's barrier.
+    const uint32_t full_at = CG == 2 ? map_to(full, 0) : full;
+    int64_t n = 0;          // stage uses so far
+    bool ok = true;
+    for (int t = first; t < tiles && ok; t += step) {
+      int tx, ty;
+      tile_at(a, t, tx, ty);
+      const int x0 = (tx * CG + (CG == 2 ? (int)rank : 0)) * 128, y0 = ty * NT;
+      for (int kb = kb0; kb < kb1; ++kb, ++n) {
+        const int st = (int)(n % S);
+        if (n >= S && !bar_wait(empty + 8 * st, (uint32_t)(n / S - 1) & 1u)) {
+          ok = false;
+          break;
+        }
+        const bool sc = (kb & 3) == 0;
+        if (CG == 1 || rank == 0)
+          bar_expect(full + 8 * st, CG * (L::kXBytes + L::kYBytes + (sc ? L::kScaleBytes : 0)));
+        const uint32_t dst = ring + st * L::kStage, bar = full_at + 8 * st;
+        tma_2d<CG>(dst, &map_x, kb * kStageDepth, x0, bar);
+        tma_2d<CG>(dst + L::kXBytes, &map_y, kb * kStageDepth, y0 + (CG == 2 ? (int)rank * L::kY : 0), bar);
+        if (sc) {
+          const uint32_t sd = scales + st * L::kScaleBytes;
+          tma_2d<CG>(sd, &map_sx, 0, (x0 >> 7) * a.panel + (kb >> 2), bar);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t r = m0 + tm + i, c = n0 + tn + j;
-      if (r < a.m && c < a.n) {
-        float v[8] = {}, x[8] = {acc[i][j]};
-        if (a.d_addend != nullptr) load8<false>(static_cast<const T*>(a.d_addend) + r * a.addend_pitch + c, 1, v);
-        x[0] += v[0];
-        store8<false>(static_cast<T*>(a.d_out) + r * a.out_pitch + c, 1, x);
+          for (int i = 0; i < L::kYScaleTiles; ++i)
+            tma_2d<CG>(sd + (1 + i) * kScaleTile, &map_sy, 0, ((y0 >> 7) + i) * a.panel + (kb >> 2), bar);
+        }
       }
     }
+    if (!ok) *failed = 1;
+    if (!ok && rank == 0)      // let what was issued land
+      for (int64_t u = n > S ? n - S : 0; u < n; ++u) bar_wait(full + 8 * (int)(u % S), (uint32_t)(u / S) & 1u);
+  } else if (warp == 1 && lane == 0 && (CG == 1 || rank == 0)) {
+    // ------------------------------------------------------------- products
+    int64_t n = 0;
+    int i = 0, set = 0;
+    bool ok = true;
+    for (int t = first; t < tiles && ok; t += step, ++i) {
+      int tx, ty;
+      tile_at(a, t, tx, ty);
+      const uint32_t acc = tmem + (i & 1) * L::kAcc1;
+      const uint32_t y_col = NT < 128 ? (uint32_t)((ty * NT & 127) >> 5) : 0u;   // y's first row within its scale tile
+      if (L::kOverlap ? (i >= 1 && !bar_wait(free_, (uint32_t)(i - 1) & 1u))
+                      : (i >= 2 && !bar_wait(free_ + 8 * (i & 1), (uint32_t)((i >> 1) - 1) & 1u))) {
+        ok = false;
+        break;
+      }
+      fence_after();
+      for (int kb = kb0; kb < kb1; ++kb, ++n) {
+        const int st = (int)(n % S);
+        if (!bar_wait(full + 8 * st, (uint32_t)(n / S) & 1u)) {
+          ok = false;
+          break;
+        }
+        fence_after();
+        if ((kb & 3) == 0) {
+          set ^= 1;
+          const uint32_t col = tmem + L::kScaleCol + set * L::kScaleCols, sd = scales + st * L::kScaleBytes;
+#pragma unroll
+          for (int j = 0; j <= L::kYScaleTiles; ++j) copy_scales<CG>(col + 4 * j, scale_desc(sd + j * kScaleTile));
+        }
+        const uint32_t col = tmem + L::kScaleCol + set * L::kScaleCols;
+        const uint64_t dx = tile_desc(ring + st * L::kStage), dy = tile_desc(ring + st * L::kStage + L::kXBytes);
+        const uint32_t instr = instr_desc<CG, NT>((uint32_t)kb & 3u);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          product<CG>(acc, dx + 2 * j, dy + 2 * j, instr, col, col + 4 + y_col, (kb > kb0 || j > 0) ? 1u : 0u);
+        commit<CG>(empty + 8 * st);
+      }
+      if (ok) commit<CG>(done + 8 * (i & 1));
+    }
+    if (!ok) {
+      *failed = 1;
+      commit<CG>(drain);       // let what was issued end
+      bar_wait(drain, 0);
+    }
+  } else if (warp >= 4) {
+    // --------------------------------------------------------------- output
+    constexpr int C = NT < 32 ? 16 : 32;       // columns at a time
+    const int q = warp - 4;                    // this warp's 32 lanes of tensor memory
+    const uint32_t free_at = CG == 2 ? map_to(free_, 0) : free_;
+    int i = 0;
+    for (int t = first; t < tiles; t += step, ++i) {
+      int tx, ty;
+      tile_at(a, t, tx, ty);
+      if (!__all_sync(0xFFFFFFFFu, bar_wait(done + 8 * (i & 1), (uint32_t)(i >> 1) & 1u))) {
+        *failed = 1;
+        break;
+      }
+      fence_after();
+      const uint32_t acc = tmem + (i & 1) * L::kAcc1 + ((uint32_t)(q * 32) << 16);
+      const int x = (tx * CG + (CG == 2 ? (int)rank : 0)) * 128 + q * 32 + lane, y0 = ty * NT;
+      for (int j = 0; j < NT / C; ++j) {
+        // the shared columns first: the first accumulator's last, the second one's first
+        const int c = (L::kOverlap && (i & 1) == 0) ? NT - C - j * C : j * C;
+        if (y0 + c >= a.ny && !(L::kOverlap && j == 0) && j != NT / C - 1) continue;
+        float v[C];
+        acc_load<C>(acc + c, v);
+        if (j == (L::kOverlap ? 0 : NT / C - 1)) {
+          fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive_cluster((L::kOverlap ? free_at : free_at + 8 * (i & 1)));
+        }
+        if (CG == 1 && a.split > 1) {
+          float* sum = reinterpret_cast<float*>(smem);
+#pragma unroll
+          for (int k = 0; k < C; ++k) sum[(c + k) * 128 + q * 32 + lane] = v[k];
+        } else {
+          store_cols<T, C>(a, x, y0 + c, v);
+        }
+      }
+    }
+  }
+
+  fence_before();
+  __syncthreads();
+  if (CG == 1 && a.split > 1) {
+    // sums of the cluster's parts, in rank order; each CTA takes 128 / split rows of x
+    cluster_sync();
+    int tx, ty;
+    tile_at(a, first, tx, ty);
+    const int rows = 128 / a.split, cols = min(NT, a.ny - ty * NT);
+    for (int e = threadIdx.x; e < rows * cols; e += kThreads) {
+      const int r = (int)rank * rows + e % rows, c = e / rows;
+      float v = 0.0f;
+      for (int p = 0; p < a.split; ++p) {
+        float w;
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(w) : "r"(map_to(ring + 4 * (c * 128 + r), p)));
+        v = p == 0 ? w : v + w;
+      }
+      if (tx * 128 + r < a.nx) store_one<T>(a, tx * 128 + r, ty * NT + c, v);
+    }
+  }
+  if (clustered) cluster_sync();      // a pair's peer, or a reader of this CTA's part, has ended
+  if (threadIdx.x == 0 && *failed) atomicOr(&g_flags, OPT_FLAG_WAIT_TIMEOUT);
+  if (warp == 2) {
+    fence_after();
+    if (CG == 1)
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(L::kCols));
+    else
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(L::kCols));
+  }
+}
+
+// A product over a depth of 0: the addend, or zero.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) no_depth_kernel(const __grid_constant__ MatmulArgs a) {
+  const int64_t n = (int64_t)a.nx * a.ny;
+  for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < n; e += (int64_t)gridDim.x * kThreads)
+    store_one<T>(a, (int)(e / a.ny), (int)(e % a.ny), 0.0f);
+}
+
+// ---------------------------------------------------------------------- host
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn encode_fn() {
+  static const EncodeFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult got;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &got) != cudaSuccess ||
+        got != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeFn>(p);
+  }();
+  return fn;
+}
+
+// rows x bytes matrix of bytes, boxes of 128 bytes by `box` rows, 128-byte swizzle
+bool codes_map(CUtensorMap* m, const void* p, int64_t k, int64_t rows, int64_t pitch, int box) {
+  const cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)(rows > 1 ? pitch : (k + 15) / 16 * 16)};
+  const cuuint32_t boxes[2] = {kStageDepth, (cuuint32_t)box}, ones[2] = {1, 1};
+  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(p), dims, strides, boxes, ones,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// scale tiles as rows of 128 words, one at a time
+bool scales_map(CUtensorMap* m, const void* p, int64_t tiles) {
+  const cuuint64_t dims[2] = {kScaleTile / 4, (cuuint64_t)tiles}, strides[1] = {kScaleTile};
+  const cuuint32_t boxes[2] = {kScaleTile / 4, 1}, ones[2] = {1, 1};
+  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(p), dims, strides, boxes, ones,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Operand {
+  const void* codes;
+  const void* scales;
+  int64_t pitch, rows;
+};
+
+template <typename T, int CG, int NT>
+cudaError_t launch(const Operand& x, const Operand& y, int64_t k, MatmulArgs a, int split, int sm_count,
+                   cudaStream_t s) {
+  using L = Layout<CG, NT>;
+  static OccupancyCache cache;
+  cached_occupancy(matmul_kernel<T, CG, NT>, cache, kThreads, L::kBytes);     // enables the shared memory
+  a.nx = (int)x.rows;
+  a.ny = (int)y.rows;
+  const int64_t xt = (x.rows + 128 * CG - 1) / (128 * CG), yt = (y.rows + NT - 1) / NT;
+  if (xt * yt > 0x7FFFFFF) return cudaErrorInvalidConfiguration;
+  a.x_tiles = (int)xt;
+  a.y_tiles = (int)yt;
+  a.split = split;
+  CUtensorMap mx, my, msx, msy;
+  if (encode_fn() == nullptr || !codes_map(&mx, x.codes, k, x.rows, x.pitch, 128) ||
+      !codes_map(&my, y.codes, k, y.rows, y.pitch, L::kY) ||
+      !scales_map(&msx, x.scales, (x.rows + 127) / 128 * a.panel) ||
+      !scales_map(&msy, y.scales, (y.rows + 127) / 128 * a.panel))
+    return cudaErrorInvalidValue;
+  const int per = CG == 2 ? 2 : split;
+  const int64_t tiles = xt * yt, slots = sm_count / per;
+  cudaLaunchConfig_t cfg = {};
+  // a split tile's cluster takes one tile; others loop
+  cfg.gridDim = dim3((unsigned)((split > 1 || tiles < slots ? tiles : slots) * per));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = L::kBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)per;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = per > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, matmul_kernel<T, CG, NT>, mx, my, msx, msy, a);
+}
+
+template <typename T>
+cudaError_t dispatch(const opt_matmul_args& c, int sm_count, cudaStream_t s) {
+  MatmulArgs a = {};
+  a.out = c.d_out;
+  a.addend = c.d_addend;
+  a.out_pitch = c.out_pitch;
+  a.addend_pitch = c.addend_pitch;
+  const auto fits = [&](const void* p, int64_t pitch) {
+    return ((uintptr_t)p & 15u) == 0 && (c.m == 1 || pitch * (int64_t)sizeof(T) % 16 == 0);
+  };
+  a.vec = fits(c.d_out, c.out_pitch) && (c.d_addend == nullptr || fits(c.d_addend, c.addend_pitch));
+  if (c.k == 0) {
+    a.nx = (int)c.m;
+    a.ny = (int)c.n;
+    no_depth_kernel<T><<<(unsigned)sm_count * 4, kThreads, 0, s>>>(a);
+    return cudaGetLastError();
+  }
+  a.blocks = (int)((c.k + 127) / 128);
+  a.panel = (a.blocks + 3) / 4;
+  Operand x{c.d_a, c.d_a_scales, c.a_pitch, c.m}, y{c.d_b, c.d_b_scales, c.b_pitch, c.n};
+  const int64_t pairs = ((c.m + 255) / 256) * ((c.n + 255) / 256);
+  if (pairs >= sm_count / 4) return launch<T, 2, 256>(x, y, c.k, a, 1, sm_count, s);
+  a.swap = c.n > c.m;
+  if (a.swap) {
+    const Operand o = x;
+    x = y;
+    y = o;
+  }
+  const int nt = y.rows <= 16 ? 16 : y.rows <= 32 ? 32 : y.rows <= 64 ? 64 : 128;
+  const int64_t tiles = ((x.rows + 127) / 128) * ((y.rows + nt - 1) / nt);
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= sm_count && split * 2 <= a.panel) split *= 2;
+  switch (nt) {
+    case 16: return launch<T, 1, 16>(x, y, c.k, a, split, sm_count, s);
+    case 32: return launch<T, 1, 32>(x, y, c.k, a, split, sm_count, s);
+    case 64: return launch<T, 1, 64>(x, y, c.k, a, split, sm_count, s);
+    default: return launch<T, 1, 128>(x, y, c.k, a, split, sm_count, s);
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_matmul(const opt_matmul_args& a, int sm_count, cudaStream_t s) {
-  (void)sm_count;
-  const int64_t ct = (a.n + kTile - 1) / kTile, tiles = (a.m + kTile - 1) / kTile * ct;
-  if (tiles > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  if (a.out_dtype == OPT_F32) matmul_kernel<float><<<(unsigned)tiles, kThreads, 0, s>>>(a, ct);
-  else matmul_kernel<Bf16><<<(unsigned)tiles, kThreads, 0, s>>>(a, ct);
-  return cudaGetLastError();
+  return a.out_dtype == OPT_F32 ? dispatch<float>(a, sm_count, s) : dispatch<Bf16>(a, sm_count, s);
+}
+
+cudaError_t layer_flags(int* flags, cudaStream_t s) {
+  const int zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbolAsync(flags, g_flags, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaMemcpyToSymbolAsync(g_flags, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  return e;
 }
 
 }  // namespace psopt

@@ -63,6 +63,7 @@ SIGS = {
     "opt_rms_norm_backward_workspace": (_i64, [_i64, _i64]),
     "opt_quantize": (_c.c_int, [_c.c_char_p, _vp]),
     "opt_matmul": (_c.c_int, [_c.c_char_p, _vp]),
+    "opt_layer_status": (_c.c_int, [_c.POINTER(_i32), _vp]),
 }
 
 _CODE = {_vp: "Q", _i64: "q", _u64: "Q", _i32: "i", _u32: "I", _f32: "f", _f64: "d"}
@@ -277,3 +278,10 @@ def opt_matmul(a, a_scales, b, b_scales, out, addend=None, stream=None):
     dq, dp = _like(addend, "addend", m, n, out.dtype, dev)
     _check(lib().opt_matmul(_pack_matmul(aq, asq, bq, bsq, dq, out.data_ptr(), ap, bp, dp, op, m, n, k, dt, 0),
                             _stream_ptr(stream)), "opt_matmul")
+
+
+def opt_layer_status(stream=None) -> int:
+    """Error flags of the layer kernels since the last call (0: all ran to completion)."""
+    out = _i32()
+    _check(lib().opt_layer_status(_c.byref(out), _stream_ptr(stream)), "opt_layer_status")
+    return out.value

@@ -434,3 +434,8 @@ def test_calls_replay_from_a_graph():
     calls(want)
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+def test_status_is_clear():
+    """Every kernel of the tests above ran to completion."""
+    assert ps.opt_layer_status() == 0
