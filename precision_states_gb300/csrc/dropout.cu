@@ -15,29 +15,47 @@ constexpr int64_t kMaxGridX = (int64_t)1 << 30;
 template <typename T, bool VEC>
 __device__ __forceinline__ void drop_chunk(const opt_dropout_args& a, const DropArgs& d, int64_t r, int64_t c,
                                            int valid) {
-  float x[8], res[8];
-  load8<VEC>(static_cast<const T*>(a.d_x) + r * a.x_pitch + c, valid, x);
+  const Raw<T> xr = load_raw<VEC>(static_cast<const T*>(a.d_x) + r * a.x_pitch + c, valid);
+  float x[8], y[8] = {};
   if (a.d_residual != nullptr)
-    load8<VEC>(static_cast<const T*>(a.d_residual) + r * a.residual_pitch + c, valid, res);
-  drop8<VEC>(x, (uint64_t)(r * a.cols + c), d);
-  if (a.d_residual != nullptr) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] += res[j];
+    load8<VEC>(static_cast<const T*>(a.d_residual) + r * a.residual_pitch + c, valid, y);
+  unpack(xr, x);
+  add_dropped8<VEC>(y, x, (uint64_t)(r * a.cols + c), d);
+  store8<VEC>(static_cast<T*>(a.d_y) + r * a.y_pitch + c, valid, y);
+}
+// A matrix's ragged end, element by element, so that it adds nothing to the main
+// path's registers; chunks of a VEC matrix start on a generator call.
+template <typename T>
+__device__ __forceinline__ void drop_end(const opt_dropout_args& a, const DropArgs& d, int64_t r, int64_t c, int valid) {
+  const uint4 w = drop_group((uint64_t)(r * a.cols + c) >> 3, d);
+#pragma unroll 1
+  for (int j = 0; j < valid; ++j) {
+    const uint32_t word = j < 2 ? w.x : j < 4 ? w.y : j < 6 ? w.z : w.w;
+    const uint32_t draw = (word >> (16 * (j & 1))) & 0xFFFFu;
+    const T* res = static_cast<const T*>(a.d_residual);
+    float x[8], y[8] = {};
+    load8<false>(static_cast<const T*>(a.d_x) + r * a.x_pitch + c + j, 1, x);
+    if (res != nullptr) load8<false>(res + r * a.residual_pitch + c + j, 1, y);
+    if (draw >= d.threshold) y[0] = fmaf(x[0], d.factor, y[0]);
+    store8<false>(static_cast<T*>(a.d_y) + r * a.y_pitch + c + j, 1, y);
   }
-  store8<VEC>(static_cast<T*>(a.d_y) + r * a.y_pitch + c, valid, x);
 }
 
 // One chunk of eight elements per thread; chunk `c` of row `r` starts at 8 c.
 // A contiguous matrix comes as one row.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant__ opt_dropout_args a,
-                                                           const __grid_constant__ DropArgs d, int64_t first) {
+__global__ void __launch_bounds__(kThreads, VEC ? 6 : 4)
+dropout_kernel(const __grid_constant__ opt_dropout_args a, const __grid_constant__ DropArgs d, int64_t first) {
   const int64_t c = 8 * (first + (int64_t)blockIdx.x * kThreads + threadIdx.x);
   if (c >= a.cols) return;
   const int valid = (int)(a.cols - c < 8 ? a.cols - c : 8);
   for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
-    if (VEC && valid == 8) drop_chunk<T, true>(a, d, r, c, 8);
-    else drop_chunk<T, false>(a, d, r, c, valid);
+    if constexpr (VEC) {
+      if (valid == 8) drop_chunk<T, true>(a, d, r, c, 8);
+      else drop_end<T>(a, d, r, c, valid);
+    } else {
+      drop_chunk<T, false>(a, d, r, c, valid);
+    }
   }
 }
 

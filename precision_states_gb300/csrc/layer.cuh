@@ -16,45 +16,63 @@ namespace psopt {
 
 struct Bf16 { uint16_t bits; };   // storage type of an OPT_BF16 element
 
+// Eight elements as they lie in memory (16 or 32 bytes): what a thread holds of
+// a row that it has loaded ahead.
+template <typename T>
+struct Raw {
+  static constexpr int kWords = 2 * sizeof(T);
+  uint32_t w[kWords];
+};
+
 // Eight elements at p.  VEC: all eight exist and p is 16-byte aligned;
 // otherwise the first `valid` exist, and the others read as 0.
-template <bool VEC>
-__device__ __forceinline__ void load8(const Bf16* p, int valid, float (&x)[8]) {
-  if (VEC) {
-    uint4 w;
-    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "l"(p));
-    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+template <bool VEC, typename T>
+__device__ __forceinline__ Raw<T> load_raw(const T* p, int valid) {
+  Raw<T> r;
+  if constexpr (VEC) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      x[2 * k] = u2f(ws[k] << 16);
-      x[2 * k + 1] = u2f(ws[k] & 0xFFFF0000u);
-    }
+    for (int k = 0; k < Raw<T>::kWords; k += 4)
+      asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(r.w[k]), "=r"(r.w[k + 1]), "=r"(r.w[k + 2]), "=r"(r.w[k + 3])
+                   : "l"(reinterpret_cast<const uint32_t*>(p) + k));
+  } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r.w[j] = j < valid ? f2u(p[j]) : 0u;
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = j < valid ? u2f((uint32_t)p[j].bits << 16) : 0.0f;
+    for (int k = 0; k < 4; ++k)
+      r.w[k] = (2 * k < valid ? (uint32_t)p[2 * k].bits : 0u) |
+               (2 * k + 1 < valid ? (uint32_t)p[2 * k + 1].bits << 16 : 0u);
+  }
+  return r;
+}
+__device__ __forceinline__ void unpack(const Raw<float>& r, float (&x)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = u2f(r.w[j]);
+}
+__device__ __forceinline__ void unpack(const Raw<Bf16>& r, float (&x)[8]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    x[2 * k] = u2f(r.w[k] << 16);
+    x[2 * k + 1] = u2f(r.w[k] & 0xFFFF0000u);
   }
 }
-template <bool VEC>
-__device__ __forceinline__ void load8(const float* p, int valid, float (&x)[8]) {
-  if (VEC) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      float4 v;
-      asm volatile("ld.global.v4.f32 {%0,%1,%2,%3}, [%4];"
-                   : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p + 4 * k));
-      x[4 * k] = v.x; x[4 * k + 1] = v.y; x[4 * k + 2] = v.z; x[4 * k + 3] = v.w;
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = j < valid ? p[j] : 0.0f;
-  }
+template <bool VEC, typename T>
+__device__ __forceinline__ void load8(const T* p, int valid, float (&x)[8]) {
+  unpack(load_raw<VEC>(p, valid), x);
 }
 
+// Nearest BF16 of two values (a NaN as the converter's canonical one).
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
 template <bool VEC>
 __device__ __forceinline__ void store8(Bf16* p, int valid, const float (&x)[8]) {
   uint32_t w[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) w[k] = bf16x2_rn(x[2 * k], x[2 * k + 1]);
+  for (int k = 0; k < 4; ++k) w[k] = bf16_pair(x[2 * k], x[2 * k + 1]);
   if (VEC) {
     st_cs_u4(p, make_uint4(w[0], w[1], w[2], w[3]));
   } else {
@@ -104,16 +122,23 @@ __device__ __forceinline__ uint4 drop_draws(uint64_t i, const DropArgs& d) {
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
-// x <- dropout(x) for the eight elements from i on.
+// sum <- sum + dropout(x) for the eight elements from i on.  Draws are compared
+// in the upper half of a word (a draw is at least T iff it is there at least T
+// shifted up): no half is taken apart, and a kept element costs one fused
+// multiply-add.  T = 65536 keeps nothing.
 template <bool VEC>
-__device__ __forceinline__ void drop8(float (&x)[8], uint64_t i, const DropArgs& d) {
-  if (d.threshold == 0u) return;
-  const uint4 r = drop_draws<VEC>(i, d);
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+__device__ __forceinline__ void add_dropped8(float (&sum)[8], const float (&x)[8], uint64_t i, const DropArgs& d) {
+  if (d.threshold == 0u) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t draw = (w[j >> 1] >> (16 * (j & 1))) & 0xFFFFu;
-    x[j] = draw >= d.threshold ? x[j] * d.factor : 0.0f;
+    for (int j = 0; j < 8; ++j) sum[j] += x[j];
+  } else if (d.threshold < 65536u) {
+    const uint4 r = drop_draws<VEC>(i, d);
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w}, least = d.threshold << 16;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if ((w[k] << 16) >= least) sum[2 * k] = fmaf(x[2 * k], d.factor, sum[2 * k]);
+      if (w[k] >= least) sum[2 * k + 1] = fmaf(x[2 * k + 1], d.factor, sum[2 * k + 1]);
+    }
   }
 }
 
@@ -128,28 +153,39 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t top_bits) {
 // 2^-e for a scale byte; scale_byte never exceeds 247, so this is normal.
 __device__ __forceinline__ float inverse_scale(uint32_t byte) { return u2f((254u - byte) << 23); }
 
-__device__ __forceinline__ uint32_t magnitude(float x) { return f2u(x) & 0x7FFFFFFFu; }
-constexpr uint32_t kInfBits = 0x7F800000u;
-
-// Largest magnitude's bits of eight elements (as integers: the order of the
-// magnitudes, with infinity and NaN above all); finite_top8 leaves those out.
-__device__ __forceinline__ uint32_t top8(const float (&x)[8]) {
-  uint32_t t = 0;
+__device__ __forceinline__ bool finite_bits(float x) { return (f2u(x) & 0x7F800000u) != 0x7F800000u; }
+// The larger magnitude; NaN if either is one.
+__device__ __forceinline__ float larger(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
+}
+__device__ __forceinline__ float largest8(const float (&x)[8]) {
+  return larger(larger(larger(x[0], x[1]), larger(x[2], x[3])), larger(larger(x[4], x[5]), larger(x[6], x[7])));
+}
+// The same of the finite elements.
+__device__ __forceinline__ float largest_finite8(const float (&x)[8]) {
+  float t = 0.0f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) t = max(t, magnitude(x[j]));
+  for (int j = 0; j < 8; ++j) t = finite_bits(x[j]) ? larger(t, x[j]) : t;
   return t;
 }
-__device__ __forceinline__ uint32_t finite_top8(const float (&x)[8]) {
-  uint32_t t = 0;
+// Over the 16 lanes of a 128-element block.
+__device__ __forceinline__ float largest16(float t) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) t = max(t, magnitude(x[j]) < kInfBits ? magnitude(x[j]) : 0u);
+  for (int o = 8; o > 0; o >>= 1) t = larger(t, __shfl_xor_sync(0xFFFFFFFFu, t, o));
   return t;
 }
-// Largest of a value over the 16 lanes of a 128-element block.
-__device__ __forceinline__ uint32_t max16(uint32_t t) {
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) t = max(t, __shfl_xor_sync(0xFFFFFFFFu, t, o));
-  return t;
+// The scale byte of the 1 x 128 block that 16 lanes hold eight elements each of,
+// by the whole warp; `odd`: it holds an infinity or NaN.
+__device__ __forceinline__ uint32_t block_byte(const float (&x)[8], bool& odd) {
+  float top = largest16(largest8(x));
+  odd = !finite_bits(top);
+  if (__any_sync(0xFFFFFFFFu, odd)) {
+    const float finite = largest16(largest_finite8(x));
+    if (odd) top = finite;
+  }
+  return scale_byte(f2u(top));
 }
 
 // Codes of eight elements over 2^e (inv = 2^-e); `odd` says that the block
@@ -162,7 +198,7 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], float inv, bool odd
   if (odd) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (magnitude(x[j]) >= kInfBits) v[j] = u2f(0x7FC00000u);
+      if (!finite_bits(x[j])) v[j] = u2f(0x7FC00000u);
   }
   return make_uint2(e4m3x2_rn(v[0], v[1]) | (e4m3x2_rn(v[2], v[3]) << 16),
                     e4m3x2_rn(v[4], v[5]) | (e4m3x2_rn(v[6], v[7]) << 16));

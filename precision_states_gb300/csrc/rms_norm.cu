@@ -1,140 +1,292 @@
 // rms_norm.cu -- branch dropout, residual sum, root-mean-square norm and 8-bit
 // output, and their gradients (opt_layer.h).
+//
+// Mathematics: each row needs one sum (of h^2, or of g h) before any output, so
+// a row's data stay in registers from the one load to the stores.  A row is
+// taken by a CTA (by one warp, eight rows per CTA, up to 256 columns), each
+// thread holding NG chunks of eight elements; a CTA goes through many rows, so
+// that the weight (and the weight's gradient) stay in registers too, and the
+// next row's loads are issued before the current row's sum is complete.  Rows
+// too wide for that take a second form that reads them twice.
 #include "layer.cuh"
 
 namespace psopt {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kWideThreads = 512;       // of the form that reads rows twice
+constexpr int kDweightCols = 32, kDweightParts = 32;
 
 // Chunk c (eight elements) of row r of h = residual + dropout(x).
 template <typename T, bool VEC>
-__device__ __forceinline__ void h_chunk(const opt_rms_norm_args& a, const DropArgs& d, int64_t r, int64_t c, int valid,
-                                        float (&h)[8]) {
-  load8<VEC>(static_cast<const T*>(a.d_x) + r * a.x_pitch + c, valid, h);
-  drop8<VEC>(h, (uint64_t)(r * a.cols + c), d);
-  if (a.d_residual != nullptr) {
-    float res[8];
-    load8<VEC>(static_cast<const T*>(a.d_residual) + r * a.residual_pitch + c, valid, res);
+__device__ __forceinline__ void h_chunk(const opt_rms_norm_args& a, const DropArgs& d, int64_t r, int64_t c,
+                                        const Raw<T>& x_raw, const Raw<T>& res_raw, float (&h)[8]) {
+  float x[8];
+  unpack(x_raw, x);
+  unpack(res_raw, h);
+  add_dropped8<VEC>(h, x, (uint64_t)(r * a.cols + c), d);
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_chunk(const opt_rms_norm_args& a, int64_t r, int64_t c, int valid, Raw<T>& x,
+                                           Raw<T>& res) {
+  x = load_raw<VEC>(static_cast<const T*>(a.d_x) + r * a.x_pitch + c, valid);
+  if (a.d_residual != nullptr) res = load_raw<VEC>(static_cast<const T*>(a.d_residual) + r * a.residual_pitch + c, valid);
+}
+
+// Everything that is written of a chunk, by whole warps; chunks beyond the row
+// come with valid <= 0.
+template <typename T, bool VEC>
+__device__ __forceinline__ void write_chunk(const opt_rms_norm_args& a, int64_t r, int64_t c, int valid, float rstd,
+                                            int64_t panel, const float (&h)[8], const float (&w)[8]) {
+  float y[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) h[j] += res[j];
+  for (int j = 0; j < 8; ++j) y[j] = (h[j] * rstd) * w[j];
+  if (valid > 0) {
+    if (a.d_h != nullptr) store8<VEC>(static_cast<T*>(a.d_h) + r * a.h_pitch + c, valid, h);
+    if (a.d_y != nullptr) store8<VEC>(static_cast<T*>(a.d_y) + r * a.y_pitch + c, valid, y);
+  }
+  if (a.d_codes == nullptr) return;
+  if (valid < 8) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = j < valid ? y[j] : 0.0f;
+  }
+  bool odd;
+  const uint32_t byte = block_byte(y, odd);
+  if (valid > 0) {
+    store_codes8(static_cast<uint8_t*>(a.d_codes) + r * a.codes_pitch + c, valid, codes8(y, inverse_scale(byte), odd));
+    if ((threadIdx.x & 15) == 0) static_cast<uint8_t*>(a.d_scales)[scale_place(r, c >> 7, panel)] = (uint8_t)byte;
   }
 }
 
-// One CTA per row, any width: a pass for the sum of squares, a second one that
-// forms h again and writes.
+// Rows in registers.  `warps` per row; thread t of a row holds chunks t + k
+// 32 warps for k < NG.
+template <typename T, typename W, bool VEC, int NG, int MAX>
+__global__ void __launch_bounds__(MAX, NG == 1 ? 2 : 1) rms_norm_kernel(const __grid_constant__ opt_rms_norm_args a,
+                                                       const __grid_constant__ DropArgs d, int warps) {
+  __shared__ float part[2][33];
+  const int in_row = warps == 1 ? (int)(threadIdx.x & 31) : (int)threadIdx.x;
+  const int64_t row0 = warps == 1 ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+  const int64_t row_step = warps == 1 ? (int64_t)gridDim.x * (blockDim.x >> 5) : gridDim.x;
+  const int64_t panel = (a.cols + 511) / 512;
+  const float inv_cols = 1.0f / (float)a.cols;
+  int64_t c[NG];
+  int valid[NG];
+  float w[NG][8];
+  Raw<T> x[NG] = {}, res[NG] = {};
+#pragma unroll
+  for (int k = 0; k < NG; ++k) {
+    c[k] = 8 * ((int64_t)in_row + k * 32 * warps);
+    valid[k] = (int)max(min(a.cols - c[k], (int64_t)8), (int64_t)0);
+    if (valid[k] > 0) {
+      if (row0 < a.rows) load_chunk<T, VEC>(a, row0, c[k], valid[k], x[k], res[k]);
+      load8<VEC>(static_cast<const W*>(a.d_weight) + c[k], valid[k], w[k]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[k][j] = 0.0f;
+    }
+  }
+  int turn = 0;
+  for (int64_t r = row0; r < a.rows; r += row_step, turn ^= 1) {
+    float h[NG][8], sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NG; ++k) {
+      h_chunk<T, VEC>(a, d, r, c[k], x[k], res[k], h[k]);
+      // the next row, while this one's sum is formed
+      if (valid[k] > 0 && r + row_step < a.rows) load_chunk<T, VEC>(a, r + row_step, c[k], valid[k], x[k], res[k]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum = fmaf(h[k][j], h[k][j], sum);
+    }
+    sum = cta_sum(sum, part[turn], warps);
+    const float rstd = 1.0f / sqrtf(fmaf(sum, inv_cols, a.eps));
+    if (in_row == 0 && a.d_rstd != nullptr) a.d_rstd[r] = rstd;
+#pragma unroll
+    for (int k = 0; k < NG; ++k) write_chunk<T, VEC>(a, r, c[k], valid[k], rstd, panel, h[k], w[k]);
+  }
+}
+
+// Wide rows: a pass for the sum of squares, a second one that forms h again
+// (the row is still in L2) and writes.
 template <typename T, typename W, bool VEC>
-__global__ void __launch_bounds__(kThreads) rms_norm_kernel(const __grid_constant__ opt_rms_norm_args a,
-                                                            const __grid_constant__ DropArgs d) {
+__global__ void __launch_bounds__(kWideThreads) rms_norm_wide_kernel(const __grid_constant__ opt_rms_norm_args a,
+                                                                     const __grid_constant__ DropArgs d) {
   __shared__ float part[2][33];
   const int64_t panel = (a.cols + 511) / 512;
   int turn = 0;
   for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, turn ^= 1) {
-    float sum = 0.0f, h[8];
-    for (int64_t c = 8 * threadIdx.x; c < a.cols; c += 8 * kThreads) {
-      h_chunk<T, VEC>(a, d, r, c, (int)min(a.cols - c, (int64_t)8), h);
+    float sum = 0.0f, h[8], w[8];
+    Raw<T> x, res = {};
+    for (int64_t c = 8 * threadIdx.x; c < a.cols; c += 8 * kWideThreads) {
+      load_chunk<T, VEC>(a, r, c, (int)min(a.cols - c, (int64_t)8), x, res);
+      h_chunk<T, VEC>(a, d, r, c, x, res, h);
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum = fmaf(h[j], h[j], sum);
     }
-    sum = cta_sum(sum, part[turn], kWarps);
-    const float rstd = 1.0f / sqrtf(sum / (float)a.cols + a.eps);
+    sum = cta_sum(sum, part[turn], kWideThreads / 32);
+    const float rstd = 1.0f / sqrtf(fmaf(sum, 1.0f / (float)a.cols, a.eps));
     if (threadIdx.x == 0 && a.d_rstd != nullptr) a.d_rstd[r] = rstd;
-    for (int64_t c0 = 0; c0 < a.cols; c0 += 8 * kThreads) {
+    for (int64_t c0 = 0; c0 < a.cols; c0 += 8 * kWideThreads) {
       const int64_t c = c0 + 8 * threadIdx.x;
       const int valid = (int)max(min(a.cols - c, (int64_t)8), (int64_t)0);
-      float y[8];
       if (valid > 0) {
-        h_chunk<T, VEC>(a, d, r, c, valid, h);
-        if (a.d_h != nullptr) store8<VEC>(static_cast<T*>(a.d_h) + r * a.h_pitch + c, valid, h);
-        load8<VEC>(static_cast<const W*>(a.d_weight) + c, valid, y);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] *= h[j] * rstd;
-        if (a.d_y != nullptr) store8<VEC>(static_cast<T*>(a.d_y) + r * a.y_pitch + c, valid, y);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = j < valid ? y[j] : 0.0f;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = 0.0f;
+        load_chunk<T, VEC>(a, r, c, valid, x, res);
+        h_chunk<T, VEC>(a, d, r, c, x, res, h);
+        load8<VEC>(static_cast<const W*>(a.d_weight) + c, valid, w);
       }
-      if (a.d_codes != nullptr) {
-        uint32_t top = max16(top8(y));
-        const bool odd = top >= kInfBits;
-        if (__any_sync(0xFFFFFFFFu, odd)) {
-          const uint32_t finite = max16(finite_top8(y));
-          if (odd) top = finite;
-        }
-        const uint32_t byte = scale_byte(top);
-        if (valid > 0) {
-          store_codes8(static_cast<uint8_t*>(a.d_codes) + r * a.codes_pitch + c, valid,
-                       codes8(y, inverse_scale(byte), odd));
-          if ((threadIdx.x & 15) == 0)
-            static_cast<uint8_t*>(a.d_scales)[scale_place(r, c >> 7, panel)] = (uint8_t)byte;
-        }
-      }
+      write_chunk<T, VEC>(a, r, c, valid, rstd, panel, h, w);
     }
   }
 }
 
-// One CTA per row at a time; the weight's gradient is summed over the CTA's
-// rows in its row of the workspace, each column by the same thread throughout.
-template <typename T, typename W, bool VEC>
-__global__ void __launch_bounds__(kThreads) rms_norm_backward_kernel(
+// ------------------------------------------------------------------ gradients
+// What is written of a chunk of the gradients: dh and dx from g = dy weight.
+template <typename T, bool VEC>
+__device__ __forceinline__ void write_gradients(const opt_rms_norm_backward_args& a, const DropArgs& d, int64_t r,
+                                                int64_t c, int valid, float rstd, float k, const float (&g)[8],
+                                                const float (&h)[8], const float (&in)[8]) {
+  float out[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) out[j] = fmaf(rstd, fmaf(-h[j], k, g[j]), in[j]);
+  store8<VEC>(static_cast<T*>(a.d_dh) + r * a.dh_pitch + c, valid, out);
+  if (a.d_dx != nullptr) {
+    float dx[8] = {};
+    add_dropped8<VEC>(dx, out, (uint64_t)(r * a.cols + c), d);
+    store8<VEC>(static_cast<T*>(a.d_dx) + r * a.dx_pitch + c, valid, dx);
+  }
+}
+
+// This CTA's (or, with a row per warp, this warp's) row of partial sums.
+__device__ __forceinline__ float* dweight_row(const opt_rms_norm_backward_args& a, int64_t part) {
+  return static_cast<float*>(a.d_workspace) + part * ((a.cols + 3) / 4 * 4);
+}
+
+template <typename T, typename W, bool VEC, int NG, int MAX, int CTAS>
+__global__ void __launch_bounds__(MAX, CTAS) rms_norm_backward_kernel(
     const __grid_constant__ opt_rms_norm_backward_args a, const __grid_constant__ DropArgs d) {
   __shared__ float part[2][33];
-  float* dw = a.d_dweight == nullptr ? nullptr
-                                     : static_cast<float*>(a.d_workspace) + (int64_t)blockIdx.x * ((a.cols + 3) / 4 * 4);
+  const int warps = blockDim.x >> 5;
+  const float inv_cols = 1.0f / (float)a.cols;
+  int64_t c[NG];
+  int valid[NG];
+  float dw[NG][8] = {};
+  Raw<W> w[NG] = {};
+  Raw<T> dy[NG] = {}, h[NG] = {}, in[NG] = {};
+  const auto load = [&](int k, int64_t r) {
+    dy[k] = load_raw<VEC>(static_cast<const T*>(a.d_dy) + r * a.dy_pitch + c[k], valid[k]);
+    h[k] = load_raw<VEC>(static_cast<const T*>(a.d_h) + r * a.h_pitch + c[k], valid[k]);
+  };
+#pragma unroll
+  for (int k = 0; k < NG; ++k) {
+    c[k] = 8 * ((int64_t)threadIdx.x + k * (int64_t)blockDim.x);
+    valid[k] = (int)max(min(a.cols - c[k], (int64_t)8), (int64_t)0);
+    if (valid[k] > 0) {
+      load(k, blockIdx.x);
+      w[k] = load_raw<VEC>(static_cast<const W*>(a.d_weight) + c[k], valid[k]);
+    }
+  }
+  int turn = 0;
+  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, turn ^= 1) {
+    const float rstd = a.d_rstd[r];
+    float g[NG][8], hv[NG][8], sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NG; ++k) {
+      float wv[8];
+      unpack(dy[k], g[k]);
+      unpack(h[k], hv[k]);
+      unpack(w[k], wv);
+      if (a.d_dh_in != nullptr && valid[k] > 0)
+        in[k] = load_raw<VEC>(static_cast<const T*>(a.d_dh_in) + r * a.dh_in_pitch + c[k], valid[k]);
+      if (valid[k] > 0 && r + gridDim.x < a.rows) load(k, r + gridDim.x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        dw[k][j] = fmaf(g[k][j], hv[k][j] * rstd, dw[k][j]);
+        g[k][j] *= wv[j];
+        sum = fmaf(g[k][j], hv[k][j], sum);
+      }
+    }
+    sum = cta_sum(sum, part[turn], warps);
+    const float scale = rstd * rstd * (sum * inv_cols);
+#pragma unroll
+    for (int k = 0; k < NG; ++k)
+      if (valid[k] > 0) {
+        float add[8];
+        unpack(in[k], add);
+        write_gradients<T, VEC>(a, d, r, c[k], valid[k], rstd, scale, g[k], hv[k], add);
+      }
+  }
+  if (a.d_dweight != nullptr) {
+    float* out = dweight_row(a, blockIdx.x);
+#pragma unroll
+    for (int k = 0; k < NG; ++k)
+      if (valid[k] > 0) {
+        if (valid[k] == 8) {
+          *reinterpret_cast<float4*>(out + c[k]) = make_float4(dw[k][0], dw[k][1], dw[k][2], dw[k][3]);
+          *reinterpret_cast<float4*>(out + c[k] + 4) = make_float4(dw[k][4], dw[k][5], dw[k][6], dw[k][7]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < valid[k]) out[c[k] + j] = dw[k][j];
+        }
+      }
+  }
+}
+
+// Wide rows, read twice; each column of the partial sums belongs to one thread.
+template <typename T, typename W, bool VEC>
+__global__ void __launch_bounds__(kWideThreads) rms_norm_backward_wide_kernel(
+    const __grid_constant__ opt_rms_norm_backward_args a, const __grid_constant__ DropArgs d) {
+  __shared__ float part[2][33];
+  float* dw = a.d_dweight == nullptr ? nullptr : dweight_row(a, blockIdx.x);
   int turn = 0;
   for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, turn ^= 1) {
     const T* dy_row = static_cast<const T*>(a.d_dy) + r * a.dy_pitch;
     const T* h_row = static_cast<const T*>(a.d_h) + r * a.h_pitch;
-    float sum = 0.0f, dy[8], h[8], w[8];
-    for (int64_t c = 8 * threadIdx.x; c < a.cols; c += 8 * kThreads) {
+    float sum = 0.0f, g[8], h[8], w[8];
+    for (int64_t c = 8 * threadIdx.x; c < a.cols; c += 8 * kWideThreads) {
       const int valid = (int)min(a.cols - c, (int64_t)8);
-      load8<VEC>(dy_row + c, valid, dy);
+      load8<VEC>(dy_row + c, valid, g);
       load8<VEC>(h_row + c, valid, h);
       load8<VEC>(static_cast<const W*>(a.d_weight) + c, valid, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum = fmaf(dy[j] * w[j], h[j], sum);
+      for (int j = 0; j < 8; ++j) sum = fmaf(g[j] * w[j], h[j], sum);
     }
-    sum = cta_sum(sum, part[turn], kWarps);
+    sum = cta_sum(sum, part[turn], kWideThreads / 32);
     const float rstd = a.d_rstd[r];
     const float k = rstd * rstd * (sum / (float)a.cols);
-    for (int64_t c = 8 * threadIdx.x; c < a.cols; c += 8 * kThreads) {
+    for (int64_t c = 8 * threadIdx.x; c < a.cols; c += 8 * kWideThreads) {
       const int valid = (int)min(a.cols - c, (int64_t)8);
-      load8<VEC>(dy_row + c, valid, dy);
+      load8<VEC>(dy_row + c, valid, g);
       load8<VEC>(h_row + c, valid, h);
       load8<VEC>(static_cast<const W*>(a.d_weight) + c, valid, w);
-      if (dw != nullptr) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j < valid) dw[c + j] = (r == blockIdx.x ? 0.0f : dw[c + j]) + dy[j] * (h[j] * rstd);
+      for (int j = 0; j < 8; ++j) {
+        if (dw != nullptr && j < valid)
+          dw[c + j] = fmaf(g[j], h[j] * rstd, r == (int64_t)blockIdx.x ? 0.0f : dw[c + j]);
+        g[j] *= w[j];
       }
-      float g[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) g[j] = rstd * (dy[j] * w[j] - h[j] * k);
-      if (a.d_dh_in != nullptr) {
-        load8<VEC>(static_cast<const T*>(a.d_dh_in) + r * a.dh_in_pitch + c, valid, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] += w[j];
-      }
-      store8<VEC>(static_cast<T*>(a.d_dh) + r * a.dh_pitch + c, valid, g);
-      if (a.d_dx != nullptr) {
-        drop8<VEC>(g, (uint64_t)(r * a.cols + c), d);
-        store8<VEC>(static_cast<T*>(a.d_dx) + r * a.dx_pitch + c, valid, g);
-      }
+      float in[8] = {};
+      if (a.d_dh_in != nullptr) load8<VEC>(static_cast<const T*>(a.d_dh_in) + r * a.dh_in_pitch + c, valid, in);
+      write_gradients<T, VEC>(a, d, r, c, valid, rstd, k, g, h, in);
     }
   }
 }
 
-// dweight = the sum over the workspace's rows, in order.
-__global__ void __launch_bounds__(kThreads) dweight_kernel(const float* __restrict__ parts, int n, int64_t cols,
-                                                           float* __restrict__ out) {
-  const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (c >= cols) return;
-  const int64_t pitch = (cols + 3) / 4 * 4;
+// dweight = the sum over the workspace's `n` rows in a fixed order: a CTA takes
+// 32 columns, thread row p the partial sums p, p + 32, ..., and the 32 thread
+// rows are added in order.
+__global__ void __launch_bounds__(kDweightCols * kDweightParts) dweight_kernel(const float* __restrict__ parts, int n,
+                                                                               int64_t cols, float* __restrict__ out) {
+  __shared__ float sums[kDweightParts][kDweightCols + 1];
+  const int x = threadIdx.x % kDweightCols, p0 = threadIdx.x / kDweightCols;
+  const int64_t c = (int64_t)blockIdx.x * kDweightCols + x, pitch = (cols + 3) / 4 * 4;
   float s = 0.0f;
-  for (int p = 0; p < n; ++p) s += parts[p * pitch + c];
+  if (c < cols) {
+#pragma unroll 4
+    for (int p = p0; p < n; p += kDweightParts) s += parts[p * pitch + c];
+  }
+  sums[p0][x] = s;
+  __syncthreads();
+  if (p0 != 0 || c >= cols) return;
+#pragma unroll
+  for (int p = 1; p < kDweightParts; ++p) s += sums[p][x];
   out[c] = s;
 }
 
@@ -147,6 +299,27 @@ struct VecRule {
   }
 };
 
+template <typename T, typename W, bool VEC, int NG, int MAX>
+cudaError_t forward_rows(const opt_rms_norm_args& a, const DropArgs& d, int sm_count, int warps, cudaStream_t s) {
+  const int threads = warps == 1 ? 256 : 32 * warps;
+  static OccupancyCache cache[33];
+  const int64_t rows_per_cta = warps == 1 ? 8 : 1, need = (a.rows + rows_per_cta - 1) / rows_per_cta;
+  const int64_t most = (int64_t)sm_count * cached_occupancy(rms_norm_kernel<T, W, VEC, NG, MAX>, cache[warps], threads, 0);
+  rms_norm_kernel<T, W, VEC, NG, MAX><<<(unsigned)(need < most ? need : most), threads, 0, s>>>(a, d, warps);
+  return cudaGetLastError();
+}
+
+template <typename T, typename W, bool VEC>
+cudaError_t forward_vec(const opt_rms_norm_args& a, const DropArgs& d, int sm_count, cudaStream_t s) {
+  const int64_t chunks = (a.cols + 7) / 8;
+  if (chunks <= 512) return forward_rows<T, W, VEC, 1, 512>(a, d, sm_count, (int)((chunks + 31) / 32), s);
+  if (chunks <= 1024) return forward_rows<T, W, VEC, 2, 512>(a, d, sm_count, (int)((chunks + 63) / 64), s);
+  if (chunks <= 2048) return forward_rows<T, W, VEC, 4, 512>(a, d, sm_count, (int)((chunks + 127) / 128), s);
+  const int64_t most = (int64_t)sm_count * 4;
+  rms_norm_wide_kernel<T, W, VEC><<<(unsigned)(a.rows < most ? a.rows : most), kWideThreads, 0, s>>>(a, d);
+  return cudaGetLastError();
+}
+
 template <typename T, typename W>
 cudaError_t forward(const opt_rms_norm_args& a, const DropArgs& d, int sm_count, cudaStream_t s) {
   VecRule v{a.rows, a.cols, a.cols % 8 == 0};
@@ -155,10 +328,36 @@ cudaError_t forward(const opt_rms_norm_args& a, const DropArgs& d, int sm_count,
   v.see(a.d_weight, 0, sizeof(W));
   v.see(a.d_h, a.h_pitch, sizeof(T));
   v.see(a.d_y, a.y_pitch, sizeof(T));
-  const int64_t most = (int64_t)sm_count * 8;
+  return v.ok ? forward_vec<T, W, true>(a, d, sm_count, s) : forward_vec<T, W, false>(a, d, sm_count, s);
+}
+
+template <typename T, typename W, bool VEC, int NG, int MAX, int CTAS>
+int backward_rows(const opt_rms_norm_backward_args& a, const DropArgs& d, int sm_count, int threads, cudaStream_t s) {
+  static OccupancyCache cache[33];
+  int64_t most = (int64_t)sm_count *
+                 cached_occupancy(rms_norm_backward_kernel<T, W, VEC, NG, MAX, CTAS>, cache[threads / 32], threads, 0);
+  if (most > kNormBackwardMaxCtas) most = kNormBackwardMaxCtas;
   const int grid = (int)(a.rows < most ? a.rows : most);
-  if (v.ok) rms_norm_kernel<T, W, true><<<grid, kThreads, 0, s>>>(a, d);
-  else rms_norm_kernel<T, W, false><<<grid, kThreads, 0, s>>>(a, d);
+  rms_norm_backward_kernel<T, W, VEC, NG, MAX, CTAS><<<grid, threads, 0, s>>>(a, d);
+  return grid;
+}
+
+template <typename T, typename W, bool VEC>
+cudaError_t backward_vec(const opt_rms_norm_backward_args& a, const DropArgs& d, int sm_count, cudaStream_t s) {
+  const int64_t chunks = (a.cols + 7) / 8;
+  int grid;
+  if (chunks <= 512) {
+    grid = backward_rows<T, W, VEC, 1, 512, 2>(a, d, sm_count, (int)((chunks + 31) / 32) * 32, s);
+  } else if (chunks <= 1024) {
+    grid = backward_rows<T, W, VEC, 2, 512, 1>(a, d, sm_count, (int)((chunks + 63) / 64) * 32, s);
+  } else {
+    const int64_t most = (int64_t)sm_count * 4;
+    grid = (int)(a.rows < most ? a.rows : most);
+    rms_norm_backward_wide_kernel<T, W, VEC><<<grid, kWideThreads, 0, s>>>(a, d);
+  }
+  if (a.d_dweight != nullptr)
+    dweight_kernel<<<(unsigned)((a.cols + kDweightCols - 1) / kDweightCols), kDweightCols * kDweightParts, 0, s>>>(
+        static_cast<const float*>(a.d_workspace), grid, a.cols, a.d_dweight);
   return cudaGetLastError();
 }
 
@@ -171,15 +370,7 @@ cudaError_t backward(const opt_rms_norm_backward_args& a, const DropArgs& d, int
   v.see(a.d_dh_in, a.dh_in_pitch, sizeof(T));
   v.see(a.d_dh, a.dh_pitch, sizeof(T));
   v.see(a.d_dx, a.dx_pitch, sizeof(T));
-  int64_t most = (int64_t)sm_count * 4;
-  if (most > kNormBackwardMaxCtas) most = kNormBackwardMaxCtas;
-  const int grid = (int)(a.rows < most ? a.rows : most);
-  if (v.ok) rms_norm_backward_kernel<T, W, true><<<grid, kThreads, 0, s>>>(a, d);
-  else rms_norm_backward_kernel<T, W, false><<<grid, kThreads, 0, s>>>(a, d);
-  if (a.d_dweight != nullptr)
-    dweight_kernel<<<(unsigned)((a.cols + kThreads - 1) / kThreads), kThreads, 0, s>>>(
-        static_cast<const float*>(a.d_workspace), grid, a.cols, a.d_dweight);
-  return cudaGetLastError();
+  return v.ok ? backward_vec<T, W, true>(a, d, sm_count, s) : backward_vec<T, W, false>(a, d, sm_count, s);
 }
 
 }  // namespace
