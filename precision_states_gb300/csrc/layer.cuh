@@ -98,8 +98,18 @@ __device__ __forceinline__ void store8(float* p, int valid, const float (&x)[8])
 // bits, element i + j in bits 16 j: the generator's four words as they are when
 // i is a multiple of 8 (VEC), else two calls' eight words moved down by i mod 8
 // half-words.
+// The generator's ten rounds with each product formed once, 64 bits wide.
 __device__ __forceinline__ uint4 drop_group(uint64_t g, const DropArgs& d) {
-  return philox10_rk(make_uint4((uint32_t)g, (uint32_t)(g >> 32) | 0x80000000u, d.tensor, d.step32), d.rk);
+  uint32_t x = (uint32_t)g, y = (uint32_t)(g >> 32) | 0x80000000u, z = d.tensor, w = d.step32;
+#pragma unroll
+  for (int r = 0; r < 10; ++r) {
+    const uint64_t p0 = (uint64_t)0xD2511F53u * x, p1 = (uint64_t)0xCD9E8D57u * z;
+    x = (uint32_t)(p1 >> 32) ^ y ^ d.rk[2 * r];
+    y = (uint32_t)p1;
+    z = (uint32_t)(p0 >> 32) ^ w ^ d.rk[2 * r + 1];
+    w = (uint32_t)p0;
+  }
+  return make_uint4(x, y, z, w);
 }
 template <bool VEC>
 __device__ __forceinline__ uint4 drop_draws(uint64_t i, const DropArgs& d) {
@@ -154,54 +164,65 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t top_bits) {
 __device__ __forceinline__ float inverse_scale(uint32_t byte) { return u2f((254u - byte) << 23); }
 
 __device__ __forceinline__ bool finite_bits(float x) { return (f2u(x) & 0x7F800000u) != 0x7F800000u; }
-// The larger magnitude; NaN if either is one.
-__device__ __forceinline__ float larger(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
-  return r;
-}
-__device__ __forceinline__ float largest8(const float (&x)[8]) {
-  return larger(larger(larger(x[0], x[1]), larger(x[2], x[3])), larger(larger(x[4], x[5]), larger(x[6], x[7])));
+// Magnitudes are compared as integers: their order, with infinity and NaN above
+// every finite value.
+constexpr uint32_t kInfBits = 0x7F800000u;
+__device__ __forceinline__ uint32_t magnitude(float x) { return f2u(x) & 0x7FFFFFFFu; }
+__device__ __forceinline__ uint32_t top8(const float (&x)[8]) {
+  return max(max(max(magnitude(x[0]), magnitude(x[1])), max(magnitude(x[2]), magnitude(x[3]))),
+             max(max(magnitude(x[4]), magnitude(x[5])), max(magnitude(x[6]), magnitude(x[7]))));
 }
 // The same of the finite elements.
-__device__ __forceinline__ float largest_finite8(const float (&x)[8]) {
-  float t = 0.0f;
+__device__ __forceinline__ uint32_t finite_top8(const float (&x)[8]) {
+  uint32_t t = 0;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) t = finite_bits(x[j]) ? larger(t, x[j]) : t;
+  for (int j = 0; j < 8; ++j) t = max(t, finite_bits(x[j]) ? magnitude(x[j]) : 0u);
   return t;
 }
 // Over the 16 lanes of a 128-element block.
-__device__ __forceinline__ float largest16(float t) {
+__device__ __forceinline__ uint32_t top16(uint32_t t) {
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) t = larger(t, __shfl_xor_sync(0xFFFFFFFFu, t, o));
+  for (int o = 8; o > 0; o >>= 1) t = max(t, __shfl_xor_sync(0xFFFFFFFFu, t, o));
   return t;
 }
 // The scale byte of the 1 x 128 block that 16 lanes hold eight elements each of,
 // by the whole warp; `odd`: it holds an infinity or NaN.
 __device__ __forceinline__ uint32_t block_byte(const float (&x)[8], bool& odd) {
-  float top = largest16(largest8(x));
-  odd = !finite_bits(top);
+  uint32_t top = top16(top8(x));
+  odd = top >= kInfBits;
   if (__any_sync(0xFFFFFFFFu, odd)) {
-    const float finite = largest16(largest_finite8(x));
+    const uint32_t finite = top16(finite_top8(x));
     if (odd) top = finite;
   }
-  return scale_byte(f2u(top));
+  return scale_byte(top);
 }
 
+// Two fp32 products per instruction.
+__device__ __forceinline__ void scaled8(const float (&x)[8], float f, float (&y)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) unpk(mul2(pk(x[j], x[j + 1]), pk(f, f)), y[j], y[j + 1]);
+}
+__device__ __forceinline__ void times8(float (&x)[8], const float (&f)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) unpk(mul2(pk(x[j], x[j + 1]), pk(f[j], f[j + 1])), x[j], x[j + 1]);
+}
+
+__device__ __forceinline__ uint2 codes8(const float (&v)[8]) {
+  return make_uint2(e4m3x2_rn(v[0], v[1]) | (e4m3x2_rn(v[2], v[3]) << 16),
+                    e4m3x2_rn(v[4], v[5]) | (e4m3x2_rn(v[6], v[7]) << 16));
+}
 // Codes of eight elements over 2^e (inv = 2^-e); `odd` says that the block
 // holds an infinity or NaN, which the converter would clamp or keep: both are
 // stored as NaN.
 __device__ __forceinline__ uint2 codes8(const float (&x)[8], float inv, bool odd) {
   float v[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = x[j] * inv;
+  scaled8(x, inv, v);
   if (odd) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (!finite_bits(x[j])) v[j] = u2f(0x7FC00000u);
   }
-  return make_uint2(e4m3x2_rn(v[0], v[1]) | (e4m3x2_rn(v[2], v[3]) << 16),
-                    e4m3x2_rn(v[4], v[5]) | (e4m3x2_rn(v[6], v[7]) << 16));
+  return codes8(v);
 }
 // Store of up to eight codes at an 8-byte aligned place.
 __device__ __forceinline__ void store_codes8(uint8_t* p, int valid, uint2 w) {

@@ -14,7 +14,7 @@
 // mostly empty 128.  Warp 0 fills a ring of stages (128 bytes of depth of both
 // tiles, 128-byte swizzle; every fourth stage the 512-byte scale tiles too) by
 // TMA; one thread of warp 1 copies scale tiles to tensor memory and issues the
-// products; warps 4-7 read finished accumulators and write out.  Two
+// products; warps 4-11 read finished accumulators and write out.  Two
 // accumulators alternate, so that a tile's output overlaps the next one's
 // products.  At NT 256 they share 24 columns (two of 256 and two sets of scales
 // do not fit into 512): the output reads those first, and the next tile's
@@ -32,12 +32,13 @@
 // and products in flight have ended.
 #include <cuda.h>
 
-#include "layer.cuh"
+#include "matmul.h"
 
 namespace psopt {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;
+constexpr int kOutWarps = 8;           // two for each 32 lanes of tensor memory, half of the columns each
 constexpr unsigned long long kWaitNs = 2000000000ull;
 constexpr int kScaleTile = 512;        // bytes: 128 rows x 4 blocks
 constexpr int kStageDepth = 128;
@@ -45,17 +46,12 @@ constexpr int kRingBytes = 204 * 1024;
 
 __device__ int g_flags;
 
-struct MatmulArgs {
-  void* out;
-  const void* addend;
-  int64_t out_pitch, addend_pitch;
+struct MatmulArgs : OutputArgs {
   int nx, ny;                // rows of x and of y
   int x_tiles, y_tiles;
   int blocks;                // ceil(k / 128)
   int panel;                 // scale tiles per 128 rows: ceil(blocks / 4)
   int split;                 // CTAs per cluster along the depth (CG 1)
-  int swap;                  // x is the call's b: out[y][x]
-  int vec;                   // rows of out and addend allow 16-byte accesses
 };
 
 template <int CG, int NT>
@@ -81,7 +77,7 @@ struct Layout {
   static constexpr int kBytes = kBarAt + kBars * 8 + 16 + 1024;        // 1024: alignment of the ring
   static_assert(kNeed <= 512, "tensor memory");
   static_assert(kBytes <= 227 * 1024, "shared memory");
-  static_assert(NT * 128 * 4 <= kScaleAt || CG == 2 || NT > 128, "split sums fit into the ring");
+  static_assert((NT + 4) * 128 * 4 <= kScaleAt || CG == 2, "split sums fit into the ring");
 };
 
 // ------------------------------------------------------------------ barriers
@@ -218,42 +214,77 @@ __device__ __forceinline__ void acc_load(uint32_t tmem, float (&v)[N]) {
 }
 
 // -------------------------------------------------------------------- output
-// N outputs of row `x` of the tile's operand, columns y0 .. y0 + N - 1.
-template <typename T>
-__device__ __forceinline__ void store_one(const MatmulArgs& a, int x, int y, float v) {
-  const int64_t row = a.swap ? y : x, col = a.swap ? x : y;
-  float t[8] = {v};
-  if (a.addend != nullptr) {
-    float c[8];
-    load8<false>(static_cast<const T*>(a.addend) + row * a.addend_pitch + col, 1, c);
-    t[0] += c[0];
-  }
-  store8<false>(static_cast<T*>(a.out) + row * a.out_pitch + col, 1, t);
-}
+// A thread's N outputs: row x of the tile, columns y0 .. y0 + N - 1.  The addend
+// is loaded whole, and before the accumulator is read, so that its latency is
+// paid once.  Whole rows go in 32-byte accesses (a sector each) where `vec` says
+// that they may.
 template <typename T, int N>
-__device__ __forceinline__ void store_cols(const MatmulArgs& a, int x, int y0, const float (&v)[N]) {
-  if (x >= a.nx) return;
-  if (a.vec && !a.swap && y0 + N <= a.ny) {
-    T* out = static_cast<T*>(a.out) + (int64_t)x * a.out_pitch + y0;
+struct Outputs {
+  static constexpr int kWords = N * (int)sizeof(T) / 4;
+  uint32_t add[kWords];
+  __device__ __forceinline__ bool whole(const MatmulArgs& a, int y0) const { return a.vec && !a.swap && y0 + N <= a.ny; }
+
+  __device__ __forceinline__ void load(const MatmulArgs& a, int x, int y0) {
+    if (a.addend == nullptr || x >= a.nx) return;
+    const T* p = static_cast<const T*>(a.addend);
+    if (whole(a, y0)) {
+      p += place(a, a.addend_pitch, x, y0);
 #pragma unroll
-    for (int i = 0; i < N; i += 8) {
-      float t[8];
-      if (a.addend != nullptr) {
-        load8<true>(static_cast<const T*>(a.addend) + (int64_t)x * a.addend_pitch + y0 + i, 8, t);
+      for (int i = 0; i < kWords; i += 8)
+        asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(add[i]), "=r"(add[i + 1]), "=r"(add[i + 2]), "=r"(add[i + 3]), "=r"(add[i + 4]),
+                       "=r"(add[i + 5]), "=r"(add[i + 6]), "=r"(add[i + 7])
+                     : "l"(reinterpret_cast<const uint32_t*>(p) + i));
+    } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) t[j] += v[i + j];
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) t[j] = v[i + j];
+      for (int i = 0; i < N; ++i) {
+        const float v = y0 + i < a.ny ? element(p + place(a, a.addend_pitch, x, y0 + i)) : 0.0f;
+        if (sizeof(T) == 4) add[i] = f2u(v);
+        else if (i & 1) add[i >> 1] |= f2u(v) & 0xFFFF0000u;
+        else add[i >> 1] = f2u(v) >> 16;
       }
-      store8<true>(out + i, 8, t);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (y0 + i < a.ny) store_one<T>(a, x, y0 + i, v[i]);
   }
-}
+  __device__ __forceinline__ void store(const MatmulArgs& a, int x, int y0, float (&v)[N]) const {
+    if (x >= a.nx) return;
+    T* p = static_cast<T*>(a.out);
+    if (a.addend != nullptr) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        v[i] += sizeof(T) == 4 ? u2f(add[i]) : u2f(i & 1 ? add[i >> 1] & 0xFFFF0000u : add[i >> 1] << 16);
+    }
+    if (whole(a, y0)) {
+      p += place(a, a.out_pitch, x, y0);
+      uint32_t w[kWords];
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) w[i] = sizeof(T) == 4 ? f2u(v[i]) : bf16_pair(v[2 * i], v[2 * i + 1]);
+#pragma unroll
+      for (int i = 0; i < kWords; i += 8)
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                     ::"l"(reinterpret_cast<uint32_t*>(p) + i), "r"(w[i]), "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]),
+                       "r"(w[i + 4]), "r"(w[i + 5]), "r"(w[i + 6]), "r"(w[i + 7]) : "memory");
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (y0 + i < a.ny) put(p + place(a, a.out_pitch, x, y0 + i), v[i]);
+    }
+  }
+};
+
+// A place in the ring: its stage, the phase of its barriers, and whether the ring
+// is still in its first turn.
+template <int S>
+struct Ring {
+  uint32_t stage = 0, phase = 0;
+  bool first = true;
+  __device__ __forceinline__ void next() {
+    if (++stage == S) {
+      stage = 0;
+      phase ^= 1u;
+      first = false;
+    }
+  }
+};
 
 // Tile t of the grid: panels of kGroup x tiles go through all y tiles, so that
 // the tiles in flight share operands in L2.
@@ -299,7 +330,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(done + 8 * i, 1);
-      bar_init(free_ + 8 * i, 4 * CG);
+      bar_init(free_ + 8 * i, kOutWarps * CG);
     }
     bar_init(drain, 1);
     *failed = 0;
@@ -324,74 +355,94 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
 
   if (warp == 0 && lane == 0) {
     // ------------------------------------------------------------- producer
-    // A pair's copies all count on the leader's barrier.
+    // A pair's copies all count on the leader's barrier.  One thread paces the
+    // ring here and one below, so their loops carry their state (stage, phase,
+    // addresses) from block to block and compute nothing per block.
     const uint32_t full_at = CG == 2 ? map_to(full, 0) : full;
-    int64_t n = 0;          // stage uses so far
+    constexpr uint32_t kBytes = CG * (L::kXBytes + L::kYBytes), kScales = CG * L::kScaleBytes;
+    const bool counts = CG == 1 || rank == 0;
+    Ring<S> at;
     bool ok = true;
     for (int t = first; t < tiles && ok; t += step) {
       int tx, ty;
       tile_at(a, t, tx, ty);
       const int x0 = (tx * CG + (CG == 2 ? (int)rank : 0)) * 128, y0 = ty * NT;
-      for (int kb = kb0; kb < kb1; ++kb, ++n) {
-        const int st = (int)(n % S);
-        if (n >= S && !bar_wait(empty + 8 * st, (uint32_t)(n / S - 1) & 1u)) {
-          ok = false;
-          break;
-        }
-        const bool sc = (kb & 3) == 0;
-        if (CG == 1 || rank == 0)
-          bar_expect(full + 8 * st, CG * (L::kXBytes + L::kYBytes + (sc ? L::kScaleBytes : 0)));
-        const uint32_t dst = ring + st * L::kStage, bar = full_at + 8 * st;
-        tma_2d<CG>(dst, &map_x, kb * kStageDepth, x0, bar);
-        tma_2d<CG>(dst + L::kXBytes, &map_y, kb * kStageDepth, y0 + (CG == 2 ? (int)rank * L::kY : 0), bar);
-        if (sc) {
-          const uint32_t sd = scales + st * L::kScaleBytes;
-          tma_2d<CG>(sd, &map_sx, 0, (x0 >> 7) * a.panel + (kb >> 2), bar);
+      const int y_row = y0 + (CG == 2 ? (int)rank * L::kY : 0);
+      int sx = (x0 >> 7) * a.panel + (kb0 >> 2), sy = (y0 >> 7) * a.panel + (kb0 >> 2);
+      for (int kb = kb0; kb < kb1; kb += 4, ++sx, ++sy) {
 #pragma unroll
-          for (int i = 0; i < L::kYScaleTiles; ++i)
-            tma_2d<CG>(sd + (1 + i) * kScaleTile, &map_sy, 0, ((y0 >> 7) + i) * a.panel + (kb >> 2), bar);
+        for (int j = 0; j < 4; ++j) {
+          if (kb + j >= kb1) break;
+          if (!at.first && !bar_wait(empty + 8 * at.stage, at.phase ^ 1u)) {
+            ok = false;
+            break;
+          }
+          const uint32_t bar = full_at + 8 * at.stage, dst = ring + at.stage * L::kStage;
+          if (counts) bar_expect(full + 8 * at.stage, j == 0 ? kBytes + kScales : kBytes);
+          if (j == 0) {
+            const uint32_t sd = scales + at.stage * L::kScaleBytes;
+            tma_2d<CG>(sd, &map_sx, 0, sx, bar);
+#pragma unroll
+            for (int i = 0; i < L::kYScaleTiles; ++i)
+              tma_2d<CG>(sd + (1 + i) * kScaleTile, &map_sy, 0, sy + i * a.panel, bar);
+          }
+          tma_2d<CG>(dst, &map_x, (kb + j) * kStageDepth, x0, bar);
+          tma_2d<CG>(dst + L::kXBytes, &map_y, (kb + j) * kStageDepth, y_row, bar);
+          at.next();
         }
+        if (!ok) break;
       }
     }
-    if (!ok) *failed = 1;
-    if (!ok && rank == 0)      // let what was issued land
-      for (int64_t u = n > S ? n - S : 0; u < n; ++u) bar_wait(full + 8 * (int)(u % S), (uint32_t)(u / S) & 1u);
+    if (!ok) {
+      *failed = 1;
+      if (rank == 0)           // let what was issued land: each stage's last use
+        for (int i = 0; i < S; ++i) {
+          if (at.first && i >= (int)at.stage) break;
+          bar_wait(full + 8 * i, i < (int)at.stage ? at.phase : at.phase ^ 1u);
+        }
+    }
   } else if (warp == 1 && lane == 0 && (CG == 1 || rank == 0)) {
     // ------------------------------------------------------------- products
-    int64_t n = 0;
-    int i = 0, set = 0;
+    const uint64_t x_desc = tile_desc(ring), y_desc = tile_desc(ring + L::kXBytes), s_desc = scale_desc(scales);
+    Ring<S> at;
+    int i = 0;
+    uint32_t set = 0;
     bool ok = true;
     for (int t = first; t < tiles && ok; t += step, ++i) {
-      int tx, ty;
-      tile_at(a, t, tx, ty);
       const uint32_t acc = tmem + (i & 1) * L::kAcc1;
-      const uint32_t y_col = NT < 128 ? (uint32_t)((ty * NT & 127) >> 5) : 0u;   // y's first row within its scale tile
       if (L::kOverlap ? (i >= 1 && !bar_wait(free_, (uint32_t)(i - 1) & 1u))
                       : (i >= 2 && !bar_wait(free_ + 8 * (i & 1), (uint32_t)((i >> 1) - 1) & 1u))) {
         ok = false;
         break;
       }
       fence_after();
-      for (int kb = kb0; kb < kb1; ++kb, ++n) {
-        const int st = (int)(n % S);
-        if (!bar_wait(full + 8 * st, (uint32_t)(n / S) & 1u)) {
-          ok = false;
-          break;
-        }
-        fence_after();
-        if ((kb & 3) == 0) {
-          set ^= 1;
-          const uint32_t col = tmem + L::kScaleCol + set * L::kScaleCols, sd = scales + st * L::kScaleBytes;
+      uint32_t add = 0;
+      for (int kb = kb0; kb < kb1; kb += 4) {
+        set = L::kScaleCols - set;                       // the two sets in turn
+        const uint32_t col = tmem + L::kScaleCol + set;
 #pragma unroll
-          for (int j = 0; j <= L::kYScaleTiles; ++j) copy_scales<CG>(col + 4 * j, scale_desc(sd + j * kScaleTile));
-        }
-        const uint32_t col = tmem + L::kScaleCol + set * L::kScaleCols;
-        const uint64_t dx = tile_desc(ring + st * L::kStage), dy = tile_desc(ring + st * L::kStage + L::kXBytes);
-        const uint32_t instr = instr_desc<CG, NT>((uint32_t)kb & 3u);
+        for (int j = 0; j < 4; ++j) {
+          if (kb + j >= kb1) break;
+          if (!bar_wait(full + 8 * at.stage, at.phase)) {
+            ok = false;
+            break;
+          }
+          fence_after();
+          if (j == 0) {
+            const uint64_t sd = s_desc + at.stage * (L::kScaleBytes >> 4);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          product<CG>(acc, dx + 2 * j, dy + 2 * j, instr, col, col + 4 + y_col, (kb > kb0 || j > 0) ? 1u : 0u);
-        commit<CG>(empty + 8 * st);
+            for (int k = 0; k <= L::kYScaleTiles; ++k) copy_scales<CG>(col + 4 * k, sd + k * (kScaleTile >> 4));
+          }
+          const uint64_t dx = x_desc + at.stage * (L::kStage >> 4), dy = y_desc + at.stage * (L::kStage >> 4);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            product<CG>(acc, dx + 2 * k, dy + 2 * k, instr_desc<CG, NT>(j), col, col + 4, add);
+            add = 1;
+          }
+          commit<CG>(empty + 8 * at.stage);
+          at.next();
+        }
+        if (!ok) break;
       }
       if (ok) commit<CG>(done + 8 * (i & 1));
     }
@@ -402,38 +453,64 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     }
   } else if (warp >= 4) {
     // --------------------------------------------------------------- output
-    constexpr int C = NT < 32 ? 16 : 32;       // columns at a time
-    const int q = warp - 4;                    // this warp's 32 lanes of tensor memory
+    // C columns at a time; `half` 0 takes the first NT / 2 columns (all 16 of the
+    // narrowest tile), 1 the others
+    constexpr int C = NT >= 64 ? 32 : 16, kCols = NT == 16 ? 16 : NT / 2;
+    const bool joined = CG == 1 && a.split > 1;
+    const int q = warp & 3, half = (warp - 4) >> 2;      // this warp's 32 lanes of tensor memory
+    const int chunks = NT == 16 && half == 1 ? 0 : kCols / C;
     const uint32_t free_at = CG == 2 ? map_to(free_, 0) : free_;
     int i = 0;
     for (int t = first; t < tiles; t += step, ++i) {
       int tx, ty;
       tile_at(a, t, tx, ty);
+      const int x = (tx * CG + (CG == 2 ? (int)rank : 0)) * 128 + q * 32 + lane, y0 = ty * NT;
+      // The shared columns first: the first accumulator's last ones, the second
+      // one's first.  The half that has none frees them at once: what it
+      // stands for is that it has read the tile before.
+      const bool down = L::kOverlap && (i & 1) == 0;
+      const bool shares = L::kOverlap && half == (down ? 1 : 0);
+      const auto column = [&](int j) { return half * kCols + (down ? kCols - C - j * C : j * C); };
+      if (L::kOverlap && !shares && lane == 0) bar_arrive_cluster(free_at);
+      Outputs<T, C> o[2];
+      if (!joined && chunks > 0) o[0].load(a, x, y0 + column(0));
       if (!__all_sync(0xFFFFFFFFu, bar_wait(done + 8 * (i & 1), (uint32_t)(i >> 1) & 1u))) {
         *failed = 1;
         break;
       }
       fence_after();
       const uint32_t acc = tmem + (i & 1) * L::kAcc1 + ((uint32_t)(q * 32) << 16);
-      const int x = (tx * CG + (CG == 2 ? (int)rank : 0)) * 128 + q * 32 + lane, y0 = ty * NT;
-      for (int j = 0; j < NT / C; ++j) {
-        // the shared columns first: the first accumulator's last, the second one's first
-        const int c = (L::kOverlap && (i & 1) == 0) ? NT - C - j * C : j * C;
-        if (y0 + c >= a.ny && !(L::kOverlap && j == 0) && j != NT / C - 1) continue;
+#pragma unroll
+      for (int j = 0; j < kCols / C; ++j) {
+        if (j >= chunks) break;
+        const int c = column(j);
+        if (!joined && j + 1 < chunks) o[(j + 1) & 1].load(a, x, y0 + column(j + 1));
         float v[C];
         acc_load<C>(acc + c, v);
-        if (j == (L::kOverlap ? 0 : NT / C - 1)) {
+        if (shares && j == 0) {
           fence_before();
           __syncwarp();
-          if (lane == 0) bar_arrive_cluster((L::kOverlap ? free_at : free_at + 8 * (i & 1)));
+          if (lane == 0) bar_arrive_cluster(free_at);
         }
-        if (CG == 1 && a.split > 1) {
-          float* sum = reinterpret_cast<float*>(smem);
-#pragma unroll
-          for (int k = 0; k < C; ++k) sum[(c + k) * 128 + q * 32 + lane] = v[k];
+        if (!joined) {
+          o[j & 1].store(a, x, y0 + c, v);
         } else {
-          store_cols<T, C>(a, x, y0 + c, v);
+          float* part = reinterpret_cast<float*>(smem);
+          if (a.swap) {
+#pragma unroll
+            for (int k = 0; k < C; ++k) part[(c + k) * 128 + q * 32 + lane] = v[k];
+          } else {
+#pragma unroll
+            for (int k = 0; k < C; k += 4)
+              *reinterpret_cast<float4*>(part + (q * 32 + lane) * (NT + 4) + c + k) =
+                  make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+          }
         }
+      }
+      if (!L::kOverlap) {
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive_cluster(free_at + 8 * (i & 1));
       }
     }
   }
@@ -441,20 +518,45 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
   fence_before();
   __syncthreads();
   if (CG == 1 && a.split > 1) {
-    // sums of the cluster's parts, in rank order; each CTA takes 128 / split rows of x
+    // sums of the cluster's parts, in rank order: each CTA takes 128 / split rows
+    // of x, four outputs at a time that lie together in `out`
     cluster_sync();
-    int tx, ty;
-    tile_at(a, first, tx, ty);
-    const int rows = 128 / a.split, cols = min(NT, a.ny - ty * NT);
-    for (int e = threadIdx.x; e < rows * cols; e += kThreads) {
-      const int r = (int)rank * rows + e % rows, c = e / rows;
-      float v = 0.0f;
-      for (int p = 0; p < a.split; ++p) {
-        float w;
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(w) : "r"(map_to(ring + 4 * (c * 128 + r), p)));
-        v = p == 0 ? w : v + w;
+    if (NT <= 128 && !*failed) {
+      int tx, ty;
+      tile_at(a, first, tx, ty);
+      const int rows = 128 / a.split, cols = min(NT, a.ny - ty * NT);
+      const int n = a.swap ? rows / 4 * cols : rows * ((cols + 3) / 4);
+#pragma unroll 2
+      for (int e = threadIdx.x; e < n; e += kThreads) {
+        int r, c;
+        if (a.swap) {
+          r = (int)rank * rows + 4 * (e % (rows / 4));
+          c = e / (rows / 4);
+        } else {
+          r = (int)rank * rows + e / ((cols + 3) / 4);
+          c = 4 * (e % ((cols + 3) / 4));
+        }
+        const uint32_t at = ring + 4 * (a.swap ? c * 128 + r : r * (NT + 4) + c);
+        float v[4] = {};
+#pragma unroll
+        for (int p = 0; p < 8; ++p)
+          if (p < a.split) {
+            float w[4];
+            asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                         : "=f"(w[0]), "=f"(w[1]), "=f"(w[2]), "=f"(w[3]) : "r"(map_to(at, p)));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = p == 0 ? w[j] : v[j] + w[j];
+          }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int x = tx * 128 + r + (a.swap ? j : 0), y = ty * NT + c + (a.swap ? 0 : j);
+          if (x < a.nx && y < a.ny) {
+            if (a.addend != nullptr)
+              v[j] += element(static_cast<const T*>(a.addend) + place(a, a.addend_pitch, x, y));
+            put(static_cast<T*>(a.out) + place(a, a.out_pitch, x, y), v[j]);
+          }
+        }
       }
-      if (tx * 128 + r < a.nx) store_one<T>(a, tx * 128 + r, ty * NT + c, v);
     }
   }
   if (clustered) cluster_sync();      // a pair's peer, or a reader of this CTA's part, has ended
@@ -473,7 +575,11 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads) no_depth_kernel(const __grid_constant__ MatmulArgs a) {
   const int64_t n = (int64_t)a.nx * a.ny;
   for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < n; e += (int64_t)gridDim.x * kThreads)
-    store_one<T>(a, (int)(e / a.ny), (int)(e % a.ny), 0.0f);
+  {
+    const int x = (int)(e / a.ny), y = (int)(e % a.ny);
+    put(static_cast<T*>(a.out) + place(a, a.out_pitch, x, y),
+        a.addend == nullptr ? 0.0f : element(static_cast<const T*>(a.addend) + place(a, a.addend_pitch, x, y)));
+  }
 }
 
 // ---------------------------------------------------------------------- host
@@ -552,6 +658,38 @@ cudaError_t launch(const Operand& x, const Operand& y, int64_t k, MatmulArgs a, 
   return cudaLaunchKernelEx(&cfg, matmul_kernel<T, CG, NT>, mx, my, msx, msy, a);
 }
 
+// Which operand is x, the tile (128 or, by a pair of CTAs, 256 rows of x, nt of
+// y) and the split, by the estimated time: the blocks that one CTA goes through,
+// times a block's time, plus a split's sum.
+struct Plan {
+  int swap, cg, nt, split;
+};
+constexpr double kStartNs = 2000, kTileNs = 500;
+Plan plan(int64_t m, int64_t n, int blocks, int sm_count) {
+  static const struct { int cg, nt, ns, split_ns; } kTiles[] = {
+      {1, 16, 255, 4000}, {1, 32, 255, 4000}, {1, 64, 260, 4500}, {1, 128, 265, 7500}, {2, 128, 272, 0}, {2, 256, 370, 0}};
+  Plan best = {0, 2, 256, 1};
+  double least = 1e300;
+  const int panel = (blocks + 3) / 4;
+  for (const auto& t : kTiles)
+    for (int swap = 0; swap < (t.nt < 128 ? 2 : 1); ++swap) {
+      const int64_t xr = swap ? n : m, yr = swap ? m : n;
+      // scales are addressed by whole tiles of 128 rows: a narrower tile of y only where it is the only one
+      if (t.nt < 128 && yr > t.nt) continue;
+      const int64_t tiles = ((xr + 128 * t.cg - 1) / (128 * t.cg)) * ((yr + t.nt - 1) / t.nt);
+      for (int split = 1; split <= (t.cg == 2 ? 1 : 8) && split <= panel; split *= 2) {
+        const int64_t slots = sm_count / (t.cg == 2 ? 2 : split);
+        const int64_t waves = (tiles + slots - 1) / slots;
+        const double time = (double)waves * ((blocks + split - 1) / split * t.ns + (split > 1 ? t.split_ns : kStartNs / waves + kTileNs));
+        if (time < least) {
+          least = time;
+          best = {swap, t.cg, t.nt, split};
+        }
+      }
+    }
+  return best;
+}
+
 template <typename T>
 cudaError_t dispatch(const opt_matmul_args& c, int sm_count, cudaStream_t s) {
   MatmulArgs a = {};
@@ -560,7 +698,7 @@ cudaError_t dispatch(const opt_matmul_args& c, int sm_count, cudaStream_t s) {
   a.out_pitch = c.out_pitch;
   a.addend_pitch = c.addend_pitch;
   const auto fits = [&](const void* p, int64_t pitch) {
-    return ((uintptr_t)p & 15u) == 0 && (c.m == 1 || pitch * (int64_t)sizeof(T) % 16 == 0);
+    return ((uintptr_t)p & 31u) == 0 && (c.m == 1 || pitch * (int64_t)sizeof(T) % 32 == 0);
   };
   a.vec = fits(c.d_out, c.out_pitch) && (c.d_addend == nullptr || fits(c.d_addend, c.addend_pitch));
   if (c.k == 0) {
@@ -571,24 +709,22 @@ cudaError_t dispatch(const opt_matmul_args& c, int sm_count, cudaStream_t s) {
   }
   a.blocks = (int)((c.k + 127) / 128);
   a.panel = (a.blocks + 3) / 4;
-  Operand x{c.d_a, c.d_a_scales, c.a_pitch, c.m}, y{c.d_b, c.d_b_scales, c.b_pitch, c.n};
-  const int64_t pairs = ((c.m + 255) / 256) * ((c.n + 255) / 256);
-  if (pairs >= sm_count / 4) return launch<T, 2, 256>(x, y, c.k, a, 1, sm_count, s);
-  a.swap = c.n > c.m;
-  if (a.swap) {
-    const Operand o = x;
-    x = y;
-    y = o;
+  if (c.m <= kFewRows || c.n <= kFewRows) {
+    a.swap = c.m < c.n;
+    return launch_matmul_few(c, a, s);
   }
-  const int nt = y.rows <= 16 ? 16 : y.rows <= 32 ? 32 : y.rows <= 64 ? 64 : 128;
-  const int64_t tiles = ((x.rows + 127) / 128) * ((y.rows + nt - 1) / nt);
-  int split = 1;
-  while (split < 8 && tiles * split * 2 <= sm_count && split * 2 <= a.panel) split *= 2;
-  switch (nt) {
-    case 16: return launch<T, 1, 16>(x, y, c.k, a, split, sm_count, s);
-    case 32: return launch<T, 1, 32>(x, y, c.k, a, split, sm_count, s);
-    case 64: return launch<T, 1, 64>(x, y, c.k, a, split, sm_count, s);
-    default: return launch<T, 1, 128>(x, y, c.k, a, split, sm_count, s);
+  const Operand ops[2] = {{c.d_a, c.d_a_scales, c.a_pitch, c.m}, {c.d_b, c.d_b_scales, c.b_pitch, c.n}};
+  const Plan p = plan(c.m, c.n, a.blocks, sm_count);
+  a.swap = p.swap;
+  const Operand &x = ops[p.swap], &y = ops[1 - p.swap];
+  switch (p.nt) {
+    case 16: return launch<T, 1, 16>(x, y, c.k, a, p.split, sm_count, s);
+    case 32: return launch<T, 1, 32>(x, y, c.k, a, p.split, sm_count, s);
+    case 64: return launch<T, 1, 64>(x, y, c.k, a, p.split, sm_count, s);
+    case 128:
+      return p.cg == 1 ? launch<T, 1, 128>(x, y, c.k, a, p.split, sm_count, s)
+                       : launch<T, 2, 128>(x, y, c.k, a, 1, sm_count, s);
+    default: return launch<T, 2, 256>(x, y, c.k, a, 1, sm_count, s);
   }
 }
 

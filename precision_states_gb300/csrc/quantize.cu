@@ -32,28 +32,28 @@ __device__ __forceinline__ void put_turned(uint2 (&w)[8], uint2 (*lines)[16], in
   turn4(w[4].y, w[5].y, w[6].y, w[7].y);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    lines[c + j][band ^ ((c + j) & 15)] = make_uint2(w[j].x, w[4 + j].x);
-    lines[c + 4 + j][band ^ ((c + 4 + j) & 15)] = make_uint2(w[j].y, w[4 + j].y);
+    lines[c + j][band ^ (c >> 3)] = make_uint2(w[j].x, w[4 + j].x);
+    lines[c + 4 + j][band ^ (c >> 3)] = make_uint2(w[j].y, w[4 + j].y);
   }
 }
 
 // m: this square's maxima of its eight columns -> those of the whole columns.
-__device__ __forceinline__ void column_tops(float (&m)[8], float (*part)[128], float* whole, int band, int c) {
+__device__ __forceinline__ void column_tops(uint32_t (&m)[8], uint32_t (*part)[128], uint32_t* whole, int band, int c) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) m[j] = larger(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], 16));   // the warp's two bands
+  for (int j = 0; j < 8; ++j) m[j] = max(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], 16));   // the warp's two bands
   if ((band & 1) == 0) {
-    *reinterpret_cast<float4*>(&part[band >> 1][c]) = make_float4(m[0], m[1], m[2], m[3]);
-    *reinterpret_cast<float4*>(&part[band >> 1][c + 4]) = make_float4(m[4], m[5], m[6], m[7]);
+    *reinterpret_cast<uint4*>(&part[band >> 1][c]) = make_uint4(m[0], m[1], m[2], m[3]);
+    *reinterpret_cast<uint4*>(&part[band >> 1][c + 4]) = make_uint4(m[4], m[5], m[6], m[7]);
   }
   __syncthreads();
   if (threadIdx.x < 128) {
-    float t = 0.0f;
+    uint32_t t = 0;
 #pragma unroll
-    for (int b = 0; b < 8; ++b) t = larger(t, part[b][threadIdx.x]);
+    for (int b = 0; b < 8; ++b) t = max(t, part[b][threadIdx.x]);
     whole[threadIdx.x] = t;
   }
   __syncthreads();
-  const float4 lo = *reinterpret_cast<const float4*>(whole + c), hi = *reinterpret_cast<const float4*>(whole + c + 4);
+  const uint4 lo = *reinterpret_cast<const uint4*>(whole + c), hi = *reinterpret_cast<const uint4*>(whole + c + 4);
   m[0] = lo.x; m[1] = lo.y; m[2] = lo.z; m[3] = lo.w;
   m[4] = hi.x; m[5] = hi.y; m[6] = hi.z; m[7] = hi.w;
 }
@@ -63,11 +63,11 @@ __global__ void __launch_bounds__(kThreads, 2) quantize_kernel(const __grid_cons
                                                                int64_t col_tiles) {
   // warps' maxima of columns; then the transposed codes, 16 pieces of 8 bytes per column, pieces turned by column
   __shared__ __align__(16) union {
-    float top[8][128];
+    uint32_t top[8][128];
     uint2 codes[128][16];
   } sh;
-  __shared__ __align__(16) float tops_t[128];
-  __shared__ float tops[2][kThreads / 32];
+  __shared__ __align__(16) uint32_t tops_t[128];
+  __shared__ uint32_t tops[2][kThreads / 32];
   const int64_t r0 = 128 * (blockIdx.x / col_tiles), c0 = 128 * (blockIdx.x % col_tiles);
   const int rows = (int)min(a.rows - r0, (int64_t)128), cols = (int)min(a.cols - c0, (int64_t)128);
   const int square = threadIdx.x & 15, band = threadIdx.x >> 4, c = 8 * square, l = 8 * band;
@@ -81,40 +81,40 @@ __global__ void __launch_bounds__(kThreads, 2) quantize_kernel(const __grid_cons
   }
 
   // the tile's one block
-  float top = 0.0f;
+  uint32_t top = 0;
   bool odd = false;
   if (WHOLE) {
-    float finite = 0.0f;
+    uint32_t finite = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float x[8];
       unpack(raw[i], x);
-      top = larger(top, largest8(x));
+      top = max(top, top8(x));
     }
-    if (!finite_bits(top)) {
+    if (top >= kInfBits) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         float x[8];
         unpack(raw[i], x);
-        finite = larger(finite, largest_finite8(x));
+        finite = max(finite, finite_top8(x));
       }
     } else {
       finite = top;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      top = larger(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-      finite = larger(finite, __shfl_xor_sync(0xFFFFFFFFu, finite, o));
+      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+      finite = max(finite, __shfl_xor_sync(0xFFFFFFFFu, finite, o));
     }
     if ((threadIdx.x & 31) == 0) {
       tops[0][threadIdx.x >> 5] = top;
       tops[1][threadIdx.x >> 5] = finite;
     }
     __syncthreads();
-    top = 0.0f;
+    top = 0;
     for (int w = 0; w < kThreads / 32; ++w) {
-      odd = odd || !finite_bits(tops[0][w]);
-      top = larger(top, tops[1][w]);
+      odd = odd || tops[0][w] >= kInfBits;
+      top = max(top, tops[1][w]);
     }
   }
 
@@ -122,28 +122,28 @@ __global__ void __launch_bounds__(kThreads, 2) quantize_kernel(const __grid_cons
   if (a.d_codes != nullptr || WHOLE) {
     const int64_t panel = (a.cols + 511) / 512;
     uint2 turned[8];
-    float tops8[8];
+    uint32_t tops8[8];
     if (!WHOLE) {
       // the eight rows' maxima together, so that their exchanges overlap
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         float x[8];
         unpack(raw[i], x);
-        tops8[i] = largest8(x);
+        tops8[i] = top8(x);
       }
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) tops8[i] = larger(tops8[i], __shfl_xor_sync(0xFFFFFFFFu, tops8[i], o));
+        for (int i = 0; i < 8; ++i) tops8[i] = max(tops8[i], __shfl_xor_sync(0xFFFFFFFFu, tops8[i], o));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) odd = odd || !finite_bits(tops8[i]);
+      for (int i = 0; i < 8; ++i) odd = odd || tops8[i] >= kInfBits;
       odd = __any_sync(0xFFFFFFFFu, odd);
       if (odd) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           float x[8];
           unpack(raw[i], x);
-          tops8[i] = largest16(largest_finite8(x));
+          tops8[i] = top16(finite_top8(x));
         }
       }
     }
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, 2) quantize_kernel(const __grid_cons
     for (int i = 0; i < 8; ++i) {
       float x[8];
       unpack(raw[i], x);
-      const uint32_t byte = scale_byte(f2u(WHOLE ? top : tops8[i]));
+      const uint32_t byte = scale_byte(WHOLE ? top : tops8[i]);
       const uint2 w = codes8(x, inverse_scale(byte), odd);
       if (a.d_codes != nullptr && l + i < rows) {
         if (c < cols)
@@ -171,34 +171,38 @@ __global__ void __launch_bounds__(kThreads, 2) quantize_kernel(const __grid_cons
   const int64_t panel = (a.rows + 511) / 512;
   uint8_t* scales = static_cast<uint8_t*>(a.d_scales_t);
   if (!WHOLE) {
-    float m[8] = {};
+    uint32_t m[8] = {};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float x[8];
       unpack(raw[i], x);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) m[j] = larger(m[j], x[j]);
+      for (int j = 0; j < 8; ++j) m[j] = max(m[j], magnitude(x[j]));
     }
     column_tops(m, sh.top, tops_t, band, c);
     odd = false;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) odd = odd || !finite_bits(m[j]);
+    for (int j = 0; j < 8; ++j) odd = odd || m[j] >= kInfBits;
     if (__syncthreads_or(odd)) {       // rare: the columns' finite maxima
 #pragma unroll
-      for (int j = 0; j < 8; ++j) m[j] = 0.0f;
+      for (int j = 0; j < 8; ++j) m[j] = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         float x[8];
         unpack(raw[i], x);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m[j] = finite_bits(x[j]) ? larger(m[j], x[j]) : m[j];
+        for (int j = 0; j < 8; ++j) m[j] = finite_bits(x[j]) ? max(m[j], magnitude(x[j])) : m[j];
       }
       column_tops(m, sh.top, tops_t, band, c);
       odd = true;
     }
     uint32_t byte[8];
+    float inv[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) byte[j] = scale_byte(f2u(m[j]));
+    for (int j = 0; j < 8; ++j) {
+      byte[j] = scale_byte(m[j]);
+      inv[j] = inverse_scale(byte[j]);
+    }
     if (band == 0) {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
@@ -209,13 +213,16 @@ __global__ void __launch_bounds__(kThreads, 2) quantize_kernel(const __grid_cons
     for (int i = 0; i < 8; ++i) {
       float x[8];
       unpack(raw[i], x);
+      if (odd) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = odd && !finite_bits(x[j]) ? u2f(0x7FC00000u) : x[j] * inverse_scale(byte[j]);
-      turned[i] = codes8(x, 1.0f, false);
+        for (int j = 0; j < 8; ++j) x[j] = finite_bits(x[j]) ? x[j] : u2f(0x7FC00000u);
+      }
+      times8(x, inv);
+      turned[i] = codes8(x);
     }
     put_turned(turned, sh.codes, c, band);
   } else if (threadIdx.x < cols) {
-    scales[scale_place(c0 + threadIdx.x, r0 >> 7, panel)] = (uint8_t)scale_byte(f2u(top));
+    scales[scale_place(c0 + threadIdx.x, r0 >> 7, panel)] = (uint8_t)scale_byte(top);
   }
   __syncthreads();
   // 16 lanes write a column's 128 codes
@@ -224,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 2) quantize_kernel(const __grid_cons
     const int col = 16 * i + band;
     if (col < cols && 8 * square < rows)
       store_codes8(static_cast<uint8_t*>(a.d_codes_t) + (c0 + col) * a.codes_t_pitch + r0 + 8 * square, rows - 8 * square,
-                   sh.codes[col][square ^ (col & 15)]);
+                   sh.codes[col][square ^ (col >> 3)]);
   }
 }
 

@@ -38,8 +38,8 @@ template <typename T, bool VEC>
 __device__ __forceinline__ void write_chunk(const opt_rms_norm_args& a, int64_t r, int64_t c, int valid, float rstd,
                                             int64_t panel, const float (&h)[8], const float (&w)[8]) {
   float y[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) y[j] = (h[j] * rstd) * w[j];
+  scaled8(h, rstd, y);
+  times8(y, w);
   if (valid > 0) {
     if (a.d_h != nullptr) store8<VEC>(static_cast<T*>(a.d_h) + r * a.h_pitch + c, valid, h);
     if (a.d_y != nullptr) store8<VEC>(static_cast<T*>(a.d_y) + r * a.y_pitch + c, valid, y);
@@ -57,28 +57,27 @@ __device__ __forceinline__ void write_chunk(const opt_rms_norm_args& a, int64_t 
   }
 }
 
-// Rows in registers.  `warps` per row; thread t of a row holds chunks t + k
-// 32 warps for k < NG.
-template <typename T, typename W, bool VEC, int NG, int MAX>
-__global__ void __launch_bounds__(MAX, NG == 1 ? 2 : 1) rms_norm_kernel(const __grid_constant__ opt_rms_norm_args a,
-                                                       const __grid_constant__ DropArgs d, int warps) {
+// Rows in registers: a row per warp (BY_WARP), or per CTA; thread t of a row holds
+// chunks t + k (threads of the row) for k < NG.
+template <typename T, typename W, bool VEC, bool BY_WARP, int NG, int MAX, int CTAS>
+__global__ void __launch_bounds__(MAX, CTAS) rms_norm_kernel(const __grid_constant__ opt_rms_norm_args a,
+                                                             const __grid_constant__ DropArgs d) {
   __shared__ float part[2][33];
-  const int in_row = warps == 1 ? (int)(threadIdx.x & 31) : (int)threadIdx.x;
-  const int64_t row0 = warps == 1 ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
-  const int64_t row_step = warps == 1 ? (int64_t)gridDim.x * (blockDim.x >> 5) : gridDim.x;
+  const int in_row = BY_WARP ? (int)(threadIdx.x & 31) : (int)threadIdx.x, of_row = BY_WARP ? 32 : (int)blockDim.x;
+  const int64_t row0 = BY_WARP ? (int64_t)blockIdx.x * (MAX / 32) + (threadIdx.x >> 5) : blockIdx.x;
+  const int64_t row_step = BY_WARP ? (int64_t)gridDim.x * (MAX / 32) : gridDim.x;
   const int64_t panel = (a.cols + 511) / 512;
-  const float inv_cols = 1.0f / (float)a.cols;
-  int64_t c[NG];
-  int valid[NG];
+  const int cols = (int)a.cols;
+  const float inv_cols = 1.0f / (float)cols;
+  const auto column = [&](int k) { return 8 * (in_row + k * of_row); };
+  const auto valid = [&](int k) { return VEC ? (column(k) < cols ? 8 : 0) : max(min(cols - column(k), 8), 0); };
   float w[NG][8];
   Raw<T> x[NG] = {}, res[NG] = {};
 #pragma unroll
   for (int k = 0; k < NG; ++k) {
-    c[k] = 8 * ((int64_t)in_row + k * 32 * warps);
-    valid[k] = (int)max(min(a.cols - c[k], (int64_t)8), (int64_t)0);
-    if (valid[k] > 0) {
-      if (row0 < a.rows) load_chunk<T, VEC>(a, row0, c[k], valid[k], x[k], res[k]);
-      load8<VEC>(static_cast<const W*>(a.d_weight) + c[k], valid[k], w[k]);
+    if (valid(k) > 0) {
+      if (row0 < a.rows) load_chunk<T, VEC>(a, row0, column(k), valid(k), x[k], res[k]);
+      load8<VEC>(static_cast<const W*>(a.d_weight) + column(k), valid(k), w[k]);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) w[k][j] = 0.0f;
@@ -86,20 +85,27 @@ __global__ void __launch_bounds__(MAX, NG == 1 ? 2 : 1) rms_norm_kernel(const __
   }
   int turn = 0;
   for (int64_t r = row0; r < a.rows; r += row_step, turn ^= 1) {
-    float h[NG][8], sum = 0.0f;
+    float h[NG][8];
+    f2_t sums = 0;                    // +0 in both lanes
 #pragma unroll
     for (int k = 0; k < NG; ++k) {
-      h_chunk<T, VEC>(a, d, r, c[k], x[k], res[k], h[k]);
+      h_chunk<T, VEC>(a, d, r, column(k), x[k], res[k], h[k]);
       // the next row, while this one's sum is formed
-      if (valid[k] > 0 && r + row_step < a.rows) load_chunk<T, VEC>(a, r + row_step, c[k], valid[k], x[k], res[k]);
+      if (valid(k) > 0 && r + row_step < a.rows)
+        load_chunk<T, VEC>(a, r + row_step, column(k), valid(k), x[k], res[k]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum = fmaf(h[k][j], h[k][j], sum);
+      for (int j = 0; j < 8; j += 2) {
+        const f2_t v = pk(h[k][j], h[k][j + 1]);
+        sums = fma2(v, v, sums);
+      }
     }
-    sum = cta_sum(sum, part[turn], warps);
-    const float rstd = 1.0f / sqrtf(fmaf(sum, inv_cols, a.eps));
+    float sum, second;
+    unpk(sums, sum, second);
+    sum = cta_sum(sum + second, part[turn], BY_WARP ? 1 : of_row >> 5);
+    const float rstd = rsqrtf(fmaf(sum, inv_cols, a.eps));
     if (in_row == 0 && a.d_rstd != nullptr) a.d_rstd[r] = rstd;
 #pragma unroll
-    for (int k = 0; k < NG; ++k) write_chunk<T, VEC>(a, r, c[k], valid[k], rstd, panel, h[k], w[k]);
+    for (int k = 0; k < NG; ++k) write_chunk<T, VEC>(a, r, column(k), valid(k), rstd, panel, h[k], w[k]);
   }
 }
 
@@ -121,7 +127,7 @@ __global__ void __launch_bounds__(kWideThreads) rms_norm_wide_kernel(const __gri
       for (int j = 0; j < 8; ++j) sum = fmaf(h[j], h[j], sum);
     }
     sum = cta_sum(sum, part[turn], kWideThreads / 32);
-    const float rstd = 1.0f / sqrtf(fmaf(sum, 1.0f / (float)a.cols, a.eps));
+    const float rstd = rsqrtf(fmaf(sum, 1.0f / (float)a.cols, a.eps));
     if (threadIdx.x == 0 && a.d_rstd != nullptr) a.d_rstd[r] = rstd;
     for (int64_t c0 = 0; c0 < a.cols; c0 += 8 * kWideThreads) {
       const int64_t c = c0 + 8 * threadIdx.x;
@@ -164,22 +170,21 @@ __global__ void __launch_bounds__(MAX, CTAS) rms_norm_backward_kernel(
   __shared__ float part[2][33];
   const int warps = blockDim.x >> 5;
   const float inv_cols = 1.0f / (float)a.cols;
-  int64_t c[NG];
-  int valid[NG];
+  const int cols = (int)a.cols;
+  const auto column = [&](int k) { return 8 * (int)(threadIdx.x + k * blockDim.x); };
+  const auto valid = [&](int k) { return VEC ? (column(k) < cols ? 8 : 0) : max(min(cols - column(k), 8), 0); };
   float dw[NG][8] = {};
   Raw<W> w[NG] = {};
   Raw<T> dy[NG] = {}, h[NG] = {}, in[NG] = {};
   const auto load = [&](int k, int64_t r) {
-    dy[k] = load_raw<VEC>(static_cast<const T*>(a.d_dy) + r * a.dy_pitch + c[k], valid[k]);
-    h[k] = load_raw<VEC>(static_cast<const T*>(a.d_h) + r * a.h_pitch + c[k], valid[k]);
+    dy[k] = load_raw<VEC>(static_cast<const T*>(a.d_dy) + r * a.dy_pitch + column(k), valid(k));
+    h[k] = load_raw<VEC>(static_cast<const T*>(a.d_h) + r * a.h_pitch + column(k), valid(k));
   };
 #pragma unroll
   for (int k = 0; k < NG; ++k) {
-    c[k] = 8 * ((int64_t)threadIdx.x + k * (int64_t)blockDim.x);
-    valid[k] = (int)max(min(a.cols - c[k], (int64_t)8), (int64_t)0);
-    if (valid[k] > 0) {
+    if (valid(k) > 0) {
       load(k, blockIdx.x);
-      w[k] = load_raw<VEC>(static_cast<const W*>(a.d_weight) + c[k], valid[k]);
+      w[k] = load_raw<VEC>(static_cast<const W*>(a.d_weight) + column(k), valid(k));
     }
   }
   int turn = 0;
@@ -192,9 +197,9 @@ __global__ void __launch_bounds__(MAX, CTAS) rms_norm_backward_kernel(
       unpack(dy[k], g[k]);
       unpack(h[k], hv[k]);
       unpack(w[k], wv);
-      if (a.d_dh_in != nullptr && valid[k] > 0)
-        in[k] = load_raw<VEC>(static_cast<const T*>(a.d_dh_in) + r * a.dh_in_pitch + c[k], valid[k]);
-      if (valid[k] > 0 && r + gridDim.x < a.rows) load(k, r + gridDim.x);
+      if (a.d_dh_in != nullptr && valid(k) > 0)
+        in[k] = load_raw<VEC>(static_cast<const T*>(a.d_dh_in) + r * a.dh_in_pitch + column(k), valid(k));
+      if (valid(k) > 0 && r + gridDim.x < a.rows) load(k, r + gridDim.x);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         dw[k][j] = fmaf(g[k][j], hv[k][j] * rstd, dw[k][j]);
@@ -206,24 +211,24 @@ __global__ void __launch_bounds__(MAX, CTAS) rms_norm_backward_kernel(
     const float scale = rstd * rstd * (sum * inv_cols);
 #pragma unroll
     for (int k = 0; k < NG; ++k)
-      if (valid[k] > 0) {
+      if (valid(k) > 0) {
         float add[8];
         unpack(in[k], add);
-        write_gradients<T, VEC>(a, d, r, c[k], valid[k], rstd, scale, g[k], hv[k], add);
+        write_gradients<T, VEC>(a, d, r, column(k), valid(k), rstd, scale, g[k], hv[k], add);
       }
   }
   if (a.d_dweight != nullptr) {
     float* out = dweight_row(a, blockIdx.x);
 #pragma unroll
     for (int k = 0; k < NG; ++k)
-      if (valid[k] > 0) {
-        if (valid[k] == 8) {
-          *reinterpret_cast<float4*>(out + c[k]) = make_float4(dw[k][0], dw[k][1], dw[k][2], dw[k][3]);
-          *reinterpret_cast<float4*>(out + c[k] + 4) = make_float4(dw[k][4], dw[k][5], dw[k][6], dw[k][7]);
+      if (valid(k) > 0) {
+        if (valid(k) == 8) {
+          *reinterpret_cast<float4*>(out + column(k)) = make_float4(dw[k][0], dw[k][1], dw[k][2], dw[k][3]);
+          *reinterpret_cast<float4*>(out + column(k) + 4) = make_float4(dw[k][4], dw[k][5], dw[k][6], dw[k][7]);
         } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if (j < valid[k]) out[c[k] + j] = dw[k][j];
+            if (j < valid(k)) out[column(k) + j] = dw[k][j];
         }
       }
   }
@@ -299,22 +304,25 @@ struct VecRule {
   }
 };
 
-template <typename T, typename W, bool VEC, int NG, int MAX>
-cudaError_t forward_rows(const opt_rms_norm_args& a, const DropArgs& d, int sm_count, int warps, cudaStream_t s) {
-  const int threads = warps == 1 ? 256 : 32 * warps;
+template <typename T, typename W, bool VEC, bool BY_WARP, int NG, int MAX, int CTAS>
+cudaError_t forward_rows(const opt_rms_norm_args& a, const DropArgs& d, int sm_count, int threads, cudaStream_t s) {
   static OccupancyCache cache[33];
-  const int64_t rows_per_cta = warps == 1 ? 8 : 1, need = (a.rows + rows_per_cta - 1) / rows_per_cta;
-  const int64_t most = (int64_t)sm_count * cached_occupancy(rms_norm_kernel<T, W, VEC, NG, MAX>, cache[warps], threads, 0);
-  rms_norm_kernel<T, W, VEC, NG, MAX><<<(unsigned)(need < most ? need : most), threads, 0, s>>>(a, d, warps);
+  const auto kernel = rms_norm_kernel<T, W, VEC, BY_WARP, NG, MAX, CTAS>;
+  const int64_t rows_per_cta = BY_WARP ? MAX / 32 : 1, need = (a.rows + rows_per_cta - 1) / rows_per_cta;
+  const int64_t most = (int64_t)sm_count * cached_occupancy(kernel, cache[threads / 32], threads, 0);
+  kernel<<<(unsigned)(need < most ? need : most), threads, 0, s>>>(a, d);
   return cudaGetLastError();
 }
 
 template <typename T, typename W, bool VEC>
 cudaError_t forward_vec(const opt_rms_norm_args& a, const DropArgs& d, int sm_count, cudaStream_t s) {
   const int64_t chunks = (a.cols + 7) / 8;
-  if (chunks <= 512) return forward_rows<T, W, VEC, 1, 512>(a, d, sm_count, (int)((chunks + 31) / 32), s);
-  if (chunks <= 1024) return forward_rows<T, W, VEC, 2, 512>(a, d, sm_count, (int)((chunks + 63) / 64), s);
-  if (chunks <= 2048) return forward_rows<T, W, VEC, 4, 512>(a, d, sm_count, (int)((chunks + 127) / 128), s);
+  const int threads = (int)((chunks + 31) / 32) * 32;
+  if (chunks <= 32) return forward_rows<T, W, VEC, true, 1, 256, 3>(a, d, sm_count, 256, s);
+  if (chunks <= 256) return forward_rows<T, W, VEC, false, 1, 256, 4>(a, d, sm_count, threads, s);
+  if (chunks <= 512) return forward_rows<T, W, VEC, false, 2, 256, 3>(a, d, sm_count, (int)((chunks + 63) / 64) * 32, s);
+  if (chunks <= 1024) return forward_rows<T, W, VEC, false, 2, 512, 1>(a, d, sm_count, (int)((chunks + 63) / 64) * 32, s);
+  if (chunks <= 2048) return forward_rows<T, W, VEC, false, 4, 512, 1>(a, d, sm_count, (int)((chunks + 127) / 128) * 32, s);
   const int64_t most = (int64_t)sm_count * 4;
   rms_norm_wide_kernel<T, W, VEC><<<(unsigned)(a.rows < most ? a.rows : most), kWideThreads, 0, s>>>(a, d);
   return cudaGetLastError();
@@ -347,7 +355,7 @@ cudaError_t backward_vec(const opt_rms_norm_backward_args& a, const DropArgs& d,
   const int64_t chunks = (a.cols + 7) / 8;
   int grid;
   if (chunks <= 512) {
-    grid = backward_rows<T, W, VEC, 1, 512, 2>(a, d, sm_count, (int)((chunks + 31) / 32) * 32, s);
+    grid = backward_rows<T, W, VEC, 1, 512, VEC && sizeof(T) == 2 ? 2 : 1>(a, d, sm_count, (int)((chunks + 31) / 32) * 32, s);
   } else if (chunks <= 1024) {
     grid = backward_rows<T, W, VEC, 2, 512, 1>(a, d, sm_count, (int)((chunks + 63) / 64) * 32, s);
   } else {

@@ -82,30 +82,47 @@ _pack_rms_norm_backward = packer(opt_rms_norm_backward_args)
 _pack_quantize = packer(opt_quantize_args)
 _pack_matmul = packer(opt_matmul_args)
 
-from . import (OPT_BF16, OPT_EUNSUPPORTED, OPT_F32, OptError, _check, _stream_ptr, lib)  # noqa: E402
-
-_DT = {}          # torch dtype -> OPT_F32 / OPT_BF16, filled at the first use of torch
-_FLAT = None      # torch's 8-bit storage dtypes
+from . import OPT_BF16, OPT_EUNSUPPORTED, OPT_F32, OptError, _check, _stream_ptr, lib  # noqa: E402
 
 
-def _dtype(t, what):
-    global _FLAT
-    if not _DT:
+class _Ready:
+    """What every call needs, resolved at the first one: the library's functions,
+    torch's dtypes and its current device and stream (by their raw forms: a call
+    of a small operator takes the GPU two microseconds)."""
+
+    def __init__(self):
         import torch
-        _FLAT = (torch.uint8, torch.float8_e4m3fn, torch.float8_e8m0fnu)
-        _DT.update({torch.float32: OPT_F32, torch.bfloat16: OPT_BF16})
-    got = _DT.get(t.dtype)
-    if got is None:
-        raise OptError(OPT_EUNSUPPORTED, f"{what}: dtype {t.dtype}")
-    return got
+        L = lib()
+        self.dtypes = {torch.float32: OPT_F32, torch.bfloat16: OPT_BF16}
+        self.bytes8 = (torch.uint8, torch.float8_e4m3fn, torch.float8_e8m0fnu)
+        self.f32 = torch.float32
+        self.device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        self.stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+        self.dropout, self.rms_norm, self.rms_norm_backward = L.opt_dropout, L.opt_rms_norm, L.opt_rms_norm_backward
+        self.quantize, self.matmul = L.opt_quantize, L.opt_matmul
 
 
-def _device(t, what):
+_ready = None
+
+
+def _get_ready():
+    global _ready
+    if _ready is None:
+        _ready = _Ready()
+    return _ready
+
+
+def _refuse_dtype(t, what):
+    raise OptError(OPT_EUNSUPPORTED, f"{what}: dtype {t.dtype}")
+
+
+def _device(t, what, ready):
     """The tensor's device index, which must be the current one."""
-    import torch
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    dev = t.get_device()
+    if dev < 0 or dev != ready.device():
         raise ValueError(f"{what} must be a CUDA tensor on the current device")
-    return t.get_device()
+    return dev
 
 
 def _matrix(t, what):
@@ -127,9 +144,7 @@ def _matrix(t, what):
 
 
 def _like(t, what, rows, cols, dtype, device):
-    """(pointer, pitch) of a matrix of the given shape and dtype; (0, 0) for None."""
-    if t is None:
-        return 0, 0
+    """(pointer, pitch) of a matrix of the given shape and dtype."""
     if t.dtype != dtype or t.get_device() != device:
         raise ValueError(f"{what}: expected {dtype} on cuda:{device}")
     r, c, pitch = _matrix(t, what)
@@ -138,27 +153,23 @@ def _like(t, what, rows, cols, dtype, device):
     return t.data_ptr(), pitch
 
 
-def _vector(t, what, n, device, dtype=None):
-    if t is None:
-        return 0
-    if t.get_device() != device or t.numel() != n or not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{what}: expected {n} contiguous elements" + (f" of {dtype}" if dtype else "") +
-                         f" on cuda:{device}")
+def _vector(t, what, n, device, dtype):
+    """The pointer of n contiguous elements."""
+    if t.dtype != dtype or t.numel() != n or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{what}: expected {n} contiguous elements of {dtype} on cuda:{device}")
     return t.data_ptr()
 
 
-def _held(codes, scales, what, rows, cols, device):
-    """(codes pointer, scales pointer, pitch) of an 8-bit operand; zeros for None."""
-    if codes is None and scales is None:
-        return 0, 0, 0
+def _held(codes, scales, what, rows, cols, device, ready):
+    """(codes pointer, scales pointer, pitch) of an 8-bit operand."""
     if codes is None or scales is None:
         raise ValueError(f"{what}: codes and scales go together")
-    if codes.dtype not in _FLAT or scales.dtype not in _FLAT or codes.get_device() != device:
+    if codes.dtype not in ready.bytes8 or scales.dtype not in ready.bytes8 or codes.get_device() != device:
         raise ValueError(f"{what}: expected 8-bit codes and scales on cuda:{device}")
     r, c, pitch = _matrix(codes, what)
     if r != rows or c != cols:
         raise ValueError(f"{what}: expected codes of {rows} x {cols}, got {tuple(codes.shape)}")
-    return codes.data_ptr(), _vector(scales, what + " scales", scales_bytes(rows, cols), device), pitch
+    return codes.data_ptr(), _vector(scales, what, -(-rows // 128) * -(-cols // 512) * 512, device, scales.dtype), pitch
 
 
 def scales_bytes(rows: int, cols: int) -> int:
@@ -181,12 +192,19 @@ def opt_scales_bytes(rows: int, cols: int) -> int:
 def opt_dropout(x, y, p: float, seed=0, tensor_index=0, step=0, residual=None, stream=None):
     """y = residual + dropout(x); y may be x or residual.  The backward pass is
     the same call on the gradient (same p, seed, tensor_index and step)."""
-    dt, dev = _dtype(x, "x"), _device(x, "x")
+    ready = _ready or _get_ready()
+    dtype = x.dtype
+    dt = ready.dtypes.get(dtype)
+    if dt is None:
+        _refuse_dtype(x, "x")
+    dev = _device(x, "x", ready)
     rows, cols, xp = _matrix(x, "x")
-    yq, yp = _like(y, "y", rows, cols, x.dtype, dev)
-    rq, rp = _like(residual, "residual", rows, cols, x.dtype, dev)
-    _check(lib().opt_dropout(_pack_dropout(x.data_ptr(), rq, yq, xp, rp, yp, rows, cols, p, seed, step,
-                                           tensor_index, dt), _stream_ptr(stream)), "opt_dropout")
+    yq, yp = _like(y, "y", rows, cols, dtype, dev)
+    rq, rp = (0, 0) if residual is None else _like(residual, "residual", rows, cols, dtype, dev)
+    st = ready.dropout(_pack_dropout(x.data_ptr(), rq, yq, xp, rp, yp, rows, cols, p, seed, step, tensor_index, dt),
+                       ready.stream(dev) if stream is None else _stream_ptr(stream))
+    if st:
+        _check(st, "opt_dropout")
 
 
 def opt_rms_norm(x, weight, eps=1e-5, y=None, rstd=None, residual=None, h=None, codes=None, scales=None, p=0.0,
@@ -194,22 +212,25 @@ def opt_rms_norm(x, weight, eps=1e-5, y=None, rstd=None, residual=None, h=None, 
     """h = residual + dropout(x), rstd = 1 / sqrt(mean(h^2) + eps) and
     y = h rstd weight, into whichever of h, rstd, y and codes with scales (y as
     E4M3, a scale for each 1 x 128) are given."""
-    dt, dev = _dtype(x, "x"), _device(x, "x")
+    ready = _ready or _get_ready()
+    dtype, wtype = x.dtype, weight.dtype
+    dt, wt = ready.dtypes.get(dtype), ready.dtypes.get(wtype)
+    if dt is None or wt is None:
+        _refuse_dtype(x if dt is None else weight, "x" if dt is None else "weight")
+    dev = _device(x, "x", ready)
     rows, cols, xp = _matrix(x, "x")
-    rq, rp = _like(residual, "residual", rows, cols, x.dtype, dev)
-    hq, hp = _like(h, "h", rows, cols, x.dtype, dev)
-    yq, yp = _like(y, "y", rows, cols, x.dtype, dev)
-    cq, sq, cp = _held(codes, scales, "codes", rows, cols, dev)
-    _check(lib().opt_rms_norm(
-        _pack_rms_norm(x.data_ptr(), rq, _vector(weight, "weight", cols, dev), hq, yq,
-                       _vector(rstd, "rstd", rows, dev, _torch_f32()), cq, sq, xp, rp, hp, yp, cp, rows, cols, p,
-                       seed, step, tensor_index, dt, _dtype(weight, "weight"), eps), _stream_ptr(stream)),
-        "opt_rms_norm")
-
-
-def _torch_f32():
-    import torch
-    return torch.float32
+    wq = _vector(weight, "weight", cols, dev, wtype)
+    rq, rp = (0, 0) if residual is None else _like(residual, "residual", rows, cols, dtype, dev)
+    hq, hp = (0, 0) if h is None else _like(h, "h", rows, cols, dtype, dev)
+    yq, yp = (0, 0) if y is None else _like(y, "y", rows, cols, dtype, dev)
+    sq = 0 if rstd is None else _vector(rstd, "rstd", rows, dev, ready.f32)
+    cq, eq, cp = ((0, 0, 0) if codes is None and scales is None
+                  else _held(codes, scales, "codes", rows, cols, dev, ready))
+    st = ready.rms_norm(_pack_rms_norm(x.data_ptr(), rq, wq, hq, yq, sq, cq, eq, xp, rp, hp, yp, cp, rows, cols, p, seed,
+                                       step, tensor_index, dt, wt, eps),
+                        ready.stream(dev) if stream is None else _stream_ptr(stream))
+    if st:
+        _check(st, "opt_rms_norm")
 
 
 def opt_rms_norm_backward(dy, h, weight, rstd, dh, dh_in=None, dx=None, dweight=None, p=0.0, seed=0, tensor_index=0,
@@ -219,27 +240,34 @@ def opt_rms_norm_backward(dy, h, weight, rstd, dh, dh_in=None, dx=None, dweight=
     (fp32).  workspace: a uint8 tensor of opt_rms_norm_backward_workspace(rows,
     cols) bytes for dweight; without one the call takes it from torch's
     allocator."""
-    dt, dev = _dtype(h, "h"), _device(h, "h")
+    ready = _ready or _get_ready()
+    dtype, wtype = h.dtype, weight.dtype
+    dt, wt = ready.dtypes.get(dtype), ready.dtypes.get(wtype)
+    if dt is None or wt is None:
+        _refuse_dtype(h if dt is None else weight, "h" if dt is None else "weight")
+    dev = _device(h, "h", ready)
     rows, cols, hp = _matrix(h, "h")
-    gq, gp = _like(dy, "dy", rows, cols, h.dtype, dev)
-    iq, ip = _like(dh_in, "dh_in", rows, cols, h.dtype, dev)
-    oq, op = _like(dh, "dh", rows, cols, h.dtype, dev)
-    xq, xp = _like(dx, "dx", rows, cols, h.dtype, dev)
-    f32 = _torch_f32()
-    sp = _stream_ptr(stream)
-    need = 0
+    wq = _vector(weight, "weight", cols, dev, wtype)
+    gq, gp = _like(dy, "dy", rows, cols, dtype, dev)
+    iq, ip = (0, 0) if dh_in is None else _like(dh_in, "dh_in", rows, cols, dtype, dev)
+    oq, op = _like(dh, "dh", rows, cols, dtype, dev)
+    xq, xp = (0, 0) if dx is None else _like(dx, "dx", rows, cols, dtype, dev)
+    sq = _vector(rstd, "rstd", rows, dev, ready.f32)
+    dq = nq = need = 0
     if dweight is not None:
-        need = lib().opt_rms_norm_backward_workspace(rows, cols)
+        dq = _vector(dweight, "dweight", cols, dev, ready.f32)
         if workspace is None:
+            need = opt_rms_norm_backward_workspace(rows, cols)
             workspace = _workspace(need, dev, stream)
         else:
             need = workspace.numel() * workspace.element_size()
-    _check(lib().opt_rms_norm_backward(
-        _pack_rms_norm_backward(gq, h.data_ptr(), _vector(weight, "weight", cols, dev),
-                                _vector(rstd, "rstd", rows, dev, f32), iq, oq, xq,
-                                _vector(dweight, "dweight", cols, dev, f32),
-                                workspace.data_ptr() if need else 0, gp, hp, ip, op, xp, need, rows, cols, p, seed,
-                                step, tensor_index, dt, _dtype(weight, "weight"), 0), sp), "opt_rms_norm_backward")
+        nq = workspace.data_ptr()
+    st = ready.rms_norm_backward(
+        _pack_rms_norm_backward(gq, h.data_ptr(), wq, sq, iq, oq, xq, dq, nq, gp, hp, ip, op, xp, need, rows, cols, p,
+                                seed, step, tensor_index, dt, wt, 0),
+        ready.stream(dev) if stream is None else _stream_ptr(stream))
+    if st:
+        _check(st, "opt_rms_norm_backward")
 
 
 def _workspace(nbytes, device, stream):
@@ -259,25 +287,40 @@ def opt_quantize(x, codes=None, scales=None, codes_t=None, scales_t=None, block_
     """x to E4M3 codes with a scale for each block of block_rows (1 or 128) x 128:
     as it is (codes, scales) and/or transposed (codes_t of cols x rows,
     scales_t)."""
-    dt, dev = _dtype(x, "x"), _device(x, "x")
+    ready = _ready or _get_ready()
+    dt = ready.dtypes.get(x.dtype)
+    if dt is None:
+        _refuse_dtype(x, "x")
+    dev = _device(x, "x", ready)
     rows, cols, xp = _matrix(x, "x")
-    cq, sq, cp = _held(codes, scales, "codes", rows, cols, dev)
-    tq, uq, tp = _held(codes_t, scales_t, "codes_t", cols, rows, dev)
-    _check(lib().opt_quantize(_pack_quantize(x.data_ptr(), cq, sq, tq, uq, xp, cp, tp, rows, cols, dt, block_rows),
-                              _stream_ptr(stream)), "opt_quantize")
+    cq, sq, cp = ((0, 0, 0) if codes is None and scales is None
+                  else _held(codes, scales, "codes", rows, cols, dev, ready))
+    tq, uq, tp = ((0, 0, 0) if codes_t is None and scales_t is None
+                  else _held(codes_t, scales_t, "codes_t", cols, rows, dev, ready))
+    st = ready.quantize(_pack_quantize(x.data_ptr(), cq, sq, tq, uq, xp, cp, tp, rows, cols, dt, block_rows),
+                        ready.stream(dev) if stream is None else _stream_ptr(stream))
+    if st:
+        _check(st, "opt_quantize")
 
 
 def opt_matmul(a, a_scales, b, b_scales, out, addend=None, stream=None):
     """out = a b^T (+ addend): a of m x k and b of n x k codes with their scales,
     out and addend float32 or bfloat16 of m x n; addend may be out."""
-    dt, dev = _dtype(out, "out"), _device(out, "out")
+    ready = _ready or _get_ready()
+    dtype = out.dtype
+    dt = ready.dtypes.get(dtype)
+    if dt is None:
+        _refuse_dtype(out, "out")
+    dev = _device(out, "out", ready)
     m, n, op = _matrix(out, "out")
     k = a.shape[-1]
-    aq, asq, ap = _held(a, a_scales, "a", m, k, dev)
-    bq, bsq, bp = _held(b, b_scales, "b", n, k, dev)
-    dq, dp = _like(addend, "addend", m, n, out.dtype, dev)
-    _check(lib().opt_matmul(_pack_matmul(aq, asq, bq, bsq, dq, out.data_ptr(), ap, bp, dp, op, m, n, k, dt, 0),
-                            _stream_ptr(stream)), "opt_matmul")
+    aq, asq, ap = _held(a, a_scales, "a", m, k, dev, ready)
+    bq, bsq, bp = _held(b, b_scales, "b", n, k, dev, ready)
+    dq, dp = (0, 0) if addend is None else _like(addend, "addend", m, n, dtype, dev)
+    st = ready.matmul(_pack_matmul(aq, asq, bq, bsq, dq, out.data_ptr(), ap, bp, dp, op, m, n, k, dt, 0),
+                      ready.stream(dev) if stream is None else _stream_ptr(stream))
+    if st:
+        _check(st, "opt_matmul")
 
 
 def opt_layer_status(stream=None) -> int:

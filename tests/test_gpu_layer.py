@@ -370,9 +370,9 @@ def test_matmul_in_place_sum_depth_zero_and_nan():
     assert torch.isnan(out[3]).all() and torch.isfinite(out[:3]).all() and torch.isfinite(out[4:]).all()
 
 
-def test_matmul_scales_far_apart():
-    """Row scales from 2^-100 to 2^100 on one side, their inverses on the other."""
-    m = n = 150
+@pytest.mark.parametrize("m,n", [(150, 150), (150, 5), (60, 150)])
+def test_matmul_scales_far_apart(m, n):
+    """Row scales from 2^-100 to 2^100 on one side, 2^20 on the other."""
     k = 256
     ia = torch.randint(1, 4, (m, k), generator=torch.Generator().manual_seed(1)).float()
     ib = torch.randint(1, 4, (n, k), generator=torch.Generator().manual_seed(2)).float()
