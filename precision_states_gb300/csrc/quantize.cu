@@ -37,31 +37,109 @@ __device__ __forceinline__ void put_turned(uint2 (&w)[8], uint2 (*lines)[16], in
   }
 }
 
-// m: this square's maxima of its eight columns -> those of the whole columns.
-__device__ __forceinline__ void column_tops(uint32_t (&m)[8], uint32_t (*part)[128], uint32_t* whole, int band, int c) {
+// Magnitudes of a chunk as they lie in its words (two BF16, or one fp32, each),
+// compared as integers; infinity and NaN are above every finite value.
+template <typename T>
+struct Magnitudes {
+  static constexpr int kWords = Raw<T>::kWords;
+  uint32_t w[kWords];
+};
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b, Bf16) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b, float) { return max(a, b); }
+__device__ __forceinline__ uint32_t word_magnitude(uint32_t w, Bf16) { return w & 0x7FFF7FFFu; }
+__device__ __forceinline__ uint32_t word_magnitude(uint32_t w, float) { return w & 0x7FFFFFFFu; }
+// The same with the elements that are not finite as 0.
+__device__ __forceinline__ uint32_t finite_magnitude(uint32_t w, Bf16) {
+  const uint32_t lo = w & 0x7FFFu, hi = w & 0x7FFF0000u;
+  return (lo < 0x7F80u ? lo : 0u) | (hi < kInfBits ? hi : 0u);
+}
+__device__ __forceinline__ uint32_t finite_magnitude(uint32_t w, float) {
+  return (w & 0x7FFFFFFFu) < kInfBits ? w & 0x7FFFFFFFu : 0u;
+}
+// Of a chunk; as fp32 bits.
+template <typename T>
+__device__ __forceinline__ Magnitudes<T> magnitudes(const Raw<T>& r, bool finite) {
+  Magnitudes<T> m;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) m[j] = max(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], 16));   // the warp's two bands
+  for (int k = 0; k < Raw<T>::kWords; ++k) m.w[k] = finite ? finite_magnitude(r.w[k], T()) : word_magnitude(r.w[k], T());
+  return m;
+}
+__device__ __forceinline__ uint32_t top_of(const Magnitudes<Bf16>& m) {
+  const uint32_t t = larger(larger(m.w[0], m.w[1], Bf16()), larger(m.w[2], m.w[3], Bf16()), Bf16());
+  return max(t << 16, t & 0xFFFF0000u);
+}
+__device__ __forceinline__ uint32_t top_of(const Magnitudes<float>& m) {
+  return max(max(max(m.w[0], m.w[1]), max(m.w[2], m.w[3])), max(max(m.w[4], m.w[5]), max(m.w[6], m.w[7])));
+}
+__device__ __forceinline__ void expand(const Magnitudes<Bf16>& m, uint32_t (&x)[8]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    x[2 * k] = m.w[k] << 16;
+    x[2 * k + 1] = m.w[k] & 0xFFFF0000u;
+  }
+}
+__device__ __forceinline__ void expand(const Magnitudes<float>& m, uint32_t (&x)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) x[k] = m.w[k];
+}
+
+// A square's magnitudes by column (its eight rows' largest) -> those of the
+// tile's whole columns, by way of shared memory.
+template <typename T>
+__device__ __forceinline__ void column_tops(const Raw<T> (&raw)[8], bool finite, uint32_t (*part)[128], uint32_t* whole,
+                                            uint32_t (&top)[8]) {
+  constexpr int W = Magnitudes<T>::kWords;
+  const int square = threadIdx.x & 15, band = threadIdx.x >> 4;
+  Magnitudes<T> m = magnitudes(raw[0], finite);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) {
+    const Magnitudes<T> n = magnitudes(raw[i], finite);
+#pragma unroll
+    for (int k = 0; k < W; ++k) m.w[k] = larger(m.w[k], n.w[k], T());
+  }
+#pragma unroll
+  for (int k = 0; k < W; ++k) m.w[k] = larger(m.w[k], __shfl_xor_sync(0xFFFFFFFFu, m.w[k], 16), T());   // the warp's two bands
   if ((band & 1) == 0) {
-    *reinterpret_cast<uint4*>(&part[band >> 1][c]) = make_uint4(m[0], m[1], m[2], m[3]);
-    *reinterpret_cast<uint4*>(&part[band >> 1][c + 4]) = make_uint4(m[4], m[5], m[6], m[7]);
+#pragma unroll
+    for (int k = 0; k < W; k += 4)
+      *reinterpret_cast<uint4*>(&part[band >> 1][W * square + k]) = make_uint4(m.w[k], m.w[k + 1], m.w[k + 2], m.w[k + 3]);
   }
   __syncthreads();
-  if (threadIdx.x < 128) {
-    uint32_t t = 0;
+  if (threadIdx.x < 16 * W) {
+    uint32_t t = part[0][threadIdx.x];
 #pragma unroll
-    for (int b = 0; b < 8; ++b) t = max(t, part[b][threadIdx.x]);
+    for (int b = 1; b < 8; ++b) t = larger(t, part[b][threadIdx.x], T());
     whole[threadIdx.x] = t;
   }
   __syncthreads();
-  const uint4 lo = *reinterpret_cast<const uint4*>(whole + c), hi = *reinterpret_cast<const uint4*>(whole + c + 4);
-  m[0] = lo.x; m[1] = lo.y; m[2] = lo.z; m[3] = lo.w;
-  m[4] = hi.x; m[5] = hi.y; m[6] = hi.z; m[7] = hi.w;
+#pragma unroll
+  for (int k = 0; k < W; k += 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(whole + W * square + k);
+    m.w[k] = v.x; m.w[k + 1] = v.y; m.w[k + 2] = v.z; m.w[k + 3] = v.w;
+  }
+  expand(m, top);
+}
+
+// Scale bytes of eight lines (rows or columns) that every lane of a square group
+// holds: lane i of the first eight stores that of line i.
+__device__ __forceinline__ void store_bytes(uint8_t* scales, const uint32_t (&byte)[8], int i, int64_t line0, int lines,
+                                            int64_t block, int64_t panel) {
+  if (i >= 8 || i >= lines) return;
+  uint32_t v = byte[0];
+#pragma unroll
+  for (int k = 1; k < 8; ++k) v = i == k ? byte[k] : v;
+  scales[scale_place(line0 + i, block, panel)] = (uint8_t)v;
 }
 
 template <typename T, bool VEC, bool WHOLE>
-__global__ void __launch_bounds__(kThreads, 2) quantize_kernel(const __grid_constant__ opt_quantize_args a,
-                                                               int64_t col_tiles) {
-  // warps' maxima of columns; then the transposed codes, 16 pieces of 8 bytes per column, pieces turned by column
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && VEC ? 3 : 2)
+quantize_kernel(const __grid_constant__ opt_quantize_args a, int64_t col_tiles) {
+  // warps' maxima of columns; then the transposed codes, 16 pieces of 8 bytes per
+  // column, pieces turned by column
   __shared__ __align__(16) union {
     uint32_t top[8][128];
     uint2 codes[128][16];
@@ -73,45 +151,36 @@ __global__ void __launch_bounds__(kThreads, 2) quantize_kernel(const __grid_cons
   const int square = threadIdx.x & 15, band = threadIdx.x >> 4, c = 8 * square, l = 8 * band;
 
   Raw<T> raw[8];
+  {
+    const T* p = static_cast<const T*>(a.d_x) + (r0 + l) * a.x_pitch + c0 + c;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    raw[i] = Raw<T>{};
-    if (l + i < rows && c < cols)
-      raw[i] = load_raw<VEC>(static_cast<const T*>(a.d_x) + (r0 + l + i) * a.x_pitch + c0 + c, min(cols - c, 8));
+    for (int i = 0; i < 8; ++i, p += a.x_pitch) {
+      raw[i] = Raw<T>{};
+      if (l + i < rows && c < cols) raw[i] = load_raw<VEC>(p, min(cols - c, 8));
+    }
   }
 
   // the tile's one block
   uint32_t top = 0;
   bool odd = false;
   if (WHOLE) {
-    uint32_t finite = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float x[8];
-      unpack(raw[i], x);
-      top = max(top, top8(x));
-    }
+    for (int i = 0; i < 8; ++i) top = max(top, top_of(magnitudes(raw[i], false)));
+    uint32_t finite = top;
     if (top >= kInfBits) {
+      finite = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float x[8];
-        unpack(raw[i], x);
-        finite = max(finite, finite_top8(x));
-      }
-    } else {
-      finite = top;
+      for (int i = 0; i < 8; ++i) finite = max(finite, top_of(magnitudes(raw[i], true)));
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-      finite = max(finite, __shfl_xor_sync(0xFFFFFFFFu, finite, o));
-    }
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    finite = __reduce_max_sync(0xFFFFFFFFu, finite);
     if ((threadIdx.x & 31) == 0) {
       tops[0][threadIdx.x >> 5] = top;
       tops[1][threadIdx.x >> 5] = finite;
     }
     __syncthreads();
     top = 0;
+#pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
       odd = odd || tops[0][w] >= kInfBits;
       top = max(top, tops[1][w]);
@@ -120,94 +189,58 @@ __global__ void __launch_bounds__(kThreads, 2) quantize_kernel(const __grid_cons
 
   // rows
   if (a.d_codes != nullptr || WHOLE) {
-    const int64_t panel = (a.cols + 511) / 512;
     uint2 turned[8];
-    uint32_t tops8[8];
+    uint32_t byte[8];
     if (!WHOLE) {
       // the eight rows' maxima together, so that their exchanges overlap
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float x[8];
-        unpack(raw[i], x);
-        tops8[i] = top8(x);
-      }
+      for (int i = 0; i < 8; ++i) byte[i] = top_of(magnitudes(raw[i], false));
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) tops8[i] = max(tops8[i], __shfl_xor_sync(0xFFFFFFFFu, tops8[i], o));
+        for (int i = 0; i < 8; ++i) byte[i] = max(byte[i], __shfl_xor_sync(0xFFFFFFFFu, byte[i], o));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) odd = odd || tops8[i] >= kInfBits;
+      for (int i = 0; i < 8; ++i) odd = odd || byte[i] >= kInfBits;
       odd = __any_sync(0xFFFFFFFFu, odd);
       if (odd) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float x[8];
-          unpack(raw[i], x);
-          tops8[i] = top16(finite_top8(x));
-        }
+        for (int i = 0; i < 8; ++i) byte[i] = top16(top_of(magnitudes(raw[i], true)));
       }
     }
+    uint8_t* p = static_cast<uint8_t*>(a.d_codes) + (r0 + l) * a.codes_pitch + c0 + c;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 8; ++i, p += a.codes_pitch) {
       float x[8];
       unpack(raw[i], x);
-      const uint32_t byte = scale_byte(WHOLE ? top : tops8[i]);
-      const uint2 w = codes8(x, inverse_scale(byte), odd);
-      if (a.d_codes != nullptr && l + i < rows) {
-        if (c < cols)
-          store_codes8(static_cast<uint8_t*>(a.d_codes) + (r0 + l + i) * a.codes_pitch + c0 + c, cols - c, w);
-        if (square == 0)
-          static_cast<uint8_t*>(a.d_scales)[scale_place(r0 + l + i, c0 >> 7, panel)] = (uint8_t)byte;
-      }
-      turned[i] = w;
+      byte[i] = scale_byte(WHOLE ? top : byte[i]);
+      turned[i] = codes8(x, inverse_scale(byte[i]), odd);
+      if (a.d_codes != nullptr && l + i < rows && c < cols) store_codes8(p, cols - c, turned[i]);
     }
+    if (a.d_codes != nullptr)
+      store_bytes(static_cast<uint8_t*>(a.d_scales), byte, square, r0 + l, rows - l, c0 >> 7, (a.cols + 511) / 512);
     if (a.d_codes_t == nullptr) return;
-    if (WHOLE) {
-      put_turned(turned, sh.codes, c, band);
-    }
+    if (WHOLE) put_turned(turned, sh.codes, c, band);
   }
 
   // columns
   const int64_t panel = (a.rows + 511) / 512;
   uint8_t* scales = static_cast<uint8_t*>(a.d_scales_t);
   if (!WHOLE) {
-    uint32_t m[8] = {};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float x[8];
-      unpack(raw[i], x);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) m[j] = max(m[j], magnitude(x[j]));
-    }
-    column_tops(m, sh.top, tops_t, band, c);
+    uint32_t byte[8];
+    column_tops(raw, false, sh.top, tops_t, byte);
     odd = false;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) odd = odd || m[j] >= kInfBits;
-    if (__syncthreads_or(odd)) {       // rare: the columns' finite maxima
-#pragma unroll
-      for (int j = 0; j < 8; ++j) m[j] = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float x[8];
-        unpack(raw[i], x);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m[j] = finite_bits(x[j]) ? max(m[j], magnitude(x[j])) : m[j];
-      }
-      column_tops(m, sh.top, tops_t, band, c);
-      odd = true;
-    }
-    uint32_t byte[8];
+    for (int j = 0; j < 8; ++j) odd = odd || byte[j] >= kInfBits;
+    odd = __syncthreads_or(odd);
+    if (odd) column_tops(raw, true, sh.top, tops_t, byte);       // rare
     float inv[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      byte[j] = scale_byte(m[j]);
+      byte[j] = scale_byte(byte[j]);
       inv[j] = inverse_scale(byte[j]);
     }
-    if (band == 0) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (c + j < cols) scales[scale_place(c0 + c + j, r0 >> 7, panel)] = (uint8_t)byte[j];
-    }
+    // each band stores one of a square's eight columns
+    store_bytes(scales, byte, band, c0 + c, cols - c, r0 >> 7, panel);
     uint2 turned[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -220,6 +253,7 @@ __global__ void __launch_bounds__(kThreads, 2) quantize_kernel(const __grid_cons
       times8(x, inv);
       turned[i] = codes8(x);
     }
+    if (odd) __syncthreads();          // the second maxima are read before their place is written
     put_turned(turned, sh.codes, c, band);
   } else if (threadIdx.x < cols) {
     scales[scale_place(c0 + threadIdx.x, r0 >> 7, panel)] = (uint8_t)scale_byte(top);
