@@ -336,6 +336,10 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     *failed = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (warp == 3 && lane < 4) {
+    const CUtensorMap* maps[4] = {&map_x, &map_y, &map_sx, &map_sy};
+    asm volatile("prefetch.tensormap [%0];" ::"l"(maps[lane]) : "memory");
+  }
   if (warp == 2) {
     if (CG == 1) {
       asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
@@ -515,6 +519,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     }
   }
 
+  __syncwarp();
   fence_before();
   __syncthreads();
   if (CG == 1 && a.split > 1) {

@@ -257,7 +257,7 @@ def opt_rms_norm_backward(dy, h, weight, rstd, dh, dh_in=None, dx=None, dweight=
     if dweight is not None:
         dq = _vector(dweight, "dweight", cols, dev, ready.f32)
         if workspace is None:
-            need = opt_rms_norm_backward_workspace(rows, cols)
+            need = min(rows, 1024) * (-(-cols // 4) * 4) * 4        # opt_rms_norm_backward_workspace
             workspace = _workspace(need, dev, stream)
         else:
             need = workspace.numel() * workspace.element_size()

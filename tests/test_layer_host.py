@@ -49,6 +49,12 @@ def test_scales_bytes():
     assert ps.lib().opt_scales_bytes(1 << 31, 4) == ps.OPT_ELIMIT
 
 
+def test_backward_workspace():
+    for rows, cols in ((0, 7), (1, 1), (5, 769), (4096, 4096)):
+        assert ps.opt_rms_norm_backward_workspace(rows, cols) == min(rows, 1024) * (-(-cols // 4) * 4) * 4
+    assert ps.lib().opt_rms_norm_backward_workspace(-1, 4) == ps.OPT_EINVAL
+
+
 DROPOUT = dict(d_x=P, d_y=P, x_pitch=8, y_pitch=8, rows=2, cols=8, p=0.1, dtype=ps.OPT_BF16)
 NORM = dict(d_x=P, d_weight=P, d_y=P, x_pitch=8, y_pitch=8, rows=2, cols=8, dtype=ps.OPT_BF16, weight_dtype=ps.OPT_F32,
             eps=1e-5)
