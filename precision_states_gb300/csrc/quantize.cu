@@ -136,7 +136,7 @@ __device__ __forceinline__ void store_bytes(uint8_t* scales, const uint32_t (&by
 }
 
 template <typename T, bool VEC, bool WHOLE>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && VEC ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && VEC ? 4 : 2)
 quantize_kernel(const __grid_constant__ opt_quantize_args a, int64_t col_tiles) {
   // warps' maxima of columns; then the transposed codes, 16 pieces of 8 bytes per
   // column, pieces turned by column
