@@ -122,6 +122,17 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
     if (now_ns() - t0 > kWaitNs) return false;
   return true;
 }
+// The same by a whole warp, with one verdict, so that what follows is uniform.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xFFFFFFFFu, bar_wait(bar, parity));
+}
+// One lane of a converged warp, always the same one.
+__device__ __forceinline__ bool elected() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -310,7 +321,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
   const uint32_t full = bars, empty = full + 8 * S, done = empty + 8 * S, free_ = done + 16, drain = free_ + 16;
   volatile uint32_t* tmem_at = reinterpret_cast<volatile uint32_t*>(smem + L::kBarAt + 8 * L::kBars);
   volatile uint32_t* failed = tmem_at + 1;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const bool clustered = CG == 2 || a.split > 1;
   const uint32_t rank = clustered ? cta_rank() : 0;
 
@@ -356,16 +367,19 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
   __syncthreads();
   if (clustered) cluster_sync();
   fence_after();
-  const uint32_t tmem = *tmem_at;
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_at, 0);
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     // ------------------------------------------------------------- producer
-    // A pair's copies all count on the leader's barrier.  One thread paces the
-    // ring here and one below, so their loops carry their state (stage, phase,
-    // addresses) from block to block and compute nothing per block.
+    // A pair's copies all count on the leader's barrier.  This warp and the next
+    // pace the ring, so their loops carry their state (stage, phase, addresses)
+    // from block to block, and the whole warp runs them, one lane issuing: what
+    // is the same in all lanes stays in uniform registers, which the copies and
+    // products take their operands from.  (16 x 4096 x 14336: 39.0 us with one
+    // thread that divided per block, 28.7 with its state carried, 20.4 by a warp.)
     const uint32_t full_at = CG == 2 ? map_to(full, 0) : full;
     constexpr uint32_t kBytes = CG * (L::kXBytes + L::kYBytes), kScales = CG * L::kScaleBytes;
-    const bool counts = CG == 1 || rank == 0;
+    const bool counts = CG == 1 || rank == 0, issues = elected();
     Ring<S> at;
     bool ok = true;
     for (int t = first; t < tiles && ok; t += step) {
@@ -378,21 +392,24 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if (kb + j >= kb1) break;
-          if (!at.first && !bar_wait(empty + 8 * at.stage, at.phase ^ 1u)) {
+          if (!at.first && !warp_wait(empty + 8 * at.stage, at.phase ^ 1u)) {
             ok = false;
             break;
           }
           const uint32_t bar = full_at + 8 * at.stage, dst = ring + at.stage * L::kStage;
-          if (counts) bar_expect(full + 8 * at.stage, j == 0 ? kBytes + kScales : kBytes);
-          if (j == 0) {
-            const uint32_t sd = scales + at.stage * L::kScaleBytes;
-            tma_2d<CG>(sd, &map_sx, 0, sx, bar);
+          if (issues) {
+            if (counts) bar_expect(full + 8 * at.stage, j == 0 ? kBytes + kScales : kBytes);
+            if (j == 0) {
+              const uint32_t sd = scales + at.stage * L::kScaleBytes;
+              tma_2d<CG>(sd, &map_sx, 0, sx, bar);
 #pragma unroll
-            for (int i = 0; i < L::kYScaleTiles; ++i)
-              tma_2d<CG>(sd + (1 + i) * kScaleTile, &map_sy, 0, sy + i * a.panel, bar);
+              for (int i = 0; i < L::kYScaleTiles; ++i)
+                tma_2d<CG>(sd + (1 + i) * kScaleTile, &map_sy, 0, sy + i * a.panel, bar);
+            }
+            tma_2d<CG>(dst, &map_x, (kb + j) * kStageDepth, x0, bar);
+            tma_2d<CG>(dst + L::kXBytes, &map_y, (kb + j) * kStageDepth, y_row, bar);
           }
-          tma_2d<CG>(dst, &map_x, (kb + j) * kStageDepth, x0, bar);
-          tma_2d<CG>(dst + L::kXBytes, &map_y, (kb + j) * kStageDepth, y_row, bar);
+          __syncwarp();
           at.next();
         }
         if (!ok) break;
@@ -406,17 +423,18 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
           bar_wait(full + 8 * i, i < (int)at.stage ? at.phase : at.phase ^ 1u);
         }
     }
-  } else if (warp == 1 && lane == 0 && (CG == 1 || rank == 0)) {
+  } else if (warp == 1 && (CG == 1 || rank == 0)) {
     // ------------------------------------------------------------- products
     const uint64_t x_desc = tile_desc(ring), y_desc = tile_desc(ring + L::kXBytes), s_desc = scale_desc(scales);
+    const bool issues = elected();
     Ring<S> at;
     int i = 0;
     uint32_t set = 0;
     bool ok = true;
     for (int t = first; t < tiles && ok; t += step, ++i) {
       const uint32_t acc = tmem + (i & 1) * L::kAcc1;
-      if (L::kOverlap ? (i >= 1 && !bar_wait(free_, (uint32_t)(i - 1) & 1u))
-                      : (i >= 2 && !bar_wait(free_ + 8 * (i & 1), (uint32_t)((i >> 1) - 1) & 1u))) {
+      if (L::kOverlap ? (i >= 1 && !warp_wait(free_, (uint32_t)(i - 1) & 1u))
+                      : (i >= 2 && !warp_wait(free_ + 8 * (i & 1), (uint32_t)((i >> 1) - 1) & 1u))) {
         ok = false;
         break;
       }
@@ -428,33 +446,35 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if (kb + j >= kb1) break;
-          if (!bar_wait(full + 8 * at.stage, at.phase)) {
+          if (!warp_wait(full + 8 * at.stage, at.phase)) {
             ok = false;
             break;
           }
           fence_after();
-          if (j == 0) {
-            const uint64_t sd = s_desc + at.stage * (L::kScaleBytes >> 4);
+          if (issues) {
+            if (j == 0) {
+              const uint64_t sd = s_desc + at.stage * (L::kScaleBytes >> 4);
 #pragma unroll
-            for (int k = 0; k <= L::kYScaleTiles; ++k) copy_scales<CG>(col + 4 * k, sd + k * (kScaleTile >> 4));
-          }
-          const uint64_t dx = x_desc + at.stage * (L::kStage >> 4), dy = y_desc + at.stage * (L::kStage >> 4);
+              for (int k = 0; k <= L::kYScaleTiles; ++k) copy_scales<CG>(col + 4 * k, sd + k * (kScaleTile >> 4));
+            }
+            const uint64_t dx = x_desc + at.stage * (L::kStage >> 4), dy = y_desc + at.stage * (L::kStage >> 4);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            product<CG>(acc, dx + 2 * k, dy + 2 * k, instr_desc<CG, NT>(j), col, col + 4, add);
-            add = 1;
+            for (int k = 0; k < 4; ++k)
+              product<CG>(acc, dx + 2 * k, dy + 2 * k, instr_desc<CG, NT>(j), col, col + 4, k > 0 ? 1u : add);
+            commit<CG>(empty + 8 * at.stage);
           }
-          commit<CG>(empty + 8 * at.stage);
+          __syncwarp();
+          add = 1;
           at.next();
         }
         if (!ok) break;
       }
-      if (ok) commit<CG>(done + 8 * (i & 1));
+      if (ok && issues) commit<CG>(done + 8 * (i & 1));
     }
     if (!ok) {
       *failed = 1;
-      commit<CG>(drain);       // let what was issued end
-      bar_wait(drain, 0);
+      if (issues) commit<CG>(drain);       // let what was issued end
+      warp_wait(drain, 0);
     }
   } else if (warp >= 4) {
     // --------------------------------------------------------------- output
@@ -479,7 +499,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
       if (L::kOverlap && !shares && lane == 0) bar_arrive_cluster(free_at);
       Outputs<T, C> o[2];
       if (!joined && chunks > 0) o[0].load(a, x, y0 + column(0));
-      if (!__all_sync(0xFFFFFFFFu, bar_wait(done + 8 * (i & 1), (uint32_t)(i >> 1) & 1u))) {
+      if (!warp_wait(done + 8 * (i & 1), (uint32_t)(i >> 1) & 1u)) {
         *failed = 1;
         break;
       }
@@ -665,31 +685,37 @@ cudaError_t launch(const Operand& x, const Operand& y, int64_t k, MatmulArgs a, 
 }
 
 // Which operand is x, the tile (128 or, by a pair of CTAs, 256 rows of x, nt of
-// y) and the split, by the estimated time: the blocks that one CTA goes through,
-// times a block's time, plus a split's sum.
+// y) and the split, by the estimated time: the blocks that one CTA goes through
+// times a block's time, plus each tile's and each split's own.  A split's CTAs
+// take one tile each, so a second wave of them starts anew.  The times are fits
+// to runs of one shape in each form, in ns: 256 x 4096 x 4096 takes 9.4 us in
+// 128-wide tiles, 9.5 in pairs of 128, 14.4 in pairs of 256, 12.2 split in two;
+// 64 x 4096 x 4096 9.0 whole, 8.3 split in four; 8192 x 14336 x 4096 418 in
+// pairs of 128, 285 in pairs of 256.
 struct Plan {
   int swap, cg, nt, split;
 };
-constexpr double kStartNs = 2000, kTileNs = 500;
 Plan plan(int64_t m, int64_t n, int blocks, int sm_count) {
-  static const struct { int cg, nt, ns, split_ns; } kTiles[] = {
-      {1, 16, 255, 4000}, {1, 32, 255, 4000}, {1, 64, 260, 4500}, {1, 128, 265, 7500}, {2, 128, 272, 0}, {2, 256, 370, 0}};
+  static const struct { int cg, nt, block, tile, split; } kForms[] = {
+      {1, 16, 155, 500, 2300}, {1, 32, 165, 500, 2500},  {1, 64, 185, 500, 3300},
+      {1, 128, 208, 500, 6200}, {2, 128, 175, 1300, 0}, {2, 256, 320, 1300, 0}};
+  constexpr double kStart = 3500;
   Plan best = {0, 2, 256, 1};
   double least = 1e300;
   const int panel = (blocks + 3) / 4;
-  for (const auto& t : kTiles)
-    for (int swap = 0; swap < (t.nt < 128 ? 2 : 1); ++swap) {
+  for (const auto& f : kForms)
+    for (int swap = 0; swap < (f.nt < 128 ? 2 : 1); ++swap) {
       const int64_t xr = swap ? n : m, yr = swap ? m : n;
       // scales are addressed by whole tiles of 128 rows: a narrower tile of y only where it is the only one
-      if (t.nt < 128 && yr > t.nt) continue;
-      const int64_t tiles = ((xr + 128 * t.cg - 1) / (128 * t.cg)) * ((yr + t.nt - 1) / t.nt);
-      for (int split = 1; split <= (t.cg == 2 ? 1 : 8) && split <= panel; split *= 2) {
-        const int64_t slots = sm_count / (t.cg == 2 ? 2 : split);
-        const int64_t waves = (tiles + slots - 1) / slots;
-        const double time = (double)waves * ((blocks + split - 1) / split * t.ns + (split > 1 ? t.split_ns : kStartNs / waves + kTileNs));
+      if (f.nt < 128 && yr > f.nt) continue;
+      const int64_t tiles = ((xr + 128 * f.cg - 1) / (128 * f.cg)) * ((yr + f.nt - 1) / f.nt);
+      for (int split = 1; split <= (f.cg == 2 ? 1 : 8) && split <= panel; split *= 2) {
+        const int64_t slots = sm_count / (f.cg == 2 ? 2 : split), waves = (tiles + slots - 1) / slots;
+        double time = (double)waves * ((blocks + split - 1) / split) * f.block;
+        time += split == 1 ? (double)waves * f.tile : (double)waves * f.split + (double)(waves - 1) * kStart;
         if (time < least) {
           least = time;
-          best = {swap, t.cg, t.nt, split};
+          best = {swap, f.cg, f.nt, split};
         }
       }
     }
