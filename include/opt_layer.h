@@ -185,9 +185,16 @@ typedef struct opt_matmul_args {
   int64_t a_pitch, b_pitch, addend_pitch, out_pitch;
   int64_t m, n, k;
   int32_t out_dtype;
-  int32_t reserved;          /* 0 */
+  int32_t flags;             /* OPT_MATMUL_* bits; others must be 0 */
 } opt_matmul_args;
 int opt_matmul(const opt_matmul_args* a, void* stream);
+
+/* Wait drill: make the product's bounded waits run out on purpose (after 1 ms,
+ * with no fault), so that a caller can test its handling of
+ * OPT_FLAG_WAIT_TIMEOUT.  No operand is loaded and nothing is written.
+ * OPT_EUNSUPPORTED where a product waits on nothing (an operand of at most eight
+ * rows, a depth of 0). */
+#define OPT_MATMUL_WAIT_DRILL 1
 
 /* Error flags raised by the current device's layer kernels since the last call,
  * then cleared; 0 means that every kernel ran to completion.  Copies to host and

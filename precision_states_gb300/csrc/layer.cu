@@ -161,7 +161,7 @@ int opt_quantize(const opt_quantize_args* a, void* stream) {
 }
 
 int opt_matmul(const opt_matmul_args* a, void* stream) {
-  if (a == nullptr || a->reserved != 0) return OPT_EINVAL;
+  if (a == nullptr || (a->flags & ~OPT_MATMUL_WAIT_DRILL) != 0) return OPT_EINVAL;
   PS_TRY(check_sizes(a->m, a->n));
   PS_TRY(check_sizes(a->k, 0));
   if (!plain_type(a->out_dtype)) return OPT_EUNSUPPORTED;
@@ -173,6 +173,7 @@ int opt_matmul(const opt_matmul_args* a, void* stream) {
     PS_TRY(check_codes(a->d_a, a->a_pitch, a->d_a_scales, a->m, a->k));
     PS_TRY(check_codes(a->d_b, a->b_pitch, a->d_b_scales, a->n, a->k));
   }
+  if (a->flags != 0 && !matmul_waits(*a)) return OPT_EUNSUPPORTED;
   int sms = 0;
   PS_TRY(sm_count_of(&sms));
   return status_of(launch_matmul(*a, sms, static_cast<cudaStream_t>(stream)));

@@ -27,7 +27,7 @@
 // Splits.  With few tiles, the depth is split over a cluster of CTAs; their
 // accumulators are summed through distributed shared memory in rank order.
 //
-// Every wait is bounded (kWaitNs of the global timer): one that runs out raises
+// Every wait is bounded (by the global timer): one that runs out raises
 // OPT_FLAG_WAIT_TIMEOUT (opt_layer_status), and the CTA leaves after its copies
 // and products in flight have ended.
 #include <cuda.h>
@@ -39,7 +39,7 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kOutWarps = 8;           // two for each 32 lanes of tensor memory, half of the columns each
-constexpr unsigned long long kWaitNs = 2000000000ull;
+constexpr unsigned long long kWaitNs = 2000000000ull, kDrillNs = 1000000ull;
 constexpr int kScaleTile = 512;        // bytes: 128 rows x 4 blocks
 constexpr int kStageDepth = 128;
 constexpr int kRingBytes = 204 * 1024;
@@ -52,6 +52,8 @@ struct MatmulArgs : OutputArgs {
   int blocks;                // ceil(k / 128)
   int panel;                 // scale tiles per 128 rows: ceil(blocks / 4)
   int split;                 // CTAs per cluster along the depth (CG 1)
+  int drill;                 // load nothing, so that the waits run out
+  unsigned long long wait_ns;   // limit of each wait
 };
 
 template <int CG, int NT>
@@ -115,16 +117,16 @@ __device__ __forceinline__ unsigned long long now_ns() {
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   return t;
 }
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, unsigned long long limit_ns) {
   if (bar_try(bar, parity)) return true;
   const unsigned long long t0 = now_ns();
   while (!bar_try(bar, parity))
-    if (now_ns() - t0 > kWaitNs) return false;
+    if (now_ns() - t0 > limit_ns) return false;
   return true;
 }
 // The same by a whole warp, with one verdict, so that what follows is uniform.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
-  return __all_sync(0xFFFFFFFFu, bar_wait(bar, parity));
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, unsigned long long limit_ns) {
+  return __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, limit_ns));
 }
 // One lane of a converged warp, always the same one.
 __device__ __forceinline__ bool elected() {
@@ -382,7 +384,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     const bool counts = CG == 1 || rank == 0, issues = elected();
     Ring<S> at;
     bool ok = true;
-    for (int t = first; t < tiles && ok; t += step) {
+    for (int t = a.drill ? tiles : first; t < tiles && ok; t += step) {
       int tx, ty;
       tile_at(a, t, tx, ty);
       const int x0 = (tx * CG + (CG == 2 ? (int)rank : 0)) * 128, y0 = ty * NT;
@@ -392,7 +394,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if (kb + j >= kb1) break;
-          if (!at.first && !warp_wait(empty + 8 * at.stage, at.phase ^ 1u)) {
+          if (!at.first && !warp_wait(empty + 8 * at.stage, at.phase ^ 1u, a.wait_ns)) {
             ok = false;
             break;
           }
@@ -420,7 +422,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
       if (rank == 0)           // let what was issued land: each stage's last use
         for (int i = 0; i < S; ++i) {
           if (at.first && i >= (int)at.stage) break;
-          bar_wait(full + 8 * i, i < (int)at.stage ? at.phase : at.phase ^ 1u);
+          bar_wait(full + 8 * i, i < (int)at.stage ? at.phase : at.phase ^ 1u, a.wait_ns);
         }
     }
   } else if (warp == 1 && (CG == 1 || rank == 0)) {
@@ -433,8 +435,8 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     bool ok = true;
     for (int t = first; t < tiles && ok; t += step, ++i) {
       const uint32_t acc = tmem + (i & 1) * L::kAcc1;
-      if (L::kOverlap ? (i >= 1 && !warp_wait(free_, (uint32_t)(i - 1) & 1u))
-                      : (i >= 2 && !warp_wait(free_ + 8 * (i & 1), (uint32_t)((i >> 1) - 1) & 1u))) {
+      if (L::kOverlap ? (i >= 1 && !warp_wait(free_, (uint32_t)(i - 1) & 1u, a.wait_ns))
+                      : (i >= 2 && !warp_wait(free_ + 8 * (i & 1), (uint32_t)((i >> 1) - 1) & 1u, a.wait_ns))) {
         ok = false;
         break;
       }
@@ -446,7 +448,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if (kb + j >= kb1) break;
-          if (!warp_wait(full + 8 * at.stage, at.phase)) {
+          if (!warp_wait(full + 8 * at.stage, at.phase, a.wait_ns)) {
             ok = false;
             break;
           }
@@ -474,7 +476,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     if (!ok) {
       *failed = 1;
       if (issues) commit<CG>(drain);       // let what was issued end
-      warp_wait(drain, 0);
+      warp_wait(drain, 0, a.wait_ns);
     }
   } else if (warp >= 4) {
     // --------------------------------------------------------------- output
@@ -499,7 +501,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
       if (L::kOverlap && !shares && lane == 0) bar_arrive_cluster(free_at);
       Outputs<T, C> o[2];
       if (!joined && chunks > 0) o[0].load(a, x, y0 + column(0));
-      if (!warp_wait(done + 8 * (i & 1), (uint32_t)(i >> 1) & 1u)) {
+      if (!warp_wait(done + 8 * (i & 1), (uint32_t)(i >> 1) & 1u, a.wait_ns)) {
         *failed = 1;
         break;
       }
@@ -739,9 +741,11 @@ cudaError_t dispatch(const opt_matmul_args& c, int sm_count, cudaStream_t s) {
     no_depth_kernel<T><<<(unsigned)sm_count * 4, kThreads, 0, s>>>(a);
     return cudaGetLastError();
   }
+  a.drill = (c.flags & OPT_MATMUL_WAIT_DRILL) != 0;
+  a.wait_ns = a.drill ? kDrillNs : kWaitNs;
   a.blocks = (int)((c.k + 127) / 128);
   a.panel = (a.blocks + 3) / 4;
-  if (c.m <= kFewRows || c.n <= kFewRows) {
+  if (!matmul_waits(c)) {
     a.swap = c.m < c.n;
     return launch_matmul_few(c, a, s);
   }
@@ -761,6 +765,8 @@ cudaError_t dispatch(const opt_matmul_args& c, int sm_count, cudaStream_t s) {
 }
 
 }  // namespace
+
+bool matmul_waits(const opt_matmul_args& a) { return a.k > 0 && a.m > kFewRows && a.n > kFewRows; }
 
 cudaError_t launch_matmul(const opt_matmul_args& a, int sm_count, cudaStream_t s) {
   return a.out_dtype == OPT_F32 ? dispatch<float>(a, sm_count, s) : dispatch<Bf16>(a, sm_count, s);

@@ -51,7 +51,7 @@ class opt_quantize_args(_c.Structure):
 class opt_matmul_args(_c.Structure):
     _fields_ = [("d_a", _vp), ("d_a_scales", _vp), ("d_b", _vp), ("d_b_scales", _vp), ("d_addend", _vp),
                 ("d_out", _vp), ("a_pitch", _i64), ("b_pitch", _i64), ("addend_pitch", _i64), ("out_pitch", _i64),
-                ("m", _i64), ("n", _i64), ("k", _i64), ("out_dtype", _i32), ("reserved", _i32)]
+                ("m", _i64), ("n", _i64), ("k", _i64), ("out_dtype", _i32), ("flags", _i32)]
 
 
 # the C ABI: name -> (restype, argtypes); the argument structs go as packed bytes
@@ -65,6 +65,8 @@ SIGS = {
     "opt_matmul": (_c.c_int, [_c.c_char_p, _vp]),
     "opt_layer_status": (_c.c_int, [_c.POINTER(_i32), _vp]),
 }
+
+OPT_MATMUL_WAIT_DRILL = 1
 
 _CODE = {_vp: "Q", _i64: "q", _u64: "Q", _i32: "i", _u32: "I", _f32: "f", _f64: "d"}
 
@@ -303,7 +305,7 @@ def opt_quantize(x, codes=None, scales=None, codes_t=None, scales_t=None, block_
         _check(st, "opt_quantize")
 
 
-def opt_matmul(a, a_scales, b, b_scales, out, addend=None, stream=None):
+def opt_matmul(a, a_scales, b, b_scales, out, addend=None, stream=None, wait_drill=False):
     """out = a b^T (+ addend): a of m x k and b of n x k codes with their scales,
     out and addend float32 or bfloat16 of m x n; addend may be out."""
     ready = _ready or _get_ready()
@@ -317,7 +319,8 @@ def opt_matmul(a, a_scales, b, b_scales, out, addend=None, stream=None):
     aq, asq, ap = _held(a, a_scales, "a", m, k, dev, ready)
     bq, bsq, bp = _held(b, b_scales, "b", n, k, dev, ready)
     dq, dp = (0, 0) if addend is None else _like(addend, "addend", m, n, dtype, dev)
-    st = ready.matmul(_pack_matmul(aq, asq, bq, bsq, dq, out.data_ptr(), ap, bp, dp, op, m, n, k, dt, 0),
+    st = ready.matmul(_pack_matmul(aq, asq, bq, bsq, dq, out.data_ptr(), ap, bp, dp, op, m, n, k, dt,
+                                   OPT_MATMUL_WAIT_DRILL if wait_drill else 0),
                       ready.stream(dev) if stream is None else _stream_ptr(stream))
     if st:
         _check(st, "opt_matmul")

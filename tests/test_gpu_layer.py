@@ -436,6 +436,135 @@ def test_calls_replay_from_a_graph():
     assert torch.equal(out, want)
 
 
+# ------------------------------------------- guards, aliases, far-off elements
+class Guarded:
+    """Storage inside a larger allocation of a byte pattern; check() that the
+    bytes before and after it still hold the pattern."""
+    BAND = 512
+
+    def __init__(self):
+        self.kept = []
+
+    def new(self, rows, cols, dtype, pitch=None):
+        es = torch.empty(0, dtype=dtype).element_size()
+        pitch = pitch or cols
+        n = ((rows - 1) * pitch + cols) * es
+        flat = torch.full((n + 2 * self.BAND + 64,), 0xA5, dtype=torch.uint8, device="cuda")
+        self.kept.append((flat, n, rows, cols, pitch, es))
+        return flat[self.BAND:self.BAND + n + (-n) % es].view(dtype).as_strided((rows, cols), (pitch, 1))
+
+    def check(self):
+        for flat, n, rows, cols, pitch, es in self.kept:
+            inside = torch.zeros_like(flat, dtype=torch.bool)
+            body = inside[self.BAND:]
+            for r in range(rows):
+                body[r * pitch * es:(r * pitch + cols) * es] = True
+            assert (flat[~inside] == 0xA5).all(), (rows, cols, pitch)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(1, 5), (3, 769), (129, 264), (20, 4096), (2, 17000), (260, 130)])
+def test_nothing_is_written_outside(dtype, rows, cols):
+    g = Guarded()
+    td, up16 = TD[dtype], lambda n: -(-n // 16) * 16
+    x, res, w = matrix(rows, cols, dtype, 80), matrix(rows, cols, dtype, 81), torch.ones(cols, device="cuda")
+    h, y, dh, dx = (g.new(rows, cols, td, cols + p) for p in (0, 3, 8, 1))
+    rstd, dw = g.new(1, rows, torch.float32).view(-1), g.new(1, cols, torch.float32).view(-1)
+    codes, codes_t = g.new(rows, cols, torch.uint8, up16(cols)), g.new(cols, rows, torch.uint8, up16(rows))
+    scales = g.new(1, ps.opt_scales_bytes(rows, cols), torch.uint8).view(-1)
+    scales_t = g.new(1, ps.opt_scales_bytes(cols, rows), torch.uint8).view(-1)
+    work = g.new(1, ps.opt_rms_norm_backward_workspace(rows, cols), torch.uint8).view(-1)
+    ps.opt_dropout(x, y, 0.2, residual=res, **DRAW)
+    ps.opt_rms_norm(x, w, y=y, rstd=rstd, residual=res, h=h, codes=codes, scales=scales, p=0.2, **DRAW)
+    ps.opt_rms_norm_backward(y, h, w, rstd, dh, dx=dx, dweight=dw, p=0.2, workspace=work, **DRAW)
+    for block in (1, 128):
+        ps.opt_quantize(x, codes, scales, codes_t, scales_t, block_rows=block)
+    for out in (torch.float32, torch.bfloat16):
+        for pitch in (rows, rows + 16, rows + 3):
+            o = g.new(rows, rows, out, pitch)
+            ps.opt_matmul(codes, scales, codes, scales, o)                # rows x rows over the columns
+        if rows > 1:
+            few = g.new(2, rows, out, rows + 1)
+            ps.opt_matmul(codes[:2], scales[:ps.opt_scales_bytes(2, cols)], codes, scales, few)
+    torch.cuda.synchronize()
+    g.check()
+
+
+@pytest.mark.parametrize("cols", [200, 769, 4096, 20000])
+def test_outputs_in_their_inputs_place(cols):
+    rows = 37
+    x, res, w = matrix(rows, cols, "bf16", 82), matrix(rows, cols, "bf16", 83), torch.ones(cols, device="cuda")
+    rstd = torch.empty(rows, device="cuda")
+    h, y = torch.empty_like(x), torch.empty_like(x)
+    ps.opt_rms_norm(x, w, residual=res, h=h, y=y, rstd=rstd, p=0.1, **DRAW)
+    for place in (0, 1):
+        ins = [x.clone(), res.clone()]
+        y2 = torch.empty_like(x)
+        ps.opt_rms_norm(ins[0], w, residual=ins[1], h=ins[place], y=y2, p=0.1, **DRAW)
+        assert torch.equal(ins[place], h) and torch.equal(y2, y)
+    dy, dh_in, dh = matrix(rows, cols, "bf16", 84), matrix(rows, cols, "bf16", 85), torch.empty_like(x)
+    ps.opt_rms_norm_backward(dy, h, w, rstd, dh, dh_in=dh_in)
+    for place in (0, 1):
+        ins = [dy.clone(), dh_in.clone()]
+        ps.opt_rms_norm_backward(ins[0], h, w, rstd, ins[place], dh_in=ins[1])
+        assert torch.equal(ins[place], dh)
+
+
+def test_rows_past_2_31_elements():
+    """The last rows of matrices of over 2^31 elements are those of the same rows alone."""
+    rows, cols = (1 << 19) + 5, 4104
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+    tail = matrix(5, cols, "bf16", 86)
+    x.zero_()
+    x[-5:] = tail
+    w = torch.ones(cols, device="cuda")
+    y, y1 = torch.empty_like(x), torch.empty_like(tail)
+    ps.opt_rms_norm(x, w, y=y)
+    ps.opt_rms_norm(tail, w, y=y1)
+    assert torch.equal(y[-5:], y1) and (y[:-5] == 0).all()
+    ps.opt_rms_norm_backward(x, x, w, torch.ones(rows, device="cuda"), y)
+    ps.opt_rms_norm_backward(tail, tail, w, torch.ones(5, device="cuda"), y1)
+    assert torch.equal(y[-5:], y1) and (y[:-5] == 0).all()
+    del y
+    c, s = ps.e4m3_storage(rows, cols)
+    c1, s1 = ps.e4m3_storage(5, cols)
+    ps.opt_quantize(x, c, s)
+    ps.opt_quantize(tail, c1, s1)
+    assert torch.equal(c[-5:], c1)
+    assert (ref.scale_bytes_of(s, rows, cols)[-5:] == ref.scale_bytes_of(s1, 5, cols)).all()
+
+
+def test_product_of_over_2_31_elements():
+    m, n = 70001, 40000
+    a, sa = operand(m, 128, 1, 87)
+    b, sb = operand(n, 128, 1, 88)
+    out = torch.empty(m, n, dtype=torch.bfloat16, device="cuda")
+    ps.opt_matmul(a, sa, b, sb, out)
+    vb = ref.values(b, sb)
+    e = ref.scale_bytes_of(sa, m, 128) - 127
+    for r in (0, 55001, m - 1):
+        row = a[r].cpu().view(torch.float8_e4m3fn).double().numpy() * 2.0 ** float(e[r, 0])
+        bound = (np.abs(vb) @ np.abs(row)) * 2.0 ** -23 * 38
+        within(out[r], vb @ row, "bf16", bound)
+
+
+@pytest.mark.parametrize("m,n,k", [(40, 256, 1024), (300, 200, 700), (1024, 2048, 256)])
+def test_wait_drill(m, n, k):
+    """A product whose waits run out reports it, leaves its output alone, and
+    changes nothing for the next one.  (One shape per form: split, single CTAs,
+    pairs.)"""
+    a, sa = operand(m, k, 1, 90)
+    b, sb = operand(n, k, 1, 91)
+    out, want = blank(m, n, "f32"), torch.empty(m, n, device="cuda")
+    assert ps.opt_layer_status() == 0
+    ps.opt_matmul(a, sa, b, sb, out, wait_drill=True)
+    assert ps.opt_layer_status() == ps.OPT_FLAG_WAIT_TIMEOUT and (out == 7).all()
+    assert ps.opt_layer_status() == 0
+    ps.opt_matmul(a, sa, b, sb, want)
+    ps.opt_matmul(a, sa, b, sb, out)
+    assert torch.equal(out, want) and ps.opt_layer_status() == 0
+
+
 def test_status_is_clear():
     """Every kernel of the tests above ran to completion."""
     assert ps.opt_layer_status() == 0

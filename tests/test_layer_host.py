@@ -99,7 +99,9 @@ BIG = 1 << 31
     ("opt_matmul", MATMUL, dict(k=-1), ps.OPT_EINVAL), ("opt_matmul", MATMUL, dict(k=BIG), ps.OPT_ELIMIT),
     ("opt_matmul", MATMUL, dict(out_dtype=ps.OPT_E4M3), ps.OPT_EUNSUPPORTED), ("opt_matmul", MATMUL, dict(out_pitch=3), ps.OPT_EINVAL),
     ("opt_matmul", MATMUL, dict(d_addend=P, addend_pitch=3), ps.OPT_EINVAL), ("opt_matmul", MATMUL, dict(d_out=P + 2), ps.OPT_EALIGN),
-    ("opt_matmul", MATMUL, dict(reserved=2), ps.OPT_EINVAL), ("opt_matmul", MATMUL, dict(m=0, d_a=0), ps.OPT_OK),
+    ("opt_matmul", MATMUL, dict(flags=2), ps.OPT_EINVAL),
+    ("opt_matmul", MATMUL, dict(flags=ps.OPT_MATMUL_WAIT_DRILL), ps.OPT_EUNSUPPORTED),
+    ("opt_matmul", MATMUL, dict(flags=ps.OPT_MATMUL_WAIT_DRILL, k=0), ps.OPT_EUNSUPPORTED), ("opt_matmul", MATMUL, dict(m=0, d_a=0), ps.OPT_OK),
 ])
 def test_refusals(name, base, change, status):
     assert call(name, getattr(layer, name + "_args"), **{**base, **change}) == status
