@@ -13,8 +13,8 @@
 // be x (`swap`), so that few rows on either side become a narrow NT and not a
 // mostly empty 128.  Warp 0 fills a ring of stages (128 bytes of depth of both
 // tiles, 128-byte swizzle; every fourth stage the 512-byte scale tiles too) by
-// TMA; one thread of warp 1 copies scale tiles to tensor memory and issues the
-// products; warps 4-11 read finished accumulators and write out.  Two
+// TMA; warp 1 copies scale tiles to tensor memory and issues the products; warps
+// 4-11 read finished accumulators and write out.  Two
 // accumulators alternate, so that a tile's output overlaps the next one's
 // products.  At NT 256 they share 24 columns (two of 256 and two sets of scales
 // do not fit into 512): the output reads those first, and the next tile's
@@ -52,6 +52,7 @@ struct MatmulArgs : OutputArgs {
   int blocks;                // ceil(k / 128)
   int panel;                 // scale tiles per 128 rows: ceil(blocks / 4)
   int split;                 // CTAs per cluster along the depth (CG 1)
+  int staged;                // whole warps' outputs leave through shared memory
   int drill;                 // load nothing, so that the waits run out
   unsigned long long wait_ns;   // limit of each wait
 };
@@ -73,9 +74,14 @@ struct Layout {
   static constexpr int kNeed = kScaleCol + 2 * kScaleCols;
   static constexpr int kCols = kNeed <= 64 ? 64 : kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
   static constexpr int kBars = 2 * kStages + 5;      // full, empty, done[2], free[2], drain
-  // dynamic shared memory: ring | scales | barriers, tensor memory address, failure
+  // columns that an output warp takes at a time: from NT 64 on, 64 bytes of out
+  template <typename T>
+  static constexpr int kOutCols = NT >= 64 ? 64 / (int)sizeof(T) : 16;
+  static constexpr int kOutBytes = NT >= 64 ? kOutWarps * 32 * 64 : 0;
+  // dynamic shared memory: ring | scales | output | barriers, tensor memory address, failure
   static constexpr int kScaleAt = kStages * kStage;
-  static constexpr int kBarAt = kScaleAt + kStages * kScaleBytes;
+  static constexpr int kOutAt = kScaleAt + kStages * kScaleBytes;
+  static constexpr int kBarAt = kOutAt + kOutBytes;
   static constexpr int kBytes = kBarAt + kBars * 8 + 16 + 1024;        // 1024: alignment of the ring
   static_assert(kNeed <= 512, "tensor memory");
   static_assert(kBytes <= 227 * 1024, "shared memory");
@@ -229,18 +235,16 @@ __device__ __forceinline__ void acc_load(uint32_t tmem, float (&v)[N]) {
 // -------------------------------------------------------------------- output
 // A thread's N outputs: row x of the tile, columns y0 .. y0 + N - 1.  The addend
 // is loaded whole, and before the accumulator is read, so that its latency is
-// paid once.  Whole rows go in 32-byte accesses (a sector each) where `vec` says
-// that they may.
+// paid once, in 32-byte accesses (a sector each) where `vec` says that it may.
 template <typename T, int N>
 struct Outputs {
   static constexpr int kWords = N * (int)sizeof(T) / 4;
   uint32_t add[kWords];
-  __device__ __forceinline__ bool whole(const MatmulArgs& a, int y0) const { return a.vec && !a.swap && y0 + N <= a.ny; }
 
   __device__ __forceinline__ void load(const MatmulArgs& a, int x, int y0) {
     if (a.addend == nullptr || x >= a.nx) return;
     const T* p = static_cast<const T*>(a.addend);
-    if (whole(a, y0)) {
+    if (a.vec && !a.swap && y0 + N <= a.ny) {
       p += place(a, a.addend_pitch, x, y0);
 #pragma unroll
       for (int i = 0; i < kWords; i += 8)
@@ -258,31 +262,58 @@ struct Outputs {
       }
     }
   }
-  __device__ __forceinline__ void store(const MatmulArgs& a, int x, int y0, float (&v)[N]) const {
-    if (x >= a.nx) return;
-    T* p = static_cast<T*>(a.out);
-    if (a.addend != nullptr) {
+  // v + addend
+  __device__ __forceinline__ void sum(const MatmulArgs& a, int x, float (&v)[N]) const {
+    if (a.addend == nullptr || x >= a.nx) return;
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        v[i] += sizeof(T) == 4 ? u2f(add[i]) : u2f(i & 1 ? add[i >> 1] & 0xFFFF0000u : add[i >> 1] << 16);
-    }
-    if (whole(a, y0)) {
-      p += place(a, a.out_pitch, x, y0);
-      uint32_t w[kWords];
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) w[i] = sizeof(T) == 4 ? f2u(v[i]) : bf16_pair(v[2 * i], v[2 * i + 1]);
-#pragma unroll
-      for (int i = 0; i < kWords; i += 8)
-        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
-                     ::"l"(reinterpret_cast<uint32_t*>(p) + i), "r"(w[i]), "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]),
-                       "r"(w[i + 4]), "r"(w[i + 5]), "r"(w[i + 6]), "r"(w[i + 7]) : "memory");
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (y0 + i < a.ny) put(p + place(a, a.out_pitch, x, y0 + i), v[i]);
-    }
+    for (int i = 0; i < N; ++i)
+      v[i] += sizeof(T) == 4 ? u2f(add[i]) : u2f(i & 1 ? add[i >> 1] & 0xFFFF0000u : add[i >> 1] << 16);
   }
 };
+
+// Outputs element by element: any place, any alignment, `swap` or not.
+template <typename T, int N>
+__device__ __forceinline__ void store_each(const MatmulArgs& a, int x, int y0, const float (&v)[N]) {
+  if (x >= a.nx) return;
+  T* p = static_cast<T*>(a.out);
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (y0 + i < a.ny) put(p + place(a, a.out_pitch, x, y0 + i), v[i]);
+}
+
+// A warp's 32 rows of 64 bytes, by TMA from its 2 KB of shared memory (64-byte
+// swizzle: 16-byte pieces turned by half the row, so that neither side meets
+// bank conflicts).  Rows beyond the matrix are left out by the copy; columns would
+// be only in pieces of 16 bytes, so a row's ragged end is stored by element.
+// 8192 x 2304 x 768 took 18.0 us with each lane storing its own row in 32-byte
+// pieces, 16.6 this way; 1024 x 4096 x 8191 to fp32 32.7 and 31.3.
+template <typename T, int N>
+__device__ __forceinline__ void store_staged(const CUtensorMap* map, uint32_t buffer, int lane, int row0, int col0,
+                                             bool exists, const float (&v)[N]) {
+  static_assert(N * sizeof(T) == 64, "a row of the buffer");
+  uint32_t w[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    if constexpr (sizeof(T) == 4) w[i] = f2u(v[i]);
+    else w[i] = bf16_pair(v[2 * i], v[2 * i + 1]);
+  }
+  // the copy before has read the buffer
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  __syncwarp();
+  const uint32_t row = buffer + 64 * lane, turn = (lane >> 1) & 3;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};"
+                 ::"r"(row + 16 * (i ^ turn)), "r"(w[4 * i]), "r"(w[4 * i + 1]), "r"(w[4 * i + 2]), "r"(w[4 * i + 3])
+                 : "memory");
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+  if (lane == 0 && exists) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
+                 ::"l"(map), "r"(col0), "r"(row0), "r"(buffer) : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+}
 
 // A place in the ring: its stage, the phase of its barriers, and whether the ring
 // is still in its first turn.
@@ -314,7 +345,7 @@ template <typename T, int CG, int NT>
 __global__ void __launch_bounds__(kThreads, 1)
 matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_y,
               const __grid_constant__ CUtensorMap map_sx, const __grid_constant__ CUtensorMap map_sy,
-              const __grid_constant__ MatmulArgs a) {
+              const __grid_constant__ CUtensorMap map_out, const __grid_constant__ MatmulArgs a) {
   using L = Layout<CG, NT>;
   constexpr int S = L::kStages;
   extern __shared__ uint8_t raw[];
@@ -350,8 +381,8 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     *failed = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 3 && lane < 4) {
-    const CUtensorMap* maps[4] = {&map_x, &map_y, &map_sx, &map_sy};
+  if (warp == 3 && lane < 5) {
+    const CUtensorMap* maps[5] = {&map_x, &map_y, &map_sx, &map_sy, &map_out};
     asm volatile("prefetch.tensormap [%0];" ::"l"(maps[lane]) : "memory");
   }
   if (warp == 2) {
@@ -482,23 +513,27 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     // --------------------------------------------------------------- output
     // C columns at a time; `half` 0 takes the first NT / 2 columns (all 16 of the
     // narrowest tile), 1 the others
-    constexpr int C = NT >= 64 ? 32 : 16, kCols = NT == 16 ? 16 : NT / 2;
+    constexpr int C = L::template kOutCols<T>, kCols = NT == 16 ? 16 : NT / 2;
     const bool joined = CG == 1 && a.split > 1;
     const int q = warp & 3, half = (warp - 4) >> 2;      // this warp's 32 lanes of tensor memory
     const int chunks = NT == 16 && half == 1 ? 0 : kCols / C;
-    const uint32_t free_at = CG == 2 ? map_to(free_, 0) : free_;
+    const uint32_t free_at = CG == 2 ? map_to(free_, 0) : free_, buffer = ring + L::kOutAt + (warp - 4) * 2048;
     int i = 0;
     for (int t = first; t < tiles; t += step, ++i) {
       int tx, ty;
       tile_at(a, t, tx, ty);
-      const int x = (tx * CG + (CG == 2 ? (int)rank : 0)) * 128 + q * 32 + lane, y0 = ty * NT;
+      const int x0 = (tx * CG + (CG == 2 ? (int)rank : 0)) * 128 + q * 32, x = x0 + lane, y0 = ty * NT;
       // The shared columns first: the first accumulator's last ones, the second
       // one's first.  The half that has none frees them at once: what it
       // stands for is that it has read the tile before.
       const bool down = L::kOverlap && (i & 1) == 0;
       const bool shares = L::kOverlap && half == (down ? 1 : 0);
       const auto column = [&](int j) { return half * kCols + (down ? kCols - C - j * C : j * C); };
-      if (L::kOverlap && !shares && lane == 0) bar_arrive_cluster(free_at);
+      if (L::kOverlap && !shares) {
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive_cluster(free_at);
+      }
       Outputs<T, C> o[2];
       if (!joined && chunks > 0) o[0].load(a, x, y0 + column(0));
       if (!warp_wait(done + 8 * (i & 1), (uint32_t)(i >> 1) & 1u, a.wait_ns)) {
@@ -514,13 +549,20 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         if (!joined && j + 1 < chunks) o[(j + 1) & 1].load(a, x, y0 + column(j + 1));
         float v[C];
         acc_load<C>(acc + c, v);
-        if (shares && j == 0) {
+        // read: the shared 24 columns, or the whole tile
+        if (L::kOverlap ? shares && j == 32 / C - 1 : j == chunks - 1) {
           fence_before();
           __syncwarp();
-          if (lane == 0) bar_arrive_cluster(free_at);
+          if (lane == 0) bar_arrive_cluster(L::kOverlap ? free_at : free_at + 8 * (i & 1));
         }
         if (!joined) {
-          o[j & 1].store(a, x, y0 + c, v);
+          o[j & 1].sum(a, x, v);
+          if constexpr (C * sizeof(T) == 64) {
+            if (a.staged && y0 + c + C <= a.ny) store_staged<T>(&map_out, buffer, lane, x0, y0 + c, x0 < a.nx, v);
+            else store_each<T>(a, x, y0 + c, v);
+          } else {
+            store_each<T>(a, x, y0 + c, v);
+          }
         } else {
           float* part = reinterpret_cast<float*>(smem);
           if (a.swap) {
@@ -534,12 +576,10 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
           }
         }
       }
-      if (!L::kOverlap) {
-        fence_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive_cluster(free_at + 8 * (i & 1));
-      }
+      if (chunks == 0 && lane == 0) bar_arrive_cluster(free_at + 8 * (i & 1));
     }
+    // the last copy has read the buffer; what it writes is complete when the grid is
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   }
 
   __syncwarp();
@@ -644,6 +684,18 @@ bool scales_map(CUtensorMap* m, const void* p, int64_t tiles) {
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// out, in boxes of 64 bytes by 32 rows, 64-byte swizzle
+template <typename T>
+bool out_map(CUtensorMap* m, const MatmulArgs& a) {
+  const int64_t es = sizeof(T);
+  const cuuint64_t dims[2] = {(cuuint64_t)a.ny, (cuuint64_t)a.nx};
+  const cuuint64_t strides[1] = {(cuuint64_t)(a.nx > 1 ? a.out_pitch * es : (a.ny * es + 15) / 16 * 16)};
+  const cuuint32_t boxes[2] = {(cuuint32_t)(64 / es), 32}, ones[2] = {1, 1};
+  return encode_fn()(m, es == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.out, dims,
+                     strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                     CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 struct Operand {
   const void* codes;
   const void* scales;
@@ -663,12 +715,16 @@ cudaError_t launch(const Operand& x, const Operand& y, int64_t k, MatmulArgs a, 
   a.x_tiles = (int)xt;
   a.y_tiles = (int)yt;
   a.split = split;
-  CUtensorMap mx, my, msx, msy;
+  // rows of 64 bytes by TMA: 16-byte aligned rows of out, as they lie in it
+  a.staged = NT >= 64 && !a.swap && split == 1 && ((uintptr_t)a.out & 15u) == 0 &&
+             (x.rows == 1 || a.out_pitch * (int64_t)sizeof(T) % 16 == 0);
+  CUtensorMap mx, my, msx, msy, mo;
   if (encode_fn() == nullptr || !codes_map(&mx, x.codes, k, x.rows, x.pitch, 128) ||
       !codes_map(&my, y.codes, k, y.rows, y.pitch, L::kY) ||
       !scales_map(&msx, x.scales, (x.rows + 127) / 128 * a.panel) ||
-      !scales_map(&msy, y.scales, (y.rows + 127) / 128 * a.panel))
+      !scales_map(&msy, y.scales, (y.rows + 127) / 128 * a.panel) || (a.staged && !out_map<T>(&mo, a)))
     return cudaErrorInvalidValue;
+  if (!a.staged) mo = mx;      // not used
   const int per = CG == 2 ? 2 : split;
   const int64_t tiles = xt * yt, slots = sm_count / per;
   cudaLaunchConfig_t cfg = {};
@@ -683,25 +739,26 @@ cudaError_t launch(const Operand& x, const Operand& y, int64_t k, MatmulArgs a, 
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = per > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, matmul_kernel<T, CG, NT>, mx, my, msx, msy, a);
+  return cudaLaunchKernelEx(&cfg, matmul_kernel<T, CG, NT>, mx, my, msx, msy, mo, a);
 }
 
 // Which operand is x, the tile (128 or, by a pair of CTAs, 256 rows of x, nt of
-// y) and the split, by the estimated time: the blocks that one CTA goes through
-// times a block's time, plus each tile's and each split's own.  A split's CTAs
-// take one tile each, so a second wave of them starts anew.  The times are fits
-// to runs of one shape in each form, in ns: 256 x 4096 x 4096 takes 9.4 us in
-// 128-wide tiles, 9.5 in pairs of 128, 14.4 in pairs of 256, 12.2 split in two;
-// 64 x 4096 x 4096 9.0 whole, 8.3 split in four; 8192 x 14336 x 4096 418 in
-// pairs of 128, 285 in pairs of 256.
+// y) and the split, by the estimated time: the tiles that one CTA goes through,
+// each its blocks' time (but no less than its output takes) and its own, plus a
+// pair's start or a split's sum.  A split's CTAs take one tile each, so a second
+// wave of them starts anew.  The times are fits, in ns, to one shape in several
+// forms: 256 x 4096 x 4096 takes 9.8 us in 128-wide tiles, 10.1 in pairs of 128,
+// 14.2 in pairs of 256 and 12.2 split in two; 2048 x 4096 x 4096 31.8, 27.4 and
+// 25.5; 8192 x 2304 x 768 22.8, 22.2 and 16.6; 64 x 4096 x 4096 9.0 whole, 8.3
+// split in four.
 struct Plan {
   int swap, cg, nt, split;
 };
 Plan plan(int64_t m, int64_t n, int blocks, int sm_count) {
-  static const struct { int cg, nt, block, tile, split; } kForms[] = {
-      {1, 16, 155, 500, 2300}, {1, 32, 165, 500, 2500},  {1, 64, 185, 500, 3300},
-      {1, 128, 208, 500, 6200}, {2, 128, 175, 1300, 0}, {2, 256, 320, 1300, 0}};
-  constexpr double kStart = 3500;
+  static const struct { int cg, nt, block, least, tile, split; } kForms[] = {
+      {1, 16, 155, 1000, 400, 2300}, {1, 32, 165, 1000, 400, 2500},   {1, 64, 185, 1500, 400, 3300},
+      {1, 128, 208, 2000, 400, 6200}, {2, 128, 175, 2000, 400, 0}, {2, 256, 320, 1900, 900, 0}};
+  constexpr double kStart = 3500, kPair = 800;
   Plan best = {0, 2, 256, 1};
   double least = 1e300;
   const int panel = (blocks + 3) / 4;
@@ -713,8 +770,9 @@ Plan plan(int64_t m, int64_t n, int blocks, int sm_count) {
       const int64_t tiles = ((xr + 128 * f.cg - 1) / (128 * f.cg)) * ((yr + f.nt - 1) / f.nt);
       for (int split = 1; split <= (f.cg == 2 ? 1 : 8) && split <= panel; split *= 2) {
         const int64_t slots = sm_count / (f.cg == 2 ? 2 : split), waves = (tiles + slots - 1) / slots;
-        double time = (double)waves * ((blocks + split - 1) / split) * f.block;
-        time += split == 1 ? (double)waves * f.tile : (double)waves * f.split + (double)(waves - 1) * kStart;
+        const double each = (double)((blocks + split - 1) / split) * f.block, out = waves > 1 ? f.least : 0;
+        double time = (double)waves * ((each > out ? each : out) + f.tile) + (f.cg == 2 ? kPair : 0);
+        if (split > 1) time += (double)waves * f.split + (double)(waves - 1) * kStart;
         if (time < least) {
           least = time;
           best = {swap, f.cg, f.nt, split};
@@ -734,7 +792,7 @@ cudaError_t dispatch(const opt_matmul_args& c, int sm_count, cudaStream_t s) {
   const auto fits = [&](const void* p, int64_t pitch) {
     return ((uintptr_t)p & 31u) == 0 && (c.m == 1 || pitch * (int64_t)sizeof(T) % 32 == 0);
   };
-  a.vec = fits(c.d_out, c.out_pitch) && (c.d_addend == nullptr || fits(c.d_addend, c.addend_pitch));
+  a.vec = c.d_addend != nullptr && fits(c.d_addend, c.addend_pitch);
   if (c.k == 0) {
     a.nx = (int)c.m;
     a.ny = (int)c.n;

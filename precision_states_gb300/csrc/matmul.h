@@ -13,7 +13,7 @@ struct OutputArgs {
   const void* addend;
   int64_t out_pitch, addend_pitch;
   int swap;
-  int vec;                   // rows of out and addend allow 32-byte accesses
+  int vec;                   // rows of addend allow 32-byte loads
 };
 
 __device__ __forceinline__ float element(const Bf16* p) { return u2f((uint32_t)p->bits << 16); }

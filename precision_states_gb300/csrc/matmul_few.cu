@@ -8,9 +8,15 @@
 // g of the short operand.  Both sides use the same permutation of the depth, so
 // the loaded words are the fragments of mma.sync m16n8k32 as they are; at eight
 // columns the product is far from any tensor peak, and tcgen05's way through
-// shared memory writes and reads 128 rows of bytes per instruction.  A block of
-// 128 is summed with no scale, then added to the fp32 sum with both scales.  A
-// CTA's warps share the depth of its 16 rows; their sums are added in order.
+// shared memory and tensor memory only adds latency (1 x 4096 x 4096: 4.7 us
+// here, 6.9 there; 1 x 14336 x 4096: 12.1 and 13.3).  A block of 128 is summed
+// with no scale, then added to the fp32 sum with both scales.  A CTA's warps
+// share the depth of its 16 rows; their sums are added in order.
+//
+// Bound by the weight's bytes once they are many (1 x 57344 x 4096: 38.7 us, 6.1
+// TB/s, 0.92 of the measured copy), by launch and one wave's latency before.
+// 512 of the depth per step at two CTAs per SM took 17.7 us instead of 12.1, and
+// the next step's loads ahead of this step's products 15.2.
 #include "layer.cuh"
 #include "matmul.h"
 
