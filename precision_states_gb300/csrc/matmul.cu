@@ -52,7 +52,8 @@ struct MatmulArgs : OutputArgs {
   int blocks;                // ceil(k / 128)
   int panel;                 // scale tiles per 128 rows: ceil(blocks / 4)
   int split;                 // CTAs per cluster along the depth (CG 1)
-  int staged;                // whole warps' outputs leave through shared memory
+  int staged;                // whole warps' outputs leave through shared memory (NT 256)
+  int vec_out;               // rows of out allow 32-byte stores
   int drill;                 // load nothing, so that the waits run out
   unsigned long long wait_ns;   // limit of each wait
 };
@@ -74,10 +75,11 @@ struct Layout {
   static constexpr int kNeed = kScaleCol + 2 * kScaleCols;
   static constexpr int kCols = kNeed <= 64 ? 64 : kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
   static constexpr int kBars = 2 * kStages + 5;      // full, empty, done[2], free[2], drain
-  // columns that an output warp takes at a time: from NT 64 on, 64 bytes of out
+  // columns that an output warp takes at a time (of the widest tile 64 bytes, by
+  // way of shared memory)
   template <typename T>
-  static constexpr int kOutCols = NT >= 64 ? 64 / (int)sizeof(T) : 16;
-  static constexpr int kOutBytes = NT >= 64 ? kOutWarps * 32 * 64 : 0;
+  static constexpr int kOutCols = NT == 256 ? 64 / (int)sizeof(T) : NT >= 64 ? 32 : 16;
+  static constexpr int kOutBytes = NT == 256 ? kOutWarps * 32 * 64 : 0;
   // dynamic shared memory: ring | scales | output | barriers, tensor memory address, failure
   static constexpr int kScaleAt = kStages * kStage;
   static constexpr int kOutAt = kScaleAt + kStages * kScaleBytes;
@@ -271,22 +273,41 @@ struct Outputs {
   }
 };
 
-// Outputs element by element: any place, any alignment, `swap` or not.
+// Each lane's outputs by itself: in 32-byte stores (a sector each) where rows of
+// out allow them, else element by element, in any place.
 template <typename T, int N>
 __device__ __forceinline__ void store_each(const MatmulArgs& a, int x, int y0, const float (&v)[N]) {
   if (x >= a.nx) return;
   T* p = static_cast<T*>(a.out);
+  if (a.vec_out && !a.swap && y0 + N <= a.ny) {
+    constexpr int kWords = N * (int)sizeof(T) / 4;
+    uint32_t w[kWords];
 #pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (y0 + i < a.ny) put(p + place(a, a.out_pitch, x, y0 + i), v[i]);
+    for (int i = 0; i < kWords; ++i) {
+      if constexpr (sizeof(T) == 4) w[i] = f2u(v[i]);
+      else w[i] = bf16_pair(v[2 * i], v[2 * i + 1]);
+    }
+    uint32_t* q = reinterpret_cast<uint32_t*>(p + place(a, a.out_pitch, x, y0));
+#pragma unroll
+    for (int i = 0; i < kWords; i += 8)
+      asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                   ::"l"(q + i), "r"(w[i]), "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]), "r"(w[i + 5]),
+                     "r"(w[i + 6]), "r"(w[i + 7]) : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (y0 + i < a.ny) put(p + place(a, a.out_pitch, x, y0 + i), v[i]);
+  }
 }
 
 // A warp's 32 rows of 64 bytes, by TMA from its 2 KB of shared memory (64-byte
 // swizzle: 16-byte pieces turned by half the row, so that neither side meets
 // bank conflicts).  Rows beyond the matrix are left out by the copy; columns would
 // be only in pieces of 16 bytes, so a row's ragged end is stored by element.
-// 8192 x 2304 x 768 took 18.0 us with each lane storing its own row in 32-byte
-// pieces, 16.6 this way; 1024 x 4096 x 8191 to fp32 32.7 and 31.3.
+// For the widest tile, whose lines a warp leaves in four or eight pieces: 8192 x
+// 2304 x 768 took 18.0 us with each lane storing its own row, 16.6 this way;
+// 1024 x 4096 x 8191 to fp32 32.7 and 31.3.  Narrower tiles gain nothing: 256 x
+// 4096 x 4096 in tiles of 128 took 9.7 us by lanes, 9.8 this way.
 template <typename T, int N>
 __device__ __forceinline__ void store_staged(const CUtensorMap* map, uint32_t buffer, int lane, int row0, int col0,
                                              bool exists, const float (&v)[N]) {
@@ -381,7 +402,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     *failed = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 3 && lane < 5) {
+  if (warp == 3 && lane < (L::kOutBytes > 0 ? 5 : 4)) {
     const CUtensorMap* maps[5] = {&map_x, &map_y, &map_sx, &map_sy, &map_out};
     asm volatile("prefetch.tensormap [%0];" ::"l"(maps[lane]) : "memory");
   }
@@ -557,7 +578,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         }
         if (!joined) {
           o[j & 1].sum(a, x, v);
-          if constexpr (C * sizeof(T) == 64) {
+          if constexpr (L::kOutBytes > 0) {
             if (a.staged && y0 + c + C <= a.ny) store_staged<T>(&map_out, buffer, lane, x0, y0 + c, x0 < a.nx, v);
             else store_each<T>(a, x, y0 + c, v);
           } else {
@@ -579,7 +600,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
       if (chunks == 0 && lane == 0) bar_arrive_cluster(free_at + 8 * (i & 1));
     }
     // the last copy has read the buffer; what it writes is complete when the grid is
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    if (L::kOutBytes > 0 && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   }
 
   __syncwarp();
@@ -716,7 +737,7 @@ cudaError_t launch(const Operand& x, const Operand& y, int64_t k, MatmulArgs a, 
   a.y_tiles = (int)yt;
   a.split = split;
   // rows of 64 bytes by TMA: 16-byte aligned rows of out, as they lie in it
-  a.staged = NT >= 64 && !a.swap && split == 1 && ((uintptr_t)a.out & 15u) == 0 &&
+  a.staged = NT == 256 && ((uintptr_t)a.out & 15u) == 0 &&
              (x.rows == 1 || a.out_pitch * (int64_t)sizeof(T) % 16 == 0);
   CUtensorMap mx, my, msx, msy, mo;
   if (encode_fn() == nullptr || !codes_map(&mx, x.codes, k, x.rows, x.pitch, 128) ||
@@ -793,6 +814,7 @@ cudaError_t dispatch(const opt_matmul_args& c, int sm_count, cudaStream_t s) {
     return ((uintptr_t)p & 31u) == 0 && (c.m == 1 || pitch * (int64_t)sizeof(T) % 32 == 0);
   };
   a.vec = c.d_addend != nullptr && fits(c.d_addend, c.addend_pitch);
+  a.vec_out = fits(c.d_out, c.out_pitch);
   if (c.k == 0) {
     a.nx = (int)c.m;
     a.ny = (int)c.n;
