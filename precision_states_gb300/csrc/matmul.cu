@@ -27,6 +27,14 @@
 // Splits.  With few tiles, the depth is split over a cluster of CTAs; their
 // accumulators are summed through distributed shared memory in rank order.
 //
+// Bound: 8192 x 14336 x 4096 takes 272 us alone (3.53 PFLOP/s; tensor pipe 87 %
+// busy) and 316 us in a loop, where the 1,360 W cap holds the clock at 1,490 MHz.
+// The same loop with no loads takes 227 us: a pair's 256 x 256 tile brings 33 KB
+// to each SM per block, about what its path from L2 carries in the products' time,
+// and a tile's end costs the next one about 1 us.  Few tiles are latency: about 3
+// us of launch and first loads, then a block's time each (0.16 us of a 16-wide
+// tile to 0.32 of a pair's 256).
+//
 // Every wait is bounded (by the global timer): one that runs out raises
 // OPT_FLAG_WAIT_TIMEOUT (opt_layer_status), and the CTA leaves after its copies
 // and products in flight have ended.

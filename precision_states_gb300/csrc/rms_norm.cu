@@ -7,7 +7,22 @@
 // thread holding NG chunks of eight elements; a CTA goes through many rows, so
 // that the weight (and the weight's gradient) stay in registers too, and the
 // next row's loads are issued before the current row's sum is complete.  Rows
-// too wide for that take a second form that reads them twice.
+// too wide for that (over 16,384 columns, 8,192 in the backward pass) take a
+// second form that reads them twice.
+//
+// Sums over a row, rstd and the weight's gradient are fp32 throughout; outputs are
+// rounded once.  rstd is rsqrtf, within 2 units in the last place.
+//
+// Forward, 16384 x 4096 BF16 with a residual to h and codes: 72.3 us without
+// dropout, 6.5 TB/s (0.97 of the measured copy), bound by memory; 87.6 us with it
+// (0.80), bound by the generator's integer work (267 instructions per eight
+// elements, issue 65 % busy).  Two chunks per thread at 256 threads and three CTAs
+// per SM: one chunk at 512 threads took 98.3 us, four at 128 threads 108.7, four
+// CTAs per SM 87.1 (but 79.7 without dropout).  Backward, 8192 x 4096 BF16 with
+// dh_in, dropout and the weight's gradient: 58.5 us (0.86), of which the sum over
+// the CTAs' rows takes 4; one chunk per thread at 512 threads and two CTAs per SM,
+// one CTA for fp32 (its rows take twice the registers).  Few rows are launches'
+// latency: one token of 4,096 2.6 us.
 #include "layer.cuh"
 
 namespace psopt {
