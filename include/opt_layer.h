@@ -126,7 +126,7 @@ int opt_rms_norm(const opt_rms_norm_args* a, void* stream);
  * in fp32, each rounded once (dx from dh before its rounding).  d_dh may be d_dy
  * or d_dh_in (same pointer and pitch).  The sum over rows runs in a fixed order;
  * it needs d_workspace of opt_rms_norm_backward_workspace(rows, cols) bytes,
- * 16-byte aligned, when d_dweight is given. */
+ * 16-byte aligned, when d_dweight is given (none for few rows: 0 bytes). */
 typedef struct opt_rms_norm_backward_args {
   const void* d_dy;
   const void* d_h;

@@ -109,8 +109,7 @@ int opt_rms_norm(const opt_rms_norm_args* a, void* stream) {
 int64_t opt_rms_norm_backward_workspace(int64_t rows, int64_t cols) {
   const int st = check_sizes(rows, cols);
   if (st != OPT_OK) return st;
-  const int64_t parts = rows < kNormBackwardMaxCtas ? rows : kNormBackwardMaxCtas;
-  return parts * ((cols + 3) / 4 * 4) * (int64_t)sizeof(float);
+  return norm_backward_parts(rows, cols) * ((cols + 3) / 4 * 4) * (int64_t)sizeof(float);
 }
 
 int opt_rms_norm_backward(const opt_rms_norm_backward_args* a, void* stream) {
@@ -134,9 +133,9 @@ int opt_rms_norm_backward(const opt_rms_norm_backward_args* a, void* stream) {
   PS_TRY(check_matrix(a->d_dh, a->dh_pitch, a->rows, a->cols, es));
   if (a->d_dh_in != nullptr) PS_TRY(check_matrix(a->d_dh_in, a->dh_in_pitch, a->rows, a->cols, es));
   if (a->d_dx != nullptr) PS_TRY(check_matrix(a->d_dx, a->dx_pitch, a->rows, a->cols, es));
-  if (a->d_dweight != nullptr) {
-    if (a->d_workspace == nullptr || a->workspace_bytes < opt_rms_norm_backward_workspace(a->rows, a->cols))
-      return OPT_EINVAL;
+  const int64_t need = opt_rms_norm_backward_workspace(a->rows, a->cols);
+  if (a->d_dweight != nullptr && need > 0) {
+    if (a->d_workspace == nullptr || a->workspace_bytes < need) return OPT_EINVAL;
     if ((uintptr_t)a->d_workspace & 15u) return OPT_EALIGN;
   }
   int sms = 0;

@@ -57,6 +57,8 @@ __device__ __forceinline__ void unpack(const Raw<Bf16>& r, float (&x)[8]) {
     x[2 * k + 1] = u2f(r.w[k] & 0xFFFF0000u);
   }
 }
+__device__ __forceinline__ float element(const Bf16* p) { return u2f((uint32_t)p->bits << 16); }
+__device__ __forceinline__ float element(const float* p) { return *p; }
 template <bool VEC, typename T>
 __device__ __forceinline__ void load8(const T* p, int valid, float (&x)[8]) {
   unpack(load_raw<VEC>(p, valid), x);

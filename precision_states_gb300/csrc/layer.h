@@ -31,5 +31,11 @@ cudaError_t layer_flags(int* flags, cudaStream_t s);      // read and clear
 // CTAs of the backward norm, and so rows of its weight-gradient partial sums:
 // never more than this, whatever the device.
 constexpr int64_t kNormBackwardMaxCtas = 1024;
+// Rows of partial sums that the workspace holds; 0 where the weight's gradient is
+// formed without them, by CTAs of the same launch that read dy and h again: up to
+// 512 rows and 2^21 elements.
+__host__ __device__ constexpr inline int64_t norm_backward_parts(int64_t rows, int64_t cols) {
+  return rows <= 512 && rows * cols <= ((int64_t)1 << 21) ? 0 : rows < kNormBackwardMaxCtas ? rows : kNormBackwardMaxCtas;
+}
 
 }  // namespace psopt

@@ -16,8 +16,6 @@ struct OutputArgs {
   int vec;                   // rows of addend allow 32-byte loads
 };
 
-__device__ __forceinline__ float element(const Bf16* p) { return u2f((uint32_t)p->bits << 16); }
-__device__ __forceinline__ float element(const float* p) { return *p; }
 __device__ __forceinline__ void put(Bf16* p, float v) { p->bits = (uint16_t)bf16_pair(v, 0.0f); }
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 

@@ -7,8 +7,7 @@
 // thread holding NG chunks of eight elements; a CTA goes through many rows, so
 // that the weight (and the weight's gradient) stay in registers too, and the
 // next row's loads are issued before the current row's sum is complete.  Rows
-// too wide for that (over 16,384 columns, 8,192 in the backward pass) take a
-// second form that reads them twice.
+// too wide for that (over 16,384 columns) take a second form that reads them twice.
 //
 // Sums over a row, rstd and the weight's gradient are fp32 throughout; outputs are
 // rounded once.  rstd is rsqrtf, within 2 units in the last place.
@@ -29,7 +28,7 @@ namespace psopt {
 namespace {
 
 constexpr int kWideThreads = 512;       // of the form that reads rows twice
-constexpr int kDweightCols = 32, kDweightParts = 32;
+constexpr int kDweightCols = 32, kDweightParts = 32, kSlabCols = 16;
 
 // Chunk c (eight elements) of row r of h = residual + dropout(x).
 template <typename T, bool VEC>
@@ -179,10 +178,59 @@ __device__ __forceinline__ float* dweight_row(const opt_rms_norm_backward_args& 
   return static_cast<float*>(a.d_workspace) + part * ((a.cols + 3) / 4 * 4);
 }
 
+__host__ __device__ __forceinline__ bool dweight_here(const opt_rms_norm_backward_args& a) {
+  return norm_backward_parts(a.rows, a.cols) == 0;
+}
+
+// dweight needs no row's sum, so few rows' is formed from dy, h and rstd again (they
+// are in L2) by CTAs of the same launch: no second launch, no workspace.  (Where dh
+// takes dy's place they run in a launch of their own, before.)  CTA `slab` takes
+// 16 columns; its half-warps share the rows in turn, and their sums are added in
+// order.
+template <typename T>
+__device__ __forceinline__ void dweight_slab(const opt_rms_norm_backward_args& a, int slab) {
+  __shared__ float sums[kWideThreads / 32][kSlabCols];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int64_t c = (int64_t)slab * kSlabCols + (lane & (kSlabCols - 1));
+  float s = 0.0f;
+  if (c < a.cols) {
+    const T* dy = static_cast<const T*>(a.d_dy) + c;
+    const T* h = static_cast<const T*>(a.d_h) + c;
+    const int rows = (int)a.rows;
+    const int of = 2 * warps;
+    for (int r0 = 2 * warp + (lane >> 4); r0 < rows; r0 += 8 * of) {      // eight rows' loads together
+      float g[8] = {}, v[8] = {}, scale[8] = {};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int r = r0 + k * of;
+        if (r < rows) {
+          g[k] = element(dy + r * a.dy_pitch);
+          v[k] = element(h + r * a.h_pitch);
+          scale[k] = a.d_rstd[r];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s = fmaf(g[k], v[k] * scale[k], s);
+    }
+  }
+  s += __shfl_xor_sync(0xFFFFFFFFu, s, 16);
+  if (lane < kSlabCols) sums[warp][lane] = s;
+  __syncthreads();
+  if (threadIdx.x >= kSlabCols || c >= a.cols) return;
+  for (int w = 1; w < warps; ++w) s += sums[w][lane];
+  a.d_dweight[c] = s;
+}
+
+// CTAs from `row_ctas` on are dweight's slabs.  With four chunks per thread the
+// registers hold neither the weight nor the next row (AHEAD false).
 template <typename T, typename W, bool VEC, int NG, int MAX, int CTAS>
 __global__ void __launch_bounds__(MAX, CTAS) rms_norm_backward_kernel(
-    const __grid_constant__ opt_rms_norm_backward_args a, const __grid_constant__ DropArgs d) {
+    const __grid_constant__ opt_rms_norm_backward_args a, const __grid_constant__ DropArgs d, int row_ctas) {
   __shared__ float part[2][33];
+  if ((int)blockIdx.x >= row_ctas) {
+    dweight_slab<T>(a, (int)blockIdx.x - row_ctas);
+    return;
+  }
   const int warps = blockDim.x >> 5;
   const float inv_cols = 1.0f / (float)a.cols;
   const int cols = (int)a.cols;
@@ -191,30 +239,37 @@ __global__ void __launch_bounds__(MAX, CTAS) rms_norm_backward_kernel(
   float dw[NG][8] = {};
   Raw<W> w[NG] = {};
   Raw<T> dy[NG] = {}, h[NG] = {}, in[NG] = {};
+  constexpr bool AHEAD = NG < 4;
   const auto load = [&](int k, int64_t r) {
     dy[k] = load_raw<VEC>(static_cast<const T*>(a.d_dy) + r * a.dy_pitch + column(k), valid(k));
     h[k] = load_raw<VEC>(static_cast<const T*>(a.d_h) + r * a.h_pitch + column(k), valid(k));
   };
 #pragma unroll
   for (int k = 0; k < NG; ++k) {
-    if (valid(k) > 0) {
+    if (AHEAD && valid(k) > 0) {
       load(k, blockIdx.x);
       w[k] = load_raw<VEC>(static_cast<const W*>(a.d_weight) + column(k), valid(k));
     }
   }
   int turn = 0;
-  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, turn ^= 1) {
+  for (int64_t r = blockIdx.x; r < a.rows; r += row_ctas, turn ^= 1) {
     const float rstd = a.d_rstd[r];
     float g[NG][8], hv[NG][8], sum = 0.0f;
+    if (!AHEAD) {
+#pragma unroll
+      for (int k = 0; k < NG; ++k)
+        if (valid(k) > 0) load(k, r);
+    }
 #pragma unroll
     for (int k = 0; k < NG; ++k) {
       float wv[8];
+      if (!AHEAD && valid(k) > 0) w[k] = load_raw<VEC>(static_cast<const W*>(a.d_weight) + column(k), valid(k));
       unpack(dy[k], g[k]);
       unpack(h[k], hv[k]);
       unpack(w[k], wv);
-      if (a.d_dh_in != nullptr && valid(k) > 0)
+      if (AHEAD && a.d_dh_in != nullptr && valid(k) > 0)
         in[k] = load_raw<VEC>(static_cast<const T*>(a.d_dh_in) + r * a.dh_in_pitch + column(k), valid(k));
-      if (valid(k) > 0 && r + gridDim.x < a.rows) load(k, r + gridDim.x);
+      if (AHEAD && valid(k) > 0 && r + row_ctas < a.rows) load(k, r + row_ctas);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         dw[k][j] = fmaf(g[k][j], hv[k][j] * rstd, dw[k][j]);
@@ -228,11 +283,13 @@ __global__ void __launch_bounds__(MAX, CTAS) rms_norm_backward_kernel(
     for (int k = 0; k < NG; ++k)
       if (valid(k) > 0) {
         float add[8];
+        if (!AHEAD && a.d_dh_in != nullptr)
+          in[k] = load_raw<VEC>(static_cast<const T*>(a.d_dh_in) + r * a.dh_in_pitch + column(k), valid(k));
         unpack(in[k], add);
         write_gradients<T, VEC>(a, d, r, column(k), valid(k), rstd, scale, g[k], hv[k], add);
       }
   }
-  if (a.d_dweight != nullptr) {
+  if (a.d_dweight != nullptr && !dweight_here(a)) {
     float* out = dweight_row(a, blockIdx.x);
 #pragma unroll
     for (int k = 0; k < NG; ++k)
@@ -252,11 +309,15 @@ __global__ void __launch_bounds__(MAX, CTAS) rms_norm_backward_kernel(
 // Wide rows, read twice; each column of the partial sums belongs to one thread.
 template <typename T, typename W, bool VEC>
 __global__ void __launch_bounds__(kWideThreads) rms_norm_backward_wide_kernel(
-    const __grid_constant__ opt_rms_norm_backward_args a, const __grid_constant__ DropArgs d) {
+    const __grid_constant__ opt_rms_norm_backward_args a, const __grid_constant__ DropArgs d, int row_ctas) {
   __shared__ float part[2][33];
-  float* dw = a.d_dweight == nullptr ? nullptr : dweight_row(a, blockIdx.x);
+  if ((int)blockIdx.x >= row_ctas) {
+    dweight_slab<T>(a, (int)blockIdx.x - row_ctas);
+    return;
+  }
+  float* dw = a.d_dweight == nullptr || dweight_here(a) ? nullptr : dweight_row(a, blockIdx.x);
   int turn = 0;
-  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, turn ^= 1) {
+  for (int64_t r = blockIdx.x; r < a.rows; r += row_ctas, turn ^= 1) {
     const T* dy_row = static_cast<const T*>(a.d_dy) + r * a.dy_pitch;
     const T* h_row = static_cast<const T*>(a.d_h) + r * a.h_pitch;
     float sum = 0.0f, g[8], h[8], w[8];
@@ -354,14 +415,28 @@ cudaError_t forward(const opt_rms_norm_args& a, const DropArgs& d, int sm_count,
   return v.ok ? forward_vec<T, W, true>(a, d, sm_count, s) : forward_vec<T, W, false>(a, d, sm_count, s);
 }
 
+// CTAs of dweight's slabs, in the launch of the rows.
+unsigned slabs(const opt_rms_norm_backward_args& a) {
+  return a.d_dweight != nullptr && dweight_here(a) ? (unsigned)((a.cols + kSlabCols - 1) / kSlabCols) : 0u;
+}
+
+template <typename K>
+void launch_backward(K kernel, const opt_rms_norm_backward_args& a, const DropArgs& d, int grid, int threads,
+                     cudaStream_t s) {
+  const bool apart = slabs(a) > 0 && a.d_dh == a.d_dy;
+  if (apart) kernel<<<slabs(a), threads, 0, s>>>(a, d, 0);
+  kernel<<<grid + (apart ? 0u : slabs(a)), threads, 0, s>>>(a, d, grid);
+}
+
 template <typename T, typename W, bool VEC, int NG, int MAX, int CTAS>
 int backward_rows(const opt_rms_norm_backward_args& a, const DropArgs& d, int sm_count, int threads, cudaStream_t s) {
   static OccupancyCache cache[33];
-  int64_t most = (int64_t)sm_count *
-                 cached_occupancy(rms_norm_backward_kernel<T, W, VEC, NG, MAX, CTAS>, cache[threads / 32], threads, 0);
+  const auto kernel = rms_norm_backward_kernel<T, W, VEC, NG, MAX, CTAS>;
+  if (slabs(a) > 0) threads = MAX;      // dweight's rows are shared by all warps
+  int64_t most = (int64_t)sm_count * cached_occupancy(kernel, cache[threads / 32], threads, 0);
   if (most > kNormBackwardMaxCtas) most = kNormBackwardMaxCtas;
   const int grid = (int)(a.rows < most ? a.rows : most);
-  rms_norm_backward_kernel<T, W, VEC, NG, MAX, CTAS><<<grid, threads, 0, s>>>(a, d);
+  launch_backward(kernel, a, d, grid, threads, s);
   return grid;
 }
 
@@ -373,12 +448,14 @@ cudaError_t backward_vec(const opt_rms_norm_backward_args& a, const DropArgs& d,
     grid = backward_rows<T, W, VEC, 1, 512, VEC && sizeof(T) == 2 ? 2 : 1>(a, d, sm_count, (int)((chunks + 31) / 32) * 32, s);
   } else if (chunks <= 1024) {
     grid = backward_rows<T, W, VEC, 2, 512, 1>(a, d, sm_count, (int)((chunks + 63) / 64) * 32, s);
+  } else if (chunks <= 2048) {
+    grid = backward_rows<T, W, VEC, 4, 512, 1>(a, d, sm_count, (int)((chunks + 127) / 128) * 32, s);
   } else {
     const int64_t most = (int64_t)sm_count * 4;
     grid = (int)(a.rows < most ? a.rows : most);
-    rms_norm_backward_wide_kernel<T, W, VEC><<<grid, kWideThreads, 0, s>>>(a, d);
+    launch_backward(rms_norm_backward_wide_kernel<T, W, VEC>, a, d, grid, kWideThreads, s);
   }
-  if (a.d_dweight != nullptr)
+  if (a.d_dweight != nullptr && !dweight_here(a))
     dweight_kernel<<<(unsigned)((a.cols + kDweightCols - 1) / kDweightCols), kDweightCols * kDweightParts, 0, s>>>(
         static_cast<const float*>(a.d_workspace), grid, a.cols, a.d_dweight);
   return cudaGetLastError();

@@ -258,12 +258,13 @@ def opt_rms_norm_backward(dy, h, weight, rstd, dh, dh_in=None, dx=None, dweight=
     dq = nq = need = 0
     if dweight is not None:
         dq = _vector(dweight, "dweight", cols, dev, ready.f32)
-        if workspace is None:
-            need = min(rows, 1024) * (-(-cols // 4) * 4) * 4        # opt_rms_norm_backward_workspace
-            workspace = _workspace(need, dev, stream)
-        else:
+        if workspace is not None:
             need = workspace.numel() * workspace.element_size()
-        nq = workspace.data_ptr()
+        elif rows > 512 or rows * cols > 1 << 21:                   # opt_rms_norm_backward_workspace
+            need = min(rows, 1024) * (-(-cols // 4) * 4) * 4
+            workspace = _workspace(need, dev, stream)
+        if need:
+            nq = workspace.data_ptr()
     st = ready.rms_norm_backward(
         _pack_rms_norm_backward(gq, h.data_ptr(), wq, sq, iq, oq, xq, dq, nq, gp, hp, ip, op, xp, need, rows, cols, p,
                                 seed, step, tensor_index, dt, wt, 0),

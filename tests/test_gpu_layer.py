@@ -117,7 +117,7 @@ def norm_reference(x, res, w, p, eps):
 
 
 NORM_SHAPES = [(1, 1, 0), (1, 4096, 0), (3, 8, 0), (2, 127, 0), (5, 129, 3), (67, 768, 0), (130, 769, 0), (9, 2304, 8),
-               (4, 5000, 0), (3, 16384, 0), (2, 33000, 0), (2, 40001, 1), (700, 136, 0)]
+               (4, 5000, 0), (3, 16384, 0), (2, 33000, 0), (2, 40001, 1), (700, 136, 0), (512, 2048, 0), (513, 64, 0), (33, 32001, 0)]
 
 
 @pytest.mark.parametrize("dtype,wdtype", [("bf16", "f32"), ("bf16", "bf16"), ("f32", "f32"), ("f32", "bf16")])
@@ -503,11 +503,12 @@ def test_outputs_in_their_inputs_place(cols):
         ps.opt_rms_norm(ins[0], w, residual=ins[1], h=ins[place], y=y2, p=0.1, **DRAW)
         assert torch.equal(ins[place], h) and torch.equal(y2, y)
     dy, dh_in, dh = matrix(rows, cols, "bf16", 84), matrix(rows, cols, "bf16", 85), torch.empty_like(x)
-    ps.opt_rms_norm_backward(dy, h, w, rstd, dh, dh_in=dh_in)
+    dw, dw2 = torch.empty(cols, device="cuda"), torch.empty(cols, device="cuda")
+    ps.opt_rms_norm_backward(dy, h, w, rstd, dh, dh_in=dh_in, dweight=dw)
     for place in (0, 1):
         ins = [dy.clone(), dh_in.clone()]
-        ps.opt_rms_norm_backward(ins[0], h, w, rstd, ins[place], dh_in=ins[1])
-        assert torch.equal(ins[place], dh)
+        ps.opt_rms_norm_backward(ins[0], h, w, rstd, ins[place], dh_in=ins[1], dweight=dw2)
+        assert torch.equal(ins[place], dh) and torch.equal(dw, dw2)
 
 
 def test_rows_past_2_31_elements():

@@ -50,7 +50,9 @@ def test_scales_bytes():
 
 
 def test_backward_workspace():
-    for rows, cols in ((0, 7), (1, 1), (5, 769), (4096, 4096)):
+    for rows, cols in ((0, 7), (1, 1), (5, 769), (512, 4096)):             # few rows need none
+        assert ps.opt_rms_norm_backward_workspace(rows, cols) == 0
+    for rows, cols in ((513, 1), (512, 4097), (4096, 4095), (1, (1 << 21) + 1)):
         assert ps.opt_rms_norm_backward_workspace(rows, cols) == min(rows, 1024) * (-(-cols // 4) * 4) * 4
     assert ps.lib().opt_rms_norm_backward_workspace(-1, 4) == ps.OPT_EINVAL
 
@@ -59,7 +61,7 @@ DROPOUT = dict(d_x=P, d_y=P, x_pitch=8, y_pitch=8, rows=2, cols=8, p=0.1, dtype=
 NORM = dict(d_x=P, d_weight=P, d_y=P, x_pitch=8, y_pitch=8, rows=2, cols=8, dtype=ps.OPT_BF16, weight_dtype=ps.OPT_F32,
             eps=1e-5)
 BACK = dict(d_dy=P, d_h=P, d_weight=P, d_rstd=P, d_dh=P, d_dweight=P, d_workspace=P, workspace_bytes=1 << 20, dy_pitch=8,
-            h_pitch=8, dh_pitch=8, rows=2, cols=8, dtype=ps.OPT_F32, weight_dtype=ps.OPT_F32)
+            h_pitch=8, dh_pitch=8, rows=600, cols=8, dtype=ps.OPT_F32, weight_dtype=ps.OPT_F32)
 QUANT = dict(d_x=P, d_codes=P, d_scales=P, x_pitch=8, codes_pitch=16, rows=2, cols=8, dtype=ps.OPT_F32, block_rows=1)
 MATMUL = dict(d_a=P, d_a_scales=P, d_b=P, d_b_scales=P, d_out=P, a_pitch=16, b_pitch=16, out_pitch=4, m=2, n=4, k=16,
               out_dtype=ps.OPT_F32)
@@ -84,7 +86,7 @@ BIG = 1 << 31
     ("opt_rms_norm", NORM, dict(d_rstd=P + 2), ps.OPT_EALIGN), ("opt_rms_norm", NORM, dict(p=2.0), ps.OPT_EINVAL),
     ("opt_rms_norm", NORM, dict(rows=0), ps.OPT_OK),
     ("opt_rms_norm_backward", BACK, dict(d_workspace=0), ps.OPT_EINVAL),
-    ("opt_rms_norm_backward", BACK, dict(workspace_bytes=63), ps.OPT_EINVAL),
+    ("opt_rms_norm_backward", BACK, dict(workspace_bytes=600 * 32 - 1), ps.OPT_EINVAL),
     ("opt_rms_norm_backward", BACK, dict(d_workspace=P + 4), ps.OPT_EALIGN),
     ("opt_rms_norm_backward", BACK, dict(d_rstd=0), ps.OPT_EINVAL), ("opt_rms_norm_backward", BACK, dict(d_dh=0), ps.OPT_EINVAL),
     ("opt_rms_norm_backward", BACK, dict(reserved=1), ps.OPT_EINVAL), ("opt_rms_norm_backward", BACK, dict(d_dx=P, dx_pitch=1), ps.OPT_EINVAL),
