@@ -9,7 +9,8 @@
 // elements (issue 65 % busy).  One thread per chunk and fresh CTAs, not a resident
 // grid; six CTAs per SM (32 registers): with the ragged end's code in the same
 // path it took 70 registers and 112 us.  One token of 4,096 takes a launch's time
-// (1.8 us back to back).
+// (1.8 us back to back).  Strided rows that begin anywhere take two generator calls
+// per chunk and go through shared memory: 8000 x 4001 BF16 68 us (0.42).
 #include "layer.cuh"
 
 namespace psopt {
@@ -20,14 +21,17 @@ constexpr int64_t kMaxGridX = (int64_t)1 << 30;
 
 template <typename T, bool VEC>
 __device__ __forceinline__ void drop_chunk(const opt_dropout_args& a, const DropArgs& d, int64_t r, int64_t c,
-                                           int valid) {
-  const Raw<T> xr = load_raw<VEC>(static_cast<const T*>(a.d_x) + r * a.x_pitch + c, valid);
-  float x[8], y[8] = {};
-  if (a.d_residual != nullptr)
-    load8<VEC>(static_cast<const T*>(a.d_residual) + r * a.residual_pitch + c, valid, y);
+                                           int valid, T* buffer) {
+  Raw<T> xr = {}, rr = {};
+  if (valid > 0) {
+    xr = load_at<VEC, T>(a.d_x, a.x_pitch, a.rows, a.cols, r, c, valid);
+    if (a.d_residual != nullptr) rr = load_at<VEC, T>(a.d_residual, a.residual_pitch, a.rows, a.cols, r, c, valid);
+  }
+  float x[8], y[8];
   unpack(xr, x);
+  unpack(rr, y);
   add_dropped8<VEC>(y, x, (uint64_t)(r * a.cols + c), d);
-  store8<VEC>(static_cast<T*>(a.d_y) + r * a.y_pitch + c, valid, y);
+  store_at<VEC>(a.d_y, a.y_pitch, a.cols, r, c, valid, y, buffer);
 }
 // A matrix's ragged end, element by element, so that it adds nothing to the main
 // path's registers; chunks of a VEC matrix start on a generator call.
@@ -50,17 +54,18 @@ __device__ __forceinline__ void drop_end(const opt_dropout_args& a, const DropAr
 // One chunk of eight elements per thread; chunk `c` of row `r` starts at 8 c.
 // A contiguous matrix comes as one row.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads, VEC ? 6 : 4)
+__global__ void __launch_bounds__(kThreads, VEC ? 6 : 5)
 dropout_kernel(const __grid_constant__ opt_dropout_args a, const __grid_constant__ DropArgs d, int64_t first) {
+  __shared__ __align__(16) Ragged<T, VEC, kThreads / 32> ragged;
   const int64_t c = 8 * (first + (int64_t)blockIdx.x * kThreads + threadIdx.x);
-  if (c >= a.cols) return;
-  const int valid = (int)(a.cols - c < 8 ? a.cols - c : 8);
+  if ((VEC ? c : c - 8 * (int)(threadIdx.x & 31)) >= a.cols) return;      // not VEC: whole warps only
+  const int valid = (int)max(min(a.cols - c, (int64_t)8), (int64_t)0);
   for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
     if constexpr (VEC) {
-      if (valid == 8) drop_chunk<T, true>(a, d, r, c, 8);
+      if (valid == 8) drop_chunk<T, true>(a, d, r, c, 8, ragged.of_warp());
       else drop_end<T>(a, d, r, c, valid);
     } else {
-      drop_chunk<T, false>(a, d, r, c, valid);
+      drop_chunk<T, false>(a, d, r, c, valid, ragged.of_warp());
     }
   }
 }

@@ -64,6 +64,51 @@ __device__ __forceinline__ void load8(const T* p, int valid, float (&x)[8]) {
   unpack(load_raw<VEC>(p, valid), x);
 }
 
+// Eight BF16 at any place of a matrix that begins at `begin` and ends at `end`, by
+// the words that they lie in; one by one where those words reach beyond the
+// matrix.  Elements from `valid` on read as 0.
+__device__ __forceinline__ Raw<Bf16> load_ragged(const Bf16* p, int valid, const void* begin, const void* end) {
+  const uintptr_t at = (uintptr_t)p & ~(uintptr_t)3;
+  const bool half = ((uintptr_t)p & 2u) != 0;
+  if (at < (uintptr_t)begin || at + 20 > (uintptr_t)end) {
+    uint64_t part[2] = {0, 0};             // a loop: it must not cost the main path registers
+#pragma unroll 1
+    for (int j = 0; j < valid; ++j) {
+      const uint64_t v = (uint64_t)p[j].bits << (16 * (j & 3));
+      if (j < 4) part[0] |= v;
+      else part[1] |= v;
+    }
+    Raw<Bf16> r;
+    r.w[0] = (uint32_t)part[0]; r.w[1] = (uint32_t)(part[0] >> 32);
+    r.w[2] = (uint32_t)part[1]; r.w[3] = (uint32_t)(part[1] >> 32);
+    return r;
+  }
+  const uint32_t* q = reinterpret_cast<const uint32_t*>(at);
+  uint32_t w[5];
+#pragma unroll
+  for (int k = 0; k < 5; ++k) w[k] = q[k];
+  Raw<Bf16> r;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) r.w[k] = half ? __funnelshift_r(w[k], w[k + 1], 16) : w[k];
+  if (valid < 8) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r.w[k] = 2 * k + 1 < valid ? r.w[k] : 2 * k < valid ? r.w[k] & 0xFFFFu : 0u;
+  }
+  return r;
+}
+// fp32 elements are words.
+__device__ __forceinline__ Raw<float> load_ragged(const float* p, int valid, const void*, const void*) {
+  return load_raw<false>(p, valid);
+}
+// The chunk at column c of row r of a rows x cols matrix.
+template <bool VEC, typename T>
+__device__ __forceinline__ Raw<T> load_at(const void* base, int64_t pitch, int64_t rows, int64_t cols, int64_t r, int64_t c,
+                                          int valid) {
+  const T* m = static_cast<const T*>(base);
+  if constexpr (VEC) return load_raw<true>(m + r * pitch + c, 8);
+  else return load_ragged(m + r * pitch + c, valid, m, m + (rows - 1) * pitch + cols);
+}
+
 // Nearest BF16 of two values (a NaN as the converter's canonical one).
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   uint32_t d;
@@ -92,6 +137,54 @@ __device__ __forceinline__ void store8(float* p, int valid, const float (&x)[8])
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (j < valid) p[j] = x[j];
+  }
+}
+
+// Storage of a warp's 32 consecutive chunks on their way to a row that starts at
+// any place: lanes' chunks in, consecutive words out, so that a store covers 128
+// bytes and not two in every sixteen.
+template <typename T, bool VEC, int WARPS>
+struct Ragged {
+  T chunk[VEC ? 1 : WARPS][VEC ? 1 : 256];
+  __device__ __forceinline__ T* of_warp() { return chunk[VEC ? 0 : threadIdx.x >> 5]; }
+};
+__device__ __forceinline__ void store_words(float* p, int n, const float* v, int lane) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (32 * i + lane < n) p[32 * i + lane] = v[32 * i + lane];
+}
+__device__ __forceinline__ void store_words(Bf16* p, int n, const Bf16* v, int lane) {
+  const int head = (int)((uintptr_t)p >> 1) & 1;       // an element before the first whole word
+  if (lane == 0 && head && n > 0) p[0] = v[0];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = head + 2 * (32 * i + lane);
+    if (e + 1 < n) *reinterpret_cast<uint32_t*>(p + e) = (uint32_t)v[e].bits | (uint32_t)v[e + 1].bits << 16;
+    else if (e < n) p[e] = v[e];
+  }
+}
+// Store of the chunk at column c (this lane's; its warp's lie side by side) of row
+// r; chunks beyond the row come with valid 0.  Not VEC: by whole warps.
+template <bool VEC, typename T>
+__device__ __forceinline__ void store_at(void* base, int64_t pitch, int64_t cols, int64_t r, int64_t c, int valid,
+                                         const float (&x)[8], T* buffer) {
+  T* row = static_cast<T*>(base) + r * pitch;
+  if constexpr (VEC) {
+    if (valid > 0) store8<true>(row + c, 8, x);
+  } else {
+    const int lane = threadIdx.x & 31;
+    const int64_t tile = c - 8 * lane;
+    uint32_t* b = reinterpret_cast<uint32_t*>(buffer + 8 * lane);
+    if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<float4*>(b) = make_float4(x[0], x[1], x[2], x[3]);
+      *reinterpret_cast<float4*>(b + 4) = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+      *reinterpret_cast<uint4*>(b) =
+          make_uint4(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7]));
+    }
+    __syncwarp();
+    if (tile < cols) store_words(row + tile, (int)min(cols - tile, (int64_t)256), buffer, lane);
+    __syncwarp();
   }
 }
 

@@ -143,7 +143,7 @@ __device__ __forceinline__ void store_bytes(uint8_t* scales, const uint32_t (&by
 }
 
 template <typename T, bool VEC, bool WHOLE>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && VEC ? 4 : 2)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? VEC ? 4 : 3 : 2)
 quantize_kernel(const __grid_constant__ opt_quantize_args a, int64_t col_tiles) {
   // warps' maxima of columns; then the transposed codes, 16 pieces of 8 bytes per
   // column, pieces turned by column
@@ -159,11 +159,16 @@ quantize_kernel(const __grid_constant__ opt_quantize_args a, int64_t col_tiles) 
 
   Raw<T> raw[8];
   {
-    const T* p = static_cast<const T*>(a.d_x) + (r0 + l) * a.x_pitch + c0 + c;
+    const T* x = static_cast<const T*>(a.d_x);
+    const T* end = x + (a.rows - 1) * a.x_pitch + a.cols;
+    const T* p = x + (r0 + l) * a.x_pitch + c0 + c;
 #pragma unroll
     for (int i = 0; i < 8; ++i, p += a.x_pitch) {
       raw[i] = Raw<T>{};
-      if (l + i < rows && c < cols) raw[i] = load_raw<VEC>(p, min(cols - c, 8));
+      if (l + i < rows && c < cols) {
+        if constexpr (VEC) raw[i] = load_raw<true>(p, 8);
+        else raw[i] = load_ragged(p, min(cols - c, 8), x, end);
+      }
     }
   }
 

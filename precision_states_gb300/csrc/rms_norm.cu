@@ -19,9 +19,11 @@
 // per SM: one chunk at 512 threads took 98.3 us, four at 128 threads 108.7, four
 // CTAs per SM 87.1 (but 79.7 without dropout).  Backward, 8192 x 4096 BF16 with
 // dh_in, dropout and the weight's gradient: 58.5 us (0.86), of which the sum over
-// the CTAs' rows takes 4; one chunk per thread at 512 threads and two CTAs per SM,
-// one CTA for fp32 (its rows take twice the registers).  Few rows are launches'
-// latency: one token of 4,096 2.6 us.
+// the CTAs' rows takes 4; one chunk per thread at 512 threads and two CTAs per SM
+// (fp32 too, in spite of some spilled registers: 8000 x 4096 120.5 us, 162.6 with one).  Few rows are launches'
+// latency: one token of 4,096 2.6 us.  Rows that begin anywhere (odd widths and pitches) are
+// loaded by words and stored through shared memory: 8000 x 4001 BF16 to y 54.6 us
+// (94.8 element by element), the backward pass 135 (271).
 #include "layer.cuh"
 
 namespace psopt {
@@ -42,22 +44,20 @@ __device__ __forceinline__ void h_chunk(const opt_rms_norm_args& a, const DropAr
 template <typename T, bool VEC>
 __device__ __forceinline__ void load_chunk(const opt_rms_norm_args& a, int64_t r, int64_t c, int valid, Raw<T>& x,
                                            Raw<T>& res) {
-  x = load_raw<VEC>(static_cast<const T*>(a.d_x) + r * a.x_pitch + c, valid);
-  if (a.d_residual != nullptr) res = load_raw<VEC>(static_cast<const T*>(a.d_residual) + r * a.residual_pitch + c, valid);
+  x = load_at<VEC, T>(a.d_x, a.x_pitch, a.rows, a.cols, r, c, valid);
+  if (a.d_residual != nullptr) res = load_at<VEC, T>(a.d_residual, a.residual_pitch, a.rows, a.cols, r, c, valid);
 }
 
 // Everything that is written of a chunk, by whole warps; chunks beyond the row
 // come with valid <= 0.
 template <typename T, bool VEC>
 __device__ __forceinline__ void write_chunk(const opt_rms_norm_args& a, int64_t r, int64_t c, int valid, float rstd,
-                                            int64_t panel, const float (&h)[8], const float (&w)[8]) {
+                                            int64_t panel, const float (&h)[8], const float (&w)[8], T* buffer) {
   float y[8];
   scaled8(h, rstd, y);
   times8(y, w);
-  if (valid > 0) {
-    if (a.d_h != nullptr) store8<VEC>(static_cast<T*>(a.d_h) + r * a.h_pitch + c, valid, h);
-    if (a.d_y != nullptr) store8<VEC>(static_cast<T*>(a.d_y) + r * a.y_pitch + c, valid, y);
-  }
+  if (a.d_h != nullptr) store_at<VEC>(a.d_h, a.h_pitch, a.cols, r, c, valid, h, buffer);
+  if (a.d_y != nullptr) store_at<VEC>(a.d_y, a.y_pitch, a.cols, r, c, valid, y, buffer);
   if (a.d_codes == nullptr) return;
   if (valid < 8) {
 #pragma unroll
@@ -77,6 +77,7 @@ template <typename T, typename W, bool VEC, bool BY_WARP, int NG, int MAX, int C
 __global__ void __launch_bounds__(MAX, CTAS) rms_norm_kernel(const __grid_constant__ opt_rms_norm_args a,
                                                              const __grid_constant__ DropArgs d) {
   __shared__ float part[2][33];
+  __shared__ __align__(16) Ragged<T, VEC, MAX / 32> ragged;
   const int in_row = BY_WARP ? (int)(threadIdx.x & 31) : (int)threadIdx.x, of_row = BY_WARP ? 32 : (int)blockDim.x;
   const int64_t row0 = BY_WARP ? (int64_t)blockIdx.x * (MAX / 32) + (threadIdx.x >> 5) : blockIdx.x;
   const int64_t row_step = BY_WARP ? (int64_t)gridDim.x * (MAX / 32) : gridDim.x;
@@ -91,7 +92,7 @@ __global__ void __launch_bounds__(MAX, CTAS) rms_norm_kernel(const __grid_consta
   for (int k = 0; k < NG; ++k) {
     if (valid(k) > 0) {
       if (row0 < a.rows) load_chunk<T, VEC>(a, row0, column(k), valid(k), x[k], res[k]);
-      load8<VEC>(static_cast<const W*>(a.d_weight) + column(k), valid(k), w[k]);
+      unpack(load_at<VEC, W>(a.d_weight, 0, 1, a.cols, 0, column(k), valid(k)), w[k]);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) w[k][j] = 0.0f;
@@ -119,7 +120,7 @@ __global__ void __launch_bounds__(MAX, CTAS) rms_norm_kernel(const __grid_consta
     const float rstd = rsqrtf(fmaf(sum, inv_cols, a.eps));
     if (in_row == 0 && a.d_rstd != nullptr) a.d_rstd[r] = rstd;
 #pragma unroll
-    for (int k = 0; k < NG; ++k) write_chunk<T, VEC>(a, r, column(k), valid(k), rstd, panel, h[k], w[k]);
+    for (int k = 0; k < NG; ++k) write_chunk<T, VEC>(a, r, column(k), valid(k), rstd, panel, h[k], w[k], ragged.of_warp());
   }
 }
 
@@ -129,6 +130,7 @@ template <typename T, typename W, bool VEC>
 __global__ void __launch_bounds__(kWideThreads) rms_norm_wide_kernel(const __grid_constant__ opt_rms_norm_args a,
                                                                      const __grid_constant__ DropArgs d) {
   __shared__ float part[2][33];
+  __shared__ __align__(16) Ragged<T, VEC, kWideThreads / 32> ragged;
   const int64_t panel = (a.cols + 511) / 512;
   int turn = 0;
   for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, turn ^= 1) {
@@ -149,27 +151,28 @@ __global__ void __launch_bounds__(kWideThreads) rms_norm_wide_kernel(const __gri
       if (valid > 0) {
         load_chunk<T, VEC>(a, r, c, valid, x, res);
         h_chunk<T, VEC>(a, d, r, c, x, res, h);
-        load8<VEC>(static_cast<const W*>(a.d_weight) + c, valid, w);
+        unpack(load_at<VEC, W>(a.d_weight, 0, 1, a.cols, 0, c, valid), w);
       }
-      write_chunk<T, VEC>(a, r, c, valid, rstd, panel, h, w);
+      write_chunk<T, VEC>(a, r, c, valid, rstd, panel, h, w, ragged.of_warp());
     }
   }
 }
 
 // ------------------------------------------------------------------ gradients
-// What is written of a chunk of the gradients: dh and dx from g = dy weight.
+// What is written of a chunk of the gradients, by whole warps: dh and dx from g =
+// dy weight.
 template <typename T, bool VEC>
 __device__ __forceinline__ void write_gradients(const opt_rms_norm_backward_args& a, const DropArgs& d, int64_t r,
                                                 int64_t c, int valid, float rstd, float k, const float (&g)[8],
-                                                const float (&h)[8], const float (&in)[8]) {
+                                                const float (&h)[8], const float (&in)[8], T* buffer) {
   float out[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) out[j] = fmaf(rstd, fmaf(-h[j], k, g[j]), in[j]);
-  store8<VEC>(static_cast<T*>(a.d_dh) + r * a.dh_pitch + c, valid, out);
+  store_at<VEC>(a.d_dh, a.dh_pitch, a.cols, r, c, valid, out, buffer);
   if (a.d_dx != nullptr) {
     float dx[8] = {};
     add_dropped8<VEC>(dx, out, (uint64_t)(r * a.cols + c), d);
-    store8<VEC>(static_cast<T*>(a.d_dx) + r * a.dx_pitch + c, valid, dx);
+    store_at<VEC>(a.d_dx, a.dx_pitch, a.cols, r, c, valid, dx, buffer);
   }
 }
 
@@ -189,7 +192,7 @@ __host__ __device__ __forceinline__ bool dweight_here(const opt_rms_norm_backwar
 // order.
 template <typename T>
 __device__ __forceinline__ void dweight_slab(const opt_rms_norm_backward_args& a, int slab) {
-  __shared__ float sums[kWideThreads / 32][kSlabCols];
+  __shared__ float sums[32][kSlabCols];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int64_t c = (int64_t)slab * kSlabCols + (lane & (kSlabCols - 1));
   float s = 0.0f;
@@ -221,12 +224,13 @@ __device__ __forceinline__ void dweight_slab(const opt_rms_norm_backward_args& a
   a.d_dweight[c] = s;
 }
 
-// CTAs from `row_ctas` on are dweight's slabs.  With four chunks per thread the
+// CTAs from `row_ctas` on are dweight's slabs.  At 1,024 threads the
 // registers hold neither the weight nor the next row (AHEAD false).
 template <typename T, typename W, bool VEC, int NG, int MAX, int CTAS>
 __global__ void __launch_bounds__(MAX, CTAS) rms_norm_backward_kernel(
     const __grid_constant__ opt_rms_norm_backward_args a, const __grid_constant__ DropArgs d, int row_ctas) {
   __shared__ float part[2][33];
+  __shared__ __align__(16) Ragged<T, VEC, MAX / 32> ragged;
   if ((int)blockIdx.x >= row_ctas) {
     dweight_slab<T>(a, (int)blockIdx.x - row_ctas);
     return;
@@ -239,16 +243,16 @@ __global__ void __launch_bounds__(MAX, CTAS) rms_norm_backward_kernel(
   float dw[NG][8] = {};
   Raw<W> w[NG] = {};
   Raw<T> dy[NG] = {}, h[NG] = {}, in[NG] = {};
-  constexpr bool AHEAD = NG < 4;
+  constexpr bool AHEAD = MAX < 1024;
   const auto load = [&](int k, int64_t r) {
-    dy[k] = load_raw<VEC>(static_cast<const T*>(a.d_dy) + r * a.dy_pitch + column(k), valid(k));
-    h[k] = load_raw<VEC>(static_cast<const T*>(a.d_h) + r * a.h_pitch + column(k), valid(k));
+    dy[k] = load_at<VEC, T>(a.d_dy, a.dy_pitch, a.rows, a.cols, r, column(k), valid(k));
+    h[k] = load_at<VEC, T>(a.d_h, a.h_pitch, a.rows, a.cols, r, column(k), valid(k));
   };
 #pragma unroll
   for (int k = 0; k < NG; ++k) {
     if (AHEAD && valid(k) > 0) {
       load(k, blockIdx.x);
-      w[k] = load_raw<VEC>(static_cast<const W*>(a.d_weight) + column(k), valid(k));
+      w[k] = load_at<VEC, W>(a.d_weight, 0, 1, a.cols, 0, column(k), valid(k));
     }
   }
   int turn = 0;
@@ -263,12 +267,12 @@ __global__ void __launch_bounds__(MAX, CTAS) rms_norm_backward_kernel(
 #pragma unroll
     for (int k = 0; k < NG; ++k) {
       float wv[8];
-      if (!AHEAD && valid(k) > 0) w[k] = load_raw<VEC>(static_cast<const W*>(a.d_weight) + column(k), valid(k));
+      if (!AHEAD && valid(k) > 0) w[k] = load_at<VEC, W>(a.d_weight, 0, 1, a.cols, 0, column(k), valid(k));
       unpack(dy[k], g[k]);
       unpack(h[k], hv[k]);
       unpack(w[k], wv);
       if (AHEAD && a.d_dh_in != nullptr && valid(k) > 0)
-        in[k] = load_raw<VEC>(static_cast<const T*>(a.d_dh_in) + r * a.dh_in_pitch + column(k), valid(k));
+        in[k] = load_at<VEC, T>(a.d_dh_in, a.dh_in_pitch, a.rows, a.cols, r, column(k), valid(k));
       if (AHEAD && valid(k) > 0 && r + row_ctas < a.rows) load(k, r + row_ctas);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -281,12 +285,12 @@ __global__ void __launch_bounds__(MAX, CTAS) rms_norm_backward_kernel(
     const float scale = rstd * rstd * (sum * inv_cols);
 #pragma unroll
     for (int k = 0; k < NG; ++k)
-      if (valid(k) > 0) {
+      if (!VEC || valid(k) > 0) {
         float add[8];
-        if (!AHEAD && a.d_dh_in != nullptr)
-          in[k] = load_raw<VEC>(static_cast<const T*>(a.d_dh_in) + r * a.dh_in_pitch + column(k), valid(k));
+        if (!AHEAD && a.d_dh_in != nullptr && valid(k) > 0)
+          in[k] = load_at<VEC, T>(a.d_dh_in, a.dh_in_pitch, a.rows, a.cols, r, column(k), valid(k));
         unpack(in[k], add);
-        write_gradients<T, VEC>(a, d, r, column(k), valid(k), rstd, scale, g[k], hv[k], add);
+        write_gradients<T, VEC>(a, d, r, column(k), valid(k), rstd, scale, g[k], hv[k], add, ragged.of_warp());
       }
   }
   if (a.d_dweight != nullptr && !dweight_here(a)) {
@@ -311,6 +315,7 @@ template <typename T, typename W, bool VEC>
 __global__ void __launch_bounds__(kWideThreads) rms_norm_backward_wide_kernel(
     const __grid_constant__ opt_rms_norm_backward_args a, const __grid_constant__ DropArgs d, int row_ctas) {
   __shared__ float part[2][33];
+  __shared__ __align__(16) Ragged<T, VEC, kWideThreads / 32> ragged;
   if ((int)blockIdx.x >= row_ctas) {
     dweight_slab<T>(a, (int)blockIdx.x - row_ctas);
     return;
@@ -318,34 +323,36 @@ __global__ void __launch_bounds__(kWideThreads) rms_norm_backward_wide_kernel(
   float* dw = a.d_dweight == nullptr || dweight_here(a) ? nullptr : dweight_row(a, blockIdx.x);
   int turn = 0;
   for (int64_t r = blockIdx.x; r < a.rows; r += row_ctas, turn ^= 1) {
-    const T* dy_row = static_cast<const T*>(a.d_dy) + r * a.dy_pitch;
-    const T* h_row = static_cast<const T*>(a.d_h) + r * a.h_pitch;
-    float sum = 0.0f, g[8], h[8], w[8];
+    const auto load = [&](int64_t c, int valid, float (&g)[8], float (&h)[8], float (&w)[8]) {
+      unpack(load_at<VEC, T>(a.d_dy, a.dy_pitch, a.rows, a.cols, r, c, valid), g);
+      unpack(load_at<VEC, T>(a.d_h, a.h_pitch, a.rows, a.cols, r, c, valid), h);
+      unpack(load_at<VEC, W>(a.d_weight, 0, 1, a.cols, 0, c, valid), w);
+    };
+    float sum = 0.0f;
     for (int64_t c = 8 * threadIdx.x; c < a.cols; c += 8 * kWideThreads) {
-      const int valid = (int)min(a.cols - c, (int64_t)8);
-      load8<VEC>(dy_row + c, valid, g);
-      load8<VEC>(h_row + c, valid, h);
-      load8<VEC>(static_cast<const W*>(a.d_weight) + c, valid, w);
+      float g[8], h[8], w[8];
+      load(c, (int)min(a.cols - c, (int64_t)8), g, h, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum = fmaf(g[j] * w[j], h[j], sum);
     }
     sum = cta_sum(sum, part[turn], kWideThreads / 32);
     const float rstd = a.d_rstd[r];
     const float k = rstd * rstd * (sum / (float)a.cols);
-    for (int64_t c = 8 * threadIdx.x; c < a.cols; c += 8 * kWideThreads) {
-      const int valid = (int)min(a.cols - c, (int64_t)8);
-      load8<VEC>(dy_row + c, valid, g);
-      load8<VEC>(h_row + c, valid, h);
-      load8<VEC>(static_cast<const W*>(a.d_weight) + c, valid, w);
+    for (int64_t c0 = 0; c0 < a.cols; c0 += 8 * kWideThreads) {
+      const int64_t c = c0 + 8 * threadIdx.x;
+      const int valid = (int)max(min(a.cols - c, (int64_t)8), (int64_t)0);
+      float g[8] = {}, h[8] = {}, w[8] = {}, in[8] = {};
+      if (valid > 0) {
+        load(c, valid, g, h, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (dw != nullptr && j < valid)
-          dw[c + j] = fmaf(g[j], h[j] * rstd, r == (int64_t)blockIdx.x ? 0.0f : dw[c + j]);
-        g[j] *= w[j];
+        for (int j = 0; j < 8; ++j) {
+          if (dw != nullptr && j < valid)
+            dw[c + j] = fmaf(g[j], h[j] * rstd, r == (int64_t)blockIdx.x ? 0.0f : dw[c + j]);
+          g[j] *= w[j];
+        }
+        if (a.d_dh_in != nullptr) unpack(load_at<VEC, T>(a.d_dh_in, a.dh_in_pitch, a.rows, a.cols, r, c, valid), in);
       }
-      float in[8] = {};
-      if (a.d_dh_in != nullptr) load8<VEC>(static_cast<const T*>(a.d_dh_in) + r * a.dh_in_pitch + c, valid, in);
-      write_gradients<T, VEC>(a, d, r, c, valid, rstd, k, g, h, in);
+      write_gradients<T, VEC>(a, d, r, c, valid, rstd, k, g, h, in, ragged.of_warp());
     }
   }
 }
@@ -445,11 +452,11 @@ cudaError_t backward_vec(const opt_rms_norm_backward_args& a, const DropArgs& d,
   const int64_t chunks = (a.cols + 7) / 8;
   int grid;
   if (chunks <= 512) {
-    grid = backward_rows<T, W, VEC, 1, 512, VEC && sizeof(T) == 2 ? 2 : 1>(a, d, sm_count, (int)((chunks + 31) / 32) * 32, s);
+    grid = backward_rows<T, W, VEC, 1, 512, 2>(a, d, sm_count, (int)((chunks + 31) / 32) * 32, s);
   } else if (chunks <= 1024) {
     grid = backward_rows<T, W, VEC, 2, 512, 1>(a, d, sm_count, (int)((chunks + 63) / 64) * 32, s);
   } else if (chunks <= 2048) {
-    grid = backward_rows<T, W, VEC, 4, 512, 1>(a, d, sm_count, (int)((chunks + 127) / 128) * 32, s);
+    grid = backward_rows<T, W, VEC, 2, 1024, 1>(a, d, sm_count, (int)((chunks + 63) / 64) * 32, s);
   } else {
     const int64_t most = (int64_t)sm_count * 4;
     grid = (int)(a.rows < most ? a.rows : most);
