@@ -164,13 +164,13 @@ __device__ __forceinline__ void store_words(Bf16* p, int n, const Bf16* v, int l
   }
 }
 // Store of the chunk at column c (this lane's; its warp's lie side by side) of row
-// r; chunks beyond the row come with valid 0.  Not VEC: by whole warps.
+// r.  Not VEC: by whole warps, in which chunks beyond the row come with valid 0.
 template <bool VEC, typename T>
 __device__ __forceinline__ void store_at(void* base, int64_t pitch, int64_t cols, int64_t r, int64_t c, int valid,
                                          const float (&x)[8], T* buffer) {
   T* row = static_cast<T*>(base) + r * pitch;
   if constexpr (VEC) {
-    if (valid > 0) store8<true>(row + c, 8, x);
+    store8<true>(row + c, 8, x);
   } else {
     const int lane = threadIdx.x & 31;
     const int64_t tile = c - 8 * lane;

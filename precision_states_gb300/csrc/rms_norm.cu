@@ -56,8 +56,10 @@ __device__ __forceinline__ void write_chunk(const opt_rms_norm_args& a, int64_t 
   float y[8];
   scaled8(h, rstd, y);
   times8(y, w);
-  if (a.d_h != nullptr) store_at<VEC>(a.d_h, a.h_pitch, a.cols, r, c, valid, h, buffer);
-  if (a.d_y != nullptr) store_at<VEC>(a.d_y, a.y_pitch, a.cols, r, c, valid, y, buffer);
+  if (!VEC || valid > 0) {
+    if (a.d_h != nullptr) store_at<VEC>(a.d_h, a.h_pitch, a.cols, r, c, valid, h, buffer);
+    if (a.d_y != nullptr) store_at<VEC>(a.d_y, a.y_pitch, a.cols, r, c, valid, y, buffer);
+  }
   if (a.d_codes == nullptr) return;
   if (valid < 8) {
 #pragma unroll
@@ -352,7 +354,7 @@ __global__ void __launch_bounds__(kWideThreads) rms_norm_backward_wide_kernel(
         }
         if (a.d_dh_in != nullptr) unpack(load_at<VEC, T>(a.d_dh_in, a.dh_in_pitch, a.rows, a.cols, r, c, valid), in);
       }
-      write_gradients<T, VEC>(a, d, r, c, valid, rstd, k, g, h, in, ragged.of_warp());
+      if (!VEC || valid > 0) write_gradients<T, VEC>(a, d, r, c, valid, rstd, k, g, h, in, ragged.of_warp());
     }
   }
 }
