@@ -783,7 +783,7 @@ cudaError_t launch(const Operand& x, const Operand& y, int64_t k, MatmulArgs a, 
 struct Plan {
   int swap, cg, nt, split;
 };
-Plan plan(int64_t m, int64_t n, int blocks, int sm_count) {
+Plan plan(int64_t m, int64_t n, int blocks, const int (&clusters)[4]) {
   static const struct { int cg, nt, block, least, tile, split; } kForms[] = {
       {1, 16, 155, 1000, 400, 2300}, {1, 32, 165, 1000, 400, 2500},   {1, 64, 185, 1500, 400, 3300},
       {1, 128, 208, 2000, 400, 6200}, {2, 128, 175, 2000, 400, 0}, {2, 256, 320, 1900, 900, 0}};
@@ -798,7 +798,8 @@ Plan plan(int64_t m, int64_t n, int blocks, int sm_count) {
       if (f.nt < 128 && yr > f.nt) continue;
       const int64_t tiles = ((xr + 128 * f.cg - 1) / (128 * f.cg)) * ((yr + f.nt - 1) / f.nt);
       for (int split = 1; split <= (f.cg == 2 ? 1 : 8) && split <= panel; split *= 2) {
-        const int64_t slots = sm_count / (f.cg == 2 ? 2 : split), waves = (tiles + slots - 1) / slots;
+        const int64_t slots = clusters[f.cg == 2 ? 1 : split == 1 ? 0 : split == 2 ? 1 : split == 4 ? 2 : 3];
+        const int64_t waves = (tiles + slots - 1) / slots;
         const double each = (double)((blocks + split - 1) / split) * f.block, out = waves > 1 ? f.least : 0;
         double time = (double)waves * ((each > out ? each : out) + f.tile) + (f.cg == 2 ? kPair : 0);
         if (split > 1) time += (double)waves * f.split + (double)(waves - 1) * kStart;
@@ -809,6 +810,39 @@ Plan plan(int64_t m, int64_t n, int blocks, int sm_count) {
       }
     }
   return best;
+}
+
+// Clusters of 1, 2, 4 and 8 CTAs that the device holds at once (a GB300's 152 SMs:
+// 152, 76, 36, 15: clusters do not straddle its groups of SMs), asked once per
+// device.
+cudaError_t active_clusters(int sm_count, int (&out)[4]) {
+  static std::atomic<int> cache[kMaxDevices][4];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) dev = 0;
+  out[0] = sm_count;
+  for (int i = 1; i < 4; ++i) {
+    out[i] = cache[dev][i].load(std::memory_order_relaxed);
+    if (out[i] > 0) continue;
+    using L = Layout<1, 128>;
+    const auto kernel = matmul_kernel<float, 1, 128>;
+    static OccupancyCache occupancy;
+    cached_occupancy(kernel, occupancy, kThreads, L::kBytes);     // enables the shared memory
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1u << i;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(sm_count >> i << i));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = L::kBytes;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(&out[i], kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    if (out[i] < 1) out[i] = 1;
+    cache[dev][i].store(out[i], std::memory_order_relaxed);
+  }
+  return cudaSuccess;
 }
 
 template <typename T>
@@ -838,7 +872,9 @@ cudaError_t dispatch(const opt_matmul_args& c, int sm_count, cudaStream_t s) {
     return launch_matmul_few(c, a, s);
   }
   const Operand ops[2] = {{c.d_a, c.d_a_scales, c.a_pitch, c.m}, {c.d_b, c.d_b_scales, c.b_pitch, c.n}};
-  const Plan p = plan(c.m, c.n, a.blocks, sm_count);
+  int clusters[4];
+  if (const cudaError_t e = active_clusters(sm_count, clusters); e != cudaSuccess) return e;
+  const Plan p = plan(c.m, c.n, a.blocks, clusters);
   a.swap = p.swap;
   const Operand &x = ops[p.swap], &y = ops[1 - p.swap];
   switch (p.nt) {
