@@ -28,6 +28,7 @@
  *
  * Codes: an 8-bit operand of rows x cols is a matrix of E4M3 bytes, 16-byte
  * aligned with a pitch that is a multiple of 16 (OPT_EALIGN), and its scales.
+ * Rows that start on 128 bytes are faster in products.
  *
  * Scales: each block of 1 x 128 elements along a row (the row's last block
  * may be shorter), or of 128 x 128 (block_rows 128), has the scale 2^e with e

@@ -59,6 +59,22 @@ __device__ __forceinline__ void unpack(const Raw<Bf16>& r, float (&x)[8]) {
 }
 __device__ __forceinline__ float element(const Bf16* p) { return u2f((uint32_t)p->bits << 16); }
 __device__ __forceinline__ float element(const float* p) { return *p; }
+// An element's fp32 bits if it exists, else 0: a load under a predicate, so that the
+// compiler neither branches around it nor waits for it before the next one (as it
+// did for 16-bit elements: 82 x 431 x 212 with a BF16 addend took 14.1 us, 6.7 so).
+__device__ __forceinline__ uint32_t bits_if(const Bf16* p, bool exists) {
+  uint16_t b;
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.s32 q, %2, 0;\n\tmov.b16 %0, 0;\n\t@q ld.global.u16 %0, [%1];\n\t}"
+               : "=h"(b) : "l"(p), "r"((int)exists));
+  return (uint32_t)b << 16;
+}
+__device__ __forceinline__ uint32_t bits_if(const float* p, bool exists) {
+  uint32_t b;
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.s32 q, %2, 0;\n\tmov.b32 %0, 0;\n\t@q ld.global.u32 %0, [%1];\n\t}"
+               : "=r"(b) : "l"(p), "r"((int)exists));
+  return b;
+}
+
 template <bool VEC, typename T>
 __device__ __forceinline__ void load8(const T* p, int valid, float (&x)[8]) {
   unpack(load_raw<VEC>(p, valid), x);

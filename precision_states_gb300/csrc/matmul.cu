@@ -60,8 +60,7 @@ struct MatmulArgs : OutputArgs {
   int blocks;                // ceil(k / 128)
   int panel;                 // scale tiles per 128 rows: ceil(blocks / 4)
   int split;                 // CTAs per cluster along the depth (CG 1)
-  int staged;                // whole warps' outputs leave through shared memory (NT 256)
-  int vec_out;               // rows of out allow 32-byte stores
+  int wide;                  // rows of out allow 32-byte stores (NT 256: 16-byte copies), of the addend 32-byte loads
   int drill;                 // load nothing, so that the waits run out
   unsigned long long wait_ns;   // limit of each wait
 };
@@ -83,11 +82,11 @@ struct Layout {
   static constexpr int kNeed = kScaleCol + 2 * kScaleCols;
   static constexpr int kCols = kNeed <= 64 ? 64 : kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
   static constexpr int kBars = 2 * kStages + 5;      // full, empty, done[2], free[2], drain
-  // columns that an output warp takes at a time (of the widest tile 64 bytes, by
-  // way of shared memory)
+  // columns that an output warp takes at a time (64 bytes of the widest tile's), and
+  // the output warps' shared memory, 32 rows of 64 bytes each
   template <typename T>
   static constexpr int kOutCols = NT == 256 ? 64 / (int)sizeof(T) : NT >= 64 ? 32 : 16;
-  static constexpr int kOutBytes = NT == 256 ? kOutWarps * 32 * 64 : 0;
+  static constexpr int kOutBytes = kOutWarps * 32 * 64;
   // dynamic shared memory: ring | scales | output | barriers, tensor memory address, failure
   static constexpr int kScaleAt = kStages * kStage;
   static constexpr int kOutAt = kScaleAt + kStages * kScaleBytes;
@@ -243,18 +242,22 @@ __device__ __forceinline__ void acc_load(uint32_t tmem, float (&v)[N]) {
 }
 
 // -------------------------------------------------------------------- output
-// A thread's N outputs: row x of the tile, columns y0 .. y0 + N - 1.  The addend
-// is loaded whole, and before the accumulator is read, so that its latency is
-// paid once, in 32-byte accesses (a sector each) where `vec` says that it may.
+// Whether N columns from y0 on leave and arrive in wide pieces: they exist, and rows
+// of out (and of the addend) allow it.
+__device__ __forceinline__ bool whole(const MatmulArgs& a, int n, int y0) { return a.wide && y0 + n <= a.ny; }
+
+// The addend of a thread's N outputs (row x of the tile, columns y0 .. y0 + N - 1),
+// where its rows allow 32-byte loads or, `swap`, lie along the lanes.  It is loaded
+// before the accumulator is read, so that its latency is paid once.
 template <typename T, int N>
-struct Outputs {
+struct Addend {
   static constexpr int kWords = N * (int)sizeof(T) / 4;
   uint32_t add[kWords];
 
   __device__ __forceinline__ void load(const MatmulArgs& a, int x, int y0) {
-    if (a.addend == nullptr || x >= a.nx) return;
+    if (a.addend == nullptr || x >= a.nx || (!a.swap && !whole(a, N, y0))) return;
     const T* p = static_cast<const T*>(a.addend);
-    if (a.vec && !a.swap && y0 + N <= a.ny) {
+    if (!a.swap) {
       p += place(a, a.addend_pitch, x, y0);
 #pragma unroll
       for (int i = 0; i < kWords; i += 8)
@@ -265,14 +268,13 @@ struct Outputs {
     } else {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const float v = y0 + i < a.ny ? element(p + place(a, a.addend_pitch, x, y0 + i)) : 0.0f;
-        if (sizeof(T) == 4) add[i] = f2u(v);
-        else if (i & 1) add[i >> 1] |= f2u(v) & 0xFFFF0000u;
-        else add[i >> 1] = f2u(v) >> 16;
+        const uint32_t v = bits_if(p + place(a, a.addend_pitch, x, y0 + i), y0 + i < a.ny);
+        if (sizeof(T) == 4) add[i] = v;
+        else if (i & 1) add[i >> 1] |= v;
+        else add[i >> 1] = v >> 16;
       }
     }
   }
-  // v + addend
   __device__ __forceinline__ void sum(const MatmulArgs& a, int x, float (&v)[N]) const {
     if (a.addend == nullptr || x >= a.nx) return;
 #pragma unroll
@@ -281,13 +283,13 @@ struct Outputs {
   }
 };
 
-// Each lane's outputs by itself: in 32-byte stores (a sector each) where rows of
-// out allow them, else element by element, in any place.
+// Each lane's outputs by itself: `swap`, where a store's lanes lie along a row of
+// out; else N whole columns in 32-byte stores (a sector each).
 template <typename T, int N>
-__device__ __forceinline__ void store_each(const MatmulArgs& a, int x, int y0, const float (&v)[N]) {
+__device__ __forceinline__ void store_lanes(const MatmulArgs& a, int x, int y0, const float (&v)[N]) {
   if (x >= a.nx) return;
   T* p = static_cast<T*>(a.out);
-  if (a.vec_out && !a.swap && y0 + N <= a.ny) {
+  if (!a.swap) {
     constexpr int kWords = N * (int)sizeof(T) / 4;
     uint32_t w[kWords];
 #pragma unroll
@@ -308,10 +310,54 @@ __device__ __forceinline__ void store_each(const MatmulArgs& a, int x, int y0, c
   }
 }
 
+// A warp's 32 rows of N outputs and their addend in rows of any place: 16 columns
+// at a time through the warp's shared memory (16-byte pieces turned as below), then
+// lanes along the rows, two at a time, so that a store or load covers pieces of
+// rows and not one element in each of 32.
+template <typename T, int N>
+__device__ __forceinline__ void store_spread(const MatmulArgs& a, uint32_t buffer, int lane, int row0, int col0,
+                                             const float (&v)[N]) {
+  const int c = lane & 15, r0 = lane >> 4;
+  uint32_t add[N];                    // the addend, all of it on its way at once
+  if (a.addend != nullptr) {
+#pragma unroll
+    for (int part = 0; part < N; part += 16) {
+      const int col = col0 + part + c, rows = col < a.ny ? a.nx - row0 - r0 : 0;       // rows from r0 on
+      const T* p = static_cast<const T*>(a.addend) + place(a, a.addend_pitch, row0 + r0, col);
+#pragma unroll
+      for (int k = 0; k < 16; ++k, p += 2 * a.addend_pitch) add[part + k] = bits_if(p, 2 * k < rows);
+    }
+  }
+#pragma unroll
+  for (int part = 0; part < N; part += 16) {
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");      // a copy before has read it
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};"
+                   ::"r"(buffer + 64 * lane + 16 * (i ^ ((lane >> 1) & 3))), "f"(v[part + 4 * i]),
+                     "f"(v[part + 4 * i + 1]), "f"(v[part + 4 * i + 2]), "f"(v[part + 4 * i + 3]) : "memory");
+    __syncwarp();
+    const int col = col0 + part + c, rows = col < a.ny ? a.nx - row0 - r0 : 0;
+    T* out = static_cast<T*>(a.out) + place(a, a.out_pitch, row0 + r0, col);
+    float s[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const int r = 2 * k + r0;
+      asm volatile("ld.shared.f32 %0, [%1];"
+                   : "=f"(s[k]) : "r"(buffer + 64 * r + 16 * ((c >> 2) ^ ((r >> 1) & 3)) + 4 * (c & 3)));
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k, out += 2 * a.out_pitch)
+      if (2 * k < rows) put(out, a.addend != nullptr ? s[k] + u2f(add[part + k]) : s[k]);
+    __syncwarp();
+  }
+}
+
 // A warp's 32 rows of 64 bytes, by TMA from its 2 KB of shared memory (64-byte
 // swizzle: 16-byte pieces turned by half the row, so that neither side meets
 // bank conflicts).  Rows beyond the matrix are left out by the copy; columns would
-// be only in pieces of 16 bytes, so a row's ragged end is stored by element.
+// be only in pieces of 16 bytes, so a row's ragged end goes another way.
 // For the widest tile, whose lines a warp leaves in four or eight pieces: 8192 x
 // 2304 x 768 took 18.0 us with each lane storing its own row, 16.6 this way;
 // 1024 x 4096 x 8191 to fp32 32.7 and 31.3.  Narrower tiles gain nothing: 256 x
@@ -410,7 +456,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     *failed = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 3 && lane < (L::kOutBytes > 0 ? 5 : 4)) {
+  if (warp == 3 && lane < (NT == 256 ? 5 : 4)) {
     const CUtensorMap* maps[5] = {&map_x, &map_y, &map_sx, &map_sy, &map_out};
     asm volatile("prefetch.tensormap [%0];" ::"l"(maps[lane]) : "memory");
   }
@@ -563,7 +609,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         __syncwarp();
         if (lane == 0) bar_arrive_cluster(free_at);
       }
-      Outputs<T, C> o[2];
+      Addend<T, C> o[2];
       if (!joined && chunks > 0) o[0].load(a, x, y0 + column(0));
       if (!warp_wait(done + 8 * (i & 1), (uint32_t)(i >> 1) & 1u, a.wait_ns)) {
         *failed = 1;
@@ -585,12 +631,14 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
           if (lane == 0) bar_arrive_cluster(L::kOverlap ? free_at : free_at + 8 * (i & 1));
         }
         if (!joined) {
-          o[j & 1].sum(a, x, v);
-          if constexpr (L::kOutBytes > 0) {
-            if (a.staged && y0 + c + C <= a.ny) store_staged<T>(&map_out, buffer, lane, x0, y0 + c, x0 < a.nx, v);
-            else store_each<T>(a, x, y0 + c, v);
-          } else {
-            store_each<T>(a, x, y0 + c, v);
+          if (a.swap || whole(a, C, y0 + c)) {
+            o[j & 1].sum(a, x, v);
+            if constexpr (C * sizeof(T) == 64 && NT == 256)
+              store_staged<T>(&map_out, buffer, lane, x0, y0 + c, x0 < a.nx, v);
+            else
+              store_lanes<T>(a, x, y0 + c, v);
+          } else if (y0 + c < a.ny) {
+            store_spread<T>(a, buffer, lane, x0, y0 + c, v);
           }
         } else {
           float* part = reinterpret_cast<float*>(smem);
@@ -608,7 +656,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
       if (chunks == 0 && lane == 0) bar_arrive_cluster(free_at + 8 * (i & 1));
     }
     // the last copy has read the buffer; what it writes is complete when the grid is
-    if (L::kOutBytes > 0 && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   }
 
   __syncwarp();
@@ -744,16 +792,18 @@ cudaError_t launch(const Operand& x, const Operand& y, int64_t k, MatmulArgs a, 
   a.x_tiles = (int)xt;
   a.y_tiles = (int)yt;
   a.split = split;
-  // rows of 64 bytes by TMA: 16-byte aligned rows of out, as they lie in it
-  a.staged = NT == 256 && ((uintptr_t)a.out & 15u) == 0 &&
-             (x.rows == 1 || a.out_pitch * (int64_t)sizeof(T) % 16 == 0);
+  const auto fits = [&](const void* p, int64_t pitch, int64_t to) {
+    return ((uintptr_t)p & (uintptr_t)(to - 1)) == 0 && (x.rows == 1 || pitch * (int64_t)sizeof(T) % to == 0);
+  };
+  a.wide = !a.swap && fits(a.out, a.out_pitch, NT == 256 ? 16 : 32) &&
+           (a.addend == nullptr || fits(a.addend, a.addend_pitch, 32));
   CUtensorMap mx, my, msx, msy, mo;
   if (encode_fn() == nullptr || !codes_map(&mx, x.codes, k, x.rows, x.pitch, 128) ||
       !codes_map(&my, y.codes, k, y.rows, y.pitch, L::kY) ||
       !scales_map(&msx, x.scales, (x.rows + 127) / 128 * a.panel) ||
-      !scales_map(&msy, y.scales, (y.rows + 127) / 128 * a.panel) || (a.staged && !out_map<T>(&mo, a)))
+      !scales_map(&msy, y.scales, (y.rows + 127) / 128 * a.panel) || (NT == 256 && a.wide && !out_map<T>(&mo, a)))
     return cudaErrorInvalidValue;
-  if (!a.staged) mo = mx;      // not used
+  if (NT != 256 || !a.wide) mo = mx;      // not used
   const int per = CG == 2 ? 2 : split;
   const int64_t tiles = xt * yt, slots = sm_count / per;
   cudaLaunchConfig_t cfg = {};
@@ -779,14 +829,15 @@ cudaError_t launch(const Operand& x, const Operand& y, int64_t k, MatmulArgs a, 
 // forms: 256 x 4096 x 4096 takes 9.8 us in 128-wide tiles, 10.1 in pairs of 128,
 // 14.2 in pairs of 256 and 12.2 split in two; 2048 x 4096 x 4096 31.8, 27.4 and
 // 25.5; 8192 x 2304 x 768 22.8, 22.2 and 16.6; 64 x 4096 x 4096 9.0 whole, 8.3
-// split in four.
+// split in four.  Rows of codes that do not start on lines (`on_lines` false) cost
+// twice L2's accesses: 773 x 10368 x 8847 takes 111, 110 and 92 us.
 struct Plan {
   int swap, cg, nt, split;
 };
-Plan plan(int64_t m, int64_t n, int blocks, const int (&clusters)[4]) {
-  static const struct { int cg, nt, block, least, tile, split; } kForms[] = {
-      {1, 16, 155, 1000, 400, 2300}, {1, 32, 165, 1000, 400, 2500},   {1, 64, 185, 1500, 400, 3300},
-      {1, 128, 208, 2000, 400, 6200}, {2, 128, 175, 2000, 400, 0}, {2, 256, 320, 1900, 900, 0}};
+Plan plan(int64_t m, int64_t n, int blocks, bool on_lines, const int (&clusters)[4]) {
+  static const struct { int cg, nt, block, off_line, least, tile, split; } kForms[] = {
+      {1, 16, 155, 220, 1000, 400, 2300}, {1, 32, 165, 245, 1000, 400, 2500},   {1, 64, 185, 295, 1500, 400, 3300},
+      {1, 128, 208, 385, 2000, 400, 5000}, {2, 128, 175, 300, 2000, 400, 0}, {2, 256, 320, 400, 1900, 900, 0}};
   constexpr double kStart = 3500, kPair = 800;
   Plan best = {0, 2, 256, 1};
   double least = 1e300;
@@ -800,7 +851,7 @@ Plan plan(int64_t m, int64_t n, int blocks, const int (&clusters)[4]) {
       for (int split = 1; split <= (f.cg == 2 ? 1 : 8) && split <= panel; split *= 2) {
         const int64_t slots = clusters[f.cg == 2 ? 1 : split == 1 ? 0 : split == 2 ? 1 : split == 4 ? 2 : 3];
         const int64_t waves = (tiles + slots - 1) / slots;
-        const double each = (double)((blocks + split - 1) / split) * f.block, out = waves > 1 ? f.least : 0;
+        const double each = (double)((blocks + split - 1) / split) * (on_lines ? f.block : f.off_line), out = waves > 1 ? f.least : 0;
         double time = (double)waves * ((each > out ? each : out) + f.tile) + (f.cg == 2 ? kPair : 0);
         if (split > 1) time += (double)waves * f.split + (double)(waves - 1) * kStart;
         if (time < least) {
@@ -852,11 +903,6 @@ cudaError_t dispatch(const opt_matmul_args& c, int sm_count, cudaStream_t s) {
   a.addend = c.d_addend;
   a.out_pitch = c.out_pitch;
   a.addend_pitch = c.addend_pitch;
-  const auto fits = [&](const void* p, int64_t pitch) {
-    return ((uintptr_t)p & 31u) == 0 && (c.m == 1 || pitch * (int64_t)sizeof(T) % 32 == 0);
-  };
-  a.vec = c.d_addend != nullptr && fits(c.d_addend, c.addend_pitch);
-  a.vec_out = fits(c.d_out, c.out_pitch);
   if (c.k == 0) {
     a.nx = (int)c.m;
     a.ny = (int)c.n;
@@ -874,7 +920,8 @@ cudaError_t dispatch(const opt_matmul_args& c, int sm_count, cudaStream_t s) {
   const Operand ops[2] = {{c.d_a, c.d_a_scales, c.a_pitch, c.m}, {c.d_b, c.d_b_scales, c.b_pitch, c.n}};
   int clusters[4];
   if (const cudaError_t e = active_clusters(sm_count, clusters); e != cudaSuccess) return e;
-  const Plan p = plan(c.m, c.n, a.blocks, clusters);
+  const auto on_lines = [](const Operand& o) { return (o.rows == 1 || o.pitch % 128 == 0) && ((uintptr_t)o.codes & 127u) == 0; };
+  const Plan p = plan(c.m, c.n, a.blocks, on_lines(ops[0]) && on_lines(ops[1]), clusters);
   a.swap = p.swap;
   const Operand &x = ops[p.swap], &y = ops[1 - p.swap];
   switch (p.nt) {

@@ -13,7 +13,6 @@ struct OutputArgs {
   const void* addend;
   int64_t out_pitch, addend_pitch;
   int swap;
-  int vec;                   // rows of addend allow 32-byte loads
 };
 
 __device__ __forceinline__ void put(Bf16* p, float v) { p->bits = (uint16_t)bf16_pair(v, 0.0f); }

@@ -204,18 +204,16 @@ __device__ __forceinline__ void dweight_slab(const opt_rms_norm_backward_args& a
     const int rows = (int)a.rows;
     const int of = 2 * warps;
     for (int r0 = 2 * warp + (lane >> 4); r0 < rows; r0 += 8 * of) {      // eight rows' loads together
-      float g[8] = {}, v[8] = {}, scale[8] = {};
+      uint32_t g[8], v[8], scale[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int r = r0 + k * of;
-        if (r < rows) {
-          g[k] = element(dy + r * a.dy_pitch);
-          v[k] = element(h + r * a.h_pitch);
-          scale[k] = a.d_rstd[r];
-        }
+        g[k] = bits_if(dy + r * a.dy_pitch, r < rows);
+        v[k] = bits_if(h + r * a.h_pitch, r < rows);
+        scale[k] = bits_if(a.d_rstd + r, r < rows);
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) s = fmaf(g[k], v[k] * scale[k], s);
+      for (int k = 0; k < 8; ++k) s = fmaf(u2f(g[k]), u2f(v[k]) * u2f(scale[k]), s);
     }
   }
   s += __shfl_xor_sync(0xFFFFFFFFu, s, 16);

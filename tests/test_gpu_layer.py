@@ -350,6 +350,23 @@ def test_matmul_exact_sums():
         assert torch.equal(out.cpu(), ia @ ib.T)
 
 
+@pytest.mark.parametrize("m,n,k", [(1, 300, 200), (40, 300, 1000), (300, 520, 77), (700, 1100, 1300)])
+def test_matmul_pitch_of_codes(m, n, k):
+    """The same bits from rows of any pitch that is a multiple of 16."""
+    a, sa = operand(m, k, 1, 48)
+    b, sb = operand(n, k, 1, 49)
+    want, out = torch.empty(m, n, device="cuda"), torch.empty(m, n, device="cuda")
+    ps.opt_matmul(a, sa, b, sb, want)
+    for pitch in (-(-k // 16) * 16, -(-k // 16) * 16 + 48):
+        wide = []
+        for t in (a, b):
+            w = torch.full((t.shape[0], pitch), 0x7F, dtype=torch.uint8, device="cuda")[:, :k]      # NaN between the rows
+            w.copy_(t)
+            wide.append(w)
+        ps.opt_matmul(wide[0], sa, wide[1], sb, out)
+        assert torch.equal(out, want)
+
+
 def test_matmul_in_place_sum_depth_zero_and_nan():
     a, sa = operand(70, 200, 1, 50)
     b, sb = operand(90, 200, 1, 51)
