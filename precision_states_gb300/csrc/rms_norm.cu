@@ -10,10 +10,10 @@
 // too wide for that (over 16,384 columns) take a second form that reads them twice.
 //
 // Sums over a row, rstd and the weight's gradient are fp32 throughout; outputs are
-// rounded once.  rstd is rsqrtf, within 2 units in the last place.
+// rounded once.
 //
 // Forward, 16384 x 4096 BF16 with a residual to h and codes: 72.3 us without
-// dropout, 6.5 TB/s (0.97 of the measured copy), bound by memory; 87.6 us with it
+// dropout, 6.5 TB/s (0.97 of the measured copy), bound by memory; 88.6 us with it
 // (0.80), bound by the generator's integer work (267 instructions per eight
 // elements, issue 65 % busy).  Two chunks per thread at 256 threads and three CTAs
 // per SM: one chunk at 512 threads took 98.3 us, four at 128 threads 108.7, four
@@ -31,6 +31,15 @@ namespace {
 
 constexpr int kWideThreads = 512;       // of the form that reads rows twice
 constexpr int kDweightCols = 32, kDweightParts = 32, kSlabCols = 16;
+
+// 1 / sqrt(v): rsqrtf, whose error of up to two units in the last place would move
+// a block's scale where its largest value lies that near to a power of two times
+// 448, and one Newton step (r += r (1 - v r^2) / 2), for positive finite v.
+__device__ __forceinline__ float reciprocal_root(float v) {
+  const float r = rsqrtf(v);
+  const float half_error = fmaf(-0.5f * v * r, r, 0.5f);
+  return r > 0.0f && r < 1e30f ? fmaf(r, half_error, r) : r;
+}
 
 // Chunk c (eight elements) of row r of h = residual + dropout(x).
 template <typename T, bool VEC>
@@ -119,7 +128,7 @@ __global__ void __launch_bounds__(MAX, CTAS) rms_norm_kernel(const __grid_consta
     float sum, second;
     unpk(sums, sum, second);
     sum = cta_sum(sum + second, part[turn], BY_WARP ? 1 : of_row >> 5);
-    const float rstd = rsqrtf(fmaf(sum, inv_cols, a.eps));
+    const float rstd = reciprocal_root(fmaf(sum, inv_cols, a.eps));
     if (in_row == 0 && a.d_rstd != nullptr) a.d_rstd[r] = rstd;
 #pragma unroll
     for (int k = 0; k < NG; ++k) write_chunk<T, VEC>(a, r, column(k), valid(k), rstd, panel, h[k], w[k], ragged.of_warp());
@@ -145,7 +154,7 @@ __global__ void __launch_bounds__(kWideThreads) rms_norm_wide_kernel(const __gri
       for (int j = 0; j < 8; ++j) sum = fmaf(h[j], h[j], sum);
     }
     sum = cta_sum(sum, part[turn], kWideThreads / 32);
-    const float rstd = rsqrtf(fmaf(sum, 1.0f / (float)a.cols, a.eps));
+    const float rstd = reciprocal_root(fmaf(sum, 1.0f / (float)a.cols, a.eps));
     if (threadIdx.x == 0 && a.d_rstd != nullptr) a.d_rstd[r] = rstd;
     for (int64_t c0 = 0; c0 < a.cols; c0 += 8 * kWideThreads) {
       const int64_t c = c0 + 8 * threadIdx.x;
