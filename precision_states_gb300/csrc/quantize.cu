@@ -160,16 +160,19 @@ quantize_kernel(const __grid_constant__ opt_quantize_args a, int64_t col_tiles) 
   Raw<T> raw[8];
   {
     const T* x = static_cast<const T*>(a.d_x);
-    const T* end = x + (a.rows - 1) * a.x_pitch + a.cols;
-    const T* p = x + (r0 + l) * a.x_pitch + c0 + c;
+    const T* p = x + (r0 + l) * a.x_pitch + c0;
+    const auto row = [&](int i) {
+      return Row<T, VEC>(p + i * a.x_pitch, x, x + (a.rows - 1) * a.x_pitch + a.cols);
+    };
+    const auto valid = [&](int i) { return l + i < rows ? max(min(cols - c, 8), 0) : 0; };
+    Ahead<T, VEC> ahead[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i, p += a.x_pitch) {
-      raw[i] = Raw<T>{};
-      if (l + i < rows && c < cols) {
-        if constexpr (VEC) raw[i] = load_raw<true>(p, 8);
-        else raw[i] = load_ragged(p, min(cols - c, 8), x, end);
-      }
+    for (int i = 0; i < 8; ++i) {
+      ahead[i] = {};
+      if (!VEC || valid(i) > 0) ahead[i] = row(i).ahead(c, valid(i));
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) raw[i] = row(i).chunk(ahead[i], c, valid(i));
   }
 
   // the tile's one block

@@ -22,8 +22,8 @@
 // the CTAs' rows takes 4; one chunk per thread at 512 threads and two CTAs per SM
 // (fp32 too, in spite of some spilled registers: 8000 x 4096 120.5 us, 162.6 with one).  Few rows are launches'
 // latency: one token of 4,096 2.6 us.  Rows that begin anywhere (odd widths and pitches) are
-// loaded by words and stored through shared memory: 8000 x 4001 BF16 to y 54.6 us
-// (94.8 element by element), the backward pass 135 (271).
+// loaded by words and stored through shared memory: 8000 x 4001 BF16 to y 47.7 us
+// (94.8 element by element), the backward pass 141 (271).
 #include "layer.cuh"
 
 namespace psopt {
@@ -44,17 +44,19 @@ __device__ __forceinline__ float reciprocal_root(float v) {
 // Chunk c (eight elements) of row r of h = residual + dropout(x).
 template <typename T, bool VEC>
 __device__ __forceinline__ void h_chunk(const opt_rms_norm_args& a, const DropArgs& d, int64_t r, int64_t c,
-                                        const Raw<T>& x_raw, const Raw<T>& res_raw, float (&h)[8]) {
+                                        int valid, const Ahead<T, VEC>& x_ahead, const Ahead<T, VEC>& res_ahead,
+                                        float (&h)[8]) {
   float x[8];
-  unpack(x_raw, x);
-  unpack(res_raw, h);
+  unpack(Row<T, VEC>(a.d_x, a.x_pitch, a.rows, a.cols, r).chunk(x_ahead, c, valid), x);
+  unpack(Row<T, VEC>(a.d_residual, a.residual_pitch, a.rows, a.cols, r)
+             .chunk(res_ahead, c, a.d_residual != nullptr ? valid : 0), h);
   add_dropped8<VEC>(h, x, (uint64_t)(r * a.cols + c), d);
 }
 template <typename T, bool VEC>
-__device__ __forceinline__ void load_chunk(const opt_rms_norm_args& a, int64_t r, int64_t c, int valid, Raw<T>& x,
-                                           Raw<T>& res) {
-  x = load_at<VEC, T>(a.d_x, a.x_pitch, a.rows, a.cols, r, c, valid);
-  if (a.d_residual != nullptr) res = load_at<VEC, T>(a.d_residual, a.residual_pitch, a.rows, a.cols, r, c, valid);
+__device__ __forceinline__ void load_chunk(const opt_rms_norm_args& a, int64_t r, int64_t c, int valid,
+                                           Ahead<T, VEC>& x, Ahead<T, VEC>& res) {
+  x = Row<T, VEC>(a.d_x, a.x_pitch, a.rows, a.cols, r).ahead(c, valid);
+  if (a.d_residual != nullptr) res = Row<T, VEC>(a.d_residual, a.residual_pitch, a.rows, a.cols, r).ahead(c, valid);
 }
 
 // Everything that is written of a chunk, by whole warps; chunks beyond the row
@@ -97,27 +99,27 @@ __global__ void __launch_bounds__(MAX, CTAS) rms_norm_kernel(const __grid_consta
   const float inv_cols = 1.0f / (float)cols;
   const auto column = [&](int k) { return 8 * (in_row + k * of_row); };
   const auto valid = [&](int k) { return VEC ? (column(k) < cols ? 8 : 0) : max(min(cols - column(k), 8), 0); };
+  const Row<W, VEC> weight(a.d_weight, 0, 1, a.cols, 0);
   float w[NG][8];
-  Raw<T> x[NG] = {}, res[NG] = {};
+  Ahead<T, VEC> x[NG] = {}, res[NG] = {};
+  Ahead<W, VEC> w_ahead[NG] = {};
 #pragma unroll
   for (int k = 0; k < NG; ++k) {
-    if (valid(k) > 0) {
-      if (row0 < a.rows) load_chunk<T, VEC>(a, row0, column(k), valid(k), x[k], res[k]);
-      unpack(load_at<VEC, W>(a.d_weight, 0, 1, a.cols, 0, column(k), valid(k)), w[k]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w[k][j] = 0.0f;
-    }
+    if (VEC && valid(k) <= 0) continue;
+    if (row0 < a.rows) load_chunk<T, VEC>(a, row0, column(k), valid(k), x[k], res[k]);
+    w_ahead[k] = weight.ahead(column(k), valid(k));
   }
+#pragma unroll
+  for (int k = 0; k < NG; ++k) unpack(weight.chunk(w_ahead[k], column(k), valid(k)), w[k]);
   int turn = 0;
   for (int64_t r = row0; r < a.rows; r += row_step, turn ^= 1) {
     float h[NG][8];
     f2_t sums = 0;                    // +0 in both lanes
 #pragma unroll
     for (int k = 0; k < NG; ++k) {
-      h_chunk<T, VEC>(a, d, r, column(k), x[k], res[k], h[k]);
+      h_chunk<T, VEC>(a, d, r, column(k), valid(k), x[k], res[k], h[k]);
       // the next row, while this one's sum is formed
-      if (valid(k) > 0 && r + row_step < a.rows)
+      if ((!VEC || valid(k) > 0) && r + row_step < a.rows)
         load_chunk<T, VEC>(a, r + row_step, column(k), valid(k), x[k], res[k]);
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
@@ -146,10 +148,12 @@ __global__ void __launch_bounds__(kWideThreads) rms_norm_wide_kernel(const __gri
   int turn = 0;
   for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, turn ^= 1) {
     float sum = 0.0f, h[8], w[8];
-    Raw<T> x, res = {};
+    Ahead<T, VEC> x, res = {};
+    const Row<W, VEC> weight(a.d_weight, 0, 1, a.cols, 0);
     for (int64_t c = 8 * threadIdx.x; c < a.cols; c += 8 * kWideThreads) {
-      load_chunk<T, VEC>(a, r, c, (int)min(a.cols - c, (int64_t)8), x, res);
-      h_chunk<T, VEC>(a, d, r, c, x, res, h);
+      const int valid = (int)min(a.cols - c, (int64_t)8);
+      load_chunk<T, VEC>(a, r, c, valid, x, res);
+      h_chunk<T, VEC>(a, d, r, c, valid, x, res, h);
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum = fmaf(h[j], h[j], sum);
     }
@@ -161,8 +165,8 @@ __global__ void __launch_bounds__(kWideThreads) rms_norm_wide_kernel(const __gri
       const int valid = (int)max(min(a.cols - c, (int64_t)8), (int64_t)0);
       if (valid > 0) {
         load_chunk<T, VEC>(a, r, c, valid, x, res);
-        h_chunk<T, VEC>(a, d, r, c, x, res, h);
-        unpack(load_at<VEC, W>(a.d_weight, 0, 1, a.cols, 0, c, valid), w);
+        h_chunk<T, VEC>(a, d, r, c, valid, x, res, h);
+        unpack(weight.chunk(weight.ahead(c, valid), c, valid), w);
       }
       write_chunk<T, VEC>(a, r, c, valid, rstd, panel, h, w, ragged.of_warp());
     }
@@ -250,18 +254,22 @@ __global__ void __launch_bounds__(MAX, CTAS) rms_norm_backward_kernel(
   const auto column = [&](int k) { return 8 * (int)(threadIdx.x + k * blockDim.x); };
   const auto valid = [&](int k) { return VEC ? (column(k) < cols ? 8 : 0) : max(min(cols - column(k), 8), 0); };
   float dw[NG][8] = {};
-  Raw<W> w[NG] = {};
-  Raw<T> dy[NG] = {}, h[NG] = {}, in[NG] = {};
+  const Row<W, VEC> weight(a.d_weight, 0, 1, a.cols, 0);
+  const auto dy_row = [&](int64_t r) { return Row<T, VEC>(a.d_dy, a.dy_pitch, a.rows, a.cols, r); };
+  const auto h_row = [&](int64_t r) { return Row<T, VEC>(a.d_h, a.h_pitch, a.rows, a.cols, r); };
+  const auto in_row = [&](int64_t r) { return Row<T, VEC>(a.d_dh_in, a.dh_in_pitch, a.rows, a.cols, r); };
+  Ahead<W, VEC> w[NG] = {};
+  Ahead<T, VEC> dy[NG] = {}, h[NG] = {}, in[NG] = {};
   constexpr bool AHEAD = MAX < 1024;
   const auto load = [&](int k, int64_t r) {
-    dy[k] = load_at<VEC, T>(a.d_dy, a.dy_pitch, a.rows, a.cols, r, column(k), valid(k));
-    h[k] = load_at<VEC, T>(a.d_h, a.h_pitch, a.rows, a.cols, r, column(k), valid(k));
+    dy[k] = dy_row(r).ahead(column(k), valid(k));
+    h[k] = h_row(r).ahead(column(k), valid(k));
   };
 #pragma unroll
   for (int k = 0; k < NG; ++k) {
-    if (AHEAD && valid(k) > 0) {
+    if (AHEAD && (!VEC || valid(k) > 0)) {
       load(k, blockIdx.x);
-      w[k] = load_at<VEC, W>(a.d_weight, 0, 1, a.cols, 0, column(k), valid(k));
+      w[k] = weight.ahead(column(k), valid(k));
     }
   }
   int turn = 0;
@@ -270,19 +278,22 @@ __global__ void __launch_bounds__(MAX, CTAS) rms_norm_backward_kernel(
     float g[NG][8], hv[NG][8], sum = 0.0f;
     if (!AHEAD) {
 #pragma unroll
-      for (int k = 0; k < NG; ++k)
-        if (valid(k) > 0) load(k, r);
+      for (int k = 0; k < NG; ++k) {
+        dy[k] = h[k] = {};          // nothing of the row before to be kept
+        w[k] = {};
+        if (VEC && valid(k) <= 0) continue;
+        load(k, r);
+        w[k] = weight.ahead(column(k), valid(k));
+      }
     }
 #pragma unroll
     for (int k = 0; k < NG; ++k) {
       float wv[8];
-      if (!AHEAD && valid(k) > 0) w[k] = load_at<VEC, W>(a.d_weight, 0, 1, a.cols, 0, column(k), valid(k));
-      unpack(dy[k], g[k]);
-      unpack(h[k], hv[k]);
-      unpack(w[k], wv);
-      if (AHEAD && a.d_dh_in != nullptr && valid(k) > 0)
-        in[k] = load_at<VEC, T>(a.d_dh_in, a.dh_in_pitch, a.rows, a.cols, r, column(k), valid(k));
-      if (AHEAD && valid(k) > 0 && r + row_ctas < a.rows) load(k, r + row_ctas);
+      unpack(dy_row(r).chunk(dy[k], column(k), valid(k)), g[k]);
+      unpack(h_row(r).chunk(h[k], column(k), valid(k)), hv[k]);
+      unpack(weight.chunk(w[k], column(k), valid(k)), wv);
+      if (AHEAD && a.d_dh_in != nullptr && (!VEC || valid(k) > 0)) in[k] = in_row(r).ahead(column(k), valid(k));
+      if (AHEAD && (!VEC || valid(k) > 0) && r + row_ctas < a.rows) load(k, r + row_ctas);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         dw[k][j] = fmaf(g[k][j], hv[k][j] * rstd, dw[k][j]);
@@ -296,9 +307,9 @@ __global__ void __launch_bounds__(MAX, CTAS) rms_norm_backward_kernel(
     for (int k = 0; k < NG; ++k)
       if (!VEC || valid(k) > 0) {
         float add[8];
-        if (!AHEAD && a.d_dh_in != nullptr && valid(k) > 0)
-          in[k] = load_at<VEC, T>(a.d_dh_in, a.dh_in_pitch, a.rows, a.cols, r, column(k), valid(k));
-        unpack(in[k], add);
+        if (!AHEAD) in[k] = {};
+        if (!AHEAD && a.d_dh_in != nullptr) in[k] = in_row(r).ahead(column(k), valid(k));
+        unpack(in_row(r).chunk(in[k], column(k), a.d_dh_in != nullptr ? valid(k) : 0), add);
         write_gradients<T, VEC>(a, d, r, column(k), valid(k), rstd, scale, g[k], hv[k], add, ragged.of_warp());
       }
   }
@@ -330,12 +341,18 @@ __global__ void __launch_bounds__(kWideThreads) rms_norm_backward_wide_kernel(
     return;
   }
   float* dw = a.d_dweight == nullptr || dweight_here(a) ? nullptr : dweight_row(a, blockIdx.x);
+  const Row<W, VEC> weight(a.d_weight, 0, 1, a.cols, 0);
+  const auto dy_row = [&](int64_t r) { return Row<T, VEC>(a.d_dy, a.dy_pitch, a.rows, a.cols, r); };
+  const auto h_row = [&](int64_t r) { return Row<T, VEC>(a.d_h, a.h_pitch, a.rows, a.cols, r); };
+  const auto in_row = [&](int64_t r) { return Row<T, VEC>(a.d_dh_in, a.dh_in_pitch, a.rows, a.cols, r); };
   int turn = 0;
   for (int64_t r = blockIdx.x; r < a.rows; r += row_ctas, turn ^= 1) {
     const auto load = [&](int64_t c, int valid, float (&g)[8], float (&h)[8], float (&w)[8]) {
-      unpack(load_at<VEC, T>(a.d_dy, a.dy_pitch, a.rows, a.cols, r, c, valid), g);
-      unpack(load_at<VEC, T>(a.d_h, a.h_pitch, a.rows, a.cols, r, c, valid), h);
-      unpack(load_at<VEC, W>(a.d_weight, 0, 1, a.cols, 0, c, valid), w);
+      const Ahead<T, VEC> g_ahead = dy_row(r).ahead(c, valid), h_ahead = h_row(r).ahead(c, valid);
+      const Ahead<W, VEC> w_ahead = weight.ahead(c, valid);
+      unpack(dy_row(r).chunk(g_ahead, c, valid), g);
+      unpack(h_row(r).chunk(h_ahead, c, valid), h);
+      unpack(weight.chunk(w_ahead, c, valid), w);
     };
     float sum = 0.0f;
     for (int64_t c = 8 * threadIdx.x; c < a.cols; c += 8 * kWideThreads) {
@@ -359,7 +376,8 @@ __global__ void __launch_bounds__(kWideThreads) rms_norm_backward_wide_kernel(
             dw[c + j] = fmaf(g[j], h[j] * rstd, r == (int64_t)blockIdx.x ? 0.0f : dw[c + j]);
           g[j] *= w[j];
         }
-        if (a.d_dh_in != nullptr) unpack(load_at<VEC, T>(a.d_dh_in, a.dh_in_pitch, a.rows, a.cols, r, c, valid), in);
+        if (a.d_dh_in != nullptr)
+          unpack(in_row(r).chunk(in_row(r).ahead(c, valid), c, valid), in);
       }
       if (!VEC || valid > 0) write_gradients<T, VEC>(a, d, r, c, valid, rstd, k, g, h, in, ragged.of_warp());
     }
@@ -414,7 +432,14 @@ cudaError_t forward_vec(const opt_rms_norm_args& a, const DropArgs& d, int sm_co
   if (chunks <= 256) return forward_rows<T, W, VEC, false, 1, 256, 4>(a, d, sm_count, threads, s);
   if (chunks <= 512) return forward_rows<T, W, VEC, false, 2, 256, 3>(a, d, sm_count, (int)((chunks + 63) / 64) * 32, s);
   if (chunks <= 1024) return forward_rows<T, W, VEC, false, 2, 512, 1>(a, d, sm_count, (int)((chunks + 63) / 64) * 32, s);
-  if (chunks <= 2048) return forward_rows<T, W, VEC, false, 4, 512, 1>(a, d, sm_count, (int)((chunks + 127) / 128) * 32, s);
+  // BF16: two chunks of 1,024 threads (4853 x 12440 80.9 us, four of 512 90.7; without
+  // whole chunks, 12435, 203.7 and 267.6); fp32's registers want the latter (161.5, 167.1)
+  if (chunks <= 2048) {
+    if constexpr (sizeof(T) == 2)
+      return forward_rows<T, W, VEC, false, 2, 1024, 1>(a, d, sm_count, (int)((chunks + 63) / 64) * 32, s);
+    else
+      return forward_rows<T, W, VEC, false, 4, 512, 1>(a, d, sm_count, (int)((chunks + 127) / 128) * 32, s);
+  }
   const int64_t most = (int64_t)sm_count * 4;
   rms_norm_wide_kernel<T, W, VEC><<<(unsigned)(a.rows < most ? a.rows : most), kWideThreads, 0, s>>>(a, d);
   return cudaGetLastError();
