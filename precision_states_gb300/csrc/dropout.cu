@@ -30,7 +30,7 @@ __device__ __forceinline__ void drop_chunk(const opt_dropout_args& a, const Drop
   float x[8], y[8];
   unpack(x_row.chunk(x_ahead, c, valid), x);
   unpack(res_row.chunk(res_ahead, c, res_valid), y);
-  add_dropped8<VEC>(y, x, (uint64_t)(r * a.cols + c), d);
+  add_dropped8<VEC>(y, x, (uint64_t)(r * a.cols + c), d, nullptr);      // (a barrier for a CTA's one row costs more)
   store_at<VEC>(a.d_y, a.y_pitch, a.cols, r, c, valid, y, buffer);
 }
 // A matrix's ragged end, element by element, so that it adds nothing to the main

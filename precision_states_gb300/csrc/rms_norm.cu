@@ -23,7 +23,7 @@
 // (fp32 too, in spite of some spilled registers: 8000 x 4096 120.5 us, 162.6 with one).  Few rows are launches'
 // latency: one token of 4,096 2.6 us.  Rows that begin anywhere (odd widths and pitches) are
 // loaded by words and stored through shared memory: 8000 x 4001 BF16 to y 47.7 us
-// (94.8 element by element), the backward pass 141 (271).
+// (94.8 element by element), the backward pass 125 (271).
 #include "layer.cuh"
 
 namespace psopt {
@@ -45,12 +45,12 @@ __device__ __forceinline__ float reciprocal_root(float v) {
 template <typename T, bool VEC>
 __device__ __forceinline__ void h_chunk(const opt_rms_norm_args& a, const DropArgs& d, int64_t r, int64_t c,
                                         int valid, const Ahead<T, VEC>& x_ahead, const Ahead<T, VEC>& res_ahead,
-                                        float (&h)[8]) {
+                                        const uint4* edge, float (&h)[8]) {
   float x[8];
   unpack(Row<T, VEC>(a.d_x, a.x_pitch, a.rows, a.cols, r).chunk(x_ahead, c, valid), x);
   unpack(Row<T, VEC>(a.d_residual, a.residual_pitch, a.rows, a.cols, r)
              .chunk(res_ahead, c, a.d_residual != nullptr ? valid : 0), h);
-  add_dropped8<VEC>(h, x, (uint64_t)(r * a.cols + c), d);
+  add_dropped8<VEC>(h, x, (uint64_t)(r * a.cols + c), d, edge);
 }
 template <typename T, bool VEC>
 __device__ __forceinline__ void load_chunk(const opt_rms_norm_args& a, int64_t r, int64_t c, int valid,
@@ -91,6 +91,7 @@ __global__ void __launch_bounds__(MAX, CTAS) rms_norm_kernel(const __grid_consta
                                                              const __grid_constant__ DropArgs d) {
   __shared__ float part[2][33];
   __shared__ __align__(16) Ragged<T, VEC, MAX / 32> ragged;
+  __shared__ __align__(16) Edges<VEC || BY_WARP, NG * (MAX / 32)> edges;
   const int in_row = BY_WARP ? (int)(threadIdx.x & 31) : (int)threadIdx.x, of_row = BY_WARP ? 32 : (int)blockDim.x;
   const int64_t row0 = BY_WARP ? (int64_t)blockIdx.x * (MAX / 32) + (threadIdx.x >> 5) : blockIdx.x;
   const int64_t row_step = BY_WARP ? (int64_t)gridDim.x * (MAX / 32) : gridDim.x;
@@ -111,13 +112,17 @@ __global__ void __launch_bounds__(MAX, CTAS) rms_norm_kernel(const __grid_consta
   }
 #pragma unroll
   for (int k = 0; k < NG; ++k) unpack(weight.chunk(w_ahead[k], column(k), valid(k)), w[k]);
+  if (!VEC && !BY_WARP) {
+    edges.put(0, (uint64_t)(row0 * a.cols), NG, d);
+    __syncthreads();
+  }
   int turn = 0;
   for (int64_t r = row0; r < a.rows; r += row_step, turn ^= 1) {
     float h[NG][8];
     f2_t sums = 0;                    // +0 in both lanes
 #pragma unroll
     for (int k = 0; k < NG; ++k) {
-      h_chunk<T, VEC>(a, d, r, column(k), valid(k), x[k], res[k], h[k]);
+      h_chunk<T, VEC>(a, d, r, column(k), valid(k), x[k], res[k], BY_WARP ? nullptr : edges.of_warp(turn, k), h[k]);
       // the next row, while this one's sum is formed
       if ((!VEC || valid(k) > 0) && r + row_step < a.rows)
         load_chunk<T, VEC>(a, r + row_step, column(k), valid(k), x[k], res[k]);
@@ -129,6 +134,7 @@ __global__ void __launch_bounds__(MAX, CTAS) rms_norm_kernel(const __grid_consta
     }
     float sum, second;
     unpk(sums, sum, second);
+    if (!VEC && !BY_WARP && r + row_step < a.rows) edges.put(turn ^ 1, (uint64_t)((r + row_step) * a.cols), NG, d);
     sum = cta_sum(sum + second, part[turn], BY_WARP ? 1 : of_row >> 5);
     const float rstd = reciprocal_root(fmaf(sum, inv_cols, a.eps));
     if (in_row == 0 && a.d_rstd != nullptr) a.d_rstd[r] = rstd;
@@ -153,7 +159,7 @@ __global__ void __launch_bounds__(kWideThreads) rms_norm_wide_kernel(const __gri
     for (int64_t c = 8 * threadIdx.x; c < a.cols; c += 8 * kWideThreads) {
       const int valid = (int)min(a.cols - c, (int64_t)8);
       load_chunk<T, VEC>(a, r, c, valid, x, res);
-      h_chunk<T, VEC>(a, d, r, c, valid, x, res, h);
+      h_chunk<T, VEC>(a, d, r, c, valid, x, res, nullptr, h);
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum = fmaf(h[j], h[j], sum);
     }
@@ -165,7 +171,7 @@ __global__ void __launch_bounds__(kWideThreads) rms_norm_wide_kernel(const __gri
       const int valid = (int)max(min(a.cols - c, (int64_t)8), (int64_t)0);
       if (valid > 0) {
         load_chunk<T, VEC>(a, r, c, valid, x, res);
-        h_chunk<T, VEC>(a, d, r, c, valid, x, res, h);
+        h_chunk<T, VEC>(a, d, r, c, valid, x, res, nullptr, h);
         unpack(weight.chunk(weight.ahead(c, valid), c, valid), w);
       }
       write_chunk<T, VEC>(a, r, c, valid, rstd, panel, h, w, ragged.of_warp());
@@ -179,14 +185,15 @@ __global__ void __launch_bounds__(kWideThreads) rms_norm_wide_kernel(const __gri
 template <typename T, bool VEC>
 __device__ __forceinline__ void write_gradients(const opt_rms_norm_backward_args& a, const DropArgs& d, int64_t r,
                                                 int64_t c, int valid, float rstd, float k, const float (&g)[8],
-                                                const float (&h)[8], const float (&in)[8], T* buffer) {
+                                                const float (&h)[8], const float (&in)[8], T* buffer,
+                                                const uint4* edge) {
   float out[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) out[j] = fmaf(rstd, fmaf(-h[j], k, g[j]), in[j]);
   store_at<VEC>(a.d_dh, a.dh_pitch, a.cols, r, c, valid, out, buffer);
   if (a.d_dx != nullptr) {
     float dx[8] = {};
-    add_dropped8<VEC>(dx, out, (uint64_t)(r * a.cols + c), d);
+    add_dropped8<VEC>(dx, out, (uint64_t)(r * a.cols + c), d, edge);
     store_at<VEC>(a.d_dx, a.dx_pitch, a.cols, r, c, valid, dx, buffer);
   }
 }
@@ -244,6 +251,7 @@ __global__ void __launch_bounds__(MAX, CTAS) rms_norm_backward_kernel(
     const __grid_constant__ opt_rms_norm_backward_args a, const __grid_constant__ DropArgs d, int row_ctas) {
   __shared__ float part[2][33];
   __shared__ __align__(16) Ragged<T, VEC, MAX / 32> ragged;
+  __shared__ __align__(16) Edges<VEC, NG * (MAX / 32)> edges;
   if ((int)blockIdx.x >= row_ctas) {
     dweight_slab<T>(a, (int)blockIdx.x - row_ctas);
     return;
@@ -301,6 +309,10 @@ __global__ void __launch_bounds__(MAX, CTAS) rms_norm_backward_kernel(
         sum = fmaf(g[k][j], hv[k][j], sum);
       }
     }
+    if (!VEC && a.d_dx != nullptr) {
+      edges.put(turn, (uint64_t)(r * a.cols), NG, d);
+      if (warps == 1) __syncwarp();
+    }
     sum = cta_sum(sum, part[turn], warps);
     const float scale = rstd * rstd * (sum * inv_cols);
 #pragma unroll
@@ -310,7 +322,8 @@ __global__ void __launch_bounds__(MAX, CTAS) rms_norm_backward_kernel(
         if (!AHEAD) in[k] = {};
         if (!AHEAD && a.d_dh_in != nullptr) in[k] = in_row(r).ahead(column(k), valid(k));
         unpack(in_row(r).chunk(in[k], column(k), a.d_dh_in != nullptr ? valid(k) : 0), add);
-        write_gradients<T, VEC>(a, d, r, column(k), valid(k), rstd, scale, g[k], hv[k], add, ragged.of_warp());
+        write_gradients<T, VEC>(a, d, r, column(k), valid(k), rstd, scale, g[k], hv[k], add, ragged.of_warp(),
+                                edges.of_warp(turn, k));
       }
   }
   if (a.d_dweight != nullptr && !dweight_here(a)) {
@@ -379,7 +392,7 @@ __global__ void __launch_bounds__(kWideThreads) rms_norm_backward_wide_kernel(
         if (a.d_dh_in != nullptr)
           unpack(in_row(r).chunk(in_row(r).ahead(c, valid), c, valid), in);
       }
-      if (!VEC || valid > 0) write_gradients<T, VEC>(a, d, r, c, valid, rstd, k, g, h, in, ragged.of_warp());
+      if (!VEC || valid > 0) write_gradients<T, VEC>(a, d, r, c, valid, rstd, k, g, h, in, ragged.of_warp(), nullptr);
     }
   }
 }

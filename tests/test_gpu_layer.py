@@ -183,6 +183,22 @@ def test_rms_norm_special_rows(cols):
     assert (y[4] == 0).all() and torch.allclose(y[5], x[5] * 1e3, rtol=1e-6, atol=0)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(6000, 261), (1500, 260), (2000, 2047), (1300, 4101), (400, 8201), (400, 12301), (400, 8200)])
+def test_rms_norm_drops_what_dropout_drops(dtype, rows, cols):
+    """Many rows per CTA, rows that begin anywhere among the generator's calls."""
+    x = matrix(rows, cols, dtype, 14)
+    w = torch.ones(cols, device="cuda")
+    want, h, y, rstd = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x), torch.empty(rows, device="cuda")
+    ps.opt_dropout(x, want, 0.3, **DRAW)
+    ps.opt_rms_norm(x, w, 1e-5, y=y, rstd=rstd, h=h, p=0.3, **DRAW)
+    assert torch.equal(h, want)
+    dh_in, dh, dx = torch.full_like(x, 64.0), torch.empty_like(x), torch.empty_like(x)
+    ps.opt_rms_norm_backward(x, h, w, rstd, dh, dh_in=dh_in, dx=dx, p=0.3, **DRAW)
+    ps.opt_dropout(torch.ones_like(x), want, 0.3, **DRAW)
+    assert (dh > 0).all() and torch.equal(dx != 0, want != 0)
+
+
 @pytest.mark.parametrize("dtype,wdtype", [("bf16", "f32"), ("bf16", "bf16"), ("f32", "f32"), ("f32", "bf16")])
 @pytest.mark.parametrize("rows,cols,pad", NORM_SHAPES)
 def test_rms_norm_backward(dtype, wdtype, rows, cols, pad):
