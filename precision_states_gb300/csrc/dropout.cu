@@ -22,7 +22,11 @@ constexpr int64_t kMaxGridX = (int64_t)1 << 30;
 template <typename T, bool VEC>
 __device__ __forceinline__ void drop_chunk(const opt_dropout_args& a, const DropArgs& d, int64_t r, int64_t c,
                                            int valid, T* buffer) {
-  const Row<T, VEC> x_row(a.d_x, a.x_pitch, a.rows, a.cols, r), res_row(a.d_residual, a.residual_pitch, a.rows, a.cols, r);
+  const auto row = [&](const void* base, int64_t pitch) {
+    const T* m = static_cast<const T*>(base);
+    return Row<T, VEC>(m + r * pitch, m, m + (a.rows - 1) * pitch + a.cols);
+  };
+  const Row<T, VEC> x_row = row(a.d_x, a.x_pitch), res_row = row(a.d_residual, a.residual_pitch);
   const int res_valid = a.d_residual != nullptr ? valid : 0;
   const Ahead<T, VEC> x_ahead = x_row.ahead(c, valid);
   Ahead<T, VEC> res_ahead = {};
