@@ -23,7 +23,7 @@
 // (fp32 too, in spite of some spilled registers: 8000 x 4096 120.5 us, 162.6 with one).  Few rows are launches'
 // latency: one token of 4,096 2.6 us.  Rows that begin anywhere (odd widths and pitches) are
 // loaded by words and stored through shared memory: 8000 x 4001 BF16 to y 47.7 us
-// (94.8 element by element), the backward pass 119 (271).
+// (94.8 element by element), the backward pass 109 (271).
 #include "layer.cuh"
 
 namespace psopt {
