@@ -541,7 +541,8 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     bool ok = true;
     for (int t = first; t < tiles && ok; t += step, ++i) {
       const uint32_t acc = tmem + (i & 1) * L::kAcc1;
-      if (L::kOverlap ? (i >= 1 && !warp_wait(free_, (uint32_t)(i - 1) & 1u, a.wait_ns))
+      // (overlapping accumulators: the release of the tile before, else of the one before that)
+      if (L::kOverlap ? (i >= 1 && !warp_wait(free_ + 8 * ((i - 1) & 1), (uint32_t)((i - 1) >> 1) & 1u, a.wait_ns))
                       : (i >= 2 && !warp_wait(free_ + 8 * (i & 1), (uint32_t)((i >> 1) - 1) & 1u, a.wait_ns))) {
         ok = false;
         break;
@@ -600,14 +601,18 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
       const int x0 = (tx * CG + (CG == 2 ? (int)rank : 0)) * 128 + q * 32, x = x0 + lane, y0 = ty * NT;
       // The shared columns first: the first accumulator's last ones, the second
       // one's first.  The half that has none frees them at once: what it
-      // stands for is that it has read the tile before.
+      // stands for is that it has read the tile before.  Tiles release in turn on
+      // two barriers: a warp may be a tile ahead of the others, so on one its
+      // arrival for this tile would count for the tile before, and the products
+      // would overwrite an accumulator that a slower warp still reads.  It is never
+      // two ahead: the next tile's products wait for this one's release.
       const bool down = L::kOverlap && (i & 1) == 0;
       const bool shares = L::kOverlap && half == (down ? 1 : 0);
       const auto column = [&](int j) { return half * kCols + (down ? kCols - C - j * C : j * C); };
       if (L::kOverlap && !shares) {
         fence_before();
         __syncwarp();
-        if (lane == 0) bar_arrive_cluster(free_at);
+        if (lane == 0) bar_arrive_cluster(free_at + 8 * (i & 1));
       }
       Addend<T, C> o[2];
       if (!joined && chunks > 0) o[0].load(a, x, y0 + column(0));
@@ -628,7 +633,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         if (L::kOverlap ? shares && j == 32 / C - 1 : j == chunks - 1) {
           fence_before();
           __syncwarp();
-          if (lane == 0) bar_arrive_cluster(L::kOverlap ? free_at : free_at + 8 * (i & 1));
+          if (lane == 0) bar_arrive_cluster(free_at + 8 * (i & 1));
         }
         if (!joined) {
           if (a.swap || whole(a, C, y0 + c)) {
