@@ -276,12 +276,16 @@ def opt_rms_norm_backward(dy, h, weight, rstd, dh, dh_in=None, dx=None, dweight=
 
 
 def _workspace(nbytes, device, stream):
-    """Scratch from torch's allocator that stays the call's until its stream has passed it."""
+    """Scratch from torch's allocator, out of the pool of the stream that uses it: a
+    block of another stream's may still be read or written by work pending there."""
     import torch
-    t = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
-    if stream is not None:
-        t.record_stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream)
-    return t
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        pointer = _stream_ptr(stream)
+        stream = torch.cuda.ExternalStream(0 if pointer == 1 else pointer, device=device)     # 1: the default stream by CUDA's other name
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 def opt_rms_norm_backward_workspace(rows: int, cols: int) -> int:
