@@ -32,14 +32,15 @@ struct FewArgs {
   const uint8_t* y;            // the short one
   const uint8_t* sy;
   int64_t x_pitch, y_pitch;
-  int nx, ny, k, panel;
+  int nx, ny, panel;
+  uint32_t k;                  // unsigned: a step beyond 2^31 - 1 must not wrap
   OutputArgs out;
 };
 
 // 16 codes at depth c of a row; those at or beyond k read as 0 (CHECK: there may
 // be such).
 template <bool CHECK>
-__device__ __forceinline__ uint4 load16(const uint8_t* row, int c, int k) {
+__device__ __forceinline__ uint4 load16(const uint8_t* row, uint32_t c, uint32_t k) {
   uint4 w = make_uint4(0u, 0u, 0u, 0u);
   if (!CHECK || c + 16 <= k) {
     asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -72,7 +73,8 @@ struct Step {          // a warp's words of one step of the depth
   uint4 u[4], v[4], w[4];
 };
 template <bool CHECK>
-__device__ __forceinline__ void load_step(Step& d, const uint8_t* x0, const uint8_t* x1, const uint8_t* y, int c0, int k) {
+__device__ __forceinline__ void load_step(Step& d, const uint8_t* x0, const uint8_t* x1, const uint8_t* y, uint32_t c0,
+                                          uint32_t k) {
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     d.u[c] = load16<CHECK>(x0, c0 + 64 * c, k);
@@ -98,11 +100,11 @@ __global__ void __launch_bounds__(kThreads, 3) matmul_few_kernel(const __grid_co
   const uint8_t* sy0 = a.sy + scale_place(y0, 0, a.panel);
   const uint8_t* sy1 = a.sy + scale_place(y1, 0, a.panel);
   float acc[4] = {};
-  for (int at = warp * kDepth; at < a.k; at += kWarps * kDepth) {
+  for (uint32_t at = warp * kDepth; at < a.k; at += kWarps * kDepth) {
     Step d;
     if (at + kDepth <= a.k) load_step<false>(d, x0, x1, y, at + 16 * t, a.k);
     else load_step<true>(d, x0, x1, y, at + 16 * t, a.k);
-    const int tile = (at >> 9) * 512, shift = (at >> 4) & 16;      // the scale bytes of this half of a tile
+    const uint32_t tile = (at >> 9) * 512, shift = (at >> 4) & 16;      // the scale bytes of this half of a tile
     const auto word = [&](const uint8_t* s) { return *reinterpret_cast<const uint32_t*>(s + tile) >> shift; };
     const uint32_t s0 = word(sx0), s1 = word(sx1), q0 = word(sy0), q1 = word(sy1);
 #pragma unroll
@@ -148,7 +150,7 @@ cudaError_t launch_matmul_few(const opt_matmul_args& c, const OutputArgs& out, c
   const auto u8 = [](const void* p) { return static_cast<const uint8_t*>(p); };
   FewArgs f = {};
   f.out = out;
-  f.k = (int)c.k;
+  f.k = (uint32_t)c.k;
   f.panel = (int)((c.k + 511) / 512);
   f.x = u8(out.swap ? c.d_b : c.d_a);
   f.sx = u8(out.swap ? c.d_b_scales : c.d_a_scales);

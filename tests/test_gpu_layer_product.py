@@ -50,3 +50,23 @@ def test_output_warps_at_different_speeds(m, n, k, out, addend, pad):
     column or row of tiles leaves some of them nothing to store): no warp's release
     of a tile counts for another tile's, so no accumulator is overwritten early."""
     check_exact(m, n, k, out, addend, pad)
+
+
+@pytest.mark.parametrize("k", [(1 << 31) - 1, (1 << 31) - 2047, (1 << 31) - 2048])
+def test_few_rows_at_the_greatest_depths(k):
+    """Powers of two at the ends of a row of over two thousand million codes, with scale 1."""
+    pitch = 1 << 31
+    a = torch.zeros(1, pitch, dtype=torch.uint8, device="cuda")
+    b = torch.zeros(2, pitch, dtype=torch.uint8, device="cuda")
+    scales = torch.full((ps.opt_scales_bytes(1, k),), 127, dtype=torch.uint8, device="cuda")
+    one, two, four = 0x38, 0x40, 0x48                          # E4M3
+    for at in (0, 2047, 1 << 30, k - 2049, k - 17, k - 1):
+        a[0, at] = two
+    b[0, 0], b[0, k - 2049], b[0, k - 1] = one, four, one
+    b[1, 1 << 30], b[1, k - 17] = two, four
+    a[0, k:], b[:, k:] = 0x7F, 0x7F                            # NaN beyond the depth
+    out = torch.empty(1, 2, device="cuda")
+    ps.opt_matmul(a[:, :k], scales, b[:, :k], scales, out)
+    assert out.tolist() == [[12.0, 12.0]]
+    ps.opt_matmul(b[:, :k], scales, a[:, :k], scales, out.view(2, 1))
+    assert out.tolist() == [[12.0, 12.0]]
