@@ -197,6 +197,15 @@ int opt_matmul(const opt_matmul_args* a, void* stream);
  * rows, a depth of 0). */
 #define OPT_MATMUL_WAIT_DRILL 1
 
+/* The form in which opt_matmul computes these sizes on the current device, for
+ * tests and reports: h_form[0] CTAs that share a tile (1, or 2 for a pair; 0 where
+ * no tiles are formed: an operand of at most eight rows, a depth of 0, no output),
+ * [1] the tile's columns (its rows are 128 for each CTA), [2] the parts in which a
+ * cluster of CTAs takes the depth, [3] 1 if the tile's rows are those of b, [4] the
+ * most tiles that a CTA or pair goes through.  Reads a's sizes, and of d_a, d_b and
+ * their pitches only whether rows start on 128 bytes; launches nothing. */
+int opt_matmul_form(const opt_matmul_args* a, int32_t h_form[5]);
+
 /* Error flags raised by the current device's layer kernels since the last call,
  * then cleared; 0 means that every kernel ran to completion.  Copies to host and
  * synchronises the stream.  OPT_FLAG_WAIT_TIMEOUT: a product gave up a wait on

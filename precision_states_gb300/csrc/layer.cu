@@ -178,6 +178,17 @@ int opt_matmul(const opt_matmul_args* a, void* stream) {
   return status_of(launch_matmul(*a, sms, static_cast<cudaStream_t>(stream)));
 }
 
+int opt_matmul_form(const opt_matmul_args* a, int32_t h_form[5]) {
+  if (a == nullptr || h_form == nullptr) return OPT_EINVAL;
+  PS_TRY(check_sizes(a->m, a->n));
+  PS_TRY(check_sizes(a->k, 0));
+  for (int i = 0; i < 5; ++i) h_form[i] = 0;
+  if (a->m == 0 || a->n == 0 || !matmul_waits(*a)) return OPT_OK;
+  int sms = 0;
+  PS_TRY(sm_count_of(&sms));
+  return status_of(matmul_form(*a, sms, h_form));
+}
+
 int opt_layer_status(int32_t* h_flags, void* stream) {
   if (h_flags == nullptr) return OPT_EINVAL;
   int flags = 0;

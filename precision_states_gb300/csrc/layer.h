@@ -26,6 +26,7 @@ cudaError_t launch_rms_norm_backward(const opt_rms_norm_backward_args& a, const 
 cudaError_t launch_quantize(const opt_quantize_args& a, cudaStream_t s);
 cudaError_t launch_matmul(const opt_matmul_args& a, int sm_count, cudaStream_t s);
 bool matmul_waits(const opt_matmul_args& a);              // whether the product's kernel waits on anything
+cudaError_t matmul_form(const opt_matmul_args& a, int sm_count, int32_t* form);      // opt_matmul_form, of one that waits
 cudaError_t layer_flags(int* flags, cudaStream_t s);      // read and clear
 
 // CTAs of the backward norm, and so rows of its weight-gradient partial sums:

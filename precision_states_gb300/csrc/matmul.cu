@@ -784,6 +784,13 @@ struct Operand {
   int64_t pitch, rows;
 };
 
+// Groups of CTAs (pairs, a split's cluster) that go through the tiles.  A split
+// tile's cluster takes one tile; others loop.
+int64_t groups(int64_t tiles, int cg, int split, int sm_count) {
+  const int64_t slots = sm_count / cg;
+  return split > 1 || tiles < slots ? tiles : slots;
+}
+
 template <typename T, int CG, int NT>
 cudaError_t launch(const Operand& x, const Operand& y, int64_t k, MatmulArgs a, int split, int sm_count,
                    cudaStream_t s) {
@@ -810,10 +817,8 @@ cudaError_t launch(const Operand& x, const Operand& y, int64_t k, MatmulArgs a, 
     return cudaErrorInvalidValue;
   if (NT != 256 || !a.wide) mo = mx;      // not used
   const int per = CG == 2 ? 2 : split;
-  const int64_t tiles = xt * yt, slots = sm_count / per;
   cudaLaunchConfig_t cfg = {};
-  // a split tile's cluster takes one tile; others loop
-  cfg.gridDim = dim3((unsigned)((split > 1 || tiles < slots ? tiles : slots) * per));
+  cfg.gridDim = dim3((unsigned)(groups(xt * yt, CG, split, sm_count) * per));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = L::kBytes;
   cfg.stream = s;
@@ -901,6 +906,17 @@ cudaError_t active_clusters(int sm_count, int (&out)[4]) {
   return cudaSuccess;
 }
 
+cudaError_t plan_of(const opt_matmul_args& c, int sm_count, Plan* p) {
+  int clusters[4];
+  if (const cudaError_t e = active_clusters(sm_count, clusters); e != cudaSuccess) return e;
+  const auto on_lines = [](const void* codes, int64_t rows, int64_t pitch) {
+    return (rows == 1 || pitch % 128 == 0) && ((uintptr_t)codes & 127u) == 0;
+  };
+  *p = plan(c.m, c.n, (int)((c.k + 127) / 128), on_lines(c.d_a, c.m, c.a_pitch) && on_lines(c.d_b, c.n, c.b_pitch),
+            clusters);
+  return cudaSuccess;
+}
+
 template <typename T>
 cudaError_t dispatch(const opt_matmul_args& c, int sm_count, cudaStream_t s) {
   MatmulArgs a = {};
@@ -923,10 +939,8 @@ cudaError_t dispatch(const opt_matmul_args& c, int sm_count, cudaStream_t s) {
     return launch_matmul_few(c, a, s);
   }
   const Operand ops[2] = {{c.d_a, c.d_a_scales, c.a_pitch, c.m}, {c.d_b, c.d_b_scales, c.b_pitch, c.n}};
-  int clusters[4];
-  if (const cudaError_t e = active_clusters(sm_count, clusters); e != cudaSuccess) return e;
-  const auto on_lines = [](const Operand& o) { return (o.rows == 1 || o.pitch % 128 == 0) && ((uintptr_t)o.codes & 127u) == 0; };
-  const Plan p = plan(c.m, c.n, a.blocks, on_lines(ops[0]) && on_lines(ops[1]), clusters);
+  Plan p;
+  if (const cudaError_t e = plan_of(c, sm_count, &p); e != cudaSuccess) return e;
   a.swap = p.swap;
   const Operand &x = ops[p.swap], &y = ops[1 - p.swap];
   switch (p.nt) {
@@ -943,6 +957,20 @@ cudaError_t dispatch(const opt_matmul_args& c, int sm_count, cudaStream_t s) {
 }  // namespace
 
 bool matmul_waits(const opt_matmul_args& a) { return a.k > 0 && a.m > kFewRows && a.n > kFewRows; }
+
+cudaError_t matmul_form(const opt_matmul_args& a, int sm_count, int32_t* form) {
+  Plan p;
+  if (const cudaError_t e = plan_of(a, sm_count, &p); e != cudaSuccess) return e;
+  const int64_t xr = p.swap ? a.n : a.m, yr = p.swap ? a.m : a.n;
+  const int64_t tiles = (xr + 128 * p.cg - 1) / (128 * p.cg) * ((yr + p.nt - 1) / p.nt);
+  const int64_t at_once = groups(tiles, p.cg, p.split, sm_count);
+  form[0] = p.cg;
+  form[1] = p.nt;
+  form[2] = p.split;
+  form[3] = p.swap;
+  form[4] = (int32_t)((tiles + at_once - 1) / at_once);
+  return cudaSuccess;
+}
 
 cudaError_t launch_matmul(const opt_matmul_args& a, int sm_count, cudaStream_t s) {
   return a.out_dtype == OPT_F32 ? dispatch<float>(a, sm_count, s) : dispatch<Bf16>(a, sm_count, s);

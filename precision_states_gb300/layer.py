@@ -63,6 +63,7 @@ SIGS = {
     "opt_rms_norm_backward_workspace": (_i64, [_i64, _i64]),
     "opt_quantize": (_c.c_int, [_c.c_char_p, _vp]),
     "opt_matmul": (_c.c_int, [_c.c_char_p, _vp]),
+    "opt_matmul_form": (_c.c_int, [_c.c_char_p, _c.POINTER(_i32)]),
     "opt_layer_status": (_c.c_int, [_c.POINTER(_i32), _vp]),
 }
 
@@ -331,6 +332,19 @@ def opt_matmul(a, a_scales, b, b_scales, out, addend=None, stream=None, wait_dri
                       ready.stream(dev) if stream is None else _stream_ptr(stream))
     if st:
         _check(st, "opt_matmul")
+
+
+def opt_matmul_form(a, b):
+    """How opt_matmul computes a b^T of these codes on the current device: (CTAs
+    that share a tile, its columns, parts of the depth, whether the tile's rows are
+    b's, most tiles per CTA or pair); zeros where no tiles are formed."""
+    (m, k, ap), (n, kb, bp) = _matrix(a, "a"), _matrix(b, "b")
+    if k != kb:
+        raise ValueError(f"a and b: depths {k} and {kb}")
+    form = (_i32 * 5)()
+    _check(lib().opt_matmul_form(_pack_matmul(a.data_ptr(), 0, b.data_ptr(), 0, 0, 0, ap, bp, 0, 0, m, n, k, 0, 0), form),
+           "opt_matmul_form")
+    return tuple(form)
 
 
 def opt_layer_status(stream=None) -> int:

@@ -124,3 +124,17 @@ def test_binding_refuses_wrong_tensors():
     assert layer._matrix(torch.zeros(3, 10)[:, :8], "x") == (3, 8, 10)
     assert layer._matrix(torch.zeros(8), "x") == (1, 8, 8)
     assert ctypes.sizeof(layer.opt_matmul_args) == 112
+
+
+def test_matmul_form_without_tiles():
+    """Answered on the host alone; refusals as in the product."""
+    form = (ctypes.c_int32 * 5)(*[9] * 5)
+    ask = lambda **f: ps.lib().opt_matmul_form(bytes(layer.opt_matmul_args(**f)), form)  # noqa: E731
+    for size in (dict(m=8, n=4096, k=512), dict(m=4096, n=1, k=512), dict(m=300, n=300, k=0), dict(m=0, n=300, k=5)):
+        assert ask(**size) == ps.OPT_OK and list(form) == [0] * 5
+    assert ask(m=-1, n=4, k=4) == ps.OPT_EINVAL and ask(m=9, n=9, k=BIG) == ps.OPT_ELIMIT
+    assert ps.lib().opt_matmul_form(None, form) == ps.OPT_EINVAL
+    assert ps.lib().opt_matmul_form(bytes(layer.opt_matmul_args()), None) == ps.OPT_EINVAL
+    assert ps.opt_matmul_form(torch.zeros(3, 64, dtype=torch.uint8), torch.zeros(40, 64, dtype=torch.uint8)) == (0,) * 5
+    with pytest.raises(ValueError):
+        ps.opt_matmul_form(torch.zeros(3, 64, dtype=torch.uint8), torch.zeros(40, 63, dtype=torch.uint8))
