@@ -207,8 +207,9 @@ int opt_matmul(const opt_matmul_args* a, void* stream);
 int opt_matmul_form(const opt_matmul_args* a, int32_t h_form[5]);
 
 /* Error flags raised by the current device's layer kernels since the last call,
- * then cleared; 0 means that every kernel ran to completion.  Copies to host and
- * synchronises the stream.  OPT_FLAG_WAIT_TIMEOUT: a product gave up a wait on
+ * on any stream, then cleared; 0 means that every kernel that ended before ran to
+ * completion.  A flag raised during the call is in its answer or in the next
+ * one's.  Copies to host and synchronises the stream.  OPT_FLAG_WAIT_TIMEOUT: a product gave up a wait on
  * its own copies or tensor-core work (each is bounded at 2 s, so the kernel never
  * hangs) and left part of its output unwritten: discard that output. */
 int opt_layer_status(int32_t* h_flags, void* stream);

@@ -732,6 +732,8 @@ __global__ void __launch_bounds__(kThreads) no_depth_kernel(const __grid_constan
   }
 }
 
+__global__ void clear_flags_kernel(int seen) { atomicAnd(&g_flags, ~seen); }
+
 // ---------------------------------------------------------------------- host
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -976,12 +978,15 @@ cudaError_t launch_matmul(const opt_matmul_args& a, int sm_count, cudaStream_t s
   return a.out_dtype == OPT_F32 ? dispatch<float>(a, sm_count, s) : dispatch<Bf16>(a, sm_count, s);
 }
 
+// Only what was read is cleared, so that a flag raised in between by a kernel on
+// another stream stays for the next call.
 cudaError_t layer_flags(int* flags, cudaStream_t s) {
-  const int zero = 0;
   cudaError_t e = cudaMemcpyFromSymbolAsync(flags, g_flags, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
-  if (e == cudaSuccess) e = cudaMemcpyToSymbolAsync(g_flags, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  return e;
+  if (e != cudaSuccess || *flags == 0) return e;
+  clear_flags_kernel<<<1, 1, 0, s>>>(*flags);
+  e = cudaGetLastError();
+  return e == cudaSuccess ? cudaStreamSynchronize(s) : e;
 }
 
 }  // namespace psopt

@@ -38,3 +38,19 @@ def test_norm_gradients_do_not_take_memory_that_pending_work_uses(form):
             torch.cuda.synchronize()
             assert (copy == fill).all(), "another tensor's memory was written"
             assert torch.equal(dw, want)
+
+
+def test_status_loses_no_flag_that_is_raised_while_it_is_asked():
+    """Products whose waits run out on one stream, while another asks all the time."""
+    codes, scales = ps.e4m3_storage(64, 256)
+    out = torch.empty(64, 64, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    assert ps.opt_layer_status() == 0
+    for _ in range(200):
+        ps.opt_matmul(codes, scales, codes, scales, out, stream=side, wait_drill=True)     # ends after 1 ms
+        flags = 0
+        while not side.query():
+            flags |= ps.opt_layer_status()
+        assert flags | ps.opt_layer_status() == ps.OPT_FLAG_WAIT_TIMEOUT
+    assert ps.opt_layer_status() == 0
