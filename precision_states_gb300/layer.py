@@ -6,8 +6,8 @@ Argument marshalling and shape checks only; the functions carry the C names
 and write into tensors that the caller owns.  A matrix argument is a CUDA
 tensor on the current device whose last dimension is contiguous: a 2-d tensor
 of any row stride, or a contiguous tensor of any other shape, taken as rows of
-its last dimension.  Wrong shapes and dtypes raise ValueError; everything else
-is checked by the library (OptError).
+its last dimension.  Wrong shapes and dtypes, and numbers that their C types do not
+hold, raise ValueError; everything else is checked by the library (OptError).
 """
 from __future__ import annotations
 
@@ -84,6 +84,7 @@ _pack_rms_norm = packer(opt_rms_norm_args)
 _pack_rms_norm_backward = packer(opt_rms_norm_backward_args)
 _pack_quantize = packer(opt_quantize_args)
 _pack_matmul = packer(opt_matmul_args)
+_NOT_HELD = (struct.error, OverflowError)      # a number outside its field's type
 
 from . import OPT_BF16, OPT_EUNSUPPORTED, OPT_F32, OptError, _check, _stream_ptr, lib  # noqa: E402
 
@@ -206,8 +207,11 @@ def opt_dropout(x, y, p: float, seed=0, tensor_index=0, step=0, residual=None, s
     rows, cols, xp = _matrix(x, "x")
     yq, yp = _like(y, "y", rows, cols, dtype, dev)
     rq, rp = (0, 0) if residual is None else _like(residual, "residual", rows, cols, dtype, dev)
-    st = ready.dropout(_pack_dropout(x.data_ptr(), rq, yq, xp, rp, yp, rows, cols, p, seed, step, tensor_index, dt),
-                       ready.stream(dev) if stream is None else _stream_ptr(stream))
+    try:
+        args = _pack_dropout(x.data_ptr(), rq, yq, xp, rp, yp, rows, cols, p, seed, step, tensor_index, dt)
+    except _NOT_HELD as e:
+        raise ValueError(f"opt_dropout: {e}") from None
+    st = ready.dropout(args, ready.stream(dev) if stream is None else _stream_ptr(stream))
     if st:
         _check(st, "opt_dropout")
 
@@ -231,9 +235,12 @@ def opt_rms_norm(x, weight, eps=1e-5, y=None, rstd=None, residual=None, h=None, 
     sq = 0 if rstd is None else _vector(rstd, "rstd", rows, dev, ready.f32)
     cq, eq, cp = ((0, 0, 0) if codes is None and scales is None
                   else _held(codes, scales, "codes", rows, cols, dev, ready))
-    st = ready.rms_norm(_pack_rms_norm(x.data_ptr(), rq, wq, hq, yq, sq, cq, eq, xp, rp, hp, yp, cp, rows, cols, p, seed,
-                                       step, tensor_index, dt, wt, eps),
-                        ready.stream(dev) if stream is None else _stream_ptr(stream))
+    try:
+        args = _pack_rms_norm(x.data_ptr(), rq, wq, hq, yq, sq, cq, eq, xp, rp, hp, yp, cp, rows, cols, p, seed, step,
+                              tensor_index, dt, wt, eps)
+    except _NOT_HELD as e:
+        raise ValueError(f"opt_rms_norm: {e}") from None
+    st = ready.rms_norm(args, ready.stream(dev) if stream is None else _stream_ptr(stream))
     if st:
         _check(st, "opt_rms_norm")
 
@@ -268,10 +275,12 @@ def opt_rms_norm_backward(dy, h, weight, rstd, dh, dh_in=None, dx=None, dweight=
             workspace = _workspace(need, dev, stream)
         if need:
             nq = workspace.data_ptr()
-    st = ready.rms_norm_backward(
-        _pack_rms_norm_backward(gq, h.data_ptr(), wq, sq, iq, oq, xq, dq, nq, gp, hp, ip, op, xp, need, rows, cols, p,
-                                seed, step, tensor_index, dt, wt, 0),
-        ready.stream(dev) if stream is None else _stream_ptr(stream))
+    try:
+        args = _pack_rms_norm_backward(gq, h.data_ptr(), wq, sq, iq, oq, xq, dq, nq, gp, hp, ip, op, xp, need, rows, cols,
+                                       p, seed, step, tensor_index, dt, wt, 0)
+    except _NOT_HELD as e:
+        raise ValueError(f"opt_rms_norm_backward: {e}") from None
+    st = ready.rms_norm_backward(args, ready.stream(dev) if stream is None else _stream_ptr(stream))
     if st:
         _check(st, "opt_rms_norm_backward")
 
@@ -307,8 +316,11 @@ def opt_quantize(x, codes=None, scales=None, codes_t=None, scales_t=None, block_
                   else _held(codes, scales, "codes", rows, cols, dev, ready))
     tq, uq, tp = ((0, 0, 0) if codes_t is None and scales_t is None
                   else _held(codes_t, scales_t, "codes_t", cols, rows, dev, ready))
-    st = ready.quantize(_pack_quantize(x.data_ptr(), cq, sq, tq, uq, xp, cp, tp, rows, cols, dt, block_rows),
-                        ready.stream(dev) if stream is None else _stream_ptr(stream))
+    try:
+        args = _pack_quantize(x.data_ptr(), cq, sq, tq, uq, xp, cp, tp, rows, cols, dt, block_rows)
+    except _NOT_HELD as e:
+        raise ValueError(f"opt_quantize: {e}") from None
+    st = ready.quantize(args, ready.stream(dev) if stream is None else _stream_ptr(stream))
     if st:
         _check(st, "opt_quantize")
 
