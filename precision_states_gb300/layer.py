@@ -269,7 +269,7 @@ def opt_rms_norm_backward(dy, h, weight, rstd, dh, dh_in=None, dx=None, dweight=
     if dweight is not None:
         dq = _vector(dweight, "dweight", cols, dev, ready.f32)
         if workspace is not None:
-            need = workspace.numel() * workspace.element_size()
+            need = _given_workspace(workspace, dev)
         elif rows > 512 or rows * cols > 1 << 21:                   # opt_rms_norm_backward_workspace
             need = min(rows, 1024) * (-(-cols // 4) * 4) * 4
             workspace = _workspace(need, dev, stream)
@@ -283,6 +283,13 @@ def opt_rms_norm_backward(dy, h, weight, rstd, dh, dh_in=None, dx=None, dweight=
     st = ready.rms_norm_backward(args, ready.stream(dev) if stream is None else _stream_ptr(stream))
     if st:
         _check(st, "opt_rms_norm_backward")
+
+
+def _given_workspace(t, device):
+    """Bytes of a caller's workspace."""
+    if t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"workspace: expected contiguous bytes on cuda:{device}")
+    return t.numel() * t.element_size()
 
 
 def _workspace(nbytes, device, stream):

@@ -24,3 +24,18 @@ def test_numbers_that_their_types_do_not_hold_are_refused():
         ps.opt_quantize(x, codes, scales, block_rows=1 << 40)
     ps.opt_dropout(x, y.clone(), 0.1, seed=(1 << 64) - 1, tensor_index=(1 << 32) - 1, step=(1 << 63) - 1)
     assert (y == 7).all()
+
+
+def test_workspace_of_another_place_or_layout_is_refused():
+    x = torch.ones(600, 8, device="cuda")
+    w, rstd, dw = torch.ones(8, device="cuda"), torch.ones(600, device="cuda"), torch.full((8,), 7.0, device="cuda")
+    need = ps.opt_rms_norm_backward_workspace(600, 8)
+    assert need == 600 * 32
+    strided = torch.empty(need, 2, dtype=torch.uint8, device="cuda")[:, 0]
+    for bad in (torch.empty(need, dtype=torch.uint8), torch.empty(need, dtype=torch.uint8).view(600, 32), strided):
+        with pytest.raises(ValueError):
+            ps.opt_rms_norm_backward(x, x, w, rstd, torch.empty_like(x), dweight=dw, workspace=bad)
+    with pytest.raises(ps.OptError) as e:
+        ps.opt_rms_norm_backward(x, x, w, rstd, torch.empty_like(x), dweight=dw,
+                                 workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == ps.OPT_EINVAL and (dw == 7).all()

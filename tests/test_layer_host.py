@@ -138,3 +138,11 @@ def test_matmul_form_without_tiles():
     assert ps.opt_matmul_form(torch.zeros(3, 64, dtype=torch.uint8), torch.zeros(40, 64, dtype=torch.uint8)) == (0,) * 5
     with pytest.raises(ValueError):
         ps.opt_matmul_form(torch.zeros(3, 64, dtype=torch.uint8), torch.zeros(40, 63, dtype=torch.uint8))
+
+
+def test_given_workspace_is_looked_at():
+    with pytest.raises(ValueError):
+        layer._given_workspace(torch.zeros(64, dtype=torch.uint8), 0)          # not on the device
+    assert layer._given_workspace(torch.zeros(4, 4), -1) == 64
+    with pytest.raises(ValueError):
+        layer._given_workspace(torch.zeros(4, 4).t()[:2], -1)
