@@ -503,14 +503,21 @@ void launch_backward(K kernel, const opt_rms_norm_backward_args& a, const DropAr
   kernel<<<grid + (apart ? 0u : n), threads, 0, s>>>(a, d, grid);
 }
 
+// CTAs that go through the rows, of `resident` that the device holds at once: each has
+// a row of partial sums, and the workspace has room for kNormBackwardMaxCtas.
+constexpr int64_t row_ctas(int64_t rows, int64_t resident) {
+  const int64_t most = resident < kNormBackwardMaxCtas ? resident : kNormBackwardMaxCtas;
+  return rows < most ? rows : most;
+}
+static_assert(row_ctas(1 << 20, 4 * 400) <= norm_backward_parts(1 << 20, 20000), "the workspace holds every CTA's row");
+static_assert(row_ctas(600, 4 * 400) <= norm_backward_parts(600, 20000), "the workspace holds every CTA's row");
+
 template <typename T, typename W, bool VEC, int NG, int MAX, int CTAS>
 int backward_rows(const opt_rms_norm_backward_args& a, const DropArgs& d, int sm_count, int threads, cudaStream_t s) {
   static OccupancyCache cache[33];
   const auto kernel = rms_norm_backward_kernel<T, W, VEC, NG, MAX, CTAS>;
   if (slabs(a, MAX) > 0 && a.rows > kSlabFewRows) threads = MAX;      // dweight's rows are shared by all warps
-  int64_t most = (int64_t)sm_count * cached_occupancy(kernel, cache[threads / 32], threads, 0);
-  if (most > kNormBackwardMaxCtas) most = kNormBackwardMaxCtas;
-  const int grid = (int)(a.rows < most ? a.rows : most);
+  const int grid = (int)row_ctas(a.rows, (int64_t)sm_count * cached_occupancy(kernel, cache[threads / 32], threads, 0));
   launch_backward(kernel, a, d, grid, threads, s);
   return grid;
 }
@@ -526,8 +533,7 @@ cudaError_t backward_vec(const opt_rms_norm_backward_args& a, const DropArgs& d,
   } else if (chunks <= 2048) {
     grid = backward_rows<T, W, VEC, 2, 1024, 1>(a, d, sm_count, (int)((chunks + 63) / 64) * 32, s);
   } else {
-    const int64_t most = (int64_t)sm_count * 4;
-    grid = (int)(a.rows < most ? a.rows : most);
+    grid = (int)row_ctas(a.rows, (int64_t)sm_count * 4);
     launch_backward(rms_norm_backward_wide_kernel<T, W, VEC>, a, d, grid, kWideThreads, s);
   }
   if (a.d_dweight != nullptr && !dweight_here(a))
