@@ -477,6 +477,8 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
   fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_at, 0);
 
+  const bool counts = CG == 1 || rank == 0;      // copies end on this CTA's barriers
+  Ring<S> at;
   if (warp == 0) {
     // ------------------------------------------------------------- producer
     // A pair's copies all count on the leader's barrier.  This warp and the next
@@ -487,8 +489,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     // thread that divided per block, 28.7 with its state carried, 20.4 by a warp.)
     const uint32_t full_at = CG == 2 ? map_to(full, 0) : full;
     constexpr uint32_t kBytes = CG * (L::kXBytes + L::kYBytes), kScales = CG * L::kScaleBytes;
-    const bool counts = CG == 1 || rank == 0, issues = elected();
-    Ring<S> at;
+    const bool issues = elected();
     bool ok = true;
     for (int t = a.drill ? tiles : first; t < tiles && ok; t += step) {
       int tx, ty;
@@ -523,19 +524,11 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         if (!ok) break;
       }
     }
-    if (!ok) {
-      *failed = 1;
-      if (rank == 0)           // let what was issued land: each stage's last use
-        for (int i = 0; i < S; ++i) {
-          if (at.first && i >= (int)at.stage) break;
-          bar_wait(full + 8 * i, i < (int)at.stage ? at.phase : at.phase ^ 1u, a.wait_ns);
-        }
-    }
-  } else if (warp == 1 && (CG == 1 || rank == 0)) {
+    if (!ok) *failed = 1;
+  } else if (warp == 1 && counts) {
     // ------------------------------------------------------------- products
     const uint64_t x_desc = tile_desc(ring), y_desc = tile_desc(ring + L::kXBytes), s_desc = scale_desc(scales);
     const bool issues = elected();
-    Ring<S> at;
     int i = 0;
     uint32_t set = 0;
     bool ok = true;
@@ -667,6 +660,14 @@ matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
   __syncwarp();
   fence_before();
   __syncthreads();
+  // After a wait that ran out, in whichever warp: the copies that were issued land
+  // before the CTA leaves (each stage's last use; else its products waited for it).
+  if (warp == 0 && counts && *failed)
+    for (int i = 0; i < S; ++i) {
+      if (at.first && i >= (int)at.stage) break;
+      warp_wait(full + 8 * i, i < (int)at.stage ? at.phase : at.phase ^ 1u, a.wait_ns);
+    }
+  __syncwarp();
   if (CG == 1 && a.split > 1) {
     // sums of the cluster's parts, in rank order: each CTA takes 128 / split rows
     // of x, four outputs at a time that lie together in `out`
