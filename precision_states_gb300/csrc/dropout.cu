@@ -10,7 +10,9 @@
 // grid; six CTAs per SM (32 registers): with the ragged end's code in the same
 // path it took 70 registers and 112 us.  One token of 4,096 takes a launch's time
 // (1.8 us back to back).  Strided rows that begin anywhere take two generator calls
-// per chunk and go through shared memory: 8000 x 4001 BF16 63.4 us (0.45).
+// per chunk and go through shared memory: 8000 x 4001 BF16 60.4 us (0.48), with the
+// matrix's ragged end loaded element by element in a loop (together: 63.0, 4000 x 3001
+// 27.0 for 25.7; but 33 x 769 2.4 for 2.65).
 #include "layer.cuh"
 
 namespace psopt {
@@ -32,8 +34,8 @@ __device__ __forceinline__ void drop_chunk(const opt_dropout_args& a, const Drop
   Ahead<T, VEC> res_ahead = {};
   if (!VEC || res_valid > 0) res_ahead = res_row.ahead(c, res_valid);
   float x[8], y[8];
-  unpack(x_row.chunk(x_ahead, c, valid), x);
-  unpack(res_row.chunk(res_ahead, c, res_valid), y);
+  unpack(x_row.template chunk<true>(x_ahead, c, valid), x);
+  unpack(res_row.template chunk<true>(res_ahead, c, res_valid), y);
   add_dropped8<VEC>(y, x, (uint64_t)(r * a.cols + c), d, nullptr);      // (a barrier for a CTA's one row costs more)
   store_at<VEC>(a.d_y, a.y_pitch, a.cols, r, c, valid, y, buffer);
 }

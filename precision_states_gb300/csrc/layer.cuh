@@ -141,7 +141,9 @@ struct Row {
   }
   // The chunk; elements from `valid` on read as 0.  One whose words reach beyond the
   // matrix is loaded here, element by element but together: the gradients of 129 x 1031
-  // BF16 rows 4.7 us, 5.8 in a loop.
+  // BF16 rows 4.7 us, 5.8 in a loop.  ONE_BY_ONE: in a loop, which costs the main path
+  // fewer registers (strided dropout: see there).
+  template <bool ONE_BY_ONE = false>
   __device__ __forceinline__ Raw<T> chunk(const Ahead<T, VEC>& a, int64_t c, int valid) const {
     Raw<T> r;
     if constexpr (VEC || sizeof(T) == 4) {
@@ -154,7 +156,17 @@ struct Row {
 #pragma unroll
         for (int k = 0; k < 4; ++k) r.w[k] = 2 * k + 1 < valid ? r.w[k] : 2 * k < valid ? r.w[k] & 0xFFFFu : 0u;
       }
-      if (valid > 0 && !whole(c)) {
+      if (ONE_BY_ONE && valid > 0 && !whole(c)) {
+        uint64_t part[2] = {0, 0};
+#pragma unroll 1
+        for (int j = 0; j < valid; ++j) {
+          const uint64_t v = (uint64_t)start[c + j].bits << (16 * (j & 3));
+          if (j < 4) part[0] |= v;
+          else part[1] |= v;
+        }
+        r.w[0] = (uint32_t)part[0]; r.w[1] = (uint32_t)(part[0] >> 32);
+        r.w[2] = (uint32_t)part[1]; r.w[3] = (uint32_t)(part[1] >> 32);
+      } else if (valid > 0 && !whole(c)) {
         uint32_t b[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) b[j] = bits_if(start + c + j, j < valid);
