@@ -171,9 +171,11 @@ typedef struct opt_quantize_args {
 int opt_quantize(const opt_quantize_args* a, void* stream);
 
 /* out[m][n] = sum over k of a[m][k] b[n][k] (+ addend[m][n]): both operands
- * with k along their rows, as codes with scales.  Products are exact, sums are
- * held in fp32; out and addend are of out_dtype (OPT_F32 or OPT_BF16), rounded
- * once.  d_addend may be d_out (same pitch).  A linear layer's three products
+ * with k along their rows, as codes with scales.  Products are exact, and sums are
+ * held in fp32.  The tensor core truncates where an fp32 addition rounds, once per
+ * 32 of the depth, so the error grows with it: about 6e-7 of the output's norm at a
+ * depth of 8191, 1.3e-7 for sums that round.  out and addend are of out_dtype
+ * (OPT_F32 or OPT_BF16), rounded once.  d_addend may be d_out (same pitch).  A linear layer's three products
  * are y = x W^T (a = x, b = W), dx = dy W (a = dy, b = W transposed) and
  * dW = dy^T x (a = dy transposed, b = x transposed). */
 typedef struct opt_matmul_args {

@@ -5,8 +5,8 @@
 // nothing else.
 //
 // Bound by memory once a matrix is large: 16384 x 4096 BF16 with a residual takes
-// 63.9 us, 6.3 TB/s (0.94 of the measured copy), at 187 instructions per eight
-// elements (issue 65 % busy).  One thread per chunk and fresh CTAs, not a resident
+// 63.7 us, 6.3 TB/s (0.95 of the measured copy), at 186 instructions per eight
+// elements (issue 64 % busy).  One thread per chunk and fresh CTAs, not a resident
 // grid; six CTAs per SM (32 registers): with the ragged end's code in the same
 // path it took 70 registers and 112 us.  One token of 4,096 takes a launch's time
 // (1.8 us back to back).  Strided rows that begin anywhere take two generator calls

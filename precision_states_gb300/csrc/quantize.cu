@@ -9,11 +9,11 @@
 // shared memory once more, as codes, so that they leave in whole 128-byte lines.
 // Maxima are taken on the words as they lie (two BF16 at a time).
 //
-// 14336 x 4096 fp32 in blocks of 128 x 128, both orientations: 57.4 us, 6.1 TB/s
-// (0.92 of the measured copy; 111.9 with the tile in shared memory as fp32), BF16
+// 14336 x 4096 fp32 in blocks of 128 x 128, both orientations: 58.4 us, 6.0 TB/s
+// (0.91 of the measured copy; 111.9 with the tile in shared memory as fp32), BF16
 // 37.3 us (0.95).  In blocks of 1 x 128 both orientations' scaling bounds it: 8192
-// x 4096 BF16 27.4 us (0.74), one orientation 18.6 (0.81).  8191 x 1024 BF16 takes
-// 10.8 us: less than one tile per CTA slot, so a tile's latency is the time.
+// x 4096 BF16 28.5 us (0.71), one orientation 19.3 (0.78).  8191 x 1024 BF16 takes
+// 10.9 us: less than one tile per CTA slot, so a tile's latency is the time.
 #include "layer.cuh"
 
 namespace psopt {

@@ -13,17 +13,20 @@
 // rounded once.
 //
 // Forward, 16384 x 4096 BF16 with a residual to h and codes: 72.3 us without
-// dropout, 6.5 TB/s (0.97 of the measured copy), bound by memory; 88.6 us with it
-// (0.80), bound by the generator's integer work (267 instructions per eight
+// dropout, 6.5 TB/s (0.97 of the measured copy), bound by memory; 89.2 us with it
+// (0.79), bound by the generator's integer work (267 instructions per eight
 // elements, issue 65 % busy).  Two chunks per thread at 256 threads and three CTAs
 // per SM: one chunk at 512 threads took 98.3 us, four at 128 threads 108.7, four
 // CTAs per SM 87.1 (but 79.7 without dropout).  Backward, 8192 x 4096 BF16 with
-// dh_in, dropout and the weight's gradient: 58.5 us (0.86), of which the sum over
+// dh_in, dropout and the weight's gradient: 57.7 us (0.87), of which the sum over
 // the CTAs' rows takes 4; one chunk per thread at 512 threads and two CTAs per SM
 // (fp32 too, in spite of some spilled registers: 8000 x 4096 120.5 us, 162.6 with one).  Few rows are launches'
 // latency: one token of 4,096 2.6 us.  Rows that begin anywhere (odd widths and pitches) are
-// loaded by words and stored through shared memory: 8000 x 4001 BF16 to y 47.7 us
-// (94.8 element by element), the backward pass 109 (271).
+// loaded by words and stored through shared memory: 8000 x 4001 BF16 to y 49.1 us
+// (94.8 element by element), the backward pass 109 (271), bound by its instructions
+// (issue 70 % busy).  4853 x 7001 takes 97.3 us with one CTA of 14 warps per SM: issue
+// 50 % and DRAM 28 % busy, so latency at low occupancy.  Backward with narrow rows is a
+// CTA of one warp each (131072 x 128 BF16 114 us, 0.13).
 #include "layer.cuh"
 
 namespace psopt {
