@@ -95,9 +95,10 @@ int opt_dropout(const opt_dropout_args* a, void* stream);
  * d_scales (y as E4M3 with a scale for each 1 x 128); at least one of them is
  * given.  y and the codes come from h and y before they are rounded to `dtype`.
  * d_h may be d_x or d_residual (same pointer and pitch); the other outputs
- * overlap no input.  eps >= 0.  mean(h^2) is held in fp32: a NaN in h makes its
- * whole row NaN; an infinity, or values whose squares overflow fp32 (beyond
- * about 1e19), make rstd 0; a row of zeros with eps 0 gives NaN. */
+ * overlap no input.  eps >= 0.  The sum of h^2 is held in fp32: a NaN in h makes
+ * its whole row NaN; an infinity, or values whose squares add up beyond fp32
+ * (about 1.8e19 / sqrt(cols) each), make rstd 0; a row of zeros with eps 0 gives
+ * NaN. */
 typedef struct opt_rms_norm_args {
   const void* d_x;
   const void* d_residual;

@@ -27,7 +27,7 @@
 // Splits.  With few tiles, the depth is split over a cluster of CTAs; their
 // accumulators are summed through distributed shared memory in rank order.
 //
-// Bound: 8192 x 14336 x 4096 takes 268 to 288 us alone, by the box (3.3 to 3.6
+// Bound: 8192 x 14336 x 4096 takes 268 to 288 us alone, by the GPU (3.3 to 3.6
 // PFLOP/s; tensor pipe 86 % busy), and 322 us in a loop, where the 1,360 W cap holds
 // the clock at 1,490 MHz.
 // The same loop with no loads takes 227 us: a pair's 256 x 256 tile brings 33 KB
@@ -360,7 +360,7 @@ __device__ __forceinline__ void store_spread(const MatmulArgs& a, uint32_t buffe
 // bank conflicts).  Rows beyond the matrix are left out by the copy; columns would
 // be only in pieces of 16 bytes, so a row's ragged end goes another way.
 // For the widest tile, whose lines a warp leaves in four or eight pieces: 8192 x
-// 2304 x 768 took 18.0 us with each lane storing its own row, 16.6 this way (17.0 to 17.6 on other boxes);
+// 2304 x 768 took 18.0 us with each lane storing its own row, 16.6 this way (17.0 to 17.6 on other GPUs);
 // 1024 x 4096 x 8191 to fp32 32.7 and 31.3.  Narrower tiles gain nothing: 256 x
 // 4096 x 4096 in tiles of 128 took 9.7 us by lanes, 9.8 this way.
 template <typename T, int N>

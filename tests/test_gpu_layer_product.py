@@ -75,6 +75,8 @@ FORMS = [
     ((1, 64, 4, 1, 1), (60, 4600, 4000), True), ((1, 64, 8, 1, 1), (60, 100, 5000), True),
     ((1, 128, 1, 0, 1), (100, 70, 300), True), ((1, 128, 1, 0, 2), (3096, 1329, 40), True), ((1, 128, 1, 0, 3), (824, 5560, 904), True),
     ((1, 128, 2, 0, 1), (66, 4711, 5055), False), ((1, 128, 4, 0, 1), (300, 700, 8000), True), ((1, 128, 8, 0, 1), (256, 256, 4000), True),
+    # more clusters than the device holds at once
+    ((1, 16, 2, 1, 1), (9, 19550, 18991), False), ((1, 64, 2, 0, 1), (19842, 33, 16254), False),
     ((2, 128, 1, 0, 1), (100, 4711, 6000), True), ((2, 128, 1, 0, 2), (3989, 1142, 784), False), ((2, 128, 1, 0, 3), (4000, 1700, 1300), True),
     ((2, 256, 1, 0, 1), (1000, 4096, 5000), True), ((2, 256, 1, 0, 2), (2048, 4096, 400), True), ((2, 256, 1, 0, 3), (2602, 3410, 260), False)]
 
