@@ -11,6 +11,14 @@
  *   opt_quantize           a matrix to E4M3 codes with a scale for each block
  *                          of 128, in one or both orientations
  *   opt_matmul             the product of two matrices held in that form
+ *   opt_gated              the gated activation between two products, with 8-bit
+ *                          output and its inputs kept in 8 bits
+ *   opt_gated_backward     its gradients, from the kept inputs or plain ones
+ *   opt_dequantize         kept codes as plain values, or turned into the
+ *                          operand of a weight's gradient
+ *   opt_head_norm          the norm of each query and key head with the position
+ *                          rotation, and the heads kept in 8 bits
+ *   opt_head_norm_backward its gradients, from the kept heads or plain ones
  *
  * Conventions (as in opt.h): pointers named d_* are device pointers on the
  * current device; `stream` is a cudaStream_t as void*.  Calls are
@@ -45,6 +53,12 @@
  * order in which the tensor core's scale memory takes them, so a product
  * copies a tile as it is.  Bytes of rows and blocks beyond the matrix are
  * neither written nor used.
+ *
+ * Kept activations: what a forward pass leaves for the backward pass may be held
+ * as such an operand with blocks of 1 x 128 (a byte and 1/128 for an element of two
+ * or four); the backward calls take it in place of the plain matrix, and their
+ * gradients are those of the values that the codes stand for (code times 2^e; a scale
+ * byte of 255 stands for NaN).
  *
  * Dropout: element i of a rows x cols matrix (i = r * cols + c, whatever the
  * pitch) is kept iff its 16-bit draw is at least T = 65536 p rounded to the
@@ -170,6 +184,174 @@ typedef struct opt_quantize_args {
   int32_t block_rows;
 } opt_quantize_args;
 int opt_quantize(const opt_quantize_args* a, void* stream);
+
+/* What a kept rows x cols matrix (codes, scales) becomes in the backward pass:
+ *   d_x                   its values, of `dtype` (OPT_F32: exact)
+ *   d_codes_t, d_scales_t its transposed operand (cols x rows), with blocks of 128
+ *                         along the matrix's rows.  The values are powers of two
+ *                         apart from their codes, so a code changes only where it
+ *                         falls among the subnormal ones of a column's scale.
+ * At least one is given; a pair is given whole.  A value beyond fp32 is an infinity. */
+typedef struct opt_dequantize_args {
+  const void* d_codes;
+  const void* d_scales;
+  void* d_x;
+  void* d_codes_t;
+  void* d_scales_t;
+  int64_t codes_pitch, x_pitch, codes_t_pitch;
+  int64_t rows, cols;
+  int32_t dtype;             /* of x: OPT_F32 or OPT_BF16 */
+  int32_t reserved;          /* 0 */
+} opt_dequantize_args;
+int opt_dequantize(const opt_dequantize_args* a, void* stream);
+
+/* Activations f(g) = g s(g) of opt_gated, formed in fp32 (a NaN stays one; minus
+ * infinity gives NaN, except OPT_ACT_RELU, which gives 0):
+ *   OPT_ACT_SILU       s(g) = 1 / (1 + exp(-g))
+ *   OPT_ACT_GELU_TANH  s(g) = (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2
+ *   OPT_ACT_GELU       s(g) = the normal distribution function
+ *   OPT_ACT_RELU       f(g) = max(g, 0) */
+#define OPT_ACT_SILU      0
+#define OPT_ACT_GELU_TANH 1
+#define OPT_ACT_GELU      2
+#define OPT_ACT_RELU      3
+
+/* y = f(gate) up (up NULL: y = f(gate)), formed in fp32 and written to d_y (of
+ * `dtype`, as gate and up are) and/or d_codes with d_scales (y as E4M3 with a scale
+ * for each 1 x 128, from y before it is rounded).  d_gate_codes with d_gate_scales and
+ * d_up_codes with d_up_scales keep the inputs for the backward pass.  At least one
+ * output is given; a pair is given whole.  d_y may be d_gate or d_up (same pointer
+ * and pitch); the other outputs overlap no input. */
+typedef struct opt_gated_args {
+  const void* d_gate;
+  const void* d_up;
+  void* d_y;
+  void* d_codes;
+  void* d_scales;
+  void* d_gate_codes;
+  void* d_gate_scales;
+  void* d_up_codes;
+  void* d_up_scales;
+  int64_t gate_pitch, up_pitch, y_pitch, codes_pitch, gate_codes_pitch, up_codes_pitch;
+  int64_t rows, cols;
+  int32_t dtype;             /* OPT_F32 or OPT_BF16 */
+  int32_t activation;        /* OPT_ACT_* */
+} opt_gated_args;
+int opt_gated(const opt_gated_args* a, void* stream);
+
+/* Gradients of opt_gated from dy (the gradient of y), gate and up:
+ *   dgate = dy up f'(gate)      dup = dy f(gate)      (up NULL: dgate = dy f'(gate))
+ * in fp32, each to any of: a plain matrix of `dtype`; codes with scales, the operand of
+ * the product that gives the input's gradient; and transposed codes with scales, the
+ * operand of the weight's gradient (rows x cols and cols x rows, blocks of 128 along
+ * the operand's rows).  d_y_codes_t with d_y_scales_t is y again, transposed: the
+ * operand of the gradient of the weight that y is multiplied by.  gate and up are of
+ * `dtype`, as dy is, or both kept (d_gate_scales and d_up_scales given: d_gate and d_up
+ * are codes).  Every output may be left NULL, but not all of them; a pair is given
+ * whole.  d_dgate and d_dup may be d_dy or a plain d_gate or d_up (same pointer and
+ * pitch); the other outputs overlap no input. */
+typedef struct opt_gated_backward_args {
+  const void* d_dy;
+  const void* d_gate;
+  const void* d_gate_scales;
+  const void* d_up;
+  const void* d_up_scales;
+  void* d_dgate;
+  void* d_dup;
+  void* d_dgate_codes;
+  void* d_dgate_scales;
+  void* d_dgate_codes_t;
+  void* d_dgate_scales_t;
+  void* d_dup_codes;
+  void* d_dup_scales;
+  void* d_dup_codes_t;
+  void* d_dup_scales_t;
+  void* d_y_codes_t;
+  void* d_y_scales_t;
+  int64_t dy_pitch, gate_pitch, up_pitch, dgate_pitch, dup_pitch;
+  int64_t dgate_codes_pitch, dgate_codes_t_pitch, dup_codes_pitch, dup_codes_t_pitch, y_codes_t_pitch;
+  int64_t rows, cols;
+  int32_t dtype;
+  int32_t activation;
+} opt_gated_backward_args;
+int opt_gated_backward(const opt_gated_backward_args* a, void* stream);
+
+/* Norm and rotation of heads.  q is rows x (q_heads dim), k is rows x (k_heads dim)
+ * (matrices of their own, or columns of one projection's output); k_heads may be 0.
+ * Per row and head, in fp32 with one rounding of each output:
+ *   n = x weight / sqrt(mean(x^2) + eps)        (the mean over the head's dim elements)
+ *   out = n with its first `rot` elements turned in pairs: with c and s the cosine and
+ *   sine of pair i at the row's position,
+ *     (a, b) -> (a c - b s, b c + a s)
+ * where pair i is (i, i + rot / 2), or (2 i, 2 i + 1) with OPT_HEADS_INTERLEAVED.
+ * d_cos and d_sin are fp32 tables of `positions` x rot / 2 (contiguous); row r stands
+ * at d_positions[r] (int64), or at r if d_positions is NULL (rows <= positions then).
+ * A position outside the tables makes the rotated elements NaN; nothing is read there.
+ * rot is even, 0 <= rot <= dim (0: no rotation, and no tables); 1 <= dim <= 1024.
+ * d_q_codes with d_q_scales (and k's) keep the inputs x for the backward pass: the
+ * whole matrix's 1 x 128 blocks, across heads.  d_q_out may be d_q (same pointer and
+ * pitch); the other outputs overlap no input. */
+#define OPT_HEADS_INTERLEAVED 1
+typedef struct opt_head_norm_args {
+  const void* d_q;
+  const void* d_q_weight;    /* dim elements of weight_dtype */
+  void* d_q_out;
+  void* d_q_codes;
+  void* d_q_scales;
+  const void* d_k;
+  const void* d_k_weight;
+  void* d_k_out;
+  void* d_k_codes;
+  void* d_k_scales;
+  const float* d_cos;
+  const float* d_sin;
+  const int64_t* d_positions;
+  int64_t q_pitch, q_out_pitch, q_codes_pitch, k_pitch, k_out_pitch, k_codes_pitch;
+  int64_t rows, q_heads, k_heads, dim, rot, positions;
+  int32_t dtype;             /* OPT_F32 or OPT_BF16 */
+  int32_t weight_dtype;      /* OPT_F32 or OPT_BF16 */
+  int32_t flags;             /* OPT_HEADS_* bits; others must be 0 */
+  float eps;
+} opt_head_norm_args;
+int opt_head_norm(const opt_head_norm_args* a, void* stream);
+
+/* Gradients of opt_head_norm from dout (the gradients of q_out and k_out) and the
+ * inputs, plain or kept (d_q_scales, and d_k_scales if there are key heads, given: d_q
+ * and d_k are codes):
+ *   g = dout turned back, t = g weight, rstd = 1 / sqrt(mean(x^2) + eps)
+ *   dx = rstd (t - x rstd^2 mean(t x))
+ *   dweight = sum over rows and heads of g x rstd          (NULL: not wanted), fp32
+ * in fp32, each rounded once.  d_dq may be d_dq_out (same pointer and pitch).  The sums
+ * run in a fixed order; they need d_workspace of
+ * opt_head_norm_backward_workspace(rows, q_heads, k_heads, dim) bytes, 16-byte aligned,
+ * when d_dq_weight or d_dk_weight is given (0 bytes: none). */
+typedef struct opt_head_norm_backward_args {
+  const void* d_dq_out;
+  const void* d_q;
+  const void* d_q_scales;
+  const void* d_q_weight;
+  void* d_dq;
+  float* d_dq_weight;
+  const void* d_dk_out;
+  const void* d_k;
+  const void* d_k_scales;
+  const void* d_k_weight;
+  void* d_dk;
+  float* d_dk_weight;
+  const float* d_cos;
+  const float* d_sin;
+  const int64_t* d_positions;
+  void* d_workspace;
+  int64_t dq_out_pitch, q_pitch, dq_pitch, dk_out_pitch, k_pitch, dk_pitch;
+  int64_t workspace_bytes;
+  int64_t rows, q_heads, k_heads, dim, rot, positions;
+  int32_t dtype;             /* of dout, dx and plain inputs */
+  int32_t weight_dtype;
+  int32_t flags;
+  float eps;
+} opt_head_norm_backward_args;
+int opt_head_norm_backward(const opt_head_norm_backward_args* a, void* stream);
+int64_t opt_head_norm_backward_workspace(int64_t rows, int64_t q_heads, int64_t k_heads, int64_t dim);
 
 /* out[m][n] = sum over k of a[m][k] b[n][k] (+ addend[m][n]): both operands
  * with k along their rows, as codes with scales.  Products are exact, and sums are

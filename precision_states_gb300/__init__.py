@@ -331,5 +331,7 @@ class Plan:
 
 # ------------------------------------------------- training-layer operators
 from . import layer as _layer  # noqa: E402
-from .layer import (OPT_MATMUL_WAIT_DRILL, e4m3_storage, opt_dropout, opt_layer_status, opt_matmul, opt_matmul_form, opt_quantize,  # noqa: E402,F401
-                    opt_rms_norm, opt_rms_norm_backward, opt_rms_norm_backward_workspace, opt_scales_bytes)
+from .layer import (OPT_HEADS_INTERLEAVED, OPT_MATMUL_WAIT_DRILL, e4m3_storage, opt_dequantize, opt_dropout, opt_gated,  # noqa: E402,F401
+                    opt_gated_backward, opt_head_norm, opt_head_norm_backward, opt_head_norm_backward_workspace,
+                    opt_layer_status, opt_matmul, opt_matmul_form, opt_quantize, opt_rms_norm, opt_rms_norm_backward,
+                    opt_rms_norm_backward_workspace, opt_scales_bytes)

@@ -1,0 +1,586 @@
+// heads.cu -- the norm of each query and key head with the position rotation in the
+// same pass, and its gradients (opt_layer.h).
+//
+// Mathematics: with x a head, rstd = (mean x^2 + eps)^(-1/2) and a pair's turn by
+// (c, s), an output element is rstd (x w c + x' w' s') where x' and w' are its partner's
+// and s' is -s for a pair's first element and s for its second.  Backward the turn is by
+// (c, -s) on dout's elements: g = dout c - dout' s'.
+//
+// Whole heads are held by groups of lanes, eight elements each (dim / 8 lanes, padded to a
+// power of two), so that sums are a few exchanges and a partner is another lane's raw
+// words or the lane's own.  A warp keeps to one set of heads and goes through rows, so
+// that the weight (and the weight's gradient) stay in registers, and the row's cosines and
+// sines serve all of the set.  Heads of other sizes and places take a form of a warp per
+// head, through shared memory.
+#include "layer.cuh"
+
+namespace psopt {
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kAnyWarps = 4;                     // of the form for any heads: 12 KB of shared memory to a warp
+
+// One side's pointers (queries or keys) out of either call's arguments.
+struct Side {
+  const void *x, *scales, *dout, *weight;
+  void *out, *codes, *code_scales;
+  int64_t x_pitch, dout_pitch, out_pitch, codes_pitch, cols, heads;
+};
+__device__ __forceinline__ Side side_of(const opt_head_norm_args& a, bool keys) {
+  return keys ? Side{a.d_k, nullptr, nullptr, a.d_k_weight, a.d_k_out, a.d_k_codes, a.d_k_scales, a.k_pitch, 0, a.k_out_pitch,
+                     a.k_codes_pitch, a.k_heads * a.dim, a.k_heads}
+              : Side{a.d_q, nullptr, nullptr, a.d_q_weight, a.d_q_out, a.d_q_codes, a.d_q_scales, a.q_pitch, 0, a.q_out_pitch,
+                     a.q_codes_pitch, a.q_heads * a.dim, a.q_heads};
+}
+__device__ __forceinline__ Side side_of(const opt_head_norm_backward_args& a, bool keys) {
+  return keys ? Side{a.d_k, a.d_k_scales, a.d_dk_out, a.d_k_weight, a.d_dk, nullptr, nullptr, a.k_pitch, a.dk_out_pitch,
+                     a.dk_pitch, 0, a.k_heads * a.dim, a.k_heads}
+              : Side{a.d_q, a.d_q_scales, a.d_dq_out, a.d_q_weight, a.d_dq, nullptr, nullptr, a.q_pitch, a.dq_out_pitch,
+                     a.dq_pitch, 0, a.q_heads * a.dim, a.q_heads};
+}
+
+// Sum over a group of `lanes` (a power of two) lanes.
+__device__ __forceinline__ float group_sum(float v, int lanes) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < lanes) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+// The partner's words: those of lane `partner`, or with neighbouring pairs the lane's own
+// with the elements of each pair exchanged.
+template <bool INTERLEAVED>
+__device__ __forceinline__ Raw<Bf16> partner_of(const Raw<Bf16>& x, int partner) {
+  Raw<Bf16> r;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    r.w[k] = INTERLEAVED ? __byte_perm(x.w[k], 0u, 0x1032) : __shfl_sync(0xFFFFFFFFu, x.w[k], partner);
+  return r;
+}
+template <bool INTERLEAVED>
+__device__ __forceinline__ Raw<float> partner_of(const Raw<float>& x, int partner) {
+  Raw<float> r;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) r.w[k] = INTERLEAVED ? x.w[k ^ 1] : __shfl_sync(0xFFFFFFFFu, x.w[k], partner);
+  return r;
+}
+
+// How the warps share the heads: a set is `per_set` heads of one side, `slots` side by
+// side in a warp, U after one another; sets of queries come first.
+struct Sets {
+  int lanes, slots;              // lanes to a head, heads side by side
+  int q_sets, sets;              // of queries; of both
+  int64_t stride;                // rows between a warp's: warps of the grid / sets
+  int warps;                     // that take part
+};
+
+// A lane's eight elements of the rotation at a row: c, and s' with the partner's sign.
+// Elements that are not rotated have c 1 and s' 0.
+template <bool INTERLEAVED>
+__device__ __forceinline__ void turn_of(const float* cos, const float* sin, const int64_t* positions, int64_t table, int rot,
+                                        int64_t r, int e, float (&c)[8], float (&s)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    c[j] = 1.0f;
+    s[j] = 0.0f;
+  }
+  if (e >= rot) return;
+  const int64_t at = positions != nullptr ? positions[r] : r;
+  if (at < 0 || at >= table) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c[j] = s[j] = u2f(0x7FC00000u);
+    return;
+  }
+  const int half = rot >> 1;
+  if constexpr (INTERLEAVED) {
+    const int64_t p = at * half + (e >> 1);
+    const float4 cv = __ldg(reinterpret_cast<const float4*>(cos + p)), sv = __ldg(reinterpret_cast<const float4*>(sin + p));
+    const float cs[4] = {cv.x, cv.y, cv.z, cv.w}, ss[4] = {sv.x, sv.y, sv.z, sv.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      c[2 * j] = c[2 * j + 1] = cs[j];
+      s[2 * j] = -ss[j];
+      s[2 * j + 1] = ss[j];
+    }
+  } else {
+    const bool second = e >= half;
+    const int64_t p = at * half + (second ? e - half : e);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float4 cv = __ldg(reinterpret_cast<const float4*>(cos + p) + k), sv = __ldg(reinterpret_cast<const float4*>(sin + p) + k);
+      c[4 * k] = cv.x; c[4 * k + 1] = cv.y; c[4 * k + 2] = cv.z; c[4 * k + 3] = cv.w;
+      s[4 * k] = sv.x; s[4 * k + 1] = sv.y; s[4 * k + 2] = sv.z; s[4 * k + 3] = sv.w;
+    }
+    if (!second) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] = -s[j];
+    }
+  }
+}
+
+// What a lane of a set of heads is.
+struct Lane {
+  int e, partner;                // its first element in the head; the lane with the partners' elements
+  bool on;                       // it has elements
+  int64_t head, head_step;       // its first head, and from one to the next
+  bool keys;
+  int64_t first_row;
+};
+__device__ __forceinline__ Lane lane_of(const Sets& sets, int dim, int rot, int u) {
+  Lane l;
+  const int lane = threadIdx.x & 31, in = lane & (sets.lanes - 1);
+  const int64_t warp = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int set = (int)(warp % sets.sets);
+  l.first_row = warp < sets.warps ? warp / sets.sets : (int64_t)1 << 62;
+  l.keys = set >= sets.q_sets;
+  l.e = 8 * in;
+  l.on = l.e < dim;
+  const int half = rot >> 1;
+  l.partner = lane + (l.e >= rot ? 0 : l.e < half ? half >> 3 : -(half >> 3));
+  l.head_step = sets.slots;
+  l.head = (int64_t)(l.keys ? set - sets.q_sets : set) * sets.slots * u + lane / sets.lanes;
+  return l;
+}
+
+// Row r, element e of the head: the column.
+template <typename T, typename W, bool INTERLEAVED, int U>
+__global__ void __launch_bounds__(kThreads, 2) head_norm_kernel(const __grid_constant__ opt_head_norm_args a, Sets sets) {
+  const int dim = (int)a.dim, rot = (int)a.rot;
+  const Lane l = lane_of(sets, dim, rot, U);
+  if (l.first_row >= a.rows) return;
+  const Side side = side_of(a, l.keys);
+  const int64_t panel = (side.cols + 511) / 512;
+  const float inv_dim = 1.0f / (float)dim;
+  float w[8] = {}, wp[8] = {};
+  if (l.on) {
+    const Raw<W> raw = load_raw<true>(static_cast<const W*>(side.weight) + l.e, 8);
+    unpack(raw, w);
+    const int pe = INTERLEAVED ? l.e : 8 * (l.partner & (sets.lanes - 1));
+    float v[8];
+    unpack(load_raw<true>(static_cast<const W*>(side.weight) + pe, 8), v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) wp[j] = v[INTERLEAVED ? j ^ 1 : j];
+  }
+  for (int64_t r = l.first_row; r < a.rows; r += sets.stride) {
+    Raw<T> x[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      x[k] = {};
+      const int64_t h = l.head + k * l.head_step;
+      if (l.on && h < side.heads) x[k] = load_raw<true>(static_cast<const T*>(side.x) + r * side.x_pitch + h * dim + l.e, 8);
+    }
+    float c[8], s[8];
+    turn_of<INTERLEAVED>(a.d_cos, a.d_sin, a.d_positions, a.positions, rot, r, l.e, c, s);
+    times8(c, w);
+    times8(s, wp);
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int64_t h = l.head + k * l.head_step, col = h * dim + l.e;
+      const bool on = l.on && h < side.heads;
+      float v[8], p[8], y[8];
+      unpack(x[k], v);
+      unpack(partner_of<INTERLEAVED>(x[k], l.partner), p);
+      float sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum = fmaf(v[j], v[j], sum);
+      sum = group_sum(sum, sets.lanes);
+      const float rstd = reciprocal_root(fmaf(sum, inv_dim, a.eps));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = rstd * fmaf(v[j], c[j], l.e < rot ? p[j] * s[j] : 0.0f);
+      if (on) store8<true>(static_cast<T*>(side.out) + r * side.out_pitch + col, 8, y);
+      if (side.codes != nullptr)
+        put_codes8(side.codes, side.code_scales, side.codes_pitch, panel, r, col, on ? 8 : 0, v);
+    }
+  }
+}
+
+// Partial sums of the weights' gradients: a CTA's row of 2 x dim, queries' first.
+template <typename T, typename S, typename W, bool INTERLEAVED, int U>
+__global__ void __launch_bounds__(kThreads, 2) head_norm_backward_kernel(const __grid_constant__ opt_head_norm_backward_args a,
+                                                                        Sets sets, float* parts) {
+  __shared__ float sums[kWarps][32][8];
+  const int dim = (int)a.dim, rot = (int)a.rot;
+  const Lane l = lane_of(sets, dim, rot, U);
+  const Side side = side_of(a, l.keys);
+  const float inv_dim = 1.0f / (float)dim;
+  float w[8] = {}, dw[8] = {};
+  if (l.on && l.first_row < a.rows) unpack(load_raw<true>(static_cast<const W*>(side.weight) + l.e, 8), w);
+  for (int64_t r = l.first_row; r < a.rows; r += sets.stride) {
+    const Source<S, true> x_row(side.x, side.scales, side.x_pitch, a.rows, side.cols, r);
+    Raw<T> d[U];
+    typename Source<S, true>::Ask x[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      d[k] = {};
+      x[k] = {};
+      const int64_t h = l.head + k * l.head_step;
+      if (l.on && h < side.heads) {
+        d[k] = load_raw<true>(static_cast<const T*>(side.dout) + r * side.dout_pitch + h * dim + l.e, 8);
+        x[k] = x_row.ahead(h * dim + l.e, 8);
+      }
+    }
+    float c[8], s[8];
+    turn_of<INTERLEAVED>(a.d_cos, a.d_sin, a.d_positions, a.positions, rot, r, l.e, c, s);
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int64_t h = l.head + k * l.head_step, col = h * dim + l.e;
+      const bool on = l.on && h < side.heads;
+      float v[8], g[8], p[8];
+      x_row.values(x[k], col, 8, v);
+      unpack(d[k], g);
+      unpack(partner_of<INTERLEAVED>(d[k], l.partner), p);
+      float square = 0.0f, dot = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        // the turn back has the opposite sign; s' belongs to this element
+        g[j] = fmaf(g[j], c[j], l.e < rot ? -p[j] * s[j] : 0.0f);
+        square = fmaf(v[j], v[j], square);
+        dot = fmaf(g[j] * w[j], v[j], dot);
+      }
+      square = group_sum(square, sets.lanes);
+      dot = group_sum(dot, sets.lanes);
+      const float rstd = reciprocal_root(fmaf(square, inv_dim, a.eps));
+      const float pull = rstd * rstd * (dot * inv_dim);
+      if (on) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dw[j] = fmaf(g[j], v[j] * rstd, dw[j]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] = rstd * fmaf(-v[j], pull, g[j] * w[j]);
+        store8<true>(static_cast<T*>(side.out) + r * side.out_pitch + col, 8, g);
+      }
+    }
+  }
+  if (parts == nullptr) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sums[threadIdx.x >> 5][threadIdx.x & 31][j] = dw[j];
+  __syncthreads();
+  // element t of a side: over the warps that had it, and the heads side by side, in order
+  float* out = parts + (int64_t)blockIdx.x * 2 * dim;
+  for (int t = threadIdx.x; t < 2 * dim; t += kThreads) {
+    const bool keys = t >= dim;
+    const int e = keys ? t - dim : t;
+    float v = 0.0f;
+    for (int k = 0; k < kWarps; ++k) {
+      const int64_t warp = (int64_t)blockIdx.x * kWarps + k;
+      if (warp >= sets.warps || ((int)(warp % sets.sets) >= sets.q_sets) != keys) continue;
+      for (int i = 0; i < sets.slots; ++i) v += sums[k][i * sets.lanes + (e >> 3)][e & 7];
+    }
+    out[t] = v;
+  }
+}
+
+// ------------------------------------------------------- heads of any size and place
+// A warp takes a head at a time through shared memory.  Element j of a head, of a plain
+// matrix or a kept one:
+template <typename T>
+__device__ __forceinline__ float element_at(const Side& side, int64_t r, int64_t col, int64_t panel, T) {
+  return element(static_cast<const T*>(side.x) + r * side.x_pitch + col);
+}
+__device__ __forceinline__ float element_at(const Side& side, int64_t r, int64_t col, int64_t panel, E4m3) {
+  const uint32_t byte = static_cast<const uint8_t*>(side.scales)[scale_place(r, col >> 7, panel)];
+  float lo, hi;
+  e4m3x2_dec(static_cast<const uint8_t*>(side.x)[r * side.x_pitch + col], lo, hi);
+  return lo * scale_of(byte);
+}
+__device__ __forceinline__ void put_element(Bf16* p, float v) { p->bits = (uint16_t)bf16_pair(v, 0.0f); }
+__device__ __forceinline__ void put_element(float* p, float v) { *p = v; }
+
+// The turn of element j: its partner, c and s'; false outside the rotated ones.
+__device__ __forceinline__ bool turn_at(const float* cos, const float* sin, int64_t at, int64_t table, int rot, bool interleaved,
+                                        int j, int& partner, float& c, float& s) {
+  if (j >= rot) return false;
+  const int half = rot >> 1;
+  const bool second = interleaved ? (j & 1) : j >= half;
+  const int pair = interleaved ? j >> 1 : second ? j - half : j;
+  partner = interleaved ? j ^ 1 : second ? j - half : j + half;
+  if (at < 0 || at >= table) {
+    c = s = u2f(0x7FC00000u);
+  } else {
+    c = cos[at * half + pair];
+    s = sin[at * half + pair];
+  }
+  if (!second) s = -s;
+  return true;
+}
+
+template <typename T, typename W>
+__global__ void __launch_bounds__(32 * kAnyWarps) head_norm_any_kernel(const __grid_constant__ opt_head_norm_args a) {
+  __shared__ float held[kAnyWarps][kHeadMaxDim];
+  float* x = held[threadIdx.x >> 5];
+  const int lane = threadIdx.x & 31, dim = (int)a.dim, rot = (int)a.rot;
+  const int64_t heads = a.q_heads + a.k_heads, n = a.rows * heads;
+  for (int64_t i = (int64_t)blockIdx.x * kAnyWarps + (threadIdx.x >> 5); i < n; i += (int64_t)gridDim.x * kAnyWarps) {
+    const int64_t r = i / heads, both = i % heads;
+    const Side side = side_of(a, both >= a.q_heads);
+    const int64_t col = (both >= a.q_heads ? both - a.q_heads : both) * dim;
+    const W* weight = static_cast<const W*>(side.weight);
+    float sum = 0.0f;
+    for (int j = lane; j < dim; j += 32) {
+      x[j] = element_at(side, r, col + j, 0, T());
+      sum = fmaf(x[j], x[j], sum);
+    }
+    sum = group_sum(sum, 32);
+    const float rstd = reciprocal_root(fmaf(sum, 1.0f / (float)dim, a.eps));
+    __syncwarp();
+    const int64_t at = rot > 0 && a.d_positions != nullptr ? a.d_positions[r] : r;
+    for (int j = lane; j < dim; j += 32) {
+      int p = j;
+      float c, s, y = x[j] * element(weight + j);
+      if (turn_at(a.d_cos, a.d_sin, at, a.positions, rot, a.flags & OPT_HEADS_INTERLEAVED, j, p, c, s))
+        y = fmaf(y, c, x[p] * element(weight + p) * s);
+      put_element(static_cast<T*>(side.out) + r * side.out_pitch + col + j, rstd * y);
+    }
+    __syncwarp();
+  }
+}
+
+// The weights' gradients of a warp's heads are summed in shared memory, queries' first and
+// then, in a launch's second half of CTAs, keys' (`q_ctas` CTAs take queries).
+template <typename T, typename S, typename W>
+__global__ void __launch_bounds__(32 * kAnyWarps) head_norm_backward_any_kernel(
+    const __grid_constant__ opt_head_norm_backward_args a, int q_ctas, float* parts) {
+  __shared__ float held[kAnyWarps][2][kHeadMaxDim];
+  __shared__ float sums[kAnyWarps][kHeadMaxDim];
+  const int wi = threadIdx.x >> 5, lane = threadIdx.x & 31, dim = (int)a.dim, rot = (int)a.rot;
+  float *x = held[wi][0], *d = held[wi][1], *dw = sums[wi];
+  const bool keys = (int)blockIdx.x >= q_ctas;
+  const Side side = side_of(a, keys);
+  const int64_t cta = keys ? blockIdx.x - q_ctas : blockIdx.x, ctas = keys ? gridDim.x - q_ctas : q_ctas;
+  const int64_t n = a.rows * side.heads, panel = (side.cols + 511) / 512;
+  const W* weight = static_cast<const W*>(side.weight);
+  for (int j = lane; j < dim; j += 32) dw[j] = 0.0f;
+  for (int64_t i = cta * kAnyWarps + wi; i < n; i += ctas * kAnyWarps) {
+    const int64_t r = i / side.heads, col = i % side.heads * dim;
+    const int64_t at = rot > 0 && a.d_positions != nullptr ? a.d_positions[r] : r;
+    for (int j = lane; j < dim; j += 32) {
+      x[j] = element_at(side, r, col + j, panel, S());
+      d[j] = element(static_cast<const T*>(side.dout) + r * side.dout_pitch + col + j);
+    }
+    __syncwarp();
+    const auto turned = [&](int j) {
+      int p = j;
+      float c, s;
+      return turn_at(a.d_cos, a.d_sin, at, a.positions, rot, a.flags & OPT_HEADS_INTERLEAVED, j, p, c, s)
+                 ? fmaf(d[j], c, -d[p] * s) : d[j];
+    };
+    float square = 0.0f, dot = 0.0f;
+    for (int j = lane; j < dim; j += 32) {
+      square = fmaf(x[j], x[j], square);
+      dot = fmaf(turned(j) * element(weight + j), x[j], dot);
+    }
+    square = group_sum(square, 32);
+    dot = group_sum(dot, 32);
+    const float rstd = reciprocal_root(fmaf(square, 1.0f / (float)dim, a.eps));
+    const float pull = rstd * rstd * (dot * (1.0f / (float)dim));
+    for (int j = lane; j < dim; j += 32) {
+      const float g = turned(j);
+      dw[j] = fmaf(g, x[j] * rstd, dw[j]);
+      put_element(static_cast<T*>(side.out) + r * side.out_pitch + col + j, rstd * fmaf(-x[j], pull, g * element(weight + j)));
+    }
+    __syncwarp();
+  }
+  if (parts == nullptr) return;
+  __syncthreads();
+  for (int t = threadIdx.x; t < 2 * dim; t += 32 * kAnyWarps) {
+    float v = 0.0f;
+    if ((t >= dim) == keys)
+      for (int k = 0; k < kAnyWarps; ++k) v += sums[k][t >= dim ? t - dim : t];
+    parts[(int64_t)blockIdx.x * 2 * dim + t] = v;
+  }
+}
+
+// The weights' gradients: the partial sums' rows in a fixed order, 32 columns to a CTA.
+constexpr int kSumCols = 32, kSumParts = 32;
+__global__ void __launch_bounds__(kSumCols * kSumParts) head_weight_kernel(const float* __restrict__ parts, int n, int dim,
+                                                                           float* dq, float* dk) {
+  __shared__ float sums[kSumParts][kSumCols + 1];
+  const int x = threadIdx.x % kSumCols, p0 = threadIdx.x / kSumCols, t = blockIdx.x * kSumCols + x;
+  float s = 0.0f;
+  if (t < 2 * dim) {
+#pragma unroll 4
+    for (int p = p0; p < n; p += kSumParts) s += parts[(int64_t)p * 2 * dim + t];
+  }
+  sums[p0][x] = s;
+  __syncthreads();
+  if (p0 != 0 || t >= 2 * dim) return;
+#pragma unroll
+  for (int p = 1; p < kSumParts; ++p) s += sums[p][x];
+  if (t < dim) {
+    if (dq != nullptr) dq[t] = s;
+  } else if (dk != nullptr) {
+    dk[t - dim] = s;
+  }
+}
+
+// Whether whole chunks of eight elements, rotated with their partners' whole chunks, start
+// on 16 bytes everywhere.
+struct Whole {
+  int64_t rows;
+  bool ok;
+  void see(const void* p, int64_t pitch, int64_t es) {
+    ok = ok && ((uintptr_t)p & 15u) == 0 && (rows == 1 || pitch * es % 16 == 0);
+  }
+};
+template <typename A>
+Whole whole_heads(const A& a, int64_t ws) {
+  Whole v{a.rows, a.dim % 8 == 0 && a.dim <= 256 && a.rot % ((a.flags & OPT_HEADS_INTERLEAVED) ? 8 : 16) == 0};
+  if (a.q_heads > 0) v.see(a.d_q_weight, 0, ws);
+  if (a.k_heads > 0) v.see(a.d_k_weight, 0, ws);
+  if (a.rot > 0) {
+    v.see(a.d_cos, 0, 4);
+    v.see(a.d_sin, 0, 4);
+  }
+  return v;
+}
+
+// The warps' sets for U heads after one another, and the CTAs.
+template <typename A>
+Sets sets_of(const A& a, int u, int64_t max_ctas, int* ctas) {
+  Sets s;
+  s.lanes = 1;
+  while (8 * s.lanes < a.dim) s.lanes *= 2;
+  s.slots = 32 / s.lanes;
+  const int64_t per = (int64_t)s.slots * u;
+  s.q_sets = (int)((a.q_heads + per - 1) / per);
+  s.sets = s.q_sets + (int)((a.k_heads + per - 1) / per);
+  const int64_t need = a.rows * s.sets, have = max_ctas * kWarps;
+  // every set as many warps as rows at most; where there are more sets than warps, each set one
+  s.stride = need <= have ? a.rows : have / s.sets;
+  if (s.stride < 1) s.stride = 1;
+  s.warps = (int)(s.stride * s.sets);
+  *ctas = (s.warps + kWarps - 1) / kWarps;
+  return s;
+}
+
+template <typename T, typename W, bool INTERLEAVED>
+cudaError_t forward_heads(const opt_head_norm_args& a, int sm_count, cudaStream_t s) {
+  constexpr int U = sizeof(T) == 2 ? 4 : 2;
+  static OccupancyCache cache;
+  const auto kernel = head_norm_kernel<T, W, INTERLEAVED, U>;
+  int ctas;
+  const Sets sets = sets_of(a, U, (int64_t)sm_count * cached_occupancy(kernel, cache, kThreads, 0), &ctas);
+  kernel<<<ctas, kThreads, 0, s>>>(a, sets);
+  return cudaGetLastError();
+}
+
+cudaError_t keep(const void* x, int64_t x_pitch, void* codes, void* scales, int64_t pitch, int64_t rows, int64_t cols,
+                 int32_t dtype, cudaStream_t s) {
+  if (codes == nullptr || cols == 0) return cudaSuccess;
+  opt_quantize_args q = {};
+  q.d_x = x;
+  q.d_codes = codes;
+  q.d_scales = scales;
+  q.x_pitch = x_pitch;
+  q.codes_pitch = pitch;
+  q.rows = rows;
+  q.cols = cols;
+  q.dtype = dtype;
+  q.block_rows = 1;
+  return launch_quantize(q, s);
+}
+
+template <typename T, typename W>
+cudaError_t forward(const opt_head_norm_args& a, int sm_count, cudaStream_t s) {
+  Whole v = whole_heads(a, sizeof(W));
+  if (a.q_heads > 0) {
+    v.see(a.d_q, a.q_pitch, sizeof(T));
+    v.see(a.d_q_out, a.q_out_pitch, sizeof(T));
+  }
+  if (a.k_heads > 0) {
+    v.see(a.d_k, a.k_pitch, sizeof(T));
+    v.see(a.d_k_out, a.k_out_pitch, sizeof(T));
+  }
+  opt_head_norm_args b = a;
+  // blocks of 128 go with groups of lanes only where heads are of 8, 16, ... 256 elements;
+  // else the quantizer keeps the inputs (before an output may take their place)
+  if (!v.ok || (a.dim & (a.dim - 1)) != 0) {
+    cudaError_t e = keep(a.d_q, a.q_pitch, a.d_q_codes, a.d_q_scales, a.q_codes_pitch, a.rows, a.q_heads * a.dim, a.dtype, s);
+    if (e == cudaSuccess)
+      e = keep(a.d_k, a.k_pitch, a.d_k_codes, a.d_k_scales, a.k_codes_pitch, a.rows, a.k_heads * a.dim, a.dtype, s);
+    if (e != cudaSuccess) return e;
+    b.d_q_codes = b.d_k_codes = nullptr;
+  }
+  if (v.ok) {
+    return a.flags & OPT_HEADS_INTERLEAVED ? forward_heads<T, W, true>(b, sm_count, s) : forward_heads<T, W, false>(b, sm_count, s);
+  }
+  const int64_t need = (a.rows * (a.q_heads + a.k_heads) + kAnyWarps - 1) / kAnyWarps, most = (int64_t)sm_count * 12;
+  head_norm_any_kernel<T, W><<<(unsigned)(need < most ? need : most), 32 * kAnyWarps, 0, s>>>(b);
+  return cudaGetLastError();
+}
+
+cudaError_t weight_sums(const opt_head_norm_backward_args& a, int ctas, cudaStream_t s) {
+  if (a.d_dq_weight != nullptr || a.d_dk_weight != nullptr)
+    head_weight_kernel<<<(unsigned)((2 * a.dim + kSumCols - 1) / kSumCols), kSumCols * kSumParts, 0, s>>>(
+        static_cast<const float*>(a.d_workspace), ctas, (int)a.dim, a.d_dq_weight, a.d_dk_weight);
+  return cudaGetLastError();
+}
+
+template <typename T, typename S, typename W>
+cudaError_t backward_any(const opt_head_norm_backward_args& a, int sm_count, float* parts, cudaStream_t s) {
+  // as many CTAs for either side as it has heads' share, and within the workspace's rows
+  const int64_t heads = a.q_heads + a.k_heads, most = (int64_t)sm_count * 4 < kHeadBackwardMaxCtas / 2 ? (int64_t)sm_count * 4 : kHeadBackwardMaxCtas / 2;
+  const auto ctas_of = [&](int64_t h) {
+    const int64_t need = (a.rows * h + kAnyWarps - 1) / kAnyWarps, share = (most * h + heads - 1) / heads;
+    return (int)(need < share ? need : share);
+  };
+  const int q_ctas = ctas_of(a.q_heads), ctas = q_ctas + ctas_of(a.k_heads);
+  head_norm_backward_any_kernel<T, S, W><<<(unsigned)ctas, 32 * kAnyWarps, 0, s>>>(a, q_ctas, parts);
+  return weight_sums(a, ctas, s);
+}
+
+template <typename T, typename S, typename W, bool INTERLEAVED>
+cudaError_t backward_heads(const opt_head_norm_backward_args& a, int sm_count, float* parts, cudaStream_t s) {
+  constexpr int U = sizeof(T) == 2 ? 4 : 2;
+  static OccupancyCache cache;
+  const auto kernel = head_norm_backward_kernel<T, S, W, INTERLEAVED, U>;
+  int64_t most = (int64_t)sm_count * cached_occupancy(kernel, cache, kThreads, 0);
+  if (most > kHeadBackwardMaxCtas) most = kHeadBackwardMaxCtas;
+  int ctas;
+  const Sets sets = sets_of(a, U, most, &ctas);
+  if (ctas > kHeadBackwardMaxCtas) return backward_any<T, S, W>(a, sm_count, parts, s);      // more sets than the workspace has room for
+  kernel<<<ctas, kThreads, 0, s>>>(a, sets, parts);
+  return weight_sums(a, ctas, s);
+}
+
+template <typename T, typename S, typename W>
+cudaError_t backward_from(const opt_head_norm_backward_args& a, int sm_count, cudaStream_t s) {
+  Whole v = whole_heads(a, sizeof(W));
+  constexpr bool kept = sizeof(S) == 1;
+  if (a.q_heads > 0) {
+    if (!kept) v.see(a.d_q, a.q_pitch, sizeof(T));
+    v.see(a.d_dq_out, a.dq_out_pitch, sizeof(T));
+    v.see(a.d_dq, a.dq_pitch, sizeof(T));
+  }
+  if (a.k_heads > 0) {
+    if (!kept) v.see(a.d_k, a.k_pitch, sizeof(T));
+    v.see(a.d_dk_out, a.dk_out_pitch, sizeof(T));
+    v.see(a.d_dk, a.dk_pitch, sizeof(T));
+  }
+  float* parts = a.d_dq_weight != nullptr || a.d_dk_weight != nullptr ? static_cast<float*>(a.d_workspace) : nullptr;
+  if (v.ok)
+    return a.flags & OPT_HEADS_INTERLEAVED ? backward_heads<T, S, W, true>(a, sm_count, parts, s)
+                                           : backward_heads<T, S, W, false>(a, sm_count, parts, s);
+  return backward_any<T, S, W>(a, sm_count, parts, s);
+}
+
+template <typename T, typename W>
+cudaError_t backward(const opt_head_norm_backward_args& a, int sm_count, cudaStream_t s) {
+  return a.d_q_scales != nullptr || a.d_k_scales != nullptr ? backward_from<T, E4m3, W>(a, sm_count, s)
+                                                            : backward_from<T, T, W>(a, sm_count, s);
+}
+
+}  // namespace
+
+cudaError_t launch_head_norm(const opt_head_norm_args& a, int sm_count, cudaStream_t s) {
+  if (a.dtype == OPT_F32)
+    return a.weight_dtype == OPT_F32 ? forward<float, float>(a, sm_count, s) : forward<float, Bf16>(a, sm_count, s);
+  return a.weight_dtype == OPT_F32 ? forward<Bf16, float>(a, sm_count, s) : forward<Bf16, Bf16>(a, sm_count, s);
+}
+
+cudaError_t launch_head_norm_backward(const opt_head_norm_backward_args& a, int sm_count, cudaStream_t s) {
+  if (a.dtype == OPT_F32)
+    return a.weight_dtype == OPT_F32 ? backward<float, float>(a, sm_count, s) : backward<float, Bf16>(a, sm_count, s);
+  return a.weight_dtype == OPT_F32 ? backward<Bf16, float>(a, sm_count, s) : backward<Bf16, Bf16>(a, sm_count, s);
+}
+
+}  // namespace psopt

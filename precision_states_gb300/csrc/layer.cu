@@ -10,6 +10,12 @@ namespace {
 
 constexpr int64_t kMaxDim = 0x7FFFFFFF;
 
+#define PS_TRY(expr)                 \
+  do {                               \
+    const int ps_st = (expr);        \
+    if (ps_st != OPT_OK) return ps_st; \
+  } while (0)
+
 bool plain_type(int32_t t) { return t == OPT_F32 || t == OPT_BF16; }
 int64_t plain_size(int32_t t) { return t == OPT_F32 ? 4 : 2; }
 
@@ -30,12 +36,6 @@ int check_sizes(int64_t rows, int64_t cols) {
   return rows > kMaxDim || cols > kMaxDim ? OPT_ELIMIT : OPT_OK;
 }
 
-#define PS_TRY(expr)                 \
-  do {                               \
-    const int ps_st = (expr);        \
-    if (ps_st != OPT_OK) return ps_st; \
-  } while (0)
-
 int drop_args(double p, uint64_t seed, uint32_t tensor, int64_t step, DropArgs* d) {
   if (!(p >= 0.0 && p <= 1.0) || step < 0) return OPT_EINVAL;
   d->threshold = (uint32_t)std::nearbyint(65536.0 * p);
@@ -44,6 +44,41 @@ int drop_args(double p, uint64_t seed, uint32_t tensor, int64_t step, DropArgs* 
   d->step32 = (uint32_t)step;
   philox_round_keys(seed, d->rk);
   return OPT_OK;
+}
+
+// A pair of codes and scales that may be left out, but not in part.
+int check_kept(const void* codes, int64_t pitch, const void* scales, int64_t rows, int64_t cols) {
+  if (codes == nullptr && scales == nullptr) return OPT_OK;
+  return check_codes(codes, pitch, scales, rows, cols);
+}
+// The same of a plain matrix.
+int check_optional(const void* p, int64_t pitch, int64_t rows, int64_t cols, int64_t align) {
+  return p == nullptr ? OPT_OK : check_matrix(p, pitch, rows, cols, align);
+}
+int check_tiles(int64_t rows, int64_t cols) {
+  return ((rows + 127) / 128) * ((cols + 127) / 128) > kMaxDim ? OPT_ELIMIT : OPT_OK;
+}
+
+// What both directions of the heads' norm share; OPT_OK with rows 0 too.
+template <typename A>
+int check_heads(const A& a) {
+  PS_TRY(check_sizes(a.rows, a.positions));
+  PS_TRY(check_sizes(a.q_heads, a.k_heads));
+  PS_TRY(check_sizes(a.dim, a.rot));
+  if (a.dim < 1 || a.rot > a.dim || a.rot % 2 != 0 || (a.flags & ~OPT_HEADS_INTERLEAVED) != 0) return OPT_EINVAL;
+  if (a.dim > kHeadMaxDim || a.q_heads * a.dim > kMaxDim || a.k_heads * a.dim > kMaxDim) return OPT_ELIMIT;
+  if (!plain_type(a.dtype) || !plain_type(a.weight_dtype)) return OPT_EUNSUPPORTED;
+  if (!(a.eps >= 0.0f) || std::isinf(a.eps)) return OPT_EINVAL;
+  return OPT_OK;
+}
+// Its tables, for rows that there are.
+template <typename A>
+int check_turn(const A& a) {
+  if (a.rot == 0) return OPT_OK;
+  PS_TRY(check_matrix(a.d_cos, a.rot / 2, a.positions, a.rot / 2, 4));
+  PS_TRY(check_matrix(a.d_sin, a.rot / 2, a.positions, a.rot / 2, 4));
+  if (a.d_positions == nullptr) return a.rows > a.positions ? OPT_EINVAL : OPT_OK;
+  return ((uintptr_t)a.d_positions & 7u) ? OPT_EALIGN : OPT_OK;
 }
 
 int status_of(cudaError_t e) { return e == cudaSuccess ? OPT_OK : OPT_ECUDA; }
@@ -155,8 +190,150 @@ int opt_quantize(const opt_quantize_args* a, void* stream) {
     PS_TRY(check_codes(a->d_codes, a->codes_pitch, a->d_scales, a->rows, a->cols));
   if (a->d_codes_t != nullptr || a->d_scales_t != nullptr)
     PS_TRY(check_codes(a->d_codes_t, a->codes_t_pitch, a->d_scales_t, a->cols, a->rows));
-  if (((a->rows + 127) / 128) * ((a->cols + 127) / 128) > kMaxDim) return OPT_ELIMIT;
+  PS_TRY(check_tiles(a->rows, a->cols));
   return status_of(launch_quantize(*a, static_cast<cudaStream_t>(stream)));
+}
+
+int opt_dequantize(const opt_dequantize_args* a, void* stream) {
+  if (a == nullptr || a->reserved != 0) return OPT_EINVAL;
+  PS_TRY(check_sizes(a->rows, a->cols));
+  if (!plain_type(a->dtype)) return OPT_EUNSUPPORTED;
+  if (a->rows == 0 || a->cols == 0) return OPT_OK;
+  PS_TRY(check_codes(a->d_codes, a->codes_pitch, a->d_scales, a->rows, a->cols));
+  PS_TRY(check_optional(a->d_x, a->x_pitch, a->rows, a->cols, plain_size(a->dtype)));
+  PS_TRY(check_kept(a->d_codes_t, a->codes_t_pitch, a->d_scales_t, a->cols, a->rows));
+  if (a->d_x == nullptr && a->d_codes_t == nullptr) return OPT_EINVAL;
+  PS_TRY(check_tiles(a->rows, a->cols));
+  return status_of(launch_dequantize(*a, static_cast<cudaStream_t>(stream)));
+}
+
+int opt_gated(const opt_gated_args* a, void* stream) {
+  if (a == nullptr || a->activation < OPT_ACT_SILU || a->activation > OPT_ACT_RELU) return OPT_EINVAL;
+  PS_TRY(check_sizes(a->rows, a->cols));
+  if (!plain_type(a->dtype)) return OPT_EUNSUPPORTED;
+  if (a->rows == 0 || a->cols == 0) return OPT_OK;
+  const int64_t es = plain_size(a->dtype);
+  PS_TRY(check_matrix(a->d_gate, a->gate_pitch, a->rows, a->cols, es));
+  PS_TRY(check_optional(a->d_up, a->up_pitch, a->rows, a->cols, es));
+  PS_TRY(check_optional(a->d_y, a->y_pitch, a->rows, a->cols, es));
+  PS_TRY(check_kept(a->d_codes, a->codes_pitch, a->d_scales, a->rows, a->cols));
+  PS_TRY(check_kept(a->d_gate_codes, a->gate_codes_pitch, a->d_gate_scales, a->rows, a->cols));
+  PS_TRY(check_kept(a->d_up_codes, a->up_codes_pitch, a->d_up_scales, a->rows, a->cols));
+  if (a->d_up == nullptr && a->d_up_codes != nullptr) return OPT_EINVAL;
+  if (a->d_y == nullptr && a->d_codes == nullptr && a->d_gate_codes == nullptr && a->d_up_codes == nullptr) return OPT_EINVAL;
+  return status_of(launch_gated(*a, static_cast<cudaStream_t>(stream)));
+}
+
+int opt_gated_backward(const opt_gated_backward_args* a, void* stream) {
+  if (a == nullptr || a->activation < OPT_ACT_SILU || a->activation > OPT_ACT_RELU) return OPT_EINVAL;
+  PS_TRY(check_sizes(a->rows, a->cols));
+  if (!plain_type(a->dtype)) return OPT_EUNSUPPORTED;
+  if (a->rows == 0 || a->cols == 0) return OPT_OK;
+  const int64_t es = plain_size(a->dtype), rows = a->rows, cols = a->cols;
+  PS_TRY(check_matrix(a->d_dy, a->dy_pitch, rows, cols, es));
+  if (a->d_gate_scales != nullptr) {
+    PS_TRY(check_codes(a->d_gate, a->gate_pitch, a->d_gate_scales, rows, cols));
+    PS_TRY(check_kept(a->d_up, a->up_pitch, a->d_up_scales, rows, cols));
+  } else {
+    if (a->d_up_scales != nullptr) return OPT_EINVAL;
+    PS_TRY(check_matrix(a->d_gate, a->gate_pitch, rows, cols, es));
+    PS_TRY(check_optional(a->d_up, a->up_pitch, rows, cols, es));
+  }
+  PS_TRY(check_optional(a->d_dgate, a->dgate_pitch, rows, cols, es));
+  PS_TRY(check_optional(a->d_dup, a->dup_pitch, rows, cols, es));
+  PS_TRY(check_kept(a->d_dgate_codes, a->dgate_codes_pitch, a->d_dgate_scales, rows, cols));
+  PS_TRY(check_kept(a->d_dup_codes, a->dup_codes_pitch, a->d_dup_scales, rows, cols));
+  PS_TRY(check_kept(a->d_dgate_codes_t, a->dgate_codes_t_pitch, a->d_dgate_scales_t, cols, rows));
+  PS_TRY(check_kept(a->d_dup_codes_t, a->dup_codes_t_pitch, a->d_dup_scales_t, cols, rows));
+  PS_TRY(check_kept(a->d_y_codes_t, a->y_codes_t_pitch, a->d_y_scales_t, cols, rows));
+  const bool dup = a->d_dup != nullptr || a->d_dup_codes != nullptr || a->d_dup_codes_t != nullptr;
+  if (a->d_up == nullptr && dup) return OPT_EINVAL;
+  if (!dup && a->d_dgate == nullptr && a->d_dgate_codes == nullptr && a->d_dgate_codes_t == nullptr && a->d_y_codes_t == nullptr)
+    return OPT_EINVAL;
+  PS_TRY(check_tiles(rows, cols));
+  return status_of(launch_gated_backward(*a, static_cast<cudaStream_t>(stream)));
+}
+
+int opt_head_norm(const opt_head_norm_args* a, void* stream) {
+  if (a == nullptr) return OPT_EINVAL;
+  PS_TRY(check_heads(*a));
+  if (a->rows == 0 || a->q_heads + a->k_heads == 0) return OPT_OK;
+  const int64_t es = plain_size(a->dtype), ws = plain_size(a->weight_dtype);
+  if (a->q_heads > 0) {
+    const int64_t cols = a->q_heads * a->dim;
+    PS_TRY(check_matrix(a->d_q, a->q_pitch, a->rows, cols, es));
+    PS_TRY(check_matrix(a->d_q_weight, a->dim, 1, a->dim, ws));
+    PS_TRY(check_matrix(a->d_q_out, a->q_out_pitch, a->rows, cols, es));
+    PS_TRY(check_kept(a->d_q_codes, a->q_codes_pitch, a->d_q_scales, a->rows, cols));
+    PS_TRY(check_tiles(a->rows, cols));
+  }
+  if (a->k_heads > 0) {
+    const int64_t cols = a->k_heads * a->dim;
+    PS_TRY(check_matrix(a->d_k, a->k_pitch, a->rows, cols, es));
+    PS_TRY(check_matrix(a->d_k_weight, a->dim, 1, a->dim, ws));
+    PS_TRY(check_matrix(a->d_k_out, a->k_out_pitch, a->rows, cols, es));
+    PS_TRY(check_kept(a->d_k_codes, a->k_codes_pitch, a->d_k_scales, a->rows, cols));
+    PS_TRY(check_tiles(a->rows, cols));
+  }
+  PS_TRY(check_turn(*a));
+  int sms = 0;
+  PS_TRY(sm_count_of(&sms));
+  return status_of(launch_head_norm(*a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t opt_head_norm_backward_workspace(int64_t rows, int64_t q_heads, int64_t k_heads, int64_t dim) {
+  PS_TRY(check_sizes(rows, dim));
+  PS_TRY(check_sizes(q_heads, k_heads));
+  if (dim < 1) return OPT_EINVAL;
+  if (dim > kHeadMaxDim || q_heads * dim > kMaxDim || k_heads * dim > kMaxDim) return OPT_ELIMIT;
+  return head_backward_parts(rows, q_heads + k_heads) * 2 * dim * (int64_t)sizeof(float);
+}
+
+int opt_head_norm_backward(const opt_head_norm_backward_args* a, void* stream) {
+  if (a == nullptr) return OPT_EINVAL;
+  PS_TRY(check_heads(*a));
+  const int64_t es = plain_size(a->dtype), ws = plain_size(a->weight_dtype);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  float* dq = a->q_heads > 0 ? a->d_dq_weight : nullptr;
+  float* dk = a->k_heads > 0 ? a->d_dk_weight : nullptr;
+  if (dq != nullptr) PS_TRY(check_matrix(dq, a->dim, 1, a->dim, 4));
+  if (dk != nullptr) PS_TRY(check_matrix(dk, a->dim, 1, a->dim, 4));
+  if (a->q_heads + a->k_heads == 0) return OPT_OK;
+  if (a->rows == 0) {      // the sums over no rows
+    if (dq != nullptr) PS_TRY(status_of(cudaMemsetAsync(dq, 0, (size_t)a->dim * sizeof(float), s)));
+    return dk == nullptr ? OPT_OK : status_of(cudaMemsetAsync(dk, 0, (size_t)a->dim * sizeof(float), s));
+  }
+  if (a->q_heads > 0 && a->k_heads > 0 && (a->d_q_scales != nullptr) != (a->d_k_scales != nullptr)) return OPT_EINVAL;
+  if (a->q_heads > 0) {
+    const int64_t cols = a->q_heads * a->dim;
+    PS_TRY(check_matrix(a->d_dq_out, a->dq_out_pitch, a->rows, cols, es));
+    if (a->d_q_scales != nullptr) PS_TRY(check_codes(a->d_q, a->q_pitch, a->d_q_scales, a->rows, cols));
+    else PS_TRY(check_matrix(a->d_q, a->q_pitch, a->rows, cols, es));
+    PS_TRY(check_matrix(a->d_q_weight, a->dim, 1, a->dim, ws));
+    PS_TRY(check_matrix(a->d_dq, a->dq_pitch, a->rows, cols, es));
+  }
+  if (a->k_heads > 0) {
+    const int64_t cols = a->k_heads * a->dim;
+    PS_TRY(check_matrix(a->d_dk_out, a->dk_out_pitch, a->rows, cols, es));
+    if (a->d_k_scales != nullptr) PS_TRY(check_codes(a->d_k, a->k_pitch, a->d_k_scales, a->rows, cols));
+    else PS_TRY(check_matrix(a->d_k, a->k_pitch, a->rows, cols, es));
+    PS_TRY(check_matrix(a->d_k_weight, a->dim, 1, a->dim, ws));
+    PS_TRY(check_matrix(a->d_dk, a->dk_pitch, a->rows, cols, es));
+  }
+  PS_TRY(check_turn(*a));
+  if (dq != nullptr || dk != nullptr) {
+    if (a->d_workspace == nullptr ||
+        a->workspace_bytes < opt_head_norm_backward_workspace(a->rows, a->q_heads, a->k_heads, a->dim)) return OPT_EINVAL;
+    if ((uintptr_t)a->d_workspace & 15u) return OPT_EALIGN;
+  }
+  opt_head_norm_backward_args b = *a;      // a side without heads has nothing
+  b.d_dq_weight = dq;
+  b.d_dk_weight = dk;
+  if (a->q_heads == 0) b.d_q_scales = nullptr;
+  if (a->k_heads == 0) b.d_k_scales = nullptr;
+  int sms = 0;
+  PS_TRY(sm_count_of(&sms));
+  return status_of(launch_head_norm_backward(b, sms, s));
 }
 
 int opt_matmul(const opt_matmul_args* a, void* stream) {

@@ -455,6 +455,102 @@ __host__ __device__ __forceinline__ int64_t scale_place(int64_t r, int64_t b, in
   return 512 * ((r >> 7) * panel + (b >> 2)) + 16 * (r & 31) + 4 * ((r >> 5) & 3) + (b & 3);
 }
 
+// ------------------------------------------------------------ kept matrices
+struct E4m3 {};                   // element type of a kept matrix, codes with scales
+
+// The scale that a byte stands for: 2^(byte - 127), NaN for 255.
+__device__ __forceinline__ float scale_of(uint32_t byte) {
+  return u2f(byte == 0u ? 0x00400000u : byte == 255u ? 0x7FC00000u : byte << 23);
+}
+// Eight codes of an 8-byte aligned place, the first `valid` of which exist; the others
+// read as 0.
+__device__ __forceinline__ uint2 load_codes8(const uint8_t* p, int valid) {
+  uint2 w = make_uint2(0u, 0u);
+  if (valid >= 8) {
+    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(w.x), "=r"(w.y) : "l"(p));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t b = j < valid ? (uint32_t)p[j] << (8 * (j & 3)) : 0u;
+      if (j < 4) w.x |= b;
+      else w.y |= b;
+    }
+  }
+  return w;
+}
+// The values that eight codes stand for.
+__device__ __forceinline__ void values8(uint2 w, float scale, float (&x)[8]) {
+  e4m3x2_dec(w.x & 0xFFFFu, x[0], x[1]);
+  e4m3x2_dec(w.x >> 16, x[2], x[3]);
+  e4m3x2_dec(w.y & 0xFFFFu, x[4], x[5]);
+  e4m3x2_dec(w.y >> 16, x[6], x[7]);
+  scaled8(x, scale, x);
+}
+// Eight values as codes with the scale of the 1 x 128 block that 16 lanes hold, by
+// whole warps; elements from `valid` on do not exist.
+__device__ __forceinline__ void put_codes8(void* codes, void* scales, int64_t pitch, int64_t panel, int64_t r, int64_t c,
+                                           int valid, const float (&x)[8]) {
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = j < valid ? x[j] : 0.0f;
+  bool odd;
+  const uint32_t byte = block_byte(v, odd);
+  if (valid <= 0) return;
+  store_codes8(static_cast<uint8_t*>(codes) + r * pitch + c, valid, codes8(v, inverse_scale(byte), odd));
+  if ((threadIdx.x & 15) == 0) static_cast<uint8_t*>(scales)[scale_place(r, c >> 7, panel)] = (uint8_t)byte;
+}
+
+// A row of a plain matrix (S its element type) or of a kept one (S E4m3), by chunks:
+// `ahead` asks for one, `values` makes it eight fp32 values.
+template <typename S, bool VEC>
+struct Source {
+  Row<S, VEC> row;
+  using Ask = Ahead<S, VEC>;
+  __device__ __forceinline__ Source(const void* base, const void*, int64_t pitch, int64_t rows, int64_t cols, int64_t r)
+      : row(base, pitch, rows, cols, r) {}
+  __device__ __forceinline__ Ask ahead(int64_t c, int valid) const { return row.ahead(c, valid); }
+  __device__ __forceinline__ void values(const Ask& a, int64_t c, int valid, float (&x)[8]) const {
+    unpack(row.chunk(a, c, valid), x);
+  }
+};
+struct KeptAsk {
+  uint2 codes;
+  uint32_t byte;
+};
+template <bool VEC>
+struct Source<E4m3, VEC> {
+  const uint8_t *codes, *scales;
+  using Ask = KeptAsk;
+  int64_t r, panel;
+  __device__ __forceinline__ Source(const void* base, const void* tiles, int64_t pitch, int64_t, int64_t cols, int64_t row)
+      : codes(static_cast<const uint8_t*>(base) + row * pitch), scales(static_cast<const uint8_t*>(tiles)), r(row),
+        panel((cols + 511) / 512) {}
+  __device__ __forceinline__ Ask ahead(int64_t c, int valid) const {
+    KeptAsk a = {};
+    if (valid > 0) {
+      a.codes = load_codes8(codes + c, valid);
+      a.byte = scales[scale_place(r, c >> 7, panel)];
+    }
+    return a;
+  }
+  __device__ __forceinline__ void values(const Ask& a, int64_t, int, float (&x)[8]) const {
+    values8(a.codes, scale_of(a.byte), x);
+  }
+};
+
+// Blocks of chunks by rows: a row's chunks (to whole 128-element blocks and whole warps)
+// in equal parts of at most a CTA's threads, and as many rows as fill it.
+struct ChunkGrid {
+  dim3 grid, block;
+  ChunkGrid(int64_t rows, int64_t cols, int threads) {
+    const int64_t slots = (cols + 255) / 256 * 32, parts = (slots + threads - 1) / threads;
+    const int64_t width = ((slots + parts - 1) / parts + 31) / 32 * 32, high = threads / width;
+    const int64_t groups = (rows + high - 1) / high;
+    block = dim3((unsigned)width, (unsigned)(high < rows ? high : rows));
+    grid = dim3((unsigned)((slots + width - 1) / width), (unsigned)(groups < 65535 ? groups : 65535));
+  }
+};
+
 // ---------------------------------------------------------------- reductions
 // Sum over a CTA of at most 32 warps, the same bits in every thread: lanes by a
 // butterfly, then the warps' sums in order.  `part` holds 33 floats; two
@@ -470,6 +566,15 @@ __device__ __forceinline__ float cta_sum(float v, float* part, int warps) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
+}
+
+// 1 / sqrt(v): rsqrtf, whose error of up to two units in the last place would move
+// a block's scale where its largest value lies that near to a power of two times
+// 448, and one Newton step (r += r (1 - v r^2) / 2), for positive finite v.
+__device__ __forceinline__ float reciprocal_root(float v) {
+  const float r = rsqrtf(v);
+  const float half_error = fmaf(-0.5f * v * r, r, 0.5f);
+  return r > 0.0f && r < 1e30f ? fmaf(r, half_error, r) : r;
 }
 
 }  // namespace psopt

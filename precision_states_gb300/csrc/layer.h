@@ -24,6 +24,11 @@ cudaError_t launch_rms_norm(const opt_rms_norm_args& a, const DropArgs& d, int s
 cudaError_t launch_rms_norm_backward(const opt_rms_norm_backward_args& a, const DropArgs& d, int sm_count,
                                      cudaStream_t s);
 cudaError_t launch_quantize(const opt_quantize_args& a, cudaStream_t s);
+cudaError_t launch_dequantize(const opt_dequantize_args& a, cudaStream_t s);
+cudaError_t launch_gated(const opt_gated_args& a, cudaStream_t s);
+cudaError_t launch_gated_backward(const opt_gated_backward_args& a, cudaStream_t s);
+cudaError_t launch_head_norm(const opt_head_norm_args& a, int sm_count, cudaStream_t s);
+cudaError_t launch_head_norm_backward(const opt_head_norm_backward_args& a, int sm_count, cudaStream_t s);
 cudaError_t launch_matmul(const opt_matmul_args& a, int sm_count, cudaStream_t s);
 bool matmul_waits(const opt_matmul_args& a);              // whether the product's kernel waits on anything
 cudaError_t matmul_form(const opt_matmul_args& a, int sm_count, int32_t* form);      // opt_matmul_form, of one that waits
@@ -37,6 +42,14 @@ constexpr int64_t kNormBackwardMaxCtas = 1024;
 // 512 rows and 2^21 elements.
 __host__ __device__ constexpr inline int64_t norm_backward_parts(int64_t rows, int64_t cols) {
   return rows <= 512 && rows * cols <= ((int64_t)1 << 21) ? 0 : rows < kNormBackwardMaxCtas ? rows : kNormBackwardMaxCtas;
+}
+
+// CTAs of the heads' backward pass, and so rows of its weight-gradient partial sums
+// (2 x dim each).
+constexpr int64_t kHeadBackwardMaxCtas = 1024;
+constexpr int64_t kHeadMaxDim = 1024;
+__host__ __device__ constexpr inline int64_t head_backward_parts(int64_t rows, int64_t heads) {
+  return rows * heads < kHeadBackwardMaxCtas ? rows * heads : kHeadBackwardMaxCtas;
 }
 
 }  // namespace psopt

@@ -35,15 +35,6 @@ namespace {
 constexpr int kWideThreads = 512;       // of the form that reads rows twice
 constexpr int kDweightCols = 32, kDweightParts = 32, kSlabCols = 16, kSlabFewRows = 8;
 
-// 1 / sqrt(v): rsqrtf, whose error of up to two units in the last place would move
-// a block's scale where its largest value lies that near to a power of two times
-// 448, and one Newton step (r += r (1 - v r^2) / 2), for positive finite v.
-__device__ __forceinline__ float reciprocal_root(float v) {
-  const float r = rsqrtf(v);
-  const float half_error = fmaf(-0.5f * v * r, r, 0.5f);
-  return r > 0.0f && r < 1e30f ? fmaf(r, half_error, r) : r;
-}
-
 // Chunk c (eight elements) of row r of h = residual + dropout(x).
 template <typename T, bool VEC>
 __device__ __forceinline__ void h_chunk(const opt_rms_norm_args& a, const DropArgs& d, int64_t r, int64_t c,
