@@ -189,7 +189,8 @@ __global__ void __launch_bounds__(kThreads, 2) head_norm_kernel(const __grid_con
       for (int j = 0; j < 8; ++j) y[j] = rstd * fmaf(v[j], c[j], l.e < rot ? p[j] * s[j] : 0.0f);
       if (on) store8<true>(static_cast<T*>(side.out) + r * side.out_pitch + col, 8, y);
       if (side.codes != nullptr)
-        put_codes8(side.codes, side.code_scales, side.codes_pitch, panel, r, col, on ? 8 : 0, v);
+        put_codes8(static_cast<uint8_t*>(side.codes) + r * side.codes_pitch + col, static_cast<uint8_t*>(side.code_scales),
+                   scale_place(r, col >> 7, panel), on ? 8 : 0, v);
     }
   }
 }

@@ -251,7 +251,9 @@ int opt_gated_backward(const opt_gated_backward_args* a, void* stream) {
   if (!dup && a->d_dgate == nullptr && a->d_dgate_codes == nullptr && a->d_dgate_codes_t == nullptr && a->d_y_codes_t == nullptr)
     return OPT_EINVAL;
   PS_TRY(check_tiles(rows, cols));
-  return status_of(launch_gated_backward(*a, static_cast<cudaStream_t>(stream)));
+  int sms = 0;
+  PS_TRY(sm_count_of(&sms));
+  return status_of(launch_gated_backward(*a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 int opt_head_norm(const opt_head_norm_args* a, void* stream) {

@@ -370,10 +370,10 @@ struct Edges {
 // ------------------------------------------------------------ block scales
 // Scale byte of a block from the bits of its largest finite magnitude: with
 // magnitude 1.f 2^E, E - 8 if 1.f <= 1.75 (448 = 1.75 2^8) else E - 7, never
-// below -127 (which also serves blocks of zeros and of subnormals).
+// below -127 (which also serves blocks of zeros and of subnormals).  What is added
+// carries into the exponent where the fraction is above 0.75.
 __device__ __forceinline__ uint32_t scale_byte(uint32_t top_bits) {
-  const int e = (int)(top_bits >> 23) - 8 + ((top_bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-  return (uint32_t)max(e, 0);
+  return (uint32_t)max((int)((top_bits + 0x1FFFFFu) >> 23) - 8, 0);
 }
 // 2^-e for a scale byte; scale_byte never exceeds 247, so this is normal.
 __device__ __forceinline__ float inverse_scale(uint32_t byte) { return u2f((254u - byte) << 23); }
@@ -386,6 +386,16 @@ __device__ __forceinline__ uint32_t magnitude(float x) { return f2u(x) & 0x7FFFF
 __device__ __forceinline__ uint32_t top8(const float (&x)[8]) {
   return max(max(max(magnitude(x[0]), magnitude(x[1])), max(magnitude(x[2]), magnitude(x[3]))),
              max(max(magnitude(x[4]), magnitude(x[5])), max(magnitude(x[6]), magnitude(x[7]))));
+}
+// The largest of three magnitudes in one instruction; a NaN stays one.
+__device__ __forceinline__ float largest3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// top8 by those (bits of an infinity or NaN are at least kInfBits).
+__device__ __forceinline__ uint32_t top8_of(const float (&x)[8]) {
+  return f2u(largest3(largest3(x[0], x[1], x[2]), largest3(x[3], x[4], x[5]), largest3(x[6], x[7], x[7])));
 }
 // The same of the finite elements.
 __device__ __forceinline__ uint32_t finite_top8(const float (&x)[8]) {
@@ -486,18 +496,27 @@ __device__ __forceinline__ void values8(uint2 w, float scale, float (&x)[8]) {
   e4m3x2_dec(w.y >> 16, x[6], x[7]);
   scaled8(x, scale, x);
 }
-// Eight values as codes with the scale of the 1 x 128 block that 16 lanes hold, by
-// whole warps; elements from `valid` on do not exist.
-__device__ __forceinline__ void put_codes8(void* codes, void* scales, int64_t pitch, int64_t panel, int64_t r, int64_t c,
-                                           int valid, const float (&x)[8]) {
-  float v[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = j < valid ? x[j] : 0.0f;
-  bool odd;
-  const uint32_t byte = block_byte(v, odd);
+// Codes of eight values with their block's scale byte, and the byte by the block's first
+// lane: to a row's chunk at `codes` and the place `at` of its scale.
+__device__ __forceinline__ void put_chunk(uint8_t* codes, uint8_t* scales, int64_t at, int valid, uint2 w, uint32_t byte) {
   if (valid <= 0) return;
-  store_codes8(static_cast<uint8_t*>(codes) + r * pitch + c, valid, codes8(v, inverse_scale(byte), odd));
-  if ((threadIdx.x & 15) == 0) static_cast<uint8_t*>(scales)[scale_place(r, c >> 7, panel)] = (uint8_t)byte;
+  store_codes8(codes, valid, w);
+  if ((threadIdx.x & 15) == 0) scales[at] = (uint8_t)byte;
+}
+// Eight values as codes with the scale of the 1 x 128 block that 16 lanes hold, by
+// whole warps; elements from `valid` on are 0.
+__device__ __forceinline__ void put_codes8(uint8_t* codes, uint8_t* scales, int64_t at, int valid, const float (&x)[8]) {
+  bool odd;
+  const uint32_t byte = block_byte(x, odd);
+  put_chunk(codes, scales, at, valid, codes8(x, inverse_scale(byte), odd), byte);
+}
+// The same where the block's largest magnitude `top` is known, and finite.
+__device__ __forceinline__ void put_finite8(uint8_t* codes, uint8_t* scales, int64_t at, int valid, const float (&x)[8],
+                                            uint32_t top) {
+  const uint32_t byte = scale_byte(top);
+  float v[8];
+  scaled8(x, inverse_scale(byte), v);
+  put_chunk(codes, scales, at, valid, codes8(v), byte);
 }
 
 // A row of a plain matrix (S its element type) or of a kept one (S E4m3), by chunks:

@@ -23,7 +23,9 @@ def activation(g, kind):
     silu, gelu_tanh: z in at most four roundings; exp(-|z|) is off by |z| times the
     error of its argument (5 roundings with the factor log2 e) and 4 units of 2^-24 of
     its own, and s and 1 - s by 4 more (sum, reciprocal, product); f by one more.  f' is
-    s + f (1 - s) z', with five more roundings in the second term.  gelu: the library's
+    s + f (1 - s) z', with five more roundings in the second term; 1 - s may be formed as
+    that, off by 2^-24.  s is 0 where it would be below 2^-128 in BF16,
+    which leaves f off by |g| 2^-128 and f' by 2^-128 (1 + |g| z').  gelu: the library's
     normal distribution function is off by at most 5 units in the last place."""
     with np.errstate(all="ignore"):
         if kind == "relu":
@@ -40,7 +42,9 @@ def activation(g, kind):
         f, second = g * s, g * s * n * dz
         second = np.where(s * n == 0, 0.0, second)
         off = np.minimum(5 * np.abs(z), 600) + 10
-        return f, s + second, E24 * off * np.abs(f) + TINY, E24 * (off * s + (2 * off + 6) * np.abs(second) + np.abs(s + second)) + TINY
+        far, far_slope = TINY * (1 + np.abs(g)), TINY * (1 + np.abs(g * dz))
+        return (f, s + second, E24 * off * np.abs(f) + far,
+                E24 * (off * s + np.minimum(np.abs(f * dz), 600) + (2 * off + 6) * np.abs(second) + np.abs(s + second)) + far_slope)
 
 
 def check_codes(codes, scales, want, d):
