@@ -3,6 +3,8 @@
 //
 // Mathematics: f(g) = g s(g), f' = s + g s (1 - s) z' where s is the logistic function of
 // z(g).
+#include <type_traits>
+
 #include "tile.cuh"
 
 namespace psopt {
@@ -13,16 +15,22 @@ constexpr float kTwoRootTwoOverPi = 1.5957691216057308f, kCubic = 0.044715f, kLo
 
 // exp(-a) for a >= 0 to fp32 (for fp32 elements).
 __device__ __forceinline__ float exp_minus(float a) { return expf(-a); }
-// 2^a: two units in the last place, besides the rounding of what is given as a.
+// 2^a and 1 / a to two units in the last place; results below 2^-126 are 0 (keeping them
+// takes nine more instructions per element).
 __device__ __forceinline__ float exp2_near(float a) {
   float r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(a));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
+  return r;
+}
+__device__ __forceinline__ float reciprocal_near(float a) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
   return r;
 }
 
 // f(g) and, if it is wanted (SLOPE), f'(g).  EXACT: for fp32 elements, to their last
 // places; else s = 1 / (1 + 2^(-z log2 e)), whose errors of a few 2^-24 are far below BF16's
-// and E4M3's steps (and which is 0 where it would be below 2^-128), two at a time.
+// and E4M3's steps (and which is 0 where it would be below 2^-126), two at a time.
 template <int KIND, bool EXACT, bool SLOPE>
 __device__ __forceinline__ void activation(float g, float& f, float& df) {
   if constexpr (KIND == OPT_ACT_RELU) {
@@ -68,7 +76,7 @@ __device__ __forceinline__ void activation8(const float (&g)[8], float (&f)[8], 
       float lo, hi;
       unpk(z, lo, hi);
       unpk(add2(pk(exp2_near(lo), exp2_near(hi)), one), lo, hi);
-      const f2_t s = pk(rcp_approx(lo), rcp_approx(hi)), fv = mul2(gv, s);
+      const f2_t s = pk(reciprocal_near(lo), reciprocal_near(hi)), fv = mul2(gv, s);
       unpk(fv, f[j], f[j + 1]);
       if constexpr (SLOPE) {
         f2_t n = fma2(s, pk(-1.0f, -1.0f), one);
@@ -101,48 +109,103 @@ __device__ __forceinline__ void tops16(uint32_t& a, uint32_t& b, float) {
   }
 }
 
-template <typename T, int KIND, bool VEC>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && VEC ? 5 : 4) gated_kernel(const __grid_constant__ opt_gated_args a) {
-  __shared__ __align__(16) Ragged<T, VEC, kThreads / 32> ragged;
-  T* buffer = ragged.chunk[VEC ? 0 : warp_of_block()];
+// What is written in 8 bits of a chunk of row r at column c: y, and the inputs that are kept.
+// By whole warps; elements from `valid` on are 0.
+template <typename T>
+__device__ __forceinline__ void put_forward(const opt_gated_args& a, int64_t at, int valid, uint8_t* codes, uint8_t* gcodes,
+                                            uint8_t* ucodes, const Raw<T>& graw, const Raw<T>& uraw, const float (&y)[8]) {
+  uint32_t top = 0, gtop = 0, utop = 0;
+  if (codes != nullptr) top = top16(top8_of(y));
+  if (gcodes != nullptr || ucodes != nullptr) {
+    gtop = top_of(magnitudes(graw, false));
+    utop = top_of(magnitudes(uraw, false));
+    tops16(gtop, utop, T());
+  }
+  uint8_t *scales = static_cast<uint8_t*>(a.d_scales), *gscales = static_cast<uint8_t*>(a.d_gate_scales),
+          *uscales = static_cast<uint8_t*>(a.d_up_scales);
+  const bool odd = __any_sync(0xFFFFFFFFu, max(max(top, gtop), utop) >= kInfBits);      // rare
+  const auto put = [&](uint8_t* p, uint8_t* tiles, const float (&x)[8], uint32_t t) {
+    if (odd) put_codes8(p, tiles, at, valid, x);
+    else put_finite8(p, tiles, at, valid, x, t);
+  };
+  if (codes != nullptr) put(codes, scales, y, top);
+  float x[8];
+  if (gcodes != nullptr) {
+    unpack(graw, x);
+    put(gcodes, gscales, x, gtop);
+  }
+  if (ucodes != nullptr) {
+    unpack(uraw, x);
+    put(ucodes, uscales, x, utop);
+  }
+}
+
+__device__ __forceinline__ uint8_t* row_of(void* codes, int64_t pitch, int64_t r, int64_t c) {
+  return codes == nullptr ? nullptr : static_cast<uint8_t*>(codes) + r * pitch + c;
+}
+
+// Whole chunks: a thread keeps to its column and goes down the rows by pointers, the next
+// row's loads under way.
+template <typename T, int KIND>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) gated_vec_kernel(const __grid_constant__ opt_gated_args a) {
   const int64_t c = 8 * ((int64_t)blockIdx.x * blockDim.x + threadIdx.x), panel = (a.cols + 511) / 512;
-  const int valid = (int)max(min(a.cols - c, (int64_t)8), (int64_t)0);
-  const bool has_up = a.d_up != nullptr;
+  const int64_t step = (int64_t)gridDim.y * blockDim.y, r0 = first_row();
+  const bool on = c < a.cols, has_up = a.d_up != nullptr;
+  const T *gate = static_cast<const T*>(a.d_gate) + r0 * a.gate_pitch + c, *up = static_cast<const T*>(a.d_up) + r0 * a.up_pitch + c;
+  T* y_out = static_cast<T*>(a.d_y) + r0 * a.y_pitch + c;
+  uint8_t *codes = row_of(a.d_codes, a.codes_pitch, r0, c), *gcodes = row_of(a.d_gate_codes, a.gate_codes_pitch, r0, c),
+          *ucodes = row_of(a.d_up_codes, a.up_codes_pitch, r0, c);
+  Raw<T> gnext = {}, unext = {};
+  if (on && r0 < a.rows) {
+    gnext = load_raw<true>(gate, 8);
+    if (has_up) unext = load_raw<true>(up, 8);
+  }
+  for (int64_t r = r0; r < a.rows; r += step) {
+    const Raw<T> graw = gnext, uraw = unext;
+    gate += step * a.gate_pitch;
+    up += step * a.up_pitch;
+    if (on && r + step < a.rows) {
+      gnext = load_raw<true>(gate, 8);
+      if (has_up) unext = load_raw<true>(up, 8);
+    }
+    float x[8], y[8], unused[8];
+    unpack(graw, x);
+    activation8<KIND, sizeof(T) == 4, false>(x, y, unused);
+    if (has_up) {
+      unpack(uraw, x);
+      times8(y, x);
+    }
+    if (a.d_y != nullptr) {
+      if (on) store8<true>(y_out, 8, y);
+      y_out += step * a.y_pitch;
+    }
+    put_forward<T>(a, scale_place(r, c >> 7, panel), on ? 8 : 0, codes, gcodes, ucodes, graw, uraw, y);
+    if (codes != nullptr) codes += step * a.codes_pitch;
+    if (gcodes != nullptr) gcodes += step * a.gate_codes_pitch;
+    if (ucodes != nullptr) ucodes += step * a.up_codes_pitch;
+  }
+}
+// Rows that begin anywhere.
+template <typename T, int KIND>
+__global__ void __launch_bounds__(kThreads, 4) gated_any_kernel(const __grid_constant__ opt_gated_args a) {
+  __shared__ __align__(16) Ragged<T, false, kThreads / 32> ragged;
+  T* buffer = ragged.chunk[warp_of_block()];
+  const int64_t c = 8 * ((int64_t)blockIdx.x * blockDim.x + threadIdx.x), panel = (a.cols + 511) / 512;
+  const int valid = (int)max(min(a.cols - c, (int64_t)8), (int64_t)0), up_valid = a.d_up != nullptr ? valid : 0;
   for (int64_t r = first_row(); r < a.rows; r += (int64_t)gridDim.y * blockDim.y) {
-    const Row<T, VEC> gate(a.d_gate, a.gate_pitch, a.rows, a.cols, r), up(a.d_up, a.up_pitch, a.rows, a.cols, r);
-    Ahead<T, VEC> ga = {}, ua = {};
-    if (!VEC || valid > 0) {
-      ga = gate.ahead(c, valid);
-      if (has_up) ua = up.ahead(c, valid);
+    const Row<T, false> gate(a.d_gate, a.gate_pitch, a.rows, a.cols, r), up(a.d_up, a.up_pitch, a.rows, a.cols, r);
+    const Ahead<T, false> ga = gate.ahead(c, valid), ua = up.ahead(c, up_valid);
+    const Raw<T> graw = gate.chunk(ga, c, valid), uraw = up.chunk(ua, c, up_valid);
+    float x[8], y[8], unused[8];
+    unpack(graw, x);
+    activation8<KIND, sizeof(T) == 4, false>(x, y, unused);
+    if (a.d_up != nullptr) {
+      unpack(uraw, x);
+      times8(y, x);
     }
-    const Raw<T> graw = gate.chunk(ga, c, valid), uraw = up.chunk(ua, c, has_up ? valid : 0);
-    float g[8], u[8], y[8], unused[8];
-    unpack(graw, g);
-    activation8<KIND, sizeof(T) == 4, false>(g, y, unused);
-    unpack(uraw, u);
-    if (has_up) times8(y, u);
-    if (a.d_y != nullptr && (!VEC || valid > 0)) store_at<VEC>(a.d_y, a.y_pitch, a.cols, r, c, valid, y, buffer);
-    if (a.d_codes == nullptr && a.d_gate_codes == nullptr && a.d_up_codes == nullptr) continue;
-    uint32_t top = 0, gtop = 0, utop = 0;
-    if (a.d_codes != nullptr) top = top16(top8_of(y));
-    if (a.d_gate_codes != nullptr || a.d_up_codes != nullptr) {
-      gtop = top_of(magnitudes(graw, false));
-      utop = top_of(magnitudes(uraw, false));
-      tops16(gtop, utop, T());
-    }
-    const int64_t at = scale_place(r, c >> 7, panel);
-    uint8_t *codes = static_cast<uint8_t*>(a.d_codes) + r * a.codes_pitch + c, *scales = static_cast<uint8_t*>(a.d_scales);
-    uint8_t *gcodes = static_cast<uint8_t*>(a.d_gate_codes) + r * a.gate_codes_pitch + c, *gscales = static_cast<uint8_t*>(a.d_gate_scales);
-    uint8_t *ucodes = static_cast<uint8_t*>(a.d_up_codes) + r * a.up_codes_pitch + c, *uscales = static_cast<uint8_t*>(a.d_up_scales);
-    if (__any_sync(0xFFFFFFFFu, max(max(top, gtop), utop) >= kInfBits)) {      // rare
-      if (a.d_codes != nullptr) put_codes8(codes, scales, at, valid, y);
-      if (a.d_gate_codes != nullptr) put_codes8(gcodes, gscales, at, valid, g);
-      if (a.d_up_codes != nullptr) put_codes8(ucodes, uscales, at, valid, u);
-    } else {
-      if (a.d_codes != nullptr) put_finite8(codes, scales, at, valid, y, top);
-      if (a.d_gate_codes != nullptr) put_finite8(gcodes, gscales, at, valid, g, gtop);
-      if (a.d_up_codes != nullptr) put_finite8(ucodes, uscales, at, valid, u, utop);
-    }
+    if (a.d_y != nullptr) store_at<false>(a.d_y, a.y_pitch, a.cols, r, c, valid, y, buffer);
+    put_forward<T>(a, scale_place(r, c >> 7, panel), valid, row_of(a.d_codes, a.codes_pitch, r, c),
+                   row_of(a.d_gate_codes, a.gate_codes_pitch, r, c), row_of(a.d_up_codes, a.up_codes_pitch, r, c), graw, uraw, y);
   }
 }
 
@@ -198,13 +261,21 @@ gated_backward_kernel(const __grid_constant__ opt_gated_backward_args a) {
 constexpr int kTurnThreads = 1024, kTile = 128 * 128;
 constexpr int kTurnBytes = 3 * kTile * (int)sizeof(float);
 
-// Place of the four columns from 4 quad on of a tile's row, in units of four values: turned so
-// that neither a row's chunks nor a column's rows meet in one bank.
-__device__ __forceinline__ int turned_place(int row, int quad) { return 32 * row + (quad ^ (row >> 2)); }
+// Offsets inside a tile: 32 bits for whole chunks (the host has seen that they hold them).
+template <bool VEC>
+using Offset = std::conditional_t<VEC, uint32_t, int64_t>;
 
-// A tile's values at `v` by columns: four columns of 128 rows to a warp.
-__device__ __forceinline__ void put_columns(const float4* v, uint8_t* codes, uint8_t* scales, int64_t pitch, int64_t panel,
-                                            int64_t r0, int64_t c0, int rows, int cols) {
+// Place of columns 4 quad ... 4 quad + 3 of a tile's row, in units of four values: a chunk's two
+// places are 16 apart, and rows turned, so that neither the chunks of a row nor the rows of
+// a column meet in a bank.
+__device__ __forceinline__ int turned_place(int row, int quad) {
+  return 32 * row + (((quad >> 1) | (quad & 1) << 4) ^ (row >> 2));
+}
+
+// A tile's values at `v` by columns, four columns of 128 rows to a warp: codes to `codes` (the
+// tile's first column's), scale bytes to `scales` (the tile's).
+template <bool VEC>
+__device__ __forceinline__ void put_columns(const float4* v, uint8_t* codes, uint8_t* scales, int64_t pitch, int rows, int cols) {
   const int lane = threadIdx.x & 31, quad = threadIdx.x >> 5;
   float x[4][4];                    // [row][column]
 #pragma unroll
@@ -241,21 +312,22 @@ __device__ __forceinline__ void put_columns(const float4* v, uint8_t* codes, uin
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j) word[j] = e4m3x2_rn(x[0][j], x[1][j]) | e4m3x2_rn(x[2][j], x[3][j]) << 16;
-  uint8_t* p = codes + (c0 + 4 * quad) * pitch + r0 + 4 * lane;
-  const int left = rows - 4 * lane;
+  const Offset<VEC> step = (Offset<VEC>)pitch;
+  Offset<VEC> at = 4 * quad * step + 4 * lane;
+  const int left = rows - 4 * lane, wide = cols - 4 * quad;
 #pragma unroll
-  for (int j = 0; j < 4; ++j, p += pitch) {
-    if (4 * quad + j >= cols) break;
-    if (left >= 4) {
-      st_cs_u1(p, word[j]);
-    } else {
+  for (int j = 0; j < 4; ++j, at += step) {
+    if (j < wide && left >= 4) {
+      st_cs_u1(codes + at, word[j]);
+    } else if (j < wide) {
 #pragma unroll
       for (int i = 0; i < 3; ++i)
-        if (i < left) p[i] = (uint8_t)(word[j] >> (8 * i));
+        if (i < left) codes[at + i] = (uint8_t)(word[j] >> (8 * i));
     }
   }
-  if (lane < 4 && 4 * quad + lane < cols)
-    scales[scale_place(c0 + 4 * quad + lane, r0 >> 7, panel)] = (uint8_t)(lane == 0 ? byte[0] : lane == 1 ? byte[1] : lane == 2 ? byte[2] : byte[3]);
+  if (lane < 4 && lane < wide)
+    scales[16 * ((4 * quad + lane) & 31) + 4 * (quad >> 3)] =
+        (uint8_t)(lane == 0 ? byte[0] : lane == 1 ? byte[1] : lane == 2 ? byte[2] : byte[3]);
 }
 
 template <typename T, typename S, bool VEC>
@@ -264,60 +336,83 @@ struct Inputs {
   typename Source<S, VEC>::Ask gate, up;
 };
 
+// CTAs take tiles gridDim.x apart, `step_rows` and `step_cols` in rows and columns of tiles.
 template <typename T, typename S, int KIND, bool VEC>
 __global__ void __launch_bounds__(kTurnThreads, 1) gated_backward_tile_kernel(
-    const __grid_constant__ opt_gated_backward_args a, int64_t col_tiles, int64_t tiles) {
+    const __grid_constant__ opt_gated_backward_args a, int row_tiles, int col_tiles, int step_rows, int step_cols) {
   extern __shared__ __align__(16) float4 held[];       // dgate, dup, y
+  using Off = Offset<VEC>;
+  constexpr bool KEPT = sizeof(S) == 1;
   // plain fp32 inputs of two rows leave no registers for the next tile's
-  constexpr bool AHEAD = sizeof(T) == 2 || sizeof(typename Source<S, VEC>::Ask) < 32;
+  constexpr bool AHEAD = sizeof(T) == 2 || KEPT;
   const int q = threadIdx.x & 15, row = 2 * (threadIdx.x >> 4);
   const int64_t panel = (a.cols + 511) / 512, panel_t = (a.rows + 511) / 512;
+  const int scale_row = 16 * (row & 31) + 4 * (row >> 5);      // row + 1: 16 more
   const bool has_up = a.d_up != nullptr;
-  const auto valid_of = [&](int64_t r, int64_t c) { return r < a.rows ? (int)max(min(a.cols - c, (int64_t)8), (int64_t)0) : 0; };
-  const auto load = [&](int64_t tile, int i) {
+  const auto rows_of = [&](int tr) { return (int)min(a.rows - 128 * (int64_t)tr, (int64_t)128); };
+  const auto cols_of = [&](int tc) { return (int)min(a.cols - 128 * (int64_t)tc, (int64_t)128); };
+  const auto tile_of = [&](int64_t pitch, int tr, int tc) { return 128 * ((int64_t)tr * pitch + tc); };
+  const auto place_of = [&](int64_t p, int tr, int tc) { return 512 * (tr * p + (tc >> 2)) + (tc & 3); };
+  const auto source = [&](const void* base, const void* tiles, int64_t pitch, int tr, int tc, int i, int valid) {
+    const Off at = (Off)(row + i) * (Off)pitch + 8 * q;
+    typename Source<S, VEC>::Ask ask = {};
+    if constexpr (KEPT) {
+      ask.codes = load_codes8(static_cast<const uint8_t*>(base) + tile_of(pitch, tr, tc) + at, valid);
+      ask.byte = (static_cast<const uint8_t*>(tiles) + place_of(panel, tr, tc))[scale_row + 16 * i];
+    } else if constexpr (VEC) {
+      const Raw<T> r = load_raw<true>(static_cast<const T*>(base) + tile_of(pitch, tr, tc) + at, 8);
+#pragma unroll
+      for (int k = 0; k < Raw<T>::kWords; ++k) ask.w[k] = r.w[k];
+    } else {
+      ask = Source<S, VEC>(base, tiles, pitch, a.rows, a.cols, 128 * (int64_t)tr + row + i).ahead(128 * (int64_t)tc + 8 * q, valid);
+    }
+    return ask;
+  };
+  const auto load = [&](int tr, int tc, int i) {
     Inputs<T, S, VEC> in = {};
-    const int64_t r = 128 * (tile / col_tiles) + row + i, c = 128 * (tile % col_tiles) + 8 * q;
-    const int valid = valid_of(r, c);
+    const int valid = row + i < rows_of(tr) ? max(min(cols_of(tc) - 8 * q, 8), 0) : 0;
     if (valid > 0) {
-      in.dy = Source<T, VEC>(a.d_dy, nullptr, a.dy_pitch, a.rows, a.cols, r).ahead(c, valid);
-      in.gate = Source<S, VEC>(a.d_gate, a.d_gate_scales, a.gate_pitch, a.rows, a.cols, r).ahead(c, valid);
-      if (has_up) in.up = Source<S, VEC>(a.d_up, a.d_up_scales, a.up_pitch, a.rows, a.cols, r).ahead(c, valid);
+      if constexpr (VEC) {
+        const Raw<T> r = load_raw<true>(static_cast<const T*>(a.d_dy) + tile_of(a.dy_pitch, tr, tc) +
+                                            ((Off)(row + i) * (Off)a.dy_pitch + 8 * q), 8);
+#pragma unroll
+        for (int k = 0; k < Raw<T>::kWords; ++k) in.dy.w[k] = r.w[k];
+      } else {
+        in.dy = Row<T, VEC>(a.d_dy, a.dy_pitch, a.rows, a.cols, 128 * (int64_t)tr + row + i).ahead(128 * (int64_t)tc + 8 * q, valid);
+      }
+      in.gate = source(a.d_gate, a.d_gate_scales, a.gate_pitch, tr, tc, i, valid);
+      if (has_up) in.up = source(a.d_up, a.d_up_scales, a.up_pitch, tr, tc, i, valid);
     }
     return in;
   };
+  int tr = (int)blockIdx.x / col_tiles, tc = (int)blockIdx.x % col_tiles;
   Inputs<T, S, VEC> in[2];
   if (AHEAD) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) in[i] = load(blockIdx.x, i);
+    for (int i = 0; i < 2; ++i) in[i] = load(tr, tc, i);
   }
-  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int64_t r0 = 128 * (tile / col_tiles), c0 = 128 * (tile % col_tiles), c = c0 + 8 * q;
+  while (tr < row_tiles) {
+    const int rows = rows_of(tr), cols = cols_of(tc);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      if (!AHEAD) in[i] = load(tile, i);
-      const int64_t r = r0 + row + i;
-      const int valid = valid_of(r, c);
+      if (!AHEAD) in[i] = load(tr, tc, i);
+      const int valid = row + i < rows ? max(min(cols - 8 * q, 8), 0) : 0;
+      const int64_t r = 128 * (int64_t)tr + row + i, c = 128 * (int64_t)tc + 8 * q;      // only of rows that begin anywhere
       float d[8], g[8], u[8], f[8], df[8];
       Source<S, VEC>(a.d_gate, a.d_gate_scales, a.gate_pitch, a.rows, a.cols, r).values(in[i].gate, c, valid, g);
       activation8<KIND, sizeof(T) == 4, true>(g, f, df);
       Source<T, VEC>(a.d_dy, nullptr, a.dy_pitch, a.rows, a.cols, r).values(in[i].dy, c, valid, d);
-      if (has_up) {
-        Source<S, VEC>(a.d_up, a.d_up_scales, a.up_pitch, a.rows, a.cols, r).values(in[i].up, c, valid, u);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) u[j] = 1.0f;
-      }
       times8(df, d);
       times8(d, f);                 // dup
-      times8(f, u);                 // y
-      if (has_up) times8(df, u);    // dgate
-      // to shared memory; half of a row's lanes store their second four first
+      if (has_up) {
+        Source<S, VEC>(a.d_up, a.d_up_scales, a.up_pitch, a.rows, a.cols, r).values(in[i].up, c, valid, u);
+        times8(f, u);               // y
+        times8(df, u);              // dgate
+      }
       const auto leave = [&](int m, const float (&x)[8]) {
         float4* v = held + m * (kTile / 4);
-        const float4 lo = make_float4(x[0], x[1], x[2], x[3]), hi = make_float4(x[4], x[5], x[6], x[7]);
-        const bool other = (q & 4) != 0;
-        v[turned_place(row + i, 2 * q + (other ? 1 : 0))] = other ? hi : lo;
-        v[turned_place(row + i, 2 * q + (other ? 0 : 1))] = other ? lo : hi;
+        v[turned_place(row + i, 2 * q)] = make_float4(x[0], x[1], x[2], x[3]);
+        v[turned_place(row + i, 2 * q + 1)] = make_float4(x[4], x[5], x[6], x[7]);
       };
       if (a.d_dgate_codes_t != nullptr) leave(0, df);
       if (a.d_dup_codes_t != nullptr) leave(1, d);
@@ -325,38 +420,45 @@ __global__ void __launch_bounds__(kTurnThreads, 1) gated_backward_tile_kernel(
       if (a.d_dgate_codes != nullptr || a.d_dup_codes != nullptr) {
         uint32_t gtop = top8_of(df), utop = top8_of(d);
         tops16(gtop, utop, 0.0f);
-        const int64_t at = scale_place(r, c >> 7, panel);
-        uint8_t *gcodes = static_cast<uint8_t*>(a.d_dgate_codes) + r * a.dgate_codes_pitch + c, *gscales = static_cast<uint8_t*>(a.d_dgate_scales);
-        uint8_t *ucodes = static_cast<uint8_t*>(a.d_dup_codes) + r * a.dup_codes_pitch + c, *uscales = static_cast<uint8_t*>(a.d_dup_scales);
-        if (__any_sync(0xFFFFFFFFu, max(gtop, utop) >= kInfBits)) {      // rare
-          if (a.d_dgate_codes != nullptr) put_codes8(gcodes, gscales, at, valid, df);
-          if (a.d_dup_codes != nullptr) put_codes8(ucodes, uscales, at, valid, d);
-        } else {
-          if (a.d_dgate_codes != nullptr) put_finite8(gcodes, gscales, at, valid, df, gtop);
-          if (a.d_dup_codes != nullptr) put_finite8(ucodes, uscales, at, valid, d, utop);
-        }
+        const bool odd = __any_sync(0xFFFFFFFFu, max(gtop, utop) >= kInfBits);      // rare
+        const auto put = [&](void* codes, void* scales, int64_t pitch, const float (&x)[8], uint32_t top) {
+          uint8_t* p = static_cast<uint8_t*>(codes) + tile_of(pitch, tr, tc) + ((Off)(row + i) * (Off)pitch + 8 * q);
+          uint8_t* tiles = static_cast<uint8_t*>(scales) + place_of(panel, tr, tc);
+          if (odd) put_codes8(p, tiles, scale_row + 16 * i, valid, x);
+          else put_finite8(p, tiles, scale_row + 16 * i, valid, x, top);
+        };
+        if (a.d_dgate_codes != nullptr) put(a.d_dgate_codes, a.d_dgate_scales, a.dgate_codes_pitch, df, gtop);
+        if (a.d_dup_codes != nullptr) put(a.d_dup_codes, a.d_dup_scales, a.dup_codes_pitch, d, utop);
       }
       __syncwarp();                 // an output may lie in an input's place, of which lanes read their neighbours' words
       if (valid > 0) {
-        if (a.d_dgate != nullptr) store8<VEC>(static_cast<T*>(a.d_dgate) + r * a.dgate_pitch + c, valid, df);
-        if (a.d_dup != nullptr) store8<VEC>(static_cast<T*>(a.d_dup) + r * a.dup_pitch + c, valid, d);
+        const auto store = [&](void* out, int64_t pitch, const float (&x)[8]) {
+          store8<VEC>(static_cast<T*>(out) + tile_of(pitch, tr, tc) + ((Off)(row + i) * (Off)pitch + 8 * q), valid, x);
+        };
+        if (a.d_dgate != nullptr) store(a.d_dgate, a.dgate_pitch, df);
+        if (a.d_dup != nullptr) store(a.d_dup, a.dup_pitch, d);
       }
     }
     __syncthreads();
-    if (AHEAD && tile + gridDim.x < tiles) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) in[i] = load(tile + gridDim.x, i);
+    const int at_row = tr, at_col = tc;
+    tr += step_rows;
+    tc += step_cols;
+    if (tc >= col_tiles) {
+      tc -= col_tiles;
+      ++tr;
     }
-    const int rows = (int)min(a.rows - r0, (int64_t)128), cols = (int)min(a.cols - c0, (int64_t)128);
-    if (a.d_dgate_codes_t != nullptr)
-      put_columns(held, static_cast<uint8_t*>(a.d_dgate_codes_t), static_cast<uint8_t*>(a.d_dgate_scales_t), a.dgate_codes_t_pitch,
-                  panel_t, r0, c0, rows, cols);
-    if (a.d_dup_codes_t != nullptr)
-      put_columns(held + kTile / 4, static_cast<uint8_t*>(a.d_dup_codes_t), static_cast<uint8_t*>(a.d_dup_scales_t), a.dup_codes_t_pitch,
-                  panel_t, r0, c0, rows, cols);
-    if (a.d_y_codes_t != nullptr)
-      put_columns(held + kTile / 2, static_cast<uint8_t*>(a.d_y_codes_t), static_cast<uint8_t*>(a.d_y_scales_t), a.y_codes_t_pitch,
-                  panel_t, r0, c0, rows, cols);
+    if (AHEAD && tr < row_tiles) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) in[i] = load(tr, tc, i);
+    }
+    const auto turn = [&](int m, void* codes, void* scales, int64_t pitch) {
+      if (codes != nullptr)
+        put_columns<VEC>(held + m * (kTile / 4), static_cast<uint8_t*>(codes) + tile_of(pitch, at_col, at_row),
+                         static_cast<uint8_t*>(scales) + place_of(panel_t, at_col, at_row), pitch, rows, cols);
+    };
+    turn(0, a.d_dgate_codes_t, a.d_dgate_scales_t, a.dgate_codes_t_pitch);
+    turn(1, a.d_dup_codes_t, a.d_dup_scales_t, a.dup_codes_t_pitch);
+    turn(2, a.d_y_codes_t, a.d_y_scales_t, a.y_codes_t_pitch);
     __syncthreads();
   }
 }
@@ -368,26 +470,35 @@ struct VecRule {
   void see(const void* p, int64_t pitch) {
     ok = ok && (p == nullptr || (((uintptr_t)p & 15u) == 0 && (rows == 1 || pitch * es % 16 == 0)));
   }
+  // and, of any matrix, 128 rows in 32-bit offsets
+  void in_tile(const void* p, int64_t pitch, int64_t size) {
+    ok = ok && (p == nullptr || pitch <= INT64_C(0x7FFFFFFF) / (128 * size));
+  }
 };
 
 template <typename T, int KIND>
-cudaError_t forward_kind(const opt_gated_args& a, cudaStream_t s) {
+cudaError_t forward_kind(const opt_gated_args& a, int sm_count, cudaStream_t s) {
   VecRule v{a.rows, sizeof(T), a.cols % 8 == 0};
   v.see(a.d_gate, a.gate_pitch);
   v.see(a.d_up, a.up_pitch);
   v.see(a.d_y, a.y_pitch);
-  const ChunkGrid g(a.rows, a.cols, kThreads);
-  if (v.ok) gated_kernel<T, KIND, true><<<g.grid, g.block, 0, s>>>(a);
-  else gated_kernel<T, KIND, false><<<g.grid, g.block, 0, s>>>(a);
+  ChunkGrid g(a.rows, a.cols, kThreads);
+  if (v.ok) {
+    static OccupancyCache cache;
+    g.limit((int64_t)sm_count * cached_occupancy(gated_vec_kernel<T, KIND>, cache, kThreads, 0));
+    gated_vec_kernel<T, KIND><<<g.grid, g.block, 0, s>>>(a);
+  } else {
+    gated_any_kernel<T, KIND><<<g.grid, g.block, 0, s>>>(a);
+  }
   return cudaGetLastError();
 }
 template <typename T>
-cudaError_t forward(const opt_gated_args& a, cudaStream_t s) {
+cudaError_t forward(const opt_gated_args& a, int sm_count, cudaStream_t s) {
   switch (a.activation) {
-    case OPT_ACT_SILU: return forward_kind<T, OPT_ACT_SILU>(a, s);
-    case OPT_ACT_GELU_TANH: return forward_kind<T, OPT_ACT_GELU_TANH>(a, s);
-    case OPT_ACT_GELU: return forward_kind<T, OPT_ACT_GELU>(a, s);
-    default: return forward_kind<T, OPT_ACT_RELU>(a, s);
+    case OPT_ACT_SILU: return forward_kind<T, OPT_ACT_SILU>(a, sm_count, s);
+    case OPT_ACT_GELU_TANH: return forward_kind<T, OPT_ACT_GELU_TANH>(a, sm_count, s);
+    case OPT_ACT_GELU: return forward_kind<T, OPT_ACT_GELU>(a, sm_count, s);
+    default: return forward_kind<T, OPT_ACT_RELU>(a, sm_count, s);
   }
 }
 
@@ -399,9 +510,11 @@ cudaError_t backward_vec(const opt_gated_backward_args& a, int sm_count, cudaStr
   } else {
     static OccupancyCache cache;
     const auto kernel = gated_backward_tile_kernel<T, S, KIND, VEC>;
-    const int64_t col_tiles = (a.cols + 127) / 128, tiles = (a.rows + 127) / 128 * col_tiles;
+    const int row_tiles = (int)((a.rows + 127) / 128), col_tiles = (int)((a.cols + 127) / 128);
+    const int64_t tiles = (int64_t)row_tiles * col_tiles;
     const int64_t most = (int64_t)sm_count * cached_occupancy(kernel, cache, kTurnThreads, kTurnBytes);
-    kernel<<<(unsigned)(tiles < most ? tiles : most), kTurnThreads, kTurnBytes, s>>>(a, col_tiles, tiles);
+    const int grid = (int)(tiles < most ? tiles : most);
+    kernel<<<grid, kTurnThreads, kTurnBytes, s>>>(a, row_tiles, col_tiles, grid / col_tiles, grid % col_tiles);
   }
   return cudaGetLastError();
 }
@@ -415,6 +528,16 @@ cudaError_t backward_kind(const opt_gated_backward_args& a, int sm_count, cudaSt
   v.see(kept ? nullptr : a.d_up, a.up_pitch);
   v.see(a.d_dgate, a.dgate_pitch);
   v.see(a.d_dup, a.dup_pitch);
+  v.in_tile(a.d_dy, a.dy_pitch, sizeof(T));
+  v.in_tile(a.d_gate, a.gate_pitch, sizeof(T));
+  v.in_tile(a.d_up, a.up_pitch, sizeof(T));
+  v.in_tile(a.d_dgate, a.dgate_pitch, sizeof(T));
+  v.in_tile(a.d_dup, a.dup_pitch, sizeof(T));
+  v.in_tile(a.d_dgate_codes, a.dgate_codes_pitch, 1);
+  v.in_tile(a.d_dgate_codes_t, a.dgate_codes_t_pitch, 1);
+  v.in_tile(a.d_dup_codes, a.dup_codes_pitch, 1);
+  v.in_tile(a.d_dup_codes_t, a.dup_codes_t_pitch, 1);
+  v.in_tile(a.d_y_codes_t, a.y_codes_t_pitch, 1);
   if (kept) return v.ok ? backward_vec<T, E4m3, KIND, true>(a, sm_count, s) : backward_vec<T, E4m3, KIND, false>(a, sm_count, s);
   return v.ok ? backward_vec<T, T, KIND, true>(a, sm_count, s) : backward_vec<T, T, KIND, false>(a, sm_count, s);
 }
@@ -430,8 +553,8 @@ cudaError_t backward(const opt_gated_backward_args& a, int sm_count, cudaStream_
 
 }  // namespace
 
-cudaError_t launch_gated(const opt_gated_args& a, cudaStream_t s) {
-  return a.dtype == OPT_F32 ? forward<float>(a, s) : forward<Bf16>(a, s);
+cudaError_t launch_gated(const opt_gated_args& a, int sm_count, cudaStream_t s) {
+  return a.dtype == OPT_F32 ? forward<float>(a, sm_count, s) : forward<Bf16>(a, sm_count, s);
 }
 
 cudaError_t launch_gated_backward(const opt_gated_backward_args& a, int sm_count, cudaStream_t s) {

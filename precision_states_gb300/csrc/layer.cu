@@ -221,7 +221,9 @@ int opt_gated(const opt_gated_args* a, void* stream) {
   PS_TRY(check_kept(a->d_up_codes, a->up_codes_pitch, a->d_up_scales, a->rows, a->cols));
   if (a->d_up == nullptr && a->d_up_codes != nullptr) return OPT_EINVAL;
   if (a->d_y == nullptr && a->d_codes == nullptr && a->d_gate_codes == nullptr && a->d_up_codes == nullptr) return OPT_EINVAL;
-  return status_of(launch_gated(*a, static_cast<cudaStream_t>(stream)));
+  int sms = 0;
+  PS_TRY(sm_count_of(&sms));
+  return status_of(launch_gated(*a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 int opt_gated_backward(const opt_gated_backward_args* a, void* stream) {

@@ -568,6 +568,11 @@ struct ChunkGrid {
     block = dim3((unsigned)width, (unsigned)(high < rows ? high : rows));
     grid = dim3((unsigned)((slots + width - 1) / width), (unsigned)(groups < 65535 ? groups : 65535));
   }
+  // At most about `ctas` of them, in equal shares of rows.
+  void limit(int64_t ctas) {
+    const int64_t most = ctas / grid.x;
+    if (grid.y > most) grid.y = (unsigned)(most < 1 ? 1 : most);
+  }
 };
 
 // ---------------------------------------------------------------- reductions
