@@ -145,44 +145,68 @@ __device__ __forceinline__ uint8_t* row_of(void* codes, int64_t pitch, int64_t r
 }
 
 // Whole chunks: a thread keeps to its column and goes down the rows by pointers, the next
-// row's loads under way.
-template <typename T, int KIND>
+// row's loads under way.  KEEP: every input is kept; else none is.
+template <typename T, int KIND, bool UP, bool KEEP>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) gated_vec_kernel(const __grid_constant__ opt_gated_args a) {
-  const int64_t c = 8 * ((int64_t)blockIdx.x * blockDim.x + threadIdx.x), panel = (a.cols + 511) / 512;
-  const int64_t step = (int64_t)gridDim.y * blockDim.y, r0 = first_row();
-  const bool on = c < a.cols, has_up = a.d_up != nullptr;
-  const T *gate = static_cast<const T*>(a.d_gate) + r0 * a.gate_pitch + c, *up = static_cast<const T*>(a.d_up) + r0 * a.up_pitch + c;
-  T* y_out = static_cast<T*>(a.d_y) + r0 * a.y_pitch + c;
-  uint8_t *codes = row_of(a.d_codes, a.codes_pitch, r0, c), *gcodes = row_of(a.d_gate_codes, a.gate_codes_pitch, r0, c),
-          *ucodes = row_of(a.d_up_codes, a.up_codes_pitch, r0, c);
-  Raw<T> gnext = {}, unext = {};
-  if (on && r0 < a.rows) {
-    gnext = load_raw<true>(gate, 8);
-    if (has_up) unext = load_raw<true>(up, 8);
-  }
-  for (int64_t r = r0; r < a.rows; r += step) {
+  const uint32_t c = 8 * (blockIdx.x * blockDim.x + threadIdx.x), rows = (uint32_t)a.rows;
+  const uint32_t step = gridDim.y * blockDim.y, panel = 512 * (uint32_t)((a.cols + 511) / 512);
+  const uint32_t place = 512 * (c >> 9) + ((c >> 7) & 3);
+  const bool on = c < (uint32_t)a.cols, first = on && (threadIdx.x & 15) == 0, want_y = a.d_y != nullptr, want_codes = a.d_codes != nullptr;
+  uint32_t r = (uint32_t)first_row();
+  const auto start = [&](auto* base, int64_t pitch) { return base + (r * pitch + c); };
+  const T *gate = start(static_cast<const T*>(a.d_gate), a.gate_pitch), *up = start(static_cast<const T*>(a.d_up), a.up_pitch);
+  T* y_out = start(static_cast<T*>(a.d_y), a.y_pitch);
+  uint8_t *codes = start(static_cast<uint8_t*>(a.d_codes), a.codes_pitch), *gcodes = start(static_cast<uint8_t*>(a.d_gate_codes), a.gate_codes_pitch),
+          *ucodes = start(static_cast<uint8_t*>(a.d_up_codes), a.up_codes_pitch);
+  const int64_t gate_step = step * a.gate_pitch, up_step = step * a.up_pitch, y_step = step * a.y_pitch, codes_step = step * a.codes_pitch,
+                gcodes_step = step * a.gate_codes_pitch, ucodes_step = step * a.up_codes_pitch;
+  Raw<T> gnext = load_if(gate, on && r < rows), unext = {};
+  if (UP) unext = load_if(up, on && r < rows);
+  for (; r < rows; r += step) {
     const Raw<T> graw = gnext, uraw = unext;
-    gate += step * a.gate_pitch;
-    up += step * a.up_pitch;
-    if (on && r + step < a.rows) {
-      gnext = load_raw<true>(gate, 8);
-      if (has_up) unext = load_raw<true>(up, 8);
+    gate += gate_step;
+    gnext = load_if(gate, on && r + step < rows);
+    if (UP) {
+      up += up_step;
+      unext = load_if(up, on && r + step < rows);
     }
-    float x[8], y[8], unused[8];
-    unpack(graw, x);
-    activation8<KIND, sizeof(T) == 4, false>(x, y, unused);
-    if (has_up) {
-      unpack(uraw, x);
-      times8(y, x);
+    float g[8], u[8], y[8], unused[8];
+    unpack(graw, g);
+    activation8<KIND, sizeof(T) == 4, false>(g, y, unused);
+    if (UP) {
+      unpack(uraw, u);
+      times8(y, u);
     }
-    if (a.d_y != nullptr) {
-      if (on) store8<true>(y_out, 8, y);
-      y_out += step * a.y_pitch;
+    if (want_y) {
+      store8_if(y_out, y, on);
+      y_out += y_step;
     }
-    put_forward<T>(a, scale_place(r, c >> 7, panel), on ? 8 : 0, codes, gcodes, ucodes, graw, uraw, y);
-    if (codes != nullptr) codes += step * a.codes_pitch;
-    if (gcodes != nullptr) gcodes += step * a.gate_codes_pitch;
-    if (ucodes != nullptr) ucodes += step * a.up_codes_pitch;
+    if (!KEEP && !want_codes) continue;
+    uint32_t top = want_codes ? top16(top8_of(y)) : 0, gtop = 0, utop = 0;
+    if (KEEP) {
+      gtop = top_of(magnitudes(graw, false));
+      if (UP) {
+        utop = top_of(magnitudes(uraw, false));
+        tops16(gtop, utop, T());
+      } else {
+        gtop = top16(gtop);
+      }
+    }
+    const uint64_t at = (uint64_t)(r >> 7) * panel + (place + 16 * (r & 31) + ((r >> 3) & 12));
+    uint8_t *scales = static_cast<uint8_t*>(a.d_scales) + at, *gscales = static_cast<uint8_t*>(a.d_gate_scales) + at,
+            *uscales = static_cast<uint8_t*>(a.d_up_scales) + at;
+    if (__any_sync(0xFFFFFFFFu, max(max(top, gtop), utop) >= kInfBits)) {      // rare
+      if (want_codes) put_codes8(codes, scales, 0, on ? 8 : 0, y);
+      if (KEEP) put_codes8(gcodes, gscales, 0, on ? 8 : 0, g);
+      if (KEEP && UP) put_codes8(ucodes, uscales, 0, on ? 8 : 0, u);
+    } else {
+      if (want_codes) put_finite_if(codes, scales, y, top, on, first);
+      if (KEEP) put_finite_if(gcodes, gscales, g, gtop, on, first);
+      if (KEEP && UP) put_finite_if(ucodes, uscales, u, utop, on, first);
+    }
+    codes += codes_step;
+    gcodes += gcodes_step;
+    ucodes += ucodes_step;
   }
 }
 // Rows that begin anywhere.
@@ -315,6 +339,13 @@ __device__ __forceinline__ void put_columns(const float4* v, uint8_t* codes, uin
   const Offset<VEC> step = (Offset<VEC>)pitch;
   Offset<VEC> at = 4 * quad * step + 4 * lane;
   const int left = rows - 4 * lane, wide = cols - 4 * quad;
+  if (rows == 128 && wide >= 4) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j, at += step) st_cs_u1(codes + at, word[j]);
+    store_byte_if(scales + (16 * ((4 * quad + lane) & 31) + 4 * (quad >> 3)),
+                  lane < 2 ? lane == 0 ? byte[0] : byte[1] : lane == 2 ? byte[2] : byte[3], lane < 4);
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < 4; ++j, at += step) {
     if (j < wide && left >= 4) {
@@ -335,6 +366,106 @@ struct Inputs {
   Ahead<T, VEC> dy;
   typename Source<S, VEC>::Ask gate, up;
 };
+
+// The whole backward pass of a training step in BF16 from kept inputs: all five 8-bit operands
+// and nothing plain.  The same work as gated_backward_tile_kernel's without its choices (which
+// take half of its instructions): CTAs take runs of tiles along a row of tiles, by offsets
+// from the row's first tile.
+template <int KIND>
+__global__ void __launch_bounds__(kTurnThreads, 1) gated_backward_turn_kernel(const __grid_constant__ opt_gated_backward_args a,
+                                                                             int row_tiles, int col_tiles, int per_cta) {
+  extern __shared__ __align__(16) float4 held[];       // dgate, dup, y
+  const uint32_t q = threadIdx.x & 15, row = 2 * (threadIdx.x >> 4);
+  const int64_t panel = 512 * ((a.cols + 511) / 512), panel_t = 512 * ((a.rows + 511) / 512);
+  const uint32_t scale_row = 16 * (row & 31) + 4 * (row >> 5), lane = threadIdx.x & 31, quad = threadIdx.x >> 5;
+  const uint32_t scale_col = 16 * ((4 * quad + lane) & 31) + 4 * (quad >> 3);
+  const auto dy_at = row * (uint32_t)a.dy_pitch + 8 * q, g_at = row * (uint32_t)a.gate_pitch + 8 * q,
+             u_at = row * (uint32_t)a.up_pitch + 8 * q, dg_at = row * (uint32_t)a.dgate_codes_pitch + 8 * q,
+             du_at = row * (uint32_t)a.dup_codes_pitch + 8 * q;
+  struct In {
+    Raw<Bf16> dy[2];
+    KeptAsk gate[2], up[2];
+  } in;
+  const int64_t tiles = (int64_t)row_tiles * col_tiles;
+  int64_t tile = (int64_t)blockIdx.x * per_cta;
+  const int64_t end = min(tile + per_cta, tiles);
+  int tr = (int)(tile / col_tiles), tc = (int)(tile % col_tiles);
+  const auto load = [&](int tr, int tc) {
+    const int rows = (int)min(a.rows - 128 * (int64_t)tr, (int64_t)128);
+    const bool in_cols = 128 * (int64_t)tc + 8 * q < a.cols;
+    const Bf16* dy = static_cast<const Bf16*>(a.d_dy) + 128 * (tr * a.dy_pitch + tc);
+    const uint8_t *g = static_cast<const uint8_t*>(a.d_gate) + 128 * (tr * a.gate_pitch + tc),
+                  *u = static_cast<const uint8_t*>(a.d_up) + 128 * (tr * a.up_pitch + tc);
+    const int64_t place = tr * panel + 512 * (tc >> 2) + (tc & 3);
+    const uint8_t *gs = static_cast<const uint8_t*>(a.d_gate_scales) + place, *us = static_cast<const uint8_t*>(a.d_up_scales) + place;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const bool on = in_cols && (int)row + i < rows;
+      in.dy[i] = load_if(dy + (dy_at + i * (uint32_t)a.dy_pitch), on);
+      in.gate[i].codes = load_codes_if(g + (g_at + i * (uint32_t)a.gate_pitch), on);
+      in.up[i].codes = load_codes_if(u + (u_at + i * (uint32_t)a.up_pitch), on);
+      in.gate[i].byte = load_byte_if(gs + (scale_row + 16 * i), on);
+      in.up[i].byte = load_byte_if(us + (scale_row + 16 * i), on);
+    }
+  };
+  if (tile < end) load(tr, tc);
+  for (; tile < end; ++tile) {
+    const int rows = (int)min(a.rows - 128 * (int64_t)tr, (int64_t)128), cols = (int)min(a.cols - 128 * (int64_t)tc, (int64_t)128);
+    {
+      uint8_t *dg = static_cast<uint8_t*>(a.d_dgate_codes) + 128 * (tr * a.dgate_codes_pitch + tc),
+              *du = static_cast<uint8_t*>(a.d_dup_codes) + 128 * (tr * a.dup_codes_pitch + tc);
+      const int64_t place = tr * panel + 512 * (tc >> 2) + (tc & 3);
+      uint8_t *dgs = static_cast<uint8_t*>(a.d_dgate_scales) + place, *dus = static_cast<uint8_t*>(a.d_dup_scales) + place;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float d[8], g[8], u[8], f[8], df[8];
+        values8(in.gate[i].codes, scale_of(in.gate[i].byte), g);
+        activation8<KIND, false, true>(g, f, df);
+        unpack(in.dy[i], d);
+        times8(df, d);
+        times8(d, f);                 // dup
+        values8(in.up[i].codes, scale_of(in.up[i].byte), u);
+        times8(f, u);                 // y
+        times8(df, u);                // dgate
+        const auto leave = [&](int m, const float (&x)[8]) {
+          float4* v = held + m * (kTile / 4);
+          v[turned_place(row + i, 2 * q)] = make_float4(x[0], x[1], x[2], x[3]);
+          v[turned_place(row + i, 2 * q + 1)] = make_float4(x[4], x[5], x[6], x[7]);
+        };
+        leave(0, df);
+        leave(1, d);
+        leave(2, f);
+        uint32_t gtop = top8_of(df), utop = top8_of(d);
+        tops16(gtop, utop, 0.0f);
+        const bool on = (int)row + i < rows && 8 * (int)q < cols;
+        uint8_t *dgp = dg + (dg_at + i * (uint32_t)a.dgate_codes_pitch), *dup = du + (du_at + i * (uint32_t)a.dup_codes_pitch);
+        if (__any_sync(0xFFFFFFFFu, max(gtop, utop) >= kInfBits)) {      // rare
+          put_codes8(dgp, dgs, scale_row + 16 * i, on ? 8 : 0, df);
+          put_codes8(dup, dus, scale_row + 16 * i, on ? 8 : 0, d);
+        } else {
+          put_finite_if(dgp, dgs + (scale_row + 16 * i), df, gtop, on, on && q == 0);
+          put_finite_if(dup, dus + (scale_row + 16 * i), d, utop, on, on && q == 0);
+        }
+      }
+    }
+    __syncthreads();
+    const int at_row = tr, at_col = tc;
+    if (++tc == col_tiles) {
+      tc = 0;
+      ++tr;
+    }
+    if (tile + 1 < end) load(tr, tc);
+    const int64_t place_t = at_col * panel_t + 512 * (at_row >> 2) + (at_row & 3);
+    const auto turn = [&](int m, void* codes, void* scales, int64_t pitch) {
+      put_columns<true>(held + m * (kTile / 4), static_cast<uint8_t*>(codes) + 128 * (at_col * pitch + at_row),
+                        static_cast<uint8_t*>(scales) + place_t, pitch, rows, cols);
+    };
+    turn(0, a.d_dgate_codes_t, a.d_dgate_scales_t, a.dgate_codes_t_pitch);
+    turn(1, a.d_dup_codes_t, a.d_dup_scales_t, a.dup_codes_t_pitch);
+    turn(2, a.d_y_codes_t, a.d_y_scales_t, a.y_codes_t_pitch);
+    __syncthreads();
+  }
+}
 
 // CTAs take tiles gridDim.x apart, `step_rows` and `step_cols` in rows and columns of tiles.
 template <typename T, typename S, int KIND, bool VEC>
@@ -476,20 +607,27 @@ struct VecRule {
   }
 };
 
+template <typename T, int KIND, bool UP, bool KEEP>
+cudaError_t forward_vec(const opt_gated_args& a, ChunkGrid g, int sm_count, cudaStream_t s) {
+  static OccupancyCache cache;
+  const auto kernel = gated_vec_kernel<T, KIND, UP, KEEP>;
+  g.limit((int64_t)sm_count * cached_occupancy(kernel, cache, kThreads, 0));
+  kernel<<<g.grid, g.block, 0, s>>>(a);
+  return cudaGetLastError();
+}
 template <typename T, int KIND>
 cudaError_t forward_kind(const opt_gated_args& a, int sm_count, cudaStream_t s) {
   VecRule v{a.rows, sizeof(T), a.cols % 8 == 0};
   v.see(a.d_gate, a.gate_pitch);
   v.see(a.d_up, a.up_pitch);
   v.see(a.d_y, a.y_pitch);
-  ChunkGrid g(a.rows, a.cols, kThreads);
-  if (v.ok) {
-    static OccupancyCache cache;
-    g.limit((int64_t)sm_count * cached_occupancy(gated_vec_kernel<T, KIND>, cache, kThreads, 0));
-    gated_vec_kernel<T, KIND><<<g.grid, g.block, 0, s>>>(a);
-  } else {
-    gated_any_kernel<T, KIND><<<g.grid, g.block, 0, s>>>(a);
+  const bool up = a.d_up != nullptr, keep = a.d_gate_codes != nullptr;
+  const ChunkGrid g(a.rows, a.cols, kThreads);
+  if (v.ok && (!up || keep == (a.d_up_codes != nullptr))) {
+    if (up) return keep ? forward_vec<T, KIND, true, true>(a, g, sm_count, s) : forward_vec<T, KIND, true, false>(a, g, sm_count, s);
+    return keep ? forward_vec<T, KIND, false, true>(a, g, sm_count, s) : forward_vec<T, KIND, false, false>(a, g, sm_count, s);
   }
+  gated_any_kernel<T, KIND><<<g.grid, g.block, 0, s>>>(a);
   return cudaGetLastError();
 }
 template <typename T>
@@ -502,8 +640,24 @@ cudaError_t forward(const opt_gated_args& a, int sm_count, cudaStream_t s) {
   }
 }
 
+template <int KIND>
+cudaError_t backward_turn(const opt_gated_backward_args& a, int sm_count, cudaStream_t s) {
+  static OccupancyCache cache;
+  const auto kernel = gated_backward_turn_kernel<KIND>;
+  const int row_tiles = (int)((a.rows + 127) / 128), col_tiles = (int)((a.cols + 127) / 128);
+  const int64_t tiles = (int64_t)row_tiles * col_tiles, most = (int64_t)sm_count * cached_occupancy(kernel, cache, kTurnThreads, kTurnBytes);
+  const int per_cta = (int)((tiles + most - 1) / most);
+  kernel<<<(unsigned)((tiles + per_cta - 1) / per_cta), kTurnThreads, kTurnBytes, s>>>(a, row_tiles, col_tiles, per_cta);
+  return cudaGetLastError();
+}
+
 template <typename T, typename S, int KIND, bool VEC>
 cudaError_t backward_vec(const opt_gated_backward_args& a, int sm_count, cudaStream_t s) {
+  if constexpr (sizeof(T) == 2 && sizeof(S) == 1 && VEC) {
+    if (a.d_up != nullptr && a.d_dgate == nullptr && a.d_dup == nullptr && a.d_dgate_codes != nullptr && a.d_dup_codes != nullptr &&
+        a.d_dgate_codes_t != nullptr && a.d_dup_codes_t != nullptr && a.d_y_codes_t != nullptr)
+      return backward_turn<KIND>(a, sm_count, s);
+  }
   if (a.d_dgate_codes_t == nullptr && a.d_dup_codes_t == nullptr && a.d_y_codes_t == nullptr) {
     const ChunkGrid g(a.rows, a.cols, kThreads);
     gated_backward_kernel<T, S, KIND, VEC><<<g.grid, g.block, 0, s>>>(a);

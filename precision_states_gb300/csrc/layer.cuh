@@ -460,6 +460,59 @@ __device__ __forceinline__ void store_codes8(uint8_t* p, int valid, uint2 w) {
   }
 }
 
+// Accesses under a predicate, without a branch: eight elements of a 16-byte aligned place
+// (0 if it is not on), eight of them or eight codes to such a place, and a byte.
+template <typename T>
+__device__ __forceinline__ Raw<T> load_if(const T* p, bool on) {
+  Raw<T> r;
+#pragma unroll
+  for (int k = 0; k < Raw<T>::kWords; k += 4)
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.s32 q, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+                 "@q ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+                 : "=&r"(r.w[k]), "=&r"(r.w[k + 1]), "=&r"(r.w[k + 2]), "=&r"(r.w[k + 3])
+                 : "l"(reinterpret_cast<const uint32_t*>(p) + k), "r"((int)on));
+  return r;
+}
+__device__ __forceinline__ uint2 load_codes_if(const uint8_t* p, bool on) {
+  uint2 r;
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.s32 q, %3, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
+               "@q ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];\n\t}" : "=&r"(r.x), "=&r"(r.y) : "l"(p), "r"((int)on));
+  return r;
+}
+__device__ __forceinline__ uint32_t load_byte_if(const uint8_t* p, bool on) {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.s32 q, %2, 0;\n\tmov.b32 %0, 0;\n\t@q ld.global.u8 %0, [%1];\n\t}"
+               : "=&r"(r) : "l"(p), "r"((int)on));
+  return r;
+}
+__device__ __forceinline__ void store_if(void* p, uint4 v, bool on) {
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.s32 q, %5, 0;\n\t@q st.global.cs.v4.u32 [%0], {%1,%2,%3,%4};\n\t}"
+               :: "l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"((int)on) : "memory");
+}
+__device__ __forceinline__ void store_if(void* p, uint2 v, bool on) {
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.s32 q, %3, 0;\n\t@q st.global.cs.v2.u32 [%0], {%1,%2};\n\t}"
+               :: "l"(p), "r"(v.x), "r"(v.y), "r"((int)on) : "memory");
+}
+__device__ __forceinline__ void store_byte_if(uint8_t* p, uint32_t v, bool on) {
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.s32 q, %2, 0;\n\t@q st.global.u8 [%0], %1;\n\t}" :: "l"(p), "r"(v), "r"((int)on) : "memory");
+}
+__device__ __forceinline__ void store8_if(Bf16* p, const float (&x)[8], bool on) {
+  store_if(p, make_uint4(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7])), on);
+}
+__device__ __forceinline__ void store8_if(float* p, const float (&x)[8], bool on) {
+  store_if(p, make_uint4(f2u(x[0]), f2u(x[1]), f2u(x[2]), f2u(x[3])), on);
+  store_if(p + 4, make_uint4(f2u(x[4]), f2u(x[5]), f2u(x[6]), f2u(x[7])), on);
+}
+// Codes of a chunk whose block's largest magnitude `top` is finite, and the block's scale
+// byte where `first` says so.
+__device__ __forceinline__ void put_finite_if(uint8_t* codes, uint8_t* scale, const float (&x)[8], uint32_t top, bool on, bool first) {
+  const uint32_t byte = scale_byte(top);
+  float v[8];
+  scaled8(x, inverse_scale(byte), v);
+  store_if(codes, codes8(v), on);
+  store_byte_if(scale, byte, first);
+}
+
 // Place of the scale byte of row r, block b (opt_layer.h); panel = ceil(B / 4).
 __host__ __device__ __forceinline__ int64_t scale_place(int64_t r, int64_t b, int64_t panel) {
   return 512 * ((r >> 7) * panel + (b >> 2)) + 16 * (r & 31) + 4 * ((r >> 5) & 3) + (b & 3);
@@ -470,7 +523,8 @@ struct E4m3 {};                   // element type of a kept matrix, codes with s
 
 // The scale that a byte stands for: 2^(byte - 127), NaN for 255.
 __device__ __forceinline__ float scale_of(uint32_t byte) {
-  return u2f(byte == 0u ? 0x00400000u : byte == 255u ? 0x7FC00000u : byte << 23);
+  // byte 0 is a subnormal, and 255 the only one whose successor has bit 8
+  return u2f(max(byte << 23, 0x00400000u) | (((byte + 1u) << 14) & 0x00400000u));
 }
 // Eight codes of an 8-byte aligned place, the first `valid` of which exist; the others
 // read as 0.
