@@ -296,24 +296,22 @@ __device__ __forceinline__ int turned_place(int row, int quad) {
   return 32 * row + (((quad >> 1) | (quad & 1) << 4) ^ (row >> 2));
 }
 
-// A tile's values at `v` by columns, four columns of 128 rows to a warp: codes to `codes` (the
-// tile's first column's), scale bytes to `scales` (the tile's).
-template <bool VEC>
-__device__ __forceinline__ void put_columns(const float4* v, uint8_t* codes, uint8_t* scales, int64_t pitch, int rows, int cols) {
-  const int lane = threadIdx.x & 31, quad = threadIdx.x >> 5;
+// A tile's values by columns, four columns of 128 rows to a warp, four rows of them to a lane
+// (`column` is the lane's first): their codes, a column's four to a word, and the scale byte of
+// column (lane mod 4).
+__device__ __forceinline__ uint32_t code_columns(const float4* column, uint32_t (&word)[4]) {
+  const int lane = threadIdx.x & 31;
   float x[4][4];                    // [row][column]
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float4 t = v[turned_place(4 * lane + i, quad)];
+    const float4 t = column[32 * i];
     x[i][0] = t.x; x[i][1] = t.y; x[i][2] = t.z; x[i][3] = t.w;
   }
-  uint32_t top[4], all = 0;
+  uint32_t field[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    top[j] = __reduce_max_sync(0xFFFFFFFFu, f2u(largest3(largest3(x[0][j], x[1][j], x[2][j]), x[3][j], x[3][j])));
-    all = max(all, top[j]);
-  }
-  if (all >= kInfBits) {            // rare: the finite ones' maxima, and NaN for the others
+  for (int j = 0; j < 4; ++j)
+    field[j] = scale_field(__reduce_max_sync(0xFFFFFFFFu, f2u(largest3(largest3(x[0][j], x[1][j], x[2][j]), x[3][j], x[3][j]))));
+  if (max(max(field[0], field[1]), max(field[2], field[3])) >= kOddField) {      // rare: the finite ones' maxima, and NaN for the others
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       uint32_t t = 0;
@@ -322,30 +320,30 @@ __device__ __forceinline__ void put_columns(const float4* v, uint8_t* codes, uin
         if (finite_bits(x[i][j])) t = max(t, magnitude(x[i][j]));
         else x[i][j] = u2f(0x7FC00000u);
       }
-      top[j] = __reduce_max_sync(0xFFFFFFFFu, t);
+      field[j] = scale_field(__reduce_max_sync(0xFFFFFFFFu, t));
     }
   }
-  uint32_t byte[4], word[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) byte[j] = scale_byte(top[j]);
 #pragma unroll
   for (int j = 0; j < 4; j += 2) {
-    const f2_t inv = pk(inverse_scale(byte[j]), inverse_scale(byte[j + 1]));
+    const f2_t inv = pk(inverse_of_field(field[j]), inverse_of_field(field[j + 1]));
 #pragma unroll
     for (int i = 0; i < 4; ++i) unpk(mul2(pk(x[i][j], x[i][j + 1]), inv), x[i][j], x[i][j + 1]);
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j) word[j] = e4m3x2_rn(x[0][j], x[1][j]) | e4m3x2_rn(x[2][j], x[3][j]) << 16;
+  return byte_of_field((lane & 1) ? (lane & 2) ? field[3] : field[1] : (lane & 2) ? field[2] : field[0]);
+}
+
+// Those of the tile at `v`: codes to `codes` (the tile's first column's), scale bytes to
+// `scales` (the tile's).
+template <bool VEC>
+__device__ __forceinline__ void put_columns(const float4* v, uint8_t* codes, uint8_t* scales, int64_t pitch, int rows, int cols) {
+  const int lane = threadIdx.x & 31, quad = threadIdx.x >> 5;
+  uint32_t word[4];
+  const uint32_t byte = code_columns(v + turned_place(4 * lane, quad), word);
   const Offset<VEC> step = (Offset<VEC>)pitch;
   Offset<VEC> at = 4 * quad * step + 4 * lane;
   const int left = rows - 4 * lane, wide = cols - 4 * quad;
-  if (rows == 128 && wide >= 4) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j, at += step) st_cs_u1(codes + at, word[j]);
-    store_byte_if(scales + (16 * ((4 * quad + lane) & 31) + 4 * (quad >> 3)),
-                  lane < 2 ? lane == 0 ? byte[0] : byte[1] : lane == 2 ? byte[2] : byte[3], lane < 4);
-    return;
-  }
 #pragma unroll
   for (int j = 0; j < 4; ++j, at += step) {
     if (j < wide && left >= 4) {
@@ -356,9 +354,7 @@ __device__ __forceinline__ void put_columns(const float4* v, uint8_t* codes, uin
         if (i < left) codes[at + i] = (uint8_t)(word[j] >> (8 * i));
     }
   }
-  if (lane < 4 && lane < wide)
-    scales[16 * ((4 * quad + lane) & 31) + 4 * (quad >> 3)] =
-        (uint8_t)(lane == 0 ? byte[0] : lane == 1 ? byte[1] : lane == 2 ? byte[2] : byte[3]);
+  if (lane < 4 && lane < wide) scales[16 * ((4 * quad + lane) & 31) + 4 * (quad >> 3)] = (uint8_t)byte;
 }
 
 template <typename T, typename S, bool VEC>
@@ -369,100 +365,110 @@ struct Inputs {
 
 // The whole backward pass of a training step in BF16 from kept inputs: all five 8-bit operands
 // and nothing plain.  The same work as gated_backward_tile_kernel's without its choices (which
-// take half of its instructions): CTAs take runs of tiles along a row of tiles, by offsets
-// from the row's first tile.
+// take half of its instructions).  CTAs take runs of tiles along a row of tiles; places in a
+// matrix are counted in chunks of eight elements (of a transposed one in four rows), so that
+// 32 bits hold them (turn_places_fit, below).
 template <int KIND>
 __global__ void __launch_bounds__(kTurnThreads, 1) gated_backward_turn_kernel(const __grid_constant__ opt_gated_backward_args a,
-                                                                             int row_tiles, int col_tiles, int per_cta) {
+                                                                             uint32_t row_tiles, uint32_t col_tiles, uint32_t per_cta) {
   extern __shared__ __align__(16) float4 held[];       // dgate, dup, y
-  const uint32_t q = threadIdx.x & 15, row = 2 * (threadIdx.x >> 4);
-  const int64_t panel = 512 * ((a.cols + 511) / 512), panel_t = 512 * ((a.rows + 511) / 512);
-  const uint32_t scale_row = 16 * (row & 31) + 4 * (row >> 5), lane = threadIdx.x & 31, quad = threadIdx.x >> 5;
-  const uint32_t scale_col = 16 * ((4 * quad + lane) & 31) + 4 * (quad >> 3);
-  const auto dy_at = row * (uint32_t)a.dy_pitch + 8 * q, g_at = row * (uint32_t)a.gate_pitch + 8 * q,
-             u_at = row * (uint32_t)a.up_pitch + 8 * q, dg_at = row * (uint32_t)a.dgate_codes_pitch + 8 * q,
-             du_at = row * (uint32_t)a.dup_codes_pitch + 8 * q;
+  const uint32_t q = threadIdx.x & 15, row = 2 * (threadIdx.x >> 4), lane = threadIdx.x & 31, quad = threadIdx.x >> 5;
+  const uint32_t all_rows = (uint32_t)a.rows, all_cols = (uint32_t)a.cols;
+  const uint32_t panel = 512 * ((all_cols + 511) / 512), panel_t = 512 * ((all_rows + 511) / 512);
+  const uint32_t dy_pitch = (uint32_t)(a.dy_pitch >> 3), g_pitch = (uint32_t)(a.gate_pitch >> 3), u_pitch = (uint32_t)(a.up_pitch >> 3),
+                 dg_pitch = (uint32_t)(a.dgate_codes_pitch >> 3), du_pitch = (uint32_t)(a.dup_codes_pitch >> 3),
+                 dgt_pitch = (uint32_t)(a.dgate_codes_t_pitch >> 2), dut_pitch = (uint32_t)(a.dup_codes_t_pitch >> 2),
+                 yt_pitch = (uint32_t)(a.y_codes_t_pitch >> 2);
+  float4 *const lo = held + turned_place(row, 2 * q), *const hi = held + turned_place(row, 2 * q + 1);      // row + 1: 32 further
+  const float4* const column = held + turned_place(4 * lane, quad);
   struct In {
     Raw<Bf16> dy[2];
     KeptAsk gate[2], up[2];
   } in;
-  const int64_t tiles = (int64_t)row_tiles * col_tiles;
-  int64_t tile = (int64_t)blockIdx.x * per_cta;
-  const int64_t end = min(tile + per_cta, tiles);
-  int tr = (int)(tile / col_tiles), tc = (int)(tile % col_tiles);
-  const auto load = [&](int tr, int tc) {
-    const int rows = (int)min(a.rows - 128 * (int64_t)tr, (int64_t)128);
-    const bool in_cols = 128 * (int64_t)tc + 8 * q < a.cols;
-    const Bf16* dy = static_cast<const Bf16*>(a.d_dy) + 128 * (tr * a.dy_pitch + tc);
-    const uint8_t *g = static_cast<const uint8_t*>(a.d_gate) + 128 * (tr * a.gate_pitch + tc),
-                  *u = static_cast<const uint8_t*>(a.d_up) + 128 * (tr * a.up_pitch + tc);
-    const int64_t place = tr * panel + 512 * (tc >> 2) + (tc & 3);
-    const uint8_t *gs = static_cast<const uint8_t*>(a.d_gate_scales) + place, *us = static_cast<const uint8_t*>(a.d_up_scales) + place;
+  const uint32_t tiles = row_tiles * col_tiles, begin = blockIdx.x * per_cta, end = min(begin + per_cta, tiles);
+  uint32_t tr = begin / col_tiles, tc = begin % col_tiles;
+  const auto load = [&](uint32_t tr, uint32_t tc) {
+    const uint32_t r = 128 * tr + row, c = 16 * tc + q;
+    const uint32_t at = panel * tr + 512 * (tc >> 2) + (tc & 3) + 16 * (row & 31) + 4 * (row >> 5);
+    const bool in_cols = 8 * c < all_cols;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const bool on = in_cols && (int)row + i < rows;
-      in.dy[i] = load_if(dy + (dy_at + i * (uint32_t)a.dy_pitch), on);
-      in.gate[i].codes = load_codes_if(g + (g_at + i * (uint32_t)a.gate_pitch), on);
-      in.up[i].codes = load_codes_if(u + (u_at + i * (uint32_t)a.up_pitch), on);
-      in.gate[i].byte = load_byte_if(gs + (scale_row + 16 * i), on);
-      in.up[i].byte = load_byte_if(us + (scale_row + 16 * i), on);
+      const bool on = in_cols && r + i < all_rows;
+      in.dy[i] = load_if(static_cast<const Bf16*>(a.d_dy) + (uint64_t)((r + i) * dy_pitch + c) * 8, on);
+      in.gate[i].codes = load_codes_if(static_cast<const uint8_t*>(a.d_gate) + (uint64_t)((r + i) * g_pitch + c) * 8, on);
+      in.up[i].codes = load_codes_if(static_cast<const uint8_t*>(a.d_up) + (uint64_t)((r + i) * u_pitch + c) * 8, on);
+      in.gate[i].byte = load_byte_if(static_cast<const uint8_t*>(a.d_gate_scales) + at + 16 * i, on);
+      in.up[i].byte = load_byte_if(static_cast<const uint8_t*>(a.d_up_scales) + at + 16 * i, on);
     }
   };
-  if (tile < end) load(tr, tc);
-  for (; tile < end; ++tile) {
-    const int rows = (int)min(a.rows - 128 * (int64_t)tr, (int64_t)128), cols = (int)min(a.cols - 128 * (int64_t)tc, (int64_t)128);
-    {
-      uint8_t *dg = static_cast<uint8_t*>(a.d_dgate_codes) + 128 * (tr * a.dgate_codes_pitch + tc),
-              *du = static_cast<uint8_t*>(a.d_dup_codes) + 128 * (tr * a.dup_codes_pitch + tc);
-      const int64_t place = tr * panel + 512 * (tc >> 2) + (tc & 3);
-      uint8_t *dgs = static_cast<uint8_t*>(a.d_dgate_scales) + place, *dus = static_cast<uint8_t*>(a.d_dup_scales) + place;
+  if (begin < end) load(tr, tc);
+  for (uint32_t tile = begin; tile < end; ++tile) {
+    const uint32_t r = 128 * tr + row, c = 16 * tc + q;
+    const uint32_t at = panel * tr + 512 * (tc >> 2) + (tc & 3) + 16 * (row & 31) + 4 * (row >> 5);
+    const bool in_cols = 8 * c < all_cols;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float d[8], g[8], u[8], f[8], df[8];
-        values8(in.gate[i].codes, scale_of(in.gate[i].byte), g);
-        activation8<KIND, false, true>(g, f, df);
-        unpack(in.dy[i], d);
-        times8(df, d);
-        times8(d, f);                 // dup
-        values8(in.up[i].codes, scale_of(in.up[i].byte), u);
-        times8(f, u);                 // y
-        times8(df, u);                // dgate
-        const auto leave = [&](int m, const float (&x)[8]) {
-          float4* v = held + m * (kTile / 4);
-          v[turned_place(row + i, 2 * q)] = make_float4(x[0], x[1], x[2], x[3]);
-          v[turned_place(row + i, 2 * q + 1)] = make_float4(x[4], x[5], x[6], x[7]);
-        };
-        leave(0, df);
-        leave(1, d);
-        leave(2, f);
-        uint32_t gtop = top8_of(df), utop = top8_of(d);
-        tops16(gtop, utop, 0.0f);
-        const bool on = (int)row + i < rows && 8 * (int)q < cols;
-        uint8_t *dgp = dg + (dg_at + i * (uint32_t)a.dgate_codes_pitch), *dup = du + (du_at + i * (uint32_t)a.dup_codes_pitch);
-        if (__any_sync(0xFFFFFFFFu, max(gtop, utop) >= kInfBits)) {      // rare
-          put_codes8(dgp, dgs, scale_row + 16 * i, on ? 8 : 0, df);
-          put_codes8(dup, dus, scale_row + 16 * i, on ? 8 : 0, d);
-        } else {
-          put_finite_if(dgp, dgs + (scale_row + 16 * i), df, gtop, on, on && q == 0);
-          put_finite_if(dup, dus + (scale_row + 16 * i), d, utop, on, on && q == 0);
-        }
+    for (int i = 0; i < 2; ++i) {
+      float d[8], g[8], u[8], f[8], df[8];
+      values8(in.gate[i].codes, scale_of(in.gate[i].byte), g);
+      activation8<KIND, false, true>(g, f, df);
+      unpack(in.dy[i], d);
+      times8(df, d);
+      times8(d, f);                 // dup
+      values8(in.up[i].codes, scale_of(in.up[i].byte), u);
+      times8(f, u);                 // y
+      times8(df, u);                // dgate
+      const auto leave = [&](int m, const float (&x)[8]) {
+        lo[m * (kTile / 4) + 32 * i] = make_float4(x[0], x[1], x[2], x[3]);
+        hi[m * (kTile / 4) + 32 * i] = make_float4(x[4], x[5], x[6], x[7]);
+      };
+      leave(0, df);
+      leave(1, d);
+      leave(2, f);
+      // both rows' fields through the exchanges in one word
+      uint32_t both = scale_field(top8_of(df)) >> 23 | (scale_field(top8_of(d)) >> 23) << 16;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) both = larger(both, __shfl_xor_sync(0xFFFFFFFFu, both, o), Bf16());
+      const uint32_t gfield = both << 23, ufield = (both >> 16) << 23;
+      const bool on = in_cols && r + i < all_rows;
+      uint8_t *dg = static_cast<uint8_t*>(a.d_dgate_codes) + (uint64_t)((r + i) * dg_pitch + c) * 8,
+              *du = static_cast<uint8_t*>(a.d_dup_codes) + (uint64_t)((r + i) * du_pitch + c) * 8;
+      uint8_t *dgs = static_cast<uint8_t*>(a.d_dgate_scales) + at + 16 * i, *dus = static_cast<uint8_t*>(a.d_dup_scales) + at + 16 * i;
+      if (__any_sync(0xFFFFFFFFu, max(both & 0xFFFFu, both >> 16) >= 255u)) {      // rare
+        put_codes8(dg, dgs, 0, on ? 8 : 0, df);
+        put_codes8(du, dus, 0, on ? 8 : 0, d);
+      } else {
+        put_field_if(dg, dgs, df, gfield, on, on && q == 0);
+        put_field_if(du, dus, d, ufield, on, on && q == 0);
       }
     }
     __syncthreads();
-    const int at_row = tr, at_col = tc;
+    const uint32_t col = 128 * tc + 4 * quad, rows4 = 32 * tr + lane;
+    const uint32_t at_t = panel_t * tc + 512 * (tr >> 2) + (tr & 3) + 16 * ((4 * quad + lane) & 31) + 4 * (quad >> 3);
+    const uint32_t left = all_rows - min(128 * tr + 4 * lane, all_rows), wide = all_cols - min(col, all_cols);
     if (++tc == col_tiles) {
       tc = 0;
       ++tr;
     }
     if (tile + 1 < end) load(tr, tc);
-    const int64_t place_t = at_col * panel_t + 512 * (at_row >> 2) + (at_row & 3);
-    const auto turn = [&](int m, void* codes, void* scales, int64_t pitch) {
-      put_columns<true>(held + m * (kTile / 4), static_cast<uint8_t*>(codes) + 128 * (at_col * pitch + at_row),
-                        static_cast<uint8_t*>(scales) + place_t, pitch, rows, cols);
+    const auto turn = [&](int m, void* codes, void* scales, uint32_t pitch) {
+      uint32_t word[4];
+      const uint32_t byte = code_columns(column + m * (kTile / 4), word);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint8_t* p = static_cast<uint8_t*>(codes) + (uint64_t)((col + j) * pitch + rows4) * 4;
+        if (left >= 4) {
+          if (j < wide) st_cs_u1(p, word[j]);
+        } else if (j < wide) {
+#pragma unroll
+          for (int i = 0; i < 3; ++i)
+            if (i < left) p[i] = (uint8_t)(word[j] >> (8 * i));
+        }
+      }
+      if (lane < 4 && lane < wide) (static_cast<uint8_t*>(scales) + at_t)[0] = (uint8_t)byte;
     };
-    turn(0, a.d_dgate_codes_t, a.d_dgate_scales_t, a.dgate_codes_t_pitch);
-    turn(1, a.d_dup_codes_t, a.d_dup_scales_t, a.dup_codes_t_pitch);
-    turn(2, a.d_y_codes_t, a.d_y_scales_t, a.y_codes_t_pitch);
+    turn(0, a.d_dgate_codes_t, a.d_dgate_scales_t, dgt_pitch);
+    turn(1, a.d_dup_codes_t, a.d_dup_scales_t, dut_pitch);
+    turn(2, a.d_y_codes_t, a.d_y_scales_t, yt_pitch);
     __syncthreads();
   }
 }
@@ -650,12 +656,22 @@ cudaError_t backward_turn(const opt_gated_backward_args& a, int sm_count, cudaSt
   kernel<<<(unsigned)((tiles + per_cta - 1) / per_cta), kTurnThreads, kTurnBytes, s>>>(a, row_tiles, col_tiles, per_cta);
   return cudaGetLastError();
 }
+// Whether 32 bits hold the places that gated_backward_turn_kernel counts (to the ends of
+// whole tiles).
+bool turn_places_fit(const opt_gated_backward_args& a) {
+  const int64_t most = INT64_C(0xFFFFFFFF), r = a.rows + 127, c = a.cols + 127;
+  const auto rows_fit = [&](int64_t pitch) { return pitch >= 0 && pitch <= most && (r * (pitch >> 3) + (c >> 3)) <= most; };
+  const auto cols_fit = [&](int64_t pitch) { return pitch >= 0 && pitch <= most && (c * (pitch >> 2) + (r >> 2)) <= most; };
+  return rows_fit(a.dy_pitch) && rows_fit(a.gate_pitch) && rows_fit(a.up_pitch) && rows_fit(a.dgate_codes_pitch) &&
+         rows_fit(a.dup_codes_pitch) && cols_fit(a.dgate_codes_t_pitch) && cols_fit(a.dup_codes_t_pitch) && cols_fit(a.y_codes_t_pitch) &&
+         r / 128 * (c / 512 + 1) * 512 + 512 <= most && c / 128 * (r / 512 + 1) * 512 + 512 <= most;
+}
 
 template <typename T, typename S, int KIND, bool VEC>
 cudaError_t backward_vec(const opt_gated_backward_args& a, int sm_count, cudaStream_t s) {
   if constexpr (sizeof(T) == 2 && sizeof(S) == 1 && VEC) {
     if (a.d_up != nullptr && a.d_dgate == nullptr && a.d_dup == nullptr && a.d_dgate_codes != nullptr && a.d_dup_codes != nullptr &&
-        a.d_dgate_codes_t != nullptr && a.d_dup_codes_t != nullptr && a.d_y_codes_t != nullptr)
+        a.d_dgate_codes_t != nullptr && a.d_dup_codes_t != nullptr && a.d_y_codes_t != nullptr && turn_places_fit(a))
       return backward_turn<KIND>(a, sm_count, s);
   }
   if (a.d_dgate_codes_t == nullptr && a.d_dup_codes_t == nullptr && a.d_y_codes_t == nullptr) {

@@ -375,6 +375,15 @@ struct Edges {
 __device__ __forceinline__ uint32_t scale_byte(uint32_t top_bits) {
   return (uint32_t)max((int)((top_bits + 0x1FFFFFu) >> 23) - 8, 0);
 }
+// The same as a biased exponent in place, e + 135 (so byte + 8), from which the inverse scale
+// and the byte are an instruction each.  An infinity gives 255, a NaN 255 or 256, and
+// finite values above 1.75 2^127 255 too.
+__device__ __forceinline__ uint32_t scale_field(uint32_t top_bits) {
+  return max((top_bits + 0x1FFFFFu) & 0xFF800000u, 8u << 23);
+}
+constexpr uint32_t kOddField = 255u << 23;
+__device__ __forceinline__ float inverse_of_field(uint32_t field) { return u2f((262u << 23) - field); }
+__device__ __forceinline__ uint32_t byte_of_field(uint32_t field) { return (field >> 23) - 8u; }
 // 2^-e for a scale byte; scale_byte never exceeds 247, so this is normal.
 __device__ __forceinline__ float inverse_scale(uint32_t byte) { return u2f((254u - byte) << 23); }
 
@@ -511,6 +520,14 @@ __device__ __forceinline__ void put_finite_if(uint8_t* codes, uint8_t* scale, co
   scaled8(x, inverse_scale(byte), v);
   store_if(codes, codes8(v), on);
   store_byte_if(scale, byte, first);
+}
+
+// The same from the block's field.
+__device__ __forceinline__ void put_field_if(uint8_t* codes, uint8_t* scale, const float (&x)[8], uint32_t field, bool on, bool first) {
+  float v[8];
+  scaled8(x, inverse_of_field(field), v);
+  store_if(codes, codes8(v), on);
+  store_byte_if(scale, byte_of_field(field), first);
 }
 
 // Place of the scale byte of row r, block b (opt_layer.h); panel = ceil(B / 4).
