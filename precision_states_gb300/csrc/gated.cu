@@ -290,71 +290,75 @@ template <bool VEC>
 using Offset = std::conditional_t<VEC, uint32_t, int64_t>;
 
 // Place of columns 4 quad ... 4 quad + 3 of a tile's row, in units of four values: a chunk's two
-// places are 16 apart, and rows turned, so that neither the chunks of a row nor the rows of
-// a column meet in a bank.
+// places are 16 apart, and every 16 rows turned by one more, so that neither eight chunks of a
+// row nor the rows 16 apart of a column meet in a bank.
 __device__ __forceinline__ int turned_place(int row, int quad) {
-  return 32 * row + (((quad >> 1) | (quad & 1) << 4) ^ (row >> 2));
+  return 32 * row + (((quad >> 1) | (quad & 1) << 4) ^ (row >> 4));
 }
 
-// A tile's values by columns, four columns of 128 rows to a warp, four rows of them to a lane
-// (`column` is the lane's first): their codes, a column's four to a word, and the scale byte of
-// column (lane mod 4).
-__device__ __forceinline__ uint32_t code_columns(const float4* column, uint32_t (&word)[4]) {
-  const int lane = threadIdx.x & 31;
-  float x[4][4];                    // [row][column]
+// A tile's values by columns: four columns to a warp, 16 rows of one of them to a lane
+// (`column` is the first of them).  Their codes, 16 bytes in the rows' order, and the column's
+// scale byte.
+__device__ __forceinline__ uint32_t code_column(const float* column, uint32_t (&word)[4]) {
+  float x[16];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 t = column[32 * i];
-    x[i][0] = t.x; x[i][1] = t.y; x[i][2] = t.z; x[i][3] = t.w;
-  }
-  uint32_t field[4];
+  for (int i = 0; i < 16; ++i) x[i] = column[128 * i];
+  const auto exchanged = [&](float t) {                 // over the column's eight lanes
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    field[j] = scale_field(__reduce_max_sync(0xFFFFFFFFu, f2u(largest3(largest3(x[0][j], x[1][j], x[2][j]), x[3][j], x[3][j]))));
-  if (max(max(field[0], field[1]), max(field[2], field[3])) >= kOddField) {      // rare: the finite ones' maxima, and NaN for the others
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint32_t t = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (finite_bits(x[i][j])) t = max(t, magnitude(x[i][j]));
-        else x[i][j] = u2f(0x7FC00000u);
-      }
-      field[j] = scale_field(__reduce_max_sync(0xFFFFFFFFu, t));
+    for (int o = 4; o > 0; o >>= 1) {
+      const float other = __shfl_xor_sync(0xFFFFFFFFu, t, o);
+      t = largest3(t, other, other);
     }
+    return f2u(t);
+  };
+  float top = largest3(x[0], x[1], x[2]);
+#pragma unroll
+  for (int i = 3; i < 15; i += 2) top = largest3(top, x[i], x[i + 1]);
+  uint32_t field = scale_field(exchanged(largest3(top, x[15], x[15])));
+  if (__any_sync(0xFFFFFFFFu, field >= kOddField)) {    // rare: the finite ones' maxima, and NaN for the others
+    float finite = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (finite_bits(x[i])) finite = fmaxf(finite, fabsf(x[i]));
+      else x[i] = u2f(0x7FC00000u);
+    }
+    field = scale_field(exchanged(finite));
   }
+  const float inv = inverse_of_field(field);
 #pragma unroll
-  for (int j = 0; j < 4; j += 2) {
-    const f2_t inv = pk(inverse_of_field(field[j]), inverse_of_field(field[j + 1]));
+  for (int i = 0; i < 16; i += 2) unpk(mul2(pk(x[i], x[i + 1]), pk(inv, inv)), x[i], x[i + 1]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) unpk(mul2(pk(x[i][j], x[i][j + 1]), inv), x[i][j], x[i][j + 1]);
+  for (int k = 0; k < 4; ++k) word[k] = e4m3x2_rn(x[4 * k], x[4 * k + 1]) | e4m3x2_rn(x[4 * k + 2], x[4 * k + 3]) << 16;
+  return byte_of_field(field);
+}
+// What a lane has of the columns: its column, and the first of its 16 rows.
+__device__ __forceinline__ int lane_column() { return 4 * (threadIdx.x >> 5) + ((threadIdx.x & 31) >> 3); }
+__device__ __forceinline__ int lane_row() { return 16 * (threadIdx.x & 7); }
+__device__ __forceinline__ const float* lane_values(const float4* held) {
+  const int column = lane_column();
+  return reinterpret_cast<const float*>(held + turned_place(lane_row(), column >> 2)) + (column & 3);
+}
+// 16 codes, the first `left` of which exist.
+__device__ __forceinline__ void store_codes16(uint8_t* p, const uint32_t (&word)[4], int left) {
+  if (left >= 16) {
+    st_cs_u4(p, make_uint4(word[0], word[1], word[2], word[3]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 15; ++i)
+      if (i < left) p[i] = (uint8_t)(word[i >> 2] >> (8 * (i & 3)));
   }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) word[j] = e4m3x2_rn(x[0][j], x[1][j]) | e4m3x2_rn(x[2][j], x[3][j]) << 16;
-  return byte_of_field((lane & 1) ? (lane & 2) ? field[3] : field[1] : (lane & 2) ? field[2] : field[0]);
 }
 
 // Those of the tile at `v`: codes to `codes` (the tile's first column's), scale bytes to
 // `scales` (the tile's).
 template <bool VEC>
 __device__ __forceinline__ void put_columns(const float4* v, uint8_t* codes, uint8_t* scales, int64_t pitch, int rows, int cols) {
-  const int lane = threadIdx.x & 31, quad = threadIdx.x >> 5;
   uint32_t word[4];
-  const uint32_t byte = code_columns(v + turned_place(4 * lane, quad), word);
-  const Offset<VEC> step = (Offset<VEC>)pitch;
-  Offset<VEC> at = 4 * quad * step + 4 * lane;
-  const int left = rows - 4 * lane, wide = cols - 4 * quad;
-#pragma unroll
-  for (int j = 0; j < 4; ++j, at += step) {
-    if (j < wide && left >= 4) {
-      st_cs_u1(codes + at, word[j]);
-    } else if (j < wide) {
-#pragma unroll
-      for (int i = 0; i < 3; ++i)
-        if (i < left) codes[at + i] = (uint8_t)(word[j] >> (8 * i));
-    }
-  }
-  if (lane < 4 && lane < wide) scales[16 * ((4 * quad + lane) & 31) + 4 * (quad >> 3)] = (uint8_t)byte;
+  const uint32_t byte = code_column(lane_values(v), word);
+  const int column = lane_column(), row = lane_row();
+  if (column >= cols) return;
+  store_codes16(codes + ((Offset<VEC>)column * (Offset<VEC>)pitch + row), word, rows - row);
+  if (row == 0) scales[16 * (column & 31) + 4 * (column >> 5)] = (uint8_t)byte;
 }
 
 template <typename T, typename S, bool VEC>
@@ -366,21 +370,21 @@ struct Inputs {
 // The whole backward pass of a training step in BF16 from kept inputs: all five 8-bit operands
 // and nothing plain.  The same work as gated_backward_tile_kernel's without its choices (which
 // take half of its instructions).  CTAs take runs of tiles along a row of tiles; places in a
-// matrix are counted in chunks of eight elements (of a transposed one in four rows), so that
+// matrix are counted in chunks of eight elements (of a transposed one of 16 rows), so that
 // 32 bits hold them (turn_places_fit, below).
 template <int KIND>
 __global__ void __launch_bounds__(kTurnThreads, 1) gated_backward_turn_kernel(const __grid_constant__ opt_gated_backward_args a,
                                                                              uint32_t row_tiles, uint32_t col_tiles, uint32_t per_cta) {
   extern __shared__ __align__(16) float4 held[];       // dgate, dup, y
-  const uint32_t q = threadIdx.x & 15, row = 2 * (threadIdx.x >> 4), lane = threadIdx.x & 31, quad = threadIdx.x >> 5;
+  const uint32_t q = threadIdx.x & 15, row = 2 * (threadIdx.x >> 4), t_col = lane_column(), t_row = lane_row();
   const uint32_t all_rows = (uint32_t)a.rows, all_cols = (uint32_t)a.cols;
   const uint32_t panel = 512 * ((all_cols + 511) / 512), panel_t = 512 * ((all_rows + 511) / 512);
   const uint32_t dy_pitch = (uint32_t)(a.dy_pitch >> 3), g_pitch = (uint32_t)(a.gate_pitch >> 3), u_pitch = (uint32_t)(a.up_pitch >> 3),
                  dg_pitch = (uint32_t)(a.dgate_codes_pitch >> 3), du_pitch = (uint32_t)(a.dup_codes_pitch >> 3),
-                 dgt_pitch = (uint32_t)(a.dgate_codes_t_pitch >> 2), dut_pitch = (uint32_t)(a.dup_codes_t_pitch >> 2),
-                 yt_pitch = (uint32_t)(a.y_codes_t_pitch >> 2);
+                 dgt_pitch = (uint32_t)(a.dgate_codes_t_pitch >> 4), dut_pitch = (uint32_t)(a.dup_codes_t_pitch >> 4),
+                 yt_pitch = (uint32_t)(a.y_codes_t_pitch >> 4);
   float4 *const lo = held + turned_place(row, 2 * q), *const hi = held + turned_place(row, 2 * q + 1);      // row + 1: 32 further
-  const float4* const column = held + turned_place(4 * lane, quad);
+  const float* const column = lane_values(held);
   struct In {
     Raw<Bf16> dy[2];
     KeptAsk gate[2], up[2];
@@ -391,6 +395,17 @@ __global__ void __launch_bounds__(kTurnThreads, 1) gated_backward_turn_kernel(co
     const uint32_t r = 128 * tr + row, c = 16 * tc + q;
     const uint32_t at = panel * tr + 512 * (tc >> 2) + (tc & 3) + 16 * (row & 31) + 4 * (row >> 5);
     const bool in_cols = 8 * c < all_cols;
+    if (128 * tr + 128 <= all_rows && 128 * tc + 128 <= all_cols) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        in.dy[i] = load_raw<true>(static_cast<const Bf16*>(a.d_dy) + (uint64_t)((r + i) * dy_pitch + c) * 8, 8);
+        in.gate[i].codes = load_codes8(static_cast<const uint8_t*>(a.d_gate) + (uint64_t)((r + i) * g_pitch + c) * 8, 8);
+        in.up[i].codes = load_codes8(static_cast<const uint8_t*>(a.d_up) + (uint64_t)((r + i) * u_pitch + c) * 8, 8);
+        in.gate[i].byte = (static_cast<const uint8_t*>(a.d_gate_scales) + at)[16 * i];
+        in.up[i].byte = (static_cast<const uint8_t*>(a.d_up_scales) + at)[16 * i];
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const bool on = in_cols && r + i < all_rows;
@@ -442,9 +457,8 @@ __global__ void __launch_bounds__(kTurnThreads, 1) gated_backward_turn_kernel(co
       }
     }
     __syncthreads();
-    const uint32_t col = 128 * tc + 4 * quad, rows4 = 32 * tr + lane;
-    const uint32_t at_t = panel_t * tc + 512 * (tr >> 2) + (tr & 3) + 16 * ((4 * quad + lane) & 31) + 4 * (quad >> 3);
-    const uint32_t left = all_rows - min(128 * tr + 4 * lane, all_rows), wide = all_cols - min(col, all_cols);
+    const uint32_t col = 128 * tc + t_col, row16 = 128 * tr + t_row;
+    const uint32_t at_t = panel_t * tc + 512 * (tr >> 2) + (tr & 3) + 16 * (t_col & 31) + 4 * (t_col >> 5);
     if (++tc == col_tiles) {
       tc = 0;
       ++tr;
@@ -452,19 +466,11 @@ __global__ void __launch_bounds__(kTurnThreads, 1) gated_backward_turn_kernel(co
     if (tile + 1 < end) load(tr, tc);
     const auto turn = [&](int m, void* codes, void* scales, uint32_t pitch) {
       uint32_t word[4];
-      const uint32_t byte = code_columns(column + m * (kTile / 4), word);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint8_t* p = static_cast<uint8_t*>(codes) + (uint64_t)((col + j) * pitch + rows4) * 4;
-        if (left >= 4) {
-          if (j < wide) st_cs_u1(p, word[j]);
-        } else if (j < wide) {
-#pragma unroll
-          for (int i = 0; i < 3; ++i)
-            if (i < left) p[i] = (uint8_t)(word[j] >> (8 * i));
-        }
+      const uint32_t byte = code_column(column + m * kTile, word);
+      if (col < all_cols) {
+        store_codes16(static_cast<uint8_t*>(codes) + (uint64_t)(col * pitch + (row16 >> 4)) * 16, word, (int)(all_rows - row16));
+        if (t_row == 0) (static_cast<uint8_t*>(scales) + at_t)[0] = (uint8_t)byte;
       }
-      if (lane < 4 && lane < wide) (static_cast<uint8_t*>(scales) + at_t)[0] = (uint8_t)byte;
     };
     turn(0, a.d_dgate_codes_t, a.d_dgate_scales_t, dgt_pitch);
     turn(1, a.d_dup_codes_t, a.d_dup_scales_t, dut_pitch);
@@ -661,7 +667,7 @@ cudaError_t backward_turn(const opt_gated_backward_args& a, int sm_count, cudaSt
 bool turn_places_fit(const opt_gated_backward_args& a) {
   const int64_t most = INT64_C(0xFFFFFFFF), r = a.rows + 127, c = a.cols + 127;
   const auto rows_fit = [&](int64_t pitch) { return pitch >= 0 && pitch <= most && (r * (pitch >> 3) + (c >> 3)) <= most; };
-  const auto cols_fit = [&](int64_t pitch) { return pitch >= 0 && pitch <= most && (c * (pitch >> 2) + (r >> 2)) <= most; };
+  const auto cols_fit = [&](int64_t pitch) { return pitch >= 0 && pitch <= most && (c * (pitch >> 4) + (r >> 4)) <= most; };
   return rows_fit(a.dy_pitch) && rows_fit(a.gate_pitch) && rows_fit(a.up_pitch) && rows_fit(a.dgate_codes_pitch) &&
          rows_fit(a.dup_codes_pitch) && cols_fit(a.dgate_codes_t_pitch) && cols_fit(a.dup_codes_t_pitch) && cols_fit(a.y_codes_t_pitch) &&
          r / 128 * (c / 512 + 1) * 512 + 512 <= most && c / 128 * (r / 512 + 1) * 512 + 512 <= most;
