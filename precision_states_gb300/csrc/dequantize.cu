@@ -25,37 +25,145 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const __grid_const
   }
 }
 
-// A 128 x 128 tile to a CTA, each thread with an 8 x 8 square.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kTileThreads, 2) dequantize_tile_kernel(const __grid_constant__ opt_dequantize_args a,
-                                                                         int64_t col_tiles) {
-  __shared__ TileTurn sh;
-  const int64_t r0 = 128 * (blockIdx.x / col_tiles), c0 = 128 * (blockIdx.x % col_tiles);
-  const int rows = (int)min(a.rows - r0, (int64_t)128), cols = (int)min(a.cols - c0, (int64_t)128);
-  const int square = threadIdx.x & 15, band = threadIdx.x >> 4, l = 8 * band;
-  const int64_t c = c0 + 8 * square;
-  Raw<float> raw[8];
-  {
-    KeptAsk ask[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int valid = l + i < rows ? max(min(cols - 8 * square, 8), 0) : 0;
-      ask[i] = Source<E4m3, VEC>(a.d_codes, a.d_scales, a.codes_pitch, a.rows, a.cols, r0 + l + i).ahead(c, valid);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int valid = l + i < rows ? max(min(cols - 8 * square, 8), 0) : 0;
-      float x[8];
-      values8(ask[i].codes, scale_of(ask[i].byte), x);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) raw[i].w[j] = j < valid ? f2u(x[j]) : 0u;
-      if (a.d_x != nullptr && valid > 0)
-        store8<VEC>(static_cast<T*>(a.d_x) + (r0 + l + i) * a.x_pitch + c, valid, x);
-    }
+// The transposed operand, and plain values with it: a 128 x 128 tile of codes in shared
+// memory to a CTA.  A warp takes 16 columns, a lane 16 rows of four of them, two at a time:
+// the column's maximum is three exchanges away, and its codes leave in whole lines.
+// Word w of a tile's row (four codes) is at w with its upper three bits turned by row / 16, so
+// that a warp's words (four of a row, rows 16 apart) meet in no bank.
+__device__ __forceinline__ int tile_word(int row, int w) { return 32 * row + (w ^ (row >> 4 << 2)); }
+
+// Row `row` of the tile as plain elements to a row that begins anywhere, by a warp: whole
+// words, consecutive lanes' side by side.
+__device__ __forceinline__ float tile_value(const uint32_t* codes, const float* scale, int row, int e) {
+  float lo, hi;
+  e4m3x2_dec(reinterpret_cast<const uint8_t*>(codes + tile_word(row, e >> 2))[e & 3], lo, hi);
+  return lo * scale[row];
+}
+__device__ __forceinline__ void put_row(float* out, const uint32_t* codes, const float* scale, int row, int cols) {
+  for (int e = threadIdx.x & 31; e < cols; e += 32) out[e] = tile_value(codes, scale, row, e);
+}
+__device__ __forceinline__ void put_row(Bf16* out, const uint32_t* codes, const float* scale, int row, int cols) {
+  const int lane = threadIdx.x & 31, head = (int)((uintptr_t)out >> 1) & 1;      // an element before the first whole word
+  if (head && lane == 0) out[0].bits = (uint16_t)bf16_pair(tile_value(codes, scale, row, 0), 0.0f);
+  for (int e = head + 2 * lane; e < cols; e += 64) {
+    const float lo = tile_value(codes, scale, row, e);
+    if (e + 1 < cols) *reinterpret_cast<uint32_t*>(out + e) = bf16_pair(lo, tile_value(codes, scale, row, e + 1));
+    else out[e].bits = (uint16_t)bf16_pair(lo, 0.0f);
   }
-  turn_square(raw, sh, r0, c0, cols, static_cast<uint8_t*>(a.d_scales_t), (a.rows + 511) / 512);
+}
+
+template <typename T, bool PLAIN, bool VEC>
+__global__ void __launch_bounds__(kTileThreads, 4) dequantize_tile_kernel(const __grid_constant__ opt_dequantize_args a,
+                                                                         uint32_t col_tiles) {
+  __shared__ __align__(16) uint32_t codes[128 * 32];
+  __shared__ __align__(16) float scale[128];
+  const uint32_t tr = blockIdx.x / col_tiles, tc = blockIdx.x % col_tiles;
+  const int64_t r0 = 128 * (int64_t)tr, c0 = 128 * (int64_t)tc;
+  const int rows = (int)min(a.rows - r0, (int64_t)128), cols = (int)min(a.cols - c0, (int64_t)128), t = threadIdx.x;
+  if (t < 128) {
+    const uint8_t* place = static_cast<const uint8_t*>(a.d_scales) + scale_place(r0 + t, tc, (a.cols + 511) / 512);
+    scale[t] = scale_of(load_byte_if(place, t < rows));
+  }
+  {
+    // rows t / 8 + 32 i, 16 codes at 16 (t mod 8)
+    const int e = 16 * (t & 7);
+    const uint8_t* p = static_cast<const uint8_t*>(a.d_codes) + (r0 + (t >> 3)) * a.codes_pitch + c0 + e;
+    uint4 w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i, p += 32 * a.codes_pitch) {
+      const int left = (t >> 3) + 32 * i < rows ? cols - e : 0;
+      w[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (left >= 16) {
+        w[i] = ld_cs_u4(p);
+      } else if (left > 0) {
+        const uint2 lo = load_codes8(p, min(left, 8)), hi = load_codes8(p + 8, left - 8);
+        w[i] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(codes + tile_word((t >> 3) + 32 * i, e >> 2)) = w[i];
+  }
   __syncthreads();
-  store_turned(sh, static_cast<uint8_t*>(a.d_codes_t), a.codes_t_pitch, r0, c0, rows, cols);
+  if constexpr (PLAIN && VEC) {
+    // a row's chunk of eight to a thread
+#pragma unroll 2
+    for (int i = 0; i < 8; ++i) {
+      const int row = (t >> 4) + 16 * i, e = 8 * (t & 15);
+      float x[8];
+      values8(*reinterpret_cast<const uint2*>(codes + tile_word(row, e >> 2)), scale[row], x);
+      store8_if(static_cast<T*>(a.d_x) + (r0 + row) * a.x_pitch + c0 + e, x, row < rows && e < cols);
+    }
+  } else if constexpr (PLAIN) {
+    for (int row = t >> 5; row < rows; row += kTileThreads / 32)
+      put_row(static_cast<T*>(a.d_x) + (r0 + row) * a.x_pitch + c0, codes, scale, row, cols);
+  }
+  const int lane = t & 31, row = 16 * (lane >> 2), word = 4 * (t >> 5) + (lane & 3);      // the lane's rows and columns' word
+  const uint32_t* mine = codes + tile_word(row, word);
+  float factor[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) factor[i] = scale[row + i];
+  uint8_t* out = static_cast<uint8_t*>(a.d_codes_t) + (c0 + 4 * word) * a.codes_t_pitch + r0 + row;
+  uint8_t* place = static_cast<uint8_t*>(a.d_scales_t) + scale_place(c0 + 4 * word, tr, (a.rows + 511) / 512);      // the next columns: 16 further
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    f2_t x[16];                      // columns 2 h and 2 h + 1
+    float top0 = 0.0f, top1 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float lo, hi;
+      e4m3x2_dec((mine[32 * i] >> (16 * h)) & 0xFFFFu, lo, hi);
+      x[i] = mul2(pk(lo, hi), pk(factor[i], factor[i]));
+    }
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      float a0, a1, b0, b1;
+      unpk(x[i], a0, a1);
+      unpk(x[i + 1], b0, b1);
+      top0 = largest3(top0, a0, b0);
+      top1 = largest3(top1, a1, b1);
+    }
+    const auto exchanged = [&](float v) {                 // over the column's eight lanes
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        const float other = __shfl_xor_sync(0xFFFFFFFFu, v, o);
+        v = largest3(v, other, other);
+      }
+      return f2u(v);
+    };
+    uint32_t f0 = scale_field(exchanged(top0)), f1 = scale_field(exchanged(top1));
+    if (__any_sync(0xFFFFFFFFu, max(f0, f1) >= kOddField)) {    // rare: the finite ones' maxima, and NaN for the others
+      top0 = top1 = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float lo, hi;
+        unpk(x[i], lo, hi);
+        top0 = finite_bits(lo) ? fmaxf(top0, fabsf(lo)) : top0;
+        top1 = finite_bits(hi) ? fmaxf(top1, fabsf(hi)) : top1;
+        x[i] = pk(finite_bits(lo) ? lo : u2f(0x7FC00000u), finite_bits(hi) ? hi : u2f(0x7FC00000u));
+      }
+      f0 = scale_field(exchanged(top0));
+      f1 = scale_field(exchanged(top1));
+    }
+    const f2_t inv = pk(inverse_of_field(f0), inverse_of_field(f1));
+    uint32_t first[4], second[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float v[4][2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) unpk(mul2(x[4 * k + i], inv), v[i][0], v[i][1]);
+      first[k] = e4m3x2_rn(v[0][0], v[1][0]) | e4m3x2_rn(v[2][0], v[3][0]) << 16;
+      second[k] = e4m3x2_rn(v[0][1], v[1][1]) | e4m3x2_rn(v[2][1], v[3][1]) << 16;
+    }
+    const int left = cols - 4 * word - 2 * h;
+    if (left > 0) store_codes16(out, first, rows - row);
+    if (left > 1) store_codes16(out + a.codes_t_pitch, second, rows - row);
+    if (row == 0) {
+      if (left > 0) place[0] = (uint8_t)byte_of_field(f0);
+      if (left > 1) place[16] = (uint8_t)byte_of_field(f1);
+    }
+    out += 2 * a.codes_t_pitch;
+    place += 32;
+  }
 }
 
 template <typename T, bool VEC>
@@ -65,7 +173,9 @@ cudaError_t launch(const opt_dequantize_args& a, cudaStream_t s) {
     dequantize_kernel<T, VEC><<<g.grid, g.block, 0, s>>>(a);
   } else {
     const int64_t col_tiles = (a.cols + 127) / 128;
-    dequantize_tile_kernel<T, VEC><<<(unsigned)((a.rows + 127) / 128 * col_tiles), kTileThreads, 0, s>>>(a, col_tiles);
+    const unsigned tiles = (unsigned)((a.rows + 127) / 128 * col_tiles);
+    if (a.d_x == nullptr) dequantize_tile_kernel<T, false, true><<<tiles, kTileThreads, 0, s>>>(a, (uint32_t)col_tiles);
+    else dequantize_tile_kernel<T, true, VEC><<<tiles, kTileThreads, 0, s>>>(a, (uint32_t)col_tiles);
   }
   return cudaGetLastError();
 }
@@ -76,6 +186,7 @@ cudaError_t launch_dequantize(const opt_dequantize_args& a, cudaStream_t s) {
   const int64_t es = a.dtype == OPT_F32 ? 4 : 2;
   const bool vec = a.cols % 8 == 0 && (a.d_x == nullptr || (((uintptr_t)a.d_x & 15u) == 0 &&
                                                             (a.rows == 1 || a.x_pitch * es % 16 == 0)));
+  if (a.d_x == nullptr) return launch<Bf16, true>(a, s);      // the same for either type
   if (a.dtype == OPT_F32) return vec ? launch<float, true>(a, s) : launch<float, false>(a, s);
   return vec ? launch<Bf16, true>(a, s) : launch<Bf16, false>(a, s);
 }

@@ -338,17 +338,6 @@ __device__ __forceinline__ const float* lane_values(const float4* held) {
   const int column = lane_column();
   return reinterpret_cast<const float*>(held + turned_place(lane_row(), column >> 2)) + (column & 3);
 }
-// 16 codes, the first `left` of which exist.
-__device__ __forceinline__ void store_codes16(uint8_t* p, const uint32_t (&word)[4], int left) {
-  if (left >= 16) {
-    st_cs_u4(p, make_uint4(word[0], word[1], word[2], word[3]));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 15; ++i)
-      if (i < left) p[i] = (uint8_t)(word[i >> 2] >> (8 * (i & 3)));
-  }
-}
-
 // Those of the tile at `v`: codes to `codes` (the tile's first column's), scale bytes to
 // `scales` (the tile's).
 template <bool VEC>

@@ -190,4 +190,15 @@ __device__ __forceinline__ void store_turned(const TileTurn& sh, uint8_t* codes_
   }
 }
 
+// 16 codes, the first `left` of which exist.
+__device__ __forceinline__ void store_codes16(uint8_t* p, const uint32_t (&word)[4], int left) {
+  if (left >= 16) {
+    st_cs_u4(p, make_uint4(word[0], word[1], word[2], word[3]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 15; ++i)
+      if (i < left) p[i] = (uint8_t)(word[i >> 2] >> (8 * (i & 3)));
+  }
+}
+
 }  // namespace psopt
