@@ -52,143 +52,168 @@ __device__ __forceinline__ void put_row(Bf16* out, const uint32_t* codes, const 
   }
 }
 
+// 16 bytes to shared memory in the background, the first `left` of them from `p`, zeros then.
+__device__ __forceinline__ void copy16(void* to, const uint8_t* p, int left) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+               :: "r"((uint32_t)__cvta_generic_to_shared(to)), "l"(p), "r"(min(max(left, 0), 16)) : "memory");
+}
+
+// CTAs take tiles gridDim.x apart (`step_rows` and `step_cols` in tiles), the next tile's codes
+// on their way while one is turned.
 template <typename T, bool PLAIN, bool VEC>
-__global__ void __launch_bounds__(kTileThreads, 4) dequantize_tile_kernel(const __grid_constant__ opt_dequantize_args a,
-                                                                         uint32_t col_tiles) {
-  __shared__ __align__(16) uint32_t codes[128 * 32];
-  __shared__ __align__(16) float scale[128];
-  const uint32_t tr = blockIdx.x / col_tiles, tc = blockIdx.x % col_tiles;
-  const int64_t r0 = 128 * (int64_t)tr, c0 = 128 * (int64_t)tc;
-  const int rows = (int)min(a.rows - r0, (int64_t)128), cols = (int)min(a.cols - c0, (int64_t)128), t = threadIdx.x;
-  if (t < 128) {
-    const uint8_t* place = static_cast<const uint8_t*>(a.d_scales) + scale_place(r0 + t, tc, (a.cols + 511) / 512);
-    scale[t] = scale_of(load_byte_if(place, t < rows));
-  }
-  {
+__global__ void __launch_bounds__(kTileThreads, 3) dequantize_tile_kernel(const __grid_constant__ opt_dequantize_args a, int row_tiles,
+                                                                         int col_tiles, int step_rows, int step_cols) {
+  __shared__ __align__(16) uint32_t held[2][128 * 32];
+  __shared__ __align__(16) float held_scale[2][128];
+  const int t = threadIdx.x, lane = t & 31, row = 16 * (lane >> 2), word = 4 * (t >> 5) + (lane & 3);      // the lane's rows and columns' word
+  const int64_t panel = (a.cols + 511) / 512, panel_t = (a.rows + 511) / 512;
+  const uint8_t* source = static_cast<const uint8_t*>(a.d_codes) + (t >> 3) * a.codes_pitch + 16 * (t & 7);
+  const uint8_t* source_scale = static_cast<const uint8_t*>(a.d_scales) + 16 * (t & 31) + 4 * ((t >> 5) & 3);
+  uint8_t* target = static_cast<uint8_t*>(a.d_codes_t) + 4 * word * a.codes_t_pitch + row;
+  uint8_t* target_scale = static_cast<uint8_t*>(a.d_scales_t) + 16 * ((4 * word) & 31) + 4 * (word >> 3);      // the next columns: 16 further
+  uint32_t byte = 0;               // row t's scale in the tile under way
+  const auto ask = [&](int tr, int tc, int turn) {
+    const int rows = (int)min(a.rows - 128 * (int64_t)tr, (int64_t)128), cols = (int)min(a.cols - 128 * (int64_t)tc, (int64_t)128);
+    const uint8_t* p = source + 128 * (tr * a.codes_pitch + tc);
     // rows t / 8 + 32 i, 16 codes at 16 (t mod 8)
-    const int e = 16 * (t & 7);
-    const uint8_t* p = static_cast<const uint8_t*>(a.d_codes) + (r0 + (t >> 3)) * a.codes_pitch + c0 + e;
-    uint4 w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i, p += 32 * a.codes_pitch) {
-      const int left = (t >> 3) + 32 * i < rows ? cols - e : 0;
-      w[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (left >= 16) {
-        w[i] = ld_cs_u4(p);
-      } else if (left > 0) {
-        const uint2 lo = load_codes8(p, min(left, 8)), hi = load_codes8(p + 8, left - 8);
-        w[i] = make_uint4(lo.x, lo.y, hi.x, hi.y);
-      }
+    for (int i = 0; i < 4; ++i, p += 32 * a.codes_pitch)
+      copy16(held[turn] + tile_word((t >> 3) + 32 * i, 4 * (t & 7)), p, (t >> 3) + 32 * i < rows ? cols - 16 * (t & 7) : 0);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    byte = load_byte_if(source_scale + 512 * (tr * panel + (tc >> 2)) + (tc & 3), t < rows);
+  };
+  int tr = (int)blockIdx.x / col_tiles, tc = (int)blockIdx.x % col_tiles;
+  ask(tr, tc, 0);
+  for (int turn = 0; tr < row_tiles; turn ^= 1) {
+    const int64_t r0 = 128 * (int64_t)tr, c0 = 128 * (int64_t)tc;
+    const int rows = (int)min(a.rows - r0, (int64_t)128), cols = (int)min(a.cols - c0, (int64_t)128);
+    uint8_t *out = target + 128 * (tc * a.codes_t_pitch + tr), *place = target_scale + 512 * (tc * panel_t + (tr >> 2)) + (tr & 3);
+    const uint32_t* const codes = held[turn];
+    const float* const scale = held_scale[turn];
+    if (t < 128) held_scale[turn][t] = scale_of(byte);
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();                 // this tile is there, and the other's place is read by nobody
+    tr += step_rows;
+    tc += step_cols;
+    if (tc >= col_tiles) {
+      tc -= col_tiles;
+      ++tr;
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(codes + tile_word((t >> 3) + 32 * i, e >> 2)) = w[i];
-  }
-  __syncthreads();
-  if constexpr (PLAIN && VEC) {
-    // a row's chunk of eight to a thread
+    if (tr < row_tiles) ask(tr, tc, turn ^ 1);
+    if constexpr (PLAIN && VEC) {
+      // a row's chunk of eight to a thread
 #pragma unroll 2
-    for (int i = 0; i < 8; ++i) {
-      const int row = (t >> 4) + 16 * i, e = 8 * (t & 15);
-      float x[8];
-      values8(*reinterpret_cast<const uint2*>(codes + tile_word(row, e >> 2)), scale[row], x);
-      store8_if(static_cast<T*>(a.d_x) + (r0 + row) * a.x_pitch + c0 + e, x, row < rows && e < cols);
-    }
-  } else if constexpr (PLAIN) {
-    for (int row = t >> 5; row < rows; row += kTileThreads / 32)
-      put_row(static_cast<T*>(a.d_x) + (r0 + row) * a.x_pitch + c0, codes, scale, row, cols);
-  }
-  const int lane = t & 31, row = 16 * (lane >> 2), word = 4 * (t >> 5) + (lane & 3);      // the lane's rows and columns' word
-  const uint32_t* mine = codes + tile_word(row, word);
-  float factor[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) factor[i] = scale[row + i];
-  uint8_t* out = static_cast<uint8_t*>(a.d_codes_t) + (c0 + 4 * word) * a.codes_t_pitch + r0 + row;
-  uint8_t* place = static_cast<uint8_t*>(a.d_scales_t) + scale_place(c0 + 4 * word, tr, (a.rows + 511) / 512);      // the next columns: 16 further
-#pragma unroll 1
-  for (int h = 0; h < 2; ++h) {
-    f2_t x[16];                      // columns 2 h and 2 h + 1
-    float top0 = 0.0f, top1 = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float lo, hi;
-      e4m3x2_dec((mine[32 * i] >> (16 * h)) & 0xFFFFu, lo, hi);
-      x[i] = mul2(pk(lo, hi), pk(factor[i], factor[i]));
-    }
-#pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-      float a0, a1, b0, b1;
-      unpk(x[i], a0, a1);
-      unpk(x[i + 1], b0, b1);
-      top0 = largest3(top0, a0, b0);
-      top1 = largest3(top1, a1, b1);
-    }
-    const auto exchanged = [&](float v) {                 // over the column's eight lanes
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        const float other = __shfl_xor_sync(0xFFFFFFFFu, v, o);
-        v = largest3(v, other, other);
+      for (int i = 0; i < 8; ++i) {
+        const int row = (t >> 4) + 16 * i, e = 8 * (t & 15);
+        float x[8];
+        values8(*reinterpret_cast<const uint2*>(codes + tile_word(row, e >> 2)), scale[row], x);
+        store8_if(static_cast<T*>(a.d_x) + (r0 + row) * a.x_pitch + c0 + e, x, row < rows && e < cols);
       }
-      return f2u(v);
-    };
-    uint32_t f0 = scale_field(exchanged(top0)), f1 = scale_field(exchanged(top1));
-    if (__any_sync(0xFFFFFFFFu, max(f0, f1) >= kOddField)) {    // rare: the finite ones' maxima, and NaN for the others
-      top0 = top1 = 0.0f;
+    } else if constexpr (PLAIN) {
+      for (int row = t >> 5; row < rows; row += kTileThreads / 32)
+        put_row(static_cast<T*>(a.d_x) + (r0 + row) * a.x_pitch + c0, codes, scale, row, cols);
+    }
+    const uint32_t* mine = codes + tile_word(row, word);
+    float factor[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) factor[i] = scale[row + i];
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      f2_t x[16];                      // columns 2 h and 2 h + 1
+      float top0 = 0.0f, top1 = 0.0f;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         float lo, hi;
-        unpk(x[i], lo, hi);
-        top0 = finite_bits(lo) ? fmaxf(top0, fabsf(lo)) : top0;
-        top1 = finite_bits(hi) ? fmaxf(top1, fabsf(hi)) : top1;
-        x[i] = pk(finite_bits(lo) ? lo : u2f(0x7FC00000u), finite_bits(hi) ? hi : u2f(0x7FC00000u));
+        e4m3x2_dec((mine[32 * i] >> (16 * h)) & 0xFFFFu, lo, hi);
+        x[i] = mul2(pk(lo, hi), pk(factor[i], factor[i]));
       }
-      f0 = scale_field(exchanged(top0));
-      f1 = scale_field(exchanged(top1));
-    }
-    const f2_t inv = pk(inverse_of_field(f0), inverse_of_field(f1));
-    uint32_t first[4], second[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float v[4][2];
+      for (int i = 0; i < 16; i += 2) {
+        float a0, a1, b0, b1;
+        unpk(x[i], a0, a1);
+        unpk(x[i + 1], b0, b1);
+        top0 = largest3(top0, a0, b0);
+        top1 = largest3(top1, a1, b1);
+      }
+      const auto exchanged = [&](float v) {                 // over the column's eight lanes
 #pragma unroll
-      for (int i = 0; i < 4; ++i) unpk(mul2(x[4 * k + i], inv), v[i][0], v[i][1]);
-      first[k] = e4m3x2_rn(v[0][0], v[1][0]) | e4m3x2_rn(v[2][0], v[3][0]) << 16;
-      second[k] = e4m3x2_rn(v[0][1], v[1][1]) | e4m3x2_rn(v[2][1], v[3][1]) << 16;
+        for (int o = 4; o < 32; o <<= 1) {
+          const float other = __shfl_xor_sync(0xFFFFFFFFu, v, o);
+          v = largest3(v, other, other);
+        }
+        return f2u(v);
+      };
+      uint32_t f0 = scale_field(exchanged(top0)), f1 = scale_field(exchanged(top1));
+      if (__any_sync(0xFFFFFFFFu, max(f0, f1) >= kOddField)) {    // rare: the finite ones' maxima, and NaN for the others
+        top0 = top1 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float lo, hi;
+          unpk(x[i], lo, hi);
+          top0 = finite_bits(lo) ? fmaxf(top0, fabsf(lo)) : top0;
+          top1 = finite_bits(hi) ? fmaxf(top1, fabsf(hi)) : top1;
+          x[i] = pk(finite_bits(lo) ? lo : u2f(0x7FC00000u), finite_bits(hi) ? hi : u2f(0x7FC00000u));
+        }
+        f0 = scale_field(exchanged(top0));
+        f1 = scale_field(exchanged(top1));
+      }
+      const f2_t inv = pk(inverse_of_field(f0), inverse_of_field(f1));
+      uint32_t first[4], second[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float v[4][2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) unpk(mul2(x[4 * k + i], inv), v[i][0], v[i][1]);
+        first[k] = e4m3x2_rn(v[0][0], v[1][0]) | e4m3x2_rn(v[2][0], v[3][0]) << 16;
+        second[k] = e4m3x2_rn(v[0][1], v[1][1]) | e4m3x2_rn(v[2][1], v[3][1]) << 16;
+      }
+      if (rows == 128 && cols == 128) {
+        st_cs_u4(out, make_uint4(first[0], first[1], first[2], first[3]));
+        st_cs_u4(out + a.codes_t_pitch, make_uint4(second[0], second[1], second[2], second[3]));
+        store_byte_if(place, byte_of_field(f0), row == 0);
+        store_byte_if(place + 16, byte_of_field(f1), row == 0);
+      } else {
+        const int left = cols - 4 * word - 2 * h;
+        if (left > 0) store_codes16(out, first, rows - row);
+        if (left > 1) store_codes16(out + a.codes_t_pitch, second, rows - row);
+        store_byte_if(place, byte_of_field(f0), row == 0 && left > 0);
+        store_byte_if(place + 16, byte_of_field(f1), row == 0 && left > 1);
+      }
+      out += 2 * a.codes_t_pitch;
+      place += 32;
     }
-    const int left = cols - 4 * word - 2 * h;
-    if (left > 0) store_codes16(out, first, rows - row);
-    if (left > 1) store_codes16(out + a.codes_t_pitch, second, rows - row);
-    if (row == 0) {
-      if (left > 0) place[0] = (uint8_t)byte_of_field(f0);
-      if (left > 1) place[16] = (uint8_t)byte_of_field(f1);
-    }
-    out += 2 * a.codes_t_pitch;
-    place += 32;
   }
 }
 
+template <typename T, bool PLAIN, bool VEC>
+cudaError_t launch_tiles(const opt_dequantize_args& a, int sm_count, cudaStream_t s) {
+  static OccupancyCache cache;
+  const auto kernel = dequantize_tile_kernel<T, PLAIN, VEC>;
+  const int row_tiles = (int)((a.rows + 127) / 128), col_tiles = (int)((a.cols + 127) / 128);
+  const int64_t tiles = (int64_t)row_tiles * col_tiles, most = (int64_t)sm_count * cached_occupancy(kernel, cache, kTileThreads, 0);
+  const int grid = (int)(tiles < most ? tiles : most);
+  kernel<<<grid, kTileThreads, 0, s>>>(a, row_tiles, col_tiles, grid / col_tiles, grid % col_tiles);
+  return cudaGetLastError();
+}
+
 template <typename T, bool VEC>
-cudaError_t launch(const opt_dequantize_args& a, cudaStream_t s) {
-  if (a.d_codes_t == nullptr) {
-    const ChunkGrid g(a.rows, a.cols, kThreads);
-    dequantize_kernel<T, VEC><<<g.grid, g.block, 0, s>>>(a);
-  } else {
-    const int64_t col_tiles = (a.cols + 127) / 128;
-    const unsigned tiles = (unsigned)((a.rows + 127) / 128 * col_tiles);
-    if (a.d_x == nullptr) dequantize_tile_kernel<T, false, true><<<tiles, kTileThreads, 0, s>>>(a, (uint32_t)col_tiles);
-    else dequantize_tile_kernel<T, true, VEC><<<tiles, kTileThreads, 0, s>>>(a, (uint32_t)col_tiles);
-  }
+cudaError_t launch(const opt_dequantize_args& a, int sm_count, cudaStream_t s) {
+  if (a.d_x == nullptr) return launch_tiles<T, false, true>(a, sm_count, s);
+  if (a.d_codes_t != nullptr) return launch_tiles<T, true, VEC>(a, sm_count, s);
+  const ChunkGrid g(a.rows, a.cols, kThreads);
+  dequantize_kernel<T, VEC><<<g.grid, g.block, 0, s>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_dequantize(const opt_dequantize_args& a, cudaStream_t s) {
+cudaError_t launch_dequantize(const opt_dequantize_args& a, int sm_count, cudaStream_t s) {
   const int64_t es = a.dtype == OPT_F32 ? 4 : 2;
   const bool vec = a.cols % 8 == 0 && (a.d_x == nullptr || (((uintptr_t)a.d_x & 15u) == 0 &&
                                                             (a.rows == 1 || a.x_pitch * es % 16 == 0)));
-  if (a.d_x == nullptr) return launch<Bf16, true>(a, s);      // the same for either type
-  if (a.dtype == OPT_F32) return vec ? launch<float, true>(a, s) : launch<float, false>(a, s);
-  return vec ? launch<Bf16, true>(a, s) : launch<Bf16, false>(a, s);
+  if (a.d_x == nullptr) return launch<Bf16, true>(a, sm_count, s);      // the same for either type
+  if (a.dtype == OPT_F32) return vec ? launch<float, true>(a, sm_count, s) : launch<float, false>(a, sm_count, s);
+  return vec ? launch<Bf16, true>(a, sm_count, s) : launch<Bf16, false>(a, sm_count, s);
 }
 
 }  // namespace psopt

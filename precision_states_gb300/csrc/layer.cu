@@ -204,7 +204,9 @@ int opt_dequantize(const opt_dequantize_args* a, void* stream) {
   PS_TRY(check_kept(a->d_codes_t, a->codes_t_pitch, a->d_scales_t, a->cols, a->rows));
   if (a->d_x == nullptr && a->d_codes_t == nullptr) return OPT_EINVAL;
   PS_TRY(check_tiles(a->rows, a->cols));
-  return status_of(launch_dequantize(*a, static_cast<cudaStream_t>(stream)));
+  int sms = 0;
+  PS_TRY(sm_count_of(&sms));
+  return status_of(launch_dequantize(*a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 int opt_gated(const opt_gated_args* a, void* stream) {

@@ -24,7 +24,7 @@ cudaError_t launch_rms_norm(const opt_rms_norm_args& a, const DropArgs& d, int s
 cudaError_t launch_rms_norm_backward(const opt_rms_norm_backward_args& a, const DropArgs& d, int sm_count,
                                      cudaStream_t s);
 cudaError_t launch_quantize(const opt_quantize_args& a, cudaStream_t s);
-cudaError_t launch_dequantize(const opt_dequantize_args& a, cudaStream_t s);
+cudaError_t launch_dequantize(const opt_dequantize_args& a, int sm_count, cudaStream_t s);
 cudaError_t launch_gated(const opt_gated_args& a, int sm_count, cudaStream_t s);
 cudaError_t launch_gated_backward(const opt_gated_backward_args& a, int sm_count, cudaStream_t s);
 cudaError_t launch_head_norm(const opt_head_norm_args& a, int sm_count, cudaStream_t s);
