@@ -12,7 +12,9 @@
 // that the weight (and the weight's gradient) stay in registers, and the row's cosines and
 // sines serve all of the set.  Heads of other sizes and places take a form of a warp per
 // head, through shared memory.
-#include "layer.cuh"
+#include <type_traits>
+
+#include "tile.cuh"
 
 namespace psopt {
 namespace {
@@ -195,7 +197,176 @@ __global__ void __launch_bounds__(kThreads, 2) head_norm_kernel(const __grid_con
   }
 }
 
-// Partial sums of the weights' gradients: a CTA's row of 2 x dim, queries' first.
+// ---------------------------------------------- heads of 8, 16, ... 256 elements
+// Such heads fill a warp's 256 columns, so a set is 256 U columns of its side and a lane's
+// chunks are 256 apart.  The next row's chunk is asked for as soon as this row's is taken.
+
+// Eight elements of the weight, of either type.
+__device__ __forceinline__ void weight8(const void* weight, int32_t type, int e, float (&w)[8]) {
+  if (type == OPT_F32) unpack(load_raw<true>(static_cast<const float*>(weight) + e, 8), w);
+  else unpack(load_raw<true>(static_cast<const Bf16*>(weight) + e, 8), w);
+}
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v, int lanes) {
+  if constexpr (LANES == 0) return group_sum(v, lanes);
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+// Cosines and sines of a lane's elements at position `at`: for halves one of each element,
+// for neighbours one of each pair (the first four).  Elements from `rot` on get 1 and 0.
+template <bool INTERLEAVED>
+__device__ __forceinline__ void angles(const float* cos, const float* sin, int64_t at, int64_t table, int rot, int dim, int pair, bool on,
+                                       float (&c)[8], float (&s)[8]) {
+  constexpr int N = INTERLEAVED ? 4 : 8;
+  const bool there = (uint64_t)at < (uint64_t)table;      // of the whole warp
+#pragma unroll
+  for (int k = 0; k < N; k += 4) {
+    const int64_t p = at * (rot >> 1) + pair + k;
+    const uint4 cv = load_words_if(cos + p, on && there), sv = load_words_if(sin + p, on && there);
+    c[k] = u2f(cv.x); c[k + 1] = u2f(cv.y); c[k + 2] = u2f(cv.z); c[k + 3] = u2f(cv.w);
+    s[k] = u2f(sv.x); s[k + 1] = u2f(sv.y); s[k + 2] = u2f(sv.z); s[k + 3] = u2f(sv.w);
+  }
+  if (rot < dim || !there) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      c[k] = !on ? 1.0f : there ? c[k] : u2f(0x7FC00000u);
+      s[k] = on && !there ? u2f(0x7FC00000u) : s[k];
+    }
+  }
+  if constexpr (INTERLEAVED) {
+#pragma unroll
+    for (int k = 3; k >= 0; --k) {
+      c[2 * k] = c[2 * k + 1] = c[k];
+      s[2 * k] = s[2 * k + 1] = s[k];
+    }
+  }
+}
+// What a lane of a dense set is: its first column, element and partner.
+struct Strip {
+  uint32_t column;               // in the side
+  int e, pair, partner;
+  bool keys, rotated;
+  uint32_t row;
+};
+template <int U>
+__device__ __forceinline__ Strip strip_of(const Sets& sets, int dim, int rot, bool interleaved) {
+  Strip l;
+  const int lane = threadIdx.x & 31, half = rot >> 1;
+  const uint32_t warp = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int set = (int)(warp % (uint32_t)sets.sets);
+  l.row = warp < (uint32_t)sets.warps ? warp / (uint32_t)sets.sets : 0xFFFFFFFFu;
+  l.keys = set >= sets.q_sets;
+  l.column = (uint32_t)(l.keys ? set - sets.q_sets : set) * (256 * U) + 8 * lane;
+  l.e = (8 * lane) & (dim - 1);
+  l.rotated = l.e < rot;
+  l.pair = interleaved ? l.e >> 1 : l.e < half ? l.e : l.e - half;
+  l.partner = !l.rotated ? lane : lane + (l.e < half ? half >> 3 : -(half >> 3));
+  return l;
+}
+
+template <typename T, bool INTERLEAVED, bool KEEP, int LANES, int U>
+__global__ void __launch_bounds__(kThreads, 3) head_norm_strip_kernel(const __grid_constant__ opt_head_norm_args a, const Sets sets) {
+  const int dim = (int)a.dim, rot = (int)a.rot;
+  const Strip l = strip_of<U>(sets, dim, rot, INTERLEAVED);
+  const uint32_t rows = (uint32_t)a.rows, stride = (uint32_t)sets.stride;
+  if (l.row >= rows) return;
+  const Side side = side_of(a, l.keys);
+  const float inv_dim = 1.0f / (float)dim;
+  float w[8], wp[8];
+  weight8(side.weight, a.weight_dtype, l.e, w);
+  weight8(side.weight, a.weight_dtype, INTERLEAVED ? l.e : (8 * l.partner) & (dim - 1), wp);
+  // the partner's weight with the sign of its term: minus for a pair's first element
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const float lo = wp[INTERLEAVED ? j + 1 : j], hi = wp[INTERLEAVED ? j : j + 1];
+    const bool first = l.e < (rot >> 1);
+    wp[j] = INTERLEAVED || first ? -lo : lo;
+    wp[j + 1] = !INTERLEAVED && first ? -hi : hi;
+  }
+  const T* x_at = static_cast<const T*>(side.x) + (l.row * side.x_pitch + l.column);
+  T* y_at = static_cast<T*>(side.out) + (l.row * side.out_pitch + l.column);
+  uint8_t* codes_at = static_cast<uint8_t*>(side.codes) + (l.row * side.codes_pitch + l.column);
+  const int64_t x_step = stride * side.x_pitch, y_step = stride * side.out_pitch, codes_step = stride * side.codes_pitch;
+  const uint32_t panel = 512 * (uint32_t)((side.cols + 511) / 512), place = 512 * (l.column >> 9) + ((l.column >> 7) & 3);
+  const uint32_t left = (uint32_t)side.cols - min(l.column, (uint32_t)side.cols);      // chunk k exists where 256 k is below
+  const bool keep = KEEP && side.codes != nullptr;
+  Raw<T> x[U];
+#pragma unroll
+  for (int k = 0; k < U; ++k) x[k] = load_if(x_at + 256 * k, 256 * k < left);
+  int64_t at = rot > 0 && a.d_positions != nullptr ? a.d_positions[l.row] : (int64_t)l.row;
+  for (uint32_t r = l.row; r < rows; r += stride) {
+    const bool more = r + stride < rows;
+    float c[8], s[8];
+    if (rot > 0) {
+      angles<INTERLEAVED>(a.d_cos, a.d_sin, at, a.positions, rot, dim, l.pair, l.rotated, c, s);
+      times8(c, w);
+      times8(s, wp);
+      at = a.d_positions == nullptr ? at + stride : more ? a.d_positions[r + stride] : 0;
+    }
+    x_at += x_step;
+    const uint64_t scale_at = (uint64_t)(r >> 7) * panel + (place + 16 * (r & 31) + ((r >> 3) & 12));
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const Raw<T> raw = x[k];
+      const bool on = 256 * k < left;
+      x[k] = load_if(x_at + 256 * k, on && more);
+      float v[8], y[8];
+      unpack(raw, v);
+      f2_t sums = 0;                    // +0 in both lanes
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        const f2_t t = pk(v[j], v[j + 1]);
+        sums = fma2(t, t, sums);
+      }
+      float sum, second;
+      unpk(sums, sum, second);
+      const float rstd = reciprocal_root(fmaf(lanes_sum<LANES>(sum + second, sets.lanes), inv_dim, a.eps));
+      const f2_t scale = pk(rstd, rstd);
+      if (rot > 0) {
+        float p[8];
+        unpack(partner_of<INTERLEAVED>(raw, l.partner), p);
+#pragma unroll
+        for (int j = 0; j < 8; j += 2)
+          unpk(mul2(fma2(pk(v[j], v[j + 1]), pk(c[j], c[j + 1]), mul2(pk(p[j], p[j + 1]), pk(s[j], s[j + 1]))), scale), y[j], y[j + 1]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) unpk(mul2(mul2(pk(v[j], v[j + 1]), pk(w[j], w[j + 1])), scale), y[j], y[j + 1]);
+      }
+      store8_if(y_at + 256 * k, y, on);
+      if (keep) {
+        const uint32_t top = top16(top_of(magnitudes(raw, false)));
+        // blocks 2 k and 2 k + 1 of the strip
+        uint8_t* to = static_cast<uint8_t*>(side.code_scales) + scale_at + (512 * (k >> 1) + 2 * (k & 1));
+        if (__any_sync(0xFFFFFFFFu, top >= kInfBits)) put_codes8(codes_at + 256 * k, to, 0, on ? 8 : 0, v);
+        else put_finite_if(codes_at + 256 * k, to, v, top, on, on && (threadIdx.x & 15) == 0);
+      }
+    }
+    y_at += y_step;
+    codes_at += codes_step;
+  }
+}
+
+// A CTA's row of the partial sums, 2 x dim with queries' first: over the warps that had a side,
+// and the heads side by side in them, in order.
+__device__ __forceinline__ void leave_sums(float (&sums)[kWarps][32][8], const float (&dw)[8], const Sets& sets, int dim, float* parts) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sums[threadIdx.x >> 5][threadIdx.x & 31][j] = dw[j];
+  __syncthreads();
+  float* out = parts + (int64_t)blockIdx.x * 2 * dim;
+  for (int t = threadIdx.x; t < 2 * dim; t += kThreads) {
+    const bool keys = t >= dim;
+    const int e = keys ? t - dim : t;
+    float v = 0.0f;
+    for (int k = 0; k < kWarps; ++k) {
+      const int64_t warp = (int64_t)blockIdx.x * kWarps + k;
+      if (warp >= sets.warps || ((int)(warp % sets.sets) >= sets.q_sets) != keys) continue;
+      for (int i = 0; i < sets.slots; ++i) v += sums[k][i * sets.lanes + (e >> 3)][e & 7];
+    }
+    out[t] = v;
+  }
+}
+
 template <typename T, typename S, typename W, bool INTERLEAVED, int U>
 __global__ void __launch_bounds__(kThreads, 2) head_norm_backward_kernel(const __grid_constant__ opt_head_norm_backward_args a,
                                                                         Sets sets, float* parts) {
@@ -251,23 +422,109 @@ __global__ void __launch_bounds__(kThreads, 2) head_norm_backward_kernel(const _
       }
     }
   }
-  if (parts == nullptr) return;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) sums[threadIdx.x >> 5][threadIdx.x & 31][j] = dw[j];
-  __syncthreads();
-  // element t of a side: over the warps that had it, and the heads side by side, in order
-  float* out = parts + (int64_t)blockIdx.x * 2 * dim;
-  for (int t = threadIdx.x; t < 2 * dim; t += kThreads) {
-    const bool keys = t >= dim;
-    const int e = keys ? t - dim : t;
-    float v = 0.0f;
-    for (int k = 0; k < kWarps; ++k) {
-      const int64_t warp = (int64_t)blockIdx.x * kWarps + k;
-      if (warp >= sets.warps || ((int)(warp % sets.sets) >= sets.q_sets) != keys) continue;
-      for (int i = 0; i < sets.slots; ++i) v += sums[k][i * sets.lanes + (e >> 3)][e & 7];
+  if (parts != nullptr) leave_sums(sums, dw, sets, dim, parts);
+}
+
+// The gradients of dense sets.
+template <typename T, typename S, bool INTERLEAVED, int LANES, int U>
+__global__ void __launch_bounds__(kThreads, 2) head_norm_backward_strip_kernel(const __grid_constant__ opt_head_norm_backward_args a,
+                                                                              const Sets sets, float* parts) {
+  __shared__ float sums[kWarps][32][8];
+  constexpr bool KEPT = sizeof(S) == 1;
+  const int dim = (int)a.dim, rot = (int)a.rot;
+  const Strip l = strip_of<U>(sets, dim, rot, INTERLEAVED);
+  const uint32_t rows = (uint32_t)a.rows, stride = (uint32_t)sets.stride;
+  const Side side = side_of(a, l.keys);
+  const float inv_dim = 1.0f / (float)dim;
+  float w[8] = {};
+  f2_t dw[4] = {};                 // +0 in both lanes
+  if (l.row < rows) weight8(side.weight, a.weight_dtype, l.e, w);
+  using X = std::conditional_t<KEPT, uint8_t, T>;
+  const T* d_at = static_cast<const T*>(side.dout) + (l.row * side.dout_pitch + l.column);
+  const X* x_at = static_cast<const X*>(side.x) + (l.row * side.x_pitch + l.column);
+  T* out_at = static_cast<T*>(side.out) + (l.row * side.out_pitch + l.column);
+  const int64_t d_step = stride * side.dout_pitch, x_step = stride * side.x_pitch, out_step = stride * side.out_pitch;
+  const uint32_t panel = 512 * (uint32_t)((side.cols + 511) / 512), place = 512 * (l.column >> 9) + ((l.column >> 7) & 3);
+  const uint32_t left = (uint32_t)side.cols - min(l.column, (uint32_t)side.cols);
+  // the turn back: plus for a pair's first element
+  const float sign = !INTERLEAVED && l.e >= (rot >> 1) ? -1.0f : 1.0f;
+  const f2_t signs = pk(sign, INTERLEAVED ? -1.0f : sign);
+  Raw<T> d[U];
+  std::conditional_t<KEPT, KeptAsk, Raw<T>> x[U];
+  const auto load = [&](int k, uint32_t r, bool on) {
+    d[k] = load_if(d_at + 256 * k, on);
+    if constexpr (KEPT) {
+      const uint64_t scale_at = (uint64_t)(r >> 7) * panel + (place + 16 * (r & 31) + ((r >> 3) & 12));
+      x[k].codes = load_codes_if(x_at + 256 * k, on);
+      x[k].byte = load_byte_if(static_cast<const uint8_t*>(side.scales) + scale_at + (512 * (k >> 1) + 2 * (k & 1)), on);
+    } else {
+      x[k] = load_if(x_at + 256 * k, on);
     }
-    out[t] = v;
+  };
+  int64_t at = 0;
+  if (l.row < rows) {
+#pragma unroll
+    for (int k = 0; k < U; ++k) load(k, l.row, 256 * k < left);
+    at = rot > 0 && a.d_positions != nullptr ? a.d_positions[l.row] : (int64_t)l.row;
   }
+  for (uint32_t r = l.row; r < rows; r += stride) {
+    const bool more = r + stride < rows;
+    float c[8], s[8];
+    if (rot > 0) {
+      angles<INTERLEAVED>(a.d_cos, a.d_sin, at, a.positions, rot, dim, l.pair, l.rotated, c, s);
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) unpk(mul2(pk(s[j], s[j + 1]), signs), s[j], s[j + 1]);
+      at = a.d_positions == nullptr ? at + stride : more ? a.d_positions[r + stride] : 0;
+    }
+    d_at += d_step;
+    x_at += x_step;
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const Raw<T> raw = d[k];
+      float v[8], g[8];
+      if constexpr (KEPT) values8(x[k].codes, scale_of(x[k].byte), v);
+      else unpack(x[k], v);
+      const bool on = 256 * k < left;
+      load(k, r + stride, on && more);
+      unpack(raw, g);
+      if (rot > 0) {
+        float p[8];
+        unpack(partner_of<INTERLEAVED>(raw, l.partner), p);
+#pragma unroll
+        for (int j = 0; j < 8; j += 2)
+          unpk(fma2(pk(g[j], g[j + 1]), pk(c[j], c[j + 1]), mul2(pk(p[j], p[j + 1]), pk(s[j], s[j + 1]))), g[j], g[j + 1]);
+      }
+      f2_t squares = 0, dots = 0, t[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const f2_t xv = pk(v[2 * j], v[2 * j + 1]);
+        squares = fma2(xv, xv, squares);
+        t[j] = mul2(pk(g[2 * j], g[2 * j + 1]), pk(w[2 * j], w[2 * j + 1]));
+        dots = fma2(t[j], xv, dots);
+      }
+      float square, dot, more_square, more_dot;
+      unpk(squares, square, more_square);
+      unpk(dots, dot, more_dot);
+      square = lanes_sum<LANES>(square + more_square, sets.lanes);
+      dot = lanes_sum<LANES>(dot + more_dot, sets.lanes);
+      const float rstd = reciprocal_root(fmaf(square, inv_dim, a.eps)), pull = -rstd * rstd * (dot * inv_dim);
+      float out[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const f2_t xv = pk(v[2 * j], v[2 * j + 1]);
+        const f2_t term = mul2(pk(g[2 * j], g[2 * j + 1]), mul2(xv, pk(rstd, rstd)));
+        if (on) dw[j] = add2(dw[j], term);
+        unpk(mul2(fma2(xv, pk(pull, pull), t[j]), pk(rstd, rstd)), out[2 * j], out[2 * j + 1]);
+      }
+      store8_if(out_at + 256 * k, out, on);
+    }
+    out_at += out_step;
+  }
+  if (parts == nullptr) return;
+  float sum[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) unpk(dw[j], sum[2 * j], sum[2 * j + 1]);
+  leave_sums(sums, sum, sets, dim, parts);
 }
 
 // ------------------------------------------------------- heads of any size and place
@@ -464,6 +721,28 @@ cudaError_t forward_heads(const opt_head_norm_args& a, int sm_count, cudaStream_
   return cudaGetLastError();
 }
 
+// U heads' chunks after one another: what the registers hold.
+template <typename T>
+constexpr int kStripChunks = sizeof(T) == 2 ? 4 : 2;
+
+template <typename T, bool INTERLEAVED, bool KEEP, int LANES>
+cudaError_t forward_strip(const opt_head_norm_args& a, int sm_count, cudaStream_t s) {
+  static OccupancyCache cache;
+  const auto kernel = head_norm_strip_kernel<T, INTERLEAVED, KEEP, LANES, kStripChunks<T>>;
+  int ctas;
+  const Sets sets = sets_of(a, kStripChunks<T>, (int64_t)sm_count * cached_occupancy(kernel, cache, kThreads, 0), &ctas);
+  kernel<<<ctas, kThreads, 0, s>>>(a, sets);
+  return cudaGetLastError();
+}
+template <typename T, bool INTERLEAVED, bool KEEP>
+cudaError_t forward_strips(const opt_head_norm_args& a, int sm_count, cudaStream_t s) {
+  switch (a.dim) {
+    case 64: return forward_strip<T, INTERLEAVED, KEEP, 8>(a, sm_count, s);
+    case 128: return forward_strip<T, INTERLEAVED, KEEP, 16>(a, sm_count, s);
+    default: return forward_strip<T, INTERLEAVED, KEEP, 0>(a, sm_count, s);
+  }
+}
+
 cudaError_t keep(const void* x, int64_t x_pitch, void* codes, void* scales, int64_t pitch, int64_t rows, int64_t cols,
                  int32_t dtype, cudaStream_t s) {
   if (codes == nullptr || cols == 0) return cudaSuccess;
@@ -501,9 +780,13 @@ cudaError_t forward(const opt_head_norm_args& a, int sm_count, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     b.d_q_codes = b.d_k_codes = nullptr;
   }
-  if (v.ok) {
-    return a.flags & OPT_HEADS_INTERLEAVED ? forward_heads<T, W, true>(b, sm_count, s) : forward_heads<T, W, false>(b, sm_count, s);
+  if (v.ok && (a.dim & (a.dim - 1)) == 0) {
+    const bool kept = b.d_q_codes != nullptr || b.d_k_codes != nullptr;
+    if (a.flags & OPT_HEADS_INTERLEAVED)
+      return kept ? forward_strips<T, true, true>(b, sm_count, s) : forward_strips<T, true, false>(b, sm_count, s);
+    return kept ? forward_strips<T, false, true>(b, sm_count, s) : forward_strips<T, false, false>(b, sm_count, s);
   }
+  if (v.ok) return a.flags & OPT_HEADS_INTERLEAVED ? forward_heads<T, W, true>(b, sm_count, s) : forward_heads<T, W, false>(b, sm_count, s);
   const int64_t need = (a.rows * (a.q_heads + a.k_heads) + kAnyWarps - 1) / kAnyWarps, most = (int64_t)sm_count * 12;
   head_norm_any_kernel<T, W><<<(unsigned)(need < most ? need : most), 32 * kAnyWarps, 0, s>>>(b);
   return cudaGetLastError();
@@ -527,6 +810,26 @@ cudaError_t backward_any(const opt_head_norm_backward_args& a, int sm_count, flo
   const int q_ctas = ctas_of(a.q_heads), ctas = q_ctas + ctas_of(a.k_heads);
   head_norm_backward_any_kernel<T, S, W><<<(unsigned)ctas, 32 * kAnyWarps, 0, s>>>(a, q_ctas, parts);
   return weight_sums(a, ctas, s);
+}
+
+template <typename T, typename S, bool INTERLEAVED, int LANES>
+cudaError_t backward_strip(const opt_head_norm_backward_args& a, int sm_count, float* parts, cudaStream_t s) {
+  static OccupancyCache cache;
+  const auto kernel = head_norm_backward_strip_kernel<T, S, INTERLEAVED, LANES, kStripChunks<T>>;
+  int64_t most = (int64_t)sm_count * cached_occupancy(kernel, cache, kThreads, 0);
+  if (most > kHeadBackwardMaxCtas) most = kHeadBackwardMaxCtas;
+  int ctas;
+  const Sets sets = sets_of(a, kStripChunks<T>, most, &ctas);
+  kernel<<<ctas, kThreads, 0, s>>>(a, sets, parts);
+  return weight_sums(a, ctas, s);
+}
+template <typename T, typename S, bool INTERLEAVED>
+cudaError_t backward_strips(const opt_head_norm_backward_args& a, int sm_count, float* parts, cudaStream_t s) {
+  switch (a.dim) {
+    case 64: return backward_strip<T, S, INTERLEAVED, 8>(a, sm_count, parts, s);
+    case 128: return backward_strip<T, S, INTERLEAVED, 16>(a, sm_count, parts, s);
+    default: return backward_strip<T, S, INTERLEAVED, 0>(a, sm_count, parts, s);
+  }
 }
 
 template <typename T, typename S, typename W, bool INTERLEAVED>
@@ -558,6 +861,9 @@ cudaError_t backward_from(const opt_head_norm_backward_args& a, int sm_count, cu
     v.see(a.d_dk, a.dk_pitch, sizeof(T));
   }
   float* parts = a.d_dq_weight != nullptr || a.d_dk_weight != nullptr ? static_cast<float*>(a.d_workspace) : nullptr;
+  // (more sets than the workspace has rows of CTAs for go by single heads)
+  if (v.ok && (a.dim & (a.dim - 1)) == 0 && (a.q_heads + a.k_heads) * a.dim <= kHeadBackwardMaxCtas * kWarps * 256)
+    return a.flags & OPT_HEADS_INTERLEAVED ? backward_strips<T, S, true>(a, sm_count, parts, s) : backward_strips<T, S, false>(a, sm_count, parts, s);
   if (v.ok)
     return a.flags & OPT_HEADS_INTERLEAVED ? backward_heads<T, S, W, true>(a, sm_count, parts, s)
                                            : backward_heads<T, S, W, false>(a, sm_count, parts, s);
