@@ -92,23 +92,6 @@ __device__ __forceinline__ void activation8(const float (&g)[8], float (&f)[8], 
 __device__ __forceinline__ int64_t first_row() { return (int64_t)blockIdx.y * blockDim.y + threadIdx.y; }
 __device__ __forceinline__ int warp_of_block() { return (int)(threadIdx.y * blockDim.x + threadIdx.x) >> 5; }
 
-// The largest magnitudes of two 1 x 128 blocks that 16 lanes hold chunks of, by whole warps:
-// BF16's go through the exchanges together.
-__device__ __forceinline__ void tops16(uint32_t& a, uint32_t& b, Bf16) {
-  uint32_t both = a | b >> 16;
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) both = larger(both, __shfl_xor_sync(0xFFFFFFFFu, both, o), Bf16());
-  a = both & 0xFFFF0000u;
-  b = both << 16;
-}
-__device__ __forceinline__ void tops16(uint32_t& a, uint32_t& b, float) {
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) {
-    a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
-    b = max(b, __shfl_xor_sync(0xFFFFFFFFu, b, o));
-  }
-}
-
 // What is written in 8 bits of a chunk of row r at column c: y, and the inputs that are kept.
 // By whole warps; elements from `valid` on are 0.
 template <typename T>

@@ -22,23 +22,61 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kAnyWarps = 4;                     // of the form for any heads: 12 KB of shared memory to a warp
 
-// One side's pointers (queries or keys) out of either call's arguments.
+// Chunks of a lane after one another, and CTAs to an SM: what the registers hold.
+template <typename T>
+constexpr int kForwardChunks = sizeof(T) == 2 ? 4 : 2;
+template <typename T>
+constexpr int kBackwardChunks = sizeof(T) == 2 ? 4 : 2;
+constexpr int kForwardCtas = 3, kBackwardCtas = 2;
+
+// One side's matrices, queries' or keys'.
 struct Side {
   const void *x, *scales, *dout, *weight;
   void *out, *codes, *code_scales;
   int64_t x_pitch, dout_pitch, out_pitch, codes_pitch, cols, heads;
 };
-__device__ __forceinline__ Side side_of(const opt_head_norm_args& a, bool keys) {
-  return keys ? Side{a.d_k, nullptr, nullptr, a.d_k_weight, a.d_k_out, a.d_k_codes, a.d_k_scales, a.k_pitch, 0, a.k_out_pitch,
-                     a.k_codes_pitch, a.k_heads * a.dim, a.k_heads}
-              : Side{a.d_q, nullptr, nullptr, a.d_q_weight, a.d_q_out, a.d_q_codes, a.d_q_scales, a.q_pitch, 0, a.q_out_pitch,
-                     a.q_codes_pitch, a.q_heads * a.dim, a.q_heads};
+// Either call as the kernels take it: sides by number (0: queries), which a CTA or a warp picks
+// out of its arguments by an index.
+struct HeadCall {
+  Side side[2];
+  const float *cos, *sin;
+  const int64_t* positions;
+  int64_t rows, table;
+  int dim, rot;
+  int32_t weight_dtype;
+  bool interleaved;
+  float eps;
+};
+template <typename A>
+HeadCall shared_call(const A& a) {
+  HeadCall c = {};
+  c.cos = a.d_cos;
+  c.sin = a.d_sin;
+  c.positions = a.d_positions;
+  c.rows = a.rows;
+  c.table = a.positions;
+  c.dim = (int)a.dim;
+  c.rot = (int)a.rot;
+  c.weight_dtype = a.weight_dtype;
+  c.interleaved = (a.flags & OPT_HEADS_INTERLEAVED) != 0;
+  c.eps = a.eps;
+  return c;
 }
-__device__ __forceinline__ Side side_of(const opt_head_norm_backward_args& a, bool keys) {
-  return keys ? Side{a.d_k, a.d_k_scales, a.d_dk_out, a.d_k_weight, a.d_dk, nullptr, nullptr, a.k_pitch, a.dk_out_pitch,
-                     a.dk_pitch, 0, a.k_heads * a.dim, a.k_heads}
-              : Side{a.d_q, a.d_q_scales, a.d_dq_out, a.d_q_weight, a.d_dq, nullptr, nullptr, a.q_pitch, a.dq_out_pitch,
-                     a.dq_pitch, 0, a.q_heads * a.dim, a.q_heads};
+HeadCall call_of(const opt_head_norm_args& a) {
+  HeadCall c = shared_call(a);
+  c.side[0] = {a.d_q, nullptr, nullptr, a.d_q_weight, a.d_q_out, a.d_q_codes, a.d_q_scales, a.q_pitch, 0, a.q_out_pitch,
+               a.q_codes_pitch, a.q_heads * a.dim, a.q_heads};
+  c.side[1] = {a.d_k, nullptr, nullptr, a.d_k_weight, a.d_k_out, a.d_k_codes, a.d_k_scales, a.k_pitch, 0, a.k_out_pitch,
+               a.k_codes_pitch, a.k_heads * a.dim, a.k_heads};
+  return c;
+}
+HeadCall call_of(const opt_head_norm_backward_args& a) {
+  HeadCall c = shared_call(a);
+  c.side[0] = {a.d_q, a.d_q_scales, a.d_dq_out, a.d_q_weight, a.d_dq, nullptr, nullptr, a.q_pitch, a.dq_out_pitch, a.dq_pitch, 0,
+               a.q_heads * a.dim, a.q_heads};
+  c.side[1] = {a.d_k, a.d_k_scales, a.d_dk_out, a.d_k_weight, a.d_dk, nullptr, nullptr, a.k_pitch, a.dk_out_pitch, a.dk_pitch, 0,
+               a.k_heads * a.dim, a.k_heads};
+  return c;
 }
 
 // Sum over a group of `lanes` (a power of two) lanes.
@@ -146,11 +184,11 @@ __device__ __forceinline__ Lane lane_of(const Sets& sets, int dim, int rot, int 
 
 // Row r, element e of the head: the column.
 template <typename T, typename W, bool INTERLEAVED, int U>
-__global__ void __launch_bounds__(kThreads, 2) head_norm_kernel(const __grid_constant__ opt_head_norm_args a, Sets sets) {
-  const int dim = (int)a.dim, rot = (int)a.rot;
+__global__ void __launch_bounds__(kThreads, 2) head_norm_kernel(const __grid_constant__ HeadCall a, Sets sets) {
+  const int dim = a.dim, rot = a.rot;
   const Lane l = lane_of(sets, dim, rot, U);
   if (l.first_row >= a.rows) return;
-  const Side side = side_of(a, l.keys);
+  const Side& side = a.side[l.keys];
   const int64_t panel = (side.cols + 511) / 512;
   const float inv_dim = 1.0f / (float)dim;
   float w[8] = {}, wp[8] = {};
@@ -172,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 2) head_norm_kernel(const __grid_con
       if (l.on && h < side.heads) x[k] = load_raw<true>(static_cast<const T*>(side.x) + r * side.x_pitch + h * dim + l.e, 8);
     }
     float c[8], s[8];
-    turn_of<INTERLEAVED>(a.d_cos, a.d_sin, a.d_positions, a.positions, rot, r, l.e, c, s);
+    turn_of<INTERLEAVED>(a.cos, a.sin, a.positions, a.table, rot, r, l.e, c, s);
     times8(c, w);
     times8(s, wp);
 #pragma unroll
@@ -213,115 +251,151 @@ __device__ __forceinline__ float lanes_sum(float v, int lanes) {
   for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
 }
-// Cosines and sines of a lane's elements at position `at`: for halves one of each element,
-// for neighbours one of each pair (the first four).  Elements from `rot` on get 1 and 0.
-template <bool INTERLEAVED>
-__device__ __forceinline__ void angles(const float* cos, const float* sin, int64_t at, int64_t table, int rot, int dim, int pair, bool on,
-                                       float (&c)[8], float (&s)[8]) {
-  constexpr int N = INTERLEAVED ? 4 : 8;
-  const bool there = (uint64_t)at < (uint64_t)table;      // of the whole warp
+// N of them, their exchanges side by side.
+template <int LANES, int N>
+__device__ __forceinline__ void lanes_sums(float (&v)[N], int lanes) {
 #pragma unroll
-  for (int k = 0; k < N; k += 4) {
-    const int64_t p = at * (rot >> 1) + pair + k;
-    const uint4 cv = load_words_if(cos + p, on && there), sv = load_words_if(sin + p, on && there);
-    c[k] = u2f(cv.x); c[k + 1] = u2f(cv.y); c[k + 2] = u2f(cv.z); c[k + 3] = u2f(cv.w);
-    s[k] = u2f(sv.x); s[k + 1] = u2f(sv.y); s[k + 2] = u2f(sv.z); s[k + 3] = u2f(sv.w);
-  }
-  if (rot < dim || !there) {
+  for (int o = 16; o > 0; o >>= 1) {
+    if (LANES > 0 ? o < LANES : o < lanes) {
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-      c[k] = !on ? 1.0f : there ? c[k] : u2f(0x7FC00000u);
-      s[k] = on && !there ? u2f(0x7FC00000u) : s[k];
-    }
-  }
-  if constexpr (INTERLEAVED) {
-#pragma unroll
-    for (int k = 3; k >= 0; --k) {
-      c[2 * k] = c[2 * k + 1] = c[k];
-      s[2 * k] = s[2 * k + 1] = s[k];
+      for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
     }
   }
 }
-// What a lane of a dense set is: its first column, element and partner.
-struct Strip {
-  uint32_t column;               // in the side
-  int e, pair, partner;
-  bool keys, rotated;
-  uint32_t row;
+// Cosines and sines of a lane's elements at position `at`: for halves one of each element,
+// for neighbours one of each pair.  Asked for, and later made eight factors: elements from `rot`
+// on get 1 and 0, those of a position outside the tables NaN.
+template <bool INTERLEAVED>
+struct Angles {
+  static constexpr int N = INTERLEAVED ? 1 : 2;
+  uint4 cos[N], sin[N];
+  bool there;                    // of the whole warp
+  __device__ __forceinline__ void ask(const float* cos_table, const float* sin_table, int64_t at, int64_t table, int rot, int pair, bool on) {
+    there = (uint64_t)at < (uint64_t)table;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int64_t p = at * (rot >> 1) + pair + 4 * k;
+      cos[k] = load_words_if(cos_table + p, on && there);
+      sin[k] = load_words_if(sin_table + p, on && there);
+    }
+  }
+  __device__ __forceinline__ void factors(int rot, int dim, bool on, float (&c)[8], float (&s)[8]) const {
+    const uint32_t cw[8] = {cos[0].x, cos[0].y, cos[0].z, cos[0].w, cos[N - 1].x, cos[N - 1].y, cos[N - 1].z, cos[N - 1].w};
+    const uint32_t sw[8] = {sin[0].x, sin[0].y, sin[0].z, sin[0].w, sin[N - 1].x, sin[N - 1].y, sin[N - 1].z, sin[N - 1].w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      c[j] = u2f(cw[INTERLEAVED ? j >> 1 : j]);
+      s[j] = u2f(sw[INTERLEAVED ? j >> 1 : j]);
+    }
+    if (rot < dim || !there) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        c[j] = !on ? 1.0f : there ? c[j] : u2f(0x7FC00000u);
+        s[j] = on && !there ? u2f(0x7FC00000u) : s[j];
+      }
+    }
+  }
+};
+// How CTAs share strips: CTA b takes strip b mod (strips), and of its rows a warp each
+// (b / strips) * kWarps + warp, and `stride` on.  Strips of queries come first.
+struct Strips {
+  int q_strips, strips;
+  uint32_t stride;
+  int lanes;                     // lanes to a head
+};
+// What a lane is in its strip.
+struct StripLane {
+  uint32_t column;               // its first, in the side
+  uint32_t row;                  // its warp's first
+  int e, pair, partner;          // of its first element: in the head, its angle; the lane with the partners
+  bool rotated;
 };
 template <int U>
-__device__ __forceinline__ Strip strip_of(const Sets& sets, int dim, int rot, bool interleaved) {
-  Strip l;
+__device__ __forceinline__ StripLane strip_lane(const Strips& strips, int strip, int dim, int rot, bool interleaved) {
+  StripLane l;
   const int lane = threadIdx.x & 31, half = rot >> 1;
-  const uint32_t warp = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int set = (int)(warp % (uint32_t)sets.sets);
-  l.row = warp < (uint32_t)sets.warps ? warp / (uint32_t)sets.sets : 0xFFFFFFFFu;
-  l.keys = set >= sets.q_sets;
-  l.column = (uint32_t)(l.keys ? set - sets.q_sets : set) * (256 * U) + 8 * lane;
+  l.row = (blockIdx.x / (uint32_t)strips.strips) * kWarps + (threadIdx.x >> 5);
+  l.column = (uint32_t)strip * (256 * U) + 8 * lane;
   l.e = (8 * lane) & (dim - 1);
   l.rotated = l.e < rot;
   l.pair = interleaved ? l.e >> 1 : l.e < half ? l.e : l.e - half;
   l.partner = !l.rotated ? lane : lane + (l.e < half ? half >> 3 : -(half >> 3));
   return l;
 }
+__device__ __forceinline__ void shared8(const float* p, float (&x)[8]) {
+  const float4 lo = *reinterpret_cast<const float4*>(p), hi = *reinterpret_cast<const float4*>(p + 4);
+  x[0] = lo.x; x[1] = lo.y; x[2] = lo.z; x[3] = lo.w;
+  x[4] = hi.x; x[5] = hi.y; x[6] = hi.z; x[7] = hi.w;
+}
+__device__ __forceinline__ float weight_at(const void* weight, int32_t type, int e) {
+  return type == OPT_F32 ? static_cast<const float*>(weight)[e] : element(static_cast<const Bf16*>(weight) + e);
+}
+// Scale byte of a row, from its strip's first block on.
+__device__ __forceinline__ uint64_t scale_row(uint32_t r, uint32_t panel512) {
+  return (uint64_t)(r >> 7) * panel512 + (16 * (r & 31) + ((r >> 3) & 12));
+}
 
 template <typename T, bool INTERLEAVED, bool KEEP, int LANES, int U>
-__global__ void __launch_bounds__(kThreads, 3) head_norm_strip_kernel(const __grid_constant__ opt_head_norm_args a, const Sets sets) {
-  const int dim = (int)a.dim, rot = (int)a.rot;
-  const Strip l = strip_of<U>(sets, dim, rot, INTERLEAVED);
-  const uint32_t rows = (uint32_t)a.rows, stride = (uint32_t)sets.stride;
-  if (l.row >= rows) return;
-  const Side side = side_of(a, l.keys);
-  const float inv_dim = 1.0f / (float)dim;
-  float w[8], wp[8];
-  weight8(side.weight, a.weight_dtype, l.e, w);
-  weight8(side.weight, a.weight_dtype, INTERLEAVED ? l.e : (8 * l.partner) & (dim - 1), wp);
-  // the partner's weight with the sign of its term: minus for a pair's first element
-#pragma unroll
-  for (int j = 0; j < 8; j += 2) {
-    const float lo = wp[INTERLEAVED ? j + 1 : j], hi = wp[INTERLEAVED ? j : j + 1];
-    const bool first = l.e < (rot >> 1);
-    wp[j] = INTERLEAVED || first ? -lo : lo;
-    wp[j + 1] = !INTERLEAVED && first ? -hi : hi;
+__global__ void __launch_bounds__(kThreads, kForwardCtas) head_norm_strip_kernel(const __grid_constant__ HeadCall a,
+                                                                                const Strips strips) {
+  // the weight, and its partner's with the sign of the partner's term (minus for a pair's
+  // first element)
+  __shared__ __align__(16) float weight[256], other[256];
+  const int dim = a.dim, rot = a.rot, half = rot >> 1, strip = (int)(blockIdx.x % (uint32_t)strips.strips);
+  const bool keys = strip >= strips.q_strips;
+  const Side& side = a.side[keys];
+  const StripLane l = strip_lane<U>(strips, keys ? strip - strips.q_strips : strip, dim, rot, INTERLEAVED);
+  if ((int)threadIdx.x < dim) {
+    const int e = threadIdx.x, p = e >= rot ? e : INTERLEAVED ? e ^ 1 : e < half ? e + half : e - half;
+    const float v = weight_at(side.weight, a.weight_dtype, p);
+    weight[e] = weight_at(side.weight, a.weight_dtype, e);
+    other[e] = (INTERLEAVED ? (e & 1) == 0 : e < half) ? -v : v;
   }
-  const T* x_at = static_cast<const T*>(side.x) + (l.row * side.x_pitch + l.column);
-  T* y_at = static_cast<T*>(side.out) + (l.row * side.out_pitch + l.column);
-  uint8_t* codes_at = static_cast<uint8_t*>(side.codes) + (l.row * side.codes_pitch + l.column);
-  const int64_t x_step = stride * side.x_pitch, y_step = stride * side.out_pitch, codes_step = stride * side.codes_pitch;
-  const uint32_t panel = 512 * (uint32_t)((side.cols + 511) / 512), place = 512 * (l.column >> 9) + ((l.column >> 7) & 3);
+  __syncthreads();
+  const uint32_t rows = (uint32_t)a.rows, panel = 512 * (uint32_t)((side.cols + 511) / 512);
   const uint32_t left = (uint32_t)side.cols - min(l.column, (uint32_t)side.cols);      // chunk k exists where 256 k is below
+  const uint32_t place = 512 * (l.column >> 9) + ((l.column >> 7) & 3);
+  const float inv_dim = 1.0f / (float)dim;
   const bool keep = KEEP && side.codes != nullptr;
+  if (l.row >= rows) return;
   Raw<T> x[U];
 #pragma unroll
-  for (int k = 0; k < U; ++k) x[k] = load_if(x_at + 256 * k, 256 * k < left);
-  int64_t at = rot > 0 && a.d_positions != nullptr ? a.d_positions[l.row] : (int64_t)l.row;
-  for (uint32_t r = l.row; r < rows; r += stride) {
-    const bool more = r + stride < rows;
-    float c[8], s[8];
+  for (int k = 0; k < U; ++k) x[k] = load_if(static_cast<const T*>(side.x) + (l.row * side.x_pitch + l.column) + 256 * k, 256 * k < left);
+  int64_t at = rot > 0 && a.positions != nullptr ? a.positions[l.row] : (int64_t)l.row;
+  for (uint32_t r = l.row; r < rows; r += strips.stride) {
+    const uint32_t next = r + strips.stride;
+    Angles<INTERLEAVED> angles;
     if (rot > 0) {
-      angles<INTERLEAVED>(a.d_cos, a.d_sin, at, a.positions, rot, dim, l.pair, l.rotated, c, s);
-      times8(c, w);
-      times8(s, wp);
-      at = a.d_positions == nullptr ? at + stride : more ? a.d_positions[r + stride] : 0;
+      angles.ask(a.cos, a.sin, at, a.table, rot, l.pair, l.rotated);
+      at = a.positions == nullptr ? (int64_t)next : next < rows ? a.positions[next] : 0;
     }
-    x_at += x_step;
-    const uint64_t scale_at = (uint64_t)(r >> 7) * panel + (place + 16 * (r & 31) + ((r >> 3) & 12));
+    float c[8], s[8], w[8];
+    shared8(weight + l.e, w);
+    if (rot > 0) {
+      angles.factors(rot, dim, l.rotated, c, s);
+      times8(c, w);
+      shared8(other + l.e, w);
+      times8(s, w);
+    }
+    T* const out = static_cast<T*>(side.out) + (r * side.out_pitch + l.column);
+    uint8_t* const codes = static_cast<uint8_t*>(side.codes) + (r * side.codes_pitch + l.column);
+    uint8_t* const scales = static_cast<uint8_t*>(side.code_scales) + (scale_row(r, panel) + place);
+    const T* const ahead = static_cast<const T*>(side.x) + (next * side.x_pitch + l.column);
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       const Raw<T> raw = x[k];
       const bool on = 256 * k < left;
-      x[k] = load_if(x_at + 256 * k, on && more);
+      x[k] = load_if(ahead + 256 * k, on && next < rows);
       float v[8], y[8];
       unpack(raw, v);
       f2_t sums = 0;                    // +0 in both lanes
 #pragma unroll
-      for (int j = 0; j < 8; j += 2) {
-        const f2_t t = pk(v[j], v[j + 1]);
-        sums = fma2(t, t, sums);
-      }
-      float sum, second;
-      unpk(sums, sum, second);
-      const float rstd = reciprocal_root(fmaf(lanes_sum<LANES>(sum + second, sets.lanes), inv_dim, a.eps));
+      for (int j = 0; j < 8; j += 2) sums = fma2(pk(v[j], v[j + 1]), pk(v[j], v[j + 1]), sums);
+      float sum[1], second;
+      unpk(sums, sum[0], second);
+      sum[0] += second;
+      lanes_sums<LANES, 1>(sum, strips.lanes);
+      const float rstd = reciprocal_root(fmaf(sum[0], inv_dim, a.eps));
       const f2_t scale = pk(rstd, rstd);
       if (rot > 0) {
         float p[8];
@@ -333,17 +407,14 @@ __global__ void __launch_bounds__(kThreads, 3) head_norm_strip_kernel(const __gr
 #pragma unroll
         for (int j = 0; j < 8; j += 2) unpk(mul2(mul2(pk(v[j], v[j + 1]), pk(w[j], w[j + 1])), scale), y[j], y[j + 1]);
       }
-      store8_if(y_at + 256 * k, y, on);
+      store8_if(out + 256 * k, y, on);
       if (keep) {
+        uint8_t* to = scales + (512 * (k >> 1) + 2 * (k & 1));      // blocks 2 k and 2 k + 1 of the strip
         const uint32_t top = top16(top_of(magnitudes(raw, false)));
-        // blocks 2 k and 2 k + 1 of the strip
-        uint8_t* to = static_cast<uint8_t*>(side.code_scales) + scale_at + (512 * (k >> 1) + 2 * (k & 1));
-        if (__any_sync(0xFFFFFFFFu, top >= kInfBits)) put_codes8(codes_at + 256 * k, to, 0, on ? 8 : 0, v);
-        else put_finite_if(codes_at + 256 * k, to, v, top, on, on && (threadIdx.x & 15) == 0);
+        if (__any_sync(0xFFFFFFFFu, top >= kInfBits)) put_codes8(codes + 256 * k, to, 0, on ? 8 : 0, v);
+        else put_finite_if(codes + 256 * k, to, v, top, on, on && (threadIdx.x & 15) == 0);
       }
     }
-    y_at += y_step;
-    codes_at += codes_step;
   }
 }
 
@@ -368,12 +439,12 @@ __device__ __forceinline__ void leave_sums(float (&sums)[kWarps][32][8], const f
 }
 
 template <typename T, typename S, typename W, bool INTERLEAVED, int U>
-__global__ void __launch_bounds__(kThreads, 2) head_norm_backward_kernel(const __grid_constant__ opt_head_norm_backward_args a,
+__global__ void __launch_bounds__(kThreads, 2) head_norm_backward_kernel(const __grid_constant__ HeadCall a,
                                                                         Sets sets, float* parts) {
   __shared__ float sums[kWarps][32][8];
-  const int dim = (int)a.dim, rot = (int)a.rot;
+  const int dim = a.dim, rot = a.rot;
   const Lane l = lane_of(sets, dim, rot, U);
-  const Side side = side_of(a, l.keys);
+  const Side& side = a.side[l.keys];
   const float inv_dim = 1.0f / (float)dim;
   float w[8] = {}, dw[8] = {};
   if (l.on && l.first_row < a.rows) unpack(load_raw<true>(static_cast<const W*>(side.weight) + l.e, 8), w);
@@ -392,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 2) head_norm_backward_kernel(const _
       }
     }
     float c[8], s[8];
-    turn_of<INTERLEAVED>(a.d_cos, a.d_sin, a.d_positions, a.positions, rot, r, l.e, c, s);
+    turn_of<INTERLEAVED>(a.cos, a.sin, a.positions, a.table, rot, r, l.e, c, s);
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       const int64_t h = l.head + k * l.head_step, col = h * dim + l.e;
@@ -425,67 +496,67 @@ __global__ void __launch_bounds__(kThreads, 2) head_norm_backward_kernel(const _
   if (parts != nullptr) leave_sums(sums, dw, sets, dim, parts);
 }
 
-// The gradients of dense sets.
+// The gradients of strips.
 template <typename T, typename S, bool INTERLEAVED, int LANES, int U>
-__global__ void __launch_bounds__(kThreads, 2) head_norm_backward_strip_kernel(const __grid_constant__ opt_head_norm_backward_args a,
-                                                                              const Sets sets, float* parts) {
+__global__ void __launch_bounds__(kThreads, kBackwardCtas) head_norm_backward_strip_kernel(
+    const __grid_constant__ HeadCall a, const Strips strips, float* parts) {
   __shared__ float sums[kWarps][32][8];
   constexpr bool KEPT = sizeof(S) == 1;
-  const int dim = (int)a.dim, rot = (int)a.rot;
-  const Strip l = strip_of<U>(sets, dim, rot, INTERLEAVED);
-  const uint32_t rows = (uint32_t)a.rows, stride = (uint32_t)sets.stride;
-  const Side side = side_of(a, l.keys);
-  const float inv_dim = 1.0f / (float)dim;
-  float w[8] = {};
-  f2_t dw[4] = {};                 // +0 in both lanes
-  if (l.row < rows) weight8(side.weight, a.weight_dtype, l.e, w);
-  using X = std::conditional_t<KEPT, uint8_t, T>;
-  const T* d_at = static_cast<const T*>(side.dout) + (l.row * side.dout_pitch + l.column);
-  const X* x_at = static_cast<const X*>(side.x) + (l.row * side.x_pitch + l.column);
-  T* out_at = static_cast<T*>(side.out) + (l.row * side.out_pitch + l.column);
-  const int64_t d_step = stride * side.dout_pitch, x_step = stride * side.x_pitch, out_step = stride * side.out_pitch;
-  const uint32_t panel = 512 * (uint32_t)((side.cols + 511) / 512), place = 512 * (l.column >> 9) + ((l.column >> 7) & 3);
+  const int dim = a.dim, rot = a.rot, strip = (int)(blockIdx.x % (uint32_t)strips.strips);
+  const bool keys = strip >= strips.q_strips;
+  const Side& side = a.side[keys];
+  const StripLane l = strip_lane<U>(strips, keys ? strip - strips.q_strips : strip, dim, rot, INTERLEAVED);
+  const uint32_t rows = (uint32_t)a.rows, panel = 512 * (uint32_t)((side.cols + 511) / 512);
   const uint32_t left = (uint32_t)side.cols - min(l.column, (uint32_t)side.cols);
+  const uint32_t place = 512 * (l.column >> 9) + ((l.column >> 7) & 3);
+  const float inv_dim = 1.0f / (float)dim;
+  float w[8];
+  weight8(side.weight, a.weight_dtype, l.e, w);
+  f2_t dw[4] = {};                 // +0 in both lanes
   // the turn back: plus for a pair's first element
   const float sign = !INTERLEAVED && l.e >= (rot >> 1) ? -1.0f : 1.0f;
   const f2_t signs = pk(sign, INTERLEAVED ? -1.0f : sign);
   Raw<T> d[U];
   std::conditional_t<KEPT, KeptAsk, Raw<T>> x[U];
-  const auto load = [&](int k, uint32_t r, bool on) {
-    d[k] = load_if(d_at + 256 * k, on);
+  const auto load = [&](int k, uint32_t r) {
+    const bool on = 256 * k < left && r < rows;
+    d[k] = load_if(static_cast<const T*>(side.dout) + (r * side.dout_pitch + l.column) + 256 * k, on);
     if constexpr (KEPT) {
-      const uint64_t scale_at = (uint64_t)(r >> 7) * panel + (place + 16 * (r & 31) + ((r >> 3) & 12));
-      x[k].codes = load_codes_if(x_at + 256 * k, on);
-      x[k].byte = load_byte_if(static_cast<const uint8_t*>(side.scales) + scale_at + (512 * (k >> 1) + 2 * (k & 1)), on);
+      x[k].codes = load_codes_if(static_cast<const uint8_t*>(side.x) + (r * side.x_pitch + l.column) + 256 * k, on);
+      x[k].byte = load_byte_if(static_cast<const uint8_t*>(side.scales) + (scale_row(r, panel) + place) + (512 * (k >> 1) + 2 * (k & 1)), on);
     } else {
-      x[k] = load_if(x_at + 256 * k, on);
+      x[k] = load_if(static_cast<const T*>(side.x) + (r * side.x_pitch + l.column) + 256 * k, on);
     }
   };
-  int64_t at = 0;
-  if (l.row < rows) {
 #pragma unroll
-    for (int k = 0; k < U; ++k) load(k, l.row, 256 * k < left);
-    at = rot > 0 && a.d_positions != nullptr ? a.d_positions[l.row] : (int64_t)l.row;
-  }
-  for (uint32_t r = l.row; r < rows; r += stride) {
-    const bool more = r + stride < rows;
-    float c[8], s[8];
+  for (int k = 0; k < U; ++k) load(k, l.row);
+  int64_t at = (int64_t)l.row;
+  if (rot > 0 && a.positions != nullptr && l.row < rows) at = a.positions[l.row];
+  for (uint32_t r = l.row; r < rows; r += strips.stride) {
+    const uint32_t next = r + strips.stride;
+    Angles<INTERLEAVED> angles;
     if (rot > 0) {
-      angles<INTERLEAVED>(a.d_cos, a.d_sin, at, a.positions, rot, dim, l.pair, l.rotated, c, s);
-#pragma unroll
-      for (int j = 0; j < 8; j += 2) unpk(mul2(pk(s[j], s[j + 1]), signs), s[j], s[j + 1]);
-      at = a.d_positions == nullptr ? at + stride : more ? a.d_positions[r + stride] : 0;
+      angles.ask(a.cos, a.sin, at, a.table, rot, l.pair, l.rotated);
+      at = a.positions == nullptr ? (int64_t)next : next < rows ? a.positions[next] : 0;
     }
-    d_at += d_step;
-    x_at += x_step;
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const Raw<T> raw = d[k];
-      float v[8], g[8];
+    const auto input = [&](int k, float (&v)[8]) {
       if constexpr (KEPT) values8(x[k].codes, scale_of(x[k].byte), v);
       else unpack(x[k], v);
+    };
+    float c[8], s[8];
+    if (rot > 0) {
+      angles.factors(rot, dim, l.rotated, c, s);
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) unpk(mul2(pk(s[j], s[j + 1]), signs), s[j], s[j + 1]);
+    }
+    T* const out = static_cast<T*>(side.out) + (r * side.out_pitch + l.column);
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
       const bool on = 256 * k < left;
-      load(k, r + stride, on && more);
+      const Raw<T> raw = d[k];
+      float v[8], g[8];
+      input(k, v);
+      load(k, next);
       unpack(raw, g);
       if (rot > 0) {
         float p[8];
@@ -502,29 +573,40 @@ __global__ void __launch_bounds__(kThreads, 2) head_norm_backward_strip_kernel(c
         t[j] = mul2(pk(g[2 * j], g[2 * j + 1]), pk(w[2 * j], w[2 * j + 1]));
         dots = fma2(t[j], xv, dots);
       }
-      float square, dot, more_square, more_dot;
-      unpk(squares, square, more_square);
-      unpk(dots, dot, more_dot);
-      square = lanes_sum<LANES>(square + more_square, sets.lanes);
-      dot = lanes_sum<LANES>(dot + more_dot, sets.lanes);
-      const float rstd = reciprocal_root(fmaf(square, inv_dim, a.eps)), pull = -rstd * rstd * (dot * inv_dim);
-      float out[8];
+      float sum[2], second, other;         // of squares, and with t
+      unpk(squares, sum[0], second);
+      unpk(dots, sum[1], other);
+      sum[0] += second;
+      sum[1] += other;
+      lanes_sums<LANES, 2>(sum, strips.lanes);
+      const float root = reciprocal_root(fmaf(sum[0], inv_dim, a.eps)), pull = -root * root * (sum[1] * inv_dim);
+      float dx[8];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const f2_t xv = pk(v[2 * j], v[2 * j + 1]);
-        const f2_t term = mul2(pk(g[2 * j], g[2 * j + 1]), mul2(xv, pk(rstd, rstd)));
-        if (on) dw[j] = add2(dw[j], term);
-        unpk(mul2(fma2(xv, pk(pull, pull), t[j]), pk(rstd, rstd)), out[2 * j], out[2 * j + 1]);
+        if (on) dw[j] = fma2(pk(g[2 * j], g[2 * j + 1]), mul2(xv, pk(root, root)), dw[j]);
+        unpk(mul2(fma2(xv, pk(pull, pull), t[j]), pk(root, root)), dx[2 * j], dx[2 * j + 1]);
       }
-      store8_if(out_at + 256 * k, out, on);
+      store8_if(out + 256 * k, dx, on);
     }
-    out_at += out_step;
   }
   if (parts == nullptr) return;
   float sum[8];
 #pragma unroll
   for (int j = 0; j < 4; ++j) unpk(dw[j], sum[2 * j], sum[2 * j + 1]);
-  leave_sums(sums, sum, sets, dim, parts);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sums[threadIdx.x >> 5][threadIdx.x & 31][j] = sum[j];
+  __syncthreads();
+  float* row = parts + (int64_t)blockIdx.x * 2 * dim;
+  for (int t = threadIdx.x; t < 2 * dim; t += kThreads) {
+    float v = 0.0f;
+    if ((t >= dim) == keys) {
+      const int e = keys ? t - dim : t;
+      for (int k = 0; k < kWarps; ++k)
+        for (int i = 0; i < 32; i += strips.lanes) v += sums[k][i + (e >> 3)][e & 7];
+    }
+    row[t] = v;
+  }
 }
 
 // ------------------------------------------------------- heads of any size and place
@@ -562,15 +644,15 @@ __device__ __forceinline__ bool turn_at(const float* cos, const float* sin, int6
 }
 
 template <typename T, typename W>
-__global__ void __launch_bounds__(32 * kAnyWarps) head_norm_any_kernel(const __grid_constant__ opt_head_norm_args a) {
+__global__ void __launch_bounds__(32 * kAnyWarps) head_norm_any_kernel(const __grid_constant__ HeadCall a) {
   __shared__ float held[kAnyWarps][kHeadMaxDim];
   float* x = held[threadIdx.x >> 5];
-  const int lane = threadIdx.x & 31, dim = (int)a.dim, rot = (int)a.rot;
-  const int64_t heads = a.q_heads + a.k_heads, n = a.rows * heads;
+  const int lane = threadIdx.x & 31, dim = a.dim, rot = a.rot;
+  const int64_t heads = a.side[0].heads + a.side[1].heads, n = a.rows * heads;
   for (int64_t i = (int64_t)blockIdx.x * kAnyWarps + (threadIdx.x >> 5); i < n; i += (int64_t)gridDim.x * kAnyWarps) {
     const int64_t r = i / heads, both = i % heads;
-    const Side side = side_of(a, both >= a.q_heads);
-    const int64_t col = (both >= a.q_heads ? both - a.q_heads : both) * dim;
+    const Side& side = a.side[both >= a.side[0].heads];
+    const int64_t col = (both >= a.side[0].heads ? both - a.side[0].heads : both) * dim;
     const W* weight = static_cast<const W*>(side.weight);
     float sum = 0.0f;
     for (int j = lane; j < dim; j += 32) {
@@ -580,11 +662,11 @@ __global__ void __launch_bounds__(32 * kAnyWarps) head_norm_any_kernel(const __g
     sum = group_sum(sum, 32);
     const float rstd = reciprocal_root(fmaf(sum, 1.0f / (float)dim, a.eps));
     __syncwarp();
-    const int64_t at = rot > 0 && a.d_positions != nullptr ? a.d_positions[r] : r;
+    const int64_t at = rot > 0 && a.positions != nullptr ? a.positions[r] : r;
     for (int j = lane; j < dim; j += 32) {
       int p = j;
       float c, s, y = x[j] * element(weight + j);
-      if (turn_at(a.d_cos, a.d_sin, at, a.positions, rot, a.flags & OPT_HEADS_INTERLEAVED, j, p, c, s))
+      if (turn_at(a.cos, a.sin, at, a.table, rot, a.interleaved, j, p, c, s))
         y = fmaf(y, c, x[p] * element(weight + p) * s);
       put_element(static_cast<T*>(side.out) + r * side.out_pitch + col + j, rstd * y);
     }
@@ -596,20 +678,20 @@ __global__ void __launch_bounds__(32 * kAnyWarps) head_norm_any_kernel(const __g
 // then, in a launch's second half of CTAs, keys' (`q_ctas` CTAs take queries).
 template <typename T, typename S, typename W>
 __global__ void __launch_bounds__(32 * kAnyWarps) head_norm_backward_any_kernel(
-    const __grid_constant__ opt_head_norm_backward_args a, int q_ctas, float* parts) {
+    const __grid_constant__ HeadCall a, int q_ctas, float* parts) {
   __shared__ float held[kAnyWarps][2][kHeadMaxDim];
   __shared__ float sums[kAnyWarps][kHeadMaxDim];
-  const int wi = threadIdx.x >> 5, lane = threadIdx.x & 31, dim = (int)a.dim, rot = (int)a.rot;
+  const int wi = threadIdx.x >> 5, lane = threadIdx.x & 31, dim = a.dim, rot = a.rot;
   float *x = held[wi][0], *d = held[wi][1], *dw = sums[wi];
   const bool keys = (int)blockIdx.x >= q_ctas;
-  const Side side = side_of(a, keys);
+  const Side& side = a.side[keys];
   const int64_t cta = keys ? blockIdx.x - q_ctas : blockIdx.x, ctas = keys ? gridDim.x - q_ctas : q_ctas;
   const int64_t n = a.rows * side.heads, panel = (side.cols + 511) / 512;
   const W* weight = static_cast<const W*>(side.weight);
   for (int j = lane; j < dim; j += 32) dw[j] = 0.0f;
   for (int64_t i = cta * kAnyWarps + wi; i < n; i += ctas * kAnyWarps) {
     const int64_t r = i / side.heads, col = i % side.heads * dim;
-    const int64_t at = rot > 0 && a.d_positions != nullptr ? a.d_positions[r] : r;
+    const int64_t at = rot > 0 && a.positions != nullptr ? a.positions[r] : r;
     for (int j = lane; j < dim; j += 32) {
       x[j] = element_at(side, r, col + j, panel, S());
       d[j] = element(static_cast<const T*>(side.dout) + r * side.dout_pitch + col + j);
@@ -618,7 +700,7 @@ __global__ void __launch_bounds__(32 * kAnyWarps) head_norm_backward_any_kernel(
     const auto turned = [&](int j) {
       int p = j;
       float c, s;
-      return turn_at(a.d_cos, a.d_sin, at, a.positions, rot, a.flags & OPT_HEADS_INTERLEAVED, j, p, c, s)
+      return turn_at(a.cos, a.sin, at, a.table, rot, a.interleaved, j, p, c, s)
                  ? fmaf(d[j], c, -d[p] * s) : d[j];
     };
     float square = 0.0f, dot = 0.0f;
@@ -717,21 +799,32 @@ cudaError_t forward_heads(const opt_head_norm_args& a, int sm_count, cudaStream_
   const auto kernel = head_norm_kernel<T, W, INTERLEAVED, U>;
   int ctas;
   const Sets sets = sets_of(a, U, (int64_t)sm_count * cached_occupancy(kernel, cache, kThreads, 0), &ctas);
-  kernel<<<ctas, kThreads, 0, s>>>(a, sets);
+  kernel<<<ctas, kThreads, 0, s>>>(call_of(a), sets);
   return cudaGetLastError();
 }
 
-// U heads' chunks after one another: what the registers hold.
-template <typename T>
-constexpr int kStripChunks = sizeof(T) == 2 ? 4 : 2;
+// Strips of U chunks, and their CTAs: as many for each as its rows fill, within `most` in all.
+template <typename A>
+Strips strips_of(const A& a, int u, int64_t most, int64_t* ctas) {
+  Strips s;
+  const int64_t width = 256 * u;
+  s.q_strips = (int)((a.q_heads * a.dim + width - 1) / width);
+  s.strips = s.q_strips + (int)((a.k_heads * a.dim + width - 1) / width);
+  s.lanes = (int)(a.dim / 8);
+  const int64_t need = (a.rows + kWarps - 1) / kWarps, have = most / s.strips;
+  const int64_t each = need <= have ? need : have > 0 ? have : 1;
+  s.stride = (uint32_t)(each * kWarps);
+  *ctas = each * s.strips;
+  return s;
+}
 
 template <typename T, bool INTERLEAVED, bool KEEP, int LANES>
 cudaError_t forward_strip(const opt_head_norm_args& a, int sm_count, cudaStream_t s) {
   static OccupancyCache cache;
-  const auto kernel = head_norm_strip_kernel<T, INTERLEAVED, KEEP, LANES, kStripChunks<T>>;
-  int ctas;
-  const Sets sets = sets_of(a, kStripChunks<T>, (int64_t)sm_count * cached_occupancy(kernel, cache, kThreads, 0), &ctas);
-  kernel<<<ctas, kThreads, 0, s>>>(a, sets);
+  const auto kernel = head_norm_strip_kernel<T, INTERLEAVED, KEEP, LANES, kForwardChunks<T>>;
+  int64_t ctas;
+  const Strips strips = strips_of(a, kForwardChunks<T>, (int64_t)sm_count * cached_occupancy(kernel, cache, kThreads, 0), &ctas);
+  kernel<<<(unsigned)ctas, kThreads, 0, s>>>(call_of(a), strips);
   return cudaGetLastError();
 }
 template <typename T, bool INTERLEAVED, bool KEEP>
@@ -788,7 +881,7 @@ cudaError_t forward(const opt_head_norm_args& a, int sm_count, cudaStream_t s) {
   }
   if (v.ok) return a.flags & OPT_HEADS_INTERLEAVED ? forward_heads<T, W, true>(b, sm_count, s) : forward_heads<T, W, false>(b, sm_count, s);
   const int64_t need = (a.rows * (a.q_heads + a.k_heads) + kAnyWarps - 1) / kAnyWarps, most = (int64_t)sm_count * 12;
-  head_norm_any_kernel<T, W><<<(unsigned)(need < most ? need : most), 32 * kAnyWarps, 0, s>>>(b);
+  head_norm_any_kernel<T, W><<<(unsigned)(need < most ? need : most), 32 * kAnyWarps, 0, s>>>(call_of(b));
   return cudaGetLastError();
 }
 
@@ -808,20 +901,19 @@ cudaError_t backward_any(const opt_head_norm_backward_args& a, int sm_count, flo
     return (int)(need < share ? need : share);
   };
   const int q_ctas = ctas_of(a.q_heads), ctas = q_ctas + ctas_of(a.k_heads);
-  head_norm_backward_any_kernel<T, S, W><<<(unsigned)ctas, 32 * kAnyWarps, 0, s>>>(a, q_ctas, parts);
+  head_norm_backward_any_kernel<T, S, W><<<(unsigned)ctas, 32 * kAnyWarps, 0, s>>>(call_of(a), q_ctas, parts);
   return weight_sums(a, ctas, s);
 }
 
 template <typename T, typename S, bool INTERLEAVED, int LANES>
 cudaError_t backward_strip(const opt_head_norm_backward_args& a, int sm_count, float* parts, cudaStream_t s) {
   static OccupancyCache cache;
-  const auto kernel = head_norm_backward_strip_kernel<T, S, INTERLEAVED, LANES, kStripChunks<T>>;
-  int64_t most = (int64_t)sm_count * cached_occupancy(kernel, cache, kThreads, 0);
+  const auto kernel = head_norm_backward_strip_kernel<T, S, INTERLEAVED, LANES, kBackwardChunks<T>>;
+  int64_t most = (int64_t)sm_count * cached_occupancy(kernel, cache, kThreads, 0), ctas;
   if (most > kHeadBackwardMaxCtas) most = kHeadBackwardMaxCtas;
-  int ctas;
-  const Sets sets = sets_of(a, kStripChunks<T>, most, &ctas);
-  kernel<<<ctas, kThreads, 0, s>>>(a, sets, parts);
-  return weight_sums(a, ctas, s);
+  const Strips strips = strips_of(a, kBackwardChunks<T>, most, &ctas);
+  kernel<<<(unsigned)ctas, kThreads, 0, s>>>(call_of(a), strips, parts);
+  return weight_sums(a, (int)ctas, s);
 }
 template <typename T, typename S, bool INTERLEAVED>
 cudaError_t backward_strips(const opt_head_norm_backward_args& a, int sm_count, float* parts, cudaStream_t s) {
@@ -842,7 +934,7 @@ cudaError_t backward_heads(const opt_head_norm_backward_args& a, int sm_count, f
   int ctas;
   const Sets sets = sets_of(a, U, most, &ctas);
   if (ctas > kHeadBackwardMaxCtas) return backward_any<T, S, W>(a, sm_count, parts, s);      // more sets than the workspace has room for
-  kernel<<<ctas, kThreads, 0, s>>>(a, sets, parts);
+  kernel<<<ctas, kThreads, 0, s>>>(call_of(a), sets, parts);
   return weight_sums(a, ctas, s);
 }
 
@@ -862,7 +954,7 @@ cudaError_t backward_from(const opt_head_norm_backward_args& a, int sm_count, cu
   }
   float* parts = a.d_dq_weight != nullptr || a.d_dk_weight != nullptr ? static_cast<float*>(a.d_workspace) : nullptr;
   // (more sets than the workspace has rows of CTAs for go by single heads)
-  if (v.ok && (a.dim & (a.dim - 1)) == 0 && (a.q_heads + a.k_heads) * a.dim <= kHeadBackwardMaxCtas * kWarps * 256)
+  if (v.ok && (a.dim & (a.dim - 1)) == 0 && (a.q_heads + a.k_heads) * a.dim <= (kHeadBackwardMaxCtas - 2) * 256)
     return a.flags & OPT_HEADS_INTERLEAVED ? backward_strips<T, S, true>(a, sm_count, parts, s) : backward_strips<T, S, false>(a, sm_count, parts, s);
   if (v.ok)
     return a.flags & OPT_HEADS_INTERLEAVED ? backward_heads<T, S, W, true>(a, sm_count, parts, s)

@@ -190,6 +190,23 @@ __device__ __forceinline__ void store_turned(const TileTurn& sh, uint8_t* codes_
   }
 }
 
+// The largest magnitudes of two 1 x 128 blocks that 16 lanes hold chunks of, by whole warps:
+// BF16's go through the exchanges together.
+__device__ __forceinline__ void tops16(uint32_t& a, uint32_t& b, Bf16) {
+  uint32_t both = a | b >> 16;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) both = larger(both, __shfl_xor_sync(0xFFFFFFFFu, both, o), Bf16());
+  a = both & 0xFFFF0000u;
+  b = both << 16;
+}
+__device__ __forceinline__ void tops16(uint32_t& a, uint32_t& b, float) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+    a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+    b = max(b, __shfl_xor_sync(0xFFFFFFFFu, b, o));
+  }
+}
+
 // 16 codes, the first `left` of which exist.
 __device__ __forceinline__ void store_codes16(uint8_t* p, const uint32_t (&word)[4], int left) {
   if (left >= 16) {
