@@ -27,7 +27,7 @@ template <typename T>
 constexpr int kForwardChunks = sizeof(T) == 2 ? 4 : 2;
 template <typename T>
 constexpr int kBackwardChunks = sizeof(T) == 2 ? 4 : 2;
-constexpr int kForwardCtas = 3, kBackwardCtas = 2;
+constexpr int kForwardCtas = 2, kBackwardCtas = 2;
 
 // One side's matrices, queries' or keys'.
 struct Side {
@@ -382,37 +382,52 @@ __global__ void __launch_bounds__(kThreads, kForwardCtas) head_norm_strip_kernel
     uint8_t* const scales = static_cast<uint8_t*>(side.code_scales) + (scale_row(r, panel) + place);
     const T* const ahead = static_cast<const T*>(side.x) + (next * side.x_pitch + l.column);
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const Raw<T> raw = x[k];
-      const bool on = 256 * k < left;
-      x[k] = load_if(ahead + 256 * k, on && next < rows);
-      float v[8], y[8];
-      unpack(raw, v);
-      f2_t sums = 0;                    // +0 in both lanes
+    for (int k = 0; k < U; k += 2) {      // two chunks' exchanges side by side
+      const Raw<T> raw[2] = {x[k], x[k + 1]};
+      x[k] = load_if(ahead + 256 * k, 256 * k < left && next < rows);
+      x[k + 1] = load_if(ahead + 256 * (k + 1), 256 * (k + 1) < left && next < rows);
+      float rstd[2];
 #pragma unroll
-      for (int j = 0; j < 8; j += 2) sums = fma2(pk(v[j], v[j + 1]), pk(v[j], v[j + 1]), sums);
-      float sum[1], second;
-      unpk(sums, sum[0], second);
-      sum[0] += second;
-      lanes_sums<LANES, 1>(sum, strips.lanes);
-      const float rstd = reciprocal_root(fmaf(sum[0], inv_dim, a.eps));
-      const f2_t scale = pk(rstd, rstd);
-      if (rot > 0) {
-        float p[8];
-        unpack(partner_of<INTERLEAVED>(raw, l.partner), p);
+      for (int i = 0; i < 2; ++i) {
+        float v[8];
+        unpack(raw[i], v);
+        f2_t sums = 0;                    // +0 in both lanes
 #pragma unroll
-        for (int j = 0; j < 8; j += 2)
-          unpk(mul2(fma2(pk(v[j], v[j + 1]), pk(c[j], c[j + 1]), mul2(pk(p[j], p[j + 1]), pk(s[j], s[j + 1]))), scale), y[j], y[j + 1]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) unpk(mul2(mul2(pk(v[j], v[j + 1]), pk(w[j], w[j + 1])), scale), y[j], y[j + 1]);
+        for (int j = 0; j < 8; j += 2) sums = fma2(pk(v[j], v[j + 1]), pk(v[j], v[j + 1]), sums);
+        float second;
+        unpk(sums, rstd[i], second);
+        rstd[i] += second;
       }
-      store8_if(out + 256 * k, y, on);
+      uint32_t top[2] = {0u, 0u};
       if (keep) {
-        uint8_t* to = scales + (512 * (k >> 1) + 2 * (k & 1));      // blocks 2 k and 2 k + 1 of the strip
-        const uint32_t top = top16(top_of(magnitudes(raw, false)));
-        if (__any_sync(0xFFFFFFFFu, top >= kInfBits)) put_codes8(codes + 256 * k, to, 0, on ? 8 : 0, v);
-        else put_finite_if(codes + 256 * k, to, v, top, on, on && (threadIdx.x & 15) == 0);
+        top[0] = top_of(magnitudes(raw[0], false));
+        top[1] = top_of(magnitudes(raw[1], false));
+        tops16(top[0], top[1], T());
+      }
+      lanes_sums<LANES, 2>(rstd, strips.lanes);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const bool on = 256 * (k + i) < left;
+        const float root = reciprocal_root(fmaf(rstd[i], inv_dim, a.eps));
+        const f2_t scale = pk(root, root);
+        float v[8], y[8];
+        unpack(raw[i], v);
+        if (rot > 0) {
+          float p[8];
+          unpack(partner_of<INTERLEAVED>(raw[i], l.partner), p);
+#pragma unroll
+          for (int j = 0; j < 8; j += 2)
+            unpk(mul2(fma2(pk(v[j], v[j + 1]), pk(c[j], c[j + 1]), mul2(pk(p[j], p[j + 1]), pk(s[j], s[j + 1]))), scale), y[j], y[j + 1]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; j += 2) unpk(mul2(mul2(pk(v[j], v[j + 1]), pk(w[j], w[j + 1])), scale), y[j], y[j + 1]);
+        }
+        store8_if(out + 256 * (k + i), y, on);
+        if (keep) {
+          uint8_t* to = scales + (512 * (k >> 1) + 2 * i);      // blocks 2 (k + i) and the next of the strip
+          if (__any_sync(0xFFFFFFFFu, top[i] >= kInfBits)) put_codes8(codes + 256 * (k + i), to, 0, on ? 8 : 0, v);
+          else put_finite_if(codes + 256 * (k + i), to, v, top[i], on, on && (threadIdx.x & 15) == 0);
+        }
       }
     }
   }
