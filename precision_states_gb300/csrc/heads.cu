@@ -28,6 +28,7 @@ constexpr int kForwardChunks = sizeof(T) == 2 ? 4 : 2;
 template <typename T>
 constexpr int kBackwardChunks = sizeof(T) == 2 ? 4 : 2;
 constexpr int kForwardCtas = 2, kBackwardCtas = 2;
+constexpr int kBackwardGroup = 1;
 
 // One side's matrices, queries' or keys'.
 struct Side {
@@ -262,36 +263,55 @@ __device__ __forceinline__ void lanes_sums(float (&v)[N], int lanes) {
     }
   }
 }
-// Cosines and sines of a lane's elements at position `at`: for halves one of each element,
-// for neighbours one of each pair.  Asked for, and later made eight factors: elements from `rot`
-// on get 1 and 0, those of a position outside the tables NaN.
-template <bool INTERLEAVED>
-struct Angles {
-  static constexpr int N = INTERLEAVED ? 1 : 2;
-  uint4 cos[N], sin[N];
-  bool there;                    // of the whole warp
-  __device__ __forceinline__ void ask(const float* cos_table, const float* sin_table, int64_t at, int64_t table, int rot, int pair, bool on) {
-    there = (uint64_t)at < (uint64_t)table;
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      const int64_t p = at * (rot >> 1) + pair + 4 * k;
-      cos[k] = load_words_if(cos_table + p, on && there);
-      sin[k] = load_words_if(sin_table + p, on && there);
+__device__ __forceinline__ void shared8(const float* p, float (&x)[8]) {
+  const float4 lo = *reinterpret_cast<const float4*>(p), hi = *reinterpret_cast<const float4*>(p + 4);
+  x[0] = lo.x; x[1] = lo.y; x[2] = lo.z; x[3] = lo.w;
+  x[4] = hi.x; x[5] = hi.y; x[6] = hi.z; x[7] = hi.w;
+}
+// A warp's cosines and sines: this row's and the next one's lines of the tables, copied to
+// shared memory in the background (in registers, asked for a row ahead, they cost the
+// gradients spills; asked for when needed, the wait for them).
+struct TurnLines {
+  float line[2][2][128];         // [turn][cosines, sines][pair]
+  // By the whole warp: the lines at position `at`, NaN outside the tables.
+  __device__ __forceinline__ void ask(int turn, const HeadCall& a, int64_t at) {
+    const int lane = threadIdx.x & 31, chunks = a.rot >> 3;
+    if ((uint64_t)at < (uint64_t)a.table) {
+      const int64_t p = at * (a.rot >> 1) + 4 * lane;
+      if (lane < chunks) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16;"
+                     :: "r"((uint32_t)__cvta_generic_to_shared(&line[turn][0][4 * lane])), "l"(a.cos + p) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16;"
+                     :: "r"((uint32_t)__cvta_generic_to_shared(&line[turn][1][4 * lane])), "l"(a.sin + p) : "memory");
+      }
+    } else {
+      const float nan = u2f(0x7FC00000u);
+      for (int i = lane; i < a.rot >> 1; i += 32) line[turn][0][i] = line[turn][1][i] = nan;
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   }
-  __device__ __forceinline__ void factors(int rot, int dim, bool on, float (&c)[8], float (&s)[8]) const {
-    const uint32_t cw[8] = {cos[0].x, cos[0].y, cos[0].z, cos[0].w, cos[N - 1].x, cos[N - 1].y, cos[N - 1].z, cos[N - 1].w};
-    const uint32_t sw[8] = {sin[0].x, sin[0].y, sin[0].z, sin[0].w, sin[N - 1].x, sin[N - 1].y, sin[N - 1].z, sin[N - 1].w};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      c[j] = u2f(cw[INTERLEAVED ? j >> 1 : j]);
-      s[j] = u2f(sw[INTERLEAVED ? j >> 1 : j]);
+  // All but the lines asked for last are there.
+  __device__ __forceinline__ void wait() const {
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncwarp();
+  }
+  // A lane's eight factors from its pair on: for halves one of each element, for neighbours one
+  // of each pair; 1 and 0 for elements that are not rotated.
+  template <bool INTERLEAVED>
+  __device__ __forceinline__ void factors(int turn, int pair, bool whole, bool rotated, float (&c)[8], float (&s)[8]) const {
+    if constexpr (INTERLEAVED) {
+      const float4 cv = *reinterpret_cast<const float4*>(&line[turn][0][pair]), sv = *reinterpret_cast<const float4*>(&line[turn][1][pair]);
+      c[0] = c[1] = cv.x; c[2] = c[3] = cv.y; c[4] = c[5] = cv.z; c[6] = c[7] = cv.w;
+      s[0] = s[1] = sv.x; s[2] = s[3] = sv.y; s[4] = s[5] = sv.z; s[6] = s[7] = sv.w;
+    } else {
+      shared8(&line[turn][0][pair], c);
+      shared8(&line[turn][1][pair], s);
     }
-    if (rot < dim || !there) {
+    if (!whole) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        c[j] = !on ? 1.0f : there ? c[j] : u2f(0x7FC00000u);
-        s[j] = on && !there ? u2f(0x7FC00000u) : s[j];
+        c[j] = rotated ? c[j] : 1.0f;
+        s[j] = rotated ? s[j] : 0.0f;
       }
     }
   }
@@ -318,14 +338,9 @@ __device__ __forceinline__ StripLane strip_lane(const Strips& strips, int strip,
   l.column = (uint32_t)strip * (256 * U) + 8 * lane;
   l.e = (8 * lane) & (dim - 1);
   l.rotated = l.e < rot;
-  l.pair = interleaved ? l.e >> 1 : l.e < half ? l.e : l.e - half;
+  l.pair = !l.rotated ? 0 : interleaved ? l.e >> 1 : l.e < half ? l.e : l.e - half;
   l.partner = !l.rotated ? lane : lane + (l.e < half ? half >> 3 : -(half >> 3));
   return l;
-}
-__device__ __forceinline__ void shared8(const float* p, float (&x)[8]) {
-  const float4 lo = *reinterpret_cast<const float4*>(p), hi = *reinterpret_cast<const float4*>(p + 4);
-  x[0] = lo.x; x[1] = lo.y; x[2] = lo.z; x[3] = lo.w;
-  x[4] = hi.x; x[5] = hi.y; x[6] = hi.z; x[7] = hi.w;
 }
 __device__ __forceinline__ float weight_at(const void* weight, int32_t type, int e) {
   return type == OPT_F32 ? static_cast<const float*>(weight)[e] : element(static_cast<const Bf16*>(weight) + e);
@@ -341,6 +356,8 @@ __global__ void __launch_bounds__(kThreads, kForwardCtas) head_norm_strip_kernel
   // the weight, and its partner's with the sign of the partner's term (minus for a pair's
   // first element)
   __shared__ __align__(16) float weight[256], other[256];
+  __shared__ __align__(16) TurnLines lines_of[kWarps];
+  TurnLines& lines = lines_of[threadIdx.x >> 5];
   const int dim = a.dim, rot = a.rot, half = rot >> 1, strip = (int)(blockIdx.x % (uint32_t)strips.strips);
   const bool keys = strip >= strips.q_strips;
   const Side& side = a.side[keys];
@@ -361,18 +378,25 @@ __global__ void __launch_bounds__(kThreads, kForwardCtas) head_norm_strip_kernel
   Raw<T> x[U];
 #pragma unroll
   for (int k = 0; k < U; ++k) x[k] = load_if(static_cast<const T*>(side.x) + (l.row * side.x_pitch + l.column) + 256 * k, 256 * k < left);
-  int64_t at = rot > 0 && a.positions != nullptr ? a.positions[l.row] : (int64_t)l.row;
-  for (uint32_t r = l.row; r < rows; r += strips.stride) {
+  const auto position = [&](uint32_t r) { return a.positions == nullptr ? (int64_t)r : r < rows ? a.positions[r] : (int64_t)0; };
+  int64_t at = 0;
+  if (rot > 0) {
+    lines.ask(0, a, position(l.row));
+    at = position(l.row + strips.stride);
+  }
+  int turn = 0;
+  for (uint32_t r = l.row; r < rows; r += strips.stride, turn ^= 1) {
     const uint32_t next = r + strips.stride;
-    Angles<INTERLEAVED> angles;
     if (rot > 0) {
-      angles.ask(a.cos, a.sin, at, a.table, rot, l.pair, l.rotated);
-      at = a.positions == nullptr ? (int64_t)next : next < rows ? a.positions[next] : 0;
+      __syncwarp();              // the lines of the row before are read
+      lines.ask(turn ^ 1, a, next < rows ? at : -1);
+      at = position(next + strips.stride);
     }
     float c[8], s[8], w[8];
     shared8(weight + l.e, w);
     if (rot > 0) {
-      angles.factors(rot, dim, l.rotated, c, s);
+      lines.wait();
+      lines.template factors<INTERLEAVED>(turn, l.pair, rot == dim, l.rotated, c, s);
       times8(c, w);
       shared8(other + l.e, w);
       times8(s, w);
@@ -516,7 +540,10 @@ template <typename T, typename S, bool INTERLEAVED, int LANES, int U>
 __global__ void __launch_bounds__(kThreads, kBackwardCtas) head_norm_backward_strip_kernel(
     const __grid_constant__ HeadCall a, const Strips strips, float* parts) {
   __shared__ float sums[kWarps][32][8];
+  __shared__ __align__(16) TurnLines lines_of[kWarps];
+  TurnLines& lines = lines_of[threadIdx.x >> 5];
   constexpr bool KEPT = sizeof(S) == 1;
+  constexpr int G = kBackwardGroup;
   const int dim = a.dim, rot = a.rot, strip = (int)(blockIdx.x % (uint32_t)strips.strips);
   const bool keys = strip >= strips.q_strips;
   const Side& side = a.side[keys];
@@ -545,64 +572,75 @@ __global__ void __launch_bounds__(kThreads, kBackwardCtas) head_norm_backward_st
   };
 #pragma unroll
   for (int k = 0; k < U; ++k) load(k, l.row);
-  int64_t at = (int64_t)l.row;
-  if (rot > 0 && a.positions != nullptr && l.row < rows) at = a.positions[l.row];
-  for (uint32_t r = l.row; r < rows; r += strips.stride) {
+  const auto position = [&](uint32_t r) { return a.positions == nullptr ? (int64_t)r : r < rows ? a.positions[r] : (int64_t)0; };
+  int64_t at = 0;
+  if (rot > 0 && l.row < rows) {
+    lines.ask(0, a, position(l.row));
+    at = position(l.row + strips.stride);
+  }
+  int turn = 0;
+  for (uint32_t r = l.row; r < rows; r += strips.stride, turn ^= 1) {
     const uint32_t next = r + strips.stride;
-    Angles<INTERLEAVED> angles;
     if (rot > 0) {
-      angles.ask(a.cos, a.sin, at, a.table, rot, l.pair, l.rotated);
-      at = a.positions == nullptr ? (int64_t)next : next < rows ? a.positions[next] : 0;
+      __syncwarp();              // the lines of the row before are read
+      lines.ask(turn ^ 1, a, next < rows ? at : -1);
+      at = position(next + strips.stride);
+      lines.wait();
     }
     const auto input = [&](int k, float (&v)[8]) {
       if constexpr (KEPT) values8(x[k].codes, scale_of(x[k].byte), v);
       else unpack(x[k], v);
     };
+    T* const out = static_cast<T*>(side.out) + (r * side.out_pitch + l.column);
     float c[8], s[8];
     if (rot > 0) {
-      angles.factors(rot, dim, l.rotated, c, s);
+      lines.template factors<INTERLEAVED>(turn, l.pair, rot == dim, l.rotated, c, s);
 #pragma unroll
       for (int j = 0; j < 8; j += 2) unpk(mul2(pk(s[j], s[j + 1]), signs), s[j], s[j + 1]);
     }
-    T* const out = static_cast<T*>(side.out) + (r * side.out_pitch + l.column);
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const bool on = 256 * k < left;
-      const Raw<T> raw = d[k];
-      float v[8], g[8];
-      input(k, v);
-      load(k, next);
-      unpack(raw, g);
-      if (rot > 0) {
-        float p[8];
-        unpack(partner_of<INTERLEAVED>(raw, l.partner), p);
+    for (int k = 0; k < U; k += G) {      // G chunks' exchanges side by side
+      float v[G][8], g[G][8], sum[2 * G];      // sums of x^2, then with t = g weight
 #pragma unroll
-        for (int j = 0; j < 8; j += 2)
-          unpk(fma2(pk(g[j], g[j + 1]), pk(c[j], c[j + 1]), mul2(pk(p[j], p[j + 1]), pk(s[j], s[j + 1]))), g[j], g[j + 1]);
+      for (int i = 0; i < G; ++i) {
+        const Raw<T> raw = d[k + i];
+        input(k + i, v[i]);
+        load(k + i, next);
+        unpack(raw, g[i]);
+        if (rot > 0) {
+          float p[8];
+          unpack(partner_of<INTERLEAVED>(raw, l.partner), p);
+#pragma unroll
+          for (int j = 0; j < 8; j += 2)
+            unpk(fma2(pk(g[i][j], g[i][j + 1]), pk(c[j], c[j + 1]), mul2(pk(p[j], p[j + 1]), pk(s[j], s[j + 1]))), g[i][j], g[i][j + 1]);
+        }
+        f2_t squares = 0, dots = 0;
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          const f2_t xv = pk(v[i][j], v[i][j + 1]);
+          squares = fma2(xv, xv, squares);
+          dots = fma2(mul2(pk(g[i][j], g[i][j + 1]), pk(w[j], w[j + 1])), xv, dots);
+        }
+        float second, other;
+        unpk(squares, sum[i], second);
+        unpk(dots, sum[G + i], other);
+        sum[i] += second;
+        sum[G + i] += other;
       }
-      f2_t squares = 0, dots = 0, t[4];
+      lanes_sums<LANES, 2 * G>(sum, strips.lanes);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const f2_t xv = pk(v[2 * j], v[2 * j + 1]);
-        squares = fma2(xv, xv, squares);
-        t[j] = mul2(pk(g[2 * j], g[2 * j + 1]), pk(w[2 * j], w[2 * j + 1]));
-        dots = fma2(t[j], xv, dots);
-      }
-      float sum[2], second, other;         // of squares, and with t
-      unpk(squares, sum[0], second);
-      unpk(dots, sum[1], other);
-      sum[0] += second;
-      sum[1] += other;
-      lanes_sums<LANES, 2>(sum, strips.lanes);
-      const float root = reciprocal_root(fmaf(sum[0], inv_dim, a.eps)), pull = -root * root * (sum[1] * inv_dim);
-      float dx[8];
+      for (int i = 0; i < G; ++i) {
+        const bool on = 256 * (k + i) < left;
+        const float root = reciprocal_root(fmaf(sum[i], inv_dim, a.eps)), pull = -root * root * (sum[G + i] * inv_dim);
+        float dx[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const f2_t xv = pk(v[2 * j], v[2 * j + 1]);
-        if (on) dw[j] = fma2(pk(g[2 * j], g[2 * j + 1]), mul2(xv, pk(root, root)), dw[j]);
-        unpk(mul2(fma2(xv, pk(pull, pull), t[j]), pk(root, root)), dx[2 * j], dx[2 * j + 1]);
+        for (int j = 0; j < 4; ++j) {
+          const f2_t xv = pk(v[i][2 * j], v[i][2 * j + 1]), gv = pk(g[i][2 * j], g[i][2 * j + 1]);
+          if (on) dw[j] = fma2(gv, mul2(xv, pk(root, root)), dw[j]);
+          unpk(mul2(fma2(xv, pk(pull, pull), mul2(gv, pk(w[2 * j], w[2 * j + 1]))), pk(root, root)), dx[2 * j], dx[2 * j + 1]);
+        }
+        store8_if(out + 256 * (k + i), dx, on);
       }
-      store8_if(out + 256 * k, dx, on);
     }
   }
   if (parts == nullptr) return;
