@@ -28,7 +28,6 @@ constexpr int kForwardChunks = sizeof(T) == 2 ? 4 : 2;
 template <typename T>
 constexpr int kBackwardChunks = sizeof(T) == 2 ? 4 : 2;
 constexpr int kForwardCtas = 2, kBackwardCtas = 2;
-constexpr int kBackwardGroup = 1;
 
 // One side's matrices, queries' or keys'.
 struct Side {
@@ -79,6 +78,9 @@ HeadCall call_of(const opt_head_norm_backward_args& a) {
                a.k_heads * a.dim, a.k_heads};
   return c;
 }
+
+// head_weight_kernel may be launched once every CTA has come here; it waits for this grid's end.
+__device__ __forceinline__ void let_sums_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // Sum over a group of `lanes` (a power of two) lanes.
 __device__ __forceinline__ float group_sum(float v, int lanes) {
@@ -481,6 +483,7 @@ template <typename T, typename S, typename W, bool INTERLEAVED, int U>
 __global__ void __launch_bounds__(kThreads, 2) head_norm_backward_kernel(const __grid_constant__ HeadCall a,
                                                                         Sets sets, float* parts) {
   __shared__ float sums[kWarps][32][8];
+  let_sums_start();
   const int dim = a.dim, rot = a.rot;
   const Lane l = lane_of(sets, dim, rot, U);
   const Side& side = a.side[l.keys];
@@ -542,8 +545,8 @@ __global__ void __launch_bounds__(kThreads, kBackwardCtas) head_norm_backward_st
   __shared__ float sums[kWarps][32][8];
   __shared__ __align__(16) TurnLines lines_of[kWarps];
   TurnLines& lines = lines_of[threadIdx.x >> 5];
+  let_sums_start();
   constexpr bool KEPT = sizeof(S) == 1;
-  constexpr int G = kBackwardGroup;
   const int dim = a.dim, rot = a.rot, strip = (int)(blockIdx.x % (uint32_t)strips.strips);
   const bool keys = strip >= strips.q_strips;
   const Side& side = a.side[keys];
@@ -599,48 +602,43 @@ __global__ void __launch_bounds__(kThreads, kBackwardCtas) head_norm_backward_st
       for (int j = 0; j < 8; j += 2) unpk(mul2(pk(s[j], s[j + 1]), signs), s[j], s[j + 1]);
     }
 #pragma unroll
-    for (int k = 0; k < U; k += G) {      // G chunks' exchanges side by side
-      float v[G][8], g[G][8], sum[2 * G];      // sums of x^2, then with t = g weight
+    for (int k = 0; k < U; ++k) {
+      const bool on = 256 * k < left;
+      const Raw<T> raw = d[k];
+      float v[8], g[8];
+      input(k, v);
+      load(k, next);
+      unpack(raw, g);
+      if (rot > 0) {
+        float p[8];
+        unpack(partner_of<INTERLEAVED>(raw, l.partner), p);
 #pragma unroll
-      for (int i = 0; i < G; ++i) {
-        const Raw<T> raw = d[k + i];
-        input(k + i, v[i]);
-        load(k + i, next);
-        unpack(raw, g[i]);
-        if (rot > 0) {
-          float p[8];
-          unpack(partner_of<INTERLEAVED>(raw, l.partner), p);
-#pragma unroll
-          for (int j = 0; j < 8; j += 2)
-            unpk(fma2(pk(g[i][j], g[i][j + 1]), pk(c[j], c[j + 1]), mul2(pk(p[j], p[j + 1]), pk(s[j], s[j + 1]))), g[i][j], g[i][j + 1]);
-        }
-        f2_t squares = 0, dots = 0;
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          const f2_t xv = pk(v[i][j], v[i][j + 1]);
-          squares = fma2(xv, xv, squares);
-          dots = fma2(mul2(pk(g[i][j], g[i][j + 1]), pk(w[j], w[j + 1])), xv, dots);
-        }
-        float second, other;
-        unpk(squares, sum[i], second);
-        unpk(dots, sum[G + i], other);
-        sum[i] += second;
-        sum[G + i] += other;
+        for (int j = 0; j < 8; j += 2)
+          unpk(fma2(pk(g[j], g[j + 1]), pk(c[j], c[j + 1]), mul2(pk(p[j], p[j + 1]), pk(s[j], s[j + 1]))), g[j], g[j + 1]);
       }
-      lanes_sums<LANES, 2 * G>(sum, strips.lanes);
+      f2_t squares = 0, dots = 0, t[4];      // t = g weight
 #pragma unroll
-      for (int i = 0; i < G; ++i) {
-        const bool on = 256 * (k + i) < left;
-        const float root = reciprocal_root(fmaf(sum[i], inv_dim, a.eps)), pull = -root * root * (sum[G + i] * inv_dim);
-        float dx[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const f2_t xv = pk(v[i][2 * j], v[i][2 * j + 1]), gv = pk(g[i][2 * j], g[i][2 * j + 1]);
-          if (on) dw[j] = fma2(gv, mul2(xv, pk(root, root)), dw[j]);
-          unpk(mul2(fma2(xv, pk(pull, pull), mul2(gv, pk(w[2 * j], w[2 * j + 1]))), pk(root, root)), dx[2 * j], dx[2 * j + 1]);
-        }
-        store8_if(out + 256 * (k + i), dx, on);
+      for (int j = 0; j < 4; ++j) {
+        const f2_t xv = pk(v[2 * j], v[2 * j + 1]);
+        squares = fma2(xv, xv, squares);
+        t[j] = mul2(pk(g[2 * j], g[2 * j + 1]), pk(w[2 * j], w[2 * j + 1]));
+        dots = fma2(t[j], xv, dots);
       }
+      float sum[2], second, other;
+      unpk(squares, sum[0], second);
+      unpk(dots, sum[1], other);
+      sum[0] += second;
+      sum[1] += other;
+      lanes_sums<LANES, 2>(sum, strips.lanes);
+      const float root = reciprocal_root(fmaf(sum[0], inv_dim, a.eps)), pull = -root * root * (sum[1] * inv_dim);
+      float dx[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const f2_t xv = pk(v[2 * j], v[2 * j + 1]);
+        if (on) dw[j] = fma2(pk(g[2 * j], g[2 * j + 1]), mul2(xv, pk(root, root)), dw[j]);
+        unpk(mul2(fma2(xv, pk(pull, pull), t[j]), pk(root, root)), dx[2 * j], dx[2 * j + 1]);
+      }
+      store8_if(out + 256 * k, dx, on);
     }
   }
   if (parts == nullptr) return;
@@ -734,6 +732,7 @@ __global__ void __launch_bounds__(32 * kAnyWarps) head_norm_backward_any_kernel(
     const __grid_constant__ HeadCall a, int q_ctas, float* parts) {
   __shared__ float held[kAnyWarps][2][kHeadMaxDim];
   __shared__ float sums[kAnyWarps][kHeadMaxDim];
+  let_sums_start();
   const int wi = threadIdx.x >> 5, lane = threadIdx.x & 31, dim = a.dim, rot = a.rot;
   float *x = held[wi][0], *d = held[wi][1], *dw = sums[wi];
   const bool keys = (int)blockIdx.x >= q_ctas;
@@ -782,26 +781,33 @@ __global__ void __launch_bounds__(32 * kAnyWarps) head_norm_backward_any_kernel(
   }
 }
 
-// The weights' gradients: the partial sums' rows in a fixed order, 32 columns to a CTA.
+// The weights' gradients: the partial sums' rows in a fixed order, 32 columns to a CTA.  Thread
+// row p takes rows p, p + 32, ..., ten loads at a time; then a warp each column's 32 sums.
+// Launched while the rows' kernel still runs, it waits for that one's end.
 constexpr int kSumCols = 32, kSumParts = 32;
-__global__ void __launch_bounds__(kSumCols * kSumParts) head_weight_kernel(const float* __restrict__ parts, int n, int dim,
-                                                                           float* dq, float* dk) {
+__global__ void __launch_bounds__(kSumCols * kSumParts) head_weight_kernel(const float* parts, int n, int dim, float* dq, float* dk) {
   __shared__ float sums[kSumParts][kSumCols + 1];
   const int x = threadIdx.x % kSumCols, p0 = threadIdx.x / kSumCols, t = blockIdx.x * kSumCols + x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   float s = 0.0f;
   if (t < 2 * dim) {
-#pragma unroll 4
-    for (int p = p0; p < n; p += kSumParts) s += parts[(int64_t)p * 2 * dim + t];
+    for (int p = p0; p < n; p += 10 * kSumParts) {
+      float v[10];
+#pragma unroll
+      for (int i = 0; i < 10; ++i) v[i] = p + i * kSumParts < n ? parts[(int64_t)(p + i * kSumParts) * 2 * dim + t] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < 10; ++i) s += v[i];
+    }
   }
   sums[p0][x] = s;
   __syncthreads();
-  if (p0 != 0 || t >= 2 * dim) return;
-#pragma unroll
-  for (int p = 1; p < kSumParts; ++p) s += sums[p][x];
-  if (t < dim) {
-    if (dq != nullptr) dq[t] = s;
+  s = group_sum(sums[x][p0], 32);          // column p0's
+  const int c = blockIdx.x * kSumCols + p0;
+  if (x != 0 || c >= 2 * dim) return;
+  if (c < dim) {
+    if (dq != nullptr) dq[c] = s;
   } else if (dk != nullptr) {
-    dk[t - dim] = s;
+    dk[c - dim] = s;
   }
 }
 
@@ -939,10 +945,18 @@ cudaError_t forward(const opt_head_norm_args& a, int sm_count, cudaStream_t s) {
 }
 
 cudaError_t weight_sums(const opt_head_norm_backward_args& a, int ctas, cudaStream_t s) {
-  if (a.d_dq_weight != nullptr || a.d_dk_weight != nullptr)
-    head_weight_kernel<<<(unsigned)((2 * a.dim + kSumCols - 1) / kSumCols), kSumCols * kSumParts, 0, s>>>(
-        static_cast<const float*>(a.d_workspace), ctas, (int)a.dim, a.d_dq_weight, a.d_dk_weight);
-  return cudaGetLastError();
+  if (a.d_dq_weight == nullptr && a.d_dk_weight == nullptr) return cudaGetLastError();
+  cudaLaunchAttribute early = {};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t config = {};
+  config.gridDim = dim3((unsigned)((2 * a.dim + kSumCols - 1) / kSumCols));
+  config.blockDim = dim3(kSumCols * kSumParts);
+  config.stream = s;
+  config.attrs = &early;
+  config.numAttrs = 1;
+  return cudaLaunchKernelEx(&config, head_weight_kernel, static_cast<const float*>(a.d_workspace), ctas, (int)a.dim, a.d_dq_weight,
+                            a.d_dk_weight);
 }
 
 template <typename T, typename S, typename W>
@@ -955,6 +969,7 @@ cudaError_t backward_any(const opt_head_norm_backward_args& a, int sm_count, flo
   };
   const int q_ctas = ctas_of(a.q_heads), ctas = q_ctas + ctas_of(a.k_heads);
   head_norm_backward_any_kernel<T, S, W><<<(unsigned)ctas, 32 * kAnyWarps, 0, s>>>(call_of(a), q_ctas, parts);
+  if (const cudaError_t e = cudaGetLastError()) return e;
   return weight_sums(a, ctas, s);
 }
 
@@ -966,6 +981,7 @@ cudaError_t backward_strip(const opt_head_norm_backward_args& a, int sm_count, f
   if (most > kHeadBackwardMaxCtas) most = kHeadBackwardMaxCtas;
   const Strips strips = strips_of(a, kBackwardChunks<T>, most, &ctas);
   kernel<<<(unsigned)ctas, kThreads, 0, s>>>(call_of(a), strips, parts);
+  if (const cudaError_t e = cudaGetLastError()) return e;
   return weight_sums(a, (int)ctas, s);
 }
 template <typename T, typename S, bool INTERLEAVED>
@@ -988,6 +1004,7 @@ cudaError_t backward_heads(const opt_head_norm_backward_args& a, int sm_count, f
   const Sets sets = sets_of(a, U, most, &ctas);
   if (ctas > kHeadBackwardMaxCtas) return backward_any<T, S, W>(a, sm_count, parts, s);      // more sets than the workspace has room for
   kernel<<<ctas, kThreads, 0, s>>>(call_of(a), sets, parts);
+  if (const cudaError_t e = cudaGetLastError()) return e;
   return weight_sums(a, ctas, s);
 }
 

@@ -520,29 +520,35 @@ def _like_heads(t, what, rows, heads, dim, dtype, device):
     """(pointer, pitch) of heads of the given number and dtype."""
     if t.dtype != dtype or t.get_device() != device:
         raise ValueError(f"{what}: expected {dtype} on cuda:{device}")
+    shape = t.shape
+    if len(shape) == 2 and shape[0] == rows and shape[1] == heads * dim:
+        pitch, step = t.stride()
+        if step == 1:                                      # the common case
+            return t.data_ptr(), pitch
     r, h, pitch = _heads(t, what, dim)
     if r != rows or h != heads:
-        raise ValueError(f"{what}: expected {rows} rows of {heads} heads of {dim}, got {tuple(t.shape)}")
+        raise ValueError(f"{what}: expected {rows} rows of {heads} heads of {dim}, got {tuple(shape)}")
     return t.data_ptr(), pitch
 
 
 def _turn(cos, sin, positions, rows, device, ready):
     """(cos, sin and positions pointers, rotated elements, positions in the tables)."""
-    if cos is None and sin is None:
+    if cos is None or sin is None:
+        if cos is not None or sin is not None:
+            raise ValueError("cos and sin go together")
         if positions is not None:
             raise ValueError("positions: without cos and sin")
         return 0, 0, 0, 0, 0
-    if cos is None or sin is None:
-        raise ValueError("cos and sin go together")
-    if len(cos.shape) != 2:
-        raise ValueError("cos: expected positions x pairs")
-    table, pairs = cos.shape
-    if tuple(sin.shape) != (table, pairs):
-        raise ValueError(f"sin: expected {table} x {pairs}, got {tuple(sin.shape)}")
-    cq = _vector(cos, "cos", table * pairs, device, ready.f32)
-    sq = _vector(sin, "sin", table * pairs, device, ready.f32)
+    shape = cos.shape
+    if len(shape) != 2 or sin.shape != shape:
+        raise ValueError(f"cos and sin: expected positions x pairs each, got {tuple(shape)} and {tuple(sin.shape)}")
+    table, pairs = shape
+    f32 = ready.f32
+    if (cos.dtype != f32 or sin.dtype != f32 or cos.get_device() != device or sin.get_device() != device
+            or not cos.is_contiguous() or not sin.is_contiguous()):
+        raise ValueError(f"cos and sin: expected contiguous {f32} on cuda:{device}")
     pq = 0 if positions is None else _vector(positions, "positions", rows, device, ready.int64)
-    return cq, sq, pq, 2 * pairs, table
+    return cos.data_ptr(), sin.data_ptr(), pq, 2 * pairs, table
 
 
 def opt_head_norm(q, q_weight, q_out, k=None, k_weight=None, k_out=None, eps=1e-5, cos=None, sin=None, positions=None,
@@ -573,8 +579,10 @@ def opt_head_norm(q, q_weight, q_out, k=None, k_weight=None, k_out=None, eps=1e-
     else:
         if k_weight is None or k_out is None:
             raise ValueError("k: needs k_weight and k_out")
-        _, hk, _ = _heads(k, "k", dim)
-        kq, kp = _like_heads(k, "k", rows, hk, dim, dtype, dev)
+        rk, hk, kp = _heads(k, "k", dim)
+        if rk != rows or k.dtype != dtype or k.get_device() != dev:
+            raise ValueError(f"k: expected {rows} rows of {dtype} on cuda:{dev}")
+        kq = k.data_ptr()
         kwq = _vector(k_weight, "k_weight", dim, dev, wtype)
         koq, kop = _like_heads(k_out, "k_out", rows, hk, dim, dtype, dev)
         kcq, ksq, kcp = _pair(k_kept, "k_kept", rows, hk * dim, dev, ready)
@@ -627,8 +635,10 @@ def opt_head_norm_backward(dq_out, q, q_weight, dq, dk_out=None, k=None, k_weigh
     else:
         if k is None or k_weight is None or dk is None:
             raise ValueError("dk_out: needs k, k_weight and dk")
-        _, hk, _ = _heads(dk_out, "dk_out", dim)
-        kgq, kgp = _like_heads(dk_out, "dk_out", rows, hk, dim, dtype, dev)
+        rk, hk, kgp = _heads(dk_out, "dk_out", dim)
+        if rk != rows or dk_out.dtype != dtype or dk_out.get_device() != dev:
+            raise ValueError(f"dk_out: expected {rows} rows of {dtype} on cuda:{dev}")
+        kgq = dk_out.data_ptr()
         kq, ksq, kp = given(k, "k", hk)
         kwq = _vector(k_weight, "k_weight", dim, dev, wtype)
         koq, kop = _like_heads(dk, "dk", rows, hk, dim, dtype, dev)
