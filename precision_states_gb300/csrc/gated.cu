@@ -272,11 +272,12 @@ constexpr int kTurnBytes = 3 * kTile * (int)sizeof(float);
 template <bool VEC>
 using Offset = std::conditional_t<VEC, uint32_t, int64_t>;
 
-// Place of columns 4 quad ... 4 quad + 3 of a tile's row, in units of four values: a chunk's two
-// places are 16 apart, and every 16 rows turned by one more, so that neither eight chunks of a
-// row nor the rows 16 apart of a column meet in a bank.
+// Place of columns 4 quad ... 4 quad + 3 of a tile's row, in units of four values: the N quads
+// that a thread has of a row lie 32 / N apart, and every 16 rows are turned by one more, so that
+// neither eight threads' quads of a row nor the rows 16 apart of a column meet in a bank.
+template <int N>
 __device__ __forceinline__ int turned_place(int row, int quad) {
-  return 32 * row + (((quad >> 1) | (quad & 1) << 4) ^ (row >> 4));
+  return 32 * row + (((quad / N) | (quad % N) * (32 / N)) ^ (row >> 4));
 }
 
 // A tile's values by columns: four columns to a warp, 16 rows of one of them to a lane
@@ -317,16 +318,17 @@ __device__ __forceinline__ uint32_t code_column(const float* column, uint32_t (&
 // What a lane has of the columns: its column, and the first of its 16 rows.
 __device__ __forceinline__ int lane_column() { return 4 * (threadIdx.x >> 5) + ((threadIdx.x & 31) >> 3); }
 __device__ __forceinline__ int lane_row() { return 16 * (threadIdx.x & 7); }
+template <int N>
 __device__ __forceinline__ const float* lane_values(const float4* held) {
   const int column = lane_column();
-  return reinterpret_cast<const float*>(held + turned_place(lane_row(), column >> 2)) + (column & 3);
+  return reinterpret_cast<const float*>(held + turned_place<N>(lane_row(), column >> 2)) + (column & 3);
 }
 // Those of the tile at `v`: codes to `codes` (the tile's first column's), scale bytes to
 // `scales` (the tile's).
 template <bool VEC>
 __device__ __forceinline__ void put_columns(const float4* v, uint8_t* codes, uint8_t* scales, int64_t pitch, int rows, int cols) {
   uint32_t word[4];
-  const uint32_t byte = code_column(lane_values(v), word);
+  const uint32_t byte = code_column(lane_values<2>(v), word);
   const int column = lane_column(), row = lane_row();
   if (column >= cols) return;
   store_codes16(codes + ((Offset<VEC>)column * (Offset<VEC>)pitch + row), word, rows - row);
@@ -342,91 +344,143 @@ struct Inputs {
 // The whole backward pass of a training step in BF16 from kept inputs: all five 8-bit operands
 // and nothing plain.  The same work as gated_backward_tile_kernel's without its choices (which
 // take half of its instructions).  CTAs take runs of tiles along a row of tiles; places in a
-// matrix are counted in chunks of eight elements (of a transposed one of 16 rows), so that
+// matrix are counted in chunks of eight or 16 elements, so that
 // 32 bits hold them (turn_places_fit, below).
 template <int KIND>
 __global__ void __launch_bounds__(kTurnThreads, 1) gated_backward_turn_kernel(const __grid_constant__ opt_gated_backward_args a,
                                                                              uint32_t row_tiles, uint32_t col_tiles, uint32_t per_cta) {
   extern __shared__ __align__(16) float4 held[];       // dgate, dup, y
-  const uint32_t q = threadIdx.x & 15, row = 2 * (threadIdx.x >> 4), t_col = lane_column(), t_row = lane_row();
+  // 16 columns of a row to a thread, in two halves; then 16 rows of a column
+  const uint32_t q = threadIdx.x & 7, row = threadIdx.x >> 3, t_col = lane_column(), t_row = lane_row();
   const uint32_t all_rows = (uint32_t)a.rows, all_cols = (uint32_t)a.cols;
   const uint32_t panel = 512 * ((all_cols + 511) / 512), panel_t = 512 * ((all_rows + 511) / 512);
-  const uint32_t dy_pitch = (uint32_t)(a.dy_pitch >> 3), g_pitch = (uint32_t)(a.gate_pitch >> 3), u_pitch = (uint32_t)(a.up_pitch >> 3),
-                 dg_pitch = (uint32_t)(a.dgate_codes_pitch >> 3), du_pitch = (uint32_t)(a.dup_codes_pitch >> 3),
+  const uint32_t dy_pitch = (uint32_t)(a.dy_pitch >> 3), g_pitch = (uint32_t)(a.gate_pitch >> 4), u_pitch = (uint32_t)(a.up_pitch >> 4),
+                 dg_pitch = (uint32_t)(a.dgate_codes_pitch >> 4), du_pitch = (uint32_t)(a.dup_codes_pitch >> 4),
                  dgt_pitch = (uint32_t)(a.dgate_codes_t_pitch >> 4), dut_pitch = (uint32_t)(a.dup_codes_t_pitch >> 4),
                  yt_pitch = (uint32_t)(a.y_codes_t_pitch >> 4);
-  float4 *const lo = held + turned_place(row, 2 * q), *const hi = held + turned_place(row, 2 * q + 1);      // row + 1: 32 further
-  const float* const column = lane_values(held);
+  float4* const mine = held + turned_place<4>(row, 4 * q);      // the next quads: 8 places further each, before the row's turn
+  const float* const column = lane_values<4>(held);
   struct In {
     Raw<Bf16> dy[2];
-    KeptAsk gate[2], up[2];
+    uint4 gate, up;
+    uint32_t gate_byte, up_byte;
   } in;
   const uint32_t tiles = row_tiles * col_tiles, begin = blockIdx.x * per_cta, end = min(begin + per_cta, tiles);
   uint32_t tr = begin / col_tiles, tc = begin % col_tiles;
   const auto load = [&](uint32_t tr, uint32_t tc) {
-    const uint32_t r = 128 * tr + row, c = 16 * tc + q;
+    const uint32_t r = 128 * tr + row, c = 8 * tc + q;
     const uint32_t at = panel * tr + 512 * (tc >> 2) + (tc & 3) + 16 * (row & 31) + 4 * (row >> 5);
-    const bool in_cols = 8 * c < all_cols;
+    const Bf16* dy = static_cast<const Bf16*>(a.d_dy) + (uint64_t)(r * dy_pitch + 2 * c) * 8;
+    const uint8_t *g = static_cast<const uint8_t*>(a.d_gate) + (uint64_t)(r * g_pitch + c) * 16,
+                  *u = static_cast<const uint8_t*>(a.d_up) + (uint64_t)(r * u_pitch + c) * 16;
+    const uint8_t *gs = static_cast<const uint8_t*>(a.d_gate_scales) + at, *us = static_cast<const uint8_t*>(a.d_up_scales) + at;
     if (128 * tr + 128 <= all_rows && 128 * tc + 128 <= all_cols) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        in.dy[i] = load_raw<true>(static_cast<const Bf16*>(a.d_dy) + (uint64_t)((r + i) * dy_pitch + c) * 8, 8);
-        in.gate[i].codes = load_codes8(static_cast<const uint8_t*>(a.d_gate) + (uint64_t)((r + i) * g_pitch + c) * 8, 8);
-        in.up[i].codes = load_codes8(static_cast<const uint8_t*>(a.d_up) + (uint64_t)((r + i) * u_pitch + c) * 8, 8);
-        in.gate[i].byte = (static_cast<const uint8_t*>(a.d_gate_scales) + at)[16 * i];
-        in.up[i].byte = (static_cast<const uint8_t*>(a.d_up_scales) + at)[16 * i];
-      }
+      in.dy[0] = load_raw<true>(dy, 8);
+      in.dy[1] = load_raw<true>(dy + 8, 8);
+      in.gate = ld_cs_u4(g);
+      in.up = ld_cs_u4(u);
+      in.gate_byte = *gs;
+      in.up_byte = *us;
       return;
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const bool on = in_cols && r + i < all_rows;
-      in.dy[i] = load_if(static_cast<const Bf16*>(a.d_dy) + (uint64_t)((r + i) * dy_pitch + c) * 8, on);
-      in.gate[i].codes = load_codes_if(static_cast<const uint8_t*>(a.d_gate) + (uint64_t)((r + i) * g_pitch + c) * 8, on);
-      in.up[i].codes = load_codes_if(static_cast<const uint8_t*>(a.d_up) + (uint64_t)((r + i) * u_pitch + c) * 8, on);
-      in.gate[i].byte = load_byte_if(static_cast<const uint8_t*>(a.d_gate_scales) + at + 16 * i, on);
-      in.up[i].byte = load_byte_if(static_cast<const uint8_t*>(a.d_up_scales) + at + 16 * i, on);
-    }
+    const bool lo = r < all_rows && 16 * c < all_cols, hi = lo && 16 * c + 8 < all_cols;      // whole chunks of eight
+    in.dy[0] = load_if(dy, lo);
+    in.dy[1] = load_if(dy + 8, hi);
+    const uint2 g0 = load_codes_if(g, lo), g1 = load_codes_if(g + 8, hi), u0 = load_codes_if(u, lo), u1 = load_codes_if(u + 8, hi);
+    in.gate = make_uint4(g0.x, g0.y, g1.x, g1.y);
+    in.up = make_uint4(u0.x, u0.y, u1.x, u1.y);
+    in.gate_byte = load_byte_if(gs, lo);
+    in.up_byte = load_byte_if(us, lo);
+  };
+  // The lines of the tile two further, to L2 (loads of the next tile are asked for while this one
+  // is turned, which is shorter than the way from memory): of each row two of dy's, one of
+  // gate's and one of up's to a thread.
+  const auto ask_l2 = [&](uint32_t tr, uint32_t tc) {
+    for (; tc >= col_tiles; tc -= col_tiles) ++tr;
+    const uint32_t t = threadIdx.x, r = 128 * tr + (t >> 2), c = 8 * tc;
+    if (t >= 512 || r >= all_rows || 16 * c + ((t & 3) == 1 ? 64 : 0) >= all_cols) return;
+    const uint8_t* p = (t & 2) == 0 ? static_cast<const uint8_t*>(a.d_dy) + (uint64_t)(r * dy_pitch + 2 * c) * 16 + 128 * (t & 1)
+                       : (t & 1) == 0 ? static_cast<const uint8_t*>(a.d_gate) + (uint64_t)(r * g_pitch + c) * 16
+                                      : static_cast<const uint8_t*>(a.d_up) + (uint64_t)(r * u_pitch + c) * 16;
+    asm volatile("prefetch.global.L2 [%0];" :: "l"(p));
   };
   if (begin < end) load(tr, tc);
+  if (begin + 1 < end) ask_l2(tr, tc + 1);
   for (uint32_t tile = begin; tile < end; ++tile) {
-    const uint32_t r = 128 * tr + row, c = 16 * tc + q;
-    const uint32_t at = panel * tr + 512 * (tc >> 2) + (tc & 3) + 16 * (row & 31) + 4 * (row >> 5);
-    const bool in_cols = 8 * c < all_cols;
+    const uint32_t r = 128 * tr + row, c = 8 * tc + q;
+    if (tile + 2 < end) ask_l2(tr, tc + 2);
+    {
+      float dgate[16], dup[16];
+      const float gate_scale = scale_of(in.gate_byte), up_scale = scale_of(in.up_byte);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float d[8], g[8], u[8], f[8], df[8];
-      values8(in.gate[i].codes, scale_of(in.gate[i].byte), g);
-      activation8<KIND, false, true>(g, f, df);
-      unpack(in.dy[i], d);
-      times8(df, d);
-      times8(d, f);                 // dup
-      values8(in.up[i].codes, scale_of(in.up[i].byte), u);
-      times8(f, u);                 // y
-      times8(df, u);                // dgate
-      const auto leave = [&](int m, const float (&x)[8]) {
-        lo[m * (kTile / 4) + 32 * i] = make_float4(x[0], x[1], x[2], x[3]);
-        hi[m * (kTile / 4) + 32 * i] = make_float4(x[4], x[5], x[6], x[7]);
-      };
-      leave(0, df);
-      leave(1, d);
-      leave(2, f);
-      // both rows' fields through the exchanges in one word
-      uint32_t both = scale_field(top8_of(df)) >> 23 | (scale_field(top8_of(d)) >> 23) << 16;
+      for (int h = 0; h < 2; ++h) {
+        float d[8], g[8], u[8], f[8], df[8];
+        values8(h == 0 ? make_uint2(in.gate.x, in.gate.y) : make_uint2(in.gate.z, in.gate.w), gate_scale, g);
+        activation8<KIND, false, true>(g, f, df);
+        unpack(in.dy[h], d);
+        times8(df, d);
+        times8(d, f);                 // dup
+        values8(h == 0 ? make_uint2(in.up.x, in.up.y) : make_uint2(in.up.z, in.up.w), up_scale, u);
+        times8(f, u);                 // y
+        times8(df, u);                // dgate
+        const auto leave = [&](int m, const float (&x)[8]) {
+          float4* v = mine + m * (kTile / 4) + 16 * h;
+          v[0] = make_float4(x[0], x[1], x[2], x[3]);
+          v[8] = make_float4(x[4], x[5], x[6], x[7]);
+        };
+        leave(0, df);
+        leave(1, d);
+        leave(2, f);
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) both = larger(both, __shfl_xor_sync(0xFFFFFFFFu, both, o), Bf16());
-      const uint32_t gfield = both << 23, ufield = (both >> 16) << 23;
-      const bool on = in_cols && r + i < all_rows;
-      uint8_t *dg = static_cast<uint8_t*>(a.d_dgate_codes) + (uint64_t)((r + i) * dg_pitch + c) * 8,
-              *du = static_cast<uint8_t*>(a.d_dup_codes) + (uint64_t)((r + i) * du_pitch + c) * 8;
-      uint8_t *dgs = static_cast<uint8_t*>(a.d_dgate_scales) + at + 16 * i, *dus = static_cast<uint8_t*>(a.d_dup_scales) + at + 16 * i;
-      if (__any_sync(0xFFFFFFFFu, max(both & 0xFFFFu, both >> 16) >= 255u)) {      // rare
-        put_codes8(dg, dgs, 0, on ? 8 : 0, df);
-        put_codes8(du, dus, 0, on ? 8 : 0, d);
-      } else {
-        put_field_if(dg, dgs, df, gfield, on, on && q == 0);
-        put_field_if(du, dus, d, ufield, on, on && q == 0);
+        for (int j = 0; j < 8; ++j) {
+          dgate[8 * h + j] = df[j];
+          dup[8 * h + j] = d[j];
+        }
       }
+      const auto largest = [&](const float (&x)[16]) {
+        float t = largest3(x[0], x[1], x[2]);
+#pragma unroll
+        for (int j = 3; j < 15; j += 2) t = largest3(t, x[j], x[j + 1]);
+        return largest3(t, x[15], x[15]);
+      };
+      // both matrices' fields through the exchanges of a row's eight lanes in one word
+      const auto fields = [&](float gt, float ut) {
+        uint32_t both = scale_field(f2u(gt)) >> 23 | (scale_field(f2u(ut)) >> 23) << 16;
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) both = larger(both, __shfl_xor_sync(0xFFFFFFFFu, both, o), Bf16());
+        return both;
+      };
+      uint32_t both = fields(largest(dgate), largest(dup));
+      if (__any_sync(0xFFFFFFFFu, max(both & 0xFFFFu, both >> 16) >= 255u)) {      // rare: the finite ones' maxima, and NaN for the others
+        float gt = 0.0f, ut = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          gt = finite_bits(dgate[j]) ? fmaxf(gt, fabsf(dgate[j])) : gt;
+          ut = finite_bits(dup[j]) ? fmaxf(ut, fabsf(dup[j])) : ut;
+          dgate[j] = finite_bits(dgate[j]) ? dgate[j] : u2f(0x7FC00000u);
+          dup[j] = finite_bits(dup[j]) ? dup[j] : u2f(0x7FC00000u);
+        }
+        both = fields(gt, ut);
+      }
+      const int left = r < all_rows ? (int)(all_cols - min(16 * c, all_cols)) : 0;
+      const uint32_t at = panel * tr + 512 * (tc >> 2) + (tc & 3) + 16 * (row & 31) + 4 * (row >> 5);
+      const auto put = [&](void* codes, void* scales, uint32_t pitch, const float (&x)[16], uint32_t field) {
+        const float inv = inverse_of_field(field);
+        uint32_t word[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float v[4];
+          unpk(mul2(pk(x[4 * k], x[4 * k + 1]), pk(inv, inv)), v[0], v[1]);
+          unpk(mul2(pk(x[4 * k + 2], x[4 * k + 3]), pk(inv, inv)), v[2], v[3]);
+          word[k] = e4m3x2_rn(v[0], v[1]) | e4m3x2_rn(v[2], v[3]) << 16;
+        }
+        uint8_t* p = static_cast<uint8_t*>(codes) + (uint64_t)(r * pitch + c) * 16;
+        if (left >= 16) st_cs_u4(p, make_uint4(word[0], word[1], word[2], word[3]));
+        else if (left > 0) st_cs_u2(p, make_uint2(word[0], word[1]));      // a whole chunk of eight
+        if (q == 0 && left > 0) static_cast<uint8_t*>(scales)[at] = (uint8_t)byte_of_field(field);
+      };
+      put(a.d_dgate_codes, a.d_dgate_scales, dg_pitch, dgate, both << 23);
+      put(a.d_dup_codes, a.d_dup_scales, du_pitch, dup, (both >> 16) << 23);
     }
     __syncthreads();
     const uint32_t col = 128 * tc + t_col, row16 = 128 * tr + t_row;
@@ -526,8 +580,8 @@ __global__ void __launch_bounds__(kTurnThreads, 1) gated_backward_tile_kernel(
       }
       const auto leave = [&](int m, const float (&x)[8]) {
         float4* v = held + m * (kTile / 4);
-        v[turned_place(row + i, 2 * q)] = make_float4(x[0], x[1], x[2], x[3]);
-        v[turned_place(row + i, 2 * q + 1)] = make_float4(x[4], x[5], x[6], x[7]);
+        v[turned_place<2>(row + i, 2 * q)] = make_float4(x[0], x[1], x[2], x[3]);
+        v[turned_place<2>(row + i, 2 * q + 1)] = make_float4(x[4], x[5], x[6], x[7]);
       };
       if (a.d_dgate_codes_t != nullptr) leave(0, df);
       if (a.d_dup_codes_t != nullptr) leave(1, d);
