@@ -397,8 +397,14 @@ __global__ void __launch_bounds__(kTurnThreads, 1) gated_backward_turn_kernel(co
   // gate's and one of up's to a thread.
   const auto ask_l2 = [&](uint32_t tr, uint32_t tc) {
     for (; tc >= col_tiles; tc -= col_tiles) ++tr;
+    if (threadIdx.x >= 512) {              // eight lines of the tiles' scales, where they begin
+      const uint32_t t = threadIdx.x - 512;
+      const uint8_t* scales = static_cast<const uint8_t*>((t & 4) ? a.d_up_scales : a.d_gate_scales) + (panel * tr + 512 * (tc >> 2)) + 128 * (t & 3);
+      if (t < 8 && (tc & 3) == 0) asm volatile("prefetch.global.L2 [%0];" :: "l"(scales));
+      return;
+    }
     const uint32_t t = threadIdx.x, r = 128 * tr + (t >> 2), c = 8 * tc;
-    if (t >= 512 || r >= all_rows || 16 * c + ((t & 3) == 1 ? 64 : 0) >= all_cols) return;
+    if (r >= all_rows || 16 * c + ((t & 3) == 1 ? 64 : 0) >= all_cols) return;
     const uint8_t* p = (t & 2) == 0 ? static_cast<const uint8_t*>(a.d_dy) + (uint64_t)(r * dy_pitch + 2 * c) * 16 + 128 * (t & 1)
                        : (t & 1) == 0 ? static_cast<const uint8_t*>(a.d_gate) + (uint64_t)(r * g_pitch + c) * 16
                                       : static_cast<const uint8_t*>(a.d_up) + (uint64_t)(r * u_pitch + c) * 16;
@@ -482,7 +488,6 @@ __global__ void __launch_bounds__(kTurnThreads, 1) gated_backward_turn_kernel(co
       put(a.d_dgate_codes, a.d_dgate_scales, dg_pitch, dgate, both << 23);
       put(a.d_dup_codes, a.d_dup_scales, du_pitch, dup, (both >> 16) << 23);
     }
-    __syncthreads();
     const uint32_t col = 128 * tc + t_col, row16 = 128 * tr + t_row;
     const uint32_t at_t = panel_t * tc + 512 * (tr >> 2) + (tr & 3) + 16 * (t_col & 31) + 4 * (t_col >> 5);
     if (++tc == col_tiles) {
@@ -490,6 +495,7 @@ __global__ void __launch_bounds__(kTurnThreads, 1) gated_backward_turn_kernel(co
       ++tr;
     }
     if (tile + 1 < end) load(tr, tc);
+    __syncthreads();
     const auto turn = [&](int m, void* codes, void* scales, uint32_t pitch) {
       uint32_t word[4];
       const uint32_t byte = code_column(column + m * kTile, word);
