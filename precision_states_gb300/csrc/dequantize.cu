@@ -32,23 +32,37 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const __grid_const
 // that a warp's words (four of a row, rows 16 apart) meet in no bank.
 __device__ __forceinline__ int tile_word(int row, int w) { return 32 * row + (w ^ (row >> 4 << 2)); }
 
-// Row `row` of the tile as plain elements to a row that begins anywhere, by a warp: whole
-// words, consecutive lanes' side by side.
-__device__ __forceinline__ float tile_value(const uint32_t* codes, const float* scale, int row, int e) {
-  float lo, hi;
-  e4m3x2_dec(reinterpret_cast<const uint8_t*>(codes + tile_word(row, e >> 2))[e & 3], lo, hi);
-  return lo * scale[row];
+// Row `row` of the tile as plain elements to a row that begins anywhere, by a warp: four elements
+// to a lane, out in words (BF16 pairs that lie in one word are put together first).
+__device__ __forceinline__ void tile_values(const uint32_t* codes, const float* scale, int row, float (&x)[4]) {
+  const uint32_t w = codes[tile_word(row, threadIdx.x & 31)];
+  e4m3x2_dec(w & 0xFFFFu, x[0], x[1]);
+  e4m3x2_dec(w >> 16, x[2], x[3]);
+  const f2_t factor = pk(scale[row], scale[row]);
+  unpk(mul2(pk(x[0], x[1]), factor), x[0], x[1]);
+  unpk(mul2(pk(x[2], x[3]), factor), x[2], x[3]);
 }
 __device__ __forceinline__ void put_row(float* out, const uint32_t* codes, const float* scale, int row, int cols) {
-  for (int e = threadIdx.x & 31; e < cols; e += 32) out[e] = tile_value(codes, scale, row, e);
+  const int e = 4 * (threadIdx.x & 31);
+  float x[4];
+  tile_values(codes, scale, row, x);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (e + j < cols) out[e + j] = x[j];
 }
 __device__ __forceinline__ void put_row(Bf16* out, const uint32_t* codes, const float* scale, int row, int cols) {
   const int lane = threadIdx.x & 31, head = (int)((uintptr_t)out >> 1) & 1;      // an element before the first whole word
-  if (head && lane == 0) out[0].bits = (uint16_t)bf16_pair(tile_value(codes, scale, row, 0), 0.0f);
-  for (int e = head + 2 * lane; e < cols; e += 64) {
-    const float lo = tile_value(codes, scale, row, e);
-    if (e + 1 < cols) *reinterpret_cast<uint32_t*>(out + e) = bf16_pair(lo, tile_value(codes, scale, row, e + 1));
-    else out[e].bits = (uint16_t)bf16_pair(lo, 0.0f);
+  float x[4];
+  tile_values(codes, scale, row, x);
+  uint32_t w[3] = {bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), 0u};
+  if (head && lane == 0) out[0].bits = (uint16_t)w[0];
+  w[2] = __shfl_down_sync(0xFFFFFFFFu, w[0], 1);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int e = head + 4 * lane + 2 * j;
+    const uint32_t pair = __funnelshift_r(w[j], w[j + 1], 16 * head);
+    if (e + 1 < cols) *reinterpret_cast<uint32_t*>(out + e) = pair;
+    else if (e < cols) out[e].bits = (uint16_t)pair;
   }
 }
 
@@ -110,6 +124,7 @@ __global__ void __launch_bounds__(kTileThreads, 3) dequantize_tile_kernel(const 
         store8_if(static_cast<T*>(a.d_x) + (r0 + row) * a.x_pitch + c0 + e, x, row < rows && e < cols);
       }
     } else if constexpr (PLAIN) {
+#pragma unroll 2
       for (int row = t >> 5; row < rows; row += kTileThreads / 32)
         put_row(static_cast<T*>(a.d_x) + (r0 + row) * a.x_pitch + c0, codes, scale, row, cols);
     }
