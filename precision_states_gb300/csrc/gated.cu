@@ -73,13 +73,17 @@ __device__ __forceinline__ void activation8(const float (&g)[8], float (&f)[8], 
         z = mul2(mul2(b, pk(c, c)), fma2(bb, pk(kCubic, kCubic), one));
         dz = fma2(bb, pk(3.0f * kCubic * kTwoRootTwoOverPi, 3.0f * kCubic * kTwoRootTwoOverPi), pk(kTwoRootTwoOverPi, kTwoRootTwoOverPi));
       }
-      float lo, hi;
+      float lo, hi, one_lo, one_hi;
       unpk(z, lo, hi);
-      unpk(add2(pk(exp2_near(lo), exp2_near(hi)), one), lo, hi);
-      const f2_t s = pk(reciprocal_near(lo), reciprocal_near(hi)), fv = mul2(gv, s);
+      lo = exp2_near(lo);
+      hi = exp2_near(hi);
+      unpk(add2(pk(lo, hi), one), one_lo, one_hi);
+      const f2_t s = pk(reciprocal_near(one_lo), reciprocal_near(one_hi)), fv = mul2(gv, s);
       unpk(fv, f[j], f[j + 1]);
       if constexpr (SLOPE) {
-        f2_t n = fma2(s, pk(-1.0f, -1.0f), one);
+        // 1 - s as e s (a difference has no digits where s is near 1, and moves the scale of a
+        // block whose largest value lies on a power of two times 448); where e is infinite f is 0
+        f2_t n = mul2(pk(fminf(lo, 3.0e38f), fminf(hi, 3.0e38f)), s);
         if constexpr (KIND == OPT_ACT_GELU_TANH) n = mul2(n, dz);
         unpk(fma2(fv, n, s), df[j], df[j + 1]);
       }
