@@ -600,3 +600,229 @@ def test_a_block_between_products_replays_from_a_graph():
     torch.cuda.synchronize()
     for k, v in want.items():
         assert all(torch.equal(a, b) for a, b in zip(v, got[k])) if isinstance(v, tuple) else torch.equal(v, got[k])
+
+
+# ------------------------------------- forms that large calls and others' sets of outputs take
+def training_outputs(rows, cols):
+    """Every operand that a training step asks for, and nothing plain."""
+    return {**{n: storage(rows, cols) for n in ("dgate_codes", "dup_codes")},
+            **{n: storage(cols, rows) for n in ("dgate_codes_t", "dup_codes_t", "y_codes_t")}}
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows,cols", [(1, 8), (128, 128), (130, 264), (257, 1032), (2000, 1400), (1, 14336), (3000, 24), (77, 4096)])
+def test_all_operands_are_those_of_single_calls(kind, rows, cols):
+    """The training step's set of outputs (BF16, kept inputs) has a kernel of its own: the same
+    bits as from calls for one output each, with several tiles to a CTA, tiles that end inside,
+    zero blocks, infinities and NaN."""
+    g, u, dy = spread(rows, cols, "bf16", 120), matrix(rows, cols, "bf16", 121), matrix(rows, cols, "bf16", 122, std=1e-2)
+    if rows > 100:
+        g[5, 3], u[70, 1], dy[90, 2], dy[100, 9], g[40] = float("nan"), float("inf"), float("-inf"), float("nan"), 0.0
+        dy[110:120] = 0.0
+    gk, uk = kept(g), kept(u)
+    out = training_outputs(rows, cols)
+    ps.opt_gated_backward(dy, gk, uk, activation=kind, **out)
+    for name, got in out.items():
+        want = storage(*got[0].shape)
+        ps.opt_gated_backward(dy, gk, uk, activation=kind, **{name: want})
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), name
+    if kind == "silu":
+        plain = blank(rows, cols, "bf16"), blank(rows, cols, "bf16")
+        more = training_outputs(rows, cols)
+        ps.opt_gated_backward(dy, gk, uk, activation=kind, dgate=plain[0], dup=plain[1], **more)
+        for name, got in out.items():
+            assert torch.equal(got[0], more[name][0]) and torch.equal(got[1], more[name][1]), name
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols,pad", [(9001, 264, 0), (3001, 2056, 8), (12000, 33, 0)])
+def test_many_rows_are_those_of_fewer(dtype, rows, cols, pad):
+    """More rows than the device takes at once: the same bits as slice by slice."""
+    g, u, dy = spread(rows, cols, dtype, 130, pad), matrix(rows, cols, dtype, 131, pad), matrix(rows, cols, dtype, 132, pad)
+    y, pair, gk, uk = blank(rows, cols, dtype), storage(rows, cols), storage(rows, cols), storage(rows, cols)
+    dg, du = blank(rows, cols, dtype), blank(rows, cols, dtype)
+    ps.opt_gated(g, u, y=y, codes=pair[0], scales=pair[1], gate_kept=gk, up_kept=uk)
+    ps.opt_gated_backward(dy, gk, uk, dgate=dg, dup=du)
+    tiles = ps.opt_scales_bytes(128, cols)
+    for a in range(0, rows, 1280):                          # whole panels of scale tiles
+        b = min(a + 1280, rows)
+        part = lambda t: t[a:b]  # noqa: E731
+        y1, p1, g1, u1 = blank(b - a, cols, dtype), storage(b - a, cols), storage(b - a, cols), storage(b - a, cols)
+        ps.opt_gated(part(g), part(u), y=y1, codes=p1[0], scales=p1[1], gate_kept=g1, up_kept=u1)
+        assert torch.equal(y1, part(y))
+        for one, whole in ((p1, pair), (g1, gk), (u1, uk)):
+            assert torch.equal(one[0], part(whole[0]))
+            assert (ref.scale_bytes_of(one[1], b - a, cols) == ref.scale_bytes_of(whole[1][a // 128 * tiles:], b - a, cols)).all()
+        d1, e1 = blank(b - a, cols, dtype), blank(b - a, cols, dtype)
+        ps.opt_gated_backward(part(dy), g1, u1, dgate=d1, dup=e1)
+        assert torch.equal(d1, part(dg)) and torch.equal(e1, part(du))
+
+
+@pytest.mark.parametrize("rows,cols", [(3001, 4008), (20000, 130), (130, 20000)])
+def test_many_tiles_turned(rows, cols):
+    """More tiles than the device holds at once: the quantizer's codes of the same values."""
+    pair = kept(matrix(rows, cols, "f32", 140, std=0.3))
+    x, (ct, st), (c1, s1) = blank(rows, cols, "f32"), storage(cols, rows), storage(cols, rows)
+    ps.opt_dequantize(*pair, x=x, codes_t=ct, scales_t=st)
+    ps.opt_quantize(x, codes_t=c1, scales_t=s1)
+    assert torch.equal(ct, c1) and torch.equal(st, s1)
+    ps.opt_dequantize(*pair, codes_t=c1, scales_t=s1)
+    assert torch.equal(ct, c1) and torch.equal(st, s1)
+    y = blank(rows, cols, "bf16")
+    ps.opt_dequantize(*pair, x=y)
+    assert torch.equal(y, x.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,hq,hk,dim,rot,interleaved", [
+    (9000, 9, 2, 64, 64, False), (6001, 12, 12, 128, 64, True), (4000, 1, 0, 256, 256, False), (5000, 40, 3, 16, 16, False),
+    (9000, 5, 1, 96, 96, False), (7000, 3, 2, 100, 50, True), (3, 2000, 300, 128, 128, False), (2, 700, 0, 80, 16, True)])
+def test_many_heads_are_those_of_fewer(dtype, rows, hq, hk, dim, rot, interleaved):
+    """More rows than warps, and more heads than a strip: the same bits as slice by slice, for
+    kept and plain inputs; the weights' gradients in any case near the exact ones."""
+    cos, sin = tables(500, rot)
+    at = places(rows, 500, 3)
+    how = dict(cos=cos, sin=sin, interleaved=interleaved)
+    w = [(1 + 0.2 * matrix(1, dim, "f32", 150 + i)[0]).contiguous() for i in range(2)]
+    x = [matrix(rows, h * dim, dtype, 152 + i) for i, h in enumerate((hq, hk))]
+    d = [matrix(rows, h * dim, dtype, 154 + i, std=0.1) for i, h in enumerate((hq, hk))]
+
+    def both(a, b, source):
+        n = b - a
+        out, keep = [blank(n, h * dim, dtype) for h in (hq, hk)], [storage(n, h * dim) for h in (hq, hk)]
+        dx, dw = [blank(n, h * dim, dtype) for h in (hq, hk)], [torch.empty(dim, device="cuda") for _ in range(2)]
+        t = [v[a:b] for v in x]
+        k = dict(k=t[1], k_weight=w[1], k_out=out[1], k_kept=keep[1]) if hk else {}
+        ps.opt_head_norm(t[0], w[0], out[0], q_kept=keep[0], positions=at[a:b], **k, **how)
+        s = keep if source == "kept" else t
+        k = dict(dk_out=d[1][a:b], k=s[1], k_weight=w[1], dk=dx[1], dk_weight=dw[1]) if hk else {}
+        ps.opt_head_norm_backward(d[0][a:b], s[0], w[0], dx[0], dq_weight=dw[0], positions=at[a:b], **k, **how)
+        return out, [p[0] for p in keep], dx, dw
+
+    step = max(rows // 7, 1)
+    for source in ("plain", "kept"):
+        out, codes, dx, dw = both(0, rows, source)
+        for a in range(0, rows, step):
+            b = min(a + step, rows)
+            for whole, part in zip((out, codes, dx), both(a, b, source)):
+                assert all(torch.equal(p, q[a:b]) for p, q in zip(part, whole))
+        if source == "plain":
+            c, s = (t.double().cpu().numpy()[at.cpu().numpy()] for t in (cos, sin))
+            for i, h in enumerate((hq, hk)[:2 if hk else 1]):
+                _, _, want, size = act.head_norm_backward(f64(heads_of(d[i], dim)), f64(heads_of(x[i], dim)), f64(w[i]), 1e-5, c, s, rot, interleaved)
+                assert (np.abs(f64(dw[i]) - want) <= E24 * (rows * h + dim / 32 + 30) * size).all()
+
+
+def test_rows_far_apart():
+    """Rows so far apart that 32-bit offsets inside a tile would not hold them."""
+    pitch, rows, cols = (1 << 24) + 64, 5, 264
+    wide = [torch.empty(rows * pitch, dtype=torch.bfloat16, device="cuda").view(rows, pitch)[:, :cols] for _ in range(3)]
+    near = [matrix(rows, cols, "bf16", 160 + i) for i in range(3)]
+    for a, b in zip(wide, near):
+        a.copy_(b)
+    got, want = training_outputs(rows, cols), training_outputs(rows, cols)
+    ps.opt_gated_backward(wide[0], wide[1], wide[2], **got)
+    ps.opt_gated_backward(near[0], near[1], near[2], **want)
+    for name in got:
+        assert all(torch.equal(p, q) for p, q in zip(got[name], want[name])), name
+    codes = [torch.empty(rows * pitch, dtype=torch.uint8, device="cuda").view(rows, pitch)[:, :cols] for _ in range(2)]
+    kg, ku = kept(near[1]), kept(near[2])
+    codes[0].copy_(kg[0])
+    codes[1].copy_(ku[0])
+    ps.opt_gated_backward(near[0], (codes[0], kg[1]), (codes[1], ku[1]), **got)
+    ps.opt_gated_backward(near[0], kg, ku, **want)
+    for name in got:
+        assert all(torch.equal(p, q) for p, q in zip(got[name], want[name])), name
+    a, b = storage(cols, rows), storage(cols, rows)
+    ps.opt_dequantize(codes[0], kg[1], codes_t=a[0], scales_t=a[1])
+    ps.opt_dequantize(*kg, codes_t=b[0], scales_t=b[1])
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    w = torch.ones(8, device="cuda")
+    one, two = torch.empty_like(near[0]), torch.empty_like(near[0])
+    ps.opt_head_norm(wide[1], w, one)
+    ps.opt_head_norm(near[1], w, two)
+    assert torch.equal(one, two)
+    ps.opt_head_norm_backward(wide[0], wide[1], w, one)
+    ps.opt_head_norm_backward(near[0], near[1], w, two)
+    assert torch.equal(one, two)
+
+
+def test_rows_behind_the_last_stay():
+    """Codes and plain outputs of a padded batch: rows behind the given ones keep what they hold."""
+    rows, cols, more = 200, 256, 56
+    buffers = {n: torch.full((rows + more, cols), 0x55, dtype=torch.uint8, device="cuda") for n in ("codes", "gate", "up", "dgate", "dup")}
+    tall = torch.full((rows + more, cols), 7.0, dtype=torch.bfloat16, device="cuda")
+    scales = lambda: torch.zeros(ps.opt_scales_bytes(rows, cols), dtype=torch.uint8, device="cuda")  # noqa: E731
+    pair = {n: (b[:rows], scales()) for n, b in buffers.items()}
+    x = matrix(rows, cols, "bf16", 170)
+    ps.opt_gated(x, x, y=tall[:rows], codes=pair["codes"][0], scales=pair["codes"][1], gate_kept=pair["gate"], up_kept=pair["up"])
+    t = {n: storage(cols, rows) for n in ("dgate_codes_t", "dup_codes_t", "y_codes_t")}
+    ps.opt_gated_backward(x, pair["gate"], pair["up"], dgate_codes=pair["dgate"], dup_codes=pair["dup"], **t)
+    ps.opt_dequantize(*pair["gate"], x=tall[:rows], codes_t=t["y_codes_t"][0], scales_t=t["y_codes_t"][1])
+    ps.opt_head_norm(x, torch.ones(64, device="cuda"), tall[:rows])
+    assert all((b[rows:] == 0x55).all() for b in buffers.values()) and (tall[rows:] == 7).all()
+
+
+def test_two_graphs_and_a_call_at_once():
+    """Two captured backward passes with workspaces of their own, replayed on two streams while
+    eager calls run on a third: each has its own results."""
+    rows, heads, dim = 3000, 6, 64
+    w = torch.ones(dim, device="cuda")
+    cos, sin = tables(rows, dim)
+    jobs = []
+    for i in range(3):
+        x, d = matrix(rows, heads * dim, "bf16", 180 + i), matrix(rows, heads * dim, "bf16", 190 + i)
+        jobs.append(dict(x=x, d=d, dx=torch.empty_like(x), dw=torch.empty(dim, device="cuda"),
+                         work=torch.empty(ps.opt_head_norm_backward_workspace(rows, heads, 0, dim), dtype=torch.uint8, device="cuda")))
+
+    def call(j, stream=None):
+        ps.opt_head_norm_backward(j["d"], j["x"], w, j["dx"], dq_weight=j["dw"], cos=cos, sin=sin, workspace=j["work"], stream=stream)
+
+    want = []
+    for j in jobs:
+        call(j)
+        torch.cuda.synchronize()
+        want.append((j["dx"].clone(), j["dw"].clone()))
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    graphs = []
+    for j, s in zip(jobs[:2], streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            call(j)
+            call(j)
+        graphs.append(g)
+    for j in jobs:
+        j["dx"].zero_()
+        j["dw"].zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        call(jobs[2], streams[2])
+    torch.cuda.synchronize()
+    for j, (dx, dw) in zip(jobs, want):
+        assert torch.equal(j["dx"], dx) and torch.equal(j["dw"], dw)
+
+
+def test_refused_calls_write_nothing():
+    x, y = matrix(4, 64, "bf16", 200), torch.full((4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    w, pair = torch.ones(64, device="cuda"), storage(4, 64)
+    cos, sin = tables(4, 64)
+    bad = [lambda: ps.opt_gated(x, x[:3], y=y), lambda: ps.opt_gated(x, y=y.float()), lambda: ps.opt_gated(x, y=y, gate_kept=(pair[0], pair[1][:256])),
+           lambda: ps.opt_gated(x, y=y, up_kept=pair), lambda: ps.opt_gated(x), lambda: ps.opt_gated_backward(x, pair, x, dgate=y, dup=y),
+           lambda: ps.opt_gated_backward(x, x, dgate=y, dup=y), lambda: ps.opt_gated_backward(x, x, x),
+           lambda: ps.opt_gated_backward(x, x, x, dgate=y, dgate_codes_t=pair), lambda: ps.opt_dequantize(*pair),
+           lambda: ps.opt_dequantize(*pair, x=y[:3]), lambda: ps.opt_head_norm(x, w[:63], y), lambda: ps.opt_head_norm(x, w, y, k=x),
+           lambda: ps.opt_head_norm(x, w, y, k_out=y), lambda: ps.opt_head_norm(x, w, y, cos=cos), lambda: ps.opt_head_norm(x, w, y, cos=cos, sin=sin[:3]),
+           lambda: ps.opt_head_norm(x, w, y, cos=cos, sin=sin, positions=torch.zeros(3, dtype=torch.int64, device="cuda")),
+           lambda: ps.opt_head_norm(x, w, y, cos=cos, sin=sin, positions=torch.zeros(4, dtype=torch.int32, device="cuda")),
+           lambda: ps.opt_head_norm(x, w, y, cos=cos.t(), sin=sin.t()), lambda: ps.opt_head_norm(x, w, y, eps=-1.0), lambda: ps.opt_head_norm(x, w, y, eps=1e300),
+           lambda: ps.opt_head_norm(x, w, y, k=x[:3], k_weight=w, k_out=y[:3]), lambda: ps.opt_head_norm(x, w[:32], y, cos=cos, sin=sin),
+           lambda: ps.opt_head_norm_backward(x, pair, w, y, dk_out=x, k=x, k_weight=w, dk=y), lambda: ps.opt_head_norm_backward(x, x, w, y, k=x),
+           lambda: ps.opt_head_norm_backward(x, x, w, y, dq_weight=torch.empty(64, device="cuda"), workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))]
+    for call in bad:
+        with pytest.raises((ValueError, ps.OptError)):
+            call()
+    torch.cuda.synchronize()
+    assert (y == 7).all() and (pair[1] == 0xEE).all()
