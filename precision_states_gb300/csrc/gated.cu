@@ -693,7 +693,8 @@ cudaError_t backward_turn(const opt_gated_backward_args& a, int sm_count, cudaSt
   static OccupancyCache cache;
   const auto kernel = gated_backward_turn_kernel<KIND>;
   const int row_tiles = (int)((a.rows + 127) / 128), col_tiles = (int)((a.cols + 127) / 128);
-  const int64_t tiles = (int64_t)row_tiles * col_tiles, most = (int64_t)sm_count * cached_occupancy(kernel, cache, kTurnThreads, kTurnBytes);
+  const int64_t tiles = (int64_t)row_tiles * col_tiles, held = (int64_t)sm_count * cached_occupancy(kernel, cache, kTurnThreads, kTurnBytes);
+  const int64_t most = held > 0 ? held : 1;      // (none where the device refuses that much shared memory: the launch says so)
   const int per_cta = (int)((tiles + most - 1) / most);
   kernel<<<(unsigned)((tiles + per_cta - 1) / per_cta), kTurnThreads, kTurnBytes, s>>>(a, row_tiles, col_tiles, per_cta);
   return cudaGetLastError();

@@ -483,7 +483,7 @@ template <typename T, typename S, typename W, bool INTERLEAVED, int U>
 __global__ void __launch_bounds__(kThreads, 2) head_norm_backward_kernel(const __grid_constant__ HeadCall a,
                                                                         Sets sets, float* parts) {
   __shared__ float sums[kWarps][32][8];
-  let_sums_start();
+  if (parts != nullptr) let_sums_start();
   const int dim = a.dim, rot = a.rot;
   const Lane l = lane_of(sets, dim, rot, U);
   const Side& side = a.side[l.keys];
@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, kBackwardCtas) head_norm_backward_st
   __shared__ float sums[kWarps][32][8];
   __shared__ __align__(16) TurnLines lines_of[kWarps];
   TurnLines& lines = lines_of[threadIdx.x >> 5];
-  let_sums_start();
+  if (parts != nullptr) let_sums_start();
   constexpr bool KEPT = sizeof(S) == 1;
   const int dim = a.dim, rot = a.rot, strip = (int)(blockIdx.x % (uint32_t)strips.strips);
   const bool keys = strip >= strips.q_strips;
@@ -732,7 +732,7 @@ __global__ void __launch_bounds__(32 * kAnyWarps) head_norm_backward_any_kernel(
     const __grid_constant__ HeadCall a, int q_ctas, float* parts) {
   __shared__ float held[kAnyWarps][2][kHeadMaxDim];
   __shared__ float sums[kAnyWarps][kHeadMaxDim];
-  let_sums_start();
+  if (parts != nullptr) let_sums_start();
   const int wi = threadIdx.x >> 5, lane = threadIdx.x & 31, dim = a.dim, rot = a.rot;
   float *x = held[wi][0], *d = held[wi][1], *dw = sums[wi];
   const bool keys = (int)blockIdx.x >= q_ctas;

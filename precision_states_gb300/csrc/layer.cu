@@ -300,17 +300,12 @@ int opt_head_norm_backward(const opt_head_norm_backward_args* a, void* stream) {
   PS_TRY(check_heads(*a));
   const int64_t es = plain_size(a->dtype), ws = plain_size(a->weight_dtype);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  float* dq = a->q_heads > 0 ? a->d_dq_weight : nullptr;
-  float* dk = a->k_heads > 0 ? a->d_dk_weight : nullptr;
+  float *dq = a->d_dq_weight, *dk = a->d_dk_weight;
   if (dq != nullptr) PS_TRY(check_matrix(dq, a->dim, 1, a->dim, 4));
   if (dk != nullptr) PS_TRY(check_matrix(dk, a->dim, 1, a->dim, 4));
-  if (a->q_heads + a->k_heads == 0) return OPT_OK;
-  if (a->rows == 0) {      // the sums over no rows
-    if (dq != nullptr) PS_TRY(status_of(cudaMemsetAsync(dq, 0, (size_t)a->dim * sizeof(float), s)));
-    return dk == nullptr ? OPT_OK : status_of(cudaMemsetAsync(dk, 0, (size_t)a->dim * sizeof(float), s));
-  }
-  if (a->q_heads > 0 && a->k_heads > 0 && (a->d_q_scales != nullptr) != (a->d_k_scales != nullptr)) return OPT_EINVAL;
-  if (a->q_heads > 0) {
+  const bool q_side = a->rows > 0 && a->q_heads > 0, k_side = a->rows > 0 && a->k_heads > 0;
+  if (q_side && k_side && (a->d_q_scales != nullptr) != (a->d_k_scales != nullptr)) return OPT_EINVAL;
+  if (q_side) {
     const int64_t cols = a->q_heads * a->dim;
     PS_TRY(check_matrix(a->d_dq_out, a->dq_out_pitch, a->rows, cols, es));
     if (a->d_q_scales != nullptr) PS_TRY(check_codes(a->d_q, a->q_pitch, a->d_q_scales, a->rows, cols));
@@ -318,7 +313,7 @@ int opt_head_norm_backward(const opt_head_norm_backward_args* a, void* stream) {
     PS_TRY(check_matrix(a->d_q_weight, a->dim, 1, a->dim, ws));
     PS_TRY(check_matrix(a->d_dq, a->dq_pitch, a->rows, cols, es));
   }
-  if (a->k_heads > 0) {
+  if (k_side) {
     const int64_t cols = a->k_heads * a->dim;
     PS_TRY(check_matrix(a->d_dk_out, a->dk_out_pitch, a->rows, cols, es));
     if (a->d_k_scales != nullptr) PS_TRY(check_codes(a->d_k, a->k_pitch, a->d_k_scales, a->rows, cols));
@@ -326,17 +321,25 @@ int opt_head_norm_backward(const opt_head_norm_backward_args* a, void* stream) {
     PS_TRY(check_matrix(a->d_k_weight, a->dim, 1, a->dim, ws));
     PS_TRY(check_matrix(a->d_dk, a->dk_pitch, a->rows, cols, es));
   }
-  PS_TRY(check_turn(*a));
-  if (dq != nullptr || dk != nullptr) {
+  if (q_side || k_side) PS_TRY(check_turn(*a));
+  const bool sums = (q_side && dq != nullptr) || (k_side && dk != nullptr);
+  if (sums) {
     if (a->d_workspace == nullptr ||
         a->workspace_bytes < opt_head_norm_backward_workspace(a->rows, a->q_heads, a->k_heads, a->dim)) return OPT_EINVAL;
     if ((uintptr_t)a->d_workspace & 15u) return OPT_EALIGN;
   }
-  opt_head_norm_backward_args b = *a;      // a side without heads has nothing
-  b.d_dq_weight = dq;
-  b.d_dk_weight = dk;
-  if (a->q_heads == 0) b.d_q_scales = nullptr;
-  if (a->k_heads == 0) b.d_k_scales = nullptr;
+  opt_head_norm_backward_args b = *a;
+  if (!q_side) {      // no rows or no heads: a sum of nothing
+    if (dq != nullptr) PS_TRY(status_of(cudaMemsetAsync(dq, 0, (size_t)a->dim * sizeof(float), s)));
+    b.d_dq_weight = nullptr;
+    b.d_q_scales = nullptr;
+  }
+  if (!k_side) {
+    if (dk != nullptr) PS_TRY(status_of(cudaMemsetAsync(dk, 0, (size_t)a->dim * sizeof(float), s)));
+    b.d_dk_weight = nullptr;
+    b.d_k_scales = nullptr;
+  }
+  if (!q_side && !k_side) return OPT_OK;
   int sms = 0;
   PS_TRY(sm_count_of(&sms));
   return status_of(launch_head_norm_backward(b, sms, s));

@@ -101,7 +101,7 @@ E, U, A, L, OK = ps.OPT_EINVAL, ps.OPT_EUNSUPPORTED, ps.OPT_EALIGN, ps.OPT_ELIMI
     ("opt_head_norm_backward", BACK, dict(d_q_scales=P, d_k_scales=P, k_pitch=40), A), ("opt_head_norm_backward", BACK, dict(d_dq=0), E),
     ("opt_head_norm_backward", BACK, dict(d_dk_out=0), E), ("opt_head_norm_backward", BACK, dict(d_dq_weight=P + 2), A),
     ("opt_head_norm_backward", BACK, dict(flags=4), E), ("opt_head_norm_backward", BACK, dict(d_positions=0, positions=2), E),
-    ("opt_head_norm_backward", BACK, dict(rows=-1), E), ("opt_head_norm_backward", BACK, dict(q_heads=0, k_heads=0), OK),
+    ("opt_head_norm_backward", BACK, dict(rows=-1), E), ("opt_head_norm_backward", BACK, dict(q_heads=0, k_heads=0, d_dq_weight=0, d_dk_weight=0), OK),
 ])
 def test_refusals(name, base, change, status):
     assert call(name, **{**base, **change}) == status

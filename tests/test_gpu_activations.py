@@ -447,6 +447,11 @@ def test_no_rows_and_no_columns():
     ps.opt_head_norm(none, w, none)
     ps.opt_head_norm_backward(none, none, w, none, dq_weight=dw)
     assert (dw == 0).all()
+    q, k = matrix(3, 64, "f32", 210), torch.empty(3, 0, device="cuda")       # no key heads
+    dw.fill_(7.0)
+    ps.opt_head_norm(q, w, q, k, w, k)
+    ps.opt_head_norm_backward(q, q, w, q, k, k, w, k, dk_weight=dw)
+    assert (dw == 0).all()
     for shape in ((0, 64), (5, 0)):
         x = torch.empty(*shape, device="cuda")
         c, s = ps.e4m3_storage(*shape)
