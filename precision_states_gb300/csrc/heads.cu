@@ -108,139 +108,11 @@ __device__ __forceinline__ Raw<float> partner_of(const Raw<float>& x, int partne
   return r;
 }
 
-// How the warps share the heads: a set is `per_set` heads of one side, `slots` side by
-// side in a warp, U after one another; sets of queries come first.
-struct Sets {
-  int lanes, slots;              // lanes to a head, heads side by side
-  int q_sets, sets;              // of queries; of both
-  int64_t stride;                // rows between a warp's: warps of the grid / sets
-  int warps;                     // that take part
-};
-
-// A lane's eight elements of the rotation at a row: c, and s' with the partner's sign.
-// Elements that are not rotated have c 1 and s' 0.
-template <bool INTERLEAVED>
-__device__ __forceinline__ void turn_of(const float* cos, const float* sin, const int64_t* positions, int64_t table, int rot,
-                                        int64_t r, int e, float (&c)[8], float (&s)[8]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    c[j] = 1.0f;
-    s[j] = 0.0f;
-  }
-  if (e >= rot) return;
-  const int64_t at = positions != nullptr ? positions[r] : r;
-  if (at < 0 || at >= table) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) c[j] = s[j] = u2f(0x7FC00000u);
-    return;
-  }
-  const int half = rot >> 1;
-  if constexpr (INTERLEAVED) {
-    const int64_t p = at * half + (e >> 1);
-    const float4 cv = __ldg(reinterpret_cast<const float4*>(cos + p)), sv = __ldg(reinterpret_cast<const float4*>(sin + p));
-    const float cs[4] = {cv.x, cv.y, cv.z, cv.w}, ss[4] = {sv.x, sv.y, sv.z, sv.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      c[2 * j] = c[2 * j + 1] = cs[j];
-      s[2 * j] = -ss[j];
-      s[2 * j + 1] = ss[j];
-    }
-  } else {
-    const bool second = e >= half;
-    const int64_t p = at * half + (second ? e - half : e);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float4 cv = __ldg(reinterpret_cast<const float4*>(cos + p) + k), sv = __ldg(reinterpret_cast<const float4*>(sin + p) + k);
-      c[4 * k] = cv.x; c[4 * k + 1] = cv.y; c[4 * k + 2] = cv.z; c[4 * k + 3] = cv.w;
-      s[4 * k] = sv.x; s[4 * k + 1] = sv.y; s[4 * k + 2] = sv.z; s[4 * k + 3] = sv.w;
-    }
-    if (!second) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s[j] = -s[j];
-    }
-  }
-}
-
-// What a lane of a set of heads is.
-struct Lane {
-  int e, partner;                // its first element in the head; the lane with the partners' elements
-  bool on;                       // it has elements
-  int64_t head, head_step;       // its first head, and from one to the next
-  bool keys;
-  int64_t first_row;
-};
-__device__ __forceinline__ Lane lane_of(const Sets& sets, int dim, int rot, int u) {
-  Lane l;
-  const int lane = threadIdx.x & 31, in = lane & (sets.lanes - 1);
-  const int64_t warp = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int set = (int)(warp % sets.sets);
-  l.first_row = warp < sets.warps ? warp / sets.sets : (int64_t)1 << 62;
-  l.keys = set >= sets.q_sets;
-  l.e = 8 * in;
-  l.on = l.e < dim;
-  const int half = rot >> 1;
-  l.partner = lane + (l.e >= rot ? 0 : l.e < half ? half >> 3 : -(half >> 3));
-  l.head_step = sets.slots;
-  l.head = (int64_t)(l.keys ? set - sets.q_sets : set) * sets.slots * u + lane / sets.lanes;
-  return l;
-}
-
-// Row r, element e of the head: the column.
-template <typename T, typename W, bool INTERLEAVED, int U>
-__global__ void __launch_bounds__(kThreads, 2) head_norm_kernel(const __grid_constant__ HeadCall a, Sets sets) {
-  const int dim = a.dim, rot = a.rot;
-  const Lane l = lane_of(sets, dim, rot, U);
-  if (l.first_row >= a.rows) return;
-  const Side& side = a.side[l.keys];
-  const int64_t panel = (side.cols + 511) / 512;
-  const float inv_dim = 1.0f / (float)dim;
-  float w[8] = {}, wp[8] = {};
-  if (l.on) {
-    const Raw<W> raw = load_raw<true>(static_cast<const W*>(side.weight) + l.e, 8);
-    unpack(raw, w);
-    const int pe = INTERLEAVED ? l.e : 8 * (l.partner & (sets.lanes - 1));
-    float v[8];
-    unpack(load_raw<true>(static_cast<const W*>(side.weight) + pe, 8), v);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) wp[j] = v[INTERLEAVED ? j ^ 1 : j];
-  }
-  for (int64_t r = l.first_row; r < a.rows; r += sets.stride) {
-    Raw<T> x[U];
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      x[k] = {};
-      const int64_t h = l.head + k * l.head_step;
-      if (l.on && h < side.heads) x[k] = load_raw<true>(static_cast<const T*>(side.x) + r * side.x_pitch + h * dim + l.e, 8);
-    }
-    float c[8], s[8];
-    turn_of<INTERLEAVED>(a.cos, a.sin, a.positions, a.table, rot, r, l.e, c, s);
-    times8(c, w);
-    times8(s, wp);
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int64_t h = l.head + k * l.head_step, col = h * dim + l.e;
-      const bool on = l.on && h < side.heads;
-      float v[8], p[8], y[8];
-      unpack(x[k], v);
-      unpack(partner_of<INTERLEAVED>(x[k], l.partner), p);
-      float sum = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sum = fmaf(v[j], v[j], sum);
-      sum = group_sum(sum, sets.lanes);
-      const float rstd = reciprocal_root(fmaf(sum, inv_dim, a.eps));
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = rstd * fmaf(v[j], c[j], l.e < rot ? p[j] * s[j] : 0.0f);
-      if (on) store8<true>(static_cast<T*>(side.out) + r * side.out_pitch + col, 8, y);
-      if (side.codes != nullptr)
-        put_codes8(static_cast<uint8_t*>(side.codes) + r * side.codes_pitch + col, static_cast<uint8_t*>(side.code_scales),
-                   scale_place(r, col >> 7, panel), on ? 8 : 0, v);
-    }
-  }
-}
-
-// ---------------------------------------------- heads of 8, 16, ... 256 elements
-// Such heads fill a warp's 256 columns, so a set is 256 U columns of its side and a lane's
-// chunks are 256 apart.  The next row's chunk is asked for as soon as this row's is taken.
+// ------------------------------------------------- heads of whole chunks of eight elements
+// A head's chunks lie side by side in a group of lanes (a power of two of them, some idle where
+// dim / 8 is none), and groups side by side fill the warp: 256 columns at a time where dim is a
+// power of two (DENSE), fewer else.  A strip is U times that of one side's columns, and a lane's
+// chunks are that far apart.  The next row's chunk is asked for as soon as this row's is taken.
 
 // Eight elements of the weight, of either type.
 __device__ __forceinline__ void weight8(const void* weight, int32_t type, int e, float (&w)[8]) {
@@ -325,20 +197,25 @@ struct Strips {
   uint32_t stride;
   int lanes;                     // lanes to a head
 };
+// Columns from a lane's chunk to its next one.
+template <bool DENSE>
+__device__ __forceinline__ uint32_t chunk_step(const Strips& strips, int dim) { return DENSE ? 256u : (uint32_t)(32 / strips.lanes * dim); }
 // What a lane is in its strip.
 struct StripLane {
-  uint32_t column;               // its first, in the side
+  uint32_t column, left;         // its first, in the side; what is there from it on (0 for an idle lane)
   uint32_t row;                  // its warp's first
   int e, pair, partner;          // of its first element: in the head, its angle; the lane with the partners
   bool rotated;
 };
-template <int U>
-__device__ __forceinline__ StripLane strip_lane(const Strips& strips, int strip, int dim, int rot, bool interleaved) {
+template <bool DENSE, int U>
+__device__ __forceinline__ StripLane strip_lane(const Strips& strips, int strip, int64_t cols, int dim, int rot, bool interleaved) {
   StripLane l;
   const int lane = threadIdx.x & 31, half = rot >> 1;
+  const uint32_t first = (uint32_t)strip * (chunk_step<DENSE>(strips, dim) * U);
   l.row = (blockIdx.x / (uint32_t)strips.strips) * kWarps + (threadIdx.x >> 5);
-  l.column = (uint32_t)strip * (256 * U) + 8 * lane;
-  l.e = (8 * lane) & (dim - 1);
+  l.e = DENSE ? (8 * lane) & (dim - 1) : 8 * (lane & (strips.lanes - 1));
+  l.column = first + (DENSE ? 8 * lane : lane / strips.lanes * dim + l.e);
+  l.left = !DENSE && l.e >= dim ? 0u : (uint32_t)cols - min(l.column, (uint32_t)cols);
   l.rotated = l.e < rot;
   l.pair = !l.rotated ? 0 : interleaved ? l.e >> 1 : l.e < half ? l.e : l.e - half;
   l.partner = !l.rotated ? lane : lane + (l.e < half ? half >> 3 : -(half >> 3));
@@ -352,7 +229,7 @@ __device__ __forceinline__ uint64_t scale_row(uint32_t r, uint32_t panel512) {
   return (uint64_t)(r >> 7) * panel512 + (16 * (r & 31) + ((r >> 3) & 12));
 }
 
-template <typename T, bool INTERLEAVED, bool KEEP, int LANES, int U>
+template <typename T, bool INTERLEAVED, bool KEEP, bool DENSE, int LANES, int U>
 __global__ void __launch_bounds__(kThreads, kForwardCtas) head_norm_strip_kernel(const __grid_constant__ HeadCall a,
                                                                                 const Strips strips) {
   // the weight, and its partner's with the sign of the partner's term (minus for a pair's
@@ -363,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, kForwardCtas) head_norm_strip_kernel
   const int dim = a.dim, rot = a.rot, half = rot >> 1, strip = (int)(blockIdx.x % (uint32_t)strips.strips);
   const bool keys = strip >= strips.q_strips;
   const Side& side = a.side[keys];
-  const StripLane l = strip_lane<U>(strips, keys ? strip - strips.q_strips : strip, dim, rot, INTERLEAVED);
+  const StripLane l = strip_lane<DENSE, U>(strips, keys ? strip - strips.q_strips : strip, side.cols, dim, rot, INTERLEAVED);
   if ((int)threadIdx.x < dim) {
     const int e = threadIdx.x, p = e >= rot ? e : INTERLEAVED ? e ^ 1 : e < half ? e + half : e - half;
     const float v = weight_at(side.weight, a.weight_dtype, p);
@@ -372,14 +249,14 @@ __global__ void __launch_bounds__(kThreads, kForwardCtas) head_norm_strip_kernel
   }
   __syncthreads();
   const uint32_t rows = (uint32_t)a.rows, panel = 512 * (uint32_t)((side.cols + 511) / 512);
-  const uint32_t left = (uint32_t)side.cols - min(l.column, (uint32_t)side.cols);      // chunk k exists where 256 k is below
+  const uint32_t left = l.left, step = chunk_step<DENSE>(strips, dim);      // chunk k exists where k step is below left
   const uint32_t place = 512 * (l.column >> 9) + ((l.column >> 7) & 3);
   const float inv_dim = 1.0f / (float)dim;
   const bool keep = KEEP && side.codes != nullptr;
   if (l.row >= rows) return;
   Raw<T> x[U];
 #pragma unroll
-  for (int k = 0; k < U; ++k) x[k] = load_if(static_cast<const T*>(side.x) + (l.row * side.x_pitch + l.column) + 256 * k, 256 * k < left);
+  for (int k = 0; k < U; ++k) x[k] = load_if(static_cast<const T*>(side.x) + (l.row * side.x_pitch + l.column) + step * k, step * k < left);
   const auto position = [&](uint32_t r) { return a.positions == nullptr ? (int64_t)r : r < rows ? a.positions[r] : (int64_t)0; };
   int64_t at = 0;
   if (rot > 0) {
@@ -410,8 +287,8 @@ __global__ void __launch_bounds__(kThreads, kForwardCtas) head_norm_strip_kernel
 #pragma unroll
     for (int k = 0; k < U; k += 2) {      // two chunks' exchanges side by side
       const Raw<T> raw[2] = {x[k], x[k + 1]};
-      x[k] = load_if(ahead + 256 * k, 256 * k < left && next < rows);
-      x[k + 1] = load_if(ahead + 256 * (k + 1), 256 * (k + 1) < left && next < rows);
+      x[k] = load_if(ahead + step * k, step * k < left && next < rows);
+      x[k + 1] = load_if(ahead + step * (k + 1), step * (k + 1) < left && next < rows);
       float rstd[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -433,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, kForwardCtas) head_norm_strip_kernel
       lanes_sums<LANES, 2>(rstd, strips.lanes);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const bool on = 256 * (k + i) < left;
+        const bool on = step * (k + i) < left;
         const float root = reciprocal_root(fmaf(rstd[i], inv_dim, a.eps));
         const f2_t scale = pk(root, root);
         float v[8], y[8];
@@ -448,98 +325,19 @@ __global__ void __launch_bounds__(kThreads, kForwardCtas) head_norm_strip_kernel
 #pragma unroll
           for (int j = 0; j < 8; j += 2) unpk(mul2(mul2(pk(v[j], v[j + 1]), pk(w[j], w[j + 1])), scale), y[j], y[j + 1]);
         }
-        store8_if(out + 256 * (k + i), y, on);
+        store8_if(out + step * (k + i), y, on);
         if (keep) {
           uint8_t* to = scales + (512 * (k >> 1) + 2 * i);      // blocks 2 (k + i) and the next of the strip
-          if (__any_sync(0xFFFFFFFFu, top[i] >= kInfBits)) put_codes8(codes + 256 * (k + i), to, 0, on ? 8 : 0, v);
-          else put_finite_if(codes + 256 * (k + i), to, v, top[i], on, on && (threadIdx.x & 15) == 0);
+          if (__any_sync(0xFFFFFFFFu, top[i] >= kInfBits)) put_codes8(codes + step * (k + i), to, 0, on ? 8 : 0, v);
+          else put_finite_if(codes + step * (k + i), to, v, top[i], on, on && (threadIdx.x & 15) == 0);
         }
       }
     }
   }
 }
 
-// A CTA's row of the partial sums, 2 x dim with queries' first: over the warps that had a side,
-// and the heads side by side in them, in order.
-__device__ __forceinline__ void leave_sums(float (&sums)[kWarps][32][8], const float (&dw)[8], const Sets& sets, int dim, float* parts) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) sums[threadIdx.x >> 5][threadIdx.x & 31][j] = dw[j];
-  __syncthreads();
-  float* out = parts + (int64_t)blockIdx.x * 2 * dim;
-  for (int t = threadIdx.x; t < 2 * dim; t += kThreads) {
-    const bool keys = t >= dim;
-    const int e = keys ? t - dim : t;
-    float v = 0.0f;
-    for (int k = 0; k < kWarps; ++k) {
-      const int64_t warp = (int64_t)blockIdx.x * kWarps + k;
-      if (warp >= sets.warps || ((int)(warp % sets.sets) >= sets.q_sets) != keys) continue;
-      for (int i = 0; i < sets.slots; ++i) v += sums[k][i * sets.lanes + (e >> 3)][e & 7];
-    }
-    out[t] = v;
-  }
-}
-
-template <typename T, typename S, typename W, bool INTERLEAVED, int U>
-__global__ void __launch_bounds__(kThreads, 2) head_norm_backward_kernel(const __grid_constant__ HeadCall a,
-                                                                        Sets sets, float* parts) {
-  __shared__ float sums[kWarps][32][8];
-  if (parts != nullptr) let_sums_start();
-  const int dim = a.dim, rot = a.rot;
-  const Lane l = lane_of(sets, dim, rot, U);
-  const Side& side = a.side[l.keys];
-  const float inv_dim = 1.0f / (float)dim;
-  float w[8] = {}, dw[8] = {};
-  if (l.on && l.first_row < a.rows) unpack(load_raw<true>(static_cast<const W*>(side.weight) + l.e, 8), w);
-  for (int64_t r = l.first_row; r < a.rows; r += sets.stride) {
-    const Source<S, true> x_row(side.x, side.scales, side.x_pitch, a.rows, side.cols, r);
-    Raw<T> d[U];
-    typename Source<S, true>::Ask x[U];
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      d[k] = {};
-      x[k] = {};
-      const int64_t h = l.head + k * l.head_step;
-      if (l.on && h < side.heads) {
-        d[k] = load_raw<true>(static_cast<const T*>(side.dout) + r * side.dout_pitch + h * dim + l.e, 8);
-        x[k] = x_row.ahead(h * dim + l.e, 8);
-      }
-    }
-    float c[8], s[8];
-    turn_of<INTERLEAVED>(a.cos, a.sin, a.positions, a.table, rot, r, l.e, c, s);
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int64_t h = l.head + k * l.head_step, col = h * dim + l.e;
-      const bool on = l.on && h < side.heads;
-      float v[8], g[8], p[8];
-      x_row.values(x[k], col, 8, v);
-      unpack(d[k], g);
-      unpack(partner_of<INTERLEAVED>(d[k], l.partner), p);
-      float square = 0.0f, dot = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        // the turn back has the opposite sign; s' belongs to this element
-        g[j] = fmaf(g[j], c[j], l.e < rot ? -p[j] * s[j] : 0.0f);
-        square = fmaf(v[j], v[j], square);
-        dot = fmaf(g[j] * w[j], v[j], dot);
-      }
-      square = group_sum(square, sets.lanes);
-      dot = group_sum(dot, sets.lanes);
-      const float rstd = reciprocal_root(fmaf(square, inv_dim, a.eps));
-      const float pull = rstd * rstd * (dot * inv_dim);
-      if (on) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) dw[j] = fmaf(g[j], v[j] * rstd, dw[j]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] = rstd * fmaf(-v[j], pull, g[j] * w[j]);
-        store8<true>(static_cast<T*>(side.out) + r * side.out_pitch + col, 8, g);
-      }
-    }
-  }
-  if (parts != nullptr) leave_sums(sums, dw, sets, dim, parts);
-}
-
 // The gradients of strips.
-template <typename T, typename S, bool INTERLEAVED, int LANES, int U>
+template <typename T, typename S, bool INTERLEAVED, bool DENSE, int LANES, int U>
 __global__ void __launch_bounds__(kThreads, kBackwardCtas) head_norm_backward_strip_kernel(
     const __grid_constant__ HeadCall a, const Strips strips, float* parts) {
   __shared__ float sums[kWarps][32][8];
@@ -550,13 +348,18 @@ __global__ void __launch_bounds__(kThreads, kBackwardCtas) head_norm_backward_st
   const int dim = a.dim, rot = a.rot, strip = (int)(blockIdx.x % (uint32_t)strips.strips);
   const bool keys = strip >= strips.q_strips;
   const Side& side = a.side[keys];
-  const StripLane l = strip_lane<U>(strips, keys ? strip - strips.q_strips : strip, dim, rot, INTERLEAVED);
+  const StripLane l = strip_lane<DENSE, U>(strips, keys ? strip - strips.q_strips : strip, side.cols, dim, rot, INTERLEAVED);
   const uint32_t rows = (uint32_t)a.rows, panel = 512 * (uint32_t)((side.cols + 511) / 512);
-  const uint32_t left = (uint32_t)side.cols - min(l.column, (uint32_t)side.cols);
+  const uint32_t left = l.left, step = chunk_step<DENSE>(strips, dim);
   const uint32_t place = 512 * (l.column >> 9) + ((l.column >> 7) & 3);
   const float inv_dim = 1.0f / (float)dim;
   float w[8];
-  weight8(side.weight, a.weight_dtype, l.e, w);
+  if (DENSE || l.e < dim) {
+    weight8(side.weight, a.weight_dtype, l.e, w);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = 0.0f;
+  }
   f2_t dw[4] = {};                 // +0 in both lanes
   // the turn back: plus for a pair's first element
   const float sign = !INTERLEAVED && l.e >= (rot >> 1) ? -1.0f : 1.0f;
@@ -564,13 +367,15 @@ __global__ void __launch_bounds__(kThreads, kBackwardCtas) head_norm_backward_st
   Raw<T> d[U];
   std::conditional_t<KEPT, KeptAsk, Raw<T>> x[U];
   const auto load = [&](int k, uint32_t r) {
-    const bool on = 256 * k < left && r < rows;
-    d[k] = load_if(static_cast<const T*>(side.dout) + (r * side.dout_pitch + l.column) + 256 * k, on);
+    const bool on = step * k < left && r < rows;
+    d[k] = load_if(static_cast<const T*>(side.dout) + (r * side.dout_pitch + l.column) + step * k, on);
     if constexpr (KEPT) {
-      x[k].codes = load_codes_if(static_cast<const uint8_t*>(side.x) + (r * side.x_pitch + l.column) + 256 * k, on);
-      x[k].byte = load_byte_if(static_cast<const uint8_t*>(side.scales) + (scale_row(r, panel) + place) + (512 * (k >> 1) + 2 * (k & 1)), on);
+      x[k].codes = load_codes_if(static_cast<const uint8_t*>(side.x) + (r * side.x_pitch + l.column) + step * k, on);
+      // a dense strip's chunks are two blocks apart
+      const uint32_t c = l.column + step * k, block = DENSE ? place + (512 * (k >> 1) + 2 * (k & 1)) : 512 * (c >> 9) + ((c >> 7) & 3);
+      x[k].byte = load_byte_if(static_cast<const uint8_t*>(side.scales) + scale_row(r, panel) + block, on);
     } else {
-      x[k] = load_if(static_cast<const T*>(side.x) + (r * side.x_pitch + l.column) + 256 * k, on);
+      x[k] = load_if(static_cast<const T*>(side.x) + (r * side.x_pitch + l.column) + step * k, on);
     }
   };
 #pragma unroll
@@ -603,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, kBackwardCtas) head_norm_backward_st
     }
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      const bool on = 256 * k < left;
+      const bool on = step * k < left;
       const Raw<T> raw = d[k];
       float v[8], g[8];
       input(k, v);
@@ -638,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, kBackwardCtas) head_norm_backward_st
         if (on) dw[j] = fma2(pk(g[2 * j], g[2 * j + 1]), mul2(xv, pk(root, root)), dw[j]);
         unpk(mul2(fma2(xv, pk(pull, pull), t[j]), pk(root, root)), dx[2 * j], dx[2 * j + 1]);
       }
-      store8_if(out + 256 * k, dx, on);
+      store8_if(out + step * k, dx, on);
     }
   }
   if (parts == nullptr) return;
@@ -705,15 +510,18 @@ __global__ void __launch_bounds__(32 * kAnyWarps) head_norm_any_kernel(const __g
     const Side& side = a.side[both >= a.side[0].heads];
     const int64_t col = (both >= a.side[0].heads ? both - a.side[0].heads : both) * dim;
     const W* weight = static_cast<const W*>(side.weight);
+    const int64_t at = rot > 0 && a.positions != nullptr ? a.positions[r] : r;
     float sum = 0.0f;
+#pragma unroll 4
     for (int j = lane; j < dim; j += 32) {
-      x[j] = element_at(side, r, col + j, 0, T());
-      sum = fmaf(x[j], x[j], sum);
+      const float v = element_at(side, r, col + j, 0, T());
+      x[j] = v;
+      sum = fmaf(v, v, sum);
     }
     sum = group_sum(sum, 32);
     const float rstd = reciprocal_root(fmaf(sum, 1.0f / (float)dim, a.eps));
     __syncwarp();
-    const int64_t at = rot > 0 && a.positions != nullptr ? a.positions[r] : r;
+#pragma unroll 4
     for (int j = lane; j < dim; j += 32) {
       int p = j;
       float c, s, y = x[j] * element(weight + j);
@@ -744,6 +552,7 @@ __global__ void __launch_bounds__(32 * kAnyWarps) head_norm_backward_any_kernel(
   for (int64_t i = cta * kAnyWarps + wi; i < n; i += ctas * kAnyWarps) {
     const int64_t r = i / side.heads, col = i % side.heads * dim;
     const int64_t at = rot > 0 && a.positions != nullptr ? a.positions[r] : r;
+#pragma unroll 4
     for (int j = lane; j < dim; j += 32) {
       x[j] = element_at(side, r, col + j, panel, S());
       d[j] = element(static_cast<const T*>(side.dout) + r * side.dout_pitch + col + j);
@@ -756,6 +565,7 @@ __global__ void __launch_bounds__(32 * kAnyWarps) head_norm_backward_any_kernel(
                  ? fmaf(d[j], c, -d[p] * s) : d[j];
     };
     float square = 0.0f, dot = 0.0f;
+#pragma unroll 4
     for (int j = lane; j < dim; j += 32) {
       square = fmaf(x[j], x[j], square);
       dot = fmaf(turned(j) * element(weight + j), x[j], dot);
@@ -764,6 +574,7 @@ __global__ void __launch_bounds__(32 * kAnyWarps) head_norm_backward_any_kernel(
     dot = group_sum(dot, 32);
     const float rstd = reciprocal_root(fmaf(square, 1.0f / (float)dim, a.eps));
     const float pull = rstd * rstd * (dot * (1.0f / (float)dim));
+#pragma unroll 4
     for (int j = lane; j < dim; j += 32) {
       const float g = turned(j);
       dw[j] = fmaf(g, x[j] * rstd, dw[j]);
@@ -832,44 +643,15 @@ Whole whole_heads(const A& a, int64_t ws) {
   return v;
 }
 
-// The warps' sets for U heads after one another, and the CTAs.
-template <typename A>
-Sets sets_of(const A& a, int u, int64_t max_ctas, int* ctas) {
-  Sets s;
-  s.lanes = 1;
-  while (8 * s.lanes < a.dim) s.lanes *= 2;
-  s.slots = 32 / s.lanes;
-  const int64_t per = (int64_t)s.slots * u;
-  s.q_sets = (int)((a.q_heads + per - 1) / per);
-  s.sets = s.q_sets + (int)((a.k_heads + per - 1) / per);
-  const int64_t need = a.rows * s.sets, have = max_ctas * kWarps;
-  // every set as many warps as rows at most; where there are more sets than warps, each set one
-  s.stride = need <= have ? a.rows : have / s.sets;
-  if (s.stride < 1) s.stride = 1;
-  s.warps = (int)(s.stride * s.sets);
-  *ctas = (s.warps + kWarps - 1) / kWarps;
-  return s;
-}
-
-template <typename T, typename W, bool INTERLEAVED>
-cudaError_t forward_heads(const opt_head_norm_args& a, int sm_count, cudaStream_t s) {
-  constexpr int U = sizeof(T) == 2 ? 4 : 2;
-  static OccupancyCache cache;
-  const auto kernel = head_norm_kernel<T, W, INTERLEAVED, U>;
-  int ctas;
-  const Sets sets = sets_of(a, U, (int64_t)sm_count * cached_occupancy(kernel, cache, kThreads, 0), &ctas);
-  kernel<<<ctas, kThreads, 0, s>>>(call_of(a), sets);
-  return cudaGetLastError();
-}
-
 // Strips of U chunks, and their CTAs: as many for each as its rows fill, within `most` in all.
 template <typename A>
 Strips strips_of(const A& a, int u, int64_t most, int64_t* ctas) {
   Strips s;
-  const int64_t width = 256 * u;
+  s.lanes = 1;
+  while (8 * s.lanes < a.dim) s.lanes *= 2;
+  const int64_t width = 32 / s.lanes * a.dim * u;
   s.q_strips = (int)((a.q_heads * a.dim + width - 1) / width);
   s.strips = s.q_strips + (int)((a.k_heads * a.dim + width - 1) / width);
-  s.lanes = (int)(a.dim / 8);
   const int64_t need = (a.rows + kWarps - 1) / kWarps, have = most / s.strips;
   const int64_t each = need <= have ? need : have > 0 ? have : 1;
   s.stride = (uint32_t)(each * kWarps);
@@ -877,22 +659,28 @@ Strips strips_of(const A& a, int u, int64_t most, int64_t* ctas) {
   return s;
 }
 
-template <typename T, bool INTERLEAVED, bool KEEP, int LANES>
+template <typename T, bool INTERLEAVED, bool KEEP, bool DENSE, int LANES>
 cudaError_t forward_strip(const opt_head_norm_args& a, int sm_count, cudaStream_t s) {
   static OccupancyCache cache;
-  const auto kernel = head_norm_strip_kernel<T, INTERLEAVED, KEEP, LANES, kForwardChunks<T>>;
+  const auto kernel = head_norm_strip_kernel<T, INTERLEAVED, KEEP, DENSE, LANES, kForwardChunks<T>>;
   int64_t ctas;
   const Strips strips = strips_of(a, kForwardChunks<T>, (int64_t)sm_count * cached_occupancy(kernel, cache, kThreads, 0), &ctas);
   kernel<<<(unsigned)ctas, kThreads, 0, s>>>(call_of(a), strips);
   return cudaGetLastError();
 }
+// The commonest groups of lanes by their number; others find theirs at run time.
 template <typename T, bool INTERLEAVED, bool KEEP>
 cudaError_t forward_strips(const opt_head_norm_args& a, int sm_count, cudaStream_t s) {
   switch (a.dim) {
-    case 64: return forward_strip<T, INTERLEAVED, KEEP, 8>(a, sm_count, s);
-    case 128: return forward_strip<T, INTERLEAVED, KEEP, 16>(a, sm_count, s);
-    default: return forward_strip<T, INTERLEAVED, KEEP, 0>(a, sm_count, s);
+    case 64: return forward_strip<T, INTERLEAVED, KEEP, true, 8>(a, sm_count, s);
+    case 128: return forward_strip<T, INTERLEAVED, KEEP, true, 16>(a, sm_count, s);
+    default: return forward_strip<T, INTERLEAVED, KEEP, true, 0>(a, sm_count, s);
   }
+}
+template <typename T, bool INTERLEAVED>
+cudaError_t forward_sparse_strips(const opt_head_norm_args& a, int sm_count, cudaStream_t s) {
+  if (a.dim > 64 && a.dim < 128) return forward_strip<T, INTERLEAVED, false, false, 16>(a, sm_count, s);
+  return forward_strip<T, INTERLEAVED, false, false, 0>(a, sm_count, s);
 }
 
 cudaError_t keep(const void* x, int64_t x_pitch, void* codes, void* scales, int64_t pitch, int64_t rows, int64_t cols,
@@ -938,7 +726,7 @@ cudaError_t forward(const opt_head_norm_args& a, int sm_count, cudaStream_t s) {
       return kept ? forward_strips<T, true, true>(b, sm_count, s) : forward_strips<T, true, false>(b, sm_count, s);
     return kept ? forward_strips<T, false, true>(b, sm_count, s) : forward_strips<T, false, false>(b, sm_count, s);
   }
-  if (v.ok) return a.flags & OPT_HEADS_INTERLEAVED ? forward_heads<T, W, true>(b, sm_count, s) : forward_heads<T, W, false>(b, sm_count, s);
+  if (v.ok) return a.flags & OPT_HEADS_INTERLEAVED ? forward_sparse_strips<T, true>(b, sm_count, s) : forward_sparse_strips<T, false>(b, sm_count, s);
   const int64_t need = (a.rows * (a.q_heads + a.k_heads) + kAnyWarps - 1) / kAnyWarps, most = (int64_t)sm_count * 12;
   head_norm_any_kernel<T, W><<<(unsigned)(need < most ? need : most), 32 * kAnyWarps, 0, s>>>(call_of(b));
   return cudaGetLastError();
@@ -973,10 +761,10 @@ cudaError_t backward_any(const opt_head_norm_backward_args& a, int sm_count, flo
   return weight_sums(a, ctas, s);
 }
 
-template <typename T, typename S, bool INTERLEAVED, int LANES>
+template <typename T, typename S, bool INTERLEAVED, bool DENSE, int LANES>
 cudaError_t backward_strip(const opt_head_norm_backward_args& a, int sm_count, float* parts, cudaStream_t s) {
   static OccupancyCache cache;
-  const auto kernel = head_norm_backward_strip_kernel<T, S, INTERLEAVED, LANES, kBackwardChunks<T>>;
+  const auto kernel = head_norm_backward_strip_kernel<T, S, INTERLEAVED, DENSE, LANES, kBackwardChunks<T>>;
   int64_t most = (int64_t)sm_count * cached_occupancy(kernel, cache, kThreads, 0), ctas;
   if (most > kHeadBackwardMaxCtas) most = kHeadBackwardMaxCtas;
   const Strips strips = strips_of(a, kBackwardChunks<T>, most, &ctas);
@@ -986,26 +774,15 @@ cudaError_t backward_strip(const opt_head_norm_backward_args& a, int sm_count, f
 }
 template <typename T, typename S, bool INTERLEAVED>
 cudaError_t backward_strips(const opt_head_norm_backward_args& a, int sm_count, float* parts, cudaStream_t s) {
-  switch (a.dim) {
-    case 64: return backward_strip<T, S, INTERLEAVED, 8>(a, sm_count, parts, s);
-    case 128: return backward_strip<T, S, INTERLEAVED, 16>(a, sm_count, parts, s);
-    default: return backward_strip<T, S, INTERLEAVED, 0>(a, sm_count, parts, s);
+  if ((a.dim & (a.dim - 1)) != 0) {
+    if (a.dim > 64 && a.dim < 128) return backward_strip<T, S, INTERLEAVED, false, 16>(a, sm_count, parts, s);
+    return backward_strip<T, S, INTERLEAVED, false, 0>(a, sm_count, parts, s);
   }
-}
-
-template <typename T, typename S, typename W, bool INTERLEAVED>
-cudaError_t backward_heads(const opt_head_norm_backward_args& a, int sm_count, float* parts, cudaStream_t s) {
-  constexpr int U = sizeof(T) == 2 ? 4 : 2;
-  static OccupancyCache cache;
-  const auto kernel = head_norm_backward_kernel<T, S, W, INTERLEAVED, U>;
-  int64_t most = (int64_t)sm_count * cached_occupancy(kernel, cache, kThreads, 0);
-  if (most > kHeadBackwardMaxCtas) most = kHeadBackwardMaxCtas;
-  int ctas;
-  const Sets sets = sets_of(a, U, most, &ctas);
-  if (ctas > kHeadBackwardMaxCtas) return backward_any<T, S, W>(a, sm_count, parts, s);      // more sets than the workspace has room for
-  kernel<<<ctas, kThreads, 0, s>>>(call_of(a), sets, parts);
-  if (const cudaError_t e = cudaGetLastError()) return e;
-  return weight_sums(a, ctas, s);
+  switch (a.dim) {
+    case 64: return backward_strip<T, S, INTERLEAVED, true, 8>(a, sm_count, parts, s);
+    case 128: return backward_strip<T, S, INTERLEAVED, true, 16>(a, sm_count, parts, s);
+    default: return backward_strip<T, S, INTERLEAVED, true, 0>(a, sm_count, parts, s);
+  }
 }
 
 template <typename T, typename S, typename W>
@@ -1023,12 +800,9 @@ cudaError_t backward_from(const opt_head_norm_backward_args& a, int sm_count, cu
     v.see(a.d_dk, a.dk_pitch, sizeof(T));
   }
   float* parts = a.d_dq_weight != nullptr || a.d_dk_weight != nullptr ? static_cast<float*>(a.d_workspace) : nullptr;
-  // (more sets than the workspace has rows of CTAs for go by single heads)
-  if (v.ok && (a.dim & (a.dim - 1)) == 0 && (a.q_heads + a.k_heads) * a.dim <= (kHeadBackwardMaxCtas - 2) * 256)
+  // (a strip of either side needs a row of the workspace; more than it has go by single heads)
+  if (v.ok && (a.q_heads + a.k_heads) * a.dim <= (kHeadBackwardMaxCtas - 2) * 128)
     return a.flags & OPT_HEADS_INTERLEAVED ? backward_strips<T, S, true>(a, sm_count, parts, s) : backward_strips<T, S, false>(a, sm_count, parts, s);
-  if (v.ok)
-    return a.flags & OPT_HEADS_INTERLEAVED ? backward_heads<T, S, W, true>(a, sm_count, parts, s)
-                                           : backward_heads<T, S, W, false>(a, sm_count, parts, s);
   return backward_any<T, S, W>(a, sm_count, parts, s);
 }
 
