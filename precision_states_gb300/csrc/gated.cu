@@ -37,10 +37,6 @@ __device__ __forceinline__ void activation(float g, float& f, float& df) {
     const float on = g == g ? 0.0f : g;
     f = g > 0.0f ? g : on;
     df = g > 0.0f ? 1.0f : on;
-  } else if constexpr (KIND == OPT_ACT_GELU) {
-    const float s = normcdff(g);
-    f = g * s;
-    if (SLOPE) df = fmaf(g, 0.3989422804014327f * (EXACT ? exp_minus(0.5f * g * g) : exp2_near(-0.5f * kLog2e * g * g)), s);
   } else {
     float z = g, dz = 1.0f;
     if (KIND == OPT_ACT_GELU_TANH) {
@@ -54,9 +50,55 @@ __device__ __forceinline__ void activation(float g, float& f, float& df) {
     if (SLOPE) df = fmaf(f * (z < 0.0f ? r : er), dz, s);
   }
 }
+// The normal distribution function of two values, and exp(-g^2 / 2).  For a = |g|, s(-a) =
+// exp(-a^2 / 2) R(a); R, a scaled complementary error function, by Hastings' way (Abramowitz and
+// Stegun 7.1.26): a polynomial in t = 1 / (1 + 0.4 a), here of degree nine for R / t, fitted to
+// equal relative errors over 0 <= a <= 16 (in fp32 5 units of 2^-24, 8 with a reciprocal that is
+// one off) and exact at 0.  EXACT: the exponential with what its argument's rounding loses.
+// (8192 x 14336 BF16 to y 120 us, with the library's function 262.)
+template <bool EXACT>
+__device__ __forceinline__ void normal2(f2_t g, f2_t& s, f2_t& bell) {
+  constexpr float c[10] = {1.595754921e-01f, 1.596362293e-01f,  1.330585480e-01f, 9.175205231e-02f,  -2.814983390e-02f,
+                           1.220970377e-01f, -3.773407638e-01f, 3.848911524e-01f, -1.779478639e-01f, 3.242795169e-02f};
+  const f2_t one = pk(1.0f, 1.0f);
+  float lo, hi;
+  unpk(g, lo, hi);
+  const f2_t a = pk(fminf(fabsf(lo), 16.0f), fminf(fabsf(hi), 16.0f));      // s(-a) is 0 in fp32 beyond
+  float tl, th;
+  unpk(fma2(a, pk(0.4f, 0.4f), one), tl, th);
+  const f2_t t = pk(reciprocal_near(tl), reciprocal_near(th));
+  f2_t q = pk(c[9], c[9]);
+#pragma unroll
+  for (int k = 8; k >= 0; --k) q = fma2(q, t, pk(c[k], c[k]));
+  constexpr float h = -0.5f * kLog2e, h_rest = (float)(-0.5 * 1.4426950408889634074 - (double)h), ln2 = 0.69314718f;
+  const f2_t square = mul2(a, a), u = mul2(square, pk(h, h));
+  float ul, uh;
+  unpk(u, ul, uh);
+  bell = pk(exp2_near(ul), exp2_near(uh));
+  if constexpr (EXACT) {
+    const f2_t minus = pk(-1.0f, -1.0f);
+    const f2_t square_rest = fma2(a, a, mul2(square, minus));
+    const f2_t rest = fma2(square, pk(h, h), mul2(u, minus)), all = fma2(square_rest, pk(h, h), fma2(square, pk(h_rest, h_rest), rest));
+    bell = fma2(mul2(bell, pk(ln2, ln2)), all, bell);
+  }
+  const f2_t below = mul2(mul2(q, t), bell);
+  float bl, bh, al, ah;
+  unpk(below, bl, bh);
+  unpk(fma2(below, pk(-1.0f, -1.0f), one), al, ah);
+  s = pk(lo > 0.0f ? al : bl, hi > 0.0f ? ah : bh);
+}
 template <int KIND, bool EXACT, bool SLOPE>
 __device__ __forceinline__ void activation8(const float (&g)[8], float (&f)[8], float (&df)[8]) {
-  if constexpr (EXACT || KIND == OPT_ACT_RELU || KIND == OPT_ACT_GELU) {
+  if constexpr (KIND == OPT_ACT_GELU) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const f2_t gv = pk(g[j], g[j + 1]);
+      f2_t s, bell;
+      normal2<EXACT>(gv, s, bell);
+      unpk(mul2(gv, s), f[j], f[j + 1]);
+      if constexpr (SLOPE) unpk(fma2(mul2(gv, pk(0.3989422804014327f, 0.3989422804014327f)), bell, s), df[j], df[j + 1]);
+    }
+  } else if constexpr (EXACT || KIND == OPT_ACT_RELU) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) activation<KIND, EXACT, SLOPE>(g[j], f[j], df[j]);
   } else {
@@ -221,12 +263,93 @@ __global__ void __launch_bounds__(kThreads, 4) gated_any_kernel(const __grid_con
 }
 
 // ------------------------------------------------------------------ gradients
-// Without transposed outputs: a chunk to a thread, as above.
-template <typename T, typename S, int KIND, bool VEC>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && VEC ? 4 : 3)
-gated_backward_kernel(const __grid_constant__ opt_gated_backward_args a) {
+// Without transposed outputs, whole chunks: down the rows by pointers, as above.
+template <typename T, typename S, int KIND, bool UP>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : sizeof(S) == 1 ? 3 : 2) gated_backward_vec_kernel(const __grid_constant__ opt_gated_backward_args a) {
+  constexpr bool KEPT = sizeof(S) == 1;
+  using In = std::conditional_t<KEPT, uint8_t, T>;
+  const uint32_t c = 8 * (blockIdx.x * blockDim.x + threadIdx.x), rows = (uint32_t)a.rows;
+  const uint32_t step = gridDim.y * blockDim.y, panel = 512 * (uint32_t)((a.cols + 511) / 512);
+  const uint32_t place = 512 * (c >> 9) + ((c >> 7) & 3);
+  const bool on = c < (uint32_t)a.cols, first = on && (threadIdx.x & 15) == 0;
+  const bool plain_g = a.d_dgate != nullptr, plain_u = UP && a.d_dup != nullptr, codes_g = a.d_dgate_codes != nullptr,
+             codes_u = UP && a.d_dup_codes != nullptr;
+  uint32_t r = (uint32_t)first_row();
+  const auto start = [&](auto* base, int64_t pitch) { return base + (r * pitch + c); };
+  const T* dy = start(static_cast<const T*>(a.d_dy), a.dy_pitch);
+  const In *gate = start(static_cast<const In*>(a.d_gate), a.gate_pitch), *up = start(static_cast<const In*>(a.d_up), a.up_pitch);
+  T *dgate = start(static_cast<T*>(a.d_dgate), a.dgate_pitch), *dup = start(static_cast<T*>(a.d_dup), a.dup_pitch);
+  uint8_t *gcodes = start(static_cast<uint8_t*>(a.d_dgate_codes), a.dgate_codes_pitch),
+          *ucodes = start(static_cast<uint8_t*>(a.d_dup_codes), a.dup_codes_pitch);
+  const int64_t dy_step = step * a.dy_pitch, gate_step = step * a.gate_pitch, up_step = step * a.up_pitch, dgate_step = step * a.dgate_pitch,
+                dup_step = step * a.dup_pitch, gcodes_step = step * a.dgate_codes_pitch, ucodes_step = step * a.dup_codes_pitch;
+  const auto scale_at = [&](uint32_t row) { return (uint64_t)(row >> 7) * panel + (place + 16 * (row & 31) + ((row >> 3) & 12)); };
+  std::conditional_t<KEPT, KeptAsk, Raw<T>> gnext, unext;
+  Raw<T> dnext;
+  const auto ask = [&](uint32_t row) {
+    const bool there = on && row < rows;
+    dnext = load_if(dy, there);
+    if constexpr (KEPT) {
+      gnext.codes = load_codes_if(gate, there);
+      gnext.byte = load_byte_if(static_cast<const uint8_t*>(a.d_gate_scales) + scale_at(row), there);
+      if (UP) {
+        unext.codes = load_codes_if(up, there);
+        unext.byte = load_byte_if(static_cast<const uint8_t*>(a.d_up_scales) + scale_at(row), there);
+      }
+    } else {
+      gnext = load_if(gate, there);
+      if (UP) unext = load_if(up, there);
+    }
+  };
+  const auto values = [](const auto& in, float (&x)[8]) {
+    if constexpr (KEPT) values8(in.codes, scale_of(in.byte), x);
+    else unpack(in, x);
+  };
+  ask(r);
+  for (; r < rows; r += step) {
+    float d[8], g[8], u[8], f[8], df[8];
+    values(gnext, g);
+    if (UP) values(unext, u);
+    unpack(dnext, d);
+    dy += dy_step;
+    gate += gate_step;
+    if (UP) up += up_step;
+    ask(r + step);
+    activation8<KIND, sizeof(T) == 4, true>(g, f, df);
+    times8(df, d);
+    times8(f, d);
+    if (UP) times8(df, u);
+    if (plain_g) {
+      store8_if(dgate, df, on);
+      dgate += dgate_step;
+    }
+    if (plain_u) {
+      store8_if(dup, f, on);
+      dup += dup_step;
+    }
+    if (!codes_g && !codes_u) continue;
+    // both matrices' fields through the exchanges in one word
+    uint32_t both = scale_field(top8_of(df)) >> 23 | (scale_field(UP ? top8_of(f) : 0u) >> 23) << 16;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) both = larger(both, __shfl_xor_sync(0xFFFFFFFFu, both, o), Bf16());
+    uint8_t *gscales = static_cast<uint8_t*>(a.d_dgate_scales) + scale_at(r), *uscales = static_cast<uint8_t*>(a.d_dup_scales) + scale_at(r);
+    if (__any_sync(0xFFFFFFFFu, max(both & 0xFFFFu, both >> 16) >= 255u)) {      // rare
+      if (codes_g) put_codes8(gcodes, gscales, 0, on ? 8 : 0, df);
+      if (codes_u) put_codes8(ucodes, uscales, 0, on ? 8 : 0, f);
+    } else {
+      if (codes_g) put_field_if(gcodes, gscales, df, both << 23, on, first);
+      if (codes_u) put_field_if(ucodes, uscales, f, (both >> 16) << 23, on, first);
+    }
+    gcodes += gcodes_step;
+    ucodes += ucodes_step;
+  }
+}
+// The same of rows that begin anywhere.
+template <typename T, typename S, int KIND>
+__global__ void __launch_bounds__(kThreads, 3) gated_backward_any_kernel(const __grid_constant__ opt_gated_backward_args a) {
+  constexpr bool VEC = false;
   __shared__ __align__(16) Ragged<T, VEC, kThreads / 32> ragged;
-  T* buffer = ragged.chunk[VEC ? 0 : warp_of_block()];
+  T* buffer = ragged.chunk[warp_of_block()];
   const int64_t c = 8 * ((int64_t)blockIdx.x * blockDim.x + threadIdx.x), panel = (a.cols + 511) / 512;
   const int valid = (int)max(min(a.cols - c, (int64_t)8), (int64_t)0);
   const bool has_up = a.d_up != nullptr;
@@ -236,11 +359,9 @@ gated_backward_kernel(const __grid_constant__ opt_gated_backward_args a) {
     const Source<S, VEC> up(a.d_up, a.d_up_scales, a.up_pitch, a.rows, a.cols, r);
     Ahead<T, VEC> da = {};
     typename Source<S, VEC>::Ask ga = {}, ua = {};
-    if (!VEC || valid > 0) {
-      da = dy.ahead(c, valid);
-      ga = gate.ahead(c, valid);
-      if (has_up) ua = up.ahead(c, valid);
-    }
+    da = dy.ahead(c, valid);
+    ga = gate.ahead(c, valid);
+    if (has_up) ua = up.ahead(c, valid);
     float d[8], g[8], u[8], f[8], df[8];
     gate.values(ga, c, valid, g);
     activation8<KIND, sizeof(T) == 4, true>(g, f, df);
@@ -251,10 +372,8 @@ gated_backward_kernel(const __grid_constant__ opt_gated_backward_args a) {
       up.values(ua, c, valid, u);
       times8(df, u);
     }
-    if (!VEC || valid > 0) {
-      if (a.d_dgate != nullptr) store_at<VEC>(a.d_dgate, a.dgate_pitch, a.cols, r, c, valid, df, buffer);
-      if (a.d_dup != nullptr) store_at<VEC>(a.d_dup, a.dup_pitch, a.cols, r, c, valid, f, buffer);
-    }
+    if (a.d_dgate != nullptr) store_at<VEC>(a.d_dgate, a.dgate_pitch, a.cols, r, c, valid, df, buffer);
+    if (a.d_dup != nullptr) store_at<VEC>(a.d_dup, a.dup_pitch, a.cols, r, c, valid, f, buffer);
     const int64_t at = scale_place(r, c >> 7, panel);
     if (a.d_dgate_codes != nullptr)
       put_codes8(static_cast<uint8_t*>(a.d_dgate_codes) + r * a.dgate_codes_pitch + c, static_cast<uint8_t*>(a.d_dgate_scales), at,
@@ -688,6 +807,15 @@ cudaError_t forward(const opt_gated_args& a, int sm_count, cudaStream_t s) {
   }
 }
 
+template <typename T, typename S, int KIND, bool UP>
+cudaError_t backward_rows(const opt_gated_backward_args& a, ChunkGrid g, int sm_count, cudaStream_t s) {
+  static OccupancyCache cache;
+  const auto kernel = gated_backward_vec_kernel<T, S, KIND, UP>;
+  g.limit((int64_t)sm_count * cached_occupancy(kernel, cache, kThreads, 0));
+  kernel<<<g.grid, g.block, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
 template <int KIND>
 cudaError_t backward_turn(const opt_gated_backward_args& a, int sm_count, cudaStream_t s) {
   static OccupancyCache cache;
@@ -719,7 +847,12 @@ cudaError_t backward_vec(const opt_gated_backward_args& a, int sm_count, cudaStr
   }
   if (a.d_dgate_codes_t == nullptr && a.d_dup_codes_t == nullptr && a.d_y_codes_t == nullptr) {
     const ChunkGrid g(a.rows, a.cols, kThreads);
-    gated_backward_kernel<T, S, KIND, VEC><<<g.grid, g.block, 0, s>>>(a);
+    if constexpr (VEC) {
+      if (a.d_up != nullptr) return backward_rows<T, S, KIND, true>(a, g, sm_count, s);
+      return backward_rows<T, S, KIND, false>(a, g, sm_count, s);
+    } else {
+      gated_backward_any_kernel<T, S, KIND><<<g.grid, g.block, 0, s>>>(a);
+    }
   } else {
     static OccupancyCache cache;
     const auto kernel = gated_backward_tile_kernel<T, S, KIND, VEC>;

@@ -25,15 +25,19 @@ def activation(g, kind):
     its own, and s and 1 - s by 4 more (sum, reciprocal, product); f by one more.  f' is
     s + f (1 - s) z', with five more roundings in the second term; 1 - s may be formed as
     that, off by 2^-24.  s is 0 where it would be below 2^-128 in BF16,
-    which leaves f off by |g| 2^-128 and f' by 2^-128 (1 + |g| z').  gelu: the library's
-    normal distribution function is off by at most 5 units in the last place."""
+    which leaves f off by |g| 2^-128 and f' by 2^-128 (1 + |g| z').  gelu: the
+    distribution function below 0 is an exponential (4 units, and g^2 for the rounding of its
+    argument, half of g^2 formed with two) times a fitted factor (8), with three products; above
+    0 it is 1 less that."""
     with np.errstate(all="ignore"):
         if kind == "relu":
             f, df = np.maximum(g, 0.0), (g > 0).astype(np.float64)
             return f, df, 0 * f, 0 * f
         if kind == "gelu":
             s, bell = phi(g), g * np.exp(-g * g / 2) / np.sqrt(2 * np.pi)
-            return g * s, s + bell, 11 * E24 * np.abs(g * s) + TINY, TINY + E24 * (11 * s + (g * g + 10) * np.abs(bell) + np.abs(s + bell))
+            far, off = TINY * (1 + np.abs(g)), 17 + np.minimum(g * g, 300)
+            return (g * s, s + bell, E24 * off * np.abs(g * s) + far,
+                    far + E24 * (off * s + (np.minimum(g * g, 300) + 10) * np.abs(bell) + np.abs(s + bell)))
         z, dz = g, np.ones_like(g)
         if kind == "gelu_tanh":
             c = 2 * np.sqrt(2 / np.pi)
