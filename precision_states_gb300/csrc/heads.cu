@@ -45,6 +45,7 @@ struct HeadCall {
   int dim, rot;
   int32_t weight_dtype;
   bool interleaved;
+  bool wide_lines;               // the tables' lines are whole 16-byte pieces
   float eps;
 };
 template <typename A>
@@ -59,6 +60,7 @@ HeadCall shared_call(const A& a) {
   c.rot = (int)a.rot;
   c.weight_dtype = a.weight_dtype;
   c.interleaved = (a.flags & OPT_HEADS_INTERLEAVED) != 0;
+  c.wide_lines = a.rot % 8 == 0 && (((uintptr_t)a.d_cos | (uintptr_t)a.d_sin) & 15u) == 0;
   c.eps = a.eps;
   return c;
 }
@@ -89,6 +91,10 @@ __device__ __forceinline__ float group_sum(float v, int lanes) {
     if (o < lanes) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
 }
+
+// How a head's elements are paired: whole chunks with whole chunks half the rotated part
+// further (rot a multiple of 16), neighbours, or elements half the rotated part further.
+enum Pairs { kChunks = 0, kNeighbours = 1, kElements = 2 };
 
 // The partner's words: those of lane `partner`, or with neighbouring pairs the lane's own
 // with the elements of each pair exchanged.
@@ -149,18 +155,25 @@ struct TurnLines {
   float line[2][2][128];         // [turn][cosines, sines][pair]
   // By the whole warp: the lines at position `at`, NaN outside the tables.
   __device__ __forceinline__ void ask(int turn, const HeadCall& a, int64_t at) {
-    const int lane = threadIdx.x & 31, chunks = a.rot >> 3;
-    if ((uint64_t)at < (uint64_t)a.table) {
-      const int64_t p = at * (a.rot >> 1) + 4 * lane;
-      if (lane < chunks) {
+    const int lane = threadIdx.x & 31, half = a.rot >> 1;
+    if ((uint64_t)at >= (uint64_t)a.table) {
+      const float nan = u2f(0x7FC00000u);
+      for (int i = lane; i < half; i += 32) line[turn][0][i] = line[turn][1][i] = nan;
+    } else if (a.wide_lines) {
+      const int64_t p = at * half + 4 * lane;
+      if (4 * lane < half) {
         asm volatile("cp.async.ca.shared.global [%0], [%1], 16;"
                      :: "r"((uint32_t)__cvta_generic_to_shared(&line[turn][0][4 * lane])), "l"(a.cos + p) : "memory");
         asm volatile("cp.async.ca.shared.global [%0], [%1], 16;"
                      :: "r"((uint32_t)__cvta_generic_to_shared(&line[turn][1][4 * lane])), "l"(a.sin + p) : "memory");
       }
     } else {
-      const float nan = u2f(0x7FC00000u);
-      for (int i = lane; i < a.rot >> 1; i += 32) line[turn][0][i] = line[turn][1][i] = nan;
+      for (int i = lane; i < half; i += 32) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;"
+                     :: "r"((uint32_t)__cvta_generic_to_shared(&line[turn][0][i])), "l"(a.cos + (at * half + i)) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;"
+                     :: "r"((uint32_t)__cvta_generic_to_shared(&line[turn][1][i])), "l"(a.sin + (at * half + i)) : "memory");
+      }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
@@ -169,27 +182,61 @@ struct TurnLines {
     asm volatile("cp.async.wait_group 1;" ::: "memory");
     __syncwarp();
   }
-  // A lane's eight factors from its pair on: for halves one of each element, for neighbours one
-  // of each pair; 1 and 0 for elements that are not rotated.
-  template <bool INTERLEAVED>
-  __device__ __forceinline__ void factors(int turn, int pair, bool whole, bool rotated, float (&c)[8], float (&s)[8]) const {
-    if constexpr (INTERLEAVED) {
+  // The factors of a lane's eight elements, from e of the head and its pair on.  For elements
+  // that are not rotated (whole: all are) they are 1 and 0, or with whole chunks, where such an
+  // element is its own partner, 1/2 and 1/2: the halves' sum rounds as the product with 1.
+  template <int PAIRS>
+  __device__ __forceinline__ void factors(int turn, int e, int pair, int rot, bool whole, float (&c)[8], float (&s)[8]) const {
+    if constexpr (PAIRS == kNeighbours) {
       const float4 cv = *reinterpret_cast<const float4*>(&line[turn][0][pair]), sv = *reinterpret_cast<const float4*>(&line[turn][1][pair]);
       c[0] = c[1] = cv.x; c[2] = c[3] = cv.y; c[4] = c[5] = cv.z; c[6] = c[7] = cv.w;
       s[0] = s[1] = sv.x; s[2] = s[3] = sv.y; s[4] = s[5] = sv.z; s[6] = s[7] = sv.w;
-    } else {
+    } else if constexpr (PAIRS == kChunks) {
       shared8(&line[turn][0][pair], c);
       shared8(&line[turn][1][pair], s);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int at = e + j < (rot >> 1) ? e + j : e + j < rot ? e + j - (rot >> 1) : 0;
+        c[j] = line[turn][0][at];
+        s[j] = line[turn][1][at];
+      }
     }
     if (!whole) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        c[j] = rotated ? c[j] : 1.0f;
-        s[j] = rotated ? s[j] : 0.0f;
+        c[j] = e + j < rot ? c[j] : PAIRS == kChunks ? 0.5f : 1.0f;
+        s[j] = e + j < rot ? s[j] : PAIRS == kChunks ? 0.5f : 0.0f;
       }
     }
   }
 };
+// The partners of a lane's eight elements v (raw its words): another lane's words, its own, or
+// by way of the warp's 256 floats at `held`, in which a head's elements lie side by side.  For
+// elements that are not rotated: themselves with whole chunks, else 0, so that the product with
+// s = 0 is 0 for infinities too.
+template <int PAIRS, typename T>
+__device__ __forceinline__ void partners_of(const Raw<T>& raw, const float (&v)[8], int partner, int e, int rot, bool whole,
+                                            float* held, float (&p)[8]) {
+  if constexpr (PAIRS != kElements) {
+    Raw<T> r = partner_of<PAIRS == kNeighbours>(raw, partner);
+    if (PAIRS == kNeighbours && !whole) {
+      constexpr int kWords = sizeof(r.w) / sizeof(r.w[0]);      // (a word's elements are rotated or not together)
+#pragma unroll
+      for (int k = 0; k < kWords; ++k) r.w[k] = e + 8 / kWords * k < rot ? r.w[k] : 0u;
+    }
+    unpack(r, p);
+  } else {
+    const int lane = threadIdx.x & 31, half = rot >> 1;
+    const float* head = held + (8 * lane - e);
+    __syncwarp();                  // what was there is read
+    *reinterpret_cast<float4*>(held + 8 * lane) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(held + 8 * lane + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) p[j] = e + j >= rot ? 0.0f : head[e + j < half ? e + j + half : e + j - half];
+  }
+}
 // How CTAs share strips: CTA b takes strip b mod (strips), and of its rows a warp each
 // (b / strips) * kWarps + warp, and `stride` on.  Strips of queries come first.
 struct Strips {
@@ -229,7 +276,7 @@ __device__ __forceinline__ uint64_t scale_row(uint32_t r, uint32_t panel512) {
   return (uint64_t)(r >> 7) * panel512 + (16 * (r & 31) + ((r >> 3) & 12));
 }
 
-template <typename T, bool INTERLEAVED, bool KEEP, bool DENSE, int LANES, int U>
+template <typename T, int PAIRS, bool KEEP, bool DENSE, int LANES, int U>
 __global__ void __launch_bounds__(kThreads, kForwardCtas) head_norm_strip_kernel(const __grid_constant__ HeadCall a,
                                                                                 const Strips strips) {
   // the weight, and its partner's with the sign of the partner's term (minus for a pair's
@@ -237,15 +284,17 @@ __global__ void __launch_bounds__(kThreads, kForwardCtas) head_norm_strip_kernel
   __shared__ __align__(16) float weight[256], other[256];
   __shared__ __align__(16) TurnLines lines_of[kWarps];
   TurnLines& lines = lines_of[threadIdx.x >> 5];
+  __shared__ __align__(16) float rows_of[PAIRS == kElements ? kWarps : 1][256];
+  float* const held = rows_of[PAIRS == kElements ? threadIdx.x >> 5 : 0];
   const int dim = a.dim, rot = a.rot, half = rot >> 1, strip = (int)(blockIdx.x % (uint32_t)strips.strips);
   const bool keys = strip >= strips.q_strips;
   const Side& side = a.side[keys];
-  const StripLane l = strip_lane<DENSE, U>(strips, keys ? strip - strips.q_strips : strip, side.cols, dim, rot, INTERLEAVED);
+  const StripLane l = strip_lane<DENSE, U>(strips, keys ? strip - strips.q_strips : strip, side.cols, dim, rot, PAIRS == kNeighbours);
   if ((int)threadIdx.x < dim) {
-    const int e = threadIdx.x, p = e >= rot ? e : INTERLEAVED ? e ^ 1 : e < half ? e + half : e - half;
+    const int e = threadIdx.x, p = e >= rot ? e : PAIRS == kNeighbours ? e ^ 1 : e < half ? e + half : e - half;
     const float v = weight_at(side.weight, a.weight_dtype, p);
     weight[e] = weight_at(side.weight, a.weight_dtype, e);
-    other[e] = (INTERLEAVED ? (e & 1) == 0 : e < half) ? -v : v;
+    other[e] = (PAIRS == kNeighbours ? (e & 1) == 0 : e < half) ? -v : v;
   }
   __syncthreads();
   const uint32_t rows = (uint32_t)a.rows, panel = 512 * (uint32_t)((side.cols + 511) / 512);
@@ -275,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, kForwardCtas) head_norm_strip_kernel
     shared8(weight + l.e, w);
     if (rot > 0) {
       lines.wait();
-      lines.template factors<INTERLEAVED>(turn, l.pair, rot == dim, l.rotated, c, s);
+      lines.template factors<PAIRS>(turn, l.e, l.pair, rot, rot == dim, c, s);
       times8(c, w);
       shared8(other + l.e, w);
       times8(s, w);
@@ -317,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, kForwardCtas) head_norm_strip_kernel
         unpack(raw[i], v);
         if (rot > 0) {
           float p[8];
-          unpack(partner_of<INTERLEAVED>(raw[i], l.partner), p);
+          partners_of<PAIRS>(raw[i], v, l.partner, l.e, rot, rot == dim, held, p);
 #pragma unroll
           for (int j = 0; j < 8; j += 2)
             unpk(mul2(fma2(pk(v[j], v[j + 1]), pk(c[j], c[j + 1]), mul2(pk(p[j], p[j + 1]), pk(s[j], s[j + 1]))), scale), y[j], y[j + 1]);
@@ -337,18 +386,20 @@ __global__ void __launch_bounds__(kThreads, kForwardCtas) head_norm_strip_kernel
 }
 
 // The gradients of strips.
-template <typename T, typename S, bool INTERLEAVED, bool DENSE, int LANES, int U>
+template <typename T, typename S, int PAIRS, bool DENSE, int LANES, int U>
 __global__ void __launch_bounds__(kThreads, kBackwardCtas) head_norm_backward_strip_kernel(
     const __grid_constant__ HeadCall a, const Strips strips, float* parts) {
   __shared__ float sums[kWarps][32][8];
   __shared__ __align__(16) TurnLines lines_of[kWarps];
   TurnLines& lines = lines_of[threadIdx.x >> 5];
+  __shared__ __align__(16) float rows_of[PAIRS == kElements ? kWarps : 1][256];
+  float* const held = rows_of[PAIRS == kElements ? threadIdx.x >> 5 : 0];
   if (parts != nullptr) let_sums_start();
   constexpr bool KEPT = sizeof(S) == 1;
   const int dim = a.dim, rot = a.rot, strip = (int)(blockIdx.x % (uint32_t)strips.strips);
   const bool keys = strip >= strips.q_strips;
   const Side& side = a.side[keys];
-  const StripLane l = strip_lane<DENSE, U>(strips, keys ? strip - strips.q_strips : strip, side.cols, dim, rot, INTERLEAVED);
+  const StripLane l = strip_lane<DENSE, U>(strips, keys ? strip - strips.q_strips : strip, side.cols, dim, rot, PAIRS == kNeighbours);
   const uint32_t rows = (uint32_t)a.rows, panel = 512 * (uint32_t)((side.cols + 511) / 512);
   const uint32_t left = l.left, step = chunk_step<DENSE>(strips, dim);
   const uint32_t place = 512 * (l.column >> 9) + ((l.column >> 7) & 3);
@@ -362,8 +413,8 @@ __global__ void __launch_bounds__(kThreads, kBackwardCtas) head_norm_backward_st
   }
   f2_t dw[4] = {};                 // +0 in both lanes
   // the turn back: plus for a pair's first element
-  const float sign = !INTERLEAVED && l.e >= (rot >> 1) ? -1.0f : 1.0f;
-  const f2_t signs = pk(sign, INTERLEAVED ? -1.0f : sign);
+  const float sign = PAIRS == kChunks && l.rotated && l.e >= (rot >> 1) ? -1.0f : 1.0f;
+  const f2_t signs = pk(sign, PAIRS == kNeighbours ? -1.0f : sign);
   Raw<T> d[U];
   std::conditional_t<KEPT, KeptAsk, Raw<T>> x[U];
   const auto load = [&](int k, uint32_t r) {
@@ -402,9 +453,16 @@ __global__ void __launch_bounds__(kThreads, kBackwardCtas) head_norm_backward_st
     T* const out = static_cast<T*>(side.out) + (r * side.out_pitch + l.column);
     float c[8], s[8];
     if (rot > 0) {
-      lines.template factors<INTERLEAVED>(turn, l.pair, rot == dim, l.rotated, c, s);
+      lines.template factors<PAIRS>(turn, l.e, l.pair, rot, rot == dim, c, s);
 #pragma unroll
-      for (int j = 0; j < 8; j += 2) unpk(mul2(pk(s[j], s[j + 1]), signs), s[j], s[j + 1]);
+      for (int j = 0; j < 8; j += 2) {
+        if constexpr (PAIRS == kElements) {
+          s[j] = l.e + j < (rot >> 1) ? s[j] : -s[j];
+          s[j + 1] = l.e + j + 1 < (rot >> 1) ? s[j + 1] : -s[j + 1];
+        } else {
+          unpk(mul2(pk(s[j], s[j + 1]), signs), s[j], s[j + 1]);
+        }
+      }
     }
 #pragma unroll
     for (int k = 0; k < U; ++k) {
@@ -416,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, kBackwardCtas) head_norm_backward_st
       unpack(raw, g);
       if (rot > 0) {
         float p[8];
-        unpack(partner_of<INTERLEAVED>(raw, l.partner), p);
+        partners_of<PAIRS>(raw, g, l.partner, l.e, rot, rot == dim, held, p);
 #pragma unroll
         for (int j = 0; j < 8; j += 2)
           unpk(fma2(pk(g[j], g[j + 1]), pk(c[j], c[j + 1]), mul2(pk(p[j], p[j + 1]), pk(s[j], s[j + 1]))), g[j], g[j + 1]);
@@ -622,8 +680,7 @@ __global__ void __launch_bounds__(kSumCols * kSumParts) head_weight_kernel(const
   }
 }
 
-// Whether whole chunks of eight elements, rotated with their partners' whole chunks, start
-// on 16 bytes everywhere.
+// Whether heads are whole chunks of eight elements that start on 16 bytes everywhere.
 struct Whole {
   int64_t rows;
   bool ok;
@@ -633,14 +690,15 @@ struct Whole {
 };
 template <typename A>
 Whole whole_heads(const A& a, int64_t ws) {
-  Whole v{a.rows, a.dim % 8 == 0 && a.dim <= 256 && a.rot % ((a.flags & OPT_HEADS_INTERLEAVED) ? 8 : 16) == 0};
+  Whole v{a.rows, a.dim % 8 == 0 && a.dim <= 256};
   if (a.q_heads > 0) v.see(a.d_q_weight, 0, ws);
   if (a.k_heads > 0) v.see(a.d_k_weight, 0, ws);
-  if (a.rot > 0) {
-    v.see(a.d_cos, 0, 4);
-    v.see(a.d_sin, 0, 4);
-  }
   return v;
+}
+
+template <typename A>
+Pairs pairs_of(const A& a) {
+  return a.flags & OPT_HEADS_INTERLEAVED ? kNeighbours : a.rot % 16 == 0 ? kChunks : kElements;
 }
 
 // Strips of U chunks, and their CTAs: as many for each as its rows fill, within `most` in all.
@@ -659,28 +717,30 @@ Strips strips_of(const A& a, int u, int64_t most, int64_t* ctas) {
   return s;
 }
 
-template <typename T, bool INTERLEAVED, bool KEEP, bool DENSE, int LANES>
+template <typename T, int PAIRS, bool KEEP, bool DENSE, int LANES>
 cudaError_t forward_strip(const opt_head_norm_args& a, int sm_count, cudaStream_t s) {
   static OccupancyCache cache;
-  const auto kernel = head_norm_strip_kernel<T, INTERLEAVED, KEEP, DENSE, LANES, kForwardChunks<T>>;
+  const auto kernel = head_norm_strip_kernel<T, PAIRS, KEEP, DENSE, LANES, kForwardChunks<T>>;
   int64_t ctas;
   const Strips strips = strips_of(a, kForwardChunks<T>, (int64_t)sm_count * cached_occupancy(kernel, cache, kThreads, 0), &ctas);
   kernel<<<(unsigned)ctas, kThreads, 0, s>>>(call_of(a), strips);
   return cudaGetLastError();
 }
 // The commonest groups of lanes by their number; others find theirs at run time.
-template <typename T, bool INTERLEAVED, bool KEEP>
+template <typename T, int PAIRS, bool KEEP>
 cudaError_t forward_strips(const opt_head_norm_args& a, int sm_count, cudaStream_t s) {
-  switch (a.dim) {
-    case 64: return forward_strip<T, INTERLEAVED, KEEP, true, 8>(a, sm_count, s);
-    case 128: return forward_strip<T, INTERLEAVED, KEEP, true, 16>(a, sm_count, s);
-    default: return forward_strip<T, INTERLEAVED, KEEP, true, 0>(a, sm_count, s);
+  if constexpr (PAIRS != kElements) {
+    if (a.dim == 64) return forward_strip<T, PAIRS, KEEP, true, 8>(a, sm_count, s);
+    if (a.dim == 128) return forward_strip<T, PAIRS, KEEP, true, 16>(a, sm_count, s);
   }
+  return forward_strip<T, PAIRS, KEEP, true, 0>(a, sm_count, s);
 }
-template <typename T, bool INTERLEAVED>
+template <typename T, int PAIRS>
 cudaError_t forward_sparse_strips(const opt_head_norm_args& a, int sm_count, cudaStream_t s) {
-  if (a.dim > 64 && a.dim < 128) return forward_strip<T, INTERLEAVED, false, false, 16>(a, sm_count, s);
-  return forward_strip<T, INTERLEAVED, false, false, 0>(a, sm_count, s);
+  if constexpr (PAIRS != kElements) {
+    if (a.dim > 64 && a.dim < 128) return forward_strip<T, PAIRS, false, false, 16>(a, sm_count, s);
+  }
+  return forward_strip<T, PAIRS, false, false, 0>(a, sm_count, s);
 }
 
 cudaError_t keep(const void* x, int64_t x_pitch, void* codes, void* scales, int64_t pitch, int64_t rows, int64_t cols,
@@ -722,11 +782,19 @@ cudaError_t forward(const opt_head_norm_args& a, int sm_count, cudaStream_t s) {
   }
   if (v.ok && (a.dim & (a.dim - 1)) == 0) {
     const bool kept = b.d_q_codes != nullptr || b.d_k_codes != nullptr;
-    if (a.flags & OPT_HEADS_INTERLEAVED)
-      return kept ? forward_strips<T, true, true>(b, sm_count, s) : forward_strips<T, true, false>(b, sm_count, s);
-    return kept ? forward_strips<T, false, true>(b, sm_count, s) : forward_strips<T, false, false>(b, sm_count, s);
+    switch (pairs_of(a)) {
+      case kChunks: return kept ? forward_strips<T, kChunks, true>(b, sm_count, s) : forward_strips<T, kChunks, false>(b, sm_count, s);
+      case kNeighbours: return kept ? forward_strips<T, kNeighbours, true>(b, sm_count, s) : forward_strips<T, kNeighbours, false>(b, sm_count, s);
+      default: return kept ? forward_strips<T, kElements, true>(b, sm_count, s) : forward_strips<T, kElements, false>(b, sm_count, s);
+    }
   }
-  if (v.ok) return a.flags & OPT_HEADS_INTERLEAVED ? forward_sparse_strips<T, true>(b, sm_count, s) : forward_sparse_strips<T, false>(b, sm_count, s);
+  if (v.ok) {
+    switch (pairs_of(a)) {
+      case kChunks: return forward_sparse_strips<T, kChunks>(b, sm_count, s);
+      case kNeighbours: return forward_sparse_strips<T, kNeighbours>(b, sm_count, s);
+      default: return forward_sparse_strips<T, kElements>(b, sm_count, s);
+    }
+  }
   const int64_t need = (a.rows * (a.q_heads + a.k_heads) + kAnyWarps - 1) / kAnyWarps, most = (int64_t)sm_count * 12;
   head_norm_any_kernel<T, W><<<(unsigned)(need < most ? need : most), 32 * kAnyWarps, 0, s>>>(call_of(b));
   return cudaGetLastError();
@@ -761,10 +829,10 @@ cudaError_t backward_any(const opt_head_norm_backward_args& a, int sm_count, flo
   return weight_sums(a, ctas, s);
 }
 
-template <typename T, typename S, bool INTERLEAVED, bool DENSE, int LANES>
+template <typename T, typename S, int PAIRS, bool DENSE, int LANES>
 cudaError_t backward_strip(const opt_head_norm_backward_args& a, int sm_count, float* parts, cudaStream_t s) {
   static OccupancyCache cache;
-  const auto kernel = head_norm_backward_strip_kernel<T, S, INTERLEAVED, DENSE, LANES, kBackwardChunks<T>>;
+  const auto kernel = head_norm_backward_strip_kernel<T, S, PAIRS, DENSE, LANES, kBackwardChunks<T>>;
   int64_t most = (int64_t)sm_count * cached_occupancy(kernel, cache, kThreads, 0), ctas;
   if (most > kHeadBackwardMaxCtas) most = kHeadBackwardMaxCtas;
   const Strips strips = strips_of(a, kBackwardChunks<T>, most, &ctas);
@@ -772,17 +840,15 @@ cudaError_t backward_strip(const opt_head_norm_backward_args& a, int sm_count, f
   if (const cudaError_t e = cudaGetLastError()) return e;
   return weight_sums(a, (int)ctas, s);
 }
-template <typename T, typename S, bool INTERLEAVED>
+template <typename T, typename S, int PAIRS>
 cudaError_t backward_strips(const opt_head_norm_backward_args& a, int sm_count, float* parts, cudaStream_t s) {
-  if ((a.dim & (a.dim - 1)) != 0) {
-    if (a.dim > 64 && a.dim < 128) return backward_strip<T, S, INTERLEAVED, false, 16>(a, sm_count, parts, s);
-    return backward_strip<T, S, INTERLEAVED, false, 0>(a, sm_count, parts, s);
+  const bool dense = (a.dim & (a.dim - 1)) == 0;
+  if constexpr (PAIRS != kElements) {
+    if (a.dim == 64) return backward_strip<T, S, PAIRS, true, 8>(a, sm_count, parts, s);
+    if (a.dim == 128) return backward_strip<T, S, PAIRS, true, 16>(a, sm_count, parts, s);
+    if (a.dim > 64 && a.dim < 128) return backward_strip<T, S, PAIRS, false, 16>(a, sm_count, parts, s);
   }
-  switch (a.dim) {
-    case 64: return backward_strip<T, S, INTERLEAVED, true, 8>(a, sm_count, parts, s);
-    case 128: return backward_strip<T, S, INTERLEAVED, true, 16>(a, sm_count, parts, s);
-    default: return backward_strip<T, S, INTERLEAVED, true, 0>(a, sm_count, parts, s);
-  }
+  return dense ? backward_strip<T, S, PAIRS, true, 0>(a, sm_count, parts, s) : backward_strip<T, S, PAIRS, false, 0>(a, sm_count, parts, s);
 }
 
 template <typename T, typename S, typename W>
@@ -801,8 +867,13 @@ cudaError_t backward_from(const opt_head_norm_backward_args& a, int sm_count, cu
   }
   float* parts = a.d_dq_weight != nullptr || a.d_dk_weight != nullptr ? static_cast<float*>(a.d_workspace) : nullptr;
   // (a strip of either side needs a row of the workspace; more than it has go by single heads)
-  if (v.ok && (a.q_heads + a.k_heads) * a.dim <= (kHeadBackwardMaxCtas - 2) * 128)
-    return a.flags & OPT_HEADS_INTERLEAVED ? backward_strips<T, S, true>(a, sm_count, parts, s) : backward_strips<T, S, false>(a, sm_count, parts, s);
+  if (v.ok && (a.q_heads + a.k_heads) * a.dim <= (kHeadBackwardMaxCtas - 2) * 128) {
+    switch (pairs_of(a)) {
+      case kChunks: return backward_strips<T, S, kChunks>(a, sm_count, parts, s);
+      case kNeighbours: return backward_strips<T, S, kNeighbours>(a, sm_count, parts, s);
+      default: return backward_strips<T, S, kElements>(a, sm_count, parts, s);
+    }
+  }
   return backward_any<T, S, W>(a, sm_count, parts, s);
 }
 

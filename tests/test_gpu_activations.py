@@ -285,10 +285,14 @@ HEADS = [(1, 32, 8, 128, 128, False, 0), (1, 1, 0, 64, 64, True, 0), (5, 3, 1, 6
          (1, 2, 1, 33, 32, False, 0), (40, 5, 3, 100, 100, False, 0), (23, 3, 2, 64, 64, False, 3), (31, 2, 2, 64, 24, False, 0),
          (7, 1, 1, 1, 0, False, 0), (12, 2, 1, 2, 2, True, 1), (3, 1, 2, 1024, 1024, True, 0), (5, 2, 0, 300, 150, False, 0),
          (2000, 3, 1, 40, 40, False, 0), (700, 1, 1, 50, 26, True, 0)]
+# whole chunks of which any even part is rotated
+PARTS = [(33, 5, 2, 64, 24, False, 0), (40, 9, 3, 80, 40, False, 8), (300, 3, 1, 128, 2, False, 0), (9, 2, 2, 256, 250, False, 0),
+         (70, 17, 3, 16, 14, False, 0), (5, 33, 1, 8, 6, False, 0), (21, 6, 1, 24, 18, False, 0), (3001, 3, 2, 96, 90, False, 0),
+         (65, 2, 2, 128, 118, True, 0), (50, 12, 1, 8, 2, True, 0), (130, 4, 2, 112, 54, True, 8), (1, 7, 2, 200, 100, False, 0)]
 
 
 @pytest.mark.parametrize("dtype,wdtype", [("bf16", "f32"), ("bf16", "bf16"), ("f32", "f32"), ("f32", "bf16")])
-@pytest.mark.parametrize("rows,hq,hk,dim,rot,interleaved,pad", HEADS)
+@pytest.mark.parametrize("rows,hq,hk,dim,rot,interleaved,pad", HEADS + PARTS)
 def test_head_norm(dtype, wdtype, rows, hq, hk, dim, rot, interleaved, pad):
     cos, sin = tables(97, rot)
     at = places(rows, 97, 1) if rot else None
@@ -323,7 +327,7 @@ def test_head_norm(dtype, wdtype, rows, hq, hk, dim, rot, interleaved, pad):
 
 @pytest.mark.parametrize("source", ["plain", "kept"])
 @pytest.mark.parametrize("dtype,wdtype", [("bf16", "f32"), ("bf16", "bf16"), ("f32", "f32"), ("f32", "bf16")])
-@pytest.mark.parametrize("rows,hq,hk,dim,rot,interleaved,pad", HEADS)
+@pytest.mark.parametrize("rows,hq,hk,dim,rot,interleaved,pad", HEADS + PARTS)
 def test_head_norm_backward(dtype, wdtype, source, rows, hq, hk, dim, rot, interleaved, pad):
     cos, sin = tables(97, rot)
     at = places(rows, 97, 1) if rot else None
@@ -414,6 +418,28 @@ def test_heads_special_rows_and_positions(dim, shift):
     ps.opt_head_norm_backward(torch.ones_like(x), x, w, dx, dq_weight=dw, cos=cos, sin=sin, positions=at)
     assert torch.isnan(dx[5:7]).all() and torch.isfinite(dx[:5]).all() and torch.isfinite(dx[7]).all()
     assert torch.isnan(dw[:rot]).all()
+
+
+@pytest.mark.parametrize("dim,rot,interleaved", [(128, 64, False), (64, 24, False), (64, 20, True), (100, 50, False)])
+def test_tables_at_any_place_and_infinities_past_the_rotated(dim, rot, interleaved):
+    """Tables that start on 4 bytes; an infinity behind the rotated elements stays out of the
+    weight's gradient of the others."""
+    rows, heads = 37, 3
+    cos, sin = tables(rows, rot)
+    odd = [torch.empty(t.numel() + 1, device="cuda")[1:].view(t.shape).copy_(t) for t in (cos, sin)]
+    for dtype in ("bf16", "f32"):
+        x, d = matrix(rows, heads * dim, dtype, 60), matrix(rows, heads * dim, dtype, 61)
+        d[5, dim + rot] = float("inf")
+        w = torch.ones(dim, device="cuda")
+        got = []
+        for c, s in ((cos, sin), odd):
+            y, dx, dw = torch.empty_like(x), torch.empty_like(x), torch.empty(dim, device="cuda")
+            ps.opt_head_norm(x, w, y, cos=c, sin=s, interleaved=interleaved)
+            ps.opt_head_norm_backward(d, x, w, dx, dq_weight=dw, cos=c, sin=s, interleaved=interleaved)
+            got.append((y, torch.nan_to_num(dx, 7.0), dw))
+        assert all(torch.equal(a, b) for a, b in zip(*got))
+        dw = got[0][2]
+        assert torch.isinf(dw[rot]) and torch.isfinite(dw[:rot]).all() and torch.isfinite(dw[rot + 1:]).all()
 
 
 def test_row_numbers_as_positions_and_shapes_of_heads():
