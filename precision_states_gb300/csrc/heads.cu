@@ -557,6 +557,153 @@ __device__ __forceinline__ bool turn_at(const float* cos, const float* sin, int6
   return true;
 }
 
+// Heads of at most 32 N elements: element j of a head is lane j mod 32's, and a warp takes
+// `group` heads of a row after one another, so that the angles and the weight stay in
+// registers; the next head is asked for while this one is taken.  Partners meet in shared
+// memory, whose last place holds the 0 that elements without a partner meet.
+template <int N>
+struct LaneTurn {
+  int partner[N];
+  float c[N], s[N];
+  __device__ __forceinline__ void set(const HeadCall& a, int64_t r) {
+    const int64_t at = a.rot > 0 && a.positions != nullptr ? a.positions[r] : r;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      partner[i] = 32 * N;
+      c[i] = 1.0f;
+      s[i] = 0.0f;
+      turn_at(a.cos, a.sin, at, a.table, a.rot, a.interleaved, (int)(threadIdx.x & 31) + 32 * i, partner[i], c[i], s[i]);
+    }
+  }
+};
+template <int N, typename F>
+__device__ __forceinline__ void lane_elements(int dim, float (&v)[N], F f) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int j = (int)(threadIdx.x & 31) + 32 * i;
+    v[i] = j < dim ? f(j) : 0.0f;
+  }
+}
+
+template <typename T, typename W, int N>
+__global__ void __launch_bounds__(kThreads) head_norm_lanes_kernel(const __grid_constant__ HeadCall a, int group) {
+  __shared__ float held_by[kWarps][32 * N + 1];
+  float* held = held_by[threadIdx.x >> 5];
+  const int lane = threadIdx.x & 31, dim = a.dim;
+  if (lane == 0) held[32 * N] = 0.0f;
+  const int64_t q_groups = (a.side[0].heads + group - 1) / group, groups = q_groups + (a.side[1].heads + group - 1) / group;
+  const int64_t n = a.rows * groups;
+  for (int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); t < n; t += (int64_t)gridDim.x * kWarps) {
+    const int64_t r = t / groups, both = t % groups;
+    const bool keys = both >= q_groups;
+    const Side& side = a.side[keys];
+    const int64_t first = (keys ? both - q_groups : both) * group;
+    const int heads = (int)(side.heads - first < group ? side.heads - first : group);
+    const T* from = static_cast<const T*>(side.x) + r * side.x_pitch + first * dim;
+    T* out = static_cast<T*>(side.out) + r * side.out_pitch + first * dim;
+    LaneTurn<N> turn;
+    turn.set(a, r);
+    float w[N], ahead[N];
+    lane_elements<N>(dim, w, [&](int j) { return element(static_cast<const W*>(side.weight) + j); });
+    lane_elements<N>(dim, ahead, [&](int j) { return element(from + j); });
+    for (int h = 0; h < heads; ++h, out += dim) {
+      float x[N], sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = ahead[i];
+      from += dim;
+      if (h + 1 < heads) lane_elements<N>(dim, ahead, [&](int j) { return element(from + j); });
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        sum = fmaf(x[i], x[i], sum);
+        x[i] *= w[i];
+        held[lane + 32 * i] = x[i];
+      }
+      sum = group_sum(sum, 32);
+      const float rstd = reciprocal_root(fmaf(sum, 1.0f / (float)dim, a.eps));
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float y = fmaf(x[i], turn.c[i], held[turn.partner[i]] * turn.s[i]);
+        if (lane + 32 * i < dim) put_element(out + lane + 32 * i, rstd * y);
+      }
+      __syncwarp();              // the partners are read
+    }
+  }
+}
+
+// Their gradients: the first q_ctas CTAs take queries, the others keys.
+template <typename T, typename S, typename W, int N>
+__global__ void __launch_bounds__(kThreads) head_norm_backward_lanes_kernel(
+    const __grid_constant__ HeadCall a, int group, int q_ctas, float* parts) {
+  __shared__ float held_by[kWarps][32 * N + 1];
+  if (parts != nullptr) let_sums_start();
+  float* held = held_by[threadIdx.x >> 5];
+  const int lane = threadIdx.x & 31, dim = a.dim;
+  if (lane == 0) held[32 * N] = 0.0f;
+  const bool keys = (int)blockIdx.x >= q_ctas;
+  const Side& side = a.side[keys];
+  const int64_t cta = keys ? blockIdx.x - q_ctas : blockIdx.x, ctas = keys ? gridDim.x - q_ctas : q_ctas;
+  const int64_t groups = (side.heads + group - 1) / group, n = a.rows * groups, panel = (side.cols + 511) / 512;
+  float w[N], dw[N];
+  lane_elements<N>(dim, w, [&](int j) { return element(static_cast<const W*>(side.weight) + j); });
+#pragma unroll
+  for (int i = 0; i < N; ++i) dw[i] = 0.0f;
+  for (int64_t t = cta * kWarps + (threadIdx.x >> 5); t < n; t += ctas * kWarps) {
+    const int64_t r = t / groups, first = t % groups * group;
+    const int heads = (int)(side.heads - first < group ? side.heads - first : group);
+    int64_t col = first * dim;
+    const T* dout = static_cast<const T*>(side.dout) + r * side.dout_pitch;
+    T* out = static_cast<T*>(side.out) + r * side.out_pitch;
+    LaneTurn<N> turn;
+    turn.set(a, r);
+    float x_ahead[N], d_ahead[N];
+    const auto ask = [&](int64_t c) {
+      lane_elements<N>(dim, x_ahead, [&](int j) { return element_at(side, r, c + j, panel, S()); });
+      lane_elements<N>(dim, d_ahead, [&](int j) { return element(dout + c + j); });
+    };
+    ask(col);
+    for (int h = 0; h < heads; ++h, col += dim) {
+      float x[N], g[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        x[i] = x_ahead[i];
+        g[i] = d_ahead[i];
+      }
+      if (h + 1 < heads) ask(col + dim);
+#pragma unroll
+      for (int i = 0; i < N; ++i) held[lane + 32 * i] = g[i];
+      __syncwarp();
+      float square = 0.0f, dot = 0.0f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        g[i] = fmaf(g[i], turn.c[i], -held[turn.partner[i]] * turn.s[i]);
+        square = fmaf(x[i], x[i], square);
+        dot = fmaf(g[i] * w[i], x[i], dot);
+      }
+      square = group_sum(square, 32);          // (and the partners are read)
+      dot = group_sum(dot, 32);
+      const float rstd = reciprocal_root(fmaf(square, 1.0f / (float)dim, a.eps));
+      const float pull = rstd * rstd * (dot * (1.0f / (float)dim));
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        dw[i] = fmaf(g[i], x[i] * rstd, dw[i]);
+        if (lane + 32 * i < dim) put_element(out + col + lane + 32 * i, rstd * fmaf(-x[i], pull, g[i] * w[i]));
+      }
+      __syncwarp();
+    }
+  }
+  if (parts == nullptr) return;
+#pragma unroll
+  for (int i = 0; i < N; ++i) held[lane + 32 * i] = dw[i];
+  __syncthreads();
+  for (int t = threadIdx.x; t < 2 * dim; t += kThreads) {
+    float v = 0.0f;
+    if ((t >= dim) == keys)
+      for (int k = 0; k < kWarps; ++k) v += held_by[k][t >= dim ? t - dim : t];
+    parts[(int64_t)blockIdx.x * 2 * dim + t] = v;
+  }
+}
+
 template <typename T, typename W>
 __global__ void __launch_bounds__(32 * kAnyWarps) head_norm_any_kernel(const __grid_constant__ HeadCall a) {
   __shared__ float held[kAnyWarps][kHeadMaxDim];
@@ -759,6 +906,13 @@ cudaError_t keep(const void* x, int64_t x_pitch, void* codes, void* scales, int6
   return launch_quantize(q, s);
 }
 
+// Heads that a warp takes after one another: one while there are fewer heads than warps, at
+// most eight.
+int lane_group(int64_t heads, int sm_count) {
+  const int64_t each = heads / ((int64_t)sm_count * 2 * kWarps);
+  return each < 1 ? 1 : each > 8 ? 8 : (int)each;
+}
+
 template <typename T, typename W>
 cudaError_t forward(const opt_head_norm_args& a, int sm_count, cudaStream_t s) {
   Whole v = whole_heads(a, sizeof(W));
@@ -795,7 +949,18 @@ cudaError_t forward(const opt_head_norm_args& a, int sm_count, cudaStream_t s) {
       default: return forward_sparse_strips<T, kElements>(b, sm_count, s);
     }
   }
-  const int64_t need = (a.rows * (a.q_heads + a.k_heads) + kAnyWarps - 1) / kAnyWarps, most = (int64_t)sm_count * 12;
+  const int64_t heads = a.q_heads + a.k_heads;
+  if (a.dim <= 256) {
+    const int group = lane_group(a.rows * heads, sm_count);
+    const int64_t tasks = a.rows * ((a.q_heads + group - 1) / group + (a.k_heads + group - 1) / group);
+    const int64_t need = (tasks + kWarps - 1) / kWarps, most = (int64_t)sm_count * 4;
+    const unsigned ctas = (unsigned)(need < most ? need : most);
+    if (a.dim <= 64) head_norm_lanes_kernel<T, W, 2><<<ctas, kThreads, 0, s>>>(call_of(b), group);
+    else if (a.dim <= 128) head_norm_lanes_kernel<T, W, 4><<<ctas, kThreads, 0, s>>>(call_of(b), group);
+    else head_norm_lanes_kernel<T, W, 8><<<ctas, kThreads, 0, s>>>(call_of(b), group);
+    return cudaGetLastError();
+  }
+  const int64_t need = (a.rows * heads + kAnyWarps - 1) / kAnyWarps, most = (int64_t)sm_count * 12;
   head_norm_any_kernel<T, W><<<(unsigned)(need < most ? need : most), 32 * kAnyWarps, 0, s>>>(call_of(b));
   return cudaGetLastError();
 }
@@ -819,12 +984,16 @@ template <typename T, typename S, typename W>
 cudaError_t backward_any(const opt_head_norm_backward_args& a, int sm_count, float* parts, cudaStream_t s) {
   // as many CTAs for either side as it has heads' share, and within the workspace's rows
   const int64_t heads = a.q_heads + a.k_heads, most = (int64_t)sm_count * 4 < kHeadBackwardMaxCtas / 2 ? (int64_t)sm_count * 4 : kHeadBackwardMaxCtas / 2;
+  const int group = a.dim <= 256 ? lane_group(a.rows * heads, sm_count) : 1, warps = a.dim <= 256 ? kWarps : kAnyWarps;
   const auto ctas_of = [&](int64_t h) {
-    const int64_t need = (a.rows * h + kAnyWarps - 1) / kAnyWarps, share = (most * h + heads - 1) / heads;
+    const int64_t need = (a.rows * ((h + group - 1) / group) + warps - 1) / warps, share = (most * h + heads - 1) / heads;
     return (int)(need < share ? need : share);
   };
   const int q_ctas = ctas_of(a.q_heads), ctas = q_ctas + ctas_of(a.k_heads);
-  head_norm_backward_any_kernel<T, S, W><<<(unsigned)ctas, 32 * kAnyWarps, 0, s>>>(call_of(a), q_ctas, parts);
+  if (a.dim <= 64) head_norm_backward_lanes_kernel<T, S, W, 2><<<(unsigned)ctas, kThreads, 0, s>>>(call_of(a), group, q_ctas, parts);
+  else if (a.dim <= 128) head_norm_backward_lanes_kernel<T, S, W, 4><<<(unsigned)ctas, kThreads, 0, s>>>(call_of(a), group, q_ctas, parts);
+  else if (a.dim <= 256) head_norm_backward_lanes_kernel<T, S, W, 8><<<(unsigned)ctas, kThreads, 0, s>>>(call_of(a), group, q_ctas, parts);
+  else head_norm_backward_any_kernel<T, S, W><<<(unsigned)ctas, 32 * kAnyWarps, 0, s>>>(call_of(a), q_ctas, parts);
   if (const cudaError_t e = cudaGetLastError()) return e;
   return weight_sums(a, ctas, s);
 }
