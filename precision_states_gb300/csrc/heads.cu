@@ -6,12 +6,12 @@
 // and s' is -s for a pair's first element and s for its second.  Backward the turn is by
 // (c, -s) on dout's elements: g = dout c - dout' s'.
 //
-// Whole heads are held by groups of lanes, eight elements each (dim / 8 lanes, padded to a
-// power of two), so that sums are a few exchanges and a partner is another lane's raw
-// words or the lane's own.  A warp keeps to one set of heads and goes through rows, so
-// that the weight (and the weight's gradient) stay in registers, and the row's cosines and
-// sines serve all of the set.  Heads of other sizes and places take a form of a warp per
-// head, through shared memory.
+// Forms, by the heads' size and place:
+// - heads of 8, 16, ... 256 elements whose rows start on 16 bytes, by strips (below): eight
+//   elements to a lane and 16-byte accesses;
+// - other heads of at most 256 elements: an element to a lane (16384 x 40 heads of 128, kept,
+//   270 us where strips take 80, their gradients at 8192 rows 351 where they take 49);
+// - longer heads, to 1,024 elements: a head to a warp at a time, in shared memory.
 #include <type_traits>
 
 #include "tile.cuh"
@@ -120,19 +120,7 @@ __device__ __forceinline__ Raw<float> partner_of(const Raw<float>& x, int partne
 // power of two (DENSE), fewer else.  A strip is U times that of one side's columns, and a lane's
 // chunks are that far apart.  The next row's chunk is asked for as soon as this row's is taken.
 
-// Eight elements of the weight, of either type.
-__device__ __forceinline__ void weight8(const void* weight, int32_t type, int e, float (&w)[8]) {
-  if (type == OPT_F32) unpack(load_raw<true>(static_cast<const float*>(weight) + e, 8), w);
-  else unpack(load_raw<true>(static_cast<const Bf16*>(weight) + e, 8), w);
-}
-template <int LANES>
-__device__ __forceinline__ float lanes_sum(float v, int lanes) {
-  if constexpr (LANES == 0) return group_sum(v, lanes);
-#pragma unroll
-  for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  return v;
-}
-// N of them, their exchanges side by side.
+// N sums over groups of lanes (LANES of them, or where that is 0 `lanes`), their exchanges side by side.
 template <int LANES, int N>
 __device__ __forceinline__ void lanes_sums(float (&v)[N], int lanes) {
 #pragma unroll
@@ -405,12 +393,8 @@ __global__ void __launch_bounds__(kThreads, kBackwardCtas) head_norm_backward_st
   const uint32_t place = 512 * (l.column >> 9) + ((l.column >> 7) & 3);
   const float inv_dim = 1.0f / (float)dim;
   float w[8];
-  if (DENSE || l.e < dim) {
-    weight8(side.weight, a.weight_dtype, l.e, w);
-  } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = 0.0f;
-  }
+  for (int j = 0; j < 8; ++j) w[j] = DENSE || l.e < dim ? weight_at(side.weight, a.weight_dtype, l.e + j) : 0.0f;
   f2_t dw[4] = {};                 // +0 in both lanes
   // the turn back: plus for a pair's first element
   const float sign = PAIRS == kChunks && l.rotated && l.e >= (rot >> 1) ? -1.0f : 1.0f;
@@ -827,7 +811,7 @@ __global__ void __launch_bounds__(kSumCols * kSumParts) head_weight_kernel(const
   }
 }
 
-// Whether heads are whole chunks of eight elements that start on 16 bytes everywhere.
+// Whether heads are at most 256 elements, whole chunks of eight that start on 16 bytes.
 struct Whole {
   int64_t rows;
   bool ok;
@@ -835,14 +819,6 @@ struct Whole {
     ok = ok && ((uintptr_t)p & 15u) == 0 && (rows == 1 || pitch * es % 16 == 0);
   }
 };
-template <typename A>
-Whole whole_heads(const A& a, int64_t ws) {
-  Whole v{a.rows, a.dim % 8 == 0 && a.dim <= 256};
-  if (a.q_heads > 0) v.see(a.d_q_weight, 0, ws);
-  if (a.k_heads > 0) v.see(a.d_k_weight, 0, ws);
-  return v;
-}
-
 template <typename A>
 Pairs pairs_of(const A& a) {
   return a.flags & OPT_HEADS_INTERLEAVED ? kNeighbours : a.rot % 16 == 0 ? kChunks : kElements;
@@ -915,7 +891,7 @@ int lane_group(int64_t heads, int sm_count) {
 
 template <typename T, typename W>
 cudaError_t forward(const opt_head_norm_args& a, int sm_count, cudaStream_t s) {
-  Whole v = whole_heads(a, sizeof(W));
+  Whole v{a.rows, a.dim % 8 == 0 && a.dim <= 256};
   if (a.q_heads > 0) {
     v.see(a.d_q, a.q_pitch, sizeof(T));
     v.see(a.d_q_out, a.q_out_pitch, sizeof(T));
@@ -1022,7 +998,7 @@ cudaError_t backward_strips(const opt_head_norm_backward_args& a, int sm_count, 
 
 template <typename T, typename S, typename W>
 cudaError_t backward_from(const opt_head_norm_backward_args& a, int sm_count, cudaStream_t s) {
-  Whole v = whole_heads(a, sizeof(W));
+  Whole v{a.rows, a.dim % 8 == 0 && a.dim <= 256};
   constexpr bool kept = sizeof(S) == 1;
   if (a.q_heads > 0) {
     if (!kept) v.see(a.d_q, a.q_pitch, sizeof(T));

@@ -482,13 +482,6 @@ __device__ __forceinline__ Raw<T> load_if(const T* p, bool on) {
                  : "l"(reinterpret_cast<const uint32_t*>(p) + k), "r"((int)on));
   return r;
 }
-__device__ __forceinline__ uint4 load_words_if(const float* p, bool on) {      // of a table: kept in L1
-  uint4 r;
-  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.s32 q, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
-               "@q ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
-               : "=&r"(r.x), "=&r"(r.y), "=&r"(r.z), "=&r"(r.w) : "l"(p), "r"((int)on));
-  return r;
-}
 __device__ __forceinline__ uint2 load_codes_if(const uint8_t* p, bool on) {
   uint2 r;
   asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.s32 q, %3, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"

@@ -24,8 +24,8 @@ def activation(g, kind):
     error of its argument (5 roundings with the factor log2 e) and 4 units of 2^-24 of
     its own, and s and 1 - s by 4 more (sum, reciprocal, product); f by one more.  f' is
     s + f (1 - s) z', with five more roundings in the second term; 1 - s may be formed as
-    that, off by 2^-24.  s is 0 where it would be below 2^-128 in BF16,
-    which leaves f off by |g| 2^-128 and f' by 2^-128 (1 + |g| z').  gelu: the
+    that, off by 2^-24.  s is 0 where it would be below 2^-126 in BF16,
+    which leaves f off by |g| 2^-126 and f' by 2^-126 (1 + |g| z').  gelu: the
     distribution function below 0 is an exponential (4 units, and g^2 for the rounding of its
     argument, half of g^2 formed with two) times a fitted factor (8), with three products; above
     0 it is 1 less that."""

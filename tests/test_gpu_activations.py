@@ -285,6 +285,9 @@ HEADS = [(1, 32, 8, 128, 128, False, 0), (1, 1, 0, 64, 64, True, 0), (5, 3, 1, 6
          (1, 2, 1, 33, 32, False, 0), (40, 5, 3, 100, 100, False, 0), (23, 3, 2, 64, 64, False, 3), (31, 2, 2, 64, 24, False, 0),
          (7, 1, 1, 1, 0, False, 0), (12, 2, 1, 2, 2, True, 1), (3, 1, 2, 1024, 1024, True, 0), (5, 2, 0, 300, 150, False, 0),
          (2000, 3, 1, 40, 40, False, 0), (700, 1, 1, 50, 26, True, 0)]
+# by single elements: up to 64, 128 and 256 of them, and rows that begin anywhere
+HEADS += [(31, 9, 2, 255, 250, False, 0), (33, 3, 3, 130, 64, True, 0), (20, 4, 1, 256, 256, False, 1), (9, 11, 5, 63, 62, True, 0),
+          (130, 2, 2, 129, 0, False, 0), (5, 17, 2, 128, 64, False, 5), (4, 1, 0, 257, 256, True, 0)]
 # whole chunks of which any even part is rotated
 PARTS = [(33, 5, 2, 64, 24, False, 0), (40, 9, 3, 80, 40, False, 8), (300, 3, 1, 128, 2, False, 0), (9, 2, 2, 256, 250, False, 0),
          (70, 17, 3, 16, 14, False, 0), (5, 33, 1, 8, 6, False, 0), (21, 6, 1, 24, 18, False, 0), (3001, 3, 2, 96, 90, False, 0),
@@ -707,7 +710,8 @@ def test_many_tiles_turned(rows, cols):
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("rows,hq,hk,dim,rot,interleaved", [
     (9000, 9, 2, 64, 64, False), (6001, 12, 12, 128, 64, True), (4000, 1, 0, 256, 256, False), (5000, 40, 3, 16, 16, False),
-    (9000, 5, 1, 96, 96, False), (7000, 3, 2, 100, 50, True), (3, 2000, 300, 128, 128, False), (2, 700, 0, 80, 16, True)])
+    (9000, 5, 1, 96, 96, False), (7000, 3, 2, 100, 50, True), (3, 2000, 300, 128, 128, False), (2, 700, 0, 80, 16, True),
+    (3000, 21, 2, 36, 36, False), (700, 19, 3, 250, 100, True), (2000, 13, 0, 63, 62, False), (1500, 9, 4, 80, 40, False)])
 def test_many_heads_are_those_of_fewer(dtype, rows, hq, hk, dim, rot, interleaved):
     """More rows than warps, and more heads than a strip: the same bits as slice by slice, for
     kept and plain inputs; the weights' gradients in any case near the exact ones."""
