@@ -210,7 +210,10 @@ int opt_dequantize(const opt_dequantize_args* a, void* stream);
  *   OPT_ACT_SILU       s(g) = 1 / (1 + exp(-g))
  *   OPT_ACT_GELU_TANH  s(g) = (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2
  *   OPT_ACT_GELU       s(g) = the normal distribution function
- *   OPT_ACT_RELU       f(g) = max(g, 0) */
+ *   OPT_ACT_RELU       f(g) = max(g, 0)
+ * For BF16 matrices s and exp(-g^2 / 2) are 0 where they are below 2^-126, and errors
+ * are a few 2^-24 of the value (at most 300 where g^2 / 2 is that large); for OPT_F32
+ * they keep fp32's last places. */
 #define OPT_ACT_SILU      0
 #define OPT_ACT_GELU_TANH 1
 #define OPT_ACT_GELU      2
@@ -221,7 +224,8 @@ int opt_dequantize(const opt_dequantize_args* a, void* stream);
  * for each 1 x 128, from y before it is rounded).  d_gate_codes with d_gate_scales and
  * d_up_codes with d_up_scales keep the inputs for the backward pass.  At least one
  * output is given; a pair is given whole.  d_y may be d_gate or d_up (same pointer
- * and pitch); the other outputs overlap no input. */
+ * and pitch); the other outputs overlap no input.  Fastest: cols a multiple of 8, plain
+ * matrices whose rows start on 16 bytes, and gate and up both kept or neither. */
 typedef struct opt_gated_args {
   const void* d_gate;
   const void* d_up;
@@ -289,8 +293,13 @@ int opt_gated_backward(const opt_gated_backward_args* a, void* stream);
  * A position outside the tables makes the rotated elements NaN; nothing is read there.
  * rot is even, 0 <= rot <= dim (0: no rotation, and no tables); 1 <= dim <= 1024.
  * d_q_codes with d_q_scales (and k's) keep the inputs x for the backward pass: the
- * whole matrix's 1 x 128 blocks, across heads.  d_q_out may be d_q (same pointer and
- * pitch); the other outputs overlap no input. */
+ * whole matrix's 1 x 128 blocks, across heads.  d_q_out may be d_q and d_k_out may be
+ * d_k (same pointer and pitch); the other outputs overlap no input.  The sum of x^2 is
+ * held in fp32, as in opt_rms_norm: a NaN makes its head NaN, squares that add up beyond
+ * fp32 make it 0 (an infinity NaN), a head of zeros with eps 0 gives NaN.  No head and no
+ * row reaches another's output.  Fastest: dim a multiple of 8 up to 256, and plain
+ * matrices whose rows start on 16 bytes; then rot a multiple of 16, or of 8 with
+ * OPT_HEADS_INTERLEAVED; and for keeping, dim a power of two. */
 #define OPT_HEADS_INTERLEAVED 1
 typedef struct opt_head_norm_args {
   const void* d_q;
@@ -321,7 +330,8 @@ int opt_head_norm(const opt_head_norm_args* a, void* stream);
  *   g = dout turned back, t = g weight, rstd = 1 / sqrt(mean(x^2) + eps)
  *   dx = rstd (t - x rstd^2 mean(t x))
  *   dweight = sum over rows and heads of g x rstd          (NULL: not wanted), fp32
- * in fp32, each rounded once.  d_dq may be d_dq_out (same pointer and pitch).  The sums
+ * in fp32, each rounded once; over no rows or no heads the sum is 0.  d_dq may be
+ * d_dq_out and d_dk may be d_dk_out (same pointer and pitch).  The sums
  * run in a fixed order; they need d_workspace of
  * opt_head_norm_backward_workspace(rows, q_heads, k_heads, dim) bytes, 16-byte aligned,
  * when d_dq_weight or d_dk_weight is given (0 bytes: none). */

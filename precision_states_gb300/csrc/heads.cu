@@ -570,7 +570,7 @@ __device__ __forceinline__ void lane_elements(int dim, float (&v)[N], F f) {
 }
 
 template <typename T, typename W, int N>
-__global__ void __launch_bounds__(kThreads) head_norm_lanes_kernel(const __grid_constant__ HeadCall a, int group) {
+__global__ void __launch_bounds__(kThreads, N <= 4 ? 4 : 2) head_norm_lanes_kernel(const __grid_constant__ HeadCall a, int group) {
   __shared__ float held_by[kWarps][32 * N + 1];
   float* held = held_by[threadIdx.x >> 5];
   const int lane = threadIdx.x & 31, dim = a.dim;
@@ -617,7 +617,7 @@ __global__ void __launch_bounds__(kThreads) head_norm_lanes_kernel(const __grid_
 
 // Their gradients: the first q_ctas CTAs take queries, the others keys.
 template <typename T, typename S, typename W, int N>
-__global__ void __launch_bounds__(kThreads) head_norm_backward_lanes_kernel(
+__global__ void __launch_bounds__(kThreads, N <= 4 ? 3 : 2) head_norm_backward_lanes_kernel(
     const __grid_constant__ HeadCall a, int group, int q_ctas, float* parts) {
   __shared__ float held_by[kWarps][32 * N + 1];
   if (parts != nullptr) let_sums_start();
@@ -889,6 +889,17 @@ int lane_group(int64_t heads, int sm_count) {
   return each < 1 ? 1 : each > 8 ? 8 : (int)each;
 }
 
+template <typename T, typename W, int N>
+cudaError_t forward_lanes(const opt_head_norm_args& a, int sm_count, cudaStream_t s) {
+  static OccupancyCache cache;
+  const auto kernel = head_norm_lanes_kernel<T, W, N>;
+  const int group = lane_group(a.rows * (a.q_heads + a.k_heads), sm_count);
+  const int64_t tasks = a.rows * ((a.q_heads + group - 1) / group + (a.k_heads + group - 1) / group);
+  const int64_t need = (tasks + kWarps - 1) / kWarps, most = (int64_t)sm_count * cached_occupancy(kernel, cache, kThreads, 0);
+  kernel<<<(unsigned)(need < most ? need : most), kThreads, 0, s>>>(call_of(a), group);
+  return cudaGetLastError();
+}
+
 template <typename T, typename W>
 cudaError_t forward(const opt_head_norm_args& a, int sm_count, cudaStream_t s) {
   Whole v{a.rows, a.dim % 8 == 0 && a.dim <= 256};
@@ -926,16 +937,9 @@ cudaError_t forward(const opt_head_norm_args& a, int sm_count, cudaStream_t s) {
     }
   }
   const int64_t heads = a.q_heads + a.k_heads;
-  if (a.dim <= 256) {
-    const int group = lane_group(a.rows * heads, sm_count);
-    const int64_t tasks = a.rows * ((a.q_heads + group - 1) / group + (a.k_heads + group - 1) / group);
-    const int64_t need = (tasks + kWarps - 1) / kWarps, most = (int64_t)sm_count * 4;
-    const unsigned ctas = (unsigned)(need < most ? need : most);
-    if (a.dim <= 64) head_norm_lanes_kernel<T, W, 2><<<ctas, kThreads, 0, s>>>(call_of(b), group);
-    else if (a.dim <= 128) head_norm_lanes_kernel<T, W, 4><<<ctas, kThreads, 0, s>>>(call_of(b), group);
-    else head_norm_lanes_kernel<T, W, 8><<<ctas, kThreads, 0, s>>>(call_of(b), group);
-    return cudaGetLastError();
-  }
+  if (a.dim <= 64) return forward_lanes<T, W, 2>(b, sm_count, s);
+  if (a.dim <= 128) return forward_lanes<T, W, 4>(b, sm_count, s);
+  if (a.dim <= 256) return forward_lanes<T, W, 8>(b, sm_count, s);
   const int64_t need = (a.rows * heads + kAnyWarps - 1) / kAnyWarps, most = (int64_t)sm_count * 12;
   head_norm_any_kernel<T, W><<<(unsigned)(need < most ? need : most), 32 * kAnyWarps, 0, s>>>(call_of(b));
   return cudaGetLastError();
@@ -956,22 +960,40 @@ cudaError_t weight_sums(const opt_head_norm_backward_args& a, int ctas, cudaStre
                             a.d_dk_weight);
 }
 
-template <typename T, typename S, typename W>
-cudaError_t backward_any(const opt_head_norm_backward_args& a, int sm_count, float* parts, cudaStream_t s) {
-  // as many CTAs for either side as it has heads' share, and within the workspace's rows
-  const int64_t heads = a.q_heads + a.k_heads, most = (int64_t)sm_count * 4 < kHeadBackwardMaxCtas / 2 ? (int64_t)sm_count * 4 : kHeadBackwardMaxCtas / 2;
-  const int group = a.dim <= 256 ? lane_group(a.rows * heads, sm_count) : 1, warps = a.dim <= 256 ? kWarps : kAnyWarps;
+// CTAs of `warps` warps for either side, which take `group` heads at a time: as many as the
+// side's share of the heads in `most`, and within the workspace's rows.
+struct SideCtas {
+  int q, all;
+};
+SideCtas side_ctas(const opt_head_norm_backward_args& a, int group, int warps, int64_t most) {
+  if (most > kHeadBackwardMaxCtas - 1) most = kHeadBackwardMaxCtas - 1;      // (shares are rounded up)
+  const int64_t heads = a.q_heads + a.k_heads;
   const auto ctas_of = [&](int64_t h) {
     const int64_t need = (a.rows * ((h + group - 1) / group) + warps - 1) / warps, share = (most * h + heads - 1) / heads;
     return (int)(need < share ? need : share);
   };
-  const int q_ctas = ctas_of(a.q_heads), ctas = q_ctas + ctas_of(a.k_heads);
-  if (a.dim <= 64) head_norm_backward_lanes_kernel<T, S, W, 2><<<(unsigned)ctas, kThreads, 0, s>>>(call_of(a), group, q_ctas, parts);
-  else if (a.dim <= 128) head_norm_backward_lanes_kernel<T, S, W, 4><<<(unsigned)ctas, kThreads, 0, s>>>(call_of(a), group, q_ctas, parts);
-  else if (a.dim <= 256) head_norm_backward_lanes_kernel<T, S, W, 8><<<(unsigned)ctas, kThreads, 0, s>>>(call_of(a), group, q_ctas, parts);
-  else head_norm_backward_any_kernel<T, S, W><<<(unsigned)ctas, 32 * kAnyWarps, 0, s>>>(call_of(a), q_ctas, parts);
+  const int q = ctas_of(a.q_heads);
+  return {q, q + ctas_of(a.k_heads)};
+}
+template <typename T, typename S, typename W, int N>
+cudaError_t backward_lanes(const opt_head_norm_backward_args& a, int sm_count, float* parts, cudaStream_t s) {
+  static OccupancyCache cache;
+  const auto kernel = head_norm_backward_lanes_kernel<T, S, W, N>;
+  const int group = lane_group(a.rows * (a.q_heads + a.k_heads), sm_count);
+  const SideCtas ctas = side_ctas(a, group, kWarps, (int64_t)sm_count * cached_occupancy(kernel, cache, kThreads, 0));
+  kernel<<<(unsigned)ctas.all, kThreads, 0, s>>>(call_of(a), group, ctas.q, parts);
   if (const cudaError_t e = cudaGetLastError()) return e;
-  return weight_sums(a, ctas, s);
+  return weight_sums(a, ctas.all, s);
+}
+template <typename T, typename S, typename W>
+cudaError_t backward_any(const opt_head_norm_backward_args& a, int sm_count, float* parts, cudaStream_t s) {
+  if (a.dim <= 64) return backward_lanes<T, S, W, 2>(a, sm_count, parts, s);
+  if (a.dim <= 128) return backward_lanes<T, S, W, 4>(a, sm_count, parts, s);
+  if (a.dim <= 256) return backward_lanes<T, S, W, 8>(a, sm_count, parts, s);
+  const SideCtas ctas = side_ctas(a, 1, kAnyWarps, (int64_t)sm_count * 4);
+  head_norm_backward_any_kernel<T, S, W><<<(unsigned)ctas.all, 32 * kAnyWarps, 0, s>>>(call_of(a), ctas.q, parts);
+  if (const cudaError_t e = cudaGetLastError()) return e;
+  return weight_sums(a, ctas.all, s);
 }
 
 template <typename T, typename S, int PAIRS, bool DENSE, int LANES>

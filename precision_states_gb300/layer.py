@@ -9,8 +9,9 @@ and write into tensors that the caller owns.  A matrix argument is a CUDA
 tensor on the current device whose last dimension is contiguous: a 2-d tensor
 of any row stride, or a contiguous tensor of any other shape, taken as rows of
 its last dimension.  A kept matrix, or another operand in 8 bits that an argument
-names as one, is a pair (codes, scales) as e4m3_storage gives it.  Wrong shapes and dtypes, and numbers that their C types do not
-hold, raise ValueError; everything else is checked by the library (OptError).
+names as one, is a pair (codes, scales) as e4m3_storage gives it.  Wrong shapes
+and dtypes, and numbers that their C types do not hold, raise ValueError;
+everything else is checked by the library (OptError).
 """
 from __future__ import annotations
 
