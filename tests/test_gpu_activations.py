@@ -782,6 +782,58 @@ def test_rows_far_apart():
     assert torch.equal(one, two)
 
 
+@pytest.mark.parametrize("rows,pitch", [(1100, (1 << 22) + 64), (300, (1 << 24) + 64)])
+def test_offsets_past_32_bits(rows, pitch):
+    """Matrices that are columns of rows so long that their last ones lie past 2^32 elements: the
+    same bits as of matrices of their own, for inputs and outputs of every call."""
+    cols = 264
+    wide = torch.empty(rows * pitch, dtype=torch.bfloat16, device="cuda").view(rows, pitch)
+    wide8 = torch.empty(max(rows, cols) * pitch, dtype=torch.uint8, device="cuda").view(max(rows, cols), pitch)
+    places = iter(range(0, 1 << 20, 1152))      # columns of either
+
+    def far(like):
+        at = next(places)
+        return wide[:, at:at + cols] if like is None else wide8[:like[0], at:at + like[1]]
+
+    g, u, dy = (matrix(rows, cols, "bf16", 170 + i) for i in range(3))
+    fg, fu, fd = far(None), far(None), far(None)
+    for a, b in ((fg, g), (fu, u), (fd, dy)):
+        a.copy_(b)
+
+    def pair(r, c, away):
+        codes, scales = storage(r, c)
+        return (far((r, c)) if away else codes), scales
+
+    def run(away, gate, up, d):
+        new = lambda: far(None) if away else torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+        y, yc, gk, uk = new(), pair(rows, cols, away), pair(rows, cols, away), pair(rows, cols, away)
+        ps.opt_gated(gate, up, y=y, codes=yc[0], scales=yc[1], gate_kept=gk, up_kept=uk)
+        every = {**{n: pair(rows, cols, away) for n in ("dgate_codes", "dup_codes")},
+                 **{n: pair(cols, rows, away) for n in ("dgate_codes_t", "dup_codes_t", "y_codes_t")}}
+        ps.opt_gated_backward(d, gk, uk, **every)
+        dg, du, dgc, dgt = new(), new(), pair(rows, cols, away), pair(cols, rows, away)
+        ps.opt_gated_backward(d, gate, up, dgate=dg, dup=du)
+        ps.opt_gated_backward(d, gk, uk, dgate_codes=dgc)
+        ps.opt_gated_backward(d, gate, up, dgate_codes_t=dgt)
+        x, xt, xu = new(), pair(cols, rows, away), new()
+        ps.opt_dequantize(*gk, x=x, codes_t=xt[0], scales_t=xt[1])
+        ps.opt_dequantize(*gk, x=xu)
+        out = [y, *yc, *gk, *uk, dg, du, *dgc, *dgt, x, *xt, xu] + [t for p in every.values() for t in p]
+        for dim in (8, 24, 33, 264):                  # strips of either kind, single elements, long heads
+            w = torch.ones(dim, device="cuda")
+            n, dn, dk, dw = new(), new(), new(), torch.empty(dim, device="cuda")
+            held = pair(rows, cols, away)
+            ps.opt_head_norm(gate, w, n, q_kept=held)
+            ps.opt_head_norm_backward(d, gate, w, dn, dq_weight=dw)
+            ps.opt_head_norm_backward(d, held, w, dk)
+            out += [n, *held, dn, dw, dk]
+        return out
+
+    assert (rows - 1) * pitch >= 1 << 32 and rows <= 1152
+    for i, (a, b) in enumerate(zip(run(True, fg, fu, fd), run(False, g, u, dy))):
+        assert torch.equal(a, b), i
+
+
 def test_rows_behind_the_last_stay():
     """Codes and plain outputs of a padded batch: rows behind the given ones keep what they hold."""
     rows, cols, more = 200, 256, 56
