@@ -10,7 +10,8 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Plain values alone: a chunk to a thread.
+// Plain values alone: a chunk to a thread.  Bound by instructions (issue 79 % busy): 16384 x 4096
+// to BF16 38.5 us, 0.77 of a copy's rate, to fp32 57 us, 0.87; rows that begin anywhere 56 us.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) dequantize_kernel(const __grid_constant__ opt_dequantize_args a) {
   __shared__ __align__(16) Ragged<T, VEC, kThreads / 32> ragged;
@@ -73,7 +74,9 @@ __device__ __forceinline__ void copy16(void* to, const uint8_t* p, int left) {
 }
 
 // CTAs take tiles gridDim.x apart (`step_rows` and `step_cols` in tiles), the next tile's codes
-// on their way while one is turned.
+// on their way while one is turned.  Three to an SM (four spill: 35 us).  Bound by instructions
+// (issue 71 % busy): 16384 x 4096 turned 27.6 us, 0.72 of a copy's rate, with BF16 values 47.6,
+// 0.83 (74 where their rows begin anywhere).
 template <typename T, bool PLAIN, bool VEC>
 __global__ void __launch_bounds__(kTileThreads, 3) dequantize_tile_kernel(const __grid_constant__ opt_dequantize_args a, int row_tiles,
                                                                          int col_tiles, int step_rows, int step_cols) {

@@ -93,7 +93,9 @@ __device__ __forceinline__ float group_sum(float v, int lanes) {
 }
 
 // How a head's elements are paired: whole chunks with whole chunks half the rotated part
-// further (rot a multiple of 16), neighbours, or elements half the rotated part further.
+// further (rot a multiple of 16; a lane's partners are another lane's words), neighbours (its
+// own), or elements half the rotated part further (by way of shared memory: 16384 x 40 heads of
+// 128, kept, 136 us where whole chunks take 79).
 enum Pairs { kChunks = 0, kNeighbours = 1, kElements = 2 };
 
 // The partner's words: those of lane `partner`, or with neighbouring pairs the lane's own
@@ -119,6 +121,11 @@ __device__ __forceinline__ Raw<float> partner_of(const Raw<float>& x, int partne
 // dim / 8 is none), and groups side by side fill the warp: 256 columns at a time where dim is a
 // power of two (DENSE), fewer else.  A strip is U times that of one side's columns, and a lane's
 // chunks are that far apart.  The next row's chunk is asked for as soon as this row's is taken.
+// Bound by latency at the 16 warps that the registers leave to an SM (two CTAs; three are slower)
+// and by instructions (issue 58 % busy in either direction): 16384 x 40 heads of 128 BF16, kept, 79 us,
+// 0.79 of a copy's rate, without keeping 78 (0.64); gradients of 8192 from kept inputs 49 us, 0.64.
+// Heads of 96 leave a quarter of the lanes idle: 16384 x 52 of them 114 us, 0.43.  Lanes to a head
+// by number (LANES) spare 3 to 7 % against the same at run time.
 
 // N sums over groups of lanes (LANES of them, or where that is 0 `lanes`), their exchanges side by side.
 template <int LANES, int N>
@@ -508,8 +515,7 @@ __global__ void __launch_bounds__(kThreads, kBackwardCtas) head_norm_backward_st
 }
 
 // ------------------------------------------------------- heads of any size and place
-// A warp takes a head at a time through shared memory.  Element j of a head, of a plain
-// matrix or a kept one:
+// By single elements.  An element of a row, of a plain matrix or a kept one:
 template <typename T>
 __device__ __forceinline__ float element_at(const Side& side, int64_t r, int64_t col, int64_t panel, T) {
   return element(static_cast<const T*>(side.x) + r * side.x_pitch + col);
@@ -544,7 +550,9 @@ __device__ __forceinline__ bool turn_at(const float* cos, const float* sin, int6
 // Heads of at most 32 N elements: element j of a head is lane j mod 32's, and a warp takes
 // `group` heads of a row after one another, so that the angles and the weight stay in
 // registers; the next head is asked for while this one is taken.  Partners meet in shared
-// memory, whose last place holds the 0 that elements without a partner meet.
+// memory, whose last place holds the 0 that elements without a partner meet.  Bound by
+// instructions on single elements: 16384 x 50 heads of 100 168 us, 0.29 of a copy's rate,
+// gradients of 4096 137, 0.13 (by the kernels for longer heads 575 and 339).
 template <int N>
 struct LaneTurn {
   int partner[N];
@@ -688,6 +696,8 @@ __global__ void __launch_bounds__(kThreads, N <= 4 ? 3 : 2) head_norm_backward_l
   }
 }
 
+// Heads of more elements (8192 x 20 heads of 300 225 us, 0.14 of a copy's rate; not made faster,
+// since attention heads are shorter).
 template <typename T, typename W>
 __global__ void __launch_bounds__(32 * kAnyWarps) head_norm_any_kernel(const __grid_constant__ HeadCall a) {
   __shared__ float held[kAnyWarps][kHeadMaxDim];
@@ -990,8 +1000,10 @@ cudaError_t backward_any(const opt_head_norm_backward_args& a, int sm_count, flo
   if (a.dim <= 64) return backward_lanes<T, S, W, 2>(a, sm_count, parts, s);
   if (a.dim <= 128) return backward_lanes<T, S, W, 4>(a, sm_count, parts, s);
   if (a.dim <= 256) return backward_lanes<T, S, W, 8>(a, sm_count, parts, s);
-  const SideCtas ctas = side_ctas(a, 1, kAnyWarps, (int64_t)sm_count * 4);
-  head_norm_backward_any_kernel<T, S, W><<<(unsigned)ctas.all, 32 * kAnyWarps, 0, s>>>(call_of(a), ctas.q, parts);
+  static OccupancyCache cache;
+  const auto kernel = head_norm_backward_any_kernel<T, S, W>;
+  const SideCtas ctas = side_ctas(a, 1, kAnyWarps, (int64_t)sm_count * cached_occupancy(kernel, cache, 32 * kAnyWarps, 0));
+  kernel<<<(unsigned)ctas.all, 32 * kAnyWarps, 0, s>>>(call_of(a), ctas.q, parts);
   if (const cudaError_t e = cudaGetLastError()) return e;
   return weight_sums(a, ctas.all, s);
 }
