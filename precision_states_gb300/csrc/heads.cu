@@ -121,9 +121,10 @@ __device__ __forceinline__ Raw<float> partner_of(const Raw<float>& x, int partne
 // dim / 8 is none), and groups side by side fill the warp: 256 columns at a time where dim is a
 // power of two (DENSE), fewer else.  A strip is U times that of one side's columns, and a lane's
 // chunks are that far apart.  The next row's chunk is asked for as soon as this row's is taken.
-// Bound by latency at the 16 warps that the registers leave to an SM (two CTAs; three are slower)
-// and by instructions (issue 58 % busy in either direction): 16384 x 40 heads of 128 BF16, kept, 79 us,
-// 0.79 of a copy's rate, without keeping 78 (0.64); gradients of 8192 from kept inputs 49 us, 0.64.
+// Bound by latency at the 16 warps that the registers leave to an SM, and by instructions (issue
+// 58 % busy in either direction): 16384 x 40 heads of 128 BF16, kept, 79 us, 0.79 of a copy's
+// rate, without keeping 78 (0.64); gradients of 8192 from kept inputs 49 us, 0.64.  Strips half
+// as wide with three CTAs to an SM take 104 and 77 us.
 // Heads of 96 leave a quarter of the lanes idle: 16384 x 52 of them 114 us, 0.43.  Lanes to a head
 // by number (LANES) spare 3 to 7 % against the same at run time.
 
@@ -1000,10 +1001,10 @@ cudaError_t backward_any(const opt_head_norm_backward_args& a, int sm_count, flo
   if (a.dim <= 64) return backward_lanes<T, S, W, 2>(a, sm_count, parts, s);
   if (a.dim <= 128) return backward_lanes<T, S, W, 4>(a, sm_count, parts, s);
   if (a.dim <= 256) return backward_lanes<T, S, W, 8>(a, sm_count, parts, s);
-  static OccupancyCache cache;
-  const auto kernel = head_norm_backward_any_kernel<T, S, W>;
-  const SideCtas ctas = side_ctas(a, 1, kAnyWarps, (int64_t)sm_count * cached_occupancy(kernel, cache, 32 * kAnyWarps, 0));
-  kernel<<<(unsigned)ctas.all, 32 * kAnyWarps, 0, s>>>(call_of(a), ctas.q, parts);
+  // three to an SM: a fourth's shared memory leaves L1 too little for the tables (4096 x 20 heads of
+  // 300 400 us for 293; of 1024 147 either way)
+  const SideCtas ctas = side_ctas(a, 1, kAnyWarps, (int64_t)sm_count * 3);
+  head_norm_backward_any_kernel<T, S, W><<<(unsigned)ctas.all, 32 * kAnyWarps, 0, s>>>(call_of(a), ctas.q, parts);
   if (const cudaError_t e = cudaGetLastError()) return e;
   return weight_sums(a, ctas.all, s);
 }
