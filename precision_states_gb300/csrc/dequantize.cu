@@ -93,9 +93,19 @@ __global__ void __launch_bounds__(kTileThreads, 3) dequantize_tile_kernel(const 
     const int rows = (int)min(a.rows - 128 * (int64_t)tr, (int64_t)128), cols = (int)min(a.cols - 128 * (int64_t)tc, (int64_t)128);
     const uint8_t* p = source + 128 * (tr * a.codes_pitch + tc);
     // rows t / 8 + 32 i, 16 codes at 16 (t mod 8)
+    if (rows == 128 && cols == 128) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i, p += 32 * a.codes_pitch)
-      copy16(held[turn] + tile_word((t >> 3) + 32 * i, 4 * (t & 7)), p, (t >> 3) + 32 * i < rows ? cols - 16 * (t & 7) : 0);
+      for (int i = 0; i < 4; ++i, p += 32 * a.codes_pitch) copy16(held[turn] + tile_word((t >> 3) + 32 * i, 4 * (t & 7)), p, 16);
+    } else {
+      // What does not exist is asked for at the matrix's own place: an address has to be aligned even
+      // where nothing is copied, and the pitch of a single row may be anything.  (Rows that exist begin
+      // on 16 bytes: the first does, and with a second one the pitch is a multiple of 16.)
+#pragma unroll
+      for (int i = 0; i < 4; ++i, p += 32 * a.codes_pitch) {
+        const int left = (t >> 3) + 32 * i < rows ? cols - 16 * (t & 7) : 0;
+        copy16(held[turn] + tile_word((t >> 3) + 32 * i, 4 * (t & 7)), left > 0 ? p : static_cast<const uint8_t*>(a.d_codes), left);
+      }
+    }
     asm volatile("cp.async.commit_group;" ::: "memory");
     byte = load_byte_if(source_scale + 512 * (tr * panel + (tc >> 2)) + (tc & 3), t < rows);
   };
