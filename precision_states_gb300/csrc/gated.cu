@@ -50,12 +50,17 @@ __device__ __forceinline__ void activation(float g, float& f, float& df) {
     if (SLOPE) df = fmaf(f * (z < 0.0f ? r : er), dz, s);
   }
 }
-// The normal distribution function of two values, and exp(-g^2 / 2).  For a = |g|, s(-a) =
+// The normal distribution function of two values, and exp(-g^2 / 2) (EXACT: scaled).  For a = |g|, s(-a) =
 // exp(-a^2 / 2) R(a); R, a scaled complementary error function, by Hastings' way (Abramowitz and
 // Stegun 7.1.26): a polynomial in t = 1 / (1 + 0.4 a), here of degree nine for R / t, fitted to
 // equal relative errors over 0 <= a <= 16 (in fp32 5 units of 2^-24, 8 with a reciprocal that is
-// one off) and exact at 0.  EXACT: the exponential with what its argument's rounding loses.
-// (8192 x 14336 BF16 to y 120 us, with the library's function 262.)
+// one off) and exact at 0.  (8192 x 14336 BF16 to y 120 us, with the library's function 262.)
+// EXACT: the exponential times 2^64 (kBellScale), which the polynomial's coefficients take back, so
+// that s is kept down to fp32's last subnormal number; and with what its argument's rounding loses.
+// (4096 x 14336 fp32 to codes, both kept, 107 us; with the exponential's own subnormal results
+// 109, with 0 below 2^-126 106.)
+template <bool EXACT>
+constexpr float kBellScale = EXACT ? 18446744073709551616.0f : 1.0f;
 template <bool EXACT>
 __device__ __forceinline__ void normal2(f2_t g, f2_t& s, f2_t& bell) {
   constexpr float c[10] = {1.595754921e-01f, 1.596362293e-01f,  1.330585480e-01f, 9.175205231e-02f,  -2.814983390e-02f,
@@ -67,18 +72,27 @@ __device__ __forceinline__ void normal2(f2_t g, f2_t& s, f2_t& bell) {
   float tl, th;
   unpk(fma2(a, pk(0.4f, 0.4f), one), tl, th);
   const f2_t t = pk(reciprocal_near(tl), reciprocal_near(th));
-  f2_t q = pk(c[9], c[9]);
+  constexpr float back = 1.0f / kBellScale<EXACT>;
+  f2_t q = pk(c[9] * back, c[9] * back);
 #pragma unroll
-  for (int k = 8; k >= 0; --k) q = fma2(q, t, pk(c[k], c[k]));
+  for (int k = 8; k >= 0; --k) q = fma2(q, t, pk(c[k] * back, c[k] * back));
   constexpr float h = -0.5f * kLog2e, h_rest = (float)(-0.5 * 1.4426950408889634074 - (double)h), ln2 = 0.69314718f;
-  const f2_t square = mul2(a, a), u = mul2(square, pk(h, h));
+  const f2_t square = mul2(a, a), hv = pk(h, h);
+  // EXACT: the argument (-185 to 0) as a whole number of 2^-15, by way of 256 to 512, so that adding
+  // 64 and taking the rest are exact
+  constexpr float whole = 511.0f;
+  f2_t u = mul2(square, hv), steps = 0;
+  if constexpr (EXACT) {
+    steps = fma2(square, hv, pk(whole, whole));
+    u = add2(steps, pk(64.0f - whole, 64.0f - whole));
+  }
   float ul, uh;
   unpk(u, ul, uh);
   bell = pk(exp2_near(ul), exp2_near(uh));
   if constexpr (EXACT) {
     const f2_t minus = pk(-1.0f, -1.0f);
-    const f2_t square_rest = fma2(a, a, mul2(square, minus));
-    const f2_t rest = fma2(square, pk(h, h), mul2(u, minus)), all = fma2(square_rest, pk(h, h), fma2(square, pk(h_rest, h_rest), rest));
+    const f2_t square_rest = fma2(a, a, mul2(square, minus)), rest = fma2(square, hv, fma2(steps, minus, pk(whole, whole)));
+    const f2_t all = fma2(square_rest, hv, fma2(square, pk(h_rest, h_rest), rest));
     bell = fma2(mul2(bell, pk(ln2, ln2)), all, bell);
   }
   const f2_t below = mul2(mul2(q, t), bell);
@@ -96,7 +110,9 @@ __device__ __forceinline__ void activation8(const float (&g)[8], float (&f)[8], 
       f2_t s, bell;
       normal2<EXACT>(gv, s, bell);
       unpk(mul2(gv, s), f[j], f[j + 1]);
-      if constexpr (SLOPE) unpk(fma2(mul2(gv, pk(0.3989422804014327f, 0.3989422804014327f)), bell, s), df[j], df[j + 1]);
+      constexpr float root = 0.3989422804014327f / kBellScale<EXACT>;
+      // (EXACT: the bell's part first, which is 0 where |g| is large)
+      if constexpr (SLOPE) unpk(EXACT ? fma2(gv, mul2(bell, pk(root, root)), s) : fma2(mul2(gv, pk(root, root)), bell, s), df[j], df[j + 1]);
     }
   } else if constexpr (EXACT || KIND == OPT_ACT_RELU) {
 #pragma unroll
