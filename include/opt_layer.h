@@ -211,9 +211,11 @@ int opt_dequantize(const opt_dequantize_args* a, void* stream);
  *   OPT_ACT_GELU_TANH  s(g) = (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2
  *   OPT_ACT_GELU       s(g) = the normal distribution function
  *   OPT_ACT_RELU       f(g) = max(g, 0)
- * For BF16 matrices s and exp(-g^2 / 2) are 0 where they are below 2^-126, and errors
- * are a few 2^-24 of the value (at most 300 where g^2 / 2 is that large); for OPT_F32
- * they keep fp32's last places. */
+ * For BF16 matrices s and exp(-g^2 / 2) are 0 where they are below 2^-126 (SiLU is 0 below
+ * -87.3), and errors are a few 2^-24 of the value, up to 150 of them where s is near 2^-126;
+ * for OPT_F32 subnormal numbers are kept, and errors are at most 8 (SiLU) and 17 (GELU) 2^-24
+ * of f, and 6 |z| more for its tanh form, z being what its s is the logistic function of (20
+ * at g = -4, 200 at -10: fp32 rounds z). */
 #define OPT_ACT_SILU      0
 #define OPT_ACT_GELU_TANH 1
 #define OPT_ACT_GELU      2

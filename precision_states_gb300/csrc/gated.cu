@@ -28,9 +28,10 @@ __device__ __forceinline__ float reciprocal_near(float a) {
   return r;
 }
 
-// f(g) and, if it is wanted (SLOPE), f'(g).  EXACT: for fp32 elements, to their last
-// places; else s = 1 / (1 + 2^(-z log2 e)), whose errors of a few 2^-24 are far below BF16's
-// and E4M3's steps (and which is 0 where it would be below 2^-126), two at a time.
+// f(g) and, if it is wanted (SLOPE), f'(g).  EXACT: for fp32 elements, by fp32's exponential and a
+// rounded reciprocal (8 units of 2^-24, and with the tanh form's z 6 |z| more: its roundings); else
+// s = 1 / (1 + 2^(-z log2 e)), whose errors of a few 2^-24 (150 where s is near 2^-126) are far below
+// BF16's and E4M3's steps (and which is 0 where it would be below 2^-126), two at a time.
 template <int KIND, bool EXACT, bool SLOPE>
 __device__ __forceinline__ void activation(float g, float& f, float& df) {
   if constexpr (KIND == OPT_ACT_RELU) {
