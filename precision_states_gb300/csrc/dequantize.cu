@@ -78,7 +78,7 @@ __device__ __forceinline__ void copy16(void* to, const uint8_t* p, int left) {
 // (issue 71 % busy): 16384 x 4096 turned 27.6 us, 0.72 of a copy's rate, with BF16 values 47.6,
 // 0.83 (74 where their rows begin anywhere).
 template <typename T, bool PLAIN, bool VEC>
-__global__ void __launch_bounds__(kTileThreads, 3) dequantize_tile_kernel(const __grid_constant__ opt_dequantize_args a, int row_tiles,
+__global__ void __launch_bounds__(kThreads, 3) dequantize_tile_kernel(const __grid_constant__ opt_dequantize_args a, int row_tiles,
                                                                          int col_tiles, int step_rows, int step_cols) {
   __shared__ __align__(16) uint32_t held[2][128 * 32];
   __shared__ __align__(16) float held_scale[2][128];
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kTileThreads, 3) dequantize_tile_kernel(const 
       }
     } else if constexpr (PLAIN) {
 #pragma unroll 2
-      for (int row = t >> 5; row < rows; row += kTileThreads / 32)
+      for (int row = t >> 5; row < rows; row += kThreads / 32)
         put_row(static_cast<T*>(a.d_x) + (r0 + row) * a.x_pitch + c0, codes, scale, row, cols);
     }
     const uint32_t* mine = codes + tile_word(row, word);
@@ -218,15 +218,14 @@ cudaError_t launch_tiles(const opt_dequantize_args& a, int sm_count, cudaStream_
   static OccupancyCache cache;
   const auto kernel = dequantize_tile_kernel<T, PLAIN, VEC>;
   const int row_tiles = (int)((a.rows + 127) / 128), col_tiles = (int)((a.cols + 127) / 128);
-  const int64_t tiles = (int64_t)row_tiles * col_tiles, most = (int64_t)sm_count * cached_occupancy(kernel, cache, kTileThreads, 0);
+  const int64_t tiles = (int64_t)row_tiles * col_tiles, most = (int64_t)sm_count * cached_occupancy(kernel, cache, kThreads, 0);
   const int grid = (int)(tiles < most ? tiles : most);
-  kernel<<<grid, kTileThreads, 0, s>>>(a, row_tiles, col_tiles, grid / col_tiles, grid % col_tiles);
+  kernel<<<grid, kThreads, 0, s>>>(a, row_tiles, col_tiles, grid / col_tiles, grid % col_tiles);
   return cudaGetLastError();
 }
 
 template <typename T, bool VEC>
 cudaError_t launch(const opt_dequantize_args& a, int sm_count, cudaStream_t s) {
-  if (a.d_x == nullptr) return launch_tiles<T, false, true>(a, sm_count, s);
   if (a.d_codes_t != nullptr) return launch_tiles<T, true, VEC>(a, sm_count, s);
   const ChunkGrid g(a.rows, a.cols, kThreads);
   dequantize_kernel<T, VEC><<<g.grid, g.block, 0, s>>>(a);
@@ -237,9 +236,8 @@ cudaError_t launch(const opt_dequantize_args& a, int sm_count, cudaStream_t s) {
 
 cudaError_t launch_dequantize(const opt_dequantize_args& a, int sm_count, cudaStream_t s) {
   const int64_t es = a.dtype == OPT_F32 ? 4 : 2;
-  const bool vec = a.cols % 8 == 0 && (a.d_x == nullptr || (((uintptr_t)a.d_x & 15u) == 0 &&
-                                                            (a.rows == 1 || a.x_pitch * es % 16 == 0)));
-  if (a.d_x == nullptr) return launch<Bf16, true>(a, sm_count, s);      // the same for either type
+  if (a.d_x == nullptr) return launch_tiles<Bf16, false, true>(a, sm_count, s);      // the same for either type
+  const bool vec = a.cols % 8 == 0 && ((uintptr_t)a.d_x & 15u) == 0 && (a.rows == 1 || a.x_pitch * es % 16 == 0);
   if (a.dtype == OPT_F32) return vec ? launch<float, true>(a, sm_count, s) : launch<float, false>(a, sm_count, s);
   return vec ? launch<Bf16, true>(a, sm_count, s) : launch<Bf16, false>(a, sm_count, s);
 }

@@ -84,11 +84,10 @@ HeadCall call_of(const opt_head_norm_backward_args& a) {
 // head_weight_kernel may be launched once every CTA has come here; it waits for this grid's end.
 __device__ __forceinline__ void let_sums_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// Sum over a group of `lanes` (a power of two) lanes.
-__device__ __forceinline__ float group_sum(float v, int lanes) {
+// Sum over a warp.
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    if (o < lanes) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
 }
 
@@ -611,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, N <= 4 ? 4 : 2) head_norm_lanes_kern
         x[i] *= w[i];
         held[lane + 32 * i] = x[i];
       }
-      sum = group_sum(sum, 32);
+      sum = warp_sum(sum);
       const float rstd = reciprocal_root(fmaf(sum, 1.0f / (float)dim, a.eps));
       __syncwarp();
 #pragma unroll
@@ -673,8 +672,8 @@ __global__ void __launch_bounds__(kThreads, N <= 4 ? 3 : 2) head_norm_backward_l
         square = fmaf(x[i], x[i], square);
         dot = fmaf(g[i] * w[i], x[i], dot);
       }
-      square = group_sum(square, 32);          // (and the partners are read)
-      dot = group_sum(dot, 32);
+      square = warp_sum(square);          // (and the partners are read)
+      dot = warp_sum(dot);
       const float rstd = reciprocal_root(fmaf(square, 1.0f / (float)dim, a.eps));
       const float pull = rstd * rstd * (dot * (1.0f / (float)dim));
 #pragma unroll
@@ -718,7 +717,7 @@ __global__ void __launch_bounds__(32 * kAnyWarps) head_norm_any_kernel(const __g
       x[j] = v;
       sum = fmaf(v, v, sum);
     }
-    sum = group_sum(sum, 32);
+    sum = warp_sum(sum);
     const float rstd = reciprocal_root(fmaf(sum, 1.0f / (float)dim, a.eps));
     __syncwarp();
 #pragma unroll 4
@@ -770,8 +769,8 @@ __global__ void __launch_bounds__(32 * kAnyWarps) head_norm_backward_any_kernel(
       square = fmaf(x[j], x[j], square);
       dot = fmaf(turned(j) * element(weight + j), x[j], dot);
     }
-    square = group_sum(square, 32);
-    dot = group_sum(dot, 32);
+    square = warp_sum(square);
+    dot = warp_sum(dot);
     const float rstd = reciprocal_root(fmaf(square, 1.0f / (float)dim, a.eps));
     const float pull = rstd * rstd * (dot * (1.0f / (float)dim));
 #pragma unroll 4
@@ -812,7 +811,7 @@ __global__ void __launch_bounds__(kSumCols * kSumParts) head_weight_kernel(const
   }
   sums[p0][x] = s;
   __syncthreads();
-  s = group_sum(sums[x][p0], 32);          // column p0's
+  s = warp_sum(sums[x][p0]);          // column p0's
   const int c = blockIdx.x * kSumCols + p0;
   if (x != 0 || c >= 2 * dim) return;
   if (c < dim) {
