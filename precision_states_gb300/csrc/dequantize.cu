@@ -75,7 +75,7 @@ __device__ __forceinline__ void copy16(void* to, const uint8_t* p, int left) {
 
 // CTAs take tiles gridDim.x apart (`step_rows` and `step_cols` in tiles), the next tile's codes
 // on their way while one is turned.  Three to an SM (four spill: 35 us).  Bound by instructions
-// (issue 71 % busy): 16384 x 4096 turned 27.6 us, 0.72 of a copy's rate, with BF16 values 47.6,
+// (issue 70 % busy): 16384 x 4096 turned 26.8 us, 0.74 of a copy's rate, with BF16 values 47.9,
 // 0.83 (74 where their rows begin anywhere).
 template <typename T, bool PLAIN, bool VEC>
 __global__ void __launch_bounds__(kThreads, 3) dequantize_tile_kernel(const __grid_constant__ opt_dequantize_args a, int row_tiles,
