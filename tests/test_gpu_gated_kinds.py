@@ -3,6 +3,7 @@ every activation with and without `up`, in whole chunks and in rows that begin a
 each set of inputs kept and of outputs that has a kernel of its own."""
 import numpy as np
 import pytest
+import torch
 
 import activation_reference as act
 import precision_states_gb300 as ps
@@ -89,3 +90,33 @@ def test_backward(kind, has_up, source, dtype, rows, cols, pad, shift, outputs):
             assert act.untouched(got[1], rows, cols, 0xEE)
         else:
             within(got, want[of], dtype, off[of])
+
+
+@pytest.mark.parametrize("rows,cols,pad,shift", PLACES)
+@pytest.mark.parametrize("source", ["plain", "kept"])
+@pytest.mark.parametrize("kind", KINDS)
+def test_codes_are_the_quantizers_of_the_fp32_values(kind, source, rows, cols, pad, shift):
+    """Of fp32 matrices codes and plain outputs are rounded from the same values: the codes are
+    those that opt_quantize makes of the plain ones, bit for bit, with infinities and NaN, zero
+    blocks, and blocks whose values leave fp32 or are subnormal."""
+    g, u, dy = spread(rows, cols, "f32", 46, pad, shift), matrix(rows, cols, "f32", 47, pad), matrix(rows, cols, "f32", 48, pad, shift, std=1e-2)
+    dy[3], u[7], dy[:, 9] = 0.0, 0.0, 0.0
+    dy[11, 5], u[11, 200], dy[90, 2] = float("nan"), float("inf"), float("-inf")
+    dy[20:24] *= 1e38
+    u[30:34] *= 3e37
+    dy[40:44] *= 1e-37
+    if source == "kept":
+        g, u = kept(g), kept(u)
+    plain = {n: blank(rows, cols, "f32", pad) for n in ("dgate", "dup")}
+    coded = {n + "_codes": storage(rows, cols) for n in ("dgate", "dup")}
+    turned = {n + "_codes_t": storage(cols, rows) for n in ("dgate", "dup")}
+    ps.opt_gated_backward(dy, g, u, activation=kind, **plain, **coded, **turned)
+    by_rows = {n + "_codes": storage(rows, cols) for n in ("dgate", "dup")}
+    ps.opt_gated_backward(dy, g, u, activation=kind, **by_rows)
+    for n in ("dgate", "dup"):
+        c, t = storage(rows, cols), storage(cols, rows)
+        ps.opt_quantize(plain[n], *c, *t)
+        assert not plain[n].isfinite().all()
+        for got, want in ((coded[n + "_codes"], c), (by_rows[n + "_codes"], c), (turned[n + "_codes_t"], t)):
+            odd = (want[0] & 0x7F) == 0x7F            # a NaN's sign is not looked at
+            assert torch.equal((got[0] & 0x7F) == 0x7F, odd) and torch.equal(got[0][~odd], want[0][~odd]) and torch.equal(got[1], want[1])
